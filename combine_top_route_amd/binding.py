@@ -8,6 +8,7 @@ memory (outputs, workspace) and the stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -20,9 +21,11 @@ MOE_F32, MOE_BF16 = 0, 1
 PREC_NATIVE, PREC_FP8_BLOCK, PREC_MXFP8, PREC_FP8_BWD = 0, 1, 2, 3
 OP_ROUTE, OP_FORWARD, OP_BACKWARD, OP_BACKWARD_RECOMPUTE = 0, 1, 2, 3
 QUANT_ROWS, QUANT_WEIGHT, QUANT_WEIGHT_T = 0, 1, 2
+DECODE_MAX_T = 256
 
 _DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _TORCH = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
+_WEIGHTS = {"native": 0, "fp8_block": 1, "mxfp8": 2}
 _PREC = {"native": PREC_NATIVE, "fp8_block": PREC_FP8_BLOCK, "mxfp8": PREC_MXFP8, "fp8_bwd": PREC_FP8_BWD}
 
 
@@ -58,6 +61,9 @@ _SIGS = [
                                    ctypes.c_size_t, _P]),
     ("moe_backward", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, ctypes.POINTER(MoeRouting), _P, _P, _P, _P,
                                     _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("moe_decode_workspace_size", ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(ctypes.c_size_t)]),
+    ("moe_decode", ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.c_int, _P, ctypes.POINTER(MoeRouting), _P, _P, _P,
+                                  _P, _P, _P, ctypes.c_size_t, _P]),
     ("moe_permute", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.POINTER(MoeRouting), _P, _P]),
     ("moe_combine", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.POINTER(MoeRouting), _P, _P]),
     ("moe_quantize_fp8", ctypes.c_int, [ctypes.c_int, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P,
@@ -138,6 +144,14 @@ def _ptr(t):
 
 def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _on(device):
+    """Context in which kernels launch on `device` (nothing to do, and nothing
+    paid, when it is the current one).  Refuses host memory."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors are on {device}; the kernels need a GPU's memory")
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _need(t, name, shape, dtype, device):
@@ -247,6 +261,99 @@ class MoeLayer:
         if dl is not None:
             res["dlogits"] = dl
         return res
+
+
+def decode_workspace_size(shape: MoeShape) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_decode_workspace_size", lib().moe_decode_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def _weight_args(name, w, shape, dtype, weights, device):
+    """Pointers of an expert weight [E, N, K] and of its scales: a tensor, or
+    (coded formats) the (codes, scales) pair of quantize_fp8 / quantize_mxfp8
+    with QUANT_WEIGHT."""
+    if weights == "native":
+        _need(w, name, shape, dtype, device)
+        return _ptr(w), None
+    if not isinstance(w, (tuple, list)) or len(w) != 2:
+        raise ValueError(f"{name} must be a (codes, scales) pair for weights={weights!r}")
+    E, N, K = shape
+    _need(w[0], f"{name} codes", shape, torch.uint8, device)
+    if weights == "fp8_block":
+        _need(w[1], f"{name} scales", (E, N // 128, K // 128), torch.float32, device)
+    else:
+        _need(w[1], f"{name} scales", (E, N, K // 32), torch.uint8, device)
+    return _ptr(w[0]), _ptr(w[1])
+
+
+class MoeDecoder:
+    """The layer for few tokens (moe_decode in include/moe.h), as a serving
+    loop calls it: forward takes x [T, d] with any 1 <= T <= max_T, and outputs
+    and workspace are allocated once, so calls allocate nothing and can be
+    captured into a graph.  out, topk_ids and topk_w are views of the decoder's
+    buffers and hold the last call's results; their rows from T on keep what
+    they held.  Calls that overlap in time (streams, replayed graphs) need a
+    decoder each.
+
+    weights: "native" (tensors in dtype), or "fp8_block" / "mxfp8": (codes,
+    scales) pairs from quantize_fp8 / quantize_mxfp8 with QUANT_WEIGHT.
+    Routing by logits [T, E], or by topk_ids and topk_w [T, k]; an id outside
+    [0, E) or a logit of -inf is an empty slot.  No gradient."""
+
+    def __init__(self, max_T, d, E, k, I, dtype=torch.bfloat16, logits_dtype=None, weights="native",
+                 device="cuda", swiglu_limit=0.0):
+        if weights not in _WEIGHTS:
+            raise ValueError(f"weights {weights!r} unknown")
+        self.max_T, self.d, self.E, self.k, self.I, self.weights = max_T, d, E, k, I, weights
+        self.dtype = dtype
+        self.logits_dtype = dtype if logits_dtype is None else logits_dtype
+        self.swiglu_limit = swiglu_limit
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        shape = make_shape(max_T, d, E, k, I, dtype, self.logits_dtype, "native", swiglu_limit)
+        self.workspace = torch.empty(decode_workspace_size(shape), dtype=torch.uint8, device=dev)
+        self._out = torch.empty((max_T, d), dtype=dtype, device=dev)
+        self._ids = torch.empty((max_T, k), dtype=torch.int32, device=dev)
+        self._w = torch.empty((max_T, k), dtype=torch.float32, device=dev)
+        self._by_T = {}
+        self.out, self.topk_ids, self.topk_w = self._out, self._ids, self._w
+
+    def _views(self, T):
+        """Shape argument and output views for T tokens (built once per T)."""
+        v = self._by_T.get(T)
+        if v is None:
+            shape = make_shape(T, self.d, self.E, self.k, self.I, self.dtype, self.logits_dtype, "native",
+                               self.swiglu_limit)
+            v = self._by_T[T] = (shape, self._out[:T], self._ids[:T], self._w[:T])
+        return v
+
+    def forward(self, x, w_gate_up, w_down, logits=None, topk_ids=None, topk_w=None):
+        E, d, I, dt, dev = self.E, self.d, self.I, self.dtype, self.device
+        T = x.shape[0]
+        if not 1 <= T <= self.max_T:
+            raise ValueError(f"x has {T} tokens, this decoder takes 1 to {self.max_T}")
+        _need(x, "x", (T, d), dt, dev)
+        gu, gu_s = _weight_args("w_gate_up", w_gate_up, (E, 2 * I, d), dt, self.weights, dev)
+        dn, dn_s = _weight_args("w_down", w_down, (E, d, I), dt, self.weights, dev)
+        shape, out, ids, w = self._views(T)
+        if logits is not None:
+            if topk_ids is not None or topk_w is not None:
+                raise ValueError("give logits, or topk_ids and topk_w, not both")
+            _need(logits, "logits", (T, E), self.logits_dtype, dev)
+        else:
+            _need(topk_ids, "topk_ids", (T, self.k), torch.int32, dev)
+            _need(topk_w, "topk_w", (T, self.k), torch.float32, dev)
+            ids, w = topk_ids, topk_w
+        routing = MoeRouting(_ptr(logits), _ptr(ids), _ptr(w), None, None, None, None)
+        with _on(dev):
+            _check("moe_decode", lib().moe_decode(
+                ctypes.byref(shape), _WEIGHTS[self.weights], _ptr(x), ctypes.byref(routing), gu, gu_s, dn, dn_s,
+                _ptr(out), _ptr(self.workspace), self.workspace.numel(), _stream(dev)))
+        self.out, self.topk_ids, self.topk_w = out, ids, w
+        return out
 
 
 def route(logits, k):

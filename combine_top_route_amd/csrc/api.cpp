@@ -392,6 +392,37 @@ hipError_t forward_gemms(const moe_shape* shape, const LaunchCtx& c, const Layer
   return fp8_fwd_gemms(c, a, q, H, A, Y);
 }
 
+// ------------------------------------------------------------ few tokens
+struct DecodeLayout {
+  size_t mid = 0, mw = 0, aw = 0, y = 0, total = 0;
+};
+
+DecodeLayout decode_layout(const moe_shape* s) {
+  DecodeLayout L;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off += align256(bytes);
+    return o;
+  };
+  const int64_t R = s->T * s->k;
+  L.mid = take(sizeof(int32_t) * R);
+  L.mw = take(sizeof(float) * R);
+  L.aw = take(elem_size(s->dtype) * R * s->I);
+  if (s->T > 16) L.y = take(sizeof(float) * R * s->d);
+  L.total = off;
+  return L;
+}
+
+moe_status check_decode(const moe_shape* s) {
+  TRY(check_shape(s));
+  if (s->T > kDecodeMaxT)
+    return fail(MOE_ERR_UNSUPPORTED, "T=%lld above %d: moe_forward takes more tokens", (long long)s->T, kDecodeMaxT);
+  if (s->precision != MOE_PREC_NATIVE)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_decode takes precision MOE_PREC_NATIVE; coded weights are its own argument");
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -560,6 +591,71 @@ moe_status moe_backward(const moe_shape* shape, const void* dout, const void* x,
                            dlogits, shape->logits_dtype), "topk_grad");
   HIP_TRY(launch_combine(c, "reduce_dx", shape->dtype, dXp, routing->row_of, nullptr, (int)shape->T,
                          (int)shape->k, (int)shape->d, dx), "reduce_dx");
+  return MOE_OK;
+}
+
+moe_status moe_decode_workspace_size(const moe_shape* shape, size_t* bytes) {
+  TRY(check_decode(shape));
+  CHECK_PTR(bytes);
+  *bytes = decode_layout(shape).total;
+  return MOE_OK;
+}
+
+moe_status moe_decode(const moe_shape* shape, int weights, const void* x, moe_routing* routing,
+                      const void* w_gate_up, const void* s_gate_up, const void* w_down, const void* s_down,
+                      void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  TRY(check_decode(shape));
+  if (weights < MOE_WEIGHTS_NATIVE || weights > MOE_WEIGHTS_MXFP8)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "weights=%d unknown", weights);
+  CHECK_PTR(x);
+  CHECK_PTR(routing);
+  CHECK_PTR(routing->topk_ids);
+  CHECK_PTR(routing->topk_w);
+  CHECK_PTR(w_gate_up);
+  CHECK_PTR(w_down);
+  CHECK_PTR(out);
+  if (weights != MOE_WEIGHTS_NATIVE) {
+    if (shape->dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "coded weights need dtype bf16");
+    if (shape->d % 128 || shape->I % 128)
+      return fail(MOE_ERR_UNSUPPORTED, "coded weights need d and I multiples of 128");
+    CHECK_PTR(s_gate_up);
+    CHECK_PTR(s_down);
+    if (((uintptr_t)s_gate_up | (uintptr_t)s_down) & 3)
+      return fail(MOE_ERR_INVALID_ARGUMENT, "scales must be 4-byte aligned");
+  } else if (s_gate_up || s_down) {
+    return fail(MOE_ERR_INVALID_ARGUMENT, "scales given for uncoded weights");
+  }
+  const DecodeLayout L = decode_layout(shape);
+  if (workspace_bytes < L.total)
+    return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, L.total);
+  CHECK_PTR(workspace);
+  if (((uintptr_t)workspace) & 255) return fail(MOE_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
+  TRY(check_aligned16(x, "x"));
+  TRY(check_aligned16(w_gate_up, "w_gate_up"));
+  TRY(check_aligned16(w_down, "w_down"));
+  TRY(check_aligned16(out, "out"));
+  DecodeArgs a;
+  a.T = (int)shape->T;
+  a.d = (int)shape->d;
+  a.E = (int)shape->E;
+  a.k = (int)shape->k;
+  a.I = (int)shape->I;
+  a.dtype = shape->dtype;
+  a.lim = shape->swiglu_limit > 0.0f ? shape->swiglu_limit : __builtin_huge_valf();
+  a.x = x;
+  a.w_gate_up = w_gate_up;
+  a.s_gate_up = s_gate_up;
+  a.w_down = w_down;
+  a.s_down = s_down;
+  a.out = out;
+  a.mid = (int32_t*)at(workspace, L.mid);
+  a.mw = (float*)at(workspace, L.mw);
+  a.aw = at(workspace, L.aw);
+  a.y = shape->T > 16 ? (float*)at(workspace, L.y) : nullptr;
+  const LaunchCtx c = make_ctx(stream);
+  (void)hipGetLastError();
+  HIP_TRY(launch_decode(c, a, routing->logits, shape->logits_dtype, routing->topk_ids, routing->topk_w, weights),
+          "decode");
   return MOE_OK;
 }
 

@@ -195,6 +195,28 @@ hipError_t f32_bwd_gemms(const LaunchCtx& c, const LayerArgs& a, const void* dou
                          const void* H, const void* Aw, void* dH, void* dXp, float* dwp,
                          void* dW_gu, void* dW_d, float* G);
 
+// ------------------------------------------------------------ few tokens
+// The whole layer for up to kDecodeMaxT tokens (decode.hip).
+constexpr int kDecodeMaxT = 256;
+struct DecodeArgs {
+  int T, d, E, k, I;
+  int dtype;              // of x, out and aw (and of uncoded weights)
+  float lim;              // SwiGLU clamp limit, +inf for the plain SwiGLU
+  const void* x;          // [T, d]
+  const void* w_gate_up;  // [E, 2I, d] in dtype, or e4m3 codes
+  const void* s_gate_up;  // coded: fp32 [E, 2I/128, d/128] or E8M0 [E, 2I, d/32]
+  const void* w_down;     // [E, d, I]
+  const void* s_down;     // fp32 [E, d/128, I/128] or E8M0 [E, d, I/32]
+  void* out;              // [T, d]
+  int32_t* mid;           // [T, k] workspace: expert of the slot, -1 for an empty or merged slot
+  float* mw;              // [T, k] workspace: its weight
+  void* aw;               // [T k, I] workspace: weighted SwiGLU output per live slot
+  float* y;               // [T k, d] workspace, T > 16: down products per live slot
+};
+// weights: moe_weight_format.  logits == null: ids and w are inputs.
+hipError_t launch_decode(const LaunchCtx& c, const DecodeArgs& a, const void* logits, int logits_dtype,
+                         int32_t* ids, float* w, int weights);
+
 // ---------------------------------------------------------------- fp8 path
 // Block quantisation to e4m3 (quant_fp8.hip).  Two formats: blockwise (fp32
 // scales; rows 1 x 128, weights 128 x 128, tokens 128-row runs) and MX

@@ -245,6 +245,46 @@ moe_status moe_backward(const moe_shape* shape, const void* dout, const void* x,
                         void* dlogits, void* workspace, size_t workspace_bytes,
                         void* stream);
 
+/* The layer for a few tokens (serving): the forward's arithmetic on at most
+ * 256 tokens, reading each selected expert's weights once, from weights that
+ * may have been encoded beforehand.  No tiles, sort or encoders run: the call
+ * is one small routing kernel, the gate/up products, and the down products
+ * with the combine (more than 16 tokens: the combine on its own).
+ *
+ * shape: T <= 256 and precision MOE_PREC_NATIVE (MOE_ERR_UNSUPPORTED
+ * otherwise; moe_forward takes more tokens); dtype is that of x and out;
+ * flags are ignored.  weights names the expert weights' format:
+ *   MOE_WEIGHTS_NATIVE:    in dtype; s_gate_up and s_down are NULL;
+ *   MOE_WEIGHTS_FP8_BLOCK: what moe_quantize_fp8 MOE_QUANT_WEIGHT writes:
+ *                          codes, and fp32 scales [E, 2I/128, d/128] and
+ *                          [E, d/128, I/128];
+ *   MOE_WEIGHTS_MXFP8:     what moe_quantize_mxfp8 MOE_QUANT_WEIGHT writes:
+ *                          codes, and scale bytes [E, 2I, d/32] and
+ *                          [E, d, I/32]; byte 255 (E8M0's NaN) is not
+ *                          recognised.
+ * Coded weights need dtype MOE_BF16 and d, I multiples of 128, and stand for
+ * code * scale; x and the activations are not quantised, unlike in
+ * moe_forward's fp8 precisions (the activations are rounded to dtype between
+ * the two products, as in moe_forward).
+ *
+ * routing: logits, topk_ids and topk_w as in moe_forward; the other members
+ * are neither read nor written and may be NULL.  A slot can be empty: a given
+ * id outside [0, E), or, with logits, a selected logit of -inf (a masked
+ * expert; topk_ids then holds -1 and topk_w 0).  An empty slot adds nothing,
+ * whatever its weight, and a token whose slots are all empty (the padding of
+ * a batch) gets a row of zeros.  An id given twice in a row counts twice.
+ * NaN and infinities stay in the tokens they reach.
+ *
+ * workspace: moe_decode_workspace_size bytes, 256-byte aligned (no initial
+ * contents needed); calls that overlap in time, replayed graphs among them,
+ * need one each. */
+typedef enum { MOE_WEIGHTS_NATIVE = 0, MOE_WEIGHTS_FP8_BLOCK = 1, MOE_WEIGHTS_MXFP8 = 2 } moe_weight_format;
+moe_status moe_decode_workspace_size(const moe_shape* shape, size_t* bytes);
+moe_status moe_decode(const moe_shape* shape, int weights, const void* x, moe_routing* routing,
+                      const void* w_gate_up, const void* s_gate_up, const void* w_down,
+                      const void* s_down, void* out, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
 /* Dispatch alone ("token sorting": "Prime Mega MoE Trains Giant AI Models
  * 55% Faster", section "Where MoE training loses time"): xp[r] =
  * x[src_of[r] / k], xp [T*k, d] (dtype), rows in expert order; reads

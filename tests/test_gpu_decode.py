@@ -1,0 +1,266 @@
+"""The layer for few tokens (moe_decode) against a plain float64 evaluation.
+
+Tolerances.  The output of a bf16 call is off by: the rounding of the weighted
+SwiGLU output (each factor of every product within 2^-8), of the result
+(2^-8), float32 sums and the hardware exp and reciprocal (both far below).
+With s_t = sum over slots and columns of |w a W_down| an output's error is at
+most 2^-8 s_t + 2^-8 |out|; float32 calls: the products' sums run over K = d
+and I terms in float32, at most (d + I + 64) 2^-24 of the sums of magnitudes,
+through SwiGLU (whose slope stays below 1.1 in the gate and |silu| in the up
+value).  bound() adds these up from magnitudes computed in float64.
+"""
+import math
+
+import pytest
+import torch
+
+from combine_top_route_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda", 0)
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def weights64(w):
+    if isinstance(w, torch.Tensor):
+        return w.double()
+    codes, scales = w
+    v = codes.view(torch.float8_e4m3fn).double()
+    if scales.dtype == torch.float32:
+        return v * scales.double().repeat_interleave(128, 1).repeat_interleave(128, 2)
+    return v * torch.exp2(scales.double() - 127.0).repeat_interleave(32, 2)
+
+
+def topk64(logits, k):
+    v, i = torch.sort(logits.double(), dim=1, descending=True, stable=True)
+    v, i = v[:, :k], i[:, :k]
+    none = v == -math.inf
+    w = torch.where(none, 0.0, torch.exp(v - v[:, :1]))
+    w = torch.where(none, 0.0, w / w.sum(1, keepdim=True))
+    return torch.where(none, -1, i), w
+
+
+def plain(x, wgu, wd, ids, w, limit=0.0, eps_act=2.0 ** -8, eps_out=2.0 ** -8):
+    """(out, error bound), float64 [T, d]."""
+    x, wgu, wd = x.double(), weights64(wgu), weights64(wd)
+    E, two_i, d = wgu.shape
+    I = two_i // 2
+    lim = limit if limit > 0 else math.inf
+    out = torch.zeros_like(x)
+    mag = torch.zeros_like(x)
+    sums = (d + I + 64) * 2.0 ** -24
+    for t in range(x.shape[0]):
+        for j in range(ids.shape[1]):
+            e = int(ids[t, j])
+            if not 0 <= e < E:
+                continue
+            h = wgu[e] @ x[t]
+            dh = sums * (wgu[e].abs() @ x[t].abs())
+            g, u = h[:I], h[I:]
+            gc, uc = g.clamp(max=lim), u.clamp(-lim, lim)
+            a = gc * torch.sigmoid(gc) * uc
+            da = 1.1 * dh[:I] * uc.abs() + (gc * torch.sigmoid(gc)).abs() * dh[I:] + 1e-6 * a.abs()
+            wj = float(w[t, j])
+            out[t] += wj * (wd[e] @ a)
+            mag[t] += abs(wj) * (wd[e].abs() @ ((eps_act + sums) * a.abs() + da))
+    return out, mag + (eps_out + sums) * out.abs() + 1e-30
+
+
+def make(T, d, E, k, I, dtype="bf16", weights="native", seed=0, scale=1.0):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    dt = DT[dtype]
+    rn = lambda *s: torch.randn(s, generator=g, device=DEV)
+    x = (scale * rn(T, d)).to(dt)
+    wgu = (rn(E, 2 * I, d) * d ** -0.5).to(dt)
+    wd = (rn(E, d, I) * I ** -0.5).to(dt)
+    logits = rn(T, E)
+    if weights == "fp8_block":
+        wgu, wd = B.quantize_fp8(wgu, B.QUANT_WEIGHT), B.quantize_fp8(wd, B.QUANT_WEIGHT)
+    elif weights == "mxfp8":
+        wgu, wd = B.quantize_mxfp8(wgu, B.QUANT_WEIGHT), B.quantize_mxfp8(wd, B.QUANT_WEIGHT)
+    return x, wgu, wd, logits
+
+
+def decoder(x, E, k, I, weights="native", limit=0.0, max_T=None, logits_dtype=torch.float32):
+    T, d = x.shape
+    return B.MoeDecoder(max_T or T, d, E, k, I, dtype=x.dtype, logits_dtype=logits_dtype, weights=weights,
+                        device=DEV, swiglu_limit=limit)
+
+
+def check(got, x, wgu, wd, ids, w, limit=0.0):
+    eps = (2.0 ** -24 if x.dtype == torch.float32 else 2.0 ** -8)
+    ref, tol = plain(x, wgu, wd, ids, w, limit, eps_act=eps, eps_out=eps)
+    err = (got.double() - ref).abs()
+    assert bool((err <= tol).all()), f"worst error over bound {float((err / tol).max()):.3g}"
+
+
+# one token, odd counts, exactly one and just over one column block, up to the
+# largest; extents with K tails and partial row tiles; one expert; k = E
+CASES = [
+    # T, d, E, k, I, dtype, weights
+    (1, 256, 16, 4, 128, "bf16", "native"),
+    (1, 8, 1, 1, 8, "bf16", "native"),
+    (3, 72, 5, 5, 40, "bf16", "native"),
+    (16, 200, 7, 3, 104, "bf16", "native"),
+    (17, 200, 7, 3, 104, "bf16", "native"),
+    (33, 136, 1, 1, 264, "bf16", "native"),
+    (64, 264, 3, 2, 72, "bf16", "native"),
+    (100, 64, 2, 1, 24, "bf16", "native"),
+    (256, 136, 40, 6, 40, "bf16", "native"),
+    (5, 1000, 19, 3, 360, "f32", "native"),
+    (1, 8, 2, 2, 8, "f32", "native"),
+    (16, 40, 9, 9, 24, "f32", "native"),
+    (49, 104, 4, 2, 56, "f32", "native"),
+    (1, 128, 4, 2, 128, "bf16", "fp8_block"),
+    (9, 384, 6, 2, 256, "bf16", "fp8_block"),
+    (70, 256, 3, 3, 128, "bf16", "fp8_block"),
+    (2, 256, 8, 8, 384, "bf16", "mxfp8"),
+    (40, 128, 2, 1, 128, "bf16", "mxfp8"),
+    (130, 384, 12, 4, 256, "bf16", "mxfp8"),
+]
+
+
+@pytest.mark.parametrize("T,d,E,k,I,dtype,weights", CASES)
+def test_logits_form(T, d, E, k, I, dtype, weights):
+    x, wgu, wd, logits = make(T, d, E, k, I, dtype, weights)
+    for lt in (torch.float32, torch.bfloat16):
+        lg = logits.to(lt)
+        dec = decoder(x, E, k, I, weights, logits_dtype=lt)
+        got = dec.forward(x, wgu, wd, logits=lg)
+        ids, w = topk64(lg, k)
+        assert torch.equal(dec.topk_ids.long(), ids)
+        assert float((dec.topk_w.double() - w).abs().max()) <= 1e-6
+        check(got, x, wgu, wd, ids, w)
+
+
+@pytest.mark.parametrize("T,d,E,k,I,dtype,weights", CASES)
+def test_ids_form_with_empty_slots_and_repeats(T, d, E, k, I, dtype, weights):
+    x, wgu, wd, _ = make(T, d, E, k, I, dtype, weights, seed=1)
+    g = torch.Generator().manual_seed(2)
+    ids = torch.randint(-2, E + 2, (T, k), generator=g, dtype=torch.int32)   # repeats and ids outside
+    w = torch.randn((T, k), generator=g)
+    ids[T // 2] = -1                                                         # a row left empty
+    w[ids < 0] = float("nan")                                                # an empty slot's weight is not read
+    ids, w = ids.to(DEV), w.to(DEV)
+    dec = decoder(x, E, k, I, weights, limit=0.75)
+    got = dec.forward(x, wgu, wd, topk_ids=ids, topk_w=w)
+    check(got, x, wgu, wd, ids, w, limit=0.75)
+    assert not bool(got[T // 2].any())
+    assert dec.topk_ids is ids and dec.topk_w is w
+
+
+def test_masked_logits():
+    """-inf logits are empty slots: none left, fewer left than k, ties."""
+    T, d, E, k, I = 6, 64, 8, 4, 32
+    x, wgu, wd, lg = make(T, d, E, k, I)
+    inf = float("inf")
+    lg[0] = -inf
+    lg[1, 1:] = -inf
+    lg[2, :] = -inf
+    lg[2, 5:7] = torch.finfo(torch.float32).min    # the type's lowest value is a value
+    lg[3] = 0.0
+    lg[3, ::2] = -0.0                               # -0 ties with +0: lowest index first
+    lg[4, 3] = 200.0
+    dec = decoder(x, E, k, I)
+    got = dec.forward(x, wgu, wd, logits=lg)
+    ids, w = topk64(lg, k)
+    assert torch.equal(dec.topk_ids.long(), ids)
+    assert dec.topk_ids[0].tolist() == [-1] * 4 and dec.topk_ids[2].tolist() == [5, 6, -1, -1]
+    assert dec.topk_ids[3].tolist() == [0, 1, 2, 3]
+    check(got, x, wgu, wd, ids, w)
+    assert not bool(got[0].any())
+
+
+@pytest.mark.parametrize("T", [5, 40])
+def test_nan_and_infinity_stay_where_they_are(T):
+    """A token's NaN reaches its own row alone; an expert's, the tokens that
+    chose it; an empty token's row is zero whatever it holds."""
+    d, E, k, I = 72, 6, 2, 40
+    x, wgu, wd, _ = make(T, d, E, k, I)
+    ids = (torch.arange(T, device=DEV)[:, None] % 3 + torch.tensor([0, 3], device=DEV)).to(torch.int32).contiguous()
+    w = torch.full((T, k), 0.5, device=DEV)
+    ids[4] = -1
+    x[1, 7] = float("nan")
+    x[4] = float("inf")
+    wgu[2, 3, 5] = float("nan")       # experts 2 and 5: tokens 2, 5, 8, ...
+    wd[2, 11, 0] = float("inf")
+    dec = decoder(x, E, k, I)
+    got = dec.forward(x, wgu, wd, topk_ids=ids, topk_w=w)
+    hit = torch.arange(T, device=DEV) % 3 == 2
+    hit[4] = False
+    ok = ~hit
+    ok[1] = False
+    assert bool(got[1].isnan().all()) and bool(got[hit].isnan().all())
+    x1 = torch.where(ok[:, None], x, 0.0)
+    ids1 = torch.where(ok[:, None], ids, -1)
+    check(torch.where(ok[:, None], got, 0.0), x1, wgu.nan_to_num(0, 0), wd.nan_to_num(0, 0, 0), ids1, w)
+    assert not bool(got[4].any())
+
+
+def test_smaller_batches_leave_the_rows_behind_alone():
+    d, E, k, I = 64, 8, 2, 32
+    x, wgu, wd, lg = make(40, d, E, k, I)
+    dec = decoder(x, E, k, I)
+    full = dec.forward(x, wgu, wd, logits=lg).clone()
+    ids_full = dec.topk_ids.clone()
+    for T in (7, 40, 1, 17):
+        part = dec.forward(x[:T], wgu, wd, logits=lg[:T])
+        assert part.shape == (T, d) and torch.equal(dec.topk_ids, ids_full[:T])
+        ids, w = topk64(lg[:T], k)
+        check(part, x[:T], wgu, wd, ids, w)
+    dec._out.copy_(full)
+    dec.forward(x[:7], wgu, wd, logits=lg[:7])
+    assert torch.equal(dec._out[7:], full[7:])
+
+
+def test_same_as_the_layer_forward():
+    """Against moe_forward on the same inputs: both round the activations and
+    the result to bf16, so they differ by at most twice the bound."""
+    T, d, E, k, I = 24, 256, 8, 2, 128
+    x, wgu, wd, lg = make(T, d, E, k, I)
+    lg = lg.bfloat16()
+    layer = B.MoeLayer(T, d, E, k, I, device=DEV)
+    want = layer.forward(x, wgu, wd, logits=lg)
+    dec = decoder(x, E, k, I, logits_dtype=torch.bfloat16)
+    got = dec.forward(x, wgu, wd, logits=lg)
+    assert torch.equal(dec.topk_ids, layer.routing.topk_ids)
+    ids, w = topk64(lg, k)
+    _, tol = plain(x, wgu, wd, ids, w)
+    # the layer also rounds each slot's product before the combine
+    assert bool(((got.double() - want.double()).abs() <= 4 * tol).all())
+
+
+def test_repeatable_and_on_another_stream():
+    T, d, E, k, I = 20, 136, 8, 3, 72
+    x, wgu, wd, lg = make(T, d, E, k, I)
+    dec = decoder(x, E, k, I)
+    want = dec.forward(x, wgu, wd, logits=lg).clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        again = dec.forward(x, wgu, wd, logits=lg).clone()
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(want, again)
+
+
+@pytest.mark.parametrize("T", [1, 30])
+def test_captured_and_replayed(T):
+    d, E, k, I = 128, 8, 2, 64
+    x, wgu, wd, lg = make(T, d, E, k, I)
+    dec = decoder(x, E, k, I)
+    dec.forward(x, wgu, wd, logits=lg)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = dec.forward(x, wgu, wd, logits=lg)
+    eager = decoder(x, E, k, I)
+    for i in range(4):
+        x.copy_(make(T, d, E, k, I, seed=10 + i)[0])
+        lg.copy_(make(T, d, E, k, I, seed=10 + i)[3])
+        dec.workspace.fill_(255)            # nothing is expected in the workspace
+        graph.replay()
+        want = eager.forward(x, wgu, wd, logits=lg)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), i
