@@ -420,6 +420,9 @@ moe_status check_decode(const moe_shape* s) {
     return fail(MOE_ERR_UNSUPPORTED, "T=%lld above %d: moe_forward takes more tokens", (long long)s->T, kDecodeMaxT);
   if (s->precision != MOE_PREC_NATIVE)
     return fail(MOE_ERR_UNSUPPORTED, "moe_decode takes precision MOE_PREC_NATIVE; coded weights are its own argument");
+  // the kernels address the per-slot buffer with 32-bit byte offsets
+  if ((uint64_t)s->T * s->k * s->I * elem_size(s->dtype) > 0xfffffe00u)
+    return fail(MOE_ERR_UNSUPPORTED, "T*k*I values of dtype exceed 4 GiB");
   return MOE_OK;
 }
 

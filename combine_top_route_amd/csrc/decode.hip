@@ -18,6 +18,8 @@
 //   * nothing is sorted: each work-group finds its expert's tokens in the ids
 //     (at most 256 k of them).
 // All sums are float32 in a fixed order; there are no atomics.
+#include <type_traits>
+
 #include "common.h"
 #include "tile.h"
 
@@ -36,42 +38,64 @@ __device__ __forceinline__ float key_value(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
-constexpr int kKeysPerLane = kMaxExperts / kWave;
+// Largest v over the wave (every lane gets it).  Row rotations by DPP reduce
+// each row of 16 lanes, a broadcast of rows joins them in lane 63.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  auto step = [&](auto ctrl) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl.value, 0xf, 0xf, false);
+    v = o > v ? o : v;
+  };
+  step(std::integral_constant<int, 0x121>{});  // row_ror:1, 2, 4, 8
+  step(std::integral_constant<int, 0x122>{});
+  step(std::integral_constant<int, 0x124>{});
+  step(std::integral_constant<int, 0x128>{});
+  step(std::integral_constant<int, 0x142>{});  // row_bcast:15, 31
+  step(std::integral_constant<int, 0x143>{});
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
 
 // Top k of one token's logits, one wave per token: k rounds of a wave-wide
-// maximum over (ordered logit, ~expert) keys, so ties go to the lower index;
+// maximum; among equal logits the lowest index (lane e % 64 holds experts e,
+// e + 64, ..., so the first of its registers and then the lowest lane).  The
 // weights are the softmax over the selected logits, summed in slot order.  A
-// slot whose logit is -inf (a masked expert) is empty: id -1, weight 0.
-template <typename LT>
+// slot whose logit is -inf (a masked expert) is empty: id -1, weight 0.  NaN
+// counts as the largest value.  KPL: keys per lane, E <= 64 KPL.
+template <typename LT, int KPL>
 __global__ __launch_bounds__(64) void decode_topk_kernel(const LT* __restrict__ logits, int E, int k,
                                                          int32_t* __restrict__ ids, float* __restrict__ w,
                                                          int32_t* __restrict__ mid, float* __restrict__ mw) {
   const int lane = threadIdx.x, t = blockIdx.x;
   const LT* row = logits + (int64_t)t * E;
-  uint64_t key[kKeysPerLane];
+  uint32_t key[KPL];  // 0: taken, or past E
 #pragma unroll
-  for (int i = 0; i < kKeysPerLane; ++i) {
+  for (int i = 0; i < KPL; ++i) {
     const int e = lane + kWave * i;
-    key[i] = e < E ? ((uint64_t)order_key(to_f32<LT>(row[e])) << 32) | (uint32_t)~(uint32_t)e : 0;
+    key[i] = 0;
+    if (e < E) {
+      const float v = to_f32<LT>(row[e]);
+      key[i] = v != v ? 0xffffffffu : order_key(v);
+    }
   }
   float top = 0.0f, sum = 0.0f;
   for (int j = 0; j < k; ++j) {
-    uint64_t m = 0;
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kKeysPerLane; ++i) m = key[i] > m ? key[i] : m;
+    for (int i = 0; i < KPL; ++i) m = key[i] > m ? key[i] : m;
+    m = wave_max_u32(m);
+    int e = 0;
+    bool found = false;
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const uint64_t o = __shfl_xor(m, off, kWave);
-      m = o > m ? o : m;
+    for (int i = 0; i < KPL; ++i) {
+      const uint64_t eq = __ballot(key[i] == m);
+      if (!found && eq) {
+        const int l = __builtin_ctzll(eq);
+        e = i * kWave + l;
+        if (lane == l) key[i] = 0;
+        found = true;
+      }
     }
-    const int e = (int)~(uint32_t)m;
-    const float l = key_value((uint32_t)(m >> 32));
+    const float l = key_value(m);
     if (j == 0) top = l;
-    if ((e & 63) == lane) {
-#pragma unroll
-      for (int i = 0; i < kKeysPerLane; ++i)
-        if (i == (e >> 6)) key[i] = 0;
-    }
     const bool none = l == -__builtin_huge_valf();
     const float ex = none ? 0.0f : expf(l - top);
     sum += ex;
@@ -142,33 +166,36 @@ template <> struct Fmt<WF_BF16> {
   static constexpr int UK = 64, BV = 2, NF = 2;
 };
 
-// Byte offset, in a weight row, of this lane's chunk c of unit `unit`.
-__device__ __forceinline__ int64_t a_off(int unit, int c, int q) { return (int64_t)unit * 128 + c * 64 + q * 16; }
-
-// Loads chunk c of a unit; lanes past the row's `bytes` get zeros (from a
-// clamped address), so a K tail adds exact zeros on both operands.
-__device__ __forceinline__ u32x4_t load16(const char* row, int64_t off, bool ok) {
-  u32x4_t v = *(const u32x4_t*)(row + (ok ? off : 0));
-  if (!ok) v = u32x4_t{0, 0, 0, 0};
-  return v;
+// Loads go through buffer descriptors: a 32-bit offset per lane, and zeros for
+// a lane that asks past the end, which is how a K tail becomes exact zeros on
+// both operands (every buffer here is below kPast bytes).
+constexpr uint32_t kPast = 0xffffff00u;
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t buffer_of(const void* p, uint64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)(uint32_t)bytes, 0x00020000);
+}
+__device__ __forceinline__ u32x4_t load16(rsrc_t r, uint32_t off, bool ok) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)(ok ? off : kPast), 0, 0);
 }
 
-template <int F>
-__device__ __forceinline__ void load_a(u32x4_t (&a)[2], const char* row, int unit, int q, int64_t bytes) {
+// This lane's 32 bytes of a weight row's unit; row: the row's offset plus 16 q,
+// bytes: the row's length.
+__device__ __forceinline__ void load_a(u32x4_t (&a)[2], rsrc_t r, uint32_t row, int unit, int q, int bytes) {
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    const int64_t off = a_off(unit, c, q);
-    a[c] = load16(row, off, off < bytes);
+    const int off = unit * 128 + c * 64;
+    a[c] = load16(r, row + off, off + q * 16 < bytes);
   }
 }
 
-// The activations that meet load_a's bytes: the same values of K.
+// The activations that meet load_a's bytes: the same values of K.  row: the
+// token's offset.
 template <int F>
-__device__ __forceinline__ void load_b(u32x4_t (&b)[Fmt<F>::BV], const char* row, int unit, int q, int64_t bytes) {
+__device__ __forceinline__ void load_b(u32x4_t (&b)[Fmt<F>::BV], rsrc_t r, uint32_t row, int unit, int q, int bytes) {
 #pragma unroll
   for (int v = 0; v < Fmt<F>::BV; ++v) {
-    const int64_t off = F >= WF_FP8 ? (int64_t)unit * 256 + (v >> 1) * 128 + q * 32 + (v & 1) * 16 : a_off(unit, v, q);
-    b[v] = load16(row, off, off < bytes);
+    const int off = F >= WF_FP8 ? unit * 256 + (v >> 1) * 128 + q * 32 + (v & 1) * 16 : unit * 128 + v * 64 + q * 16;
+    b[v] = load16(r, row + off, off < bytes);
   }
 }
 
@@ -301,51 +328,71 @@ __device__ __forceinline__ int find_rows(Rows& rows, const int32_t* __restrict__
 
 // ------------------------------------------------------------ gate/up product
 // One work-group: 16 gate rows and the same 16 up rows of one expert, for all
-// of its tokens; 8 waves take the units of K in turn.
-constexpr int kGuWaves = 8;
+// of its tokens; the NW waves take the units of K in turn, UN at a time.
+template <int F, int UN>
+struct GuWeights {  // UN units of this lane's gate and up row, in flight
+  u32x4_t g[UN][2], u[UN][2];
+  uint32_t mg[UN], mu[UN];
+};
 
-template <int F, int NB, int UN>
-__device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, const char* wg,
-                                            const char* wu, const void* sc, int n0, int row, float* red) {
+template <int F, int NW, int UN>
+__device__ __forceinline__ void load_gu(GuWeights<F, UN>& w, rsrc_t wr, const void* sc, int I, int K, int row,
+                                        int base, int q) {
+  const int units = (K + Fmt<F>::UK - 1) / Fmt<F>::UK;
+  const int bytes = F >= WF_FP8 ? K : K * (int)sizeof(typename Fmt<F>::act);
+  const uint32_t g = (uint32_t)row * bytes + q * 16, u = (uint32_t)(I + row) * bytes + q * 16;
+#pragma unroll
+  for (int i = 0; i < UN; ++i) {
+    const int unit = base + i * NW, us = min(unit, units - 1);
+    load_a(w.g[i], wr, g, unit, q, bytes);
+    load_a(w.u[i], wr, u, unit, q, bytes);
+    w.mg[i] = mx_word_of<F>(sc, row, K, us);
+    w.mu[i] = mx_word_of<F>(sc, I + row, K, us);
+  }
+}
+
+// The tokens r0 .. r0 + 16 NB of the expert.  w holds the first units; UB
+// units' activations are loaded at a time (they come from the caches).
+template <int F, int NW, int UN, int NB, int UB>
+__device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& rows, int r0, int n,
+                                            GuWeights<F, UN>& w, rsrc_t wr, const void* sc, int n0, int row,
+                                            float* red) {
   typedef typename Fmt<F>::act AT;
   const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
   const int K = a.d;
   const int units = (K + Fmt<F>::UK - 1) / Fmt<F>::UK;
-  const int64_t abytes = F >= WF_FP8 ? K : (int64_t)K * sizeof(AT), bbytes = (int64_t)K * sizeof(AT);
-  const char* xr[NB];
+  const int bytes = K * (int)sizeof(AT);
+  const rsrc_t xb = buffer_of(a.x, (uint64_t)a.T * bytes);
+  uint32_t xr[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const int r = min(r0 + b * 16 + col, n - 1);  // columns past the last token repeat it and are dropped
-    xr[b] = (const char*)a.x + (int64_t)(rows.slot[r] / a.k) * K * sizeof(AT);
+    xr[b] = (uint32_t)(rows.slot[r] / a.k) * bytes;
   }
   f32x4_t ag[NB], au[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) ag[b] = au[b] = f32x4_t{0, 0, 0, 0};
-  for (int base = wave; base < units; base += kGuWaves * UN) {
-    u32x4_t wgv[UN][2], wuv[UN][2], xv[UN][NB][Fmt<F>::BV];
-    uint32_t mg[UN], mu[UN];
+  for (int base = wave; base < units; base += NW * UN) {
+    if (base != wave || r0) load_gu<F, NW, UN>(w, wr, sc, a.I, K, row, base, q);
 #pragma unroll
-    for (int i = 0; i < UN; ++i) {
-      const int unit = base + i * kGuWaves;
-      load_a<F>(wgv[i], wg, unit, q, abytes);
-      load_a<F>(wuv[i], wu, unit, q, abytes);
-      const int us = min(unit, units - 1);
-      mg[i] = mx_word_of<F>(sc, row, K, us);
-      mu[i] = mx_word_of<F>(sc, a.I + row, K, us);
+    for (int i0 = 0; i0 < UN; i0 += UB) {
+      u32x4_t xv[UB][NB][Fmt<F>::BV];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) load_b<F>(xv[i][b], xr[b], unit, q, bbytes);
-    }
+      for (int i = 0; i < UB; ++i)
 #pragma unroll
-    for (int i = 0; i < UN; ++i) {
-      const int us = min(base + i * kGuWaves, units - 1);
-      typename Fmt<F>::frag fg[Fmt<F>::NF], fu[Fmt<F>::NF];
-      to_frags<F>(fg, wgv[i], mg[i], q);
-      to_frags<F>(fu, wuv[i], mu[i], q);
-      const float sg = block_scale_of<F>(sc, n0, K, us), su = block_scale_of<F>(sc, a.I + n0, K, us);
+        for (int b = 0; b < NB; ++b) load_b<F>(xv[i][b], xb, xr[b], base + (i0 + i) * NW, q, bytes);
+      __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        unit_mma<F>(ag[b], fg, xv[i][b], sg);
-        unit_mma<F>(au[b], fu, xv[i][b], su);
+      for (int i = 0; i < UB; ++i) {
+        const int us = min(base + (i0 + i) * NW, units - 1);
+        const float sg = block_scale_of<F>(sc, n0, K, us), su = block_scale_of<F>(sc, a.I + n0, K, us);
+        typename Fmt<F>::frag fr[Fmt<F>::NF];
+        to_frags<F>(fr, w.g[i0 + i], w.mg[i0 + i], q);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) unit_mma<F>(ag[b], fr, xv[i][b], sg);
+        to_frags<F>(fr, w.u[i0 + i], w.mu[i0 + i], q);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) unit_mma<F>(au[b], fr, xv[i][b], su);
       }
     }
   }
@@ -357,14 +404,14 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
     *(f32x4_t*)(p + 256) = au[b];
   }
   __syncthreads();
-  for (int o = threadIdx.x; o < NB * 256; o += kGuWaves * 64) {
+  for (int o = threadIdx.x; o < NB * 256; o += NW * 64) {
     const int b = o >> 8, c = (o >> 4) & 15, m = o & 15;
     const int r = r0 + b * 16 + c;
     if (r < n && n0 + m < a.I) {
       float g = 0.0f, u = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kGuWaves; ++w) {
-        const float* p = red + ((w * NB + b) * 2 * 16 + c) * 16 + m;
+      for (int v = 0; v < NW; ++v) {
+        const float* p = red + ((v * NB + b) * 2 * 16 + c) * 16 + m;
         g += p[0];
         u += p[256];
       }
@@ -374,31 +421,34 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
   __syncthreads();
 }
 
-template <int F, int NBMAX>
-__global__ __launch_bounds__(kGuWaves * 64) void decode_gateup_kernel(DecodeArgs a) {
+template <int F, int NBMAX, int NW, int UN>
+__global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   __shared__ Rows rows;
-  __shared__ float red[kGuWaves * NBMAX * 512];
-  const int e = item_expert(a.mid, blockIdx.y, a.T * a.k, a.E);
+  __shared__ float red[NW * NBMAX * 512];
+  const int e = __builtin_amdgcn_readfirstlane(item_expert(a.mid, blockIdx.y, a.T * a.k, a.E));
   if (e < 0) return;
-  const int n = find_rows(rows, a.mid, a.mw, e, a.T, a.k);
-  if (n == 0) return;
+  const int lane = threadIdx.x & 63, q = lane >> 4;
   const int n0 = blockIdx.x * 16;
-  const int row = min(n0 + (int)(threadIdx.x & 15), a.I - 1);  // rows past I repeat the last and are dropped
+  const int row = min(n0 + (lane & 15), a.I - 1);  // rows past I repeat the last and are dropped
   const int64_t wb = F >= WF_FP8 ? 1 : sizeof(typename Fmt<F>::act);
-  const char* w = (const char*)a.w_gate_up + (int64_t)e * 2 * a.I * a.d * wb;
-  const char* wg = w + (int64_t)row * a.d * wb;
-  const char* wu = w + (int64_t)(a.I + row) * a.d * wb;
+  const uint64_t wbytes = (uint64_t)2 * a.I * a.d * wb;
+  const rsrc_t wr = buffer_of((const char*)a.w_gate_up + e * wbytes, wbytes);
   const char* sc = (const char*)a.s_gate_up;
   if (F == WF_FP8) sc += (int64_t)e * (2 * a.I / 128) * (a.d / 128) * 4;
   if (F == WF_MX) sc += (int64_t)e * 2 * a.I * (a.d / 32);
+  const int n = find_rows(rows, a.mid, a.mw, e, a.T, a.k);
+  if (n == 0) return;
+  GuWeights<F, UN> w;
+  load_gu<F, NW, UN>(w, wr, sc, a.I, a.d, row, tile::wave_id(), q);
+  constexpr int UB1 = F >= WF_FP8 ? (UN > 2 ? 2 : UN) : UN;
   if constexpr (NBMAX == 1) {
-    gateup_rows<F, 1, 4>(a, rows, 0, n, wg, wu, sc, n0, row, red);
+    gateup_rows<F, NW, UN, 1, UB1>(a, rows, 0, n, w, wr, sc, n0, row, red);
   } else {
     for (int r0 = 0; r0 < n; r0 += 64) {
       const int left = n - r0;
-      if (left <= 16) gateup_rows<F, 1, 4>(a, rows, r0, n, wg, wu, sc, n0, row, red);
-      else if (left <= 32) gateup_rows<F, 2, 2>(a, rows, r0, n, wg, wu, sc, n0, row, red);
-      else gateup_rows<F, 4, 1>(a, rows, r0, n, wg, wu, sc, n0, row, red);
+      if (left <= 16) gateup_rows<F, NW, UN, 1, UB1>(a, rows, r0, n, w, wr, sc, n0, row, red);
+      else if (left <= 32) gateup_rows<F, NW, UN, 2, (UB1 + 1) / 2>(a, rows, r0, n, w, wr, sc, n0, row, red);
+      else gateup_rows<F, NW, UN, 4, 1>(a, rows, r0, n, w, wr, sc, n0, row, red);
     }
   }
 }
@@ -445,8 +495,10 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_kernel(DecodeArgs
   const int K = a.I, n0 = blockIdx.x * 16;
   const int row = min(n0 + col, a.d - 1);
   const int units = (K + Fmt<F>::UK - 1) / Fmt<F>::UK;
-  const int64_t wb = F >= WF_FP8 ? 1 : sizeof(AT);
-  const int64_t abytes = K * wb, bbytes = (int64_t)K * sizeof(AT);
+  const int abytes = F >= WF_FP8 ? K : K * (int)sizeof(AT), bbytes = K * (int)sizeof(AT);
+  const uint64_t wbytes = (uint64_t)a.d * abytes;
+  const uint32_t wrow = (uint32_t)row * abytes + q * 16;
+  const rsrc_t xb = buffer_of(a.aw, (uint64_t)a.T * a.k * bbytes);
   const int total = nact * units;
   constexpr int UN = 4;
   f32x4_t acc = {0, 0, 0, 0};
@@ -463,16 +515,15 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_kernel(DecodeArgs
       const int e = __builtin_amdgcn_readfirstlane(active[idx]);
       const int j = col < a.T ? tab[e * a.T + col] : 0;
       const bool mine = on_expert[i] = live && j != 0;
-      const char* w = (const char*)a.w_down + ((int64_t)e * a.d + row) * abytes;
-      const char* x = (const char*)a.aw + (mine ? (int64_t)(col * a.k + j - 1) * bbytes : 0);
-      load_a<F>(wv[i], w, unit, q, live ? abytes : 0);
-      load_b<F>(xv[i], x, unit, q, mine ? bbytes : 0);
+      load_a(wv[i], buffer_of((const char*)a.w_down + e * wbytes, wbytes), wrow, unit, q, live ? abytes : 0);
+      load_b<F>(xv[i], xb, (uint32_t)(col * a.k + j - 1) * bbytes, unit, q, mine ? bbytes : 0);
       const char* sc = (const char*)a.s_down;
       if (F == WF_FP8) sc += (int64_t)e * (a.d / 128) * (K / 128) * 4;
       if (F == WF_MX) sc += (int64_t)e * a.d * (K / 32);
       mx[i] = mx_word_of<F>(sc, row, K, unit);
       sb[i] = block_scale_of<F>(sc, n0, K, unit);
     }
+    __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
       typename Fmt<F>::frag fr[Fmt<F>::NF];
@@ -503,17 +554,18 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_kernel(DecodeArgs
 constexpr int kDownRowWaves = 4;
 
 template <int F, int NB, int UN>
-__device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, const char* w,
+__device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, rsrc_t wr,
                                           const void* sc, int n0, int row) {
   typedef typename Fmt<F>::act AT;
   const int lane = threadIdx.x & 63, q = lane >> 4, col = lane & 15;
   const int K = a.I;
   const int units = (K + Fmt<F>::UK - 1) / Fmt<F>::UK;
-  const int64_t abytes = F >= WF_FP8 ? K : (int64_t)K * sizeof(AT), bbytes = (int64_t)K * sizeof(AT);
-  const char* xr[NB];
+  const int abytes = F >= WF_FP8 ? K : K * (int)sizeof(AT), bbytes = K * (int)sizeof(AT);
+  const uint32_t wrow = (uint32_t)row * abytes + q * 16;
+  const rsrc_t xb = buffer_of(a.aw, (uint64_t)a.T * a.k * bbytes);
+  uint32_t xr[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-    xr[b] = (const char*)a.aw + (int64_t)rows.slot[min(r0 + b * 16 + col, n - 1)] * bbytes;
+  for (int b = 0; b < NB; ++b) xr[b] = (uint32_t)rows.slot[min(r0 + b * 16 + col, n - 1)] * bbytes;
   f32x4_t acc[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) acc[b] = f32x4_t{0, 0, 0, 0};
@@ -522,11 +574,12 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
     uint32_t mx[UN];
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
-      load_a<F>(wv[i], w, base + i, q, abytes);
+      load_a(wv[i], wr, wrow, base + i, q, abytes);
       mx[i] = mx_word_of<F>(sc, row, K, min(base + i, units - 1));
 #pragma unroll
-      for (int b = 0; b < NB; ++b) load_b<F>(xv[i][b], xr[b], base + i, q, bbytes);
+      for (int b = 0; b < NB; ++b) load_b<F>(xv[i][b], xb, xr[b], base + i, q, bbytes);
     }
+    __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
       typename Fmt<F>::frag fr[Fmt<F>::NF];
@@ -547,22 +600,23 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
 template <int F>
 __global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(DecodeArgs a) {
   __shared__ Rows rows;
-  const int e = item_expert(a.mid, blockIdx.y, a.T * a.k, a.E);
+  const int e = __builtin_amdgcn_readfirstlane(item_expert(a.mid, blockIdx.y, a.T * a.k, a.E));
   if (e < 0) return;
   const int n = find_rows(rows, a.mid, a.mw, e, a.T, a.k);
   const int n0 = (blockIdx.x * kDownRowWaves + tile::wave_id()) * 16;
   if (n == 0 || n0 >= a.d) return;  // no barrier follows
   const int row = min(n0 + (int)(threadIdx.x & 15), a.d - 1);
   const int64_t wb = F >= WF_FP8 ? 1 : sizeof(typename Fmt<F>::act);
-  const char* w = (const char*)a.w_down + ((int64_t)e * a.d + row) * a.I * wb;
+  const uint64_t wbytes = (uint64_t)a.d * a.I * wb;
+  const rsrc_t wr = buffer_of((const char*)a.w_down + e * wbytes, wbytes);
   const char* sc = (const char*)a.s_down;
   if (F == WF_FP8) sc += (int64_t)e * (a.d / 128) * (a.I / 128) * 4;
   if (F == WF_MX) sc += (int64_t)e * a.d * (a.I / 32);
   for (int r0 = 0; r0 < n; r0 += 64) {
     const int left = n - r0;
-    if (left <= 16) down_rows<F, 1, 4>(a, rows, r0, n, w, sc, n0, row);
-    else if (left <= 32) down_rows<F, 2, 2>(a, rows, r0, n, w, sc, n0, row);
-    else down_rows<F, 4, 1>(a, rows, r0, n, w, sc, n0, row);
+    if (left <= 16) down_rows<F, 1, 4>(a, rows, r0, n, wr, sc, n0, row);
+    else if (left <= 32) down_rows<F, 2, 2>(a, rows, r0, n, wr, sc, n0, row);
+    else down_rows<F, 4, 1>(a, rows, r0, n, wr, sc, n0, row);
   }
 }
 
@@ -590,13 +644,14 @@ hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
   const int R = a.T * a.k;
   const unsigned items = (unsigned)(R > a.E ? a.E : R);
   const dim3 gu((unsigned)cdiv(a.I, 16), items);
+  constexpr int UN = F >= WF_FP8 ? 2 : 4;
   if (a.T <= 16) {
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1>), gu, dim3(kGuWaves * 64), 0, a);
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 8, UN>), gu, dim3(8 * 64), 0, a);
     const size_t smem = kDownWaves * 1024 + (size_t)a.E * 4 + (size_t)a.E * a.T * 2;  // at most 52 KB
     MOE_LAUNCH(c, "decode_down", decode_down_kernel<F>, dim3((unsigned)cdiv(a.d, 16)), dim3(kDownWaves * 64), smem, a);
     return hipSuccess;
   }
-  MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 4>), gu, dim3(kGuWaves * 64), 0, a);
+  MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 4, 4, UN / 2>), gu, dim3(4 * 64), 0, a);
   MOE_LAUNCH(c, "decode_down", decode_down_rows_kernel<F>, dim3((unsigned)cdiv(a.d, 16 * kDownRowWaves), items),
              dim3(kDownRowWaves * 64), 0, a);
   const dim3 cg((unsigned)cdiv(a.d, 1024), (unsigned)a.T);
@@ -609,14 +664,22 @@ hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
 
 hipError_t launch_decode(const LaunchCtx& c, const DecodeArgs& a, const void* logits, int logits_dtype, int32_t* ids,
                          float* w, int weights) {
+#define TOPK(LT, KPL)                                                                                   \
+  MOE_LAUNCH(c, "decode_route", (decode_topk_kernel<LT, KPL>), dim3((unsigned)a.T), dim3(64), 0,        \
+             (const LT*)logits, a.E, a.k, ids, w, a.mid, a.mw)
+#define TOPK_E(LT)                    \
+  if (a.E <= 128) TOPK(LT, 2);        \
+  else if (a.E <= 512) TOPK(LT, 8);   \
+  else TOPK(LT, 16)
   if (!logits)
     MOE_LAUNCH(c, "decode_route", decode_ids_kernel, dim3((unsigned)a.T), dim3(64), 0, ids, w, a.E, a.k, a.mid, a.mw);
-  else if (logits_dtype == F32)
-    MOE_LAUNCH(c, "decode_route", decode_topk_kernel<float>, dim3((unsigned)a.T), dim3(64), 0, (const float*)logits,
-               a.E, a.k, ids, w, a.mid, a.mw);
-  else
-    MOE_LAUNCH(c, "decode_route", decode_topk_kernel<bf16_t>, dim3((unsigned)a.T), dim3(64), 0,
-               (const bf16_t*)logits, a.E, a.k, ids, w, a.mid, a.mw);
+  else if (logits_dtype == F32) {
+    TOPK_E(float);
+  } else {
+    TOPK_E(bf16_t);
+  }
+#undef TOPK_E
+#undef TOPK
   if (weights == 1) return run<WF_FP8>(c, a);
   if (weights == 2) return run<WF_MX>(c, a);
   return a.dtype == F32 ? run<WF_F32>(c, a) : run<WF_BF16>(c, a);

@@ -252,8 +252,8 @@ moe_status moe_backward(const moe_shape* shape, const void* dout, const void* x,
  * with the combine (more than 16 tokens: the combine on its own).
  *
  * shape: T <= 256 and precision MOE_PREC_NATIVE (MOE_ERR_UNSUPPORTED
- * otherwise; moe_forward takes more tokens); dtype is that of x and out;
- * flags are ignored.  weights names the expert weights' format:
+ * otherwise; moe_forward takes more tokens), T*k*I values of dtype below
+ * 4 GiB - 512; dtype is that of x and out; flags are ignored.  weights names the expert weights' format:
  *   MOE_WEIGHTS_NATIVE:    in dtype; s_gate_up and s_down are NULL;
  *   MOE_WEIGHTS_FP8_BLOCK: what moe_quantize_fp8 MOE_QUANT_WEIGHT writes:
  *                          codes, and fp32 scales [E, 2I/128, d/128] and

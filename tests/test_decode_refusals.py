@@ -37,7 +37,8 @@ def test_workspace_sizes():
     # grows with T, so a workspace for the largest batch serves the smaller
     sizes = [size(shape(T=T))[1] for T in range(1, 257)]
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
-    assert size(shape(T=256, E=1024, k=1024, I=16384, d=16384))[1] > 1 << 33  # beyond 32 bits
+    assert size(shape(T=256, E=1024, k=256, I=16384, d=16384))[1] > 1 << 32   # sizes beyond 32 bits
+    assert size(shape(T=256, E=1024, k=512, I=16384))[0] == 2 and b"4 GiB" in B.lib().moe_last_error()
     assert size(shape(T=257))[0] == 2 and b"moe_forward" in B.lib().moe_last_error()
     assert size(shape(T=0))[0] == 1
     assert size(shape(precision="fp8_block"))[0] == 2
