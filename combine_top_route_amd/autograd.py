@@ -200,13 +200,109 @@ def _backward(ctx, dout, *unused):
 moe_fwd.register_autograd(_backward, setup_context=_setup_context)
 
 
+# The same pair with the 8-bit activation checkpoint (moe_forward8 and
+# moe_backward8): `saved` holds H as e4m3 codes and scale bytes.
+@torch.library.custom_op(f"{_NS}::moe_fwd8", mutates_args=())
+def moe_fwd8(x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: Tensor, k: int, swiglu_limit: float = 0.0
+             ) -> tuple[Tensor, Tensor, Tensor, Tensor, Tensor, Tensor, Tensor, Tensor]:
+    """Layer forward.  Returns (out [T,d], saved8 (uint8), topk_ids, topk_w,
+    counts, offsets, row_of, src_of)."""
+    _check_layer_args(x, logits, w_gate_up, w_down, k, "native")
+    _check_devices(x=x, logits=logits, w_gate_up=w_gate_up, w_down=w_down)
+    shape = _shape(x, logits, w_gate_up, k, "native", swiglu_limit)
+    T, d = x.shape
+    E = w_gate_up.shape[0]
+    dev = x.device
+    with B._on(dev):
+        out = torch.empty((T, d), dtype=x.dtype, device=dev)
+        saved = torch.empty(B.saved8_size(shape), dtype=torch.uint8, device=dev)
+        rt = _routing_empty(T, E, k, dev)
+        cr = B.Routing(*rt, logits=logits).c()
+        ws = torch.empty(B.workspace8_size(shape, B.OP_FORWARD), dtype=torch.uint8, device=dev)
+        B._check("moe_forward8", B.lib().moe_forward8(
+            ctypes.byref(shape), B._ptr(x), ctypes.byref(cr), B._ptr(w_gate_up), B._ptr(w_down), B._ptr(out),
+            B._ptr(saved), B._ptr(ws), ws.numel(), B._stream(dev)))
+    return (out, saved) + rt
+
+
+@moe_fwd8.register_fake
+def _(x, logits, w_gate_up, w_down, k, swiglu_limit=0.0):
+    T, d = x.shape
+    E = w_gate_up.shape[0]
+    n = B.saved8_size(_shape(x, logits, w_gate_up, k, "native", swiglu_limit))
+    i32 = dict(dtype=torch.int32)
+    return (x.new_empty((T, d)), x.new_empty((n,), dtype=torch.uint8), x.new_empty((T, k), **i32),
+            x.new_empty((T, k), dtype=torch.float32), x.new_empty((E,), **i32),
+            x.new_empty((E + 1,), **i32), x.new_empty((T * k,), **i32), x.new_empty((T * k,), **i32))
+
+
+@torch.library.custom_op(f"{_NS}::moe_bwd8", mutates_args=())
+def moe_bwd8(dout: Tensor, x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: Tensor, saved: Tensor,
+             topk_ids: Tensor, topk_w: Tensor, counts: Tensor, offsets: Tensor, row_of: Tensor,
+             src_of: Tensor, k: int, swiglu_limit: float = 0.0) -> tuple[Tensor, Tensor, Tensor, Tensor]:
+    """Layer backward from the 8-bit checkpoint: (dx, dlogits, dw_gate_up,
+    dw_down)."""
+    _check_layer_args(x, logits, w_gate_up, w_down, k, "native")
+    dout = dout.contiguous()
+    _check_backward_args(dout, x, saved, (topk_ids, topk_w, counts, offsets, row_of, src_of), k, "native")
+    shape = _shape(x, logits, w_gate_up, k, "native", swiglu_limit)
+    _require(saved.numel() == B.saved8_size(shape),
+             f"saved holds {saved.numel()} bytes, expected {B.saved8_size(shape)}")
+    _check_devices(x=x, dout=dout, logits=logits, w_gate_up=w_gate_up, w_down=w_down, saved=saved,
+                   topk_ids=topk_ids, topk_w=topk_w, counts=counts, offsets=offsets, row_of=row_of,
+                   src_of=src_of)
+    T, d = x.shape
+    dev = x.device
+    with B._on(dev):
+        dx = torch.empty_like(x)
+        dlogits = torch.empty_like(logits)
+        dwgu = torch.empty_like(w_gate_up)
+        dwd = torch.empty_like(w_down)
+        d_topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        cr = B.Routing(topk_ids, topk_w, counts, offsets, row_of, src_of, logits=logits).c()
+        ws = torch.empty(B.workspace8_size(shape, B.OP_BACKWARD), dtype=torch.uint8, device=dev)
+        B._check("moe_backward8", B.lib().moe_backward8(
+            ctypes.byref(shape), B._ptr(dout), B._ptr(x), ctypes.byref(cr), B._ptr(w_gate_up), B._ptr(w_down),
+            B._ptr(saved), B._ptr(dx), B._ptr(dwgu), B._ptr(dwd), B._ptr(d_topk_w), B._ptr(dlogits), B._ptr(ws),
+            ws.numel(), B._stream(dev)))
+    return dx, dlogits, dwgu, dwd
+
+
+@moe_bwd8.register_fake
+def _(dout, x, logits, w_gate_up, w_down, saved, topk_ids, topk_w, counts, offsets, row_of, src_of, k,
+      swiglu_limit=0.0):
+    return (torch.empty_like(x), torch.empty_like(logits), torch.empty_like(w_gate_up),
+            torch.empty_like(w_down))
+
+
+def _setup_context8(ctx, inputs, output):
+    x, logits, w_gate_up, w_down, k, swiglu_limit = inputs
+    ctx.save_for_backward(x, logits, w_gate_up, w_down, *output[1:])
+    ctx.k, ctx.swiglu_limit = k, swiglu_limit
+
+
+def _backward8(ctx, dout, *unused):
+    x, logits, w_gate_up, w_down, saved, ids, w, counts, offsets, row_of, src_of = ctx.saved_tensors
+    return moe_bwd8(dout, x, logits, w_gate_up, w_down, saved, ids, w, counts, offsets, row_of, src_of, ctx.k,
+                    ctx.swiglu_limit) + (None, None)
+
+
+moe_fwd8.register_autograd(_backward8, setup_context=_setup_context8)
+
+
 def moe_layer(x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: Tensor, k: int,
-              precision: str = "native", recompute: bool = False, swiglu_limit: float = 0.0) -> Tensor:
+              precision: str = "native", recompute: bool = False, swiglu_limit: float = 0.0,
+              save8: bool = False) -> Tensor:
     """out [T,d] of the layer, differentiable in x, logits and both weights.
     recompute=True: activation checkpointing inside the operator (nothing
     kept between forward and backward but the routing).  swiglu_limit > 0:
-    the clamped SwiGLU with that limit."""
+    the clamped SwiGLU with that limit.  save8=True (precision "native"): the
+    activations are kept in 8 bits between forward and backward."""
     for name, t in (("x", x), ("logits", logits), ("w_gate_up", w_gate_up), ("w_down", w_down)):
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+    if save8:
+        _require(not recompute, "save8 keeps a checkpoint, recompute keeps none: give one of them")
+        _require(precision == "native", f"save8 needs precision 'native', got {precision!r}")
+        return moe_fwd8(x, logits, w_gate_up, w_down, k, swiglu_limit)[0]
     return moe_fwd(x, logits, w_gate_up, w_down, k, precision, not recompute, swiglu_limit)[0]

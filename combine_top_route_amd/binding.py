@@ -61,6 +61,15 @@ _SIGS = [
                                    ctypes.c_size_t, _P]),
     ("moe_backward", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, ctypes.POINTER(MoeRouting), _P, _P, _P, _P,
                                     _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("moe_saved8_size", ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(ctypes.c_size_t)]),
+    ("moe_workspace8_size", ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
+    ("moe_forward8", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.POINTER(MoeRouting), _P, _P, _P, _P, _P,
+                                    ctypes.c_size_t, _P]),
+    ("moe_backward8", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, ctypes.POINTER(MoeRouting), _P, _P, _P, _P,
+                                     _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("moe_swiglu_save8", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.POINTER(MoeRouting), _P, _P, _P, _P]),
+    ("moe_swiglu_backward8", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, _P, ctypes.POINTER(MoeRouting), _P, _P,
+                                            _P, _P]),
     ("moe_decode_workspace_size", ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(ctypes.c_size_t)]),
     ("moe_decode", ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.c_int, _P, ctypes.POINTER(MoeRouting), _P, _P, _P,
                                   _P, _P, _P, ctypes.c_size_t, _P]),
@@ -196,10 +205,12 @@ class MoeLayer:
     """One layer shape with preallocated outputs and workspaces, so repeated
     calls (benchmarks, training loops) allocate nothing.  save=False: the
     forward keeps nothing and the backward recomputes H and Aw from x
-    (activation checkpointing)."""
+    (activation checkpointing).  save8=True: the forward keeps H in 8 bits
+    (moe_forward8, moe_backward8), about a third of the bytes."""
 
     def __init__(self, T, d, E, k, I, dtype=torch.bfloat16, logits_dtype=None,
-                 precision="native", device="cuda", save=True, swiglu_limit=0.0, persistent=False):
+                 precision="native", device="cuda", save=True, swiglu_limit=0.0, persistent=False,
+                 save8=False):
         self.T, self.d, self.E, self.k, self.I = T, d, E, k, I
         self.dtype = dtype
         self.logits_dtype = dtype if logits_dtype is None else logits_dtype
@@ -209,10 +220,19 @@ class MoeLayer:
         self.device = dev
         self.shape = make_shape(T, d, E, k, I, dtype, self.logits_dtype, precision, swiglu_limit, persistent)
         dev = self.device
-        self.ws_fwd = torch.empty(workspace_size(self.shape, OP_FORWARD), dtype=torch.uint8, device=dev)
-        self.ws_bwd = torch.empty(workspace_size(self.shape, OP_BACKWARD if save else OP_BACKWARD_RECOMPUTE),
-                                  dtype=torch.uint8, device=dev)
-        self.saved = (torch.empty(saved_size(self.shape), dtype=torch.uint8, device=dev) if save else None)
+        self.save8 = save8
+        if save8:
+            if not save:
+                raise ValueError("save8 keeps a checkpoint; save=False keeps none")
+            wf, wb = workspace8_size(self.shape, OP_FORWARD), workspace8_size(self.shape, OP_BACKWARD)
+            ns = saved8_size(self.shape)
+        else:
+            wf = workspace_size(self.shape, OP_FORWARD)
+            wb = workspace_size(self.shape, OP_BACKWARD if save else OP_BACKWARD_RECOMPUTE)
+            ns = saved_size(self.shape) if save else 0
+        self.ws_fwd = torch.empty(wf, dtype=torch.uint8, device=dev)
+        self.ws_bwd = torch.empty(wb, dtype=torch.uint8, device=dev)
+        self.saved = torch.empty(ns, dtype=torch.uint8, device=dev) if save else None
         self.out = torch.empty((T, d), dtype=dtype, device=dev)
         self.routing = Routing.empty(T, E, k, dev)
         self.dx = torch.empty((T, d), dtype=dtype, device=dev)
@@ -222,8 +242,12 @@ class MoeLayer:
         self.dlogits = torch.empty((T, E), dtype=self.logits_dtype, device=dev)
 
     def saved_views(self):
-        """(H [R,2I], A [R,I]) views of the saved buffer."""
+        """(H [R,2I], A [R,I]) views of the saved buffer; with save8 its
+        (codes [R,2I], scales [R,2 ceil(I/32)])."""
         R, I = self.T * self.k, self.I
+        if self.save8:
+            n, at, nb = R * 2 * I, -(-R * 2 * I // 256) * 256, 2 * -(-I // 32)
+            return self.saved[:n].view(R, 2 * I), self.saved[at:at + R * nb].view(R, nb)
         flat = self.saved.view(self.dtype)
         return flat[:R * 2 * I].view(R, 2 * I), flat[R * 2 * I:].view(R, I)
 
@@ -242,7 +266,8 @@ class MoeLayer:
             r.logits = None
             r.topk_ids, r.topk_w = topk_ids, topk_w
         cr = r.c()
-        _check("moe_forward", lib().moe_forward(
+        name = "moe_forward8" if self.save8 else "moe_forward"
+        _check(name, getattr(lib(), name)(
             ctypes.byref(self.shape), _ptr(x), ctypes.byref(cr), _ptr(w_gate_up), _ptr(w_down),
             _ptr(self.out), _ptr(self.saved), _ptr(self.ws_fwd), self.ws_fwd.numel(), _stream(dev)))
         return self.out
@@ -253,7 +278,8 @@ class MoeLayer:
         r = self.routing
         cr = r.c()
         dl = self.dlogits if (want_dlogits and r.logits is not None) else None
-        _check("moe_backward", lib().moe_backward(
+        name = "moe_backward8" if self.save8 else "moe_backward"
+        _check(name, getattr(lib(), name)(
             ctypes.byref(self.shape), _ptr(dout), _ptr(x), ctypes.byref(cr), _ptr(w_gate_up),
             _ptr(w_down), _ptr(self.saved), _ptr(self.dx), _ptr(self.dw_gate_up), _ptr(self.dw_down),
             _ptr(self.d_topk_w), _ptr(dl), _ptr(self.ws_bwd), self.ws_bwd.numel(), _stream(dev)))
@@ -261,6 +287,72 @@ class MoeLayer:
         if dl is not None:
             res["dlogits"] = dl
         return res
+
+
+def saved8_size(shape: MoeShape) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_saved8_size", lib().moe_saved8_size(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def workspace8_size(shape: MoeShape, op: int) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_workspace8_size", lib().moe_workspace8_size(ctypes.byref(shape), op, ctypes.byref(n)))
+    return n.value
+
+
+def _row_args(rows, routing: Routing, T, k, name, width):
+    """Checks of the checkpoint's row passes: rows [T*k, width]."""
+    dev = rows.device
+    if rows.dtype not in _DT:
+        raise ValueError(f"{name} has dtype {rows.dtype}, expected one of {tuple(_DT)}")
+    _need(rows, name, (T * k, width), rows.dtype, dev)
+    if routing is not None:
+        _need(routing.src_of, "src_of", (T * k,), torch.int32, dev)
+        _need(routing.topk_w, "topk_w", (T, k), torch.float32, dev)
+    return dev
+
+
+def swiglu_save8(H, routing: Routing | None, T, k, swiglu_limit=0.0):
+    """(Aw [T*k, I], codes uint8 [T*k, 2I], scales uint8 [T*k, 2 ceil(I/32)])
+    of gate|up pre-activations H [T*k, 2I] in expert order (moe_swiglu_save8 in
+    include/moe.h).  routing=None: the codes and scales alone (Aw is None)."""
+    if H.dim() != 2 or H.shape[1] % 2:
+        raise ValueError(f"H must be [T*k, 2I], got {tuple(H.shape)}")
+    I = H.shape[1] // 2
+    dev = _row_args(H, routing, T, k, "H", 2 * I)
+    shape = make_shape(T, 8, max(k, 1), k, I, H.dtype, swiglu_limit=swiglu_limit)
+    saved8_size(shape)  # refuses a bad T, k or I before anything is allocated
+    with _on(dev):
+        aw = None if routing is None else torch.empty((T * k, I), dtype=H.dtype, device=dev)
+        codes = torch.empty((T * k, 2 * I), dtype=torch.uint8, device=dev)
+        scales = torch.empty((T * k, 2 * -(-I // 32)), dtype=torch.uint8, device=dev)
+        cr = None if routing is None else ctypes.byref(routing.c())
+        _check("moe_swiglu_save8", lib().moe_swiglu_save8(ctypes.byref(shape), _ptr(H), cr, _ptr(aw), _ptr(codes),
+                                                          _ptr(scales), _stream(dev)))
+    return aw, codes, scales
+
+
+def swiglu_backward8(G, codes, scales, routing: Routing, T, k, swiglu_limit=0.0):
+    """(dH [T*k, 2I], Aw [T*k, I], dw [T*k] float32) from G [T*k, I] and the
+    codes and scales of swiglu_save8 (moe_swiglu_backward8)."""
+    if G.dim() != 2:
+        raise ValueError(f"G must be [T*k, I], got {tuple(G.shape)}")
+    I = G.shape[1]
+    dev = _row_args(G, routing, T, k, "G", I)
+    _need(codes, "codes", (T * k, 2 * I), torch.uint8, dev)
+    _need(scales, "scales", (T * k, 2 * -(-I // 32)), torch.uint8, dev)
+    shape = make_shape(T, 8, max(k, 1), k, I, G.dtype, swiglu_limit=swiglu_limit)
+    saved8_size(shape)
+    with _on(dev):
+        dh = torch.empty((T * k, 2 * I), dtype=G.dtype, device=dev)
+        aw = torch.empty((T * k, I), dtype=G.dtype, device=dev)
+        dw = torch.empty(T * k, dtype=torch.float32, device=dev)
+        cr = routing.c()
+        _check("moe_swiglu_backward8", lib().moe_swiglu_backward8(
+            ctypes.byref(shape), _ptr(G), _ptr(codes), _ptr(scales), ctypes.byref(cr), _ptr(dh), _ptr(aw), _ptr(dw),
+            _stream(dev)))
+    return dh, aw, dw
 
 
 def decode_workspace_size(shape: MoeShape) -> int:

@@ -121,6 +121,8 @@ moe_status check_shape(const moe_shape* s) {
   if (!(p)) return fail(MOE_ERR_INVALID_ARGUMENT, "%s is NULL", #p)
 
 size_t elem_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
+// SwiGLU clamp of the kernels: +inf for the plain SwiGLU
+float swiglu_lim(const moe_shape* s) { return s->swiglu_limit > 0.0f ? s->swiglu_limit : __builtin_huge_valf(); }
 // fp8 GEMMs in the forward / in the backward
 bool fwd_fp8(const moe_shape* s) { return s->precision == MOE_PREC_FP8_BLOCK || s->precision == MOE_PREC_MXFP8; }
 bool bwd_fp8(const moe_shape* s) { return s->precision != MOE_PREC_NATIVE; }
@@ -280,12 +282,15 @@ moe_status check_routing(const moe_routing* r, bool need_all) {
   return MOE_OK;
 }
 
-moe_status check_ws(const moe_shape* s, int op, void* ws, size_t bytes) {
-  const size_t need = layout(s, op).total;
+moe_status check_ws_bytes(size_t need, void* ws, size_t bytes) {
   if (bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", bytes, need);
   if (need && !ws) return fail(MOE_ERR_INVALID_ARGUMENT, "workspace is NULL");
   if (((uintptr_t)ws) & 255) return fail(MOE_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
   return MOE_OK;
+}
+
+moe_status check_ws(const moe_shape* s, int op, void* ws, size_t bytes) {
+  return check_ws_bytes(layout(s, op).total, ws, bytes);
 }
 
 moe_status check_aligned16(const void* p, const char* name) {
@@ -369,7 +374,7 @@ LayerArgs layer_args(const moe_shape* s, const moe_routing* r, const void* x, co
   a.order = (const int32_t*)at(ws, L.order);
   a.xorder = a.order + s->E;
   a.tok_of = L.tok ? (const int32_t*)at(ws, L.tok) : nullptr;  // backward layouts only
-  a.swiglu_lim = s->swiglu_limit > 0.0f ? s->swiglu_limit : __builtin_huge_valf();
+  a.swiglu_lim = swiglu_lim(s);
   a.persistent = (s->flags & MOE_FLAG_PERSISTENT) != 0;
   return a;
 }
@@ -390,6 +395,33 @@ hipError_t forward_gemms(const moe_shape* shape, const LaunchCtx& c, const Layer
   q.awq = Y ? (uint8_t*)at(ws, L.awq) : nullptr; q.aws = Y ? at(ws, L.aws) : nullptr;
   q.sv = fp8_saved(shape, saved);
   return fp8_fwd_gemms(c, a, q, H, A, Y);
+}
+
+// ------------------------------------------------- 8-bit activation checkpoint
+moe_status check_save8(const moe_shape* s) {
+  TRY(check_shape(s));
+  if (s->precision != MOE_PREC_NATIVE)
+    return fail(MOE_ERR_UNSUPPORTED, "the 8-bit checkpoint needs precision MOE_PREC_NATIVE");
+  return MOE_OK;
+}
+
+// `saved8`: codes [R, 2I], then scales [R, 2 ceil(I/32)].
+size_t saved8_scales_at(const moe_shape* s) { return align256((size_t)s->T * s->k * 2 * s->I); }
+size_t saved8_total(const moe_shape* s) { return saved8_scales_at(s) + (size_t)s->T * s->k * save8_scales(s->I); }
+
+// The layer's workspace for `op`, then what the plain call finds in `saved`:
+// the forward's H (float32 has it in the workspace), the backward's Aw.
+struct Layout8 {
+  Layout base;
+  size_t extra = 0, total = 0;
+};
+Layout8 layout8(const moe_shape* s, int op) {
+  Layout8 L;
+  L.base = layout(s, op);
+  const size_t R = (size_t)s->T * s->k, row = elem_size(s->dtype) * s->I;
+  L.extra = align256(L.base.total);
+  L.total = L.extra + (op == MOE_OP_BACKWARD ? R * row : (s->dtype == MOE_F32 ? 0 : 2 * R * row));
+  return L;
 }
 
 // ------------------------------------------------------------ few tokens
@@ -597,6 +629,157 @@ moe_status moe_backward(const moe_shape* shape, const void* dout, const void* x,
   return MOE_OK;
 }
 
+moe_status moe_swiglu_save8(const moe_shape* shape, const void* H, const moe_routing* routing, void* Aw,
+                            uint8_t* codes, uint8_t* scales, void* stream) {
+  TRY(check_save8(shape));
+  CHECK_PTR(H);
+  CHECK_PTR(codes);
+  CHECK_PTR(scales);
+  if (Aw) {
+    CHECK_PTR(routing);
+    CHECK_PTR(routing->src_of);
+    CHECK_PTR(routing->topk_w);
+    TRY(check_aligned16(Aw, "Aw"));
+  }
+  TRY(check_aligned16(H, "H"));
+  TRY(check_aligned16(codes, "codes"));
+  const LaunchCtx c = make_ctx(stream);
+  (void)hipGetLastError();
+  HIP_TRY(launch_save8(c, shape->dtype, H, Aw ? routing->topk_w : nullptr, Aw ? routing->src_of : nullptr,
+                       (int)(shape->T * shape->k), (int)shape->I, swiglu_lim(shape), Aw, codes, scales),
+          "swiglu_save8");
+  return MOE_OK;
+}
+
+moe_status moe_swiglu_backward8(const moe_shape* shape, const void* G, const uint8_t* codes, const uint8_t* scales,
+                                const moe_routing* routing, void* dH, void* Aw, float* dw, void* stream) {
+  TRY(check_save8(shape));
+  CHECK_PTR(G);
+  CHECK_PTR(codes);
+  CHECK_PTR(scales);
+  CHECK_PTR(routing);
+  CHECK_PTR(routing->src_of);
+  CHECK_PTR(routing->topk_w);
+  CHECK_PTR(dH);
+  CHECK_PTR(dw);
+  TRY(check_aligned16(G, "G"));
+  TRY(check_aligned16(codes, "codes"));
+  TRY(check_aligned16(dH, "dH"));
+  if (Aw) TRY(check_aligned16(Aw, "Aw"));
+  const LaunchCtx c = make_ctx(stream);
+  (void)hipGetLastError();
+  HIP_TRY(launch_swiglu_bwd8(c, shape->dtype, G, codes, scales, routing->topk_w, routing->src_of,
+                             (int)(shape->T * shape->k), (int)shape->I, swiglu_lim(shape), dH, Aw, dw),
+          "swiglu_backward8");
+  return MOE_OK;
+}
+
+moe_status moe_saved8_size(const moe_shape* shape, size_t* bytes) {
+  TRY(check_save8(shape));
+  CHECK_PTR(bytes);
+  *bytes = saved8_total(shape);
+  return MOE_OK;
+}
+
+moe_status moe_workspace8_size(const moe_shape* shape, int op, size_t* bytes) {
+  TRY(check_save8(shape));
+  CHECK_PTR(bytes);
+  if (op != MOE_OP_FORWARD && op != MOE_OP_BACKWARD)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "op=%d is neither MOE_OP_FORWARD nor MOE_OP_BACKWARD", op);
+  *bytes = layout8(shape, op).total;
+  return MOE_OK;
+}
+
+moe_status moe_forward8(const moe_shape* shape, const void* x, moe_routing* routing, const void* w_gate_up,
+                        const void* w_down, void* out, void* saved8, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  TRY(check_save8(shape));
+  CHECK_PTR(x);
+  CHECK_PTR(w_gate_up);
+  CHECK_PTR(w_down);
+  CHECK_PTR(out);
+  CHECK_PTR(saved8);
+  TRY(check_routing(routing, true));
+  const Layout8 L8 = layout8(shape, MOE_OP_FORWARD);
+  TRY(check_ws_bytes(L8.total, workspace, workspace_bytes));
+  TRY(check_aligned16(x, "x"));
+  TRY(check_aligned16(w_gate_up, "w_gate_up"));
+  TRY(check_aligned16(w_down, "w_down"));
+  TRY(check_aligned16(out, "out"));
+  TRY(check_aligned16(saved8, "saved8"));
+  const Layout& L = L8.base;
+  const LaunchCtx c = make_ctx(stream);
+  (void)hipGetLastError();
+  TRY(run_route(shape, routing, (int32_t*)at(workspace, L.hist), c));
+  HIP_TRY(launch_schedule(c, routing->offsets, (int)shape->E, (int32_t*)at(workspace, L.tile_off),
+                          (int32_t*)at(workspace, L.order), nullptr, nullptr, (int4*)at(workspace, L.tiles)),
+          "route_schedule");
+  const LayerArgs a = layer_args(shape, routing, x, w_gate_up, w_down, workspace, L);
+  void* H = shape->dtype == MOE_F32 ? at(workspace, L.H) : at(workspace, L8.extra);
+  void* Y = at(workspace, L.Y);
+  HIP_TRY(forward_gemms(shape, c, a, workspace, L, nullptr, H, at(workspace, L.A), Y), "forward GEMMs");
+  HIP_TRY(launch_save8(c, shape->dtype, H, nullptr, nullptr, a.R, a.I, a.swiglu_lim, nullptr, (uint8_t*)saved8,
+                       (uint8_t*)at(saved8, saved8_scales_at(shape))), "swiglu_save8");
+  HIP_TRY(launch_combine(c, "combine", shape->dtype, Y, routing->row_of, nullptr, (int)shape->T,
+                         (int)shape->k, (int)shape->d, out), "combine");
+  return MOE_OK;
+}
+
+moe_status moe_backward8(const moe_shape* shape, const void* dout, const void* x, const moe_routing* routing,
+                         const void* w_gate_up, const void* w_down, const void* saved8, void* dx, void* dw_gate_up,
+                         void* dw_down, float* d_topk_w, void* dlogits, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  TRY(check_save8(shape));
+  CHECK_PTR(dout);
+  CHECK_PTR(x);
+  CHECK_PTR(w_gate_up);
+  CHECK_PTR(w_down);
+  CHECK_PTR(saved8);
+  CHECK_PTR(dx);
+  CHECK_PTR(dw_gate_up);
+  CHECK_PTR(dw_down);
+  CHECK_PTR(d_topk_w);
+  TRY(check_routing(routing, true));
+  if (dlogits && !routing->logits)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dlogits needs the logits form of routing");
+  const Layout8 L8 = layout8(shape, MOE_OP_BACKWARD);
+  TRY(check_ws_bytes(L8.total, workspace, workspace_bytes));
+  TRY(check_aligned16(dout, "dout"));
+  TRY(check_aligned16(x, "x"));
+  TRY(check_aligned16(w_gate_up, "w_gate_up"));
+  TRY(check_aligned16(w_down, "w_down"));
+  TRY(check_aligned16(saved8, "saved8"));
+  TRY(check_aligned16(dx, "dx"));
+  TRY(check_aligned16(dw_gate_up, "dw_gate_up"));
+  TRY(check_aligned16(dw_down, "dw_down"));
+  const Layout& L = L8.base;
+  const LaunchCtx c = make_ctx(stream);
+  (void)hipGetLastError();
+  HIP_TRY(launch_schedule(c, routing->offsets, (int)shape->E, (int32_t*)at(workspace, L.tile_off),
+                          (int32_t*)at(workspace, L.order), (int32_t*)at(workspace, L.order) + shape->E, nullptr,
+                          (int4*)at(workspace, L.tiles)), "route_schedule");
+  HIP_TRY(launch_tok_of(c, routing->src_of, (int)(shape->T * shape->k), (int)shape->k,
+                        (int32_t*)at(workspace, L.tok)), "route_tok");
+  const LayerArgs a = layer_args(shape, routing, x, w_gate_up, w_down, workspace, L);
+  Save8 s8;
+  s8.codes = (const uint8_t*)saved8;
+  s8.scales = s8.codes + saved8_scales_at(shape);
+  s8.aw = at(workspace, L8.extra);
+  void* dH = at(workspace, L.dH);
+  void* dXp = at(workspace, L.dXp);
+  float* dwp = (float*)at(workspace, L.dwp);  // one value a row: the row pass sums the whole row
+  if (shape->dtype == MOE_F32)
+    HIP_TRY(f32_bwd_gemms(c, a, dout, nullptr, nullptr, dH, dXp, dwp, dw_gate_up, dw_down,
+                          (float*)at(workspace, L.G), &s8), "backward GEMMs");
+  else
+    HIP_TRY(bf16_bwd_gemms(c, a, dout, nullptr, nullptr, dH, dXp, dwp, dw_gate_up, dw_down, &s8), "backward GEMMs");
+  HIP_TRY(launch_topk_grad(c, dwp, 1, routing->row_of, routing->topk_ids, routing->topk_w, (int)shape->T,
+                           (int)shape->k, (int)shape->E, d_topk_w, dlogits, shape->logits_dtype), "topk_grad");
+  HIP_TRY(launch_combine(c, "reduce_dx", shape->dtype, dXp, routing->row_of, nullptr, (int)shape->T,
+                         (int)shape->k, (int)shape->d, dx), "reduce_dx");
+  return MOE_OK;
+}
+
 moe_status moe_decode_workspace_size(const moe_shape* shape, size_t* bytes) {
   TRY(check_decode(shape));
   CHECK_PTR(bytes);
@@ -629,10 +812,7 @@ moe_status moe_decode(const moe_shape* shape, int weights, const void* x, moe_ro
     return fail(MOE_ERR_INVALID_ARGUMENT, "scales given for uncoded weights");
   }
   const DecodeLayout L = decode_layout(shape);
-  if (workspace_bytes < L.total)
-    return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace_bytes, L.total);
-  CHECK_PTR(workspace);
-  if (((uintptr_t)workspace) & 255) return fail(MOE_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
+  TRY(check_ws_bytes(L.total, workspace, workspace_bytes));
   TRY(check_aligned16(x, "x"));
   TRY(check_aligned16(w_gate_up, "w_gate_up"));
   TRY(check_aligned16(w_down, "w_down"));
@@ -644,7 +824,7 @@ moe_status moe_decode(const moe_shape* shape, int weights, const void* x, moe_ro
   a.k = (int)shape->k;
   a.I = (int)shape->I;
   a.dtype = shape->dtype;
-  a.lim = shape->swiglu_limit > 0.0f ? shape->swiglu_limit : __builtin_huge_valf();
+  a.lim = swiglu_lim(shape);
   a.x = x;
   a.w_gate_up = w_gate_up;
   a.s_gate_up = s_gate_up;

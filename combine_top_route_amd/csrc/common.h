@@ -60,6 +60,11 @@ __device__ __forceinline__ float clamp_gate(float g, float lim) {
 }
 __device__ __forceinline__ float clamp_up(float u, float lim) { return __builtin_amdgcn_fmed3f(u, -lim, lim); }
 
+// The same clamps where a NaN has to come through (a comparison with NaN is
+// false; the median above may drop it).
+__device__ __forceinline__ float clip_gate(float g, float lim) { return g > lim ? lim : g; }
+__device__ __forceinline__ float clip_up(float u, float lim) { return u > lim ? lim : (u < -lim ? -lim : u); }
+
 __host__ __device__ constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Order of a row GEMM's tiles within an expert.  Either order re-reads one
@@ -153,6 +158,24 @@ hipError_t launch_topk_grad(const LaunchCtx& c, const float* dwp, int nblk, cons
                             const int32_t* ids, const float* w, int T, int k, int E,
                             float* d_topk_w, void* dlogits, int logits_dtype);
 
+// ------------------------------------------------- 8-bit activation checkpoint
+// (save8.hip) H [R, 2I] as e4m3 codes with one E8M0 scale per 32 columns of
+// either half: codes [R, 2I], scales [R, 2 ceil(I/32)].
+inline int64_t save8_scales(int64_t I) { return 2 * cdiv(I, 32); }
+// codes and scales from H, and (aw non-null) the weighted SwiGLU output.
+hipError_t launch_save8(const LaunchCtx& c, int dtype, const void* H, const float* topk_w, const int32_t* src_of,
+                        int R, int I, float lim, void* aw, uint8_t* codes, uint8_t* scales);
+// SwiGLU backward from them and G [R, I]: dH, dw [R] = <G, a>, aw (may be null).
+hipError_t launch_swiglu_bwd8(const LaunchCtx& c, int dtype, const void* G, const uint8_t* codes,
+                              const uint8_t* scales, const float* topk_w, const int32_t* src_of, int R, int I,
+                              float lim, void* dH, void* aw, float* dw);
+// A checkpoint in place of the backward's H and Aw: aw is then written.
+struct Save8 {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  void* aw;  // [R, I] workspace
+};
+
 // ---------------------------------------------------------------- GEMMs
 struct LayerArgs {
   int T, d, E, k, I, R;
@@ -180,9 +203,10 @@ struct LayerArgs {
 // bf16 MFMA path.
 hipError_t bf16_fwd_gemms(const LaunchCtx& c, const LayerArgs& a, void* H, void* Aw, void* Yw);
 // backward outputs dH [R,2I], dXp [R,d], dwp [R, bf16_dw_blocks(I)] fp32, dW_gu, dW_d.
+// s8 (non-null): the checkpoint that stands for H and Aw (both null then).
 hipError_t bf16_bwd_gemms(const LaunchCtx& c, const LayerArgs& a, const void* dout,
                           const void* H, const void* Aw, void* dH, void* dXp, float* dwp,
-                          void* dW_gu, void* dW_d);
+                          void* dW_gu, void* dW_d, const Save8* s8 = nullptr);
 
 // Number of per-row partials of <G, a> that the down dgrad writes (dwp [R, n]).
 int bf16_dw_blocks(int I);
@@ -193,7 +217,7 @@ hipError_t f32_fwd_gemms(const LaunchCtx& c, const LayerArgs& a, void* H, void* 
 // backward needs G [R,I] fp32 scratch.
 hipError_t f32_bwd_gemms(const LaunchCtx& c, const LayerArgs& a, const void* dout,
                          const void* H, const void* Aw, void* dH, void* dXp, float* dwp,
-                         void* dW_gu, void* dW_d, float* G);
+                         void* dW_gu, void* dW_d, float* G, const Save8* s8 = nullptr);
 
 // ------------------------------------------------------------ few tokens
 // The whole layer for up to kDecodeMaxT tokens (decode.hip).

@@ -273,11 +273,9 @@ __device__ __forceinline__ uint32_t mx_word_of(const void* s, int64_t n, int K, 
   return 0;
 }
 
-// The clamps keep NaN (a comparison with NaN is false).
 __device__ __forceinline__ float swiglu(float g, float u, float lim) {
-  const float gc = g > lim ? lim : g;
-  const float uc = u > lim ? lim : (u < -lim ? -lim : u);
-  return gc * sigmoidf_(gc) * uc;
+  const float gc = clip_gate(g, lim);
+  return gc * sigmoidf_(gc) * clip_up(u, lim);
 }
 
 // ------------------------------------------------------- an expert's tokens

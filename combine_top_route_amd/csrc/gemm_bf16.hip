@@ -1296,7 +1296,7 @@ hipError_t bf16_fwd_gemms(const LaunchCtx& c, const LayerArgs& a, void* H, void*
 
 hipError_t bf16_bwd_gemms(const LaunchCtx& c, const LayerArgs& a, const void* dout,
                           const void* H, const void* Aw, void* dH, void* dXp, float* dwp,
-                          void* dW_gu, void* dW_d) {
+                          void* dW_gu, void* dW_d, const Save8* s8) {
   const int64_t I = a.I, d = a.d;
   hipError_t err;
   {  // down dgrad: G = dout_t W_down[e] (into the dXp buffer, free until the
@@ -1311,7 +1311,13 @@ hipError_t bf16_bwd_gemms(const LaunchCtx& c, const LayerArgs& a, const void* do
     p.C = G; p.ldc = I;
     err = launch_rows<EPI_STORE, B_KM, 1>(c, "gemm_down_dgrad", p, a.R, a.persistent);
     if (err != hipSuccess) return err;
-    err = launch_swiglu_bwd(c, G, H, a.topk_w, a.src_of, a.R, a.I, a.swiglu_lim, dH, dwp);
+    if (s8) {
+      err = launch_swiglu_bwd8(c, BF16, G, s8->codes, s8->scales, a.topk_w, a.src_of, a.R, a.I, a.swiglu_lim, dH,
+                               s8->aw, dwp);
+      Aw = s8->aw;
+    } else {
+      err = launch_swiglu_bwd(c, G, H, a.topk_w, a.src_of, a.R, a.I, a.swiglu_lim, dH, dwp);
+    }
     if (err != hipSuccess) return err;
   }
   {  // down wgrad: dW_d[e][c, i] = sum_r dout[t_r, c] Aw[r, i]

@@ -218,16 +218,22 @@ hipError_t f32_fwd_gemms(const LaunchCtx& c, const LayerArgs& a, void* H, void* 
 
 hipError_t f32_bwd_gemms(const LaunchCtx& c, const LayerArgs& a, const void* dout, const void* H,
                          const void* Aact, void* dH, void* dXp, float* dwp, void* dW_gu,
-                         void* dW_d, float* G) {
+                         void* dW_d, float* G, const Save8* s8) {
   const int64_t I = a.I, d = a.d, R = a.R;
   const int nblk = f32_dw_blocks(a.I);
   // down dgrad: G[r, i] = sum_c dout[t_r, c] W_down[e][c, i]
   hipError_t err = rows_gemm(c, "gemm_down_dgrad", a, (const float*)dout, d, a.src_of, a.k,
                              (const float*)a.w_down, d * I, 1, I, G, I, a.I, a.d);
   if (err != hipSuccess) return err;
-  MOE_LAUNCH(c, "swiglu_bwd", f32_swiglu_bwd, dim3((unsigned)cdiv(R * nblk, 256)), dim3(256), 0,
-             (const float*)G, (const float*)H, a.topk_w, a.src_of, R, a.I, nblk, a.swiglu_lim,
-             (float*)dH, dwp);
+  if (s8) {
+    HIP_RET(launch_swiglu_bwd8(c, F32, G, s8->codes, s8->scales, a.topk_w, a.src_of, a.R, a.I, a.swiglu_lim, dH,
+                               s8->aw, dwp));
+    Aact = s8->aw;
+  } else {
+    MOE_LAUNCH(c, "swiglu_bwd", f32_swiglu_bwd, dim3((unsigned)cdiv(R * nblk, 256)), dim3(256), 0,
+               (const float*)G, (const float*)H, a.topk_w, a.src_of, R, a.I, nblk, a.swiglu_lim,
+               (float*)dH, dwp);
+  }
   // down wgrad: dW_d[e][c, i] = sum_r dout[t_r, c] Aw[r, i]  (Aw carries w_r)
   err = wgrad(c, "gemm_down_wgrad", a, (const float*)dout, d, 1, nullptr, (const float*)Aact, I,
               0, a.d, a.I, (float*)dW_d);

@@ -1,0 +1,224 @@
+// 8-bit activation checkpoint: the gate/up pre-activations H = [g | u] of the
+// expert-sorted rows, kept between forward and backward as e4m3 codes with one
+// E8M0 scale per 32 columns of either half (the MXFP8 row encoding: X the
+// smallest exponent with amax <= 448 2^X, the code of h 2^-X to nearest even):
+// 2 I + 2 ceil(I/32) bytes a row instead of the 6 I of a bf16 H and Aw.  Aw is
+// not kept: the backward's row pass rebuilds it from the decoded H.
+//
+//   forward:  codes, scales = encode(H);  aw = w silu(min(g, L)) clamp(u, -L, L)
+//   backward: g, u = decode;  s = sigmoid(min(g, L));  a = silu u;  dw = <G, a>;
+//             aw = w a;  dA = w G;  dg = dA u s (1 + g (1 - s));  du = dA g s
+//             (zero where a clamp is active)
+//
+// Both are one pass over the rows, bound by memory: at I = 768 in bf16 the
+// forward moves 6.2 KB a row and the backward 7.7 KB.  One wave takes a row; a
+// lane takes 8 columns of both halves, so a block of 32 is four neighbouring
+// lanes, whose largest magnitude two DPP steps find.
+#include "common.h"
+
+namespace moe {
+namespace {
+
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+
+template <typename T>
+__device__ __forceinline__ void load8(float (&f)[8], const T* p) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4_t v = *(const u32x4_t*)(p + 4 * h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[4 * h + i] = __uint_as_float(v[i]);
+    }
+  } else {
+    const u32x4_t v = *(const u32x4_t*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(v[i] << 16);
+      f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4_t v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(f[4 * h + i]);
+      *(u32x4_t*)(p + 4 * h) = v;
+    }
+  } else {
+    u32x4_t v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    *(u32x4_t*)p = v;
+  }
+}
+
+// Largest of the four lanes of a quad (quad permutations: lane xor 1, xor 2).
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  uint32_t o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xf, 0xf, true);
+  v = o > v ? o : v;
+  o = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xf, 0xf, true);
+  return o > v ? o : v;
+}
+
+// Codes of a lane's 8 values of a block whose four lanes call together (past
+// the row's end: zeros), and the block's scale byte.  Magnitudes compare as
+// integers, where infinities and NaN come out largest: such a block gets the
+// scale byte 255 (NaN) and decodes to NaN throughout.
+__device__ __forceinline__ u32x2_t encode8(const float (&f)[8], uint32_t* byte) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = __float_as_uint(f[i]) & 0x7fffffffu;
+    m = b > m ? b : m;
+  }
+  m = quad_max(m);
+  // amax = c 2^e with c in [1, 2): X = e - 8, plus one when c > 1.75 (448 =
+  // 1.75 2^8); a subnormal amax lies far below the clamp at -127
+  int X = (int)(m >> 23) - 135 + ((m & 0x7fffffu) > 0x600000u ? 1 : 0);
+  X = m == 0 ? 0 : (X < -127 ? -127 : X);
+  const bool bad = m >= 0x7f800000u;
+  *byte = bad ? 255u : (uint32_t)(X + 127);
+  const float inv = __uint_as_float((uint32_t)(127 - X) << 23);  // 2^-X: exact products, at most 448
+  u32x2_t q;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h] * inv, f[4 * h + 1] * inv, 0, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * h + 2] * inv, f[4 * h + 3] * inv, v, true);
+    q[h] = bad ? 0x7f7f7f7fu : (uint32_t)v;
+  }
+  return q;
+}
+
+__device__ __forceinline__ void decode8(float (&f)[8], u32x2_t q, uint32_t byte) {
+  // 2^X; byte 0 is 2^-127, a subnormal, byte 255 NaN
+  const float s = __uint_as_float(byte == 0 ? 0x00400000u : (byte == 255u ? 0x7fc00000u : byte << 23));
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[h], false);
+    const f32x2_t hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[h], true);
+    f[4 * h] = lo[0] * s;
+    f[4 * h + 1] = lo[1] * s;
+    f[4 * h + 2] = hi[0] * s;
+    f[4 * h + 3] = hi[1] * s;
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void save8_kernel(const T* __restrict__ H, const float* __restrict__ topk_w,
+                                                    const int32_t* __restrict__ src_of, int R, int I, float lim,
+                                                    T* __restrict__ aw, uint8_t* __restrict__ codes,
+                                                    uint8_t* __restrict__ scales) {
+  const int r = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (r >= R) return;
+  const int lane = threadIdx.x & 63;
+  const int nb = (I + 31) / 32;
+  const float wr = aw ? topk_w[src_of[r]] : 0.0f;
+  const T* Hr = H + (int64_t)r * 2 * I;
+  uint8_t* cr = codes + (int64_t)r * 2 * I;
+  uint8_t* sr = scales + (int64_t)r * 2 * nb;
+  for (int c = lane; c < nb * 4; c += kWave) {
+    const bool in = c * 8 < I;  // I is a multiple of 8: a lane's columns are in or out together
+    float g[8] = {}, u[8] = {};
+    if (in) {
+      load8(g, Hr + c * 8);
+      load8(u, Hr + I + c * 8);
+    }
+    uint32_t bg, bu;
+    const u32x2_t qg = encode8(g, &bg), qu = encode8(u, &bu);
+    if (in) {
+      *(u32x2_t*)(cr + c * 8) = qg;
+      *(u32x2_t*)(cr + I + c * 8) = qu;
+      if (aw) {
+        float a[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float gc = clip_gate(g[i], lim);
+          a[i] = wr * (gc * sigmoidf_(gc) * clip_up(u[i], lim));
+        }
+        store8(aw + (int64_t)r * I + c * 8, a);
+      }
+    }
+    if ((c & 3) == 0) {
+      sr[c >> 2] = (uint8_t)bg;
+      sr[nb + (c >> 2)] = (uint8_t)bu;
+    }
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void swiglu_bwd8_kernel(const T* __restrict__ G, const uint8_t* __restrict__ codes,
+                                                          const uint8_t* __restrict__ scales,
+                                                          const float* __restrict__ topk_w,
+                                                          const int32_t* __restrict__ src_of, int R, int I, float lim,
+                                                          T* __restrict__ dH, T* __restrict__ aw,
+                                                          float* __restrict__ dw) {
+  const int r = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (r >= R) return;
+  const int lane = threadIdx.x & 63;
+  const int nb = (I + 31) / 32;
+  const float wr = topk_w[src_of[r]];
+  const uint8_t* cr = codes + (int64_t)r * 2 * I;
+  const uint8_t* sr = scales + (int64_t)r * 2 * nb;
+  const T* Gr = G + (int64_t)r * I;
+  T* dr = dH + (int64_t)r * 2 * I;
+  float part = 0.0f;
+  for (int c = lane; c * 8 < I; c += kWave) {
+    float gv[8], g[8], u[8], a[8], dg[8], du[8];
+    load8(gv, Gr + c * 8);
+    decode8(g, *(const u32x2_t*)(cr + c * 8), sr[c >> 2]);
+    decode8(u, *(const u32x2_t*)(cr + I + c * 8), sr[nb + (c >> 2)]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float gc = clip_gate(g[i], lim), uc = clip_up(u[i], lim);
+      const float s = sigmoidf_(gc);
+      const float act = gc * s * uc;
+      part += gv[i] * act;
+      const float dA = wr * gv[i];
+      a[i] = wr * act;
+      dg[i] = g[i] > lim ? 0.0f : dA * uc * s * (1.0f + gc * (1.0f - s));
+      du[i] = fabsf(u[i]) > lim ? 0.0f : dA * gc * s;
+    }
+    store8(dr + c * 8, dg);
+    store8(dr + I + c * 8, du);
+    if (aw) store8(aw + (int64_t)r * I + c * 8, a);
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) part += __shfl_xor(part, off, kWave);
+  if (lane == 0) dw[r] = part;
+}
+
+}  // namespace
+
+hipError_t launch_save8(const LaunchCtx& c, int dtype, const void* H, const float* topk_w, const int32_t* src_of,
+                        int R, int I, float lim, void* aw, uint8_t* codes, uint8_t* scales) {
+  const dim3 grid((unsigned)cdiv(R, 4));
+  if (dtype == F32)
+    MOE_LAUNCH(c, "swiglu_save8", save8_kernel<float>, grid, dim3(256), 0, (const float*)H, topk_w, src_of, R, I, lim,
+               (float*)aw, codes, scales);
+  else
+    MOE_LAUNCH(c, "swiglu_save8", save8_kernel<bf16_t>, grid, dim3(256), 0, (const bf16_t*)H, topk_w, src_of, R, I,
+               lim, (bf16_t*)aw, codes, scales);
+  return hipSuccess;
+}
+
+hipError_t launch_swiglu_bwd8(const LaunchCtx& c, int dtype, const void* G, const uint8_t* codes,
+                              const uint8_t* scales, const float* topk_w, const int32_t* src_of, int R, int I,
+                              float lim, void* dH, void* aw, float* dw) {
+  const dim3 grid((unsigned)cdiv(R, 4));
+  if (dtype == F32)
+    MOE_LAUNCH(c, "swiglu_bwd8", swiglu_bwd8_kernel<float>, grid, dim3(256), 0, (const float*)G, codes, scales,
+               topk_w, src_of, R, I, lim, (float*)dH, (float*)aw, dw);
+  else
+    MOE_LAUNCH(c, "swiglu_bwd8", swiglu_bwd8_kernel<bf16_t>, grid, dim3(256), 0, (const bf16_t*)G, codes, scales,
+               topk_w, src_of, R, I, lim, (bf16_t*)dH, (bf16_t*)aw, dw);
+  return hipSuccess;
+}
+
+}  // namespace moe

@@ -245,6 +245,46 @@ moe_status moe_backward(const moe_shape* shape, const void* dout, const void* x,
                         void* dlogits, void* workspace, size_t workspace_bytes,
                         void* stream);
 
+/* Activation checkpoint in 8 bits: the training step with `saved` at about a
+ * third of its size.  Of the forward's H and Aw (6 I bytes a row in bf16) only
+ * H is kept, as e4m3 codes with one E8M0 scale byte per 32 columns, counted
+ * from the first column of either half (moe_quantize_mxfp8's row encoding; a
+ * last block may be short); the backward works from the decoded H wherever
+ * moe_backward works from H, and rebuilds Aw from it, rounded to dtype.  The
+ * forward's out is moe_forward's, bit for bit.  A block with an infinity or a
+ * NaN gets the scale byte 255 and decodes to NaN.  Precision
+ * MOE_PREC_NATIVE, both dtypes.
+ *   saved8:    moe_saved8_size bytes: codes [T*k, 2I], then, at the next
+ *              multiple of 256 bytes, scale bytes [T*k, 2 ceil(I/32)];
+ *   workspace: moe_workspace8_size bytes (op MOE_OP_FORWARD or
+ *              MOE_OP_BACKWARD).
+ * Everything else is as for moe_forward and moe_backward. */
+moe_status moe_saved8_size(const moe_shape* shape, size_t* bytes);
+moe_status moe_workspace8_size(const moe_shape* shape, int op, size_t* bytes);
+moe_status moe_forward8(const moe_shape* shape, const void* x, moe_routing* routing,
+                        const void* w_gate_up, const void* w_down, void* out, void* saved8,
+                        void* workspace, size_t workspace_bytes, void* stream);
+moe_status moe_backward8(const moe_shape* shape, const void* dout, const void* x,
+                         const moe_routing* routing, const void* w_gate_up, const void* w_down,
+                         const void* saved8, void* dx, void* dw_gate_up, void* dw_down,
+                         float* d_topk_w, void* dlogits, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* The checkpoint's row passes alone, on expert-sorted rows r < T*k with weight
+ * w_r = topk_w[src_of[r]] (T, k, I, dtype and swiglu_limit of shape are used,
+ * and of routing, src_of and topk_w).  moe_swiglu_save8: H [T*k, 2I] -> codes
+ * [T*k, 2I], scales [T*k, 2 ceil(I/32)] and, unless Aw is NULL (routing is
+ * then not read), Aw [T*k, I] = w_r silu(g) u (in dtype).
+ * moe_swiglu_backward8: from G [T*k, I] (dtype; the gradient of silu(g) u
+ * before the row's weight) and the decoded H: dH [T*k, 2I], dw [T*k] float32 =
+ * sum over columns of G silu(g) u, and Aw unless NULL.  H, G, Aw, dH and codes
+ * 16-byte aligned. */
+moe_status moe_swiglu_save8(const moe_shape* shape, const void* H, const moe_routing* routing,
+                            void* Aw, uint8_t* codes, uint8_t* scales, void* stream);
+moe_status moe_swiglu_backward8(const moe_shape* shape, const void* G, const uint8_t* codes,
+                                const uint8_t* scales, const moe_routing* routing, void* dH,
+                                void* Aw, float* dw, void* stream);
+
 /* The layer for a few tokens (serving): the forward's arithmetic on at most
  * 256 tokens, reading each selected expert's weights once, from weights that
  * may have been encoded beforehand.  No tiles, sort or encoders run: the call
