@@ -61,6 +61,10 @@ _SIGS = [
                                    ctypes.c_size_t, _P]),
     ("moe_backward", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, ctypes.POINTER(MoeRouting), _P, _P, _P, _P,
                                     _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    ("moe_router_forward", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, _P, _P]),
+    ("moe_router_workspace_size", ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(ctypes.c_size_t)]),
+    ("moe_router_backward", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t,
+                                           _P]),
     ("moe_saved8_size", ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(ctypes.c_size_t)]),
     ("moe_workspace8_size", ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
     ("moe_forward8", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.POINTER(MoeRouting), _P, _P, _P, _P, _P,
@@ -287,6 +291,51 @@ class MoeLayer:
         if dl is not None:
             res["dlogits"] = dl
         return res
+
+
+def _router_shape(x, w_router, logits_dtype) -> MoeShape:
+    if x.dim() != 2 or w_router.dim() != 2 or w_router.shape[1] != x.shape[1]:
+        raise ValueError(f"x must be [T, d] and w_router [E, d], got {tuple(x.shape)} and {tuple(w_router.shape)}")
+    if x.dtype not in _DT or logits_dtype not in _DT:
+        raise ValueError(f"x has dtype {x.dtype}, the logits {logits_dtype}, expected two of {tuple(_DT)}")
+    _need(x, "x", x.shape, x.dtype, x.device)
+    _need(w_router, "w_router", w_router.shape, x.dtype, x.device)
+    return make_shape(x.shape[0], x.shape[1], w_router.shape[0], 1, 8, x.dtype, logits_dtype)
+
+
+def router_workspace_size(shape: MoeShape) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_router_workspace_size", lib().moe_router_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def router_logits(x, w_router, logits_dtype=torch.float32):
+    """Router logits x w_router^T [T, E] (moe_router_forward in include/moe.h)
+    of x [T, d] and w_router [E, d], both float32 or both bfloat16."""
+    shape = _router_shape(x, w_router, logits_dtype)
+    with _on(x.device):
+        logits = torch.empty((x.shape[0], w_router.shape[0]), dtype=logits_dtype, device=x.device)
+        _check("moe_router_forward", lib().moe_router_forward(ctypes.byref(shape), _ptr(x), _ptr(w_router),
+                                                              _ptr(logits), _stream(x.device)))
+    return logits
+
+
+def router_backward(dlogits, x, w_router, dx_in=None):
+    """(dx, dw_router) of the projection: dx = dx_in + dlogits w_router (dx_in
+    None: zeros), dw_router = dlogits^T x (moe_router_backward)."""
+    shape = _router_shape(x, w_router, dlogits.dtype)
+    dev = x.device
+    _need(dlogits, "dlogits", (x.shape[0], w_router.shape[0]), dlogits.dtype, dev)
+    if dx_in is not None:
+        _need(dx_in, "dx_in", x.shape, x.dtype, dev)
+    n = router_workspace_size(shape)
+    with _on(dev):
+        dx, dw = torch.empty_like(x), torch.empty_like(w_router)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        _check("moe_router_backward", lib().moe_router_backward(
+            ctypes.byref(shape), _ptr(dlogits), _ptr(x), _ptr(w_router), _ptr(dx_in), _ptr(dx), _ptr(dw), _ptr(ws), n,
+            _stream(dev)))
+    return dx, dw
 
 
 def saved8_size(shape: MoeShape) -> int:

@@ -20,7 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_mi355x.so")
 SOURCES = ["api.cpp", "route.hip", "rows.hip", "gemm_bf16.hip", "gemm_f32.hip", "gemm_fp8.hip",
-           "quant_fp8.hip", "decode.hip", "save8.hip"]
+           "quant_fp8.hip", "decode.hip", "save8.hip",
+           "router.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

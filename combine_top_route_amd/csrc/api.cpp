@@ -424,6 +424,34 @@ Layout8 layout8(const moe_shape* s, int op) {
   return L;
 }
 
+// ------------------------------------------------------------------ router
+RouterArgs router_args(const moe_shape* s, const void* x, const void* w) {
+  RouterArgs a = {};
+  a.T = (int)s->T;
+  a.d = (int)s->d;
+  a.E = (int)s->E;
+  a.dtype = s->dtype;
+  a.logits_dtype = s->logits_dtype;
+  a.x = x;
+  a.w = w;
+  a.Ep = (int)(cdiv(s->E, 32) * 32);
+  const RouterPlan p = router_plan(s->T, s->d, s->E, s->dtype);
+  a.run_tokens = p.run_tokens;
+  a.runs = (int)p.runs;
+  return a;
+}
+
+struct RouterLayout {
+  size_t wt = 0, parts = 0, total = 0;
+};
+RouterLayout router_layout(const moe_shape* s) {
+  RouterLayout L;
+  const RouterArgs a = router_args(s, nullptr, nullptr);
+  L.parts = s->dtype == MOE_F32 ? 0 : align256(sizeof(bf16_t) * s->d * a.Ep);
+  L.total = L.parts + sizeof(float) * a.runs * s->E * s->d;
+  return L;
+}
+
 // ------------------------------------------------------------ few tokens
 struct DecodeLayout {
   size_t mid = 0, mw = 0, aw = 0, y = 0, total = 0;
@@ -626,6 +654,58 @@ moe_status moe_backward(const moe_shape* shape, const void* dout, const void* x,
                            dlogits, shape->logits_dtype), "topk_grad");
   HIP_TRY(launch_combine(c, "reduce_dx", shape->dtype, dXp, routing->row_of, nullptr, (int)shape->T,
                          (int)shape->k, (int)shape->d, dx), "reduce_dx");
+  return MOE_OK;
+}
+
+moe_status moe_router_forward(const moe_shape* shape, const void* x, const void* w_router, void* logits,
+                              void* stream) {
+  TRY(check_shape(shape));
+  CHECK_PTR(x);
+  CHECK_PTR(w_router);
+  CHECK_PTR(logits);
+  TRY(check_aligned16(x, "x"));
+  TRY(check_aligned16(w_router, "w_router"));
+  TRY(check_aligned16(logits, "logits"));
+  const LaunchCtx c = make_ctx(stream);
+  (void)hipGetLastError();
+  HIP_TRY(launch_router_fwd(c, router_args(shape, x, w_router), logits), "router_forward");
+  return MOE_OK;
+}
+
+moe_status moe_router_workspace_size(const moe_shape* shape, size_t* bytes) {
+  TRY(check_shape(shape));
+  CHECK_PTR(bytes);
+  *bytes = router_layout(shape).total;
+  return MOE_OK;
+}
+
+moe_status moe_router_backward(const moe_shape* shape, const void* dlogits, const void* x, const void* w_router,
+                               const void* dx_in, void* dx, void* dw_router, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  TRY(check_shape(shape));
+  CHECK_PTR(dlogits);
+  CHECK_PTR(x);
+  CHECK_PTR(w_router);
+  CHECK_PTR(dx);
+  CHECK_PTR(dw_router);
+  const RouterLayout L = router_layout(shape);
+  TRY(check_ws_bytes(L.total, workspace, workspace_bytes));
+  TRY(check_aligned16(dlogits, "dlogits"));
+  TRY(check_aligned16(x, "x"));
+  TRY(check_aligned16(w_router, "w_router"));
+  if (dx_in) TRY(check_aligned16(dx_in, "dx_in"));
+  TRY(check_aligned16(dx, "dx"));
+  TRY(check_aligned16(dw_router, "dw_router"));
+  RouterArgs a = router_args(shape, x, w_router);
+  a.dlogits = dlogits;
+  a.dx_in = dx_in;
+  a.dx = dx;
+  a.dw = dw_router;
+  a.wt = (bf16_t*)at(workspace, L.wt);
+  a.parts = (float*)at(workspace, L.parts);
+  const LaunchCtx c = make_ctx(stream);
+  (void)hipGetLastError();
+  HIP_TRY(launch_router_bwd(c, a), "router_backward");
   return MOE_OK;
 }
 

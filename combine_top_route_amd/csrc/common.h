@@ -219,6 +219,32 @@ hipError_t f32_bwd_gemms(const LaunchCtx& c, const LayerArgs& a, const void* dou
                          const void* H, const void* Aw, void* dH, void* dXp, float* dwp,
                          void* dW_gu, void* dW_d, float* G, const Save8* s8 = nullptr);
 
+// ------------------------------------------------------------------ router
+// (router.hip) The router's projection and its gradients.
+struct RouterPlan {
+  int64_t run_tokens, runs;  // dw is summed in `runs` parts of run_tokens tokens
+};
+RouterPlan router_plan(int64_t T, int64_t d, int64_t E, int dtype);
+struct RouterArgs {
+  int T, d, E;
+  int dtype, logits_dtype;
+  const void* x;        // [T, d]
+  const void* w;        // [E, d]
+  const void* dlogits;  // [T, E], backward
+  const void* dx_in;    // [T, d] or null
+  void* dx;             // [T, d]
+  void* dw;             // [E, d]
+  bf16_t* wt;           // [d, Ep] workspace, bf16: w transposed
+  float* parts;         // [runs, E, d] workspace
+  int Ep;               // E rounded up to a multiple of 32
+  int64_t run_tokens;
+  int runs;
+  // set by the launcher
+  int d_blocks, e_blocks, dw_groups, dx_blocks, dx_tokens, dx_groups;
+};
+hipError_t launch_router_fwd(const LaunchCtx& c, const RouterArgs& a, void* logits);
+hipError_t launch_router_bwd(const LaunchCtx& c, RouterArgs a);
+
 // ------------------------------------------------------------ few tokens
 // The whole layer for up to kDecodeMaxT tokens (decode.hip).
 constexpr int kDecodeMaxT = 256;

@@ -245,6 +245,25 @@ moe_status moe_backward(const moe_shape* shape, const void* dout, const void* x,
                         void* dlogits, void* workspace, size_t workspace_bytes,
                         void* stream);
 
+/* The router's projection, which makes the logits, and its gradients (of shape
+ * T, d, E, dtype and logits_dtype are used):
+ *   logits [T,E] (logits_dtype) = x w_router^T,  x [T,d], w_router [E,d];
+ *   dx [T,d] = dx_in + dlogits w_router,  dlogits [T,E] in logits_dtype,
+ *     dx_in [T,d] (for instance moe_backward's dx; may be dx itself) or NULL
+ *     for zeros;
+ *   dw_router [E,d] = dlogits^T x;
+ * all others in dtype; float32 sums in a fixed order, one rounding each.  With
+ * dtype MOE_BF16 a float32 dlogits enters the products as the sum of two bf16
+ * values (2^-18 of it is lost).  Every pointer 16-byte aligned; workspace:
+ * moe_router_workspace_size bytes, for the backward only. */
+moe_status moe_router_forward(const moe_shape* shape, const void* x, const void* w_router,
+                              void* logits, void* stream);
+moe_status moe_router_workspace_size(const moe_shape* shape, size_t* bytes);
+moe_status moe_router_backward(const moe_shape* shape, const void* dlogits, const void* x,
+                               const void* w_router, const void* dx_in, void* dx,
+                               void* dw_router, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
 /* Activation checkpoint in 8 bits: the training step with `saved` at about a
  * third of its size.  Of the forward's H and Aw (6 I bytes a row in bf16) only
  * H is kept, as e4m3 codes with one E8M0 scale byte per 32 columns, counted
