@@ -306,3 +306,83 @@ def moe_layer(x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: Tensor, k: i
         _require(precision == "native", f"save8 needs precision 'native', got {precision!r}")
         return moe_fwd8(x, logits, w_gate_up, w_down, k, swiglu_limit)[0]
     return moe_fwd(x, logits, w_gate_up, w_down, k, precision, not recompute, swiglu_limit)[0]
+
+
+# ------------------------------------------------------------------ router
+def _check_router_args(x: Tensor, w_router: Tensor, logits_dtype: torch.dtype):
+    """x [T,d] and w_router [E,d], contiguous, of one float type."""
+    _require(x.dim() == 2 and w_router.dim() == 2 and w_router.shape[1] == x.shape[1],
+             f"x must be [T, d] and w_router [E, d], got {tuple(x.shape)} and {tuple(w_router.shape)}")
+    _require(x.dtype in _FLOATS and w_router.dtype == x.dtype,
+             f"x and w_router need one dtype of {_FLOATS}, got {x.dtype}, {w_router.dtype}")
+    _require(logits_dtype in _FLOATS, f"logits dtype {logits_dtype} not in {_FLOATS}")
+    for name, t in (("x", x), ("w_router", w_router)):
+        _require(t.is_contiguous(), f"{name} must be contiguous")
+
+
+@torch.library.custom_op(f"{_NS}::router_fwd", mutates_args=())
+def router_fwd(x: Tensor, w_router: Tensor, logits_dtype: torch.dtype) -> Tensor:
+    """Router logits x w_router^T [T,E]."""
+    _check_router_args(x, w_router, logits_dtype)
+    _check_devices(x=x, w_router=w_router)
+    return B.router_logits(x, w_router, logits_dtype)
+
+
+@router_fwd.register_fake
+def _(x, w_router, logits_dtype):
+    return x.new_empty((x.shape[0], w_router.shape[0]), dtype=logits_dtype)
+
+
+@torch.library.custom_op(f"{_NS}::router_bwd", mutates_args=())
+def router_bwd(dlogits: Tensor, x: Tensor, w_router: Tensor, dx_in: Tensor | None) -> tuple[Tensor, Tensor]:
+    """(dx, dw_router): dx = dx_in + dlogits w_router, dw_router = dlogits^T x."""
+    _check_router_args(x, w_router, dlogits.dtype)
+    dlogits = dlogits.contiguous()
+    _require(tuple(dlogits.shape) == (x.shape[0], w_router.shape[0]),
+             f"dlogits must be [T={x.shape[0]}, E={w_router.shape[0]}], got {tuple(dlogits.shape)}")
+    tensors = dict(x=x, w_router=w_router, dlogits=dlogits)
+    if dx_in is not None:
+        dx_in = dx_in.contiguous()
+        _require(dx_in.shape == x.shape and dx_in.dtype == x.dtype,
+                 f"dx_in must be {tuple(x.shape)} {x.dtype}, got {tuple(dx_in.shape)} {dx_in.dtype}")
+        tensors["dx_in"] = dx_in
+    _check_devices(**tensors)
+    return B.router_backward(dlogits, x, w_router, dx_in=dx_in)
+
+
+@router_bwd.register_fake
+def _(dlogits, x, w_router, dx_in):
+    return torch.empty_like(x), torch.empty_like(w_router)
+
+
+class _Router(torch.autograd.Function):
+    """logits, and x passed through: what comes back to x from the layer
+    enters the router's backward, which adds its own part in the same pass."""
+
+    @staticmethod
+    def forward(ctx, x, w_router, logits_dtype):
+        ctx.save_for_backward(x, w_router)
+        return router_fwd(x, w_router, logits_dtype), x.view_as(x)
+
+    @staticmethod
+    def backward(ctx, dlogits, dx_in):
+        x, w_router = ctx.saved_tensors
+        dx, dw = router_bwd(dlogits, x, w_router, dx_in)
+        return dx, dw, None
+
+
+def router(x: Tensor, w_router: Tensor, logits_dtype: torch.dtype = torch.float32) -> Tensor:
+    """Router logits x w_router^T [T,E], differentiable in both."""
+    _check_router_args(x, w_router, logits_dtype)
+    return _Router.apply(x, w_router, logits_dtype)[0]
+
+
+def moe_block(x: Tensor, w_router: Tensor, w_gate_up: Tensor, w_down: Tensor, k: int, precision: str = "native",
+              recompute: bool = False, swiglu_limit: float = 0.0, save8: bool = False,
+              logits_dtype: torch.dtype = torch.float32) -> Tensor:
+    """The router and the layer: out [T,d] of moe_layer at the logits
+    x w_router^T, differentiable in x and the three weights; x's gradient is
+    written once, by the router's backward."""
+    _check_router_args(x, w_router, logits_dtype)
+    logits, x = _Router.apply(x, w_router, logits_dtype)
+    return moe_layer(x, logits, w_gate_up, w_down, k, precision, recompute, swiglu_limit, save8)
