@@ -146,9 +146,8 @@ __global__ __launch_bounds__(64) void decode_ids_kernel(const int32_t* __restric
 }
 
 // ------------------------------------------------------------ weight formats
-// A unit is 128 bytes of each of 16 weight rows; lane l holds row l % 16, bytes
-// 16 q and 64 + 16 q with q = l / 16.  UK: values of K per unit; BV: 16-byte
-// loads of a token's matching activations per lane; NF: MFMA operands.
+// A unit is 128 bytes of each of 16 weight rows.  UK: values of K per unit; BV:
+// 16-byte operands of a token's matching activations per lane; NF: MFMAs.
 enum WFormat { WF_F32 = 0, WF_BF16 = 1, WF_FP8 = 2, WF_MX = 3 };
 template <int F> struct Fmt {  // coded: 128 codes, 4 MFMAs of 32
   typedef bf16_t act;
@@ -178,44 +177,66 @@ __device__ __forceinline__ u32x4_t load16(rsrc_t r, uint32_t off, bool ok) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, (int)(ok ? off : kPast), 0, 0);
 }
 
-// This lane's 32 bytes of a weight row's unit; row: the row's offset plus 16 q,
-// bytes: the row's length.
-__device__ __forceinline__ void load_a(u32x4_t (&a)[2], rsrc_t r, uint32_t row, int unit, int q, int bytes) {
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int off = unit * 128 + c * 64;
-    a[c] = load16(r, row + off, off + q * 16 < bytes);
-  }
+// An MFMA wants neighbouring lanes to hold neighbouring rows, but a load whose
+// neighbouring lanes lie in different rows costs the vector memory unit 64
+// cycles, and one whose neighbours are contiguous 25 (measured, 1 KB from the
+// caches; 64 cycles for every 1 KB would cap the chip at 9.8 TB/s with the
+// activations' loads included).  So a load takes 8 rows of 128 bytes, eight
+// lanes a row, and a wave turns the rows around through its own 2 KB of LDS:
+// [16 rows][128 bytes], 16-byte chunks XOR-swizzled so that the writes and the
+// reads of 16 rows at one chunk are free of bank conflicts.  No barriers: the
+// LDS serves one wave's accesses in order.
+typedef __attribute__((address_space(3))) char lds_t;
+__device__ __forceinline__ int row_chunk(int row, int chunk) { return row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4); }
+
+// 8 half + lane / 8: the row of a 16-row group that this lane loads.
+__device__ __forceinline__ int load_row(int half) { return half * 8 + (int)((threadIdx.x & 63) >> 3); }
+
+// 128 bytes at byte `at` of rows at offsets row[0], row[1] (this lane's two
+// rows), of which `bytes` exist; rows with live[h] false read as zeros.
+__device__ __forceinline__ void load_rows(u32x4_t (&v)[2], rsrc_t r, const uint32_t (&row)[2], int at, int bytes,
+                                          bool live0 = true, bool live1 = true) {
+  const int off = at + (int)(threadIdx.x & 7) * 16;
+  v[0] = load16(r, row[0] + off, live0 && off < bytes);
+  v[1] = load16(r, row[1] + off, live1 && off < bytes);
 }
 
-// The activations that meet load_a's bytes: the same values of K.  row: the
-// token's offset.
+__device__ __forceinline__ void put_rows(lds_t* p, const u32x4_t (&v)[2]) {
+  const int chunk = threadIdx.x & 7;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    *(__attribute__((address_space(3))) u32x4_t*)(p + row_chunk(load_row(h), chunk)) = v[h];
+}
+__device__ __forceinline__ u32x4_t get_chunk(const lds_t* p, int row, int chunk) {
+  return *(const __attribute__((address_space(3))) u32x4_t*)(p + row_chunk(row, chunk));
+}
+
+// A unit's weights in flight, and its scale bytes: `mx` holds, in lane 4 r + i,
+// row r's four scale bytes of unit i of a batch of up to four units.
 template <int F>
-__device__ __forceinline__ void load_b(u32x4_t (&b)[Fmt<F>::BV], rsrc_t r, uint32_t row, int unit, int q, int bytes) {
-#pragma unroll
-  for (int v = 0; v < Fmt<F>::BV; ++v) {
-    const int off = F >= WF_FP8 ? unit * 256 + (v >> 1) * 128 + q * 32 + (v & 1) * 16 : unit * 128 + v * 64 + q * 16;
-    b[v] = load16(r, row + off, off < bytes);
-  }
+__device__ __forceinline__ uint32_t mx_words(const void* s, int row4, int K, int unit) {
+  if constexpr (F == WF_MX) return ((const uint32_t*)s)[(int64_t)row4 * (K >> 7) + min(unit, (K >> 7) - 1)];
+  return 0;
 }
 
-// MFMA operands of a unit's weights.  Codes become bfloat16 exactly (e4m3 has
-// four significant bits); an E8M0 scale is a power of two and rides on the
+// MFMA operands of a unit's weights, of which this lane's row is col and its
+// chunks are q and 4 + q.  Codes become bfloat16 exactly (e4m3 has four
+// significant bits); an E8M0 scale is a power of two and rides on the
 // conversion, also exactly down to bfloat16's smallest numbers (2^-133).
 // mx: the row's four scale bytes of this unit.
 template <int F>
-__device__ __forceinline__ void to_frags(typename Fmt<F>::frag (&fr)[Fmt<F>::NF], const u32x4_t (&a)[2], uint32_t mx,
-                                         int q) {
-  if constexpr (F == WF_F32) {
+__device__ __forceinline__ void to_frags(typename Fmt<F>::frag (&fr)[Fmt<F>::NF], const lds_t* p, uint32_t mx, int q,
+                                         int col) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) fr[i] = __uint_as_float(a[i >> 2][i & 3]);
-  } else if constexpr (F == WF_BF16) {
+  for (int c = 0; c < 2; ++c) {
+    const u32x4_t a = get_chunk(p, col, c * 4 + q);
+    if constexpr (F == WF_F32) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) fr[c] = __builtin_bit_cast(bf16x8_t, a[c]);
-  } else {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      // this lane's 16 codes of chunk c lie in block 2 c + q / 2
+      for (int i = 0; i < 4; ++i) fr[4 * c + i] = __uint_as_float(a[i]);
+    } else if constexpr (F == WF_BF16) {
+      fr[c] = __builtin_bit_cast(bf16x8_t, a);
+    } else {
+      // this lane's 16 codes of chunk 4 c + q lie in block 2 c + q / 2
       const float s =
           F == WF_MX ? __uint_as_float(((mx >> (16 * c + 8 * (q >> 1))) & 0xffu) << 23) : 1.0f;
 #pragma unroll
@@ -223,7 +244,7 @@ __device__ __forceinline__ void to_frags(typename Fmt<F>::frag (&fr)[Fmt<F>::NF]
         u32x4_t o;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t word = a[c][2 * h + i];
+          const uint32_t word = a[2 * h + i];
           o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(word, s, false));
           o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(word, s, true));
         }
@@ -231,6 +252,36 @@ __device__ __forceinline__ void to_frags(typename Fmt<F>::frag (&fr)[Fmt<F>::NF]
       }
     }
   }
+}
+
+// The activations of 16 tokens that meet a unit's weights: the same values of
+// K, 128 bytes a token, or 256 beside codes.  Tokens 8.. are neither loaded
+// nor stored with `eight` (their columns hold anything and are dropped).
+template <int F> constexpr int kActHalves = F >= WF_FP8 ? 2 : 1;
+template <int F>
+__device__ __forceinline__ void load_acts(u32x4_t (&v)[kActHalves<F>][2], rsrc_t r, const uint32_t (&row)[2],
+                                          const bool (&live)[2], int unit, int bytes, bool eight) {
+#pragma unroll
+  for (int h = 0; h < kActHalves<F>; ++h) {
+    const int off = (unit * kActHalves<F> + h) * 128 + (int)(threadIdx.x & 7) * 16;
+    v[h][0] = load16(r, row[0] + off, live[0] && off < bytes);
+    if (!eight) v[h][1] = load16(r, row[1] + off, live[1] && off < bytes);
+  }
+}
+template <int F>
+__device__ __forceinline__ void put_acts(lds_t* p, const u32x4_t (&v)[kActHalves<F>][2], bool eight) {
+  const int chunk = threadIdx.x & 7;
+#pragma unroll
+  for (int h = 0; h < kActHalves<F>; ++h) {
+    *(__attribute__((address_space(3))) u32x4_t*)(p + h * 2048 + row_chunk(load_row(0), chunk)) = v[h][0];
+    if (!eight) *(__attribute__((address_space(3))) u32x4_t*)(p + h * 2048 + row_chunk(load_row(1), chunk)) = v[h][1];
+  }
+}
+template <int F>
+__device__ __forceinline__ void get_acts(u32x4_t (&b)[Fmt<F>::BV], const lds_t* p, int q, int col) {
+#pragma unroll
+  for (int v = 0; v < Fmt<F>::BV; ++v)
+    b[v] = F >= WF_FP8 ? get_chunk(p + (v >> 1) * 2048, col, 2 * q + (v & 1)) : get_chunk(p, col, 4 * v + q);
 }
 
 // s + the unit's weights times the unit's activations, unscaled.
@@ -260,17 +311,11 @@ __device__ __forceinline__ void unit_mma(f32x4_t& acc, const typename Fmt<F>::fr
   }
 }
 
-// Scales of one matrix [N, K] of an expert: blockwise fp32 [N/128, K/128], or
-// E8M0 bytes [N, K/32].
+// Blockwise scale of row n and unit `unit` of one matrix [N, K] of an expert.
 template <int F>
-__device__ __forceinline__ float block_scale_of(const void* s, int64_t n, int K, int unit) {
-  if constexpr (F == WF_FP8) return ((const float*)s)[(n >> 7) * (K >> 7) + unit];
+__device__ __forceinline__ float block_scale_of(const void* s, int n, int K, int unit) {
+  if constexpr (F == WF_FP8) return ((const float*)s)[(int64_t)(n >> 7) * (K >> 7) + unit];
   return 1.0f;
-}
-template <int F>
-__device__ __forceinline__ uint32_t mx_word_of(const void* s, int64_t n, int K, int unit) {
-  if constexpr (F == WF_MX) return ((const uint32_t*)s)[n * (K >> 7) + unit];
-  return 0;
 }
 
 __device__ __forceinline__ float swiglu(float g, float u, float lim) {
@@ -324,77 +369,110 @@ __device__ __forceinline__ int find_rows(Rows& rows, const int32_t* __restrict__
   return n;
 }
 
+// Token blocks of 16 that one pass over an expert's weights serves (the rest
+// take another pass, from the caches): as many as the registers hold beside
+// the weights in flight.
+template <int F> constexpr int kMaxBlocks = F >= WF_FP8 ? 2 : 4;
+
 // ------------------------------------------------------------ gate/up product
 // One work-group: 16 gate rows and the same 16 up rows of one expert, for all
-// of its tokens; the NW waves take the units of K in turn, UN at a time.
+// of its tokens; the NW waves take batches of UN units of K in turn.
 template <int F, int UN>
-struct GuWeights {  // UN units of this lane's gate and up row, in flight
+struct GuWeights {  // UN units of the tile's gate and up rows, in flight
   u32x4_t g[UN][2], u[UN][2];
-  uint32_t mg[UN], mu[UN];
+  uint32_t mg, mu;
 };
 
-template <int F, int NW, int UN>
-__device__ __forceinline__ void load_gu(GuWeights<F, UN>& w, rsrc_t wr, const void* sc, int I, int K, int row,
-                                        int base, int q) {
-  const int units = (K + Fmt<F>::UK - 1) / Fmt<F>::UK;
+struct GuTile {  // where a lane finds them
+  rsrc_t w;
+  const void* sc;
+  uint32_t g[2], u[2];  // offsets of this lane's two gate and up rows
+  int row4;             // row whose scale bytes it loads
+  int n0;
+};
+
+template <int F, int UN>
+__device__ __forceinline__ void load_gu(GuWeights<F, UN>& w, const GuTile& t, int I, int K, int base) {
   const int bytes = F >= WF_FP8 ? K : K * (int)sizeof(typename Fmt<F>::act);
-  const uint32_t g = (uint32_t)row * bytes + q * 16, u = (uint32_t)(I + row) * bytes + q * 16;
 #pragma unroll
   for (int i = 0; i < UN; ++i) {
-    const int unit = base + i * NW, us = min(unit, units - 1);
-    load_a(w.g[i], wr, g, unit, q, bytes);
-    load_a(w.u[i], wr, u, unit, q, bytes);
-    w.mg[i] = mx_word_of<F>(sc, row, K, us);
-    w.mu[i] = mx_word_of<F>(sc, I + row, K, us);
+    load_rows(w.g[i], t.w, t.g, (base + i) * 128, bytes);
+    load_rows(w.u[i], t.w, t.u, (base + i) * 128, bytes);
   }
+  w.mg = mx_words<F>(t.sc, t.row4, K, base + (int)(threadIdx.x & 3));
+  w.mu = mx_words<F>(t.sc, I + t.row4, K, base + (int)(threadIdx.x & 3));
 }
 
-// The tokens r0 .. r0 + 16 NB of the expert.  w holds the first units; UB
-// units' activations are loaded at a time (they come from the caches).
-template <int F, int NW, int UN, int NB, int UB>
+template <int F, int NW, int NBMAX>
+constexpr size_t gu_smem() {  // per wave: gate, up, activations; then the waves' parts
+  const size_t work = (size_t)NW * (4096 + 2048 * kActHalves<F>), parts = (size_t)NW * NBMAX * 2048;
+  return work > parts ? work : parts;
+}
+
+// The tokens r0 .. r0 + 16 NB of the expert.  w holds the first units.
+template <int F, int NW, int UN, int NB>
 __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& rows, int r0, int n,
-                                            GuWeights<F, UN>& w, rsrc_t wr, const void* sc, int n0, int row,
-                                            float* red) {
+                                            GuWeights<F, UN>& w, const GuTile& t, char* smem) {
   typedef typename Fmt<F>::act AT;
   const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
   const int K = a.d;
   const int units = (K + Fmt<F>::UK - 1) / Fmt<F>::UK;
   const int bytes = K * (int)sizeof(AT);
   const rsrc_t xb = buffer_of(a.x, (uint64_t)a.T * bytes);
-  uint32_t xr[NB];
+  const bool eight = NB == 1 && n - r0 <= 8;
+  lds_t* lw = (lds_t*)smem + wave * (4096 + 2048 * kActHalves<F>);
+  uint32_t xr[NB][2];
+  bool live[NB][2];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int r = min(r0 + b * 16 + col, n - 1);  // columns past the last token repeat it and are dropped
-    xr[b] = (uint32_t)(rows.slot[r] / a.k) * bytes;
-  }
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = r0 + b * 16 + load_row(h);
+      live[b][h] = r < n;
+      xr[b][h] = (uint32_t)(rows.slot[live[b][h] ? r : n - 1] / a.k) * bytes;
+    }
   f32x4_t ag[NB], au[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) ag[b] = au[b] = f32x4_t{0, 0, 0, 0};
-  for (int base = wave; base < units; base += NW * UN) {
-    if (base != wave || r0) load_gu<F, NW, UN>(w, wr, sc, a.I, K, row, base, q);
+  constexpr int UB = NB == 1 ? UN : 1;  // units whose activations are in flight together
+  for (int base = wave * UN; base < units; base += NW * UN) {
+    if (base != wave * UN || r0) load_gu<F, UN>(w, t, a.I, K, base);
 #pragma unroll
     for (int i0 = 0; i0 < UN; i0 += UB) {
-      u32x4_t xv[UB][NB][Fmt<F>::BV];
+      u32x4_t xv[UB][NB][kActHalves<F>][2];
 #pragma unroll
       for (int i = 0; i < UB; ++i)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) load_b<F>(xv[i][b], xb, xr[b], base + (i0 + i) * NW, q, bytes);
+        for (int b = 0; b < NB; ++b) load_acts<F>(xv[i][b], xb, xr[b], live[b], base + i0 + i, bytes, eight);
       __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
 #pragma unroll
       for (int i = 0; i < UB; ++i) {
-        const int us = min(base + (i0 + i) * NW, units - 1);
-        const float sg = block_scale_of<F>(sc, n0, K, us), su = block_scale_of<F>(sc, a.I + n0, K, us);
-        typename Fmt<F>::frag fr[Fmt<F>::NF];
-        to_frags<F>(fr, w.g[i0 + i], w.mg[i0 + i], q);
+        const int unit = base + i0 + i, us = min(unit, units - 1);
+        put_rows(lw, w.g[i0 + i]);
+        put_rows(lw + 2048, w.u[i0 + i]);
+        const float sg = block_scale_of<F>(t.sc, t.n0, K, us), su = block_scale_of<F>(t.sc, a.I + t.n0, K, us);
+        uint32_t mg = 0, mu = 0;
+        if constexpr (F == WF_MX) {
+          mg = (uint32_t)__shfl((int)w.mg, col * 4 + i0 + i, kWave);
+          mu = (uint32_t)__shfl((int)w.mu, col * 4 + i0 + i, kWave);
+        }
+        typename Fmt<F>::frag fg[Fmt<F>::NF], fu[Fmt<F>::NF];
+        to_frags<F>(fg, lw, mg, q, col);
+        to_frags<F>(fu, lw + 2048, mu, q, col);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) unit_mma<F>(ag[b], fr, xv[i][b], sg);
-        to_frags<F>(fr, w.u[i0 + i], w.mu[i0 + i], q);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) unit_mma<F>(au[b], fr, xv[i][b], su);
+        for (int b = 0; b < NB; ++b) {
+          u32x4_t xf[Fmt<F>::BV];
+          put_acts<F>(lw + 4096, xv[i][b], eight);
+          get_acts<F>(xf, lw + 4096, q, col);
+          unit_mma<F>(ag[b], fg, xf, sg);
+          unit_mma<F>(au[b], fu, xf, su);
+        }
       }
     }
   }
-  // red [wave][2 b + gate/up][col][16 rows]
+  // parts [wave][2 b + gate/up][col][16 rows], over the waves' work space
+  float* red = (float*)smem;
+  __syncthreads();
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     float* p = red + ((wave * NB + b) * 2 * 16 + col) * 16 + q * 4;
@@ -405,7 +483,7 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
   for (int o = threadIdx.x; o < NB * 256; o += NW * 64) {
     const int b = o >> 8, c = (o >> 4) & 15, m = o & 15;
     const int r = r0 + b * 16 + c;
-    if (r < n && n0 + m < a.I) {
+    if (r < n && t.n0 + m < a.I) {
       float g = 0.0f, u = 0.0f;
 #pragma unroll
       for (int v = 0; v < NW; ++v) {
@@ -413,7 +491,7 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
         g += p[0];
         u += p[256];
       }
-      ((AT*)a.aw)[(int64_t)rows.slot[r] * a.I + n0 + m] = from_f32<AT>(rows.w[r] * swiglu(g, u, a.lim));
+      ((AT*)a.aw)[(int64_t)rows.slot[r] * a.I + t.n0 + m] = from_f32<AT>(rows.w[r] * swiglu(g, u, a.lim));
     }
   }
   __syncthreads();
@@ -421,32 +499,40 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
 
 template <int F, int NBMAX, int NW, int UN>
 __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
+  static_assert(UN <= 4, "mx_words holds four units");
   __shared__ Rows rows;
-  __shared__ float red[NW * NBMAX * 512];
+  __shared__ __align__(16) char smem[gu_smem<F, NW, NBMAX>()];
   const int e = __builtin_amdgcn_readfirstlane(item_expert(a.mid, blockIdx.y, a.T * a.k, a.E));
   if (e < 0) return;
-  const int lane = threadIdx.x & 63, q = lane >> 4;
-  const int n0 = blockIdx.x * 16;
-  const int row = min(n0 + (lane & 15), a.I - 1);  // rows past I repeat the last and are dropped
-  const int64_t wb = F >= WF_FP8 ? 1 : sizeof(typename Fmt<F>::act);
-  const uint64_t wbytes = (uint64_t)2 * a.I * a.d * wb;
-  const rsrc_t wr = buffer_of((const char*)a.w_gate_up + e * wbytes, wbytes);
+  const int lane = threadIdx.x & 63;
+  const int n = find_rows(rows, a.mid, a.mw, e, a.T, a.k);
+  if (n == 0) return;
+  GuTile t;
+  t.n0 = blockIdx.x * 16;
+  const int rowb = a.d * (F >= WF_FP8 ? 1 : (int)sizeof(typename Fmt<F>::act));
+  const uint64_t wbytes = (uint64_t)2 * a.I * rowb;
+  t.w = buffer_of((const char*)a.w_gate_up + e * wbytes, wbytes);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = min(t.n0 + load_row(h), a.I - 1);  // rows past I repeat the last and are dropped
+    t.g[h] = (uint32_t)row * rowb;
+    t.u[h] = (uint32_t)(a.I + row) * rowb;
+  }
+  t.row4 = t.n0 + (lane >> 2);  // read for WF_MX, where I is a multiple of 128
   const char* sc = (const char*)a.s_gate_up;
   if (F == WF_FP8) sc += (int64_t)e * (2 * a.I / 128) * (a.d / 128) * 4;
   if (F == WF_MX) sc += (int64_t)e * 2 * a.I * (a.d / 32);
-  const int n = find_rows(rows, a.mid, a.mw, e, a.T, a.k);
-  if (n == 0) return;
+  t.sc = sc;
   GuWeights<F, UN> w;
-  load_gu<F, NW, UN>(w, wr, sc, a.I, a.d, row, tile::wave_id(), q);
-  constexpr int UB1 = F >= WF_FP8 ? (UN > 2 ? 2 : UN) : UN;
+  load_gu<F, UN>(w, t, a.I, a.d, tile::wave_id() * UN);
   if constexpr (NBMAX == 1) {
-    gateup_rows<F, NW, UN, 1, UB1>(a, rows, 0, n, w, wr, sc, n0, row, red);
+    gateup_rows<F, NW, UN, 1>(a, rows, 0, n, w, t, smem);
   } else {
-    for (int r0 = 0; r0 < n; r0 += 64) {
+    for (int r0 = 0; r0 < n; r0 += 16 * NBMAX) {
       const int left = n - r0;
-      if (left <= 16) gateup_rows<F, NW, UN, 1, UB1>(a, rows, r0, n, w, wr, sc, n0, row, red);
-      else if (left <= 32) gateup_rows<F, NW, UN, 2, (UB1 + 1) / 2>(a, rows, r0, n, w, wr, sc, n0, row, red);
-      else gateup_rows<F, NW, UN, 4, 1>(a, rows, r0, n, w, wr, sc, n0, row, red);
+      if (left <= 16) gateup_rows<F, NW, UN, 1>(a, rows, r0, n, w, t, smem);
+      else if (NBMAX == 2 || left <= 32) gateup_rows<F, NW, UN, 2>(a, rows, r0, n, w, t, smem);
+      else gateup_rows<F, NW, UN, NBMAX>(a, rows, r0, n, w, t, smem);
     }
   }
 }
@@ -457,13 +543,15 @@ __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
 // I) pair, and the combine is the sum itself (aw carries the weights).  aw is
 // rounded to the activations' type like the layer's, for the MFMA's operand.
 constexpr int kDownWaves = 16;
+template <int F> constexpr int down_work() { return kDownWaves * (2048 + 2048 * kActHalves<F>); }
 
 template <int F>
 __global__ __launch_bounds__(kDownWaves * 64) void decode_down_kernel(DecodeArgs a) {
   typedef typename Fmt<F>::act AT;
   extern __shared__ __align__(16) char smem[];
-  float* red = (float*)smem;                              // [waves][16 tokens][16 rows]
-  int* active = (int*)(red + kDownWaves * 256);           // [E] experts with tokens
+  char* work = smem;                                      // per wave: a unit's weights and activations
+  float* red = (float*)smem;                              // then [waves][16 tokens][16 rows]
+  int* active = (int*)(work + down_work<F>());            // [E] experts with tokens
   uint16_t* tab = (uint16_t*)(active + a.E);              // [E][T] slot of the token + 1, 0: none
   __shared__ int counts[kDownWaves];
   const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
@@ -491,48 +579,63 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_kernel(DecodeArgs
   __syncthreads();
 
   const int K = a.I, n0 = blockIdx.x * 16;
-  const int row = min(n0 + col, a.d - 1);
   const int units = (K + Fmt<F>::UK - 1) / Fmt<F>::UK;
   const int abytes = F >= WF_FP8 ? K : K * (int)sizeof(AT), bbytes = K * (int)sizeof(AT);
   const uint64_t wbytes = (uint64_t)a.d * abytes;
-  const uint32_t wrow = (uint32_t)row * abytes + q * 16;
+  uint32_t wrow[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) wrow[h] = (uint32_t)min(n0 + load_row(h), a.d - 1) * abytes;
   const rsrc_t xb = buffer_of(a.aw, (uint64_t)a.T * a.k * bbytes);
+  const bool eight = a.T <= 8;
+  lds_t* lw = (lds_t*)work + wave * (2048 + 2048 * kActHalves<F>);
   const int total = nact * units;
-  constexpr int UN = 4;
+  constexpr int UN = F >= WF_FP8 ? 2 : 4;
   f32x4_t acc = {0, 0, 0, 0};
-  for (int base = wave; base < total; base += kDownWaves * UN) {
-    u32x4_t wv[UN][2], xv[UN][Fmt<F>::BV];
+  for (int base = wave * UN; base < total; base += kDownWaves * UN) {
+    u32x4_t wv[UN][2], xv[UN][kActHalves<F>][2];
     uint32_t mx[UN];
     float sb[UN];
     bool on_expert[UN];
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
-      const int p = base + i * kDownWaves;
-      const bool live = p < total;  // uniform in the wave
-      const int idx = live ? p / units : 0, unit = live ? p - idx * units : 0;
+      const int p = base + i;
+      const bool on = p < total;  // uniform in the wave
+      const int idx = on ? p / units : 0, unit = on ? p - idx * units : 0;
       const int e = __builtin_amdgcn_readfirstlane(active[idx]);
-      const int j = col < a.T ? tab[e * a.T + col] : 0;
-      const bool mine = on_expert[i] = live && j != 0;
-      load_a(wv[i], buffer_of((const char*)a.w_down + e * wbytes, wbytes), wrow, unit, q, live ? abytes : 0);
-      load_b<F>(xv[i], xb, (uint32_t)(col * a.k + j - 1) * bbytes, unit, q, mine ? bbytes : 0);
+      load_rows(wv[i], buffer_of((const char*)a.w_down + e * wbytes, wbytes), wrow, unit * 128, on ? abytes : 0);
+      uint32_t xr[2];
+      bool live[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = load_row(h), j = t < a.T ? tab[e * a.T + t] : 0;
+        live[h] = on && j != 0;
+        xr[h] = (uint32_t)(t * a.k + j - 1) * bbytes;
+      }
+      load_acts<F>(xv[i], xb, xr, live, unit, bbytes, eight);
+      on_expert[i] = on && col < a.T && tab[e * a.T + min(col, a.T - 1)] != 0;
       const char* sc = (const char*)a.s_down;
       if (F == WF_FP8) sc += (int64_t)e * (a.d / 128) * (K / 128) * 4;
       if (F == WF_MX) sc += (int64_t)e * a.d * (K / 32);
-      mx[i] = mx_word_of<F>(sc, row, K, unit);
+      mx[i] = F == WF_MX ? ((const uint32_t*)sc)[(int64_t)(n0 + col) * (K >> 7) + unit] : 0;
       sb[i] = block_scale_of<F>(sc, n0, K, unit);
     }
     __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
       typename Fmt<F>::frag fr[Fmt<F>::NF];
-      to_frags<F>(fr, wv[i], mx[i], q);
+      u32x4_t xf[Fmt<F>::BV];
+      put_rows(lw, wv[i]);
+      put_acts<F>(lw + 2048, xv[i], eight);
+      to_frags<F>(fr, lw, mx[i], q, col);
+      get_acts<F>(xf, lw + 2048, q, col);
       // a lane's results are its own column's: a token takes nothing from an
       // expert that it did not choose, whatever that expert's weights hold
-      const f32x4_t s = unit_dot<F>(f32x4_t{0, 0, 0, 0}, fr, xv[i]);
+      const f32x4_t s = unit_dot<F>(f32x4_t{0, 0, 0, 0}, fr, xf);
 #pragma unroll
       for (int m = 0; m < 4; ++m) acc[m] = on_expert[i] ? fmaf(sb[i], s[m], acc[m]) : acc[m];
     }
   }
+  __syncthreads();  // red lies over the waves' work space
   *(f32x4_t*)(red + (wave * 16 + col) * 16 + q * 4) = acc;
   __syncthreads();
   for (int o = threadIdx.x; o < 256; o += kDownWaves * 64) {
@@ -551,70 +654,104 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_kernel(DecodeArgs
 // go to y [T k, d] in float32, which decode_combine_kernel sums in slot order.
 constexpr int kDownRowWaves = 4;
 
+struct DownTile {
+  rsrc_t w;
+  const void* sc;
+  uint32_t row[2];  // offsets of this lane's two rows
+  int row4, n0;
+};
+
 template <int F, int NB, int UN>
-__device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, rsrc_t wr,
-                                          const void* sc, int n0, int row) {
+__device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, const DownTile& t,
+                                          lds_t* lw) {
   typedef typename Fmt<F>::act AT;
   const int lane = threadIdx.x & 63, q = lane >> 4, col = lane & 15;
   const int K = a.I;
   const int units = (K + Fmt<F>::UK - 1) / Fmt<F>::UK;
   const int abytes = F >= WF_FP8 ? K : K * (int)sizeof(AT), bbytes = K * (int)sizeof(AT);
-  const uint32_t wrow = (uint32_t)row * abytes + q * 16;
   const rsrc_t xb = buffer_of(a.aw, (uint64_t)a.T * a.k * bbytes);
-  uint32_t xr[NB];
+  const bool eight = NB == 1 && n - r0 <= 8;
+  uint32_t xr[NB][2];
+  bool live[NB][2];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) xr[b] = (uint32_t)rows.slot[min(r0 + b * 16 + col, n - 1)] * bbytes;
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = r0 + b * 16 + load_row(h);
+      live[b][h] = r < n;
+      xr[b][h] = (uint32_t)rows.slot[live[b][h] ? r : n - 1] * bbytes;
+    }
   f32x4_t acc[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) acc[b] = f32x4_t{0, 0, 0, 0};
+  constexpr int UB = NB == 1 ? UN : 1;
   for (int base = 0; base < units; base += UN) {
-    u32x4_t wv[UN][2], xv[UN][NB][Fmt<F>::BV];
-    uint32_t mx[UN];
+    u32x4_t wv[UN][2];
 #pragma unroll
-    for (int i = 0; i < UN; ++i) {
-      load_a(wv[i], wr, wrow, base + i, q, abytes);
-      mx[i] = mx_word_of<F>(sc, row, K, min(base + i, units - 1));
+    for (int i = 0; i < UN; ++i) load_rows(wv[i], t.w, t.row, (base + i) * 128, abytes);
+    const uint32_t mx = mx_words<F>(t.sc, t.row4, K, base + (lane & 3));
 #pragma unroll
-      for (int b = 0; b < NB; ++b) load_b<F>(xv[i][b], xb, xr[b], base + i, q, bbytes);
-    }
-    __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
+    for (int i0 = 0; i0 < UN; i0 += UB) {
+      u32x4_t xv[UB][NB][kActHalves<F>][2];
 #pragma unroll
-    for (int i = 0; i < UN; ++i) {
-      typename Fmt<F>::frag fr[Fmt<F>::NF];
-      to_frags<F>(fr, wv[i], mx[i], q);
-      const float sb = block_scale_of<F>(sc, n0, K, min(base + i, units - 1));
+      for (int i = 0; i < UB; ++i)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) unit_mma<F>(acc[b], fr, xv[i][b], sb);
+        for (int b = 0; b < NB; ++b) load_acts<F>(xv[i][b], xb, xr[b], live[b], base + i0 + i, bbytes, eight);
+      __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
+#pragma unroll
+      for (int i = 0; i < UB; ++i) {
+        typename Fmt<F>::frag fr[Fmt<F>::NF];
+        put_rows(lw, wv[i0 + i]);
+        uint32_t m = 0;
+        if constexpr (F == WF_MX) m = (uint32_t)__shfl((int)mx, col * 4 + i0 + i, kWave);
+        to_frags<F>(fr, lw, m, q, col);
+        const float sb = block_scale_of<F>(t.sc, t.n0, K, min(base + i0 + i, units - 1));
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          u32x4_t xf[Fmt<F>::BV];
+          put_acts<F>(lw + 2048, xv[i][b], eight);
+          get_acts<F>(xf, lw + 2048, q, col);
+          unit_mma<F>(acc[b], fr, xf, sb);
+        }
+      }
     }
   }
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const int r = r0 + b * 16 + col;
-    if (r < n && n0 + q * 4 < a.d)  // d is a multiple of 8: four rows are in or out together
-      *(f32x4_t*)(a.y + (int64_t)rows.slot[r] * a.d + n0 + q * 4) = acc[b];
+    if (r < n && t.n0 + q * 4 < a.d)  // d is a multiple of 8: four rows are in or out together
+      *(f32x4_t*)(a.y + (int64_t)rows.slot[r] * a.d + t.n0 + q * 4) = acc[b];
   }
 }
 
 template <int F>
 __global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(DecodeArgs a) {
   __shared__ Rows rows;
+  __shared__ __align__(16) char work[kDownRowWaves * (2048 + 2048 * kActHalves<F>)];
   const int e = __builtin_amdgcn_readfirstlane(item_expert(a.mid, blockIdx.y, a.T * a.k, a.E));
   if (e < 0) return;
   const int n = find_rows(rows, a.mid, a.mw, e, a.T, a.k);
-  const int n0 = (blockIdx.x * kDownRowWaves + tile::wave_id()) * 16;
-  if (n == 0 || n0 >= a.d) return;  // no barrier follows
-  const int row = min(n0 + (int)(threadIdx.x & 15), a.d - 1);
-  const int64_t wb = F >= WF_FP8 ? 1 : sizeof(typename Fmt<F>::act);
-  const uint64_t wbytes = (uint64_t)a.d * a.I * wb;
-  const rsrc_t wr = buffer_of((const char*)a.w_down + e * wbytes, wbytes);
+  DownTile t;
+  const int lane = threadIdx.x & 63, wave = tile::wave_id();
+  t.n0 = (blockIdx.x * kDownRowWaves + wave) * 16;
+  if (n == 0 || t.n0 >= a.d) return;  // no barrier follows
+  const int rowb = a.I * (F >= WF_FP8 ? 1 : (int)sizeof(typename Fmt<F>::act));
+  const uint64_t wbytes = (uint64_t)a.d * rowb;
+  t.w = buffer_of((const char*)a.w_down + e * wbytes, wbytes);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) t.row[h] = (uint32_t)min(t.n0 + load_row(h), a.d - 1) * rowb;
+  t.row4 = t.n0 + (lane >> 2);  // read for WF_MX, where d is a multiple of 128
   const char* sc = (const char*)a.s_down;
   if (F == WF_FP8) sc += (int64_t)e * (a.d / 128) * (a.I / 128) * 4;
   if (F == WF_MX) sc += (int64_t)e * a.d * (a.I / 32);
-  for (int r0 = 0; r0 < n; r0 += 64) {
+  t.sc = sc;
+  lds_t* lw = (lds_t*)work + wave * (2048 + 2048 * kActHalves<F>);
+  constexpr int NBMAX = kMaxBlocks<F>, UN = F >= WF_FP8 ? 2 : 4;
+  for (int r0 = 0; r0 < n; r0 += 16 * NBMAX) {
     const int left = n - r0;
-    if (left <= 16) down_rows<F, 1, 4>(a, rows, r0, n, wr, sc, n0, row);
-    else if (left <= 32) down_rows<F, 2, 2>(a, rows, r0, n, wr, sc, n0, row);
-    else down_rows<F, 4, 1>(a, rows, r0, n, wr, sc, n0, row);
+    if (left <= 16) down_rows<F, 1, UN>(a, rows, r0, n, t, lw);
+    else if (NBMAX == 2 || left <= 32) down_rows<F, 2, UN>(a, rows, r0, n, t, lw);
+    else down_rows<F, NBMAX, UN>(a, rows, r0, n, t, lw);
   }
 }
 
@@ -645,11 +782,12 @@ hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
   constexpr int UN = F >= WF_FP8 ? 2 : 4;
   if (a.T <= 16) {
     MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 8, UN>), gu, dim3(8 * 64), 0, a);
-    const size_t smem = kDownWaves * 1024 + (size_t)a.E * 4 + (size_t)a.E * a.T * 2;  // at most 52 KB
+    const size_t smem = down_work<F>() + (size_t)a.E * 4 + (size_t)a.E * a.T * 2;
+    HIP_RET(tile::allow_smem_once<decode_down_kernel<F>>(down_work<F>() + kMaxExperts * (4 + 16 * 2)));
     MOE_LAUNCH(c, "decode_down", decode_down_kernel<F>, dim3((unsigned)cdiv(a.d, 16)), dim3(kDownWaves * 64), smem, a);
     return hipSuccess;
   }
-  MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 4, 4, UN / 2>), gu, dim3(4 * 64), 0, a);
+  MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, kMaxBlocks<F>, 4, 2>), gu, dim3(4 * 64), 0, a);
   MOE_LAUNCH(c, "decode_down", decode_down_rows_kernel<F>, dim3((unsigned)cdiv(a.d, 16 * kDownRowWaves), items),
              dim3(kDownRowWaves * 64), 0, a);
   const dim3 cg((unsigned)cdiv(a.d, 1024), (unsigned)a.T);
