@@ -434,7 +434,6 @@ RouterArgs router_args(const moe_shape* s, const void* x, const void* w) {
   a.logits_dtype = s->logits_dtype;
   a.x = x;
   a.w = w;
-  a.Ep = (int)(cdiv(s->E, 32) * 32);
   const RouterPlan p = router_plan(s->T, s->d, s->E, s->dtype);
   a.run_tokens = p.run_tokens;
   a.runs = (int)p.runs;
@@ -442,13 +441,13 @@ RouterArgs router_args(const moe_shape* s, const void* x, const void* w) {
 }
 
 struct RouterLayout {
-  size_t wt = 0, parts = 0, total = 0;
+  size_t wf = 0, parts = 0, total = 0;
 };
 RouterLayout router_layout(const moe_shape* s) {
   RouterLayout L;
-  const RouterArgs a = router_args(s, nullptr, nullptr);
-  L.parts = s->dtype == MOE_F32 ? 0 : align256(sizeof(bf16_t) * s->d * a.Ep);
-  L.total = L.parts + sizeof(float) * a.runs * s->E * s->d;
+  const RouterPlan p = router_plan(s->T, s->d, s->E, s->dtype);
+  L.parts = align256(p.wf_bytes);
+  L.total = L.parts + sizeof(float) * p.runs * s->E * s->d;
   return L;
 }
 
@@ -701,7 +700,7 @@ moe_status moe_router_backward(const moe_shape* shape, const void* dlogits, cons
   a.dx_in = dx_in;
   a.dx = dx;
   a.dw = dw_router;
-  a.wt = (bf16_t*)at(workspace, L.wt);
+  a.wf = at(workspace, L.wf);
   a.parts = (float*)at(workspace, L.parts);
   const LaunchCtx c = make_ctx(stream);
   (void)hipGetLastError();

@@ -21,11 +21,13 @@
 #include <type_traits>
 
 #include "common.h"
+#include "rowload.h"
 #include "tile.h"
 
 namespace moe {
 namespace {
 
+using namespace rowload;
 using tile::u32x4_t;
 
 // ------------------------------------------------------------------- routing
@@ -165,52 +167,6 @@ template <> struct Fmt<WF_BF16> {
   static constexpr int UK = 64, BV = 2, NF = 2;
 };
 
-// Loads go through buffer descriptors: a 32-bit offset per lane, and zeros for
-// a lane that asks past the end, which is how a K tail becomes exact zeros on
-// both operands (every buffer here is below kPast bytes).
-constexpr uint32_t kPast = 0xffffff00u;
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-__device__ __forceinline__ rsrc_t buffer_of(const void* p, uint64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)(uint32_t)bytes, 0x00020000);
-}
-__device__ __forceinline__ u32x4_t load16(rsrc_t r, uint32_t off, bool ok) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)(ok ? off : kPast), 0, 0);
-}
-
-// An MFMA wants neighbouring lanes to hold neighbouring rows, but a load whose
-// neighbouring lanes lie in different rows costs the vector memory unit 64
-// cycles, and one whose neighbours are contiguous 25 (measured, 1 KB from the
-// caches; 64 cycles for every 1 KB would cap the chip at 9.8 TB/s with the
-// activations' loads included).  So a load takes 8 rows of 128 bytes, eight
-// lanes a row, and a wave turns the rows around through its own 2 KB of LDS:
-// [16 rows][128 bytes], 16-byte chunks XOR-swizzled so that the writes and the
-// reads of 16 rows at one chunk are free of bank conflicts.  No barriers: the
-// LDS serves one wave's accesses in order.
-typedef __attribute__((address_space(3))) char lds_t;
-__device__ __forceinline__ int row_chunk(int row, int chunk) { return row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4); }
-
-// 8 half + lane / 8: the row of a 16-row group that this lane loads.
-__device__ __forceinline__ int load_row(int half) { return half * 8 + (int)((threadIdx.x & 63) >> 3); }
-
-// 128 bytes at byte `at` of rows at offsets row[0], row[1] (this lane's two
-// rows), of which `bytes` exist; rows with live[h] false read as zeros.
-__device__ __forceinline__ void load_rows(u32x4_t (&v)[2], rsrc_t r, const uint32_t (&row)[2], int at, int bytes,
-                                          bool live0 = true, bool live1 = true) {
-  const int off = at + (int)(threadIdx.x & 7) * 16;
-  v[0] = load16(r, row[0] + off, live0 && off < bytes);
-  v[1] = load16(r, row[1] + off, live1 && off < bytes);
-}
-
-__device__ __forceinline__ void put_rows(lds_t* p, const u32x4_t (&v)[2]) {
-  const int chunk = threadIdx.x & 7;
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-    *(__attribute__((address_space(3))) u32x4_t*)(p + row_chunk(load_row(h), chunk)) = v[h];
-}
-__device__ __forceinline__ u32x4_t get_chunk(const lds_t* p, int row, int chunk) {
-  return *(const __attribute__((address_space(3))) u32x4_t*)(p + row_chunk(row, chunk));
-}
-
 // A unit's weights in flight, and its scale bytes: `mx` holds, in lane 4 r + i,
 // row r's four scale bytes of unit i of a batch of up to four units.
 template <int F>
@@ -271,11 +227,13 @@ __device__ __forceinline__ void load_acts(u32x4_t (&v)[kActHalves<F>][2], rsrc_t
 template <int F>
 __device__ __forceinline__ void put_acts(lds_t* p, const u32x4_t (&v)[kActHalves<F>][2], bool eight) {
   const int chunk = threadIdx.x & 7;
+  turn_fence();
 #pragma unroll
   for (int h = 0; h < kActHalves<F>; ++h) {
     *(__attribute__((address_space(3))) u32x4_t*)(p + h * 2048 + row_chunk(load_row(0), chunk)) = v[h][0];
     if (!eight) *(__attribute__((address_space(3))) u32x4_t*)(p + h * 2048 + row_chunk(load_row(1), chunk)) = v[h][1];
   }
+  turn_fence();
 }
 template <int F>
 __device__ __forceinline__ void get_acts(u32x4_t (&b)[Fmt<F>::BV], const lds_t* p, int q, int col) {
@@ -500,6 +458,7 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
 template <int F, int NBMAX, int NW, int UN>
 __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   static_assert(UN <= 4, "mx_words holds four units");
+  static_assert(NW * 64 >= kDecodeMaxT, "find_rows takes a thread per token");
   __shared__ Rows rows;
   __shared__ __align__(16) char smem[gu_smem<F, NW, NBMAX>()];
   const int e = __builtin_amdgcn_readfirstlane(item_expert(a.mid, blockIdx.y, a.T * a.k, a.E));
@@ -726,6 +685,7 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
 
 template <int F>
 __global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(DecodeArgs a) {
+  static_assert(kDownRowWaves * 64 >= kDecodeMaxT, "find_rows takes a thread per token");
   __shared__ Rows rows;
   __shared__ __align__(16) char work[kDownRowWaves * (2048 + 2048 * kActHalves<F>)];
   const int e = __builtin_amdgcn_readfirstlane(item_expert(a.mid, blockIdx.y, a.T * a.k, a.E));

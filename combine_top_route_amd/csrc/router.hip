@@ -15,27 +15,16 @@
 // No product uses atomics: K or T is split over waves or work-groups and the
 // parts are added in a fixed order.
 #include "common.h"
+#include "rowload.h"
 #include "tile.h"
 
 namespace moe {
 namespace {
 
+using namespace rowload;
 using tile::s16x4_t;
 using tile::s16x8_t;
 using tile::u32x4_t;
-
-constexpr uint32_t kPast = 0xffffff00u;  // an offset past every buffer here: loads give 0
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-__device__ __forceinline__ rsrc_t buffer_of(const void* p, uint64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)(uint32_t)bytes, 0x00020000);
-}
-__device__ __forceinline__ u32x4_t load16(rsrc_t r, uint32_t off) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
-}
-
-// One value of a tensor in either type.
-__device__ __forceinline__ float value_at(const float* p) { return *p; }
-__device__ __forceinline__ float value_at(const bf16_t* p) { return bf2f(*p); }
 
 // s + a b over the 16 (float) or 32 (bf16) values of K in two 16-byte operands.
 template <typename T>
@@ -53,16 +42,23 @@ __device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, f32x4_t s) {
 
 // ------------------------------------------------------------------ forward
 // Work-group: 16 MB tokens by 16 NB experts.  Each of the 8 waves computes the
-// whole tile over every eighth 128-byte unit of K straight from memory (no
+// whole tile over every eighth 128-byte unit of K from its own loads (no
 // operand is read twice by a work-group), and the eight parts meet in LDS.
 constexpr int kFwdWaves = 8;
+
+template <int MB, int NB>
+constexpr size_t fwd_smem() {  // the waves' turning space, then MR token blocks of parts
+  constexpr int MR = MB * NB > 16 ? 16 / NB : MB;
+  const size_t turn = (size_t)kFwdWaves * 4096, parts = (size_t)kFwdWaves * MR * NB * 1024;
+  return turn > parts ? turn : parts;
+}
 
 template <typename T, int MB, int NB>
 __global__ __launch_bounds__(kFwdWaves * 64, 2) void router_fwd_kernel(const T* __restrict__ x,
                                                                        const T* __restrict__ w, int Tn, int E, int d,
                                                                        void* __restrict__ logits, int logits_f32) {
   constexpr int MR = MB * NB > 16 ? 16 / NB : MB;  // token blocks per LDS round: at most 128 KB
-  extern __shared__ __align__(16) float red[];     // [wave][MR][NB][16 tokens][16 experts]
+  extern __shared__ __align__(16) char smem[];
   const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
   const int64_t t0 = (int64_t)blockIdx.x * (16 * MB);
   const int e0 = blockIdx.y * (16 * NB);
@@ -71,58 +67,82 @@ __global__ __launch_bounds__(kFwdWaves * 64, 2) void router_fwd_kernel(const T* 
   // rows past the end of either buffer read as zeros
   const rsrc_t xb = buffer_of(x + t0 * d, (uint64_t)tn * bytes);
   const rsrc_t wb = buffer_of(w + (int64_t)e0 * d, (uint64_t)en * bytes);
+  lds_t* turn = (lds_t*)smem + wave * 4096;
+  const uint32_t row[2] = {(uint32_t)load_row(0) * bytes, (uint32_t)load_row(1) * bytes};
   f32x4_t acc[MB][NB];
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
     for (int n = 0; n < NB; ++n) acc[m][n] = f32x4_t{0, 0, 0, 0};
   for (int off = wave * 128; off < bytes; off += kFwdWaves * 128) {
-    u32x4_t xv[MB][2], wv[NB][2];
+    u32x4_t xv[MB][2], wv[MB * NB > 16 ? NB / 2 : NB][2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int o = off + c * 64 + q * 16;
-      const bool ok = o < bytes;
+    for (int m = 0; m < MB; ++m) {
+      const uint32_t r[2] = {row[0] + m * 16 * bytes, row[1] + m * 16 * bytes};
+      load_rows(xv[m], xb, r, off, bytes);
+    }
+    // at the largest tile half of w's rows wait for x's registers
+    constexpr int NH = MB * NB > 16 ? NB / 2 : NB;
+    auto load_w = [&](int n) {
+      const uint32_t r[2] = {row[0] + n * 16 * bytes, row[1] + n * 16 * bytes};
+      load_rows(wv[n % NH], wb, r, off, bytes);
+    };
 #pragma unroll
-      for (int m = 0; m < MB; ++m) xv[m][c] = load16(xb, ok ? (uint32_t)((m * 16 + col) * bytes + o) : kPast);
+    for (int n = 0; n < NH; ++n) load_w(n);
 #pragma unroll
-      for (int n = 0; n < NB; ++n) wv[n][c] = load16(wb, ok ? (uint32_t)((n * 16 + col) * bytes + o) : kPast);
+    for (int m = 0; m < MB; ++m) {
+      put_rows(turn + (m & 1) * 2048, xv[m]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) xv[m][c] = get_chunk(turn + (m & 1) * 2048, col, 4 * c + q);
     }
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int n = 0; n < NB; ++n) {
+      put_rows(turn + (n & 1) * 2048, wv[n % NH]);
+      if (n + NH < NB) load_w(n + NH);
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
+      for (int c = 0; c < 2; ++c) {
+        const u32x4_t wf = get_chunk(turn + (n & 1) * 2048, col, 4 * c + q);
 #pragma unroll
-        for (int n = 0; n < NB; ++n) acc[m][n] = mma16<T>(wv[n][c], xv[m][c], acc[m][n]);
+        for (int m = 0; m < MB; ++m) acc[m][n] = mma16<T>(wf, xv[m][c], acc[m][n]);
+      }
+    }
   }
-  // a lane holds 4 experts (rows 4 q ..) of token `col`
+  // parts [wave][MR][NB][16 tokens][16 experts]: a lane holds 4 experts (rows
+  // 4 q ..) of token `col`; threads then add them 16 bytes by 16 bytes as they lie
+  float* red = (float*)smem;
+  const bool vec = E % 4 == 0;
 #pragma unroll
   for (int m0 = 0; m0 < MB; m0 += MR) {
-    if (m0) __syncthreads();
+    __syncthreads();
 #pragma unroll
     for (int m = 0; m < MR; ++m)
 #pragma unroll
       for (int n = 0; n < NB; ++n)
         *(f32x4_t*)(red + (((wave * MR + m) * NB + n) * 16 + col) * 16 + q * 4) = acc[m0 + m][n];
     __syncthreads();
-    for (int o = threadIdx.x; o < MR * NB * 64; o += kFwdWaves * 64) {  // four experts each
-      const int e4 = o % (NB * 4), tt = o / (NB * 4);                  // consecutive threads: consecutive experts
-      const int m = tt >> 4, c = tt & 15, n = e4 >> 2;
+    for (int o = threadIdx.x; o < MR * NB * 64; o += kFwdWaves * 64) {
       f32x4_t s = {0, 0, 0, 0};
 #pragma unroll
       for (int v = 0; v < kFwdWaves; ++v) {
-        const f32x4_t p = *(const f32x4_t*)(red + (((v * MR + m) * NB + n) * 16 + c) * 16 + (e4 & 3) * 4);
+        const f32x4_t p = *(const f32x4_t*)(red + (v * MR * NB * 64 + o) * 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] += p[i];
       }
-      const int t = (m0 + m) * 16 + c;
-      if (t < tn) {
-        const int64_t at = (t0 + t) * E + e0 + e4 * 4;
+      const int e = (o >> 6) % NB * 16 + (o & 3) * 4, t = (m0 + (o >> 6) / NB) * 16 + ((o >> 2) & 15);
+      if (t < tn && e < en) {
+        const int64_t at = (t0 + t) * E + e0 + e;
+        if (vec && logits_f32) {
+          *(f32x4_t*)((float*)logits + at) = s;
+        } else if (vec) {
+          *(uint2*)((bf16_t*)logits + at) = uint2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (e4 * 4 + i < en) {
-            if (logits_f32) ((float*)logits)[at + i] = s[i];
-            else ((bf16_t*)logits)[at + i] = f2bf(s[i]);
-          }
+          for (int i = 0; i < 4; ++i)
+            if (e + i < en) {
+              if (logits_f32) ((float*)logits)[at + i] = s[i];
+              else ((bf16_t*)logits)[at + i] = f2bf(s[i]);
+            }
+        }
       }
     }
   }
@@ -130,8 +150,7 @@ __global__ __launch_bounds__(kFwdWaves * 64, 2) void router_fwd_kernel(const T* 
 
 template <typename T, int MB, int NB>
 hipError_t fwd(const LaunchCtx& c, const RouterArgs& a, void* logits) {
-  constexpr int MR = MB * NB > 16 ? 16 / NB : MB;
-  constexpr size_t smem = (size_t)kFwdWaves * MR * NB * 1024;
+  constexpr size_t smem = fwd_smem<MB, NB>();
   HIP_RET(tile::allow_smem_once<router_fwd_kernel<T, MB, NB>>(smem));
   MOE_LAUNCH(c, "router_fwd", (router_fwd_kernel<T, MB, NB>),
              dim3((unsigned)cdiv(a.T, 16 * MB), (unsigned)cdiv(a.E, 16 * NB)), dim3(kFwdWaves * 64), smem,
@@ -159,12 +178,15 @@ hipError_t fwd_any(const LaunchCtx& c, const RouterArgs& a, void* logits) {
 }
 
 // ------------------------------------------------- backward, first launch
-// dw parts: work-group (E block of 128, d block of 128, run of tokens); steps
-// of TS tokens pass through LDS as they lie in memory, [token][column], and a
-// transposing LDS read (16-bit) or plain 4-byte reads (K = 4 float32 MFMA)
-// hand the MFMA its token-contiguous operands.  Parts are float32 [run][E][d].
-// The remaining work-groups write w's transpose [d][Ep] for the second launch
-// (bf16: K = expert has to be contiguous there).
+// dw parts: work-group (E block of 128, d block of 128, run of tokens).  Steps
+// of TS tokens pass through two LDS buffers as they lie in memory,
+// [token][column], the next step's loads in flight; a transposing LDS read
+// (16-bit) or plain 4-byte reads (the K = 4 float32 MFMA) hand the MFMA its
+// token-contiguous operands.  Each half of the waves takes half of a step's
+// tokens and the whole 128 x 128 tile in quarters of 64 x 64 (the least LDS
+// traffic per product: it is what bounds the kernel beside the loads); the
+// halves meet in LDS.  Parts are float32 [run][E][d].
+// The remaining work-groups lay w out as the second launch's MFMA operands.
 constexpr int kDwE = 128, kDwD = 128;
 
 template <typename T> struct DwTile;
@@ -182,15 +204,91 @@ __device__ __forceinline__ void split_bf16(float v, bf16_t& hi, bf16_t& lo) {
   lo = fabsf(h) < __builtin_huge_valf() ? f2bf(v - h) : (bf16_t)0;
 }
 
+// Sixteen bytes of dlogits as floats.
+template <typename LT>
+__device__ __forceinline__ void unpack16(float* f, u32x4_t v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (sizeof(LT) == 4) {
+      f[j] = __uint_as_float(v[j]);
+    } else {
+      f[2 * j] = __uint_as_float(v[j] << 16);
+      f[2 * j + 1] = __uint_as_float(v[j] & 0xffff0000u);
+    }
+  }
+}
+
+// A tile of dlogits, rows t0 .. t0 + ROWS (of which `rows` exist) by experts
+// e0 .. e0 + 128, loaded by NT threads 16 bytes each (neighbours contiguous)
+// and stored for the MFMAs: float32 [row][ST], or the two bf16 parts in hs and
+// ls.  Rows and experts that do not exist become zeros.
+template <typename T, typename LT, int ROWS, int NT, int ST>
+struct DlTile {
+  static constexpr int PER = 16 / (int)sizeof(LT);       // values per load
+  static constexpr int UPR = 128 / PER;                  // loads per row
+  static constexpr int N = ROWS * UPR / NT;              // loads per thread
+  static constexpr bool LO = sizeof(T) == 2 && sizeof(LT) == 4;
+  u32x4_t v[N];
+  __device__ __forceinline__ void load(const LT* p, int E, int e0, int rows, bool vec) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = (int)threadIdx.x + i * NT, r = u / UPR, e = e0 + (u % UPR) * PER;
+      v[i] = u32x4_t{0, 0, 0, 0};
+      if (r < rows && e < E) {
+        const LT* a = p + (int64_t)r * E + e;
+        if (vec) {  // E is a multiple of PER and the rows are aligned
+          v[i] = *(const u32x4_t*)a;
+        } else {
+#pragma unroll
+          for (int j = 0; j < PER; ++j)
+            if (e + j < E) {
+              if constexpr (sizeof(LT) == 4) v[i][j] = __float_as_uint(a[j]);
+              else v[i][j >> 1] |= (uint32_t)a[j] << (16 * (j & 1));
+            }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(char* hs, char* ls) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = (int)threadIdx.x + i * NT, r = u / UPR, c = (u % UPR) * PER;
+      if constexpr (sizeof(T) == 4) {
+        float f[PER];
+        unpack16<LT>(f, v[i]);
+#pragma unroll
+        for (int j = 0; j < PER; j += 4)
+          *(f32x4_t*)(hs + r * ST + (c + j) * 4) = f32x4_t{f[j], f[j + 1], f[j + 2], f[j + 3]};
+      } else if constexpr (!LO) {
+        *(u32x4_t*)(hs + r * ST + c * 2) = v[i];
+      } else {
+        uint2 h, l;
+        bf16_t a[4], b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split_bf16(__uint_as_float(v[i][j]), a[j], b[j]);
+        h.x = (uint32_t)a[0] | ((uint32_t)a[1] << 16);
+        h.y = (uint32_t)a[2] | ((uint32_t)a[3] << 16);
+        l.x = (uint32_t)b[0] | ((uint32_t)b[1] << 16);
+        l.y = (uint32_t)b[2] | ((uint32_t)b[3] << 16);
+        *(uint2*)(hs + r * ST + c * 2) = h;
+        *(uint2*)(ls + r * ST + c * 2) = l;
+      }
+    }
+  }
+};
+
+template <typename T, typename LT>
+__device__ __forceinline__ bool dl_vec(const RouterArgs& a) { return (a.E * sizeof(LT)) % 16 == 0; }
+
+template <typename T, typename LT>
+constexpr int dw_stage() { return (sizeof(T) == 2 && sizeof(LT) == 4 ? 3 : 2) * DwTile<T>::TS * DwTile<T>::STRIDE; }
+
 template <typename T, typename LT>
 __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb, int db, int run) {
   constexpr int TS = DwTile<T>::TS, ST = DwTile<T>::STRIDE;
   constexpr bool LO = sizeof(T) == 2 && sizeof(LT) == 4;  // dlogits has a second part
-  constexpr int XV = TS * kDwD * (int)sizeof(T) / (512 * 16);  // 16-byte loads of x per thread
-  constexpr int LV = TS * kDwE / 512;                          // dlogits values per thread, consecutive experts
-  char* xs = smem;
-  char* hs = smem + TS * ST;
-  char* ls = smem + 2 * TS * ST;
+  constexpr int XU = kDwD * (int)sizeof(T) / 16;          // 16-byte loads per row of x
+  constexpr int XV = TS * XU / 512;
   const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
   const int e0 = eb * kDwE, d0 = db * kDwD;
   const int64_t tb = (int64_t)run * a.run_tokens;
@@ -198,322 +296,284 @@ __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb,
   const int xrow = a.d * (int)sizeof(T);
   const T* xp = (const T*)a.x + tb * a.d;
   const LT* lp = (const LT*)a.dlogits + tb * a.E;
-  // this thread's dlogits values: row lr, experts le .. le + LV of the block
-  const int lr = (int)threadIdx.x / (kDwE / LV), le = ((int)threadIdx.x % (kDwE / LV)) * LV;
-  const bool lvec = (a.E * sizeof(LT)) % 16 == 0 && ((uintptr_t)a.dlogits & 15) == 0 && e0 + le + LV <= a.E;
+  const bool vec = dl_vec<T, LT>(a);
   u32x4_t xv[XV];
-  float lv[LV];
+  DlTile<T, LT, TS, 512, ST> dl;
   auto fetch = [&](int s) {  // tokens s .. s + TS of the run; zeros past its end and past E and d
 #pragma unroll
     for (int i = 0; i < XV; ++i) {
-      const int u = (int)threadIdx.x + i * 512;
-      const int r = u / (kDwD * (int)sizeof(T) / 16), cb = (u % (kDwD * (int)sizeof(T) / 16)) * 16;
+      const int u = (int)threadIdx.x + i * 512, r = u / XU, cb = (u % XU) * 16;
       xv[i] = u32x4_t{0, 0, 0, 0};
       if (s + r < tn && d0 * (int)sizeof(T) + cb < xrow)
         xv[i] = *(const u32x4_t*)((const char*)(xp + (int64_t)(s + r) * a.d + d0) + cb);
     }
-    const LT* p = lp + (int64_t)(s + lr) * a.E + e0 + le;
-#pragma unroll
-    for (int i = 0; i < LV; ++i) lv[i] = 0.0f;
-    if (s + lr < tn) {
-      if (lvec) {
-#pragma unroll
-        for (int i = 0; i < LV * (int)sizeof(LT) / 16; ++i) {
-          const u32x4_t v = ((const u32x4_t*)p)[i];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (sizeof(LT) == 4) {
-              lv[4 * i + j] = __uint_as_float(v[j]);
-            } else {
-              lv[8 * i + 2 * j] = __uint_as_float(v[j] << 16);
-              lv[8 * i + 2 * j + 1] = __uint_as_float(v[j] & 0xffff0000u);
-            }
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < LV; ++i)
-          if (e0 + le + i < a.E) lv[i] = value_at(p + i);
-      }
-    }
+    dl.load(lp + (int64_t)s * a.E, a.E, e0, tn - s, vec);
   };
-  const int we = (wave >> 2) * 64, wd = (wave & 3) * 32;  // this wave's 64 experts by 32 columns
-  f32x4_t acc[4][2];
+  auto stage = [&](char* b) {
+#pragma unroll
+    for (int i = 0; i < XV; ++i) {
+      const int u = (int)threadIdx.x + i * 512, r = u / XU, cb = (u % XU) * 16;
+      *(u32x4_t*)(b + r * ST + cb) = xv[i];
+    }
+    dl.store(b + TS * ST, b + 2 * TS * ST);
+  };
+  const int kh = (wave >> 2) * (TS / 2), we = ((wave >> 1) & 1) * 64, wd = (wave & 1) * 64;
+  const bool busy = e0 + we < a.E && d0 + wd < a.d;  // uniform: this quarter exists
+  f32x4_t acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
   fetch(0);
-  for (int s = 0; s < tn; s += TS) {
-    __syncthreads();  // the previous step's reads are done
+  stage(smem);
+  if (TS < tn) fetch(TS);
+  for (int s = 0, buf = 0; s < tn; s += TS, buf ^= 1) {
+    __syncthreads();  // this step's buffer is written, the other one's reads are done
+    const char* xs = smem + buf * dw_stage<T, LT>();
+    const char* hs = xs + TS * ST;
+    const char* ls = hs + TS * ST;
+    if (busy) {
+      if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < XV; ++i) {
-      const int u = (int)threadIdx.x + i * 512;
-      const int r = u / (kDwD * (int)sizeof(T) / 16), cb = (u % (kDwD * (int)sizeof(T) / 16)) * 16;
-      *(u32x4_t*)(xs + r * ST + cb) = xv[i];
-    }
-    if constexpr (sizeof(T) == 4) {
+        for (int k = 0; k < TS / 2; k += 4) {
+          float av[4], bv[4];
 #pragma unroll
-      for (int i = 0; i < LV; i += 4)
-        *(f32x4_t*)(hs + lr * ST + (le + i) * 4) = f32x4_t{lv[i], lv[i + 1], lv[i + 2], lv[i + 3]};
-    } else {
+          for (int i = 0; i < 4; ++i) av[i] = *(const float*)(hs + (kh + k + q) * ST + (we + i * 16 + col) * 4);
 #pragma unroll
-      for (int i = 0; i < LV; i += 8) {
-        u32x4_t h, l;
+          for (int j = 0; j < 4; ++j) bv[j] = *(const float*)(xs + (kh + k + q) * ST + (wd + j * 16 + col) * 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          bf16_t h0, l0, h1, l1;
-          split_bf16(lv[i + 2 * j], h0, l0);
-          split_bf16(lv[i + 2 * j + 1], h1, l1);
-          h[j] = (uint32_t)h0 | ((uint32_t)h1 << 16);
-          l[j] = (uint32_t)l0 | ((uint32_t)l1 << 16);
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[i], bv[j], acc[i][j], 0, 0, 0);
         }
-        *(u32x4_t*)(hs + lr * ST + (le + i) * 2) = h;
-        if constexpr (LO) *(u32x4_t*)(ls + lr * ST + (le + i) * 2) = l;
-      }
-    }
-    __syncthreads();
-    if (s + TS < tn) fetch(s + TS);  // lands while this step computes
-    if constexpr (sizeof(T) == 4) {
+      } else {
+        // eight tokens 8 q .. of column `col`: the 16 lanes of a group read 4
+        // tokens by 16 columns and get them transposed
+        auto frag = [&](const char* base, int c0) {
+          const char* p = base + (kh + q * 8 + (col >> 2)) * ST + (c0 + 4 * (col & 3)) * 2;
+          const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
+          const s16x4_t hi =
+              __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(p + 4 * ST));
+          return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+        static_assert(TS == 64, "a half step is one MFMA's K");
+        bf16x8_t bv[4];
 #pragma unroll
-      for (int k = 0; k < TS; k += 4) {
-        float av[4], bv[2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) av[i] = *(const float*)(hs + (k + q) * ST + (we + i * 16 + col) * 4);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) bv[j] = *(const float*)(xs + (k + q) * ST + (wd + j * 16 + col) * 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[i], bv[j], acc[i][j], 0, 0, 0);
-      }
-    } else {
-      // eight tokens 8 q .. of column `col`: the 16 lanes of a group read 4
-      // tokens by 16 columns and get them transposed
-      auto frag = [&](const char* base, int k, int c0) {
-        const char* p = base + (k + q * 8 + (col >> 2)) * ST + (c0 + 4 * (col & 3)) * 2;
-        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
-        const s16x4_t hi =
-            __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(p + 4 * ST));
-        return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-      };
-#pragma unroll
-      for (int k = 0; k < TS; k += 32) {
-        bf16x8_t bv[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) bv[j] = frag(xs, k, wd + j * 16);
+        for (int j = 0; j < 4; ++j) bv[j] = frag(xs, wd + j * 16);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bf16x8_t h = frag(hs, k, we + i * 16);
+          const bf16x8_t h = frag(hs, we + i * 16);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h, bv[j], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h, bv[j], acc[i][j], 0, 0, 0);
           if constexpr (LO) {
-            const bf16x8_t l = frag(ls, k, we + i * 16);
+            const bf16x8_t l = frag(ls, we + i * 16);
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 4; ++j)
               acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(l, bv[j], acc[i][j], 0, 0, 0);
           }
         }
       }
     }
+    if (s + TS < tn) {
+      stage(smem + (buf ^ 1) * dw_stage<T, LT>());
+      if (s + 2 * TS < tn) fetch(s + 2 * TS);  // a step to land in
+    }
   }
+  // the halves: waves 4 .. 7 leave theirs in LDS, 0 .. 3 add and write
+  __syncthreads();
+  float* half = (float*)smem + (wave & 3) * 4096;
+  if (wave >= 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *(f32x4_t*)(half + ((i * 4 + j) * 64 + lane) * 4) = acc[i][j];
+  }
+  __syncthreads();
+  if (wave >= 4 || !busy) return;
   float* part = a.parts + (int64_t)run * a.E * a.d;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 4; ++j) {
+      const f32x4_t o = *(const f32x4_t*)(half + ((i * 4 + j) * 64 + lane) * 4);
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const int e = e0 + we + i * 16 + q * 4 + m, c = d0 + wd + j * 16 + col;
-        if (e < a.E && c < a.d) part[(int64_t)e * a.d + c] = acc[i][j][m];
+        if (e < a.E && c < a.d) part[(int64_t)e * a.d + c] = acc[i][j][m] + o[m];
       }
+    }
 }
 
-// wt[c][e] = w[e][c] for 64 columns, experts up to the next multiple of 32
-// (zeros past E).
-__device__ __forceinline__ void transpose_w(const RouterArgs& a, char* smem, int cb) {
-  bf16_t* s = (bf16_t*)smem;  // [32 experts][64 + 2 columns]
-  const int c0 = cb * 64;
-  for (int e0 = 0; e0 < a.Ep; e0 += 32) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < 32 * 64; i += 512) {
-      const int e = i >> 6, c = i & 63;
-      s[e * 66 + c] = e0 + e < a.E && c0 + c < a.d ? ((const bf16_t*)a.w)[(int64_t)(e0 + e) * a.d + c0 + c] : 0;
+// The second launch's operand layout of w.  A wave there takes 16 DT columns
+// of d, tile j of which holds columns base + DT col + j (so that its results
+// are DT neighbouring columns of a lane); step k of KS experts is 16 bytes a
+// lane: experts k KS + q 16/size .. of column col.  wf holds them [column
+// block][expert block of 128][j][k][lane], zeros past E and d.
+template <typename T> constexpr int dx_tiles = 8 / (int)sizeof(T);
+constexpr int kDxE = 128;
+template <typename T> constexpr int dx_steps = kDxE * (int)sizeof(T) / 64;
+
+template <typename T>
+__device__ __forceinline__ void lay_out_w(const RouterArgs& a, int cb, int eb) {
+  constexpr int DT = dx_tiles<T>, NK = dx_steps<T>, PER = 16 / (int)sizeof(T);
+  T* out = (T*)a.wf + ((int64_t)cb * a.dx_eblocks + eb) * DT * NK * 64 * PER;
+  // neighbouring threads read neighbouring columns of w
+  for (int i = threadIdx.x; i < DT * NK * 64; i += 512) {
+    const int j = i % DT, col = i / DT % 16, q = i / (16 * DT) % 4, k = i / (64 * DT);
+    const int c = cb * 16 * DT + DT * col + j;
+    T v[PER];
+#pragma unroll
+    for (int m = 0; m < PER; ++m) {
+      const int e = eb * kDxE + k * 4 * PER + q * PER + m;
+      v[m] = e < a.E && c < a.d ? ((const T*)a.w)[(int64_t)e * a.d + c] : (T)0;
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 32 * 64; i += 512) {
-      const int c = i >> 5, e = i & 31;
-      if (c0 + c < a.d) a.wt[(int64_t)(c0 + c) * a.Ep + e0 + e] = s[e * 66 + c];
-    }
+    *(u32x4_t*)(out + ((int64_t)(j * NK + k) * 64 + q * 16 + col) * PER) = *(const u32x4_t*)v;
   }
 }
 
 template <typename T, typename LT>
-__global__ __launch_bounds__(512, 4) void router_dw_kernel(RouterArgs a) {
-  constexpr int parts = sizeof(T) == 2 && sizeof(LT) == 4 ? 3 : 2;
-  __shared__ __align__(16) char smem[parts * DwTile<T>::TS * DwTile<T>::STRIDE];
+__global__ __launch_bounds__(512, 2) void router_dw_kernel(RouterArgs a) {
+  extern __shared__ __align__(16) char smem[];
   int b = blockIdx.x;
   if (b < a.dw_groups) {
     const int db = b % a.d_blocks;
     b /= a.d_blocks;
     dw_part<T, LT>(a, smem, b % a.e_blocks, db, b / a.e_blocks);
-  } else if constexpr (sizeof(T) == 2) {
-    transpose_w(a, smem, b - a.dw_groups);
+  } else {
+    b -= a.dw_groups;
+    lay_out_w<T>(a, b / a.dx_eblocks, b % a.dx_eblocks);
   }
 }
 
 // ------------------------------------------------ backward, second launch
-// dx: one wave keeps the operands of 16 DT columns of d and up to 128 experts
-// in registers and runs over blocks of 16 tokens, whose dlogits it reads from
-// the caches.  The MFMA's rows are columns of d, taken so that a lane holds
-// 4 DT consecutive ones of its token.
-constexpr int kDxWaves = 4, kDxE = 128;
+// dx: work-group of 4 waves, each with the operands of its 16 DT columns and
+// up to 128 experts in registers, over blocks of 32 tokens whose dlogits pass
+// through LDS once for all four.
+constexpr int kDxWaves = 4, kDxTok = 32;
+template <typename T> constexpr int dx_stride = 128 * (int)sizeof(T) + 16;  // bytes per token row in LDS
 
-// Values e .. e + n of dlogits row t; zeros past E or T.
-template <typename LT, int N>
-__device__ __forceinline__ void dl_row(float (&v)[N], const RouterArgs& a, int64_t t, int e, bool vec) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = 0.0f;
-  if (t >= a.T) return;
-  const LT* p = (const LT*)a.dlogits + t * a.E + e;
-  if (vec && e + N <= a.E) {
-    constexpr int PER = 16 / (int)sizeof(LT);
-    if constexpr (N >= PER) {
-#pragma unroll
-      for (int i = 0; i < N / PER; ++i) {
-        const u32x4_t u = ((const u32x4_t*)p)[i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (sizeof(LT) == 4) {
-            v[4 * i + j] = __uint_as_float(u[j]);
-          } else {
-            v[8 * i + 2 * j] = __uint_as_float(u[j] << 16);
-            v[8 * i + 2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-          }
-        }
-      }
-      return;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (e + i < a.E) v[i] = value_at(p + i);
-}
-
-template <typename T, typename LT>
-__device__ __forceinline__ void dx_part(const RouterArgs& a, int cb, int run) {
-  constexpr bool BF = sizeof(T) == 2;
-  constexpr bool LO = BF && sizeof(LT) == 4;
-  constexpr int DT = BF ? 4 : 2;            // tiles of 16 columns per wave
-  constexpr int KS = BF ? 32 : 16;          // experts per 16-byte operand step
-  constexpr int NK = kDxE / KS;
+// MULTI: more than 128 experts; w's operands then pass through the registers a
+// step at a time, for all 32 tokens, instead of staying in them.
+template <typename T, typename LT, bool MULTI>
+__device__ __forceinline__ void dx_part(const RouterArgs& a, char* smem, int cb, int run) {
+  constexpr bool LO = sizeof(T) == 2 && sizeof(LT) == 4;
+  constexpr int DT = dx_tiles<T>, NK = dx_steps<T>, ST = dx_stride<T>, PER = 16 / (int)sizeof(T);
+  constexpr int HG = MULTI ? 2 : 1;  // groups of 16 tokens whose sums are held together
   const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
-  const int c0 = (cb * kDxWaves + wave) * 16 * DT;
-  if (c0 >= a.d) return;
-  const bool vec = (a.E * sizeof(LT)) % 16 == 0 && ((uintptr_t)a.dlogits & 15) == 0;
-  // operand row `col` of tile j is column c0 + (col / 4) 4 DT + 4 j + col % 4,
-  // so that result rows 4 q .. of the tiles are 4 DT consecutive columns
-  u32x4_t wv[DT][NK];
-  auto load_w = [&](int e0) {
+  const int wcb = cb * kDxWaves + wave;             // this wave's block of 16 DT columns
+  const bool busy = wcb * 16 * DT < a.d;            // uniform
+  const int c = wcb * 16 * DT + col * DT;           // this lane's DT columns; d is a multiple of 8
+  const bool in = c < a.d;
+  const bool vec = dl_vec<T, LT>(a);
+  const int ebs = a.dx_eblocks;
+  const T* wp = (const T*)a.wf + (int64_t)wcb * ebs * DT * NK * 64 * PER + lane * PER;
+  u32x4_t wv[DT][MULTI ? 1 : NK];
+  if (!MULTI && busy) {
 #pragma unroll
-    for (int j = 0; j < DT; ++j) {
-      const int c = c0 + (col >> 2) * 4 * DT + 4 * j + (col & 3);
+    for (int j = 0; j < DT; ++j)
 #pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        wv[j][k] = u32x4_t{0, 0, 0, 0};
-        if constexpr (BF) {
-          const int e = e0 + k * KS + q * 8;
-          if (c < a.d && e < a.Ep) wv[j][k] = *(const u32x4_t*)(a.wt + (int64_t)c * a.Ep + e);
-        } else {
+      for (int k = 0; k < NK; ++k) wv[j][MULTI ? 0 : k] = *(const u32x4_t*)(wp + (j * NK + k) * 64 * PER);
+  }
+  const int64_t tb = (int64_t)run * a.dx_tokens, te = tb + a.dx_tokens < a.T ? tb + a.dx_tokens : a.T;
+  DlTile<T, LT, kDxTok, kDxWaves * 64, ST> dl;
+  auto fetch = [&](int64_t t, int eb) {
+    dl.load((const LT*)a.dlogits + t * a.E, a.E, eb * kDxE, (int)(te - t < kDxTok ? te - t : kDxTok), vec);
+  };
+  uint2 old[2][4];
+  f32x4_t acc[HG][DT];
+  auto clear = [&]() {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = e0 + k * KS + q * 4 + i;
-            if (c < a.d && e < a.E) wv[j][k][i] = __float_as_uint(((const float*)a.w)[(int64_t)e * a.d + c]);
+    for (int h = 0; h < HG; ++h)
+#pragma unroll
+      for (int j = 0; j < DT; ++j) acc[h][j] = f32x4_t{0, 0, 0, 0};
+  };
+  // acc[g] += step k of expert block eb for tokens 16 h ..
+  auto step = [&](const char* hs, const char* ls, int g, int h, int k) {
+    const int at = (h * 16 + col) * ST + (k * 4 + q) * 16;
+    const u32x4_t hv = *(const u32x4_t*)(hs + at);
+#pragma unroll
+    for (int j = 0; j < DT; ++j) acc[g][j] = mma16<T>(hv, wv[j][MULTI ? 0 : k], acc[g][j]);
+    if constexpr (LO) {
+      const u32x4_t lv = *(const u32x4_t*)(ls + at);
+#pragma unroll
+      for (int j = 0; j < DT; ++j) acc[g][j] = mma16<T>(lv, wv[j][MULTI ? 0 : k], acc[g][j]);
+    }
+  };
+  // result row 4 q + m is a token, and tile j column c + j of it
+  auto write = [&](int64_t t0, int g, int h) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int64_t t = t0 + h * 16 + q * 4 + m;
+      if (t < te && in) {
+        float v[DT];
+#pragma unroll
+        for (int j = 0; j < DT; ++j) v[j] = acc[g][j][m];
+        uint2 o;
+        if constexpr (sizeof(T) == 2) {
+          if (a.dx_in) {
+            v[0] += __uint_as_float(old[h][m].x << 16);
+            v[1] += __uint_as_float(old[h][m].x & 0xffff0000u);
+            v[2] += __uint_as_float(old[h][m].y << 16);
+            v[3] += __uint_as_float(old[h][m].y & 0xffff0000u);
           }
+          o = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        } else {
+          if (a.dx_in) {
+            v[0] += __uint_as_float(old[h][m].x);
+            v[1] += __uint_as_float(old[h][m].y);
+          }
+          o = uint2{__float_as_uint(v[0]), __float_as_uint(v[1])};
         }
+        *(uint2*)((T*)a.dx + t * a.d + c) = o;
       }
     }
   };
-  const int ebs = (a.E + kDxE - 1) / kDxE;
-  if (ebs == 1) load_w(0);
-  const int64_t tb = (int64_t)run * a.dx_tokens, te = tb + a.dx_tokens < a.T ? tb + a.dx_tokens : a.T;
-  const int cl = c0 + q * 4 * DT;  // this lane's columns
-  for (int64_t t0 = tb; t0 < te; t0 += 16) {
-    const int64_t t = t0 + col;
-    const bool live = t < te;
-    // d is a multiple of 8, so 8-column groups are in or out together
-    u32x4_t in[DT * 4 * sizeof(T) / 16];
-    if (a.dx_in) {
+  fetch(tb, 0);
+  int buf = 0;
+  for (int64_t t0 = tb; t0 < te; t0 += kDxTok) {
+    if (a.dx_in && busy && in) {
 #pragma unroll
-      for (int i = 0; i < (int)(DT * 4 * sizeof(T) / 16); ++i) {
-        const int c = cl + i * (16 / (int)sizeof(T));
-        in[i] = u32x4_t{0, 0, 0, 0};
-        if (live && c < a.d) in[i] = *(const u32x4_t*)((const T*)a.dx_in + t * a.d + c);
-      }
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const int64_t t = t0 + h * 16 + q * 4 + m;
+          if (t < te) old[h][m] = *(const uint2*)((const T*)a.dx_in + t * a.d + c);
+        }
     }
-    f32x4_t acc[DT];
+    if (MULTI) clear();
+    for (int eb = 0; eb < (MULTI ? ebs : 1); ++eb, buf ^= 1) {
+      char* hs = smem + buf * 2 * kDxTok * ST;
+      char* ls = hs + kDxTok * ST;
+      dl.store(hs, ls);
+      __syncthreads();  // written; the other buffer's reads are done once every wave is here again
+      if (eb + 1 < (MULTI ? ebs : 1)) fetch(t0, eb + 1);
+      else if (t0 + kDxTok < te) fetch(t0 + kDxTok, 0);
+      if (!busy) continue;
+      if constexpr (MULTI) {
+#pragma unroll 1
+        for (int k = 0; k < NK; ++k) {
+          if (eb * kDxE + k * 4 * PER >= a.E) break;
 #pragma unroll
-    for (int j = 0; j < DT; ++j) acc[j] = f32x4_t{0, 0, 0, 0};
-    for (int eb = 0; eb < ebs; ++eb) {
-      const int e0 = eb * kDxE;
-      if (ebs > 1) load_w(e0);
+          for (int j = 0; j < DT; ++j)
+            wv[j][0] = *(const u32x4_t*)(wp + (((int64_t)eb * DT + j) * NK + k) * 64 * PER);
+          step(hs, ls, 0, 0, k);
+          step(hs, ls, 1, 1, k);
+        }
+      } else {
 #pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        if (e0 + k * KS < a.E) {
-          if constexpr (BF) {
-            float v[8];
-            dl_row<LT, 8>(v, a, live ? t : a.T, e0 + k * KS + q * 8, vec);
-            u32x4_t h, l;
+        for (int h = 0; h < 2; ++h) {
+          clear();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              bf16_t h0, l0, h1, l1;
-              split_bf16(v[2 * i], h0, l0);
-              split_bf16(v[2 * i + 1], h1, l1);
-              h[i] = (uint32_t)h0 | ((uint32_t)h1 << 16);
-              l[i] = (uint32_t)l0 | ((uint32_t)l1 << 16);
-            }
-#pragma unroll
-            for (int j = 0; j < DT; ++j) acc[j] = mma16<T>(wv[j][k], h, acc[j]);
-            if constexpr (LO) {
-#pragma unroll
-              for (int j = 0; j < DT; ++j) acc[j] = mma16<T>(wv[j][k], l, acc[j]);
-            }
-          } else {
-            float v[4];
-            dl_row<LT, 4>(v, a, live ? t : a.T, e0 + k * KS + q * 4, vec);
-            const u32x4_t b = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                               __float_as_uint(v[3])};
-#pragma unroll
-            for (int j = 0; j < DT; ++j) acc[j] = mma16<T>(wv[j][k], b, acc[j]);
-          }
+          for (int k = 0; k < NK; ++k)
+            if (k * 4 * PER < a.E) step(hs, ls, 0, h, k);
+          write(t0, 0, h);
         }
       }
     }
-    if (live) {
-#pragma unroll
-      for (int i = 0; i < (int)(DT * 4 * sizeof(T) / 16); ++i) {
-        constexpr int PER = 16 / (int)sizeof(T);
-        const int c = cl + i * PER;
-        if (c < a.d) {
-          u32x4_t o;
-          if constexpr (BF) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              float lo = acc[(i * PER + 2 * m) / 4][(2 * m) & 3], hi = acc[(i * PER + 2 * m) / 4][(2 * m + 1) & 3];
-              if (a.dx_in) {
-                lo += __uint_as_float(in[i][m] << 16);
-                hi += __uint_as_float(in[i][m] & 0xffff0000u);
-              }
-              o[m] = pack_bf16x2(lo, hi);
-            }
-          } else {
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-              o[m] = __float_as_uint(a.dx_in ? acc[i][m] + __uint_as_float(in[i][m]) : acc[i][m]);
-          }
-          *(u32x4_t*)((T*)a.dx + t * a.d + c) = o;
-        }
-      }
+    if (MULTI && busy) {
+      write(t0, 0, 0);
+      write(t0, HG - 1, 1);
     }
   }
 }
@@ -524,28 +584,36 @@ __device__ __forceinline__ void join_dw(const RouterArgs& a, int b) {
   const int64_t n = (int64_t)a.E * a.d, i = ((int64_t)b * kDxWaves * 64 + threadIdx.x) * 4;
   if (i >= n) return;  // d is a multiple of 8: whole groups of 4
   f32x4_t s = {0, 0, 0, 0};
+#pragma unroll 4
   for (int r = 0; r < a.runs; ++r) {
     const f32x4_t v = *(const f32x4_t*)(a.parts + r * n + i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) s[j] += v[j];
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) ((T*)a.dw)[i + j] = from_f32<T>(s[j]);
+  if constexpr (sizeof(T) == 4) *(f32x4_t*)((float*)a.dw + i) = s;
+  else *(uint2*)((bf16_t*)a.dw + i) = uint2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
 }
 
-template <typename T, typename LT>
-__global__ __launch_bounds__(kDxWaves * 64) void router_dx_kernel(RouterArgs a) {
+template <typename T, typename LT, bool MULTI>
+__global__ __launch_bounds__(kDxWaves * 64, 2) void router_dx_kernel(RouterArgs a) {
+  __shared__ __align__(16) char smem[4 * kDxTok * dx_stride<T>];
   const int b = blockIdx.x;
-  if (b < a.dx_groups) dx_part<T, LT>(a, b % a.dx_blocks, b / a.dx_blocks);
+  if (b < a.dx_groups) dx_part<T, LT, MULTI>(a, smem, b % a.dx_blocks, b / a.dx_blocks);
   else join_dw<T>(a, b - a.dx_groups);
 }
 
 template <typename T, typename LT>
 hipError_t bwd(const LaunchCtx& c, const RouterArgs& a) {
-  const unsigned tr = sizeof(T) == 2 ? (unsigned)cdiv(a.d, 64) : 0;
-  MOE_LAUNCH(c, "router_dw", (router_dw_kernel<T, LT>), dim3((unsigned)a.dw_groups + tr), dim3(512), 0, a);
-  MOE_LAUNCH(c, "router_dx", (router_dx_kernel<T, LT>),
-             dim3((unsigned)(a.dx_groups + cdiv((int64_t)a.E * a.d, kDxWaves * 256))), dim3(kDxWaves * 64), 0, a);
+  constexpr size_t smem = 2 * dw_stage<T, LT>();
+  static_assert(smem >= 4 * 4096 * sizeof(float), "the halves' parts fit");
+  HIP_RET(tile::allow_smem_once<router_dw_kernel<T, LT>>(smem));
+  const int64_t lay = cdiv(a.d, 16 * dx_tiles<T>) * a.dx_eblocks;
+  MOE_LAUNCH(c, "router_dw", (router_dw_kernel<T, LT>), dim3((unsigned)(a.dw_groups + lay)), dim3(512), smem, a);
+  const dim3 grid((unsigned)(a.dx_groups + cdiv((int64_t)a.E * a.d, kDxWaves * 256)));
+  if (a.dx_eblocks > 1)
+    MOE_LAUNCH(c, "router_dx", (router_dx_kernel<T, LT, true>), grid, dim3(kDxWaves * 64), 0, a);
+  else
+    MOE_LAUNCH(c, "router_dx", (router_dx_kernel<T, LT, false>), grid, dim3(kDxWaves * 64), 0, a);
   return hipSuccess;
 }
 
@@ -554,14 +622,14 @@ hipError_t bwd(const LaunchCtx& c, const RouterArgs& a) {
 RouterPlan router_plan(int64_t T, int64_t d, int64_t E, int dtype) {
   RouterPlan p;
   const int step = dtype == F32 ? DwTile<float>::TS : DwTile<bf16_t>::TS;
-  // two work-groups per CU, in whole steps, at least four of them a run (the
-  // parts cost E d floats of traffic each way)
+  // a work-group per CU, in whole steps (a part costs E d floats of traffic
+  // each way, so no more of them than that)
   const int64_t tiles = cdiv(d, kDwD) * cdiv(E, kDwE);
-  const int64_t want = cdiv(512, tiles) < 1 ? 1 : cdiv(512, tiles);
-  int64_t steps = cdiv(cdiv(T, step), want);
-  if (steps < 4) steps = 4;
-  p.run_tokens = steps * step;
+  const int64_t want = 256 / tiles < 1 ? 1 : 256 / tiles;
+  p.run_tokens = cdiv(cdiv(T, step), want) * step;
   p.runs = cdiv(T, p.run_tokens);
+  const int64_t cols = 16 * (dtype == F32 ? dx_tiles<float> : dx_tiles<bf16_t>);
+  p.wf_bytes = cdiv(d, cols) * cols * cdiv(E, kDxE) * kDxE * (dtype == F32 ? 4 : 2);
   return p;
 }
 
@@ -573,10 +641,10 @@ hipError_t launch_router_bwd(const LaunchCtx& c, RouterArgs a) {
   a.d_blocks = (int)cdiv(a.d, kDwD);
   a.e_blocks = (int)cdiv(a.E, kDwE);
   a.dw_groups = a.d_blocks * a.e_blocks * a.runs;
-  a.dx_blocks = (int)cdiv(a.d, 16 * (a.dtype == F32 ? 2 : 4) * kDxWaves);
-  // four work-groups per CU, at least two token blocks each
-  int64_t tok = cdiv(cdiv((int64_t)a.T * a.dx_blocks, 1024), 16) * 16;
-  if (tok < 32) tok = 32;
+  a.dx_eblocks = (int)cdiv(a.E, kDxE);
+  a.dx_blocks = (int)cdiv(a.d, 16 * (a.dtype == F32 ? dx_tiles<float> : dx_tiles<bf16_t>) * kDxWaves);
+  // two work-groups per CU (each first loads its part of w), in whole blocks
+  const int64_t tok = cdiv(cdiv((int64_t)a.T * a.dx_blocks, 512), kDxTok) * kDxTok;
   a.dx_tokens = (int)tok;
   a.dx_groups = a.dx_blocks * (int)cdiv(a.T, tok);
   if (a.dtype == F32) return a.logits_dtype == F32 ? bwd<float, float>(c, a) : bwd<float, bf16_t>(c, a);
