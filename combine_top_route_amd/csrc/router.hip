@@ -14,6 +14,8 @@
 //
 // No product uses atomics: K or T is split over waves or work-groups and the
 // parts are added in a fixed order.
+#include <type_traits>
+
 #include "common.h"
 #include "rowload.h"
 #include "tile.h"
@@ -180,18 +182,18 @@ hipError_t fwd_any(const LaunchCtx& c, const RouterArgs& a, void* logits) {
 // ------------------------------------------------- backward, first launch
 // dw parts: work-group (E block of 128, d block of 128, run of tokens).  Steps
 // of TS tokens pass through two LDS buffers as they lie in memory,
-// [token][column], the next step's loads in flight; a transposing LDS read
-// (16-bit) or plain 4-byte reads (the K = 4 float32 MFMA) hand the MFMA its
-// token-contiguous operands.  Each half of the waves takes half of a step's
-// tokens and the whole 128 x 128 tile in quarters of 64 x 64 (the least LDS
-// traffic per product: it is what bounds the kernel beside the loads); the
-// halves meet in LDS.  Parts are float32 [run][E][d].
-// The remaining work-groups lay w out as the second launch's MFMA operands.
+// [token][column], two more steps' loads in flight in registers; a transposing
+// LDS read (16-bit) or plain 4-byte reads (the K = 4 float32 MFMA) hand the
+// MFMA its token-contiguous operands.  Two work-groups share a CU, so that one's
+// staging and barriers run beside the other's products: 31 us at the size
+// above; one work-group with 64-token steps took 35.  Parts are float32
+// [run][E][d].
+// The first work-groups lay w out as the second launch's MFMA operands.
 constexpr int kDwE = 128, kDwD = 128;
 
 template <typename T> struct DwTile;
 template <> struct DwTile<bf16_t> {
-  static constexpr int TS = 64, STRIDE = 288;  // bytes a row: 256 + 32 (row r starts at bank 8 r)
+  static constexpr int TS = 32, STRIDE = 288;  // bytes a row: 256 + 32 (row r starts at bank 8 r)
 };
 template <> struct DwTile<float> {
   static constexpr int TS = 32, STRIDE = 576;  // 512 + 64 (16 r)
@@ -297,9 +299,11 @@ __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb,
   const T* xp = (const T*)a.x + tb * a.d;
   const LT* lp = (const LT*)a.dlogits + tb * a.E;
   const bool vec = dl_vec<T, LT>(a);
-  u32x4_t xv[XV];
-  DlTile<T, LT, TS, 512, ST> dl;
-  auto fetch = [&](int s) {  // tokens s .. s + TS of the run; zeros past its end and past E and d
+  u32x4_t xr[2][XV];
+  DlTile<T, LT, TS, 512, ST> dlr[2];
+  auto fetch = [&](auto set, int s) {  // tokens s .. s + TS of the run; zeros past its end and past E and d
+    auto& xv = xr[set.value];
+    auto& dl = dlr[set.value];
 #pragma unroll
     for (int i = 0; i < XV; ++i) {
       const int u = (int)threadIdx.x + i * 512, r = u / XU, cb = (u % XU) * 16;
@@ -309,7 +313,9 @@ __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb,
     }
     dl.load(lp + (int64_t)s * a.E, a.E, e0, tn - s, vec);
   };
-  auto stage = [&](char* b) {
+  auto stage = [&](auto set, char* b) {
+    const auto& xv = xr[set.value];
+    const auto& dl = dlr[set.value];
 #pragma unroll
     for (int i = 0; i < XV; ++i) {
       const int u = (int)threadIdx.x + i * 512, r = u / XU, cb = (u % XU) * 16;
@@ -317,92 +323,87 @@ __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb,
     }
     dl.store(b + TS * ST, b + 2 * TS * ST);
   };
-  const int kh = (wave >> 2) * (TS / 2), we = ((wave >> 1) & 1) * 64, wd = (wave & 1) * 64;
+  const int we = (wave >> 2) * 64, wd = (wave & 3) * 32;
   const bool busy = e0 + we < a.E && d0 + wd < a.d;  // uniform: this quarter exists
-  f32x4_t acc[4][4];
+  f32x4_t acc[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
-  fetch(0);
-  stage(smem);
-  if (TS < tn) fetch(TS);
-  for (int s = 0, buf = 0; s < tn; s += TS, buf ^= 1) {
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4_t{0, 0, 0, 0};
+  std::integral_constant<int, 0> set0;
+  std::integral_constant<int, 1> set1;
+  fetch(set0, 0);
+  if (TS < tn) fetch(set1, TS);
+  stage(set0, smem);
+  if (2 * TS < tn) fetch(set0, 2 * TS);
+  auto step = [&](auto set, auto next, int s) {  // the step at token s, in buffer and registers `set`
     __syncthreads();  // this step's buffer is written, the other one's reads are done
-    const char* xs = smem + buf * dw_stage<T, LT>();
+    const char* xs = smem + set.value * dw_stage<T, LT>();
     const char* hs = xs + TS * ST;
     const char* ls = hs + TS * ST;
     if (busy) {
       if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int k = 0; k < TS / 2; k += 4) {
-          float av[4], bv[4];
+        for (int k = 0; k < TS; k += 4) {
+          float av[4], bv[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) av[i] = *(const float*)(hs + (kh + k + q) * ST + (we + i * 16 + col) * 4);
+          for (int i = 0; i < 4; ++i) av[i] = *(const float*)(hs + (k + q) * ST + (we + i * 16 + col) * 4);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) bv[j] = *(const float*)(xs + (kh + k + q) * ST + (wd + j * 16 + col) * 4);
+          for (int j = 0; j < 2; ++j) bv[j] = *(const float*)(xs + (k + q) * ST + (wd + j * 16 + col) * 4);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 2; ++j)
               acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[i], bv[j], acc[i][j], 0, 0, 0);
         }
       } else {
         // eight tokens 8 q .. of column `col`: the 16 lanes of a group read 4
         // tokens by 16 columns and get them transposed
         auto frag = [&](const char* base, int c0) {
-          const char* p = base + (kh + q * 8 + (col >> 2)) * ST + (c0 + 4 * (col & 3)) * 2;
+          const char* p = base + (q * 8 + (col >> 2)) * ST + (c0 + 4 * (col & 3)) * 2;
           const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
           const s16x4_t hi =
               __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(p + 4 * ST));
           return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         };
-        static_assert(TS == 64, "a half step is one MFMA's K");
-        bf16x8_t bv[4];
+        static_assert(TS == 32, "a step is one MFMA's K");
+        bf16x8_t bv[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) bv[j] = frag(xs, wd + j * 16);
+        for (int j = 0; j < 2; ++j) bv[j] = frag(xs, wd + j * 16);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bf16x8_t h = frag(hs, we + i * 16);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h, bv[j], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h, bv[j], acc[i][j], 0, 0, 0);
           if constexpr (LO) {
             const bf16x8_t l = frag(ls, we + i * 16);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 2; ++j)
               acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(l, bv[j], acc[i][j], 0, 0, 0);
           }
         }
       }
     }
     if (s + TS < tn) {
-      stage(smem + (buf ^ 1) * dw_stage<T, LT>());
-      if (s + 2 * TS < tn) fetch(s + 2 * TS);  // a step to land in
+      stage(next, smem + next.value * dw_stage<T, LT>());
+      if (s + 3 * TS < tn) fetch(next, s + 3 * TS);
     }
+  };
+  for (int s = 0; s < tn; s += 2 * TS) {
+    step(set0, set1, s);
+    if (s + TS < tn) step(set1, set0, s + TS);
   }
-  // the halves: waves 4 .. 7 leave theirs in LDS, 0 .. 3 add and write
-  __syncthreads();
-  float* half = (float*)smem + (wave & 3) * 4096;
-  if (wave >= 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) *(f32x4_t*)(half + ((i * 4 + j) * 64 + lane) * 4) = acc[i][j];
-  }
-  __syncthreads();
-  if (wave >= 4 || !busy) return;
+  if (!busy) return;
   float* part = a.parts + (int64_t)run * a.E * a.d;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const f32x4_t o = *(const f32x4_t*)(half + ((i * 4 + j) * 64 + lane) * 4);
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const int e = e0 + we + i * 16 + q * 4 + m, c = d0 + wd + j * 16 + col;
-        if (e < a.E && c < a.d) part[(int64_t)e * a.d + c] = acc[i][j][m] + o[m];
+        if (e < a.E && c < a.d) part[(int64_t)e * a.d + c] = acc[i][j][m];
       }
-    }
 }
 
 // The second launch's operand layout of w.  A wave there takes 16 DT columns
@@ -433,16 +434,16 @@ __device__ __forceinline__ void lay_out_w(const RouterArgs& a, int cb, int eb) {
 }
 
 template <typename T, typename LT>
-__global__ __launch_bounds__(512, 2) void router_dw_kernel(RouterArgs a) {
+__global__ __launch_bounds__(512, 4) void router_dw_kernel(RouterArgs a) {
   extern __shared__ __align__(16) char smem[];
-  int b = blockIdx.x;
-  if (b < a.dw_groups) {
+  int b = (int)blockIdx.x - a.lay_groups;
+  if (b < 0) {  // first, or they would wait for a place beside the others
+    b += a.lay_groups;
+    lay_out_w<T>(a, b / a.dx_eblocks, b % a.dx_eblocks);
+  } else {
     const int db = b % a.d_blocks;
     b /= a.d_blocks;
     dw_part<T, LT>(a, smem, b % a.e_blocks, db, b / a.e_blocks);
-  } else {
-    b -= a.dw_groups;
-    lay_out_w<T>(a, b / a.dx_eblocks, b % a.dx_eblocks);
   }
 }
 
@@ -605,10 +606,9 @@ __global__ __launch_bounds__(kDxWaves * 64, 2) void router_dx_kernel(RouterArgs 
 template <typename T, typename LT>
 hipError_t bwd(const LaunchCtx& c, const RouterArgs& a) {
   constexpr size_t smem = 2 * dw_stage<T, LT>();
-  static_assert(smem >= 4 * 4096 * sizeof(float), "the halves' parts fit");
   HIP_RET(tile::allow_smem_once<router_dw_kernel<T, LT>>(smem));
-  const int64_t lay = cdiv(a.d, 16 * dx_tiles<T>) * a.dx_eblocks;
-  MOE_LAUNCH(c, "router_dw", (router_dw_kernel<T, LT>), dim3((unsigned)(a.dw_groups + lay)), dim3(512), smem, a);
+  MOE_LAUNCH(c, "router_dw", (router_dw_kernel<T, LT>), dim3((unsigned)(a.dw_groups + a.lay_groups)), dim3(512), smem,
+             a);
   const dim3 grid((unsigned)(a.dx_groups + cdiv((int64_t)a.E * a.d, kDxWaves * 256)));
   if (a.dx_eblocks > 1)
     MOE_LAUNCH(c, "router_dx", (router_dx_kernel<T, LT, true>), grid, dim3(kDxWaves * 64), 0, a);
@@ -622,10 +622,10 @@ hipError_t bwd(const LaunchCtx& c, const RouterArgs& a) {
 RouterPlan router_plan(int64_t T, int64_t d, int64_t E, int dtype) {
   RouterPlan p;
   const int step = dtype == F32 ? DwTile<float>::TS : DwTile<bf16_t>::TS;
-  // a work-group per CU, in whole steps (a part costs E d floats of traffic
-  // each way, so no more of them than that)
+  // two work-groups per CU, in whole steps; more runs cost more (E d floats of
+  // traffic each way) than they hide
   const int64_t tiles = cdiv(d, kDwD) * cdiv(E, kDwE);
-  const int64_t want = 256 / tiles < 1 ? 1 : 256 / tiles;
+  const int64_t want = 512 / tiles < 1 ? 1 : 512 / tiles;
   p.run_tokens = cdiv(cdiv(T, step), want) * step;
   p.runs = cdiv(T, p.run_tokens);
   const int64_t cols = 16 * (dtype == F32 ? dx_tiles<float> : dx_tiles<bf16_t>);
@@ -642,6 +642,7 @@ hipError_t launch_router_bwd(const LaunchCtx& c, RouterArgs a) {
   a.e_blocks = (int)cdiv(a.E, kDwE);
   a.dw_groups = a.d_blocks * a.e_blocks * a.runs;
   a.dx_eblocks = (int)cdiv(a.E, kDxE);
+  a.lay_groups = (int)cdiv(a.d, 16 * (a.dtype == F32 ? dx_tiles<float> : dx_tiles<bf16_t>)) * a.dx_eblocks;
   a.dx_blocks = (int)cdiv(a.d, 16 * (a.dtype == F32 ? dx_tiles<float> : dx_tiles<bf16_t>) * kDxWaves);
   // two work-groups per CU (each first loads its part of w), in whole blocks
   const int64_t tok = cdiv(cdiv((int64_t)a.T * a.dx_blocks, 512), kDxTok) * kDxTok;
