@@ -269,10 +269,12 @@ __device__ __forceinline__ void unit_mma(f32x4_t& acc, const typename Fmt<F>::fr
   }
 }
 
-// Blockwise scale of row n and unit `unit` of one matrix [N, K] of an expert.
+// Blockwise scale of row n and unit `unit` (past K: any) of one matrix [N, K]
+// of an expert.  Loaded with the weights it belongs to: a load of its own at
+// the time of use waits for memory again.
 template <int F>
 __device__ __forceinline__ float block_scale_of(const void* s, int n, int K, int unit) {
-  if constexpr (F == WF_FP8) return ((const float*)s)[(int64_t)(n >> 7) * (K >> 7) + unit];
+  if constexpr (F == WF_FP8) return ((const float*)s)[(int64_t)(n >> 7) * (K >> 7) + min(unit, (K >> 7) - 1)];
   return 1.0f;
 }
 
@@ -330,7 +332,7 @@ __device__ __forceinline__ int find_rows(Rows& rows, const int32_t* __restrict__
 // Token blocks of 16 that one pass over an expert's weights serves (the rest
 // take another pass, from the caches): as many as the registers hold beside
 // the weights in flight.
-template <int F> constexpr int kMaxBlocks = F >= WF_FP8 ? 2 : 4;
+template <int F> constexpr int kMaxBlocks = 2;
 
 // ------------------------------------------------------------ gate/up product
 // One work-group: 16 gate rows and the same 16 up rows of one expert, for all
@@ -339,6 +341,7 @@ template <int F, int UN>
 struct GuWeights {  // UN units of the tile's gate and up rows, in flight
   u32x4_t g[UN][2], u[UN][2];
   uint32_t mg, mu;
+  float sg[UN], su[UN];  // blockwise scales
 };
 
 struct GuTile {  // where a lane finds them
@@ -356,6 +359,8 @@ __device__ __forceinline__ void load_gu(GuWeights<F, UN>& w, const GuTile& t, in
   for (int i = 0; i < UN; ++i) {
     load_rows(w.g[i], t.w, t.g, (base + i) * 128, bytes);
     load_rows(w.u[i], t.w, t.u, (base + i) * 128, bytes);
+    w.sg[i] = block_scale_of<F>(t.sc, t.n0, K, base + i);
+    w.su[i] = block_scale_of<F>(t.sc, I + t.n0, K, base + i);
   }
   w.mg = mx_words<F>(t.sc, t.row4, K, base + (int)(threadIdx.x & 3));
   w.mu = mx_words<F>(t.sc, I + t.row4, K, base + (int)(threadIdx.x & 3));
@@ -405,10 +410,8 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
       __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
 #pragma unroll
       for (int i = 0; i < UB; ++i) {
-        const int unit = base + i0 + i, us = min(unit, units - 1);
         put_rows(lw, w.g[i0 + i]);
         put_rows(lw + 2048, w.u[i0 + i]);
-        const float sg = block_scale_of<F>(t.sc, t.n0, K, us), su = block_scale_of<F>(t.sc, a.I + t.n0, K, us);
         uint32_t mg = 0, mu = 0;
         if constexpr (F == WF_MX) {
           mg = (uint32_t)__shfl((int)w.mg, col * 4 + i0 + i, kWave);
@@ -422,8 +425,8 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
           u32x4_t xf[Fmt<F>::BV];
           put_acts<F>(lw + 4096, xv[i][b], eight);
           get_acts<F>(xf, lw + 4096, q, col);
-          unit_mma<F>(ag[b], fg, xf, sg);
-          unit_mma<F>(au[b], fu, xf, su);
+          unit_mma<F>(ag[b], fg, xf, w.sg[i0 + i]);
+          unit_mma<F>(au[b], fu, xf, w.su[i0 + i]);
         }
       }
     }
@@ -646,8 +649,12 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
   constexpr int UB = NB == 1 ? UN : 1;
   for (int base = 0; base < units; base += UN) {
     u32x4_t wv[UN][2];
+    float sb[UN];
 #pragma unroll
-    for (int i = 0; i < UN; ++i) load_rows(wv[i], t.w, t.row, (base + i) * 128, abytes);
+    for (int i = 0; i < UN; ++i) {
+      load_rows(wv[i], t.w, t.row, (base + i) * 128, abytes);
+      sb[i] = block_scale_of<F>(t.sc, t.n0, K, base + i);
+    }
     const uint32_t mx = mx_words<F>(t.sc, t.row4, K, base + (lane & 3));
 #pragma unroll
     for (int i0 = 0; i0 < UN; i0 += UB) {
@@ -664,13 +671,12 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
         uint32_t m = 0;
         if constexpr (F == WF_MX) m = (uint32_t)__shfl((int)mx, col * 4 + i0 + i, kWave);
         to_frags<F>(fr, lw, m, q, col);
-        const float sb = block_scale_of<F>(t.sc, t.n0, K, min(base + i0 + i, units - 1));
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           u32x4_t xf[Fmt<F>::BV];
           put_acts<F>(lw + 2048, xv[i][b], eight);
           get_acts<F>(xf, lw + 2048, q, col);
-          unit_mma<F>(acc[b], fr, xf, sb);
+          unit_mma<F>(acc[b], fr, xf, sb[i0 + i]);
         }
       }
     }
