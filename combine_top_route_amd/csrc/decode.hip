@@ -78,7 +78,15 @@ __global__ __launch_bounds__(64) void decode_topk_kernel(const LT* __restrict__ 
       key[i] = v != v ? 0xffffffffu : order_key(v);
     }
   }
-  float top = 0.0f, sum = 0.0f;
+  float top = 0.0f, sum = 0.0f, my_ex = 0.0f;
+  int my_id = -1;  // lane j % 64 holds slot j until the next 64 (or the end) push it out
+  auto push = [&](int j) {  // unnormalised
+    if (lane <= (j & 63)) {
+      const int64_t f = (int64_t)t * k + (j & ~63) + lane;
+      ids[f] = mid[f] = my_id;
+      w[f] = my_ex;
+    }
+  };
   for (int j = 0; j < k; ++j) {
     uint32_t m = 0;
 #pragma unroll
@@ -102,12 +110,18 @@ __global__ __launch_bounds__(64) void decode_topk_kernel(const LT* __restrict__ 
     const float ex = none ? 0.0f : expf(l - top);
     sum += ex;
     if (lane == (j & 63)) {
-      const int64_t f = (int64_t)t * k + j;
-      ids[f] = mid[f] = none ? -1 : e;
-      w[f] = ex;
+      my_id = none ? -1 : e;
+      my_ex = ex;
     }
+    if ((j & 63) == 63 && j + 1 < k) push(j);
   }
-  for (int j = lane; j < k; j += kWave) {  // each lane reads back its own stores
+  const int j0 = (k - 1) & ~63;  // the last 64 are still in the lanes
+  if (lane < k - j0) {
+    const int64_t f = (int64_t)t * k + j0 + lane;
+    ids[f] = mid[f] = my_id;
+    w[f] = mw[f] = my_id < 0 ? 0.0f : my_ex / sum;
+  }
+  for (int j = lane; j < j0; j += kWave) {  // each lane reads back its own stores
     const int64_t f = (int64_t)t * k + j;
     const float v = ids[f] < 0 ? 0.0f : w[f] / sum;
     w[f] = mw[f] = v;
@@ -302,32 +316,44 @@ struct Rows {  // an expert's tokens in token order
   int part[4];
 };
 
-// Fills `rows` with the slots that chose expert e; returns their number.  At
-// least 256 threads.
-__device__ __forceinline__ int find_rows(Rows& rows, const int32_t* __restrict__ mid, const float* __restrict__ mw,
-                                         int e, int T, int k) {
-  const int t = threadIdx.x, wave = t >> 6;
-  int slot = -1;
-  if (t < T)
-    for (int j = 0; j < k; ++j)
-      if (mid[t * k + j] == e) slot = t * k + j;  // at most one (see decode_ids_kernel)
-  const uint64_t has = __ballot(slot >= 0);
-  if (wave < 4 && (t & 63) == 0) rows.part[wave] = __popcll(has);
-  __syncthreads();
-  int before = 0, n = 0;
+// Finds the slots that chose expert e, a thread per token (at least
+// kDecodeMaxT threads): count() returns their number, list() then fills rows
+// in token order.  What a caller loads in between is in flight meanwhile (a
+// barrier does not wait for loads).
+struct Finder {
+  int slot;
+  float w;
+  uint64_t has;
+  __device__ __forceinline__ int count(Rows& rows, const int32_t* __restrict__ mid, const float* __restrict__ mw, int e,
+                                       int T, int k) {
+    const int t = threadIdx.x, wave = t >> 6;
+    slot = -1;
+    for (int j0 = 0; j0 < k; j0 += 8) {  // eight loads at a time
+      int v[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    before += i < wave ? rows.part[i] : 0;
-    n += rows.part[i];
+      for (int i = 0; i < 8; ++i) v[i] = mid[min(t * k + j0 + i, T * k - 1)];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (t < T && j0 + i < k && v[i] == e) slot = t * k + j0 + i;  // at most one (see decode_ids_kernel)
+    }
+    w = slot >= 0 ? mw[slot] : 0.0f;
+    has = __ballot(slot >= 0);
+    if (wave < 4 && (t & 63) == 0) rows.part[wave] = __popcll(has);
+    __syncthreads();
+    return rows.part[0] + rows.part[1] + rows.part[2] + rows.part[3];
   }
-  if (slot >= 0) {
-    const int r = before + __popcll(has & ((1ull << (t & 63)) - 1));
-    rows.slot[r] = slot;
-    rows.w[r] = mw[slot];
+  __device__ __forceinline__ void list(Rows& rows) const {
+    const int t = threadIdx.x, wave = t >> 6;
+    int r = __popcll(has & ((1ull << (t & 63)) - 1));
+#pragma unroll
+    for (int i = 0; i < 3; ++i) r += i < wave ? rows.part[i] : 0;
+    if (slot >= 0) {
+      rows.slot[r] = slot;
+      rows.w[r] = w;
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  return n;
-}
+};
 
 // Token blocks of 16 that one pass over an expert's weights serves (the rest
 // take another pass, from the caches): as many as the registers hold beside
@@ -461,13 +487,14 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
 template <int F, int NBMAX, int NW, int UN>
 __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   static_assert(UN <= 4, "mx_words holds four units");
-  static_assert(NW * 64 >= kDecodeMaxT, "find_rows takes a thread per token");
+  static_assert(NW * 64 >= kDecodeMaxT, "Finder takes a thread per token");
   __shared__ Rows rows;
   __shared__ __align__(16) char smem[gu_smem<F, NW, NBMAX>()];
   const int e = __builtin_amdgcn_readfirstlane(item_expert(a.mid, blockIdx.y, a.T * a.k, a.E));
   if (e < 0) return;
   const int lane = threadIdx.x & 63;
-  const int n = find_rows(rows, a.mid, a.mw, e, a.T, a.k);
+  Finder find;
+  const int n = find.count(rows, a.mid, a.mw, e, a.T, a.k);
   if (n == 0) return;
   GuTile t;
   t.n0 = blockIdx.x * 16;
@@ -487,6 +514,7 @@ __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   t.sc = sc;
   GuWeights<F, UN> w;
   load_gu<F, UN>(w, t, a.I, a.d, tile::wave_id() * UN);
+  find.list(rows);
   if constexpr (NBMAX == 1) {
     gateup_rows<F, NW, UN, 1>(a, rows, 0, n, w, t, smem);
   } else {
@@ -691,12 +719,14 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
 
 template <int F>
 __global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(DecodeArgs a) {
-  static_assert(kDownRowWaves * 64 >= kDecodeMaxT, "find_rows takes a thread per token");
+  static_assert(kDownRowWaves * 64 >= kDecodeMaxT, "Finder takes a thread per token");
   __shared__ Rows rows;
   __shared__ __align__(16) char work[kDownRowWaves * (2048 + 2048 * kActHalves<F>)];
   const int e = __builtin_amdgcn_readfirstlane(item_expert(a.mid, blockIdx.y, a.T * a.k, a.E));
   if (e < 0) return;
-  const int n = find_rows(rows, a.mid, a.mw, e, a.T, a.k);
+  Finder find;
+  const int n = find.count(rows, a.mid, a.mw, e, a.T, a.k);
+  find.list(rows);
   DownTile t;
   const int lane = threadIdx.x & 63, wave = tile::wave_id();
   t.n0 = (blockIdx.x * kDownRowWaves + wave) * 16;
@@ -727,17 +757,25 @@ __global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a) {
   const int c = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
   if (c * 4 >= a.d) return;
   f32x4_t acc = {0, 0, 0, 0};
-  for (int j = 0; j < a.k; ++j) {
-    const int64_t f = (int64_t)t * a.k + j;
-    if (a.mid[f] >= 0) {
-      const f32x4_t v = *(const f32x4_t*)(a.y + f * a.d + c * 4);
+  const int64_t f0 = (int64_t)t * a.k;
+  for (int j0 = 0; j0 < a.k; j0 += 8) {  // eight loads at a time
+    bool live[8];
+    f32x4_t v[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] += v[i];
+    for (int i = 0; i < 8; ++i) live[i] = j0 + i < a.k && a.mid[f0 + min(j0 + i, a.k - 1)] >= 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = f32x4_t{0, 0, 0, 0};
+      if (live[i]) v[i] = *(const f32x4_t*)(a.y + (f0 + j0 + i) * a.d + c * 4);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) acc[m] += v[i][m];
   }
   AT* o = (AT*)a.out + (int64_t)t * a.d + c * 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = from_f32<AT>(acc[i]);
+  if constexpr (sizeof(AT) == 4) *(f32x4_t*)o = acc;
+  else *(uint2*)o = uint2{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
 }
 
 template <int F>
@@ -747,7 +785,14 @@ hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
   const dim3 gu((unsigned)cdiv(a.I, 16), items);
   constexpr int UN = F >= WF_FP8 ? 2 : 4;
   if (a.T <= 16) {
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 8, UN>), gu, dim3(8 * 64), 0, a);
+    // Few work-groups: eight waves each, so that all bytes are in flight at
+    // once (T = 1 above: 24.7 us with eight, 26.3 with four).  Many: four, of
+    // which more fit beside each other (16 tokens of 8 of 64 experts, d = 4096,
+    // I = 1024, e4m3: 139 us with four, 150 with eight).
+    if ((int64_t)gu.x * gu.y < 1024)
+      MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 8, UN>), gu, dim3(8 * 64), 0, a);
+    else
+      MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 4, UN>), gu, dim3(4 * 64), 0, a);
     const size_t smem = down_work<F>() + (size_t)a.E * 4 + (size_t)a.E * a.T * 2;
     HIP_RET(tile::allow_smem_once<decode_down_kernel<F>>(down_work<F>() + kMaxExperts * (4 + 16 * 2)));
     MOE_LAUNCH(c, "decode_down", decode_down_kernel<F>, dim3((unsigned)cdiv(a.d, 16)), dim3(kDownWaves * 64), smem, a);
