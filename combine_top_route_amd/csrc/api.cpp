@@ -910,14 +910,18 @@ moe_status moe_decode(const moe_shape* shape, int weights, const void* x, moe_ro
   a.w_down = w_down;
   a.s_down = s_down;
   a.out = out;
+  a.logits = routing->logits;
+  a.ids = routing->topk_ids;
+  a.w = routing->topk_w;
+  a.logits_f32 = shape->logits_dtype == MOE_F32;
+  a.route_inline = false;
   a.mid = (int32_t*)at(workspace, L.mid);
   a.mw = (float*)at(workspace, L.mw);
   a.aw = at(workspace, L.aw);
   a.y = shape->T > 16 ? (float*)at(workspace, L.y) : nullptr;
   const LaunchCtx c = make_ctx(stream);
   (void)hipGetLastError();
-  HIP_TRY(launch_decode(c, a, routing->logits, shape->logits_dtype, routing->topk_ids, routing->topk_w, weights),
-          "decode");
+  HIP_TRY(launch_decode(c, a, weights), "decode");
   return MOE_OK;
 }
 

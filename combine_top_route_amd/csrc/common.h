@@ -258,14 +258,18 @@ struct DecodeArgs {
   const void* w_down;     // [E, d, I]
   const void* s_down;     // fp32 [E, d/128, I/128] or E8M0 [E, d, I/32]
   void* out;              // [T, d]
+  const void* logits;     // [T, E], or null: ids and w are inputs
+  int32_t* ids;           // [T, k]
+  float* w;               // [T, k]
+  bool logits_f32;
+  bool route_inline;      // set by the launcher: the gate/up kernel routes
   int32_t* mid;           // [T, k] workspace: expert of the slot, -1 for an empty or merged slot
   float* mw;              // [T, k] workspace: its weight
   void* aw;               // [T k, I] workspace: weighted SwiGLU output per live slot
   float* y;               // [T k, d] workspace, T > 16: down products per live slot
 };
-// weights: moe_weight_format.  logits == null: ids and w are inputs.
-hipError_t launch_decode(const LaunchCtx& c, const DecodeArgs& a, const void* logits, int logits_dtype,
-                         int32_t* ids, float* w, int weights);
+// weights: moe_weight_format.
+hipError_t launch_decode(const LaunchCtx& c, DecodeArgs a, int weights);
 
 // ---------------------------------------------------------------- fp8 path
 // Block quantisation to e4m3 (quant_fp8.hip).  Two formats: blockwise (fp32

@@ -56,74 +56,91 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// Top k of one token's logits, one wave per token: k rounds of a wave-wide
-// maximum; among equal logits the lowest index (lane e % 64 holds experts e,
-// e + 64, ..., so the first of its registers and then the lowest lane).  The
-// weights are the softmax over the selected logits, summed in slot order.  A
-// slot whose logit is -inf (a masked expert) is empty: id -1, weight 0.  NaN
-// counts as the largest value.  KPL: keys per lane, E <= 64 KPL.
+// Top k of one token's logits, by one wave: k rounds of a wave-wide maximum;
+// among equal logits the lowest index (lane e % 64 holds experts e, e + 64, ...,
+// so the first of its registers and then the lowest lane).  The weights are the
+// softmax over the selected logits, summed in slot order.  A slot whose logit
+// is -inf (a masked expert) is empty: id -1, weight 0.  NaN counts as the
+// largest value.  KPL: keys per lane, E <= 64 KPL.
+template <int KPL>
+struct TopK {
+  uint32_t key[KPL];  // 0: taken, or past E
+  int id = -1;        // of slot j in lane j % 64
+  float ex = 0.0f;    // its unnormalised weight
+  float sum = 0.0f;
+  template <typename LT>
+  __device__ __forceinline__ void load(const LT* __restrict__ row, int E) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < KPL; ++i) {
+      const int e = lane + kWave * i;
+      key[i] = 0;
+      if (e < E) {
+        const float v = to_f32<LT>(row[e]);
+        key[i] = v != v ? 0xffffffffu : order_key(v);
+      }
+    }
+  }
+  // slots 0 .. k - 1; full(j) is called when slots j - 63 .. j are in the lanes
+  // and more follow
+  template <class Full>
+  __device__ __forceinline__ void select(int k, Full&& full) {
+    const int lane = threadIdx.x & 63;
+    float top = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < KPL; ++i) m = key[i] > m ? key[i] : m;
+      m = wave_max_u32(m);
+      int e = 0;
+      bool found = false;
+#pragma unroll
+      for (int i = 0; i < KPL; ++i) {
+        const uint64_t eq = __ballot(key[i] == m);
+        if (!found && eq) {
+          const int l = __builtin_ctzll(eq);
+          e = i * kWave + l;
+          if (lane == l) key[i] = 0;
+          found = true;
+        }
+      }
+      const float l = key_value(m);
+      if (j == 0) top = l;
+      const bool none = l == -__builtin_huge_valf();
+      const float x = none ? 0.0f : expf(l - top);
+      sum += x;
+      if (lane == (j & 63)) {
+        id = none ? -1 : e;
+        ex = x;
+      }
+      if ((j & 63) == 63 && j + 1 < k) full(j);
+    }
+  }
+  __device__ __forceinline__ float weight() const { return id < 0 ? 0.0f : ex / sum; }
+};
+
 template <typename LT, int KPL>
 __global__ __launch_bounds__(64) void decode_topk_kernel(const LT* __restrict__ logits, int E, int k,
                                                          int32_t* __restrict__ ids, float* __restrict__ w,
                                                          int32_t* __restrict__ mid, float* __restrict__ mw) {
-  const int lane = threadIdx.x, t = blockIdx.x;
-  const LT* row = logits + (int64_t)t * E;
-  uint32_t key[KPL];  // 0: taken, or past E
-#pragma unroll
-  for (int i = 0; i < KPL; ++i) {
-    const int e = lane + kWave * i;
-    key[i] = 0;
-    if (e < E) {
-      const float v = to_f32<LT>(row[e]);
-      key[i] = v != v ? 0xffffffffu : order_key(v);
-    }
-  }
-  float top = 0.0f, sum = 0.0f, my_ex = 0.0f;
-  int my_id = -1;  // lane j % 64 holds slot j until the next 64 (or the end) push it out
-  auto push = [&](int j) {  // unnormalised
-    if (lane <= (j & 63)) {
-      const int64_t f = (int64_t)t * k + (j & ~63) + lane;
-      ids[f] = mid[f] = my_id;
-      w[f] = my_ex;
-    }
-  };
-  for (int j = 0; j < k; ++j) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < KPL; ++i) m = key[i] > m ? key[i] : m;
-    m = wave_max_u32(m);
-    int e = 0;
-    bool found = false;
-#pragma unroll
-    for (int i = 0; i < KPL; ++i) {
-      const uint64_t eq = __ballot(key[i] == m);
-      if (!found && eq) {
-        const int l = __builtin_ctzll(eq);
-        e = i * kWave + l;
-        if (lane == l) key[i] = 0;
-        found = true;
-      }
-    }
-    const float l = key_value(m);
-    if (j == 0) top = l;
-    const bool none = l == -__builtin_huge_valf();
-    const float ex = none ? 0.0f : expf(l - top);
-    sum += ex;
-    if (lane == (j & 63)) {
-      my_id = none ? -1 : e;
-      my_ex = ex;
-    }
-    if ((j & 63) == 63 && j + 1 < k) push(j);
-  }
+  const int lane = threadIdx.x;
+  const int64_t f0 = (int64_t)blockIdx.x * k;
+  TopK<KPL> t;
+  t.load(logits + (int64_t)blockIdx.x * E, E);
+  t.select(k, [&](int j) {
+    const int64_t f = f0 + (j & ~63) + lane;
+    ids[f] = mid[f] = t.id;
+    w[f] = t.ex;
+  });
   const int j0 = (k - 1) & ~63;  // the last 64 are still in the lanes
   if (lane < k - j0) {
-    const int64_t f = (int64_t)t * k + j0 + lane;
-    ids[f] = mid[f] = my_id;
-    w[f] = mw[f] = my_id < 0 ? 0.0f : my_ex / sum;
+    const int64_t f = f0 + j0 + lane;
+    ids[f] = mid[f] = t.id;
+    w[f] = mw[f] = t.weight();
   }
   for (int j = lane; j < j0; j += kWave) {  // each lane reads back its own stores
-    const int64_t f = (int64_t)t * k + j;
-    const float v = ids[f] < 0 ? 0.0f : w[f] / sum;
+    const int64_t f = f0 + j;
+    const float v = ids[f] < 0 ? 0.0f : w[f] / t.sum;
     w[f] = mw[f] = v;
   }
 }
@@ -297,11 +314,63 @@ __device__ __forceinline__ float swiglu(float g, float u, float lim) {
   return gc * sigmoidf_(gc) * clip_up(u, lim);
 }
 
+// The same routing inside the gate/up kernel, for a token or a few: every
+// work-group does it for itself, which costs it less than another launch and
+// the way through memory (T = 1, the case above: INLINEGAIN).
+constexpr int kInlineT = 8, kInlineSlots = 256, kInlineE = 128;
+struct InlineRoute {
+  int32_t mid[kInlineSlots];
+  float mw[kInlineSlots];
+};
+__host__ __device__ inline bool inline_route_fits(int T, int k, int E) {
+  return T <= kInlineT && k <= kWave && T * k <= kInlineSlots && E <= kInlineE;
+}
+
+// 512 threads.  The first work-group leaves the results in memory.
+__device__ __forceinline__ void route_inline(InlineRoute& r, const DecodeArgs& a) {
+  const int lane = threadIdx.x & 63, t = tile::wave_id(), k = a.k;
+  const bool first_group = blockIdx.x == 0 && blockIdx.y == 0;
+  if (a.logits) {
+    if (t < a.T) {
+      TopK<2> top;
+      if (a.logits_f32) top.load((const float*)a.logits + (int64_t)t * a.E, a.E);
+      else top.load((const bf16_t*)a.logits + (int64_t)t * a.E, a.E);
+      top.select(k, [](int) {});
+      if (lane < k) {
+        const int f = t * k + lane;
+        const float w = top.weight();
+        r.mid[f] = top.id;
+        r.mw[f] = w;
+        if (first_group) {
+          a.ids[f] = a.mid[f] = top.id;
+          a.w[f] = a.mw[f] = w;
+        }
+      }
+    }
+  } else if ((int)threadIdx.x < a.T * k) {  // as decode_ids_kernel
+    const int f = threadIdx.x, j = f % k, f0 = f - j;
+    const int e = a.ids[f];
+    bool mine = e >= 0 && e < a.E;
+    for (int i = 0; i < j; ++i) mine &= a.ids[f0 + i] != e;
+    float v = mine ? a.w[f] : 0.0f;
+    if (mine)
+      for (int i = j + 1; i < k; ++i)
+        if (a.ids[f0 + i] == e) v += a.w[f0 + i];
+    r.mid[f] = mine ? e : -1;
+    r.mw[f] = v;
+    if (first_group) {
+      a.mid[f] = mine ? e : -1;
+      a.mw[f] = v;
+    }
+  }
+  __syncthreads();
+}
+
 // ------------------------------------------------------- an expert's tokens
 // Work item -> expert.  With at least as many experts as slots, item i is
 // slot i, and only the first slot of an expert works on it; otherwise item e
 // is expert e.  -1: nothing to do.  Uniform over the work-group.
-__device__ __forceinline__ int item_expert(const int32_t* __restrict__ mid, int item, int R, int E) {
+__device__ __forceinline__ int item_expert(const int32_t* mid, int item, int R, int E) {
   if (R > E) return item;
   const int e = mid[item];
   if (e < 0) return -1;
@@ -324,8 +393,7 @@ struct Finder {
   int slot;
   float w;
   uint64_t has;
-  __device__ __forceinline__ int count(Rows& rows, const int32_t* __restrict__ mid, const float* __restrict__ mw, int e,
-                                       int T, int k) {
+  __device__ __forceinline__ int count(Rows& rows, const int32_t* mid, const float* mw, int e, int T, int k) {
     const int t = threadIdx.x, wave = t >> 6;
     slot = -1;
     for (int j0 = 0; j0 < k; j0 += 8) {  // eight loads at a time
@@ -484,17 +552,25 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
   __syncthreads();
 }
 
-template <int F, int NBMAX, int NW, int UN>
+template <int F, int NBMAX, int NW, int UN, bool INLINE = false>
 __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   static_assert(UN <= 4, "mx_words holds four units");
   static_assert(NW * 64 >= kDecodeMaxT, "Finder takes a thread per token");
   __shared__ Rows rows;
   __shared__ __align__(16) char smem[gu_smem<F, NW, NBMAX>()];
-  const int e = __builtin_amdgcn_readfirstlane(item_expert(a.mid, blockIdx.y, a.T * a.k, a.E));
+  const int32_t* mid = a.mid;
+  const float* mw = a.mw;
+  if constexpr (INLINE) {
+    __shared__ InlineRoute route;
+    route_inline(route, a);
+    mid = route.mid;
+    mw = route.mw;
+  }
+  const int e = __builtin_amdgcn_readfirstlane(item_expert(mid, blockIdx.y, a.T * a.k, a.E));
   if (e < 0) return;
   const int lane = threadIdx.x & 63;
   Finder find;
-  const int n = find.count(rows, a.mid, a.mw, e, a.T, a.k);
+  const int n = find.count(rows, mid, mw, e, a.T, a.k);
   if (n == 0) return;
   GuTile t;
   t.n0 = blockIdx.x * 16;
@@ -778,10 +854,12 @@ __global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a) {
   else *(uint2*)o = uint2{pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3])};
 }
 
+int work_items(const DecodeArgs& a) { return a.T * a.k > a.E ? a.E : a.T * a.k; }
+bool few_groups(const DecodeArgs& a) { return cdiv(a.I, 16) * work_items(a) < 1024; }
+
 template <int F>
 hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
-  const int R = a.T * a.k;
-  const unsigned items = (unsigned)(R > a.E ? a.E : R);
+  const unsigned items = (unsigned)work_items(a);
   const dim3 gu((unsigned)cdiv(a.I, 16), items);
   constexpr int UN = F >= WF_FP8 ? 2 : 4;
   if (a.T <= 16) {
@@ -789,7 +867,9 @@ hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
     // once (T = 1 above: 24.7 us with eight, 26.3 with four).  Many: four, of
     // which more fit beside each other (16 tokens of 8 of 64 experts, d = 4096,
     // I = 1024, e4m3: 139 us with four, 150 with eight).
-    if ((int64_t)gu.x * gu.y < 1024)
+    if (a.route_inline)
+      MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 8, UN, true>), gu, dim3(8 * 64), 0, a);
+    else if (few_groups(a))
       MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 8, UN>), gu, dim3(8 * 64), 0, a);
     else
       MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 4, UN>), gu, dim3(4 * 64), 0, a);
@@ -809,18 +889,21 @@ hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
 
 }  // namespace
 
-hipError_t launch_decode(const LaunchCtx& c, const DecodeArgs& a, const void* logits, int logits_dtype, int32_t* ids,
-                         float* w, int weights) {
+hipError_t launch_decode(const LaunchCtx& c, DecodeArgs a, int weights) {
+  a.route_inline = few_groups(a) && inline_route_fits(a.T, a.k, a.E);
 #define TOPK(LT, KPL)                                                                                   \
   MOE_LAUNCH(c, "decode_route", (decode_topk_kernel<LT, KPL>), dim3((unsigned)a.T), dim3(64), 0,        \
-             (const LT*)logits, a.E, a.k, ids, w, a.mid, a.mw)
+             (const LT*)a.logits, a.E, a.k, a.ids, a.w, a.mid, a.mw)
 #define TOPK_E(LT)                    \
   if (a.E <= 128) TOPK(LT, 2);        \
   else if (a.E <= 512) TOPK(LT, 8);   \
   else TOPK(LT, 16)
-  if (!logits)
-    MOE_LAUNCH(c, "decode_route", decode_ids_kernel, dim3((unsigned)a.T), dim3(64), 0, ids, w, a.E, a.k, a.mid, a.mw);
-  else if (logits_dtype == F32) {
+  if (a.route_inline) {
+    // the gate/up kernel's
+  } else if (!a.logits) {
+    MOE_LAUNCH(c, "decode_route", decode_ids_kernel, dim3((unsigned)a.T), dim3(64), 0, a.ids, a.w, a.E, a.k, a.mid,
+               a.mw);
+  } else if (a.logits_f32) {
     TOPK_E(float);
   } else {
     TOPK_E(bf16_t);

@@ -119,6 +119,16 @@ CASES = [
     (2, 256, 8, 8, 384, "bf16", "mxfp8"),
     (40, 128, 2, 1, 128, "bf16", "mxfp8"),
     (130, 384, 12, 4, 256, "bf16", "mxfp8"),
+    # more slots a token than a wave has lanes; more experts than 128 and 512
+    (3, 16, 200, 150, 16, "bf16", "native"),
+    (2, 24, 600, 64, 8, "f32", "native"),
+    (20, 16, 130, 129, 8, "bf16", "native"),
+    # a few tokens with the most slots that are routed inside the first kernel,
+    # one more token, and one more slot
+    (4, 40, 64, 64, 24, "bf16", "native"),
+    (8, 72, 128, 8, 40, "f32", "native"),
+    (9, 72, 128, 8, 40, "bf16", "native"),
+    (4, 40, 66, 65, 24, "bf16", "native"),
 ]
 
 
