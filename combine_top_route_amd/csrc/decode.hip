@@ -206,39 +206,40 @@ __device__ __forceinline__ uint32_t mx_words(const void* s, int row4, int K, int
   return 0;
 }
 
-// MFMA operands of a unit's weights, of which this lane's row is col and its
-// chunks are q and 4 + q.  Codes become bfloat16 exactly (e4m3 has four
-// significant bits); an E8M0 scale is a power of two and rides on the
-// conversion, also exactly down to bfloat16's smallest numbers (2^-133).
-// mx: the row's four scale bytes of this unit.
+// The NF / 2 MFMA operands of 16 bytes of a weight row, chunk 4 c + q of its
+// unit.  Codes become bfloat16 exactly (e4m3 has four significant bits); an
+// E8M0 scale is a power of two and rides on the conversion, also exactly down
+// to bfloat16's smallest numbers (2^-133).  mx: the row's four scale bytes of
+// this unit.
+template <int F>
+__device__ __forceinline__ void chunk_frags(typename Fmt<F>::frag* fr, u32x4_t a, uint32_t mx, int c, int q) {
+  if constexpr (F == WF_F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fr[i] = __uint_as_float(a[i]);
+  } else if constexpr (F == WF_BF16) {
+    fr[0] = __builtin_bit_cast(bf16x8_t, a);
+  } else {
+    // its 16 codes lie in block 2 c + q / 2
+    const float s = F == WF_MX ? __uint_as_float(((mx >> (16 * c + 8 * (q >> 1))) & 0xffu) << 23) : 1.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4_t o;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t word = a[2 * h + i];
+        o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(word, s, false));
+        o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(word, s, true));
+      }
+      fr[h] = __builtin_bit_cast(bf16x8_t, o);
+    }
+  }
+}
+// All of a unit's: this lane's row is col, its chunks are q and 4 + q.
 template <int F>
 __device__ __forceinline__ void to_frags(typename Fmt<F>::frag (&fr)[Fmt<F>::NF], const lds_t* p, uint32_t mx, int q,
                                          int col) {
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const u32x4_t a = get_chunk(p, col, c * 4 + q);
-    if constexpr (F == WF_F32) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) fr[4 * c + i] = __uint_as_float(a[i]);
-    } else if constexpr (F == WF_BF16) {
-      fr[c] = __builtin_bit_cast(bf16x8_t, a);
-    } else {
-      // this lane's 16 codes of chunk 4 c + q lie in block 2 c + q / 2
-      const float s =
-          F == WF_MX ? __uint_as_float(((mx >> (16 * c + 8 * (q >> 1))) & 0xffu) << 23) : 1.0f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4_t o;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t word = a[2 * h + i];
-          o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(word, s, false));
-          o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(word, s, true));
-        }
-        fr[2 * c + h] = __builtin_bit_cast(bf16x8_t, o);
-      }
-    }
-  }
+  for (int c = 0; c < 2; ++c) chunk_frags<F>(fr + c * (Fmt<F>::NF / 2), get_chunk(p, col, c * 4 + q), mx, c, q);
 }
 
 // The activations of 16 tokens that meet a unit's weights: the same values of
@@ -266,19 +267,27 @@ __device__ __forceinline__ void put_acts(lds_t* p, const u32x4_t (&v)[kActHalves
   }
   turn_fence();
 }
+// The BV / 2 operands that meet weight chunk 4 c + q, and all of a unit's.
+template <int F>
+__device__ __forceinline__ void chunk_acts(u32x4_t* b, const lds_t* p, int c, int q, int col) {
+  if constexpr (F >= WF_FP8) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) b[v] = get_chunk(p + c * 2048, col, 2 * q + v);
+  } else {
+    b[0] = get_chunk(p, col, 4 * c + q);
+  }
+}
 template <int F>
 __device__ __forceinline__ void get_acts(u32x4_t (&b)[Fmt<F>::BV], const lds_t* p, int q, int col) {
 #pragma unroll
-  for (int v = 0; v < Fmt<F>::BV; ++v)
-    b[v] = F >= WF_FP8 ? get_chunk(p + (v >> 1) * 2048, col, 2 * q + (v & 1)) : get_chunk(p, col, 4 * v + q);
+  for (int c = 0; c < 2; ++c) chunk_acts<F>(b + c * (Fmt<F>::BV / 2), p, c, q, col);
 }
 
-// s + the unit's weights times the unit's activations, unscaled.
-template <int F>
-__device__ __forceinline__ f32x4_t unit_dot(f32x4_t s, const typename Fmt<F>::frag (&fr)[Fmt<F>::NF],
-                                            const u32x4_t (&b)[Fmt<F>::BV]) {
+// s + the products of N operands (a unit's: NF of them), unscaled.
+template <int F, int N = Fmt<F>::NF>
+__device__ __forceinline__ f32x4_t unit_dot(f32x4_t s, const typename Fmt<F>::frag* fr, const u32x4_t* b) {
 #pragma unroll
-  for (int i = 0; i < Fmt<F>::NF; ++i) {
+  for (int i = 0; i < N; ++i) {
     if constexpr (F == WF_F32)
       s = __builtin_amdgcn_mfma_f32_16x16x4f32(fr[i], __uint_as_float(b[i >> 2][i & 3]), s, 0, 0, 0);
     else
@@ -715,6 +724,106 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_kernel(DecodeArgs
   }
 }
 
+// The same for at most 8 tokens with 64 slots in all: tiles of 8 rows, so twice
+// the work-groups, and the experts are found in the lanes of each wave, slot f
+// in lane f, without LDS or barriers.  An MFMA's rows and columns 0 .. 7 are
+// the tile's rows and the tokens at the first half of a unit, 8 .. 15 the same
+// rows and tokens at the second half; the two diagonal blocks of its result
+// are the sums, the others are dropped.  (T = 1, the case above: SMALLGAIN.)
+constexpr int kSmallT = 8;
+inline bool small_down(const DecodeArgs& a) { return a.T <= kSmallT && a.T * a.k <= kWave; }
+
+template <int F>
+__global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(DecodeArgs a) {
+  typedef typename Fmt<F>::act AT;
+  constexpr int WORK = 2048 + 2048 * kActHalves<F>, UN = F >= WF_FP8 ? 4 : 6;
+  __shared__ __align__(16) char work[kDownWaves * WORK];  // then the parts [2 waves][8 tokens][8 rows]
+  const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
+  const int r8 = col & 7, half = col >> 3;
+  const int R = a.T * a.k;
+  const int mine = lane < R ? a.mid[lane] : -1;
+  bool first = mine >= 0;
+  for (int f = 0; f < R; ++f) first &= f >= lane || __builtin_amdgcn_readlane(mine, f) != mine;
+  const uint64_t firsts = __ballot(first);
+  const int nact = __popcll(firsts);
+  const int K = a.I, n0 = blockIdx.x * 8;
+  const int units = (K + Fmt<F>::UK - 1) / Fmt<F>::UK;
+  const int abytes = F >= WF_FP8 ? K : K * (int)sizeof(AT), bbytes = K * (int)sizeof(AT);
+  const uint64_t wbytes = (uint64_t)a.d * abytes;
+  const uint32_t wrow = (uint32_t)min(n0 + load_row(0), a.d - 1) * abytes;
+  const rsrc_t xb = buffer_of(a.aw, (uint64_t)R * bbytes);
+  lds_t* lw = (lds_t*)work + wave * WORK;
+  const int total = nact * units;
+  const uint64_t slots = a.k == 64 ? ~0ull : (1ull << a.k) - 1;  // a token's slots
+  f32x4_t acc = {0, 0, 0, 0};
+  for (int base = wave * UN; base < total; base += kDownWaves * UN) {
+    u32x4_t wv[UN], xv[UN][kActHalves<F>];
+    uint32_t mx[UN];
+    float sb[UN];
+    bool on_expert[UN];
+    int idx = base / units, unit = base - idx * units;
+    uint64_t rest = firsts;
+    for (int i = 0; i < idx; ++i) rest &= rest - 1;
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const bool on = base + i < total;  // uniform in the wave
+      const int e = on ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(rest)) : 0;
+      const uint64_t has = __ballot(mine == e);
+      const int off = unit * 128 + (lane & 7) * 16;
+      wv[i] = load16(buffer_of((const char*)a.w_down + e * wbytes, wbytes), wrow + off, on && off < abytes);
+      const int t = load_row(0);
+      const uint64_t ts = t < a.T ? (has >> (t * a.k)) & slots : 0;
+      const uint32_t xrow = (uint32_t)(t * a.k + (ts ? __builtin_ctzll(ts) : 0)) * bbytes;
+#pragma unroll
+      for (int h = 0; h < kActHalves<F>; ++h) {
+        const int o = (unit * kActHalves<F> + h) * 128 + (lane & 7) * 16;
+        xv[i][h] = load16(xb, xrow + o, on && ts && o < bbytes);
+      }
+      on_expert[i] = on && r8 < a.T && ((has >> (r8 * a.k)) & slots);
+      const char* sc = (const char*)a.s_down;
+      if (F == WF_FP8) sc += (int64_t)e * (a.d / 128) * (K / 128) * 4;
+      if (F == WF_MX) sc += (int64_t)e * a.d * (K / 32);
+      mx[i] = F == WF_MX ? ((const uint32_t*)sc)[(int64_t)(n0 + r8) * (K >> 7) + unit] : 0;
+      sb[i] = block_scale_of<F>(sc, n0, K, unit);
+      if (on && ++unit == units) {
+        unit = 0;
+        rest &= rest - 1;
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int chunk = lane & 7;
+      turn_fence();
+      *(__attribute__((address_space(3))) u32x4_t*)(lw + row_chunk(load_row(0), chunk)) = wv[i];
+#pragma unroll
+      for (int h = 0; h < kActHalves<F>; ++h)
+        *(__attribute__((address_space(3))) u32x4_t*)(lw + 2048 + h * 2048 + row_chunk(load_row(0), chunk)) = xv[i][h];
+      turn_fence();
+      typename Fmt<F>::frag fr[Fmt<F>::NF / 2];
+      u32x4_t xf[Fmt<F>::BV / 2];
+      chunk_frags<F>(fr, get_chunk(lw, r8, 4 * half + q), mx[i], half, q);
+      chunk_acts<F>(xf, lw + 2048, half, q, r8);
+      const f32x4_t s = unit_dot<F, Fmt<F>::NF / 2>(f32x4_t{0, 0, 0, 0}, fr, xf);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) acc[m] = on_expert[i] ? fmaf(sb[i], s[m], acc[m]) : acc[m];
+    }
+  }
+  float* red = (float*)work;
+  __syncthreads();
+  if ((q >> 1) == half) *(f32x4_t*)(red + ((wave * 2 + half) * 8 + r8) * 8 + (q & 1) * 4) = acc;
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int t = threadIdx.x >> 3, m = threadIdx.x & 7;
+    if (t < a.T) {  // d is a multiple of 8
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 2 * kDownWaves; ++w) v += red[(w * 8 + t) * 8 + m];
+      ((AT*)a.out)[(int64_t)t * a.d + n0 + m] = from_f32<AT>(v);
+    }
+  }
+}
+
 // --------------------------------------------- down product, more tokens
 // One wave: 16 rows of d of one expert for its tokens, all of I; the products
 // go to y [T k, d] in float32, which decode_combine_kernel sums in slot order.
@@ -873,6 +982,10 @@ hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
       MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 8, UN>), gu, dim3(8 * 64), 0, a);
     else
       MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 4, UN>), gu, dim3(4 * 64), 0, a);
+    if (small_down(a)) {
+      MOE_LAUNCH(c, "decode_down", decode_down_small_kernel<F>, dim3((unsigned)(a.d / 8)), dim3(kDownWaves * 64), 0, a);
+      return hipSuccess;
+    }
     const size_t smem = down_work<F>() + (size_t)a.E * 4 + (size_t)a.E * a.T * 2;
     HIP_RET(tile::allow_smem_once<decode_down_kernel<F>>(down_work<F>() + kMaxExperts * (4 + 16 * 2)));
     MOE_LAUNCH(c, "decode_down", decode_down_kernel<F>, dim3((unsigned)cdiv(a.d, 16)), dim3(kDownWaves * 64), smem, a);
