@@ -156,7 +156,13 @@ def _ptr(t):
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """torch's current stream on a device, as the library takes it (the raw
+    handle: building a torch.cuda.Stream object costs 2 us a call)."""
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(
+        torch.cuda.current_device() if device.index is None else device.index))
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _on(device):
@@ -164,7 +170,7 @@ def _on(device):
     paid, when it is the current one).  Refuses host memory."""
     if device.type != "cuda":
         raise ValueError(f"tensors are on {device}; the kernels need a GPU's memory")
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _need(t, name, shape, dtype, device):

@@ -468,7 +468,7 @@ DecodeLayout decode_layout(const moe_shape* s) {
   L.mid = take(sizeof(int32_t) * R);
   L.mw = take(sizeof(float) * R);
   L.aw = take(elem_size(s->dtype) * R * s->I);
-  if (s->T > 16) L.y = take(sizeof(float) * R * s->d);
+  if (!decode_one_down(s->T, s->k, s->d)) L.y = take(sizeof(float) * R * s->d);
   L.total = off;
   return L;
 }
@@ -918,7 +918,7 @@ moe_status moe_decode(const moe_shape* shape, int weights, const void* x, moe_ro
   a.mid = (int32_t*)at(workspace, L.mid);
   a.mw = (float*)at(workspace, L.mw);
   a.aw = at(workspace, L.aw);
-  a.y = shape->T > 16 ? (float*)at(workspace, L.y) : nullptr;
+  a.y = decode_one_down(shape->T, shape->k, shape->d) ? nullptr : (float*)at(workspace, L.y);
   const LaunchCtx c = make_ctx(stream);
   (void)hipGetLastError();
   HIP_TRY(launch_decode(c, a, weights), "decode");

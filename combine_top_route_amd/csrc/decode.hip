@@ -325,7 +325,8 @@ __device__ __forceinline__ float swiglu(float g, float u, float lim) {
 
 // The same routing inside the gate/up kernel, for a token or a few: every
 // work-group does it for itself, which costs it less than another launch and
-// the way through memory (T = 1, the case above: INLINEGAIN).
+// the way through memory (T = 1, the case above: 24.5 us with a launch
+// for it, 23.3 without).
 constexpr int kInlineT = 8, kInlineSlots = 256, kInlineE = 128;
 struct InlineRoute {
   int32_t mid[kInlineSlots];
@@ -335,12 +336,15 @@ __host__ __device__ inline bool inline_route_fits(int T, int k, int E) {
   return T <= kInlineT && k <= kWave && T * k <= kInlineSlots && E <= kInlineE;
 }
 
-// 512 threads.  The first work-group leaves the results in memory.
+// NW waves (at least a thread per slot).  The first work-group leaves the
+// results in memory.
+template <int NW>
 __device__ __forceinline__ void route_inline(InlineRoute& r, const DecodeArgs& a) {
-  const int lane = threadIdx.x & 63, t = tile::wave_id(), k = a.k;
+  static_assert(NW * 64 >= kInlineSlots, "a thread per slot");
+  const int lane = threadIdx.x & 63, k = a.k;
   const bool first_group = blockIdx.x == 0 && blockIdx.y == 0;
   if (a.logits) {
-    if (t < a.T) {
+    for (int t = tile::wave_id(); t < a.T; t += NW) {
       TopK<2> top;
       if (a.logits_f32) top.load((const float*)a.logits + (int64_t)t * a.E, a.E);
       else top.load((const bf16_t*)a.logits + (int64_t)t * a.E, a.E);
@@ -571,7 +575,7 @@ __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   const float* mw = a.mw;
   if constexpr (INLINE) {
     __shared__ InlineRoute route;
-    route_inline(route, a);
+    route_inline<NW>(route, a);
     mid = route.mid;
     mw = route.mw;
   }
@@ -729,7 +733,8 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_kernel(DecodeArgs
 // in lane f, without LDS or barriers.  An MFMA's rows and columns 0 .. 7 are
 // the tile's rows and the tokens at the first half of a unit, 8 .. 15 the same
 // rows and tokens at the second half; the two diagonal blocks of its result
-// are the sums, the others are dropped.  (T = 1, the case above: SMALLGAIN.)
+// are the sums, the others are dropped.  (T = 1, the case above: 23.1 us with the
+// kernel before, 22.4 with this one; 7 tokens in float32 22.8 and 21.6.)
 constexpr int kSmallT = 8;
 inline bool small_down(const DecodeArgs& a) { return a.T <= kSmallT && a.T * a.k <= kWave; }
 
@@ -964,34 +969,38 @@ __global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a) {
 }
 
 int work_items(const DecodeArgs& a) { return a.T * a.k > a.E ? a.E : a.T * a.k; }
-bool few_groups(const DecodeArgs& a) { return cdiv(a.I, 16) * work_items(a) < 1024; }
+int64_t gu_groups(const DecodeArgs& a) { return cdiv(a.I, 16) * work_items(a); }
 
 template <int F>
 hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
   const unsigned items = (unsigned)work_items(a);
   const dim3 gu((unsigned)cdiv(a.I, 16), items);
   constexpr int UN = F >= WF_FP8 ? 2 : 4;
-  if (a.T <= 16) {
-    // Few work-groups: eight waves each, so that all bytes are in flight at
-    // once (T = 1 above: 24.7 us with eight, 26.3 with four).  Many: four, of
-    // which more fit beside each other (16 tokens of 8 of 64 experts, d = 4096,
-    // I = 1024, e4m3: 139 us with four, 150 with eight).
-    if (a.route_inline)
-      MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 8, UN, true>), gu, dim3(8 * 64), 0, a);
-    else if (few_groups(a))
-      MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 8, UN>), gu, dim3(8 * 64), 0, a);
-    else
-      MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 4, UN>), gu, dim3(4 * 64), 0, a);
-    if (small_down(a)) {
-      MOE_LAUNCH(c, "decode_down", decode_down_small_kernel<F>, dim3((unsigned)(a.d / 8)), dim3(kDownWaves * 64), 0, a);
-      return hipSuccess;
-    }
+  if (a.T > 16)
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, kMaxBlocks<F>, 4, 2>), gu, dim3(4 * 64), 0, a);
+  // As many work-groups as fit beside each other, two per CU: eight waves each,
+  // so that all bytes are in flight at once (T = 1 above, 384 work-groups: 24.7
+  // us with eight, 26.3 with four).  More: four, of which more fit (T = 2, 768:
+  // 38.7 us with eight, 36.1 with four; 16 tokens of 8 of 64 experts, d = 4096,
+  // I = 1024, e4m3: 150 and 139).
+  else if (gu_groups(a) <= 512 && a.route_inline)
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 8, UN, true>), gu, dim3(8 * 64), 0, a);
+  else if (gu_groups(a) <= 512)
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 8, UN>), gu, dim3(8 * 64), 0, a);
+  else if (a.route_inline)
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 4, UN, true>), gu, dim3(4 * 64), 0, a);
+  else
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 4, UN>), gu, dim3(4 * 64), 0, a);
+  if (small_down(a)) {
+    MOE_LAUNCH(c, "decode_down", decode_down_small_kernel<F>, dim3((unsigned)(a.d / 8)), dim3(kDownWaves * 64), 0, a);
+    return hipSuccess;
+  }
+  if (decode_one_down(a.T, a.k, a.d)) {
     const size_t smem = down_work<F>() + (size_t)a.E * 4 + (size_t)a.E * a.T * 2;
     HIP_RET(tile::allow_smem_once<decode_down_kernel<F>>(down_work<F>() + kMaxExperts * (4 + 16 * 2)));
     MOE_LAUNCH(c, "decode_down", decode_down_kernel<F>, dim3((unsigned)cdiv(a.d, 16)), dim3(kDownWaves * 64), smem, a);
     return hipSuccess;
   }
-  MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, kMaxBlocks<F>, 4, 2>), gu, dim3(4 * 64), 0, a);
   MOE_LAUNCH(c, "decode_down", decode_down_rows_kernel<F>, dim3((unsigned)cdiv(a.d, 16 * kDownRowWaves), items),
              dim3(kDownRowWaves * 64), 0, a);
   const dim3 cg((unsigned)cdiv(a.d, 1024), (unsigned)a.T);
@@ -1003,7 +1012,9 @@ hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
 }  // namespace
 
 hipError_t launch_decode(const LaunchCtx& c, DecodeArgs a, int weights) {
-  a.route_inline = few_groups(a) && inline_route_fits(a.T, a.k, a.E);
+  // 8 tokens above, 3072 work-groups: 103 us with each routing for itself, 98
+  // with a launch before; 4 tokens, 1536: 58.9 both ways
+  a.route_inline = inline_route_fits(a.T, a.k, a.E) && gu_groups(a) <= 1024;
 #define TOPK(LT, KPL)                                                                                   \
   MOE_LAUNCH(c, "decode_route", (decode_topk_kernel<LT, KPL>), dim3((unsigned)a.T), dim3(64), 0,        \
              (const LT*)a.logits, a.E, a.k, a.ids, a.w, a.mid, a.mw)
