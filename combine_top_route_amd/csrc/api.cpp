@@ -409,8 +409,8 @@ moe_status check_save8(const moe_shape* s) {
 size_t saved8_scales_at(const moe_shape* s) { return align256((size_t)s->T * s->k * 2 * s->I); }
 size_t saved8_total(const moe_shape* s) { return saved8_scales_at(s) + (size_t)s->T * s->k * save8_scales(s->I); }
 
-// The layer's workspace for `op`, then what the plain call finds in `saved`:
-// the forward's H (float32 has it in the workspace), the backward's Aw.
+// The layer's workspace for `op`, then the Aw that the plain backward finds in
+// `saved`.
 struct Layout8 {
   Layout base;
   size_t extra = 0, total = 0;
@@ -418,9 +418,8 @@ struct Layout8 {
 Layout8 layout8(const moe_shape* s, int op) {
   Layout8 L;
   L.base = layout(s, op);
-  const size_t R = (size_t)s->T * s->k, row = elem_size(s->dtype) * s->I;
   L.extra = align256(L.base.total);
-  L.total = L.extra + (op == MOE_OP_BACKWARD ? R * row : (s->dtype == MOE_F32 ? 0 : 2 * R * row));
+  L.total = op == MOE_OP_BACKWARD ? L.extra + elem_size(s->dtype) * s->T * s->k * s->I : L.base.total;
   return L;
 }
 
@@ -794,11 +793,17 @@ moe_status moe_forward8(const moe_shape* shape, const void* x, moe_routing* rout
                           (int32_t*)at(workspace, L.order), nullptr, nullptr, (int4*)at(workspace, L.tiles)),
           "route_schedule");
   const LayerArgs a = layer_args(shape, routing, x, w_gate_up, w_down, workspace, L);
-  void* H = shape->dtype == MOE_F32 ? at(workspace, L.H) : at(workspace, L8.extra);
+  uint8_t* codes = (uint8_t*)saved8;
+  uint8_t* scales = (uint8_t*)at(saved8, saved8_scales_at(shape));
+  void* A = at(workspace, L.A);
   void* Y = at(workspace, L.Y);
-  HIP_TRY(forward_gemms(shape, c, a, workspace, L, nullptr, H, at(workspace, L.A), Y), "forward GEMMs");
-  HIP_TRY(launch_save8(c, shape->dtype, H, nullptr, nullptr, a.R, a.I, a.swiglu_lim, nullptr, (uint8_t*)saved8,
-                       (uint8_t*)at(saved8, saved8_scales_at(shape))), "swiglu_save8");
+  if (shape->dtype == MOE_F32) {
+    HIP_TRY(f32_fwd_gemms(c, a, at(workspace, L.H), A, Y), "forward GEMMs");
+    HIP_TRY(launch_save8(c, MOE_F32, at(workspace, L.H), nullptr, nullptr, a.R, a.I, a.swiglu_lim, nullptr, codes,
+                         scales), "swiglu_save8");
+  } else {  // encoded in the gate/up GEMM's epilogue
+    HIP_TRY(bf16_fwd_gemms(c, a, nullptr, A, Y, codes, scales), "forward GEMMs");
+  }
   HIP_TRY(launch_combine(c, "combine", shape->dtype, Y, routing->row_of, nullptr, (int)shape->T,
                          (int)shape->k, (int)shape->d, out), "combine");
   return MOE_OK;

@@ -200,8 +200,9 @@ struct LayerArgs {
 // silu(gate) * up (each row already carries its top-k weight) and Yw [R,d] =
 // Aw W_down^T, so the combine is a plain sum of each token's k rows.  Yw ==
 // null: the gate/up GEMM alone (the recomputing backward).
-// bf16 MFMA path.
-hipError_t bf16_fwd_gemms(const LaunchCtx& c, const LayerArgs& a, void* H, void* Aw, void* Yw);
+// bf16 MFMA path.  codes and scales (non-null): H's 8-bit checkpoint instead of H.
+hipError_t bf16_fwd_gemms(const LaunchCtx& c, const LayerArgs& a, void* H, void* Aw, void* Yw,
+                          uint8_t* codes = nullptr, uint8_t* scales = nullptr);
 // backward outputs dH [R,2I], dXp [R,d], dwp [R, bf16_dw_blocks(I)] fp32, dW_gu, dW_d.
 // s8 (non-null): the checkpoint that stands for H and Aw (both null then).
 hipError_t bf16_bwd_gemms(const LaunchCtx& c, const LayerArgs& a, const void* dout,

@@ -34,6 +34,7 @@
 // layouts are XOR-swizzled so the reads of one instruction hit distinct
 // banks.
 #include "common.h"
+#include "save8.h"
 #include "tile.h"
 
 #include <algorithm>
@@ -604,10 +605,38 @@ __device__ __forceinline__ void lds_to_global(const lds_t* t, bf16_t* C, int64_t
   }
 }
 
+// Encodes the staged ROWS x 128 tile (one half of H's columns from a multiple
+// of 128) into e4m3 codes and a scale byte per 32 columns: a block is four
+// neighbouring lanes' chunks.  Columns >= col_lim count as zeros.
+template <int ROWS, int S>
+__device__ __forceinline__ void lds_to_codes(const lds_t* t, uint8_t* C, int64_t ldc, uint8_t* scales, int64_t lds,
+                                             int row_lim, int col_lim) {
+  constexpr int CPR = TBN / 2 / 8, NQ = ROWS * CPR / NTHR;
+  static_assert(ROWS * CPR % NTHR == 0 && CPR % 4 == 0, "whole blocks per four lanes");
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const int q = threadIdx.x + i * NTHR, row = q / CPR, c8 = q % CPR;
+    const bool in = c8 * 8 < col_lim;
+    const u32x4_t v = *(const __attribute__((address_space(3))) u32x4_t*)(t + row * S + c8 * 16);
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = in ? __uint_as_float(v[j] << 16) : 0.0f;
+      f[2 * j + 1] = in ? __uint_as_float(v[j] & 0xffff0000u) : 0.0f;
+    }
+    uint32_t byte;
+    const u32x2_t code = save8::encode8(f, &byte);
+    if (row < row_lim && in) {
+      __builtin_nontemporal_store(code, (u32x2_t*)(C + (int64_t)row * ldc + c8 * 8));
+      if (c8 % 4 == 0) scales[(int64_t)row * lds + c8 / 4] = (uint8_t)byte;
+    }
+  }
+}
+
 // ===========================================================================
 // Ragged-M GEMMs: rows are an expert's segment of the expert-sorted rows.
 // ===========================================================================
-enum Epi { EPI_STORE = 0, EPI_GATEUP = 1 };
+enum Epi { EPI_STORE = 0, EPI_GATEUP = 1, EPI_GATEUP8 = 2 };
 enum BLay { B_MK = 0, B_MK_GATEUP = 1, B_KM = 2 };
 
 struct RowsArgs {
@@ -639,6 +668,9 @@ struct RowsArgs {
   float lim;
   const float* topk_w;
   const int32_t* src_of;
+  // EPI_GATEUP8: the same with H left as its 8-bit checkpoint
+  uint8_t* codes;   // [R, 2I]
+  uint8_t* scales;  // [R, 2 ceil(I/32)]
 };
 
 // Rows of a row tile that instruction i of OpMK<ROWS> loads: through a_src
@@ -710,11 +742,11 @@ __device__ __forceinline__ void rows_tile(const RowsArgs& p, char* smem, int nt,
   // second, dependent load) and the gathered A rows.  Address math between
   // loads made the compiler wait for each before issuing the next.
   int wsrc = 0;
-  if constexpr (EPI == EPI_GATEUP) wsrc = fetch_wsrc<ROWS>(p, m0, seg1);
+  if constexpr (EPI != EPI_STORE) wsrc = fetch_wsrc<ROWS>(p, m0, seg1);
   int arow[OpMK<ROWS>::NI];
   fetch_arow<ROWS>(p, m0, seg1, arow);
   float wrow = 0.0f;
-  if constexpr (EPI == EPI_GATEUP) {
+  if constexpr (EPI != EPI_STORE) {
     if (wsrc) wrow = p.topk_w[wsrc - 1];
   }
   OpMK<ROWS> oa;
@@ -745,7 +777,7 @@ __device__ __forceinline__ void rows_tile(const RowsArgs& p, char* smem, int nt,
     barrier_lds();
     lds_to_global<ROWS, TBN, S>(lds, p.C + (int64_t)m0 * p.ldc + nt * TBN, p.ldc, rows_valid,
                                 p.N - nt * TBN);
-  } else if constexpr (EPI == EPI_GATEUP) {
+  } else {
     // acc[i][0] = gate, acc[i][1] = up, register by register for the same
     // gate column wn * 32 + acc_col(0, r / 4, lane) + r % 4 (128 gate columns
     // per tile)
@@ -759,11 +791,20 @@ __device__ __forceinline__ void rows_tile(const RowsArgs& p, char* smem, int nt,
       const float g = clamp_gate(acc[i][0][r], p.lim), u = clamp_up(acc[i][1][r], p.lim);
       return wl[r0w + acc_row(i, lane)] * (g * sigmoidf_(g) * u);
     });
-    if (p.H) stage_quads<TMX, 1, S>(lds + TB, r0w, c0w, [&](int i, int, int r) { return acc[i][0][r]; });
+    if (EPI == EPI_GATEUP8 || p.H) stage_quads<TMX, 1, S>(lds + TB, r0w, c0w, [&](int i, int, int r) { return acc[i][0][r]; });
     barrier_lds();
     const int gc0 = nt * (TBN / 2);
     lds_to_global<ROWS, TBN / 2, S>(lds, p.Aout + (int64_t)m0 * p.I + gc0, p.I, rows_valid, p.I - gc0);
-    if (p.H) {
+    if constexpr (EPI == EPI_GATEUP8) {
+      const int64_t nb = cdiv(p.I, 32);
+      uint8_t* C0 = p.codes + (int64_t)m0 * 2 * p.I + gc0;
+      uint8_t* s0 = p.scales + m0 * 2 * nb + gc0 / 32;
+      lds_to_codes<ROWS, S>(lds + TB, C0, 2 * p.I, s0, 2 * nb, rows_valid, p.I - gc0);
+      barrier_lds();
+      stage_quads<TMX, 1, S>(lds, r0w, c0w, [&](int i, int, int r) { return acc[i][1][r]; });
+      barrier_lds();
+      lds_to_codes<ROWS, S>(lds, C0 + p.I, 2 * p.I, s0 + nb, 2 * nb, rows_valid, p.I - gc0);
+    } else if (p.H) {
       bf16_t* H0 = p.H + (int64_t)m0 * 2 * p.I + gc0;
       lds_to_global<ROWS, TBN / 2, S>(lds + TB, H0, 2 * p.I, rows_valid, p.I - gc0);
       barrier_lds();
@@ -1268,7 +1309,8 @@ hipError_t launch_rows(const LaunchCtx& c, const char* name, const RowsArgs& p, 
 
 int bf16_dw_blocks(int) { return 1; }
 
-hipError_t bf16_fwd_gemms(const LaunchCtx& c, const LayerArgs& a, void* H, void* Aw, void* Yw) {
+hipError_t bf16_fwd_gemms(const LaunchCtx& c, const LayerArgs& a, void* H, void* Aw, void* Yw, uint8_t* codes,
+                          uint8_t* scales) {
   const int64_t I = a.I, d = a.d;
   {  // gate/up GEMM: token rows gathered from x; SwiGLU and top-k weight in the epilogue
     RowsArgs p = {};
@@ -1279,7 +1321,9 @@ hipError_t bf16_fwd_gemms(const LaunchCtx& c, const LayerArgs& a, void* H, void*
     p.row_major = rows_tile_order(a.T * d, a.E * 2 * I * d);
     p.H = (bf16_t*)H; p.Aout = (bf16_t*)Aw; p.I = a.I; p.lim = a.swiglu_lim;
     p.topk_w = a.topk_w; p.src_of = a.src_of;
-    hipError_t err = launch_rows<EPI_GATEUP, B_MK_GATEUP>(c, "gemm_gateup_fwd", p, a.R, a.persistent);
+    p.codes = codes; p.scales = scales;
+    hipError_t err = codes ? launch_rows_tiles<EPI_GATEUP8, B_MK_GATEUP>(c, "gemm_gateup_fwd8", p, a.R)
+                           : launch_rows<EPI_GATEUP, B_MK_GATEUP>(c, "gemm_gateup_fwd", p, a.R, a.persistent);
     if (err != hipSuccess) return err;
   }
   if (!Yw) return hipSuccess;  // the gate/up half alone (recomputation)
