@@ -290,6 +290,64 @@ def _backward8(ctx, dout, *unused):
 moe_fwd8.register_autograd(_backward8, setup_context=_setup_context8)
 
 
+# ---------------------------------------------------------------- few tokens
+def _check_decode_args(x, logits, w_gate_up, w_down, k, s_gate_up, s_down) -> str:
+    """Shapes and dtypes of moe_decode; returns the weights' format."""
+    _require(x.dim() == 2 and w_gate_up.dim() == 3 and w_gate_up.shape[2] == x.shape[1]
+             and w_gate_up.shape[1] % 2 == 0,
+             f"x must be [T, d] and w_gate_up [E, 2I, d], got {tuple(x.shape)} and {tuple(w_gate_up.shape)}")
+    T, d = x.shape
+    E, two_i, _ = w_gate_up.shape
+    I = two_i // 2
+    _require(tuple(w_down.shape) == (E, d, I), f"w_down must be [E={E}, d={d}, I={I}], got {tuple(w_down.shape)}")
+    _require(tuple(logits.shape) == (T, E) and logits.dtype in _FLOATS,
+             f"logits must be [T={T}, E={E}] of one of {_FLOATS}, got {tuple(logits.shape)} {logits.dtype}")
+    _require(1 <= k <= E, f"k={k} outside [1, E={E}]")
+    _require(x.dtype in _FLOATS, f"x dtype {x.dtype} not in {_FLOATS}")
+    _require((s_gate_up is None) == (s_down is None), "give the scales of both weights or of neither")
+    tensors = [("x", x), ("logits", logits), ("w_gate_up", w_gate_up), ("w_down", w_down)]
+    if s_gate_up is None:
+        fmt, dt = "native", x.dtype
+    else:
+        fmt, dt = ("fp8_block" if s_gate_up.dtype == torch.float32 else "mxfp8"), torch.uint8
+        _require(d % 128 == 0 and I % 128 == 0, f"coded weights need d and I multiples of 128, got {d} and {I}")
+        shapes = (((E, two_i // 128, d // 128), (E, d // 128, I // 128)) if fmt == "fp8_block"
+                  else ((E, two_i, d // 32), (E, d, I // 32)))
+        sdt = torch.float32 if fmt == "fp8_block" else torch.uint8
+        for name, t, sh in (("s_gate_up", s_gate_up, shapes[0]), ("s_down", s_down, shapes[1])):
+            _require(tuple(t.shape) == sh and t.dtype == sdt, f"{name} must be {sh} {sdt}, got {tuple(t.shape)} {t.dtype}")
+            tensors.append((name, t))
+    _require(w_gate_up.dtype == dt and w_down.dtype == dt,
+             f"the weights must be {dt}, got {w_gate_up.dtype}, {w_down.dtype}")
+    for name, t in tensors:
+        _require(t.is_contiguous(), f"{name} must be contiguous")
+    return fmt
+
+
+@torch.library.custom_op(f"{_NS}::moe_decode", mutates_args=())
+def moe_decode(x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: Tensor, k: int,
+               s_gate_up: Tensor | None = None, s_down: Tensor | None = None, swiglu_limit: float = 0.0) -> Tensor:
+    """The layer for at most 256 tokens (binding.MoeDecoder as one operator that
+    allocates its output and workspace): out [T,d].  With s_gate_up and s_down
+    the weights are e4m3 codes, their scales float32 per 128x128 block or E8M0
+    bytes per 32 columns.  No gradient."""
+    fmt = _check_decode_args(x, logits, w_gate_up, w_down, k, s_gate_up, s_down)
+    tensors = dict(x=x, logits=logits, w_gate_up=w_gate_up, w_down=w_down)
+    if fmt != "native":
+        tensors.update(s_gate_up=s_gate_up, s_down=s_down)
+    _check_devices(**tensors)
+    E, two_i, d = w_gate_up.shape
+    with B._on(x.device):
+        dec = B.MoeDecoder(x.shape[0], d, E, k, two_i // 2, x.dtype, logits.dtype, fmt, x.device, swiglu_limit)
+        pair = (lambda w, s: w) if fmt == "native" else (lambda w, s: (w, s))
+        return dec.forward(x, pair(w_gate_up, s_gate_up), pair(w_down, s_down), logits=logits)
+
+
+@moe_decode.register_fake
+def _(x, logits, w_gate_up, w_down, k, s_gate_up=None, s_down=None, swiglu_limit=0.0):
+    return torch.empty_like(x)
+
+
 def moe_layer(x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: Tensor, k: int,
               precision: str = "native", recompute: bool = False, swiglu_limit: float = 0.0,
               save8: bool = False) -> Tensor:
@@ -297,7 +355,12 @@ def moe_layer(x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: Tensor, k: i
     recompute=True: activation checkpointing inside the operator (nothing
     kept between forward and backward but the routing).  swiglu_limit > 0:
     the clamped SwiGLU with that limit.  save8=True (precision "native"): the
-    activations are kept in 8 bits between forward and backward."""
+    activations are kept in 8 bits between forward and backward.
+
+    In a HIP graph, capture forward and backward on leaves of the graph's own
+    (t.detach().requires_grad_()): a leaf that an eager autograd graph still
+    holds takes its gradient on the stream it was first used on, and torch
+    ends the capture, or the process, when that stream is drawn in."""
     for name, t in (("x", x), ("logits", logits), ("w_gate_up", w_gate_up), ("w_down", w_down)):
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")

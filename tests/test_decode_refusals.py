@@ -118,3 +118,32 @@ def test_decoder_arguments():
         bad("scales has shape", w_gate_up=gu, w_down=(dn[0], gu[1]))
         bad("codes has shape", w_gate_up=(dn[0], gu[1]), w_down=dn)
         bad("scales has dtype", w_gate_up=(gu[0], gu[1].to(torch.int32)), w_down=dn)
+
+
+def test_operator_refuses_and_traces():
+    from combine_top_route_amd.autograd import moe_decode
+    bf, u8 = torch.bfloat16, torch.uint8
+    good = dict(x=torch.zeros(3, 128, dtype=bf), logits=torch.zeros(3, 4), w_gate_up=torch.zeros(4, 256, 128, dtype=bf),
+                w_down=torch.zeros(4, 128, 128, dtype=bf), k=2)
+
+    def bad(match, **kw):
+        with pytest.raises(ValueError, match=match):
+            moe_decode(**{**good, **kw})
+
+    bad("GPU")
+    bad("w_gate_up", x=torch.zeros(3, 64, dtype=bf))
+    bad("w_down", w_down=torch.zeros(4, 128, 64, dtype=bf))
+    bad("logits", logits=torch.zeros(2, 4))
+    bad("k=5", k=5)
+    bad("weights must be", w_down=torch.zeros(4, 128, 128))
+    bad("both weights or of neither", s_down=torch.zeros(4, 1, 1))
+    bad("weights must be", s_gate_up=torch.zeros(4, 2, 1), s_down=torch.zeros(4, 1, 1))
+    bad("s_down must be", s_gate_up=torch.zeros(4, 2, 1), s_down=torch.zeros(4, 2, 1))
+    bad("contiguous", x=torch.zeros(3, 256, dtype=bf)[:, ::2])
+    meta = {n: t.to("meta") if isinstance(t, torch.Tensor) else t for n, t in good.items()}
+    assert moe_decode(**meta).shape == (3, 128)
+    codes = dict(meta, w_gate_up=torch.zeros(4, 256, 128, dtype=u8, device="meta"),
+                 w_down=torch.zeros(4, 128, 128, dtype=u8, device="meta"),
+                 s_gate_up=torch.zeros(4, 256, 4, dtype=u8, device="meta"),
+                 s_down=torch.zeros(4, 128, 4, dtype=u8, device="meta"))
+    assert moe_decode(**codes).dtype == bf

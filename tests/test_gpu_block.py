@@ -132,3 +132,40 @@ def test_compiled_block_traces():
     got = torch.autograd.grad(fn(*leaves), leaves, dout)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_captured_step_beside_a_live_eager_graph():
+    """Forward and backward of the block in a HIP graph, on leaves of its own,
+    while an eager autograd graph of the same weights lives; every replay
+    against the eager gradients."""
+    from combine_top_route_amd.autograd import moe_block
+    leaves, dout = tensors(torch.bfloat16, seed=11)
+    leaves = [t.requires_grad_() for t in leaves]
+    live = moe_block(*leaves, k, save8=True)               # kept until the end
+    own = [t.detach().requires_grad_() for t in leaves]    # the same memory
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        warm = [t.detach().requires_grad_() for t in leaves]
+        torch.autograd.grad(moe_block(*warm, k, save8=True), warm, dout)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = moe_block(*own, k, save8=True)
+        grads = torch.autograd.grad(out, own, dout)
+    for i in range(3):
+        fresh, d2 = tensors(torch.bfloat16, seed=20 + i)
+        with torch.no_grad():
+            for t, f in zip(leaves, fresh):
+                t.detach().copy_(f)
+            dout.copy_(d2)
+        graph.replay()
+        eager = [t.detach().requires_grad_() for t in leaves]
+        want_out = moe_block(*eager, k, save8=True)
+        want = torch.autograd.grad(want_out, eager, dout)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want_out)
+        for a, b in zip(grads, want):
+            assert torch.equal(a, b)
+    assert live.shape == (T, d)

@@ -274,3 +274,36 @@ def test_captured_and_replayed(T):
         want = eager.forward(x, wgu, wd, logits=lg)
         torch.cuda.synchronize()
         assert torch.equal(out, want), i
+
+
+def test_two_decoders_at_once():
+    """Two decoders on two streams at a time, each against its own result alone."""
+    cases = [make(24, 136, 8, 3, 72, seed=1), make(3, 264, 6, 2, 104, seed=2)]
+    decs = [decoder(cases[0][0], 8, 3, 72), decoder(cases[1][0], 6, 2, 104)]
+    want = [d.forward(x, wgu, wd, logits=lg).clone() for d, (x, wgu, wd, lg) in zip(decs, cases)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for d, s, (x, wgu, wd, lg) in zip(decs, streams, cases):
+            with torch.cuda.stream(s):
+                d.forward(x, wgu, wd, logits=lg)
+        torch.cuda.synchronize()
+        for d, w in zip(decs, want):
+            assert torch.equal(d.out, w)
+
+
+@pytest.mark.parametrize("T,dtype,weights", [(3, "bf16", "native"), (40, "f32", "native"), (20, "bf16", "fp8_block"),
+                                             (2, "bf16", "mxfp8")])
+def test_operator(T, dtype, weights):
+    from combine_top_route_amd.autograd import moe_decode
+    d, E, k, I = 128, 6, 2, 128
+    x, wgu, wd, lg = make(T, d, E, k, I, dtype, weights)
+    want = decoder(x, E, k, I, weights, limit=0.5).forward(x, wgu, wd, logits=lg)
+    args = (wgu, wd, k) if weights == "native" else (wgu[0], wd[0], k, wgu[1], wd[1])
+    got = moe_decode(x, lg, *args, swiglu_limit=0.5)
+    assert torch.equal(got, want)
+    fn = torch.compile(lambda x, lg: moe_decode(x, lg, *args, swiglu_limit=0.5), fullgraph=True, backend="aot_eager")
+    assert torch.equal(fn(x, lg), want)
+    xr = (x.clone() if weights == "native" else x.float().to(x.dtype)).requires_grad_()
+    with pytest.raises(RuntimeError):
+        moe_decode(xr, lg, *args).sum().backward()
