@@ -459,13 +459,13 @@ struct GuTile {  // where a lane finds them
   int n0;
 };
 
-template <int F, int UN>
+template <int F, bool NT, int UN>
 __device__ __forceinline__ void load_gu(GuWeights<F, UN>& w, const GuTile& t, int I, int K, int base) {
   const int bytes = F >= WF_FP8 ? K : K * (int)sizeof(typename Fmt<F>::act);
 #pragma unroll
   for (int i = 0; i < UN; ++i) {
-    load_rows(w.g[i], t.w, t.g, (base + i) * 128, bytes);
-    load_rows(w.u[i], t.w, t.u, (base + i) * 128, bytes);
+    load_rows<NT>(w.g[i], t.w, t.g, (base + i) * 128, bytes);
+    load_rows<NT>(w.u[i], t.w, t.u, (base + i) * 128, bytes);
     w.sg[i] = block_scale_of<F>(t.sc, t.n0, K, base + i);
     w.su[i] = block_scale_of<F>(t.sc, I + t.n0, K, base + i);
   }
@@ -480,7 +480,7 @@ constexpr size_t gu_smem() {  // per wave: gate, up, activations; then the waves
 }
 
 // The tokens r0 .. r0 + 16 NB of the expert.  w holds the first units.
-template <int F, int NW, int UN, int NB>
+template <int F, bool NT, int NW, int UN, int NB>
 __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& rows, int r0, int n,
                                             GuWeights<F, UN>& w, const GuTile& t, char* smem) {
   typedef typename Fmt<F>::act AT;
@@ -506,7 +506,7 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
   for (int b = 0; b < NB; ++b) ag[b] = au[b] = f32x4_t{0, 0, 0, 0};
   constexpr int UB = NB == 1 ? UN : 1;  // units whose activations are in flight together
   for (int base = wave * UN; base < units; base += NW * UN) {
-    if (base != wave * UN || r0) load_gu<F, UN>(w, t, a.I, K, base);
+    if (base != wave * UN || r0) load_gu<F, NT>(w, t, a.I, K, base);
 #pragma unroll
     for (int i0 = 0; i0 < UN; i0 += UB) {
       u32x4_t xv[UB][NB][kActHalves<F>][2];
@@ -565,7 +565,7 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
   __syncthreads();
 }
 
-template <int F, int NBMAX, int NW, int UN, bool INLINE = false>
+template <int F, bool NT, int NBMAX, int NW, int UN, bool INLINE = false>
 __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   static_assert(UN <= 4, "mx_words holds four units");
   static_assert(NW * 64 >= kDecodeMaxT, "Finder takes a thread per token");
@@ -602,16 +602,16 @@ __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   if (F == WF_MX) sc += (int64_t)e * 2 * a.I * (a.d / 32);
   t.sc = sc;
   GuWeights<F, UN> w;
-  load_gu<F, UN>(w, t, a.I, a.d, tile::wave_id() * UN);
+  load_gu<F, NT>(w, t, a.I, a.d, tile::wave_id() * UN);
   find.list(rows);
   if constexpr (NBMAX == 1) {
-    gateup_rows<F, NW, UN, 1>(a, rows, 0, n, w, t, smem);
+    gateup_rows<F, NT, NW, UN, 1>(a, rows, 0, n, w, t, smem);
   } else {
     for (int r0 = 0; r0 < n; r0 += 16 * NBMAX) {
       const int left = n - r0;
-      if (left <= 16) gateup_rows<F, NW, UN, 1>(a, rows, r0, n, w, t, smem);
-      else if (NBMAX == 2 || left <= 32) gateup_rows<F, NW, UN, 2>(a, rows, r0, n, w, t, smem);
-      else gateup_rows<F, NW, UN, NBMAX>(a, rows, r0, n, w, t, smem);
+      if (left <= 16) gateup_rows<F, NT, NW, UN, 1>(a, rows, r0, n, w, t, smem);
+      else if (NBMAX == 2 || left <= 32) gateup_rows<F, NT, NW, UN, 2>(a, rows, r0, n, w, t, smem);
+      else gateup_rows<F, NT, NW, UN, NBMAX>(a, rows, r0, n, w, t, smem);
     }
   }
 }
@@ -624,7 +624,7 @@ __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
 constexpr int kDownWaves = 16;
 template <int F> constexpr int down_work() { return kDownWaves * (2048 + 2048 * kActHalves<F>); }
 
-template <int F>
+template <int F, bool NT>
 __global__ __launch_bounds__(kDownWaves * 64) void decode_down_kernel(DecodeArgs a) {
   typedef typename Fmt<F>::act AT;
   extern __shared__ __align__(16) char smem[];
@@ -681,7 +681,7 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_kernel(DecodeArgs
       const bool on = p < total;  // uniform in the wave
       const int idx = on ? p / units : 0, unit = on ? p - idx * units : 0;
       const int e = __builtin_amdgcn_readfirstlane(active[idx]);
-      load_rows(wv[i], buffer_of((const char*)a.w_down + e * wbytes, wbytes), wrow, unit * 128, on ? abytes : 0);
+      load_rows<NT>(wv[i], buffer_of((const char*)a.w_down + e * wbytes, wbytes), wrow, unit * 128, on ? abytes : 0);
       uint32_t xr[2];
       bool live[2];
 #pragma unroll
@@ -841,7 +841,7 @@ struct DownTile {
   int row4, n0;
 };
 
-template <int F, int NB, int UN>
+template <int F, bool NT, int NB, int UN>
 __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, const DownTile& t,
                                           lds_t* lw) {
   typedef typename Fmt<F>::act AT;
@@ -870,7 +870,7 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
     float sb[UN];
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
-      load_rows(wv[i], t.w, t.row, (base + i) * 128, abytes);
+      load_rows<NT>(wv[i], t.w, t.row, (base + i) * 128, abytes);
       sb[i] = block_scale_of<F>(t.sc, t.n0, K, base + i);
     }
     const uint32_t mx = mx_words<F>(t.sc, t.row4, K, base + (lane & 3));
@@ -907,7 +907,7 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
   }
 }
 
-template <int F>
+template <int F, bool NT>
 __global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(DecodeArgs a) {
   static_assert(kDownRowWaves * 64 >= kDecodeMaxT, "Finder takes a thread per token");
   __shared__ Rows rows;
@@ -935,9 +935,9 @@ __global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(De
   constexpr int NBMAX = kMaxBlocks<F>, UN = F >= WF_FP8 ? 2 : 4;
   for (int r0 = 0; r0 < n; r0 += 16 * NBMAX) {
     const int left = n - r0;
-    if (left <= 16) down_rows<F, 1, UN>(a, rows, r0, n, t, lw);
-    else if (NBMAX == 2 || left <= 32) down_rows<F, 2, UN>(a, rows, r0, n, t, lw);
-    else down_rows<F, NBMAX, UN>(a, rows, r0, n, t, lw);
+    if (left <= 16) down_rows<F, NT, 1, UN>(a, rows, r0, n, t, lw);
+    else if (NBMAX == 2 || left <= 32) down_rows<F, NT, 2, UN>(a, rows, r0, n, t, lw);
+    else down_rows<F, NT, NBMAX, UN>(a, rows, r0, n, t, lw);
   }
 }
 
@@ -971,38 +971,64 @@ __global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a) {
 int work_items(const DecodeArgs& a) { return a.T * a.k > a.E ? a.E : a.T * a.k; }
 int64_t gu_groups(const DecodeArgs& a) { return cdiv(a.I, 16) * work_items(a); }
 
+// Whether the weights that the tokens may select exceed the last-level cache.
+// Nothing of them is left there for the next call then, and non-temporal loads
+// keep them from displacing what this call reads again (64 tokens of 8 of 128
+// experts above: 221 us without, 204 with; 8 experts of the same size for 256
+// tokens, 75 MB read twice: 55 and 64).
+template <int F>
+bool past_cache(const DecodeArgs& a) {
+  constexpr int64_t kLastLevelCache = int64_t(256) << 20;
+  const int64_t value = F >= WF_FP8 ? 1 : sizeof(typename Fmt<F>::act);
+  return work_items(a) * int64_t(3) * a.I * a.d * value > kLastLevelCache;
+}
+
 template <int F>
 hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
   const unsigned items = (unsigned)work_items(a);
   const dim3 gu((unsigned)cdiv(a.I, 16), items);
   constexpr int UN = F >= WF_FP8 ? 2 : 4;
-  if (a.T > 16)
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, kMaxBlocks<F>, 4, 2>), gu, dim3(4 * 64), 0, a);
+  if (a.T > 16 && past_cache<F>(a))
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, true, kMaxBlocks<F>, 4, 2>), gu, dim3(4 * 64), 0, a);
+  else if (a.T > 16)
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, false, kMaxBlocks<F>, 4, 2>), gu, dim3(4 * 64), 0, a);
   // As many work-groups as fit beside each other, two per CU: eight waves each,
   // so that all bytes are in flight at once (T = 1 above, 384 work-groups: 24.7
   // us with eight, 26.3 with four).  More: four, of which more fit (T = 2, 768:
   // 38.7 us with eight, 36.1 with four; 16 tokens of 8 of 64 experts, d = 4096,
   // I = 1024, e4m3: 150 and 139).
   else if (gu_groups(a) <= 512 && a.route_inline)
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 8, UN, true>), gu, dim3(8 * 64), 0, a);
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, false, 1, 8, UN, true>), gu, dim3(8 * 64), 0, a);
   else if (gu_groups(a) <= 512)
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 8, UN>), gu, dim3(8 * 64), 0, a);
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, false, 1, 8, UN>), gu, dim3(8 * 64), 0, a);
   else if (a.route_inline)
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 4, UN, true>), gu, dim3(4 * 64), 0, a);
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, false, 1, 4, UN, true>), gu, dim3(4 * 64), 0, a);
+  else if (past_cache<F>(a))
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, true, 1, 4, UN>), gu, dim3(4 * 64), 0, a);
   else
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, 1, 4, UN>), gu, dim3(4 * 64), 0, a);
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, false, 1, 4, UN>), gu, dim3(4 * 64), 0, a);
   if (small_down(a)) {
     MOE_LAUNCH(c, "decode_down", decode_down_small_kernel<F>, dim3((unsigned)(a.d / 8)), dim3(kDownWaves * 64), 0, a);
     return hipSuccess;
   }
   if (decode_one_down(a.T, a.k, a.d)) {
     const size_t smem = down_work<F>() + (size_t)a.E * 4 + (size_t)a.E * a.T * 2;
-    HIP_RET(tile::allow_smem_once<decode_down_kernel<F>>(down_work<F>() + kMaxExperts * (4 + 16 * 2)));
-    MOE_LAUNCH(c, "decode_down", decode_down_kernel<F>, dim3((unsigned)cdiv(a.d, 16)), dim3(kDownWaves * 64), smem, a);
+    constexpr size_t most = down_work<F>() + kMaxExperts * (4 + 16 * 2);
+    const dim3 grid((unsigned)cdiv(a.d, 16));
+    if (past_cache<F>(a)) {
+      HIP_RET(tile::allow_smem_once<decode_down_kernel<F, true>>(most));
+      MOE_LAUNCH(c, "decode_down", (decode_down_kernel<F, true>), grid, dim3(kDownWaves * 64), smem, a);
+    } else {
+      HIP_RET(tile::allow_smem_once<decode_down_kernel<F, false>>(most));
+      MOE_LAUNCH(c, "decode_down", (decode_down_kernel<F, false>), grid, dim3(kDownWaves * 64), smem, a);
+    }
     return hipSuccess;
   }
-  MOE_LAUNCH(c, "decode_down", decode_down_rows_kernel<F>, dim3((unsigned)cdiv(a.d, 16 * kDownRowWaves), items),
-             dim3(kDownRowWaves * 64), 0, a);
+  const dim3 dr((unsigned)cdiv(a.d, 16 * kDownRowWaves), items);
+  if (past_cache<F>(a))
+    MOE_LAUNCH(c, "decode_down", (decode_down_rows_kernel<F, true>), dr, dim3(kDownRowWaves * 64), 0, a);
+  else
+    MOE_LAUNCH(c, "decode_down", (decode_down_rows_kernel<F, false>), dr, dim3(kDownRowWaves * 64), 0, a);
   const dim3 cg((unsigned)cdiv(a.d, 1024), (unsigned)a.T);
   if constexpr (F == WF_F32) MOE_LAUNCH(c, "decode_combine", decode_combine_kernel<float>, cg, dim3(256), 0, a);
   else MOE_LAUNCH(c, "decode_combine", decode_combine_kernel<bf16_t>, cg, dim3(256), 0, a);

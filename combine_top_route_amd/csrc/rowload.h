@@ -20,8 +20,10 @@ typedef __amdgpu_buffer_rsrc_t rsrc_t;
 __device__ __forceinline__ rsrc_t buffer_of(const void* p, uint64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)(uint32_t)bytes, 0x00020000);
 }
+// NT: non-temporal, for data that no later load finds in the caches.
+template <bool NT = false>
 __device__ __forceinline__ u32x4_t load16(rsrc_t r, uint32_t off, bool ok) {
-  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)(ok ? off : kPast), 0, 0);
+  return __builtin_amdgcn_raw_buffer_load_b128(r, (int)(ok ? off : kPast), 0, NT ? 2 : 0);
 }
 
 // An MFMA wants neighbouring lanes to hold neighbouring rows, but a load whose
@@ -40,12 +42,12 @@ __device__ __forceinline__ int row_chunk(int row, int chunk) { return row * 128 
 __device__ __forceinline__ int load_row(int half) { return half * 8 + (int)((threadIdx.x & 63) >> 3); }
 
 // 128 bytes at byte `at` of rows at offsets row[0], row[1] (this lane's two
-// rows), of which `bytes` exist; rows with live[h] false read as zeros.
-__device__ __forceinline__ void load_rows(u32x4_t (&v)[2], rsrc_t r, const uint32_t (&row)[2], int at, int bytes,
-                                          bool live0 = true, bool live1 = true) {
+// rows), of which `bytes` exist.
+template <bool NT = false>
+__device__ __forceinline__ void load_rows(u32x4_t (&v)[2], rsrc_t r, const uint32_t (&row)[2], int at, int bytes) {
   const int off = at + (int)(threadIdx.x & 7) * 16;
-  v[0] = load16(r, row[0] + off, live0 && off < bytes);
-  v[1] = load16(r, row[1] + off, live1 && off < bytes);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) v[h] = load16<NT>(r, row[h] + off, off < bytes);
 }
 
 // Keeps the compiler from moving this lane's LDS accesses past each other: the

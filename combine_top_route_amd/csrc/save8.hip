@@ -44,7 +44,17 @@ __device__ __forceinline__ void load8(float (&f)[8], const T* p) {
   }
 }
 
-template <typename T>
+// NT: non-temporal stores, where a launch writes more than the last-level cache
+// holds (131072 rows of I = 768 in bf16: forward 142 us without, 134 with;
+// backward 176 and 168); a smaller result is left there for its reader.
+template <bool NT, typename V>
+__device__ __forceinline__ void put(V v, V* p) {
+  if constexpr (NT) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+constexpr int64_t kLastLevelCache = int64_t(256) << 20;
+
+template <bool NT, typename T>
 __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -52,13 +62,13 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
       u32x4_t v;
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = __float_as_uint(f[4 * h + i]);
-      *(u32x4_t*)(p + 4 * h) = v;
+      put<NT>(v, (u32x4_t*)(p + 4 * h));
     }
   } else {
     u32x4_t v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-    *(u32x4_t*)p = v;
+    put<NT>(v, (u32x4_t*)p);
   }
 }
 
@@ -76,7 +86,7 @@ __device__ __forceinline__ void decode8(float (&f)[8], u32x2_t q, uint32_t byte)
   }
 }
 
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(256) void save8_kernel(const T* __restrict__ H, const float* __restrict__ topk_w,
                                                     const int32_t* __restrict__ src_of, int R, int I, float lim,
                                                     T* __restrict__ aw, uint8_t* __restrict__ codes,
@@ -99,8 +109,8 @@ __global__ __launch_bounds__(256) void save8_kernel(const T* __restrict__ H, con
     uint32_t bg, bu;
     const u32x2_t qg = encode8(g, &bg), qu = encode8(u, &bu);
     if (in) {
-      *(u32x2_t*)(cr + c * 8) = qg;
-      *(u32x2_t*)(cr + I + c * 8) = qu;
+      put<NT>(qg, (u32x2_t*)(cr + c * 8));
+      put<NT>(qu, (u32x2_t*)(cr + I + c * 8));
       if (aw) {
         float a[8];
 #pragma unroll
@@ -108,7 +118,7 @@ __global__ __launch_bounds__(256) void save8_kernel(const T* __restrict__ H, con
           const float gc = clip_gate(g[i], lim);
           a[i] = wr * (gc * sigmoidf_(gc) * clip_up(u[i], lim));
         }
-        store8(aw + (int64_t)r * I + c * 8, a);
+        store8<NT>(aw + (int64_t)r * I + c * 8, a);
       }
     }
     if ((c & 3) == 0) {
@@ -118,7 +128,7 @@ __global__ __launch_bounds__(256) void save8_kernel(const T* __restrict__ H, con
   }
 }
 
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(256) void swiglu_bwd8_kernel(const T* __restrict__ G, const uint8_t* __restrict__ codes,
                                                           const uint8_t* __restrict__ scales,
                                                           const float* __restrict__ topk_w,
@@ -151,9 +161,9 @@ __global__ __launch_bounds__(256) void swiglu_bwd8_kernel(const T* __restrict__ 
       dg[i] = g[i] > lim ? 0.0f : dA * uc * s * (1.0f + gc * (1.0f - s));
       du[i] = fabsf(u[i]) > lim ? 0.0f : dA * gc * s;
     }
-    store8(dr + c * 8, dg);
-    store8(dr + I + c * 8, du);
-    if (aw) store8(aw + (int64_t)r * I + c * 8, a);
+    store8<NT>(dr + c * 8, dg);
+    store8<NT>(dr + I + c * 8, du);
+    if (aw) store8<NT>(aw + (int64_t)r * I + c * 8, a);
   }
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) part += __shfl_xor(part, off, kWave);
@@ -162,29 +172,41 @@ __global__ __launch_bounds__(256) void swiglu_bwd8_kernel(const T* __restrict__ 
 
 }  // namespace
 
+namespace {
+template <typename T, bool NT>
+hipError_t save(const LaunchCtx& c, const void* H, const float* topk_w, const int32_t* src_of, int R, int I, float lim,
+                void* aw, uint8_t* codes, uint8_t* scales) {
+  MOE_LAUNCH(c, "swiglu_save8", (save8_kernel<T, NT>), dim3((unsigned)cdiv(R, 4)), dim3(256), 0, (const T*)H, topk_w,
+             src_of, R, I, lim, (T*)aw, codes, scales);
+  return hipSuccess;
+}
+template <typename T, bool NT>
+hipError_t backward(const LaunchCtx& c, const void* G, const uint8_t* codes, const uint8_t* scales,
+                    const float* topk_w, const int32_t* src_of, int R, int I, float lim, void* dH, void* aw,
+                    float* dw) {
+  MOE_LAUNCH(c, "swiglu_bwd8", (swiglu_bwd8_kernel<T, NT>), dim3((unsigned)cdiv(R, 4)), dim3(256), 0, (const T*)G,
+             codes, scales, topk_w, src_of, R, I, lim, (T*)dH, (T*)aw, dw);
+  return hipSuccess;
+}
+}  // namespace
+
 hipError_t launch_save8(const LaunchCtx& c, int dtype, const void* H, const float* topk_w, const int32_t* src_of,
                         int R, int I, float lim, void* aw, uint8_t* codes, uint8_t* scales) {
-  const dim3 grid((unsigned)cdiv(R, 4));
-  if (dtype == F32)
-    MOE_LAUNCH(c, "swiglu_save8", save8_kernel<float>, grid, dim3(256), 0, (const float*)H, topk_w, src_of, R, I, lim,
-               (float*)aw, codes, scales);
-  else
-    MOE_LAUNCH(c, "swiglu_save8", save8_kernel<bf16_t>, grid, dim3(256), 0, (const bf16_t*)H, topk_w, src_of, R, I,
-               lim, (bf16_t*)aw, codes, scales);
-  return hipSuccess;
+  const int es = dtype == F32 ? 4 : 2;
+  const bool nt = (int64_t)R * I * (2 + (aw ? es : 0)) > kLastLevelCache;
+  const auto run = dtype == F32 ? (nt ? save<float, true> : save<float, false>)
+                                : (nt ? save<bf16_t, true> : save<bf16_t, false>);
+  return run(c, H, topk_w, src_of, R, I, lim, aw, codes, scales);
 }
 
 hipError_t launch_swiglu_bwd8(const LaunchCtx& c, int dtype, const void* G, const uint8_t* codes,
                               const uint8_t* scales, const float* topk_w, const int32_t* src_of, int R, int I,
                               float lim, void* dH, void* aw, float* dw) {
-  const dim3 grid((unsigned)cdiv(R, 4));
-  if (dtype == F32)
-    MOE_LAUNCH(c, "swiglu_bwd8", swiglu_bwd8_kernel<float>, grid, dim3(256), 0, (const float*)G, codes, scales,
-               topk_w, src_of, R, I, lim, (float*)dH, (float*)aw, dw);
-  else
-    MOE_LAUNCH(c, "swiglu_bwd8", swiglu_bwd8_kernel<bf16_t>, grid, dim3(256), 0, (const bf16_t*)G, codes, scales,
-               topk_w, src_of, R, I, lim, (bf16_t*)dH, (bf16_t*)aw, dw);
-  return hipSuccess;
+  const int es = dtype == F32 ? 4 : 2;
+  const bool nt = (int64_t)R * I * (aw ? 3 : 2) * es > kLastLevelCache;
+  const auto run = dtype == F32 ? (nt ? backward<float, true> : backward<float, false>)
+                                : (nt ? backward<bf16_t, true> : backward<bf16_t, false>);
+  return run(c, G, codes, scales, topk_w, src_of, R, I, lim, dH, aw, dw);
 }
 
 }  // namespace moe

@@ -161,6 +161,28 @@ def test_ids_form_with_empty_slots_and_repeats(T, d, E, k, I, dtype, weights):
     assert dec.topk_ids is ids and dec.topk_w is w
 
 
+# weights beyond the last-level cache (256 MiB) take the kernels' non-temporal
+# loads: more than 16 tokens, 9 to 16, and 9 to 16 at a d that fills the chip
+@pytest.mark.parametrize("T,d,E,k,I,dtype,weights", [
+    (20, 1024, 48, 3, 1024, "bf16", "native"), (40, 1024, 24, 2, 1032, "f32", "native"),
+    (24, 1024, 96, 5, 1024, "bf16", "fp8_block"), (130, 1024, 96, 2, 1024, "bf16", "mxfp8"),
+    (12, 1032, 48, 6, 1024, "bf16", "native"), (9, 1024, 30, 8, 1024, "f32", "native"),
+    (10, 4096, 16, 8, 1024, "bf16", "native"), (16, 4096, 8, 5, 1024, "f32", "native"),
+    (13, 4096, 24, 6, 1024, "bf16", "fp8_block"), (9, 4096, 24, 8, 1024, "bf16", "mxfp8"),
+])
+def test_weights_past_the_cache(T, d, E, k, I, dtype, weights):
+    x, wgu, wd, logits = make(T, d, E, k, I, dtype, weights, seed=3)
+    dec = decoder(x, E, k, I, weights)
+    got = dec.forward(x, wgu, wd, logits=logits)
+    ids, w = topk64(logits, k)
+    assert torch.equal(dec.topk_ids.long(), ids)
+    used = torch.unique(ids).tolist()                       # the plain form on the experts in use
+    remap = torch.full((E,), -1, device=DEV)
+    remap[used] = torch.arange(len(used), device=DEV)
+    cut = lambda m: m[used] if isinstance(m, torch.Tensor) else tuple(t[used] for t in m)
+    check(got, x, cut(wgu), cut(wd), remap[ids], w)
+
+
 def test_masked_logits():
     """-inf logits are empty slots: none left, fewer left than k, ties."""
     T, d, E, k, I = 6, 64, 8, 4, 32

@@ -120,6 +120,28 @@ def test_save8_rows(T, k, E, I, dtype):
         assert only[0] is None and torch.equal(only[1], codes) and torch.equal(only[2], scales)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_past_the_cache(dtype):
+    """More than 256 MiB written (non-temporal stores): the same results, bit
+    for bit, as the same rows in pieces below that."""
+    k, I, dt = 1, 1000, DT[dtype]
+    T = 150000 if dtype == "bf16" else 70000
+    r = routing(T, k, 2)
+    H = torch.randn((T, 2 * I), generator=gen(12), device=DEV).to(dt)
+    G = torch.randn((T, I), generator=gen(13), device=DEV).to(dt)
+    aw, codes, scales = B.swiglu_save8(H, r, T, k)
+    back = B.swiglu_backward8(G, codes, scales, r, T, k)
+    w = r.topk_w.view(-1)[r.src_of.long()]
+    for lo in range(0, T, T // 10):
+        s = slice(lo, lo + T // 10)
+        n = T // 10
+        part = B.Routing(r.topk_ids[s], w[s].view(n, 1).contiguous(), r.counts, r.offsets, r.row_of[:n],
+                         torch.arange(n, dtype=torch.int32, device=DEV))
+        p = B.swiglu_save8(H[s], part, n, k)
+        assert all(torch.equal(a[s], b) for a, b in zip((aw, codes, scales), p))
+        assert all(torch.equal(a[s], b) for a, b in zip(back, B.swiglu_backward8(G[s], *p[1:], part, n, k)))
+
+
 def test_save8_codes_are_the_mxfp8_row_encoding():
     T, k, I = 40, 2, 128
     H = test_matrix(T * k, I, torch.bfloat16, seed=3)
