@@ -241,7 +241,7 @@ struct RouterArgs {
   int64_t run_tokens;
   int runs;
   // set by the launcher
-  int d_blocks, e_blocks, dw_groups, lay_groups, dx_eblocks, dx_blocks, dx_tokens, dx_groups;
+  int d_blocks, e_blocks, dw_groups, dx_eblocks, dx_blocks, dx_tokens, dx_groups;
 };
 hipError_t launch_router_fwd(const LaunchCtx& c, const RouterArgs& a, void* logits);
 hipError_t launch_router_bwd(const LaunchCtx& c, RouterArgs a);

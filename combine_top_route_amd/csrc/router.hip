@@ -188,15 +188,26 @@ hipError_t fwd_any(const LaunchCtx& c, const RouterArgs& a, void* logits) {
 // staging and barriers run beside the other's products: 31 us at the size
 // above; one work-group with 64-token steps took 35.  Parts are float32
 // [run][E][d].
-// The first work-groups lay w out as the second launch's MFMA operands.
+// Each work-group then lays a piece of w out as the second launch's MFMA
+// operands (in work-groups of their own that took 2 us more: the others fill
+// the chip).
 constexpr int kDwE = 128, kDwD = 128;
 
 template <typename T> struct DwTile;
+// `at` is the place of byte b of row r.  16-bit: a transposing read's first 32
+// lanes take 32 bytes each of rows r .. r + 3 and r + 8 .. r + 11, so the row's
+// 32-byte chunks are XORed with a number that differs between those eight and
+// the lanes meet all 64 banks once.  Float32: row r starts at bank 16 r, for
+// reads of 16 columns of four rows.
 template <> struct DwTile<bf16_t> {
-  static constexpr int TS = 32, STRIDE = 288;  // bytes a row: 256 + 32 (row r starts at bank 8 r)
+  static constexpr int TS = 32, STRIDE = 256;
+  static __device__ __forceinline__ int at(int r, int b) {
+    return r * STRIDE + (b ^ (((r & 3) | ((r >> 1) & 4)) << 5));
+  }
 };
 template <> struct DwTile<float> {
-  static constexpr int TS = 32, STRIDE = 576;  // 512 + 64 (16 r)
+  static constexpr int TS = 32, STRIDE = 576;
+  static __device__ __forceinline__ int at(int r, int b) { return r * STRIDE + b; }
 };
 
 __device__ __forceinline__ void split_bf16(float v, bf16_t& hi, bf16_t& lo) {
@@ -222,9 +233,9 @@ __device__ __forceinline__ void unpack16(float* f, u32x4_t v) {
 
 // A tile of dlogits, rows t0 .. t0 + ROWS (of which `rows` exist) by experts
 // e0 .. e0 + 128, loaded by NT threads 16 bytes each (neighbours contiguous)
-// and stored for the MFMAs: float32 [row][ST], or the two bf16 parts in hs and
-// ls.  Rows and experts that do not exist become zeros.
-template <typename T, typename LT, int ROWS, int NT, int ST>
+// and stored for the MFMAs at Place::at(row, byte): float32, or the two bf16
+// parts in hs and ls.  Rows and experts that do not exist become zeros.
+template <typename T, typename LT, int ROWS, int NT, class Place>
 struct DlTile {
   static constexpr int PER = 16 / (int)sizeof(LT);       // values per load
   static constexpr int UPR = 128 / PER;                  // loads per row
@@ -232,23 +243,26 @@ struct DlTile {
   static constexpr bool LO = sizeof(T) == 2 && sizeof(LT) == 4;
   u32x4_t v[N];
   __device__ __forceinline__ void load(const LT* p, int E, int e0, int rows, bool vec) {
+    if (vec) {  // E is a multiple of PER and the rows are aligned
+      const rsrc_t b = buffer_of(p, (uint64_t)min(rows, ROWS) * E * sizeof(LT));
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int u = (int)threadIdx.x + i * NT, e = e0 + (u % UPR) * PER;
+        v[i] = load16(b, (uint32_t)((u / UPR * E + e) * (int)sizeof(LT)), e < E);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int u = (int)threadIdx.x + i * NT, r = u / UPR, e = e0 + (u % UPR) * PER;
       v[i] = u32x4_t{0, 0, 0, 0};
-      if (r < rows && e < E) {
-        const LT* a = p + (int64_t)r * E + e;
-        if (vec) {  // E is a multiple of PER and the rows are aligned
-          v[i] = *(const u32x4_t*)a;
-        } else {
+      const LT* a = p + (int64_t)r * E + e;
 #pragma unroll
-          for (int j = 0; j < PER; ++j)
-            if (e + j < E) {
-              if constexpr (sizeof(LT) == 4) v[i][j] = __float_as_uint(a[j]);
-              else v[i][j >> 1] |= (uint32_t)a[j] << (16 * (j & 1));
-            }
+      for (int j = 0; j < PER; ++j)
+        if (r < rows && e + j < E) {
+          if constexpr (sizeof(LT) == 4) v[i][j] = __float_as_uint(a[j]);
+          else v[i][j >> 1] |= (uint32_t)a[j] << (16 * (j & 1));
         }
-      }
     }
   }
   __device__ __forceinline__ void store(char* hs, char* ls) const {
@@ -260,9 +274,9 @@ struct DlTile {
         unpack16<LT>(f, v[i]);
 #pragma unroll
         for (int j = 0; j < PER; j += 4)
-          *(f32x4_t*)(hs + r * ST + (c + j) * 4) = f32x4_t{f[j], f[j + 1], f[j + 2], f[j + 3]};
+          *(f32x4_t*)(hs + Place::at(r, (c + j) * 4)) = f32x4_t{f[j], f[j + 1], f[j + 2], f[j + 3]};
       } else if constexpr (!LO) {
-        *(u32x4_t*)(hs + r * ST + c * 2) = v[i];
+        *(u32x4_t*)(hs + Place::at(r, c * 2)) = v[i];
       } else {
         uint2 h, l;
         bf16_t a[4], b[4];
@@ -272,8 +286,8 @@ struct DlTile {
         h.y = (uint32_t)a[2] | ((uint32_t)a[3] << 16);
         l.x = (uint32_t)b[0] | ((uint32_t)b[1] << 16);
         l.y = (uint32_t)b[2] | ((uint32_t)b[3] << 16);
-        *(uint2*)(hs + r * ST + c * 2) = h;
-        *(uint2*)(ls + r * ST + c * 2) = l;
+        *(uint2*)(hs + Place::at(r, c * 2)) = h;
+        *(uint2*)(ls + Place::at(r, c * 2)) = l;
       }
     }
   }
@@ -300,16 +314,15 @@ __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb,
   const LT* lp = (const LT*)a.dlogits + tb * a.E;
   const bool vec = dl_vec<T, LT>(a);
   u32x4_t xr[2][XV];
-  DlTile<T, LT, TS, 512, ST> dlr[2];
+  DlTile<T, LT, TS, 512, DwTile<T>> dlr[2];
   auto fetch = [&](auto set, int s) {  // tokens s .. s + TS of the run; zeros past its end and past E and d
     auto& xv = xr[set.value];
     auto& dl = dlr[set.value];
+    const rsrc_t xb = buffer_of(xp + (int64_t)s * a.d, (uint64_t)min(tn - s, TS) * xrow);
 #pragma unroll
     for (int i = 0; i < XV; ++i) {
-      const int u = (int)threadIdx.x + i * 512, r = u / XU, cb = (u % XU) * 16;
-      xv[i] = u32x4_t{0, 0, 0, 0};
-      if (s + r < tn && d0 * (int)sizeof(T) + cb < xrow)
-        xv[i] = *(const u32x4_t*)((const char*)(xp + (int64_t)(s + r) * a.d + d0) + cb);
+      const int u = (int)threadIdx.x + i * 512, at = d0 * (int)sizeof(T) + (u % XU) * 16;
+      xv[i] = load16(xb, (uint32_t)(u / XU * xrow + at), at < xrow);
     }
     dl.load(lp + (int64_t)s * a.E, a.E, e0, tn - s, vec);
   };
@@ -319,7 +332,7 @@ __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb,
 #pragma unroll
     for (int i = 0; i < XV; ++i) {
       const int u = (int)threadIdx.x + i * 512, r = u / XU, cb = (u % XU) * 16;
-      *(u32x4_t*)(b + r * ST + cb) = xv[i];
+      *(u32x4_t*)(b + DwTile<T>::at(r, cb)) = xv[i];
     }
     dl.store(b + TS * ST, b + 2 * TS * ST);
   };
@@ -341,15 +354,19 @@ __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb,
     const char* xs = smem + set.value * dw_stage<T, LT>();
     const char* hs = xs + TS * ST;
     const char* ls = hs + TS * ST;
+    if (s + TS < tn) {
+      stage(next, smem + next.value * dw_stage<T, LT>());
+      if (s + 3 * TS < tn) fetch(next, s + 3 * TS);
+    }
     if (busy) {
       if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int k = 0; k < TS; k += 4) {
           float av[4], bv[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) av[i] = *(const float*)(hs + (k + q) * ST + (we + i * 16 + col) * 4);
+          for (int i = 0; i < 4; ++i) av[i] = *(const float*)(hs + DwTile<T>::at(k + q, (we + i * 16 + col) * 4));
 #pragma unroll
-          for (int j = 0; j < 2; ++j) bv[j] = *(const float*)(xs + (k + q) * ST + (wd + j * 16 + col) * 4);
+          for (int j = 0; j < 2; ++j) bv[j] = *(const float*)(xs + DwTile<T>::at(k + q, (wd + j * 16 + col) * 4));
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -360,10 +377,10 @@ __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb,
         // eight tokens 8 q .. of column `col`: the 16 lanes of a group read 4
         // tokens by 16 columns and get them transposed
         auto frag = [&](const char* base, int c0) {
-          const char* p = base + (q * 8 + (col >> 2)) * ST + (c0 + 4 * (col & 3)) * 2;
-          const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
-          const s16x4_t hi =
-              __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(p + 4 * ST));
+          typedef __attribute__((address_space(3))) s16x4_t* lds_p;
+          const int r = q * 8 + (col >> 2), b = (c0 + 4 * (col & 3)) * 2;
+          const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(base + DwTile<T>::at(r, b)));
+          const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(base + DwTile<T>::at(r + 4, b)));
           return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         };
         static_assert(TS == 32, "a step is one MFMA's K");
@@ -383,10 +400,6 @@ __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb,
           }
         }
       }
-    }
-    if (s + TS < tn) {
-      stage(next, smem + next.value * dw_stage<T, LT>());
-      if (s + 3 * TS < tn) fetch(next, s + 3 * TS);
     }
   };
   for (int s = 0; s < tn; s += 2 * TS) {
@@ -416,12 +429,16 @@ constexpr int kDxE = 128;
 template <typename T> constexpr int dx_steps = kDxE * (int)sizeof(T) / 64;
 
 template <typename T>
-__device__ __forceinline__ void lay_out_w(const RouterArgs& a, int cb, int eb) {
+__device__ __forceinline__ void lay_out_w(const RouterArgs& a, int group, int groups) {
   constexpr int DT = dx_tiles<T>, NK = dx_steps<T>, PER = 16 / (int)sizeof(T);
-  T* out = (T*)a.wf + ((int64_t)cb * a.dx_eblocks + eb) * DT * NK * 64 * PER;
-  // neighbouring threads read neighbouring columns of w
-  for (int i = threadIdx.x; i < DT * NK * 64; i += 512) {
+  const int lane = threadIdx.x & 63, wave = tile::wave_id();
+  // 64 operands a wave, neighbouring lanes reading neighbouring columns of w
+  const int64_t chunks = (int64_t)((a.d + 16 * DT - 1) / (16 * DT)) * a.dx_eblocks * DT * NK;
+  for (int64_t ck = group + (int64_t)wave * groups; ck < chunks; ck += (int64_t)8 * groups) {
+    const int64_t blk = ck / (DT * NK);  // [column block][expert block]
+    const int i = (int)(ck % (DT * NK)) * 64 + lane;
     const int j = i % DT, col = i / DT % 16, q = i / (16 * DT) % 4, k = i / (64 * DT);
+    const int cb = (int)(blk / a.dx_eblocks), eb = (int)(blk % a.dx_eblocks);
     const int c = cb * 16 * DT + DT * col + j;
     T v[PER];
 #pragma unroll
@@ -429,22 +446,18 @@ __device__ __forceinline__ void lay_out_w(const RouterArgs& a, int cb, int eb) {
       const int e = eb * kDxE + k * 4 * PER + q * PER + m;
       v[m] = e < a.E && c < a.d ? ((const T*)a.w)[(int64_t)e * a.d + c] : (T)0;
     }
-    *(u32x4_t*)(out + ((int64_t)(j * NK + k) * 64 + q * 16 + col) * PER) = *(const u32x4_t*)v;
+    *(u32x4_t*)((T*)a.wf + ((blk * DT + j) * NK + k) * 64 * PER + (q * 16 + col) * PER) = *(const u32x4_t*)v;
   }
 }
 
 template <typename T, typename LT>
 __global__ __launch_bounds__(512, 4) void router_dw_kernel(RouterArgs a) {
   extern __shared__ __align__(16) char smem[];
-  int b = (int)blockIdx.x - a.lay_groups;
-  if (b < 0) {  // first, or they would wait for a place beside the others
-    b += a.lay_groups;
-    lay_out_w<T>(a, b / a.dx_eblocks, b % a.dx_eblocks);
-  } else {
-    const int db = b % a.d_blocks;
-    b /= a.d_blocks;
-    dw_part<T, LT>(a, smem, b % a.e_blocks, db, b / a.e_blocks);
-  }
+  int b = blockIdx.x;
+  const int db = b % a.d_blocks;
+  b /= a.d_blocks;
+  dw_part<T, LT>(a, smem, b % a.e_blocks, db, b / a.e_blocks);
+  lay_out_w<T>(a, blockIdx.x, a.dw_groups);
 }
 
 // ------------------------------------------------ backward, second launch
@@ -453,6 +466,9 @@ __global__ __launch_bounds__(512, 4) void router_dw_kernel(RouterArgs a) {
 // through LDS once for all four.
 constexpr int kDxWaves = 4, kDxTok = 32;
 template <typename T> constexpr int dx_stride = 128 * (int)sizeof(T) + 16;  // bytes per token row in LDS
+template <typename T> struct DxPlace {
+  static __device__ __forceinline__ int at(int r, int b) { return r * dx_stride<T> + b; }
+};
 
 // MULTI: more than 128 experts; w's operands then pass through the registers a
 // step at a time, for all 32 tokens, instead of staying in them.
@@ -477,7 +493,7 @@ __device__ __forceinline__ void dx_part(const RouterArgs& a, char* smem, int cb,
       for (int k = 0; k < NK; ++k) wv[j][MULTI ? 0 : k] = *(const u32x4_t*)(wp + (j * NK + k) * 64 * PER);
   }
   const int64_t tb = (int64_t)run * a.dx_tokens, te = tb + a.dx_tokens < a.T ? tb + a.dx_tokens : a.T;
-  DlTile<T, LT, kDxTok, kDxWaves * 64, ST> dl;
+  DlTile<T, LT, kDxTok, kDxWaves * 64, DxPlace<T>> dl;
   auto fetch = [&](int64_t t, int eb) {
     dl.load((const LT*)a.dlogits + t * a.E, a.E, eb * kDxE, (int)(te - t < kDxTok ? te - t : kDxTok), vec);
   };
@@ -607,8 +623,7 @@ template <typename T, typename LT>
 hipError_t bwd(const LaunchCtx& c, const RouterArgs& a) {
   constexpr size_t smem = 2 * dw_stage<T, LT>();
   HIP_RET(tile::allow_smem_once<router_dw_kernel<T, LT>>(smem));
-  MOE_LAUNCH(c, "router_dw", (router_dw_kernel<T, LT>), dim3((unsigned)(a.dw_groups + a.lay_groups)), dim3(512), smem,
-             a);
+  MOE_LAUNCH(c, "router_dw", (router_dw_kernel<T, LT>), dim3((unsigned)a.dw_groups), dim3(512), smem, a);
   const dim3 grid((unsigned)(a.dx_groups + cdiv((int64_t)a.E * a.d, kDxWaves * 256)));
   if (a.dx_eblocks > 1)
     MOE_LAUNCH(c, "router_dx", (router_dx_kernel<T, LT, true>), grid, dim3(kDxWaves * 64), 0, a);
@@ -642,7 +657,6 @@ hipError_t launch_router_bwd(const LaunchCtx& c, RouterArgs a) {
   a.e_blocks = (int)cdiv(a.E, kDwE);
   a.dw_groups = a.d_blocks * a.e_blocks * a.runs;
   a.dx_eblocks = (int)cdiv(a.E, kDxE);
-  a.lay_groups = (int)cdiv(a.d, 16 * (a.dtype == F32 ? dx_tiles<float> : dx_tiles<bf16_t>)) * a.dx_eblocks;
   a.dx_blocks = (int)cdiv(a.d, 16 * (a.dtype == F32 ? dx_tiles<float> : dx_tiles<bf16_t>) * kDxWaves);
   // two work-groups per CU (each first loads its part of w), in whole blocks
   const int64_t tok = cdiv(cdiv((int64_t)a.T * a.dx_blocks, 512), kDxTok) * kDxTok;
