@@ -436,53 +436,55 @@ struct Finder {
   }
 };
 
-// Token blocks of 16 that one pass over an expert's weights serves (the rest
-// take another pass, from the caches): as many as the registers hold beside
-// the weights in flight.
-template <int F> constexpr int kMaxBlocks = 2;
-
 // ------------------------------------------------------------ gate/up product
-// One work-group: 16 gate rows and the same 16 up rows of one expert, for all
-// of its tokens; the NW waves take batches of UN units of K in turn.
-template <int F, int UN>
+// One work-group: TB times 16 gate rows and the same up rows of one expert, for
+// all of its tokens, NBMAX blocks of 16 a pass; the NW waves take batches of UN units of K in turn.
+template <int F, int TB, int UN>
 struct GuWeights {  // UN units of the tile's gate and up rows, in flight
-  u32x4_t g[UN][2], u[UN][2];
-  uint32_t mg, mu;
-  float sg[UN], su[UN];  // blockwise scales
+  u32x4_t g[TB][UN][2], u[TB][UN][2];
+  uint32_t mg[TB], mu[TB];
+  float sg[UN], su[UN];  // blockwise scales (a tile lies in one block of rows)
 };
 
+template <int TB>
 struct GuTile {  // where a lane finds them
   rsrc_t w;
   const void* sc;
-  uint32_t g[2], u[2];  // offsets of this lane's two gate and up rows
-  int row4;             // row whose scale bytes it loads
+  uint32_t g[TB][2], u[TB][2];  // offsets of this lane's gate and up rows
+  int row4;                     // row whose scale bytes it loads, and 16 on
   int n0;
 };
 
-template <int F, bool NT, int UN>
-__device__ __forceinline__ void load_gu(GuWeights<F, UN>& w, const GuTile& t, int I, int K, int base) {
+template <int F, bool NT, int TB, int UN>
+__device__ __forceinline__ void load_gu(GuWeights<F, TB, UN>& w, const GuTile<TB>& t, int I, int K, int base) {
   const int bytes = F >= WF_FP8 ? K : K * (int)sizeof(typename Fmt<F>::act);
 #pragma unroll
   for (int i = 0; i < UN; ++i) {
-    load_rows<NT>(w.g[i], t.w, t.g, (base + i) * 128, bytes);
-    load_rows<NT>(w.u[i], t.w, t.u, (base + i) * 128, bytes);
+#pragma unroll
+    for (int b = 0; b < TB; ++b) {
+      load_rows<NT>(w.g[b][i], t.w, t.g[b], (base + i) * 128, bytes);
+      load_rows<NT>(w.u[b][i], t.w, t.u[b], (base + i) * 128, bytes);
+    }
     w.sg[i] = block_scale_of<F>(t.sc, t.n0, K, base + i);
     w.su[i] = block_scale_of<F>(t.sc, I + t.n0, K, base + i);
   }
-  w.mg = mx_words<F>(t.sc, t.row4, K, base + (int)(threadIdx.x & 3));
-  w.mu = mx_words<F>(t.sc, I + t.row4, K, base + (int)(threadIdx.x & 3));
+#pragma unroll
+  for (int b = 0; b < TB; ++b) {
+    w.mg[b] = mx_words<F>(t.sc, t.row4 + 16 * b, K, base + (int)(threadIdx.x & 3));
+    w.mu[b] = mx_words<F>(t.sc, I + t.row4 + 16 * b, K, base + (int)(threadIdx.x & 3));
+  }
 }
 
-template <int F, int NW, int NBMAX>
+template <int F, int NW, int TB, int NBMAX>
 constexpr size_t gu_smem() {  // per wave: gate, up, activations; then the waves' parts
-  const size_t work = (size_t)NW * (4096 + 2048 * kActHalves<F>), parts = (size_t)NW * NBMAX * 2048;
+  const size_t work = (size_t)NW * (4096 + 2048 * kActHalves<F>), parts = (size_t)NW * NBMAX * TB * 2048;
   return work > parts ? work : parts;
 }
 
 // The tokens r0 .. r0 + 16 NB of the expert.  w holds the first units.
-template <int F, bool NT, int NW, int UN, int NB>
+template <int F, bool NT, int NW, int TB, int UN, int NB>
 __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& rows, int r0, int n,
-                                            GuWeights<F, UN>& w, const GuTile& t, char* smem) {
+                                            GuWeights<F, TB, UN>& w, const GuTile<TB>& t, char* smem) {
   typedef typename Fmt<F>::act AT;
   const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
   const int K = a.d;
@@ -501,9 +503,11 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
       live[b][h] = r < n;
       xr[b][h] = (uint32_t)(rows.slot[live[b][h] ? r : n - 1] / a.k) * bytes;
     }
-  f32x4_t ag[NB], au[NB];
+  f32x4_t ag[NB][TB], au[NB][TB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) ag[b] = au[b] = f32x4_t{0, 0, 0, 0};
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int m = 0; m < TB; ++m) ag[b][m] = au[b][m] = f32x4_t{0, 0, 0, 0};
   constexpr int UB = NB == 1 ? UN : 1;  // units whose activations are in flight together
   for (int base = wave * UN; base < units; base += NW * UN) {
     if (base != wave * UN || r0) load_gu<F, NT>(w, t, a.I, K, base);
@@ -517,60 +521,70 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
       __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
 #pragma unroll
       for (int i = 0; i < UB; ++i) {
-        put_rows(lw, w.g[i0 + i]);
-        put_rows(lw + 2048, w.u[i0 + i]);
-        uint32_t mg = 0, mu = 0;
-        if constexpr (F == WF_MX) {
-          mg = (uint32_t)__shfl((int)w.mg, col * 4 + i0 + i, kWave);
-          mu = (uint32_t)__shfl((int)w.mu, col * 4 + i0 + i, kWave);
-        }
-        typename Fmt<F>::frag fg[Fmt<F>::NF], fu[Fmt<F>::NF];
-        to_frags<F>(fg, lw, mg, q, col);
-        to_frags<F>(fu, lw + 2048, mu, q, col);
+        u32x4_t xf[NB][Fmt<F>::BV];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          u32x4_t xf[Fmt<F>::BV];
-          put_acts<F>(lw + 4096, xv[i][b], eight);
-          get_acts<F>(xf, lw + 4096, q, col);
-          unit_mma<F>(ag[b], fg, xf, w.sg[i0 + i]);
-          unit_mma<F>(au[b], fu, xf, w.su[i0 + i]);
+        for (int m = 0; m < TB; ++m) {
+          put_rows(lw, w.g[m][i0 + i]);
+          put_rows(lw + 2048, w.u[m][i0 + i]);
+          uint32_t mg = 0, mu = 0;
+          if constexpr (F == WF_MX) {
+            mg = (uint32_t)__shfl((int)w.mg[m], col * 4 + i0 + i, kWave);
+            mu = (uint32_t)__shfl((int)w.mu[m], col * 4 + i0 + i, kWave);
+          }
+          typename Fmt<F>::frag fr[Fmt<F>::NF];
+          to_frags<F>(fr, lw, mg, q, col);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            if (m == 0) {
+              put_acts<F>(lw + 4096, xv[i][b], eight);
+              get_acts<F>(xf[b], lw + 4096, q, col);
+            }
+            unit_mma<F>(ag[b][m], fr, xf[b], w.sg[i0 + i]);
+          }
+          to_frags<F>(fr, lw + 2048, mu, q, col);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) unit_mma<F>(au[b][m], fr, xf[b], w.su[i0 + i]);
         }
       }
     }
   }
-  // parts [wave][2 b + gate/up][col][16 rows], over the waves' work space
+  // parts [wave][b][tile of 16 rows][gate, up][col][16 rows], over the waves'
+  // work space
   float* red = (float*)smem;
   __syncthreads();
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    float* p = red + ((wave * NB + b) * 2 * 16 + col) * 16 + q * 4;
-    *(f32x4_t*)p = ag[b];
-    *(f32x4_t*)(p + 256) = au[b];
-  }
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int m = 0; m < TB; ++m) {
+      float* p = red + (((wave * NB + b) * TB + m) * 2 * 16 + col) * 16 + q * 4;
+      *(f32x4_t*)p = ag[b][m];
+      *(f32x4_t*)(p + 256) = au[b][m];
+    }
   __syncthreads();
-  for (int o = threadIdx.x; o < NB * 256; o += NW * 64) {
-    const int b = o >> 8, c = (o >> 4) & 15, m = o & 15;
-    const int r = r0 + b * 16 + c;
-    if (r < n && t.n0 + m < a.I) {
+  for (int o = threadIdx.x; o < NB * TB * 256; o += NW * 64) {
+    // neighbouring threads: neighbouring rows of all TB tiles, then tokens
+    const int m = o & 15, tb = (o >> 4) % TB, c = o / (16 * TB) & 15, b = o / (256 * TB);
+    const int r = r0 + b * 16 + c, row = t.n0 + tb * 16 + m;
+    if (r < n && row < a.I) {
       float g = 0.0f, u = 0.0f;
 #pragma unroll
       for (int v = 0; v < NW; ++v) {
-        const float* p = red + ((v * NB + b) * 2 * 16 + c) * 16 + m;
+        const float* p = red + (((v * NB + b) * TB + tb) * 2 * 16 + c) * 16 + m;
         g += p[0];
         u += p[256];
       }
-      ((AT*)a.aw)[(int64_t)rows.slot[r] * a.I + t.n0 + m] = from_f32<AT>(rows.w[r] * swiglu(g, u, a.lim));
+      ((AT*)a.aw)[(int64_t)rows.slot[r] * a.I + row] = from_f32<AT>(rows.w[r] * swiglu(g, u, a.lim));
     }
   }
   __syncthreads();
 }
 
-template <int F, bool NT, int NBMAX, int NW, int UN, bool INLINE = false>
+template <int F, bool NT, int NBMAX, int NW, int TB, int UN, bool INLINE = false>
 __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   static_assert(UN <= 4, "mx_words holds four units");
   static_assert(NW * 64 >= kDecodeMaxT, "Finder takes a thread per token");
   __shared__ Rows rows;
-  __shared__ __align__(16) char smem[gu_smem<F, NW, NBMAX>()];
+  __shared__ __align__(16) char smem[gu_smem<F, NW, TB, NBMAX>()];
   const int32_t* mid = a.mid;
   const float* mw = a.mw;
   if constexpr (INLINE) {
@@ -585,33 +599,33 @@ __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   Finder find;
   const int n = find.count(rows, mid, mw, e, a.T, a.k);
   if (n == 0) return;
-  GuTile t;
-  t.n0 = blockIdx.x * 16;
+  GuTile<TB> t;
+  t.n0 = blockIdx.x * 16 * TB;
   const int rowb = a.d * (F >= WF_FP8 ? 1 : (int)sizeof(typename Fmt<F>::act));
   const uint64_t wbytes = (uint64_t)2 * a.I * rowb;
   t.w = buffer_of((const char*)a.w_gate_up + e * wbytes, wbytes);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = min(t.n0 + load_row(h), a.I - 1);  // rows past I repeat the last and are dropped
-    t.g[h] = (uint32_t)row * rowb;
-    t.u[h] = (uint32_t)(a.I + row) * rowb;
-  }
+  for (int b = 0; b < TB; ++b)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = min(t.n0 + b * 16 + load_row(h), a.I - 1);  // rows past I repeat the last and are dropped
+      t.g[b][h] = (uint32_t)row * rowb;
+      t.u[b][h] = (uint32_t)(a.I + row) * rowb;
+    }
   t.row4 = t.n0 + (lane >> 2);  // read for WF_MX, where I is a multiple of 128
   const char* sc = (const char*)a.s_gate_up;
   if (F == WF_FP8) sc += (int64_t)e * (2 * a.I / 128) * (a.d / 128) * 4;
   if (F == WF_MX) sc += (int64_t)e * 2 * a.I * (a.d / 32);
   t.sc = sc;
-  GuWeights<F, UN> w;
+  GuWeights<F, TB, UN> w;
   load_gu<F, NT>(w, t, a.I, a.d, tile::wave_id() * UN);
   find.list(rows);
   if constexpr (NBMAX == 1) {
-    gateup_rows<F, NT, NW, UN, 1>(a, rows, 0, n, w, t, smem);
+    gateup_rows<F, NT, NW, TB, UN, 1>(a, rows, 0, n, w, t, smem);
   } else {
     for (int r0 = 0; r0 < n; r0 += 16 * NBMAX) {
-      const int left = n - r0;
-      if (left <= 16) gateup_rows<F, NT, NW, UN, 1>(a, rows, r0, n, w, t, smem);
-      else if (NBMAX == 2 || left <= 32) gateup_rows<F, NT, NW, UN, 2>(a, rows, r0, n, w, t, smem);
-      else gateup_rows<F, NT, NW, UN, NBMAX>(a, rows, r0, n, w, t, smem);
+      if (n - r0 <= 16) gateup_rows<F, NT, NW, TB, UN, 1>(a, rows, r0, n, w, t, smem);
+      else gateup_rows<F, NT, NW, TB, UN, NBMAX>(a, rows, r0, n, w, t, smem);
     }
   }
 }
@@ -834,15 +848,16 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(Deco
 // go to y [T k, d] in float32, which decode_combine_kernel sums in slot order.
 constexpr int kDownRowWaves = 4;
 
+template <int TB>
 struct DownTile {
   rsrc_t w;
   const void* sc;
-  uint32_t row[2];  // offsets of this lane's two rows
+  uint32_t row[TB][2];  // offsets of this lane's rows
   int row4, n0;
 };
 
-template <int F, bool NT, int NB, int UN>
-__device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, const DownTile& t,
+template <int F, bool NT, int TB, int UN, int NB>
+__device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, const DownTile<TB>& t,
                                           lds_t* lw) {
   typedef typename Fmt<F>::act AT;
   const int lane = threadIdx.x & 63, q = lane >> 4, col = lane & 15;
@@ -861,19 +876,24 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
       live[b][h] = r < n;
       xr[b][h] = (uint32_t)rows.slot[live[b][h] ? r : n - 1] * bbytes;
     }
-  f32x4_t acc[NB];
+  f32x4_t acc[NB][TB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) acc[b] = f32x4_t{0, 0, 0, 0};
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int m = 0; m < TB; ++m) acc[b][m] = f32x4_t{0, 0, 0, 0};
   constexpr int UB = NB == 1 ? UN : 1;
   for (int base = 0; base < units; base += UN) {
-    u32x4_t wv[UN][2];
+    u32x4_t wv[TB][UN][2];
     float sb[UN];
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
-      load_rows<NT>(wv[i], t.w, t.row, (base + i) * 128, abytes);
+#pragma unroll
+      for (int m = 0; m < TB; ++m) load_rows<NT>(wv[m][i], t.w, t.row[m], (base + i) * 128, abytes);
       sb[i] = block_scale_of<F>(t.sc, t.n0, K, base + i);
     }
-    const uint32_t mx = mx_words<F>(t.sc, t.row4, K, base + (lane & 3));
+    uint32_t mx[TB];
+#pragma unroll
+    for (int m = 0; m < TB; ++m) mx[m] = mx_words<F>(t.sc, t.row4 + 16 * m, K, base + (lane & 3));
 #pragma unroll
     for (int i0 = 0; i0 < UN; i0 += UB) {
       u32x4_t xv[UB][NB][kActHalves<F>][2];
@@ -884,17 +904,22 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
       __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
 #pragma unroll
       for (int i = 0; i < UB; ++i) {
-        typename Fmt<F>::frag fr[Fmt<F>::NF];
-        put_rows(lw, wv[i0 + i]);
-        uint32_t m = 0;
-        if constexpr (F == WF_MX) m = (uint32_t)__shfl((int)mx, col * 4 + i0 + i, kWave);
-        to_frags<F>(fr, lw, m, q, col);
+        u32x4_t xf[NB][Fmt<F>::BV];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          u32x4_t xf[Fmt<F>::BV];
-          put_acts<F>(lw + 2048, xv[i][b], eight);
-          get_acts<F>(xf, lw + 2048, q, col);
-          unit_mma<F>(acc[b], fr, xf, sb[i0 + i]);
+        for (int m = 0; m < TB; ++m) {
+          typename Fmt<F>::frag fr[Fmt<F>::NF];
+          put_rows(lw, wv[m][i0 + i]);
+          uint32_t code = 0;
+          if constexpr (F == WF_MX) code = (uint32_t)__shfl((int)mx[m], col * 4 + i0 + i, kWave);
+          to_frags<F>(fr, lw, code, q, col);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            if (m == 0) {
+              put_acts<F>(lw + 2048, xv[i][b], eight);
+              get_acts<F>(xf[b], lw + 2048, q, col);
+            }
+            unit_mma<F>(acc[b][m], fr, xf[b], sb[i0 + i]);
+          }
         }
       }
     }
@@ -902,12 +927,16 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const int r = r0 + b * 16 + col;
-    if (r < n && t.n0 + q * 4 < a.d)  // d is a multiple of 8: four rows are in or out together
-      *(f32x4_t*)(a.y + (int64_t)rows.slot[r] * a.d + t.n0 + q * 4) = acc[b];
+#pragma unroll
+    for (int m = 0; m < TB; ++m) {
+      const int row = t.n0 + 16 * m + q * 4;
+      if (r < n && row < a.d)  // d is a multiple of 8: four rows are in or out together
+        *(f32x4_t*)(a.y + (int64_t)rows.slot[r] * a.d + row) = acc[b][m];
+    }
   }
 }
 
-template <int F, bool NT>
+template <int F, bool NT, int TB, int UN>
 __global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(DecodeArgs a) {
   static_assert(kDownRowWaves * 64 >= kDecodeMaxT, "Finder takes a thread per token");
   __shared__ Rows rows;
@@ -917,27 +946,26 @@ __global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(De
   Finder find;
   const int n = find.count(rows, a.mid, a.mw, e, a.T, a.k);
   find.list(rows);
-  DownTile t;
+  DownTile<TB> t;
   const int lane = threadIdx.x & 63, wave = tile::wave_id();
-  t.n0 = (blockIdx.x * kDownRowWaves + wave) * 16;
+  t.n0 = (blockIdx.x * kDownRowWaves + wave) * 16 * TB;
   if (n == 0 || t.n0 >= a.d) return;  // no barrier follows
   const int rowb = a.I * (F >= WF_FP8 ? 1 : (int)sizeof(typename Fmt<F>::act));
   const uint64_t wbytes = (uint64_t)a.d * rowb;
   t.w = buffer_of((const char*)a.w_down + e * wbytes, wbytes);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) t.row[h] = (uint32_t)min(t.n0 + load_row(h), a.d - 1) * rowb;
+  for (int m = 0; m < TB; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) t.row[m][h] = (uint32_t)min(t.n0 + 16 * m + load_row(h), a.d - 1) * rowb;
   t.row4 = t.n0 + (lane >> 2);  // read for WF_MX, where d is a multiple of 128
   const char* sc = (const char*)a.s_down;
   if (F == WF_FP8) sc += (int64_t)e * (a.d / 128) * (a.I / 128) * 4;
   if (F == WF_MX) sc += (int64_t)e * a.d * (a.I / 32);
   t.sc = sc;
   lds_t* lw = (lds_t*)work + wave * (2048 + 2048 * kActHalves<F>);
-  constexpr int NBMAX = kMaxBlocks<F>, UN = F >= WF_FP8 ? 2 : 4;
-  for (int r0 = 0; r0 < n; r0 += 16 * NBMAX) {
-    const int left = n - r0;
-    if (left <= 16) down_rows<F, NT, 1, UN>(a, rows, r0, n, t, lw);
-    else if (NBMAX == 2 || left <= 32) down_rows<F, NT, 2, UN>(a, rows, r0, n, t, lw);
-    else down_rows<F, NT, NBMAX, UN>(a, rows, r0, n, t, lw);
+  for (int r0 = 0; r0 < n; r0 += 32) {
+    if (n - r0 <= 16) down_rows<F, NT, TB, UN, 1>(a, rows, r0, n, t, lw);
+    else down_rows<F, NT, TB, UN, 2>(a, rows, r0, n, t, lw);
   }
 }
 
@@ -971,6 +999,20 @@ __global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a) {
 int work_items(const DecodeArgs& a) { return a.T * a.k > a.E ? a.E : a.T * a.k; }
 int64_t gu_groups(const DecodeArgs& a) { return cdiv(a.I, 16) * work_items(a); }
 
+// Whether work-groups of 32 rows (a wave's, in the down product) leave four for
+// each CU.  Twice the rows halve what is read of the activations; fewer groups
+// leave CUs idle at the end.  Above, us with 16 and 32 rows at 256 tokens, by
+// the experts: gate/up bf16 128 151 and 137, 64 (1536 groups) 94 and 86, 32
+// (768) 51 and 55; mxfp8, 200 tokens, 128 experts 97 and 82, 8 (192) 20 and 25.
+bool wide_gateup(const DecodeArgs& a) { return cdiv(a.I, 32) * work_items(a) >= 1024; }
+
+// For the down product also eight tokens an expert, below which its activations
+// are little beside its weights (64 tokens, four an expert: 64 and 65 us; 256:
+// 90 and 84; mxfp8, 200: 53 and 46; 32 experts, 512 groups: bf16 27 and 30).
+bool wide_down(const DecodeArgs& a) {
+  return cdiv(a.d, 32 * kDownRowWaves) * work_items(a) >= 1024 && a.T * a.k >= 8 * work_items(a);
+}
+
 // Whether the weights that the tokens may select exceed the last-level cache.
 // Nothing of them is left there for the next call then, and non-temporal loads
 // keep them from displacing what this call reads again (64 tokens of 8 of 128
@@ -983,56 +1025,72 @@ bool past_cache(const DecodeArgs& a) {
   return work_items(a) * int64_t(3) * a.I * a.d * value > kLastLevelCache;
 }
 
-template <int F>
-hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
-  const unsigned items = (unsigned)work_items(a);
-  const dim3 gu((unsigned)cdiv(a.I, 16), items);
+template <int F, bool NT>
+hipError_t run_gateup(const LaunchCtx& c, const DecodeArgs& a) {
+  const dim3 grid((unsigned)cdiv(a.I, 16), (unsigned)work_items(a));
   constexpr int UN = F >= WF_FP8 ? 2 : 4;
-  if (a.T > 16 && past_cache<F>(a))
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, true, kMaxBlocks<F>, 4, 2>), gu, dim3(4 * 64), 0, a);
-  else if (a.T > 16)
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, false, kMaxBlocks<F>, 4, 2>), gu, dim3(4 * 64), 0, a);
+  if (a.T > 16 && wide_gateup(a)) {
+    // units of K at a time: coded weights one (two leave room for fewer waves: 84
+    // us and 111 at 200 tokens), the others two (137 both ways at 256, at 64 125
+    // and with one 131)
+    constexpr int UNW = F >= WF_FP8 ? 1 : 2;
+    const dim3 wide((unsigned)cdiv(a.I, 32), grid.y);
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, NT, 2, 4, 2, UNW>), wide, dim3(4 * 64), 0, a);
+  } else if (a.T > 16) {
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, NT, 2, 4, 1, 2>), grid, dim3(4 * 64), 0, a);
+  }
   // As many work-groups as fit beside each other, two per CU: eight waves each,
   // so that all bytes are in flight at once (T = 1 above, 384 work-groups: 24.7
   // us with eight, 26.3 with four).  More: four, of which more fit (T = 2, 768:
   // 38.7 us with eight, 36.1 with four; 16 tokens of 8 of 64 experts, d = 4096,
   // I = 1024, e4m3: 150 and 139).
   else if (gu_groups(a) <= 512 && a.route_inline)
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, false, 1, 8, UN, true>), gu, dim3(8 * 64), 0, a);
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, NT, 1, 8, 1, UN, true>), grid, dim3(8 * 64), 0, a);
   else if (gu_groups(a) <= 512)
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, false, 1, 8, UN>), gu, dim3(8 * 64), 0, a);
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, NT, 1, 8, 1, UN>), grid, dim3(8 * 64), 0, a);
   else if (a.route_inline)
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, false, 1, 4, UN, true>), gu, dim3(4 * 64), 0, a);
-  else if (past_cache<F>(a))
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, true, 1, 4, UN>), gu, dim3(4 * 64), 0, a);
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, NT, 1, 4, 1, UN, true>), grid, dim3(4 * 64), 0, a);
   else
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, false, 1, 4, UN>), gu, dim3(4 * 64), 0, a);
+    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, NT, 1, 4, 1, UN>), grid, dim3(4 * 64), 0, a);
+  return hipSuccess;
+}
+
+template <int F, bool NT>
+hipError_t run_down(const LaunchCtx& c, const DecodeArgs& a) {
   if (small_down(a)) {
     MOE_LAUNCH(c, "decode_down", decode_down_small_kernel<F>, dim3((unsigned)(a.d / 8)), dim3(kDownWaves * 64), 0, a);
     return hipSuccess;
   }
   if (decode_one_down(a.T, a.k, a.d)) {
     const size_t smem = down_work<F>() + (size_t)a.E * 4 + (size_t)a.E * a.T * 2;
-    constexpr size_t most = down_work<F>() + kMaxExperts * (4 + 16 * 2);
-    const dim3 grid((unsigned)cdiv(a.d, 16));
-    if (past_cache<F>(a)) {
-      HIP_RET(tile::allow_smem_once<decode_down_kernel<F, true>>(most));
-      MOE_LAUNCH(c, "decode_down", (decode_down_kernel<F, true>), grid, dim3(kDownWaves * 64), smem, a);
-    } else {
-      HIP_RET(tile::allow_smem_once<decode_down_kernel<F, false>>(most));
-      MOE_LAUNCH(c, "decode_down", (decode_down_kernel<F, false>), grid, dim3(kDownWaves * 64), smem, a);
-    }
+    HIP_RET(tile::allow_smem_once<decode_down_kernel<F, NT>>(down_work<F>() + kMaxExperts * (4 + 16 * 2)));
+    MOE_LAUNCH(c, "decode_down", (decode_down_kernel<F, NT>), dim3((unsigned)cdiv(a.d, 16)), dim3(kDownWaves * 64),
+               smem, a);
     return hipSuccess;
   }
-  const dim3 dr((unsigned)cdiv(a.d, 16 * kDownRowWaves), items);
-  if (past_cache<F>(a))
-    MOE_LAUNCH(c, "decode_down", (decode_down_rows_kernel<F, true>), dr, dim3(kDownRowWaves * 64), 0, a);
-  else
-    MOE_LAUNCH(c, "decode_down", (decode_down_rows_kernel<F, false>), dr, dim3(kDownRowWaves * 64), 0, a);
+  constexpr int UN = F >= WF_FP8 ? 2 : 4;
+  const unsigned items = (unsigned)work_items(a);
+  if (wide_down(a)) {
+    const dim3 grid((unsigned)cdiv(a.d, 32 * kDownRowWaves), items);
+    MOE_LAUNCH(c, "decode_down", (decode_down_rows_kernel<F, NT, 2, UN / 2>), grid, dim3(kDownRowWaves * 64), 0, a);
+  } else {
+    const dim3 grid((unsigned)cdiv(a.d, 16 * kDownRowWaves), items);
+    MOE_LAUNCH(c, "decode_down", (decode_down_rows_kernel<F, NT, 1, UN>), grid, dim3(kDownRowWaves * 64), 0, a);
+  }
   const dim3 cg((unsigned)cdiv(a.d, 1024), (unsigned)a.T);
   if constexpr (F == WF_F32) MOE_LAUNCH(c, "decode_combine", decode_combine_kernel<float>, cg, dim3(256), 0, a);
   else MOE_LAUNCH(c, "decode_combine", decode_combine_kernel<bf16_t>, cg, dim3(256), 0, a);
   return hipSuccess;
+}
+
+template <int F>
+hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
+  if (past_cache<F>(a)) {
+    HIP_RET((run_gateup<F, true>(c, a)));
+    return run_down<F, true>(c, a);
+  }
+  HIP_RET((run_gateup<F, false>(c, a)));
+  return run_down<F, false>(c, a);
 }
 
 }  // namespace

@@ -183,6 +183,26 @@ def test_weights_past_the_cache(T, d, E, k, I, dtype, weights):
     check(got, x, cut(wgu), cut(wd), remap[ids], w)
 
 
+# more experts and rows than 1024 work-groups of 32 rows: gate/up for a few
+# rows an expert, then also the down product (8 rows an expert and more), with
+# extents that end inside a tile of 32 and an expert with more than 32 rows
+@pytest.mark.parametrize("T,d,E,k,I,dtype,weights", [
+    (17, 72, 128, 8, 264, "bf16", "native"), (20, 40, 256, 6, 136, "f32", "native"),
+    (33, 128, 256, 4, 128, "bf16", "fp8_block"), (20, 256, 256, 6, 128, "bf16", "mxfp8"),
+    (130, 1032, 120, 9, 264, "bf16", "native"), (90, 1144, 114, 11, 280, "f32", "native"),
+    (101, 1024, 128, 12, 256, "bf16", "fp8_block"), (256, 1152, 128, 5, 256, "bf16", "mxfp8"),
+])
+def test_wide_row_tiles(T, d, E, k, I, dtype, weights):
+    x, wgu, wd, logits = make(T, d, E, k, I, dtype, weights, seed=6)
+    logits[: T // 3, 5] = 9.0                                 # one expert with many rows
+    logits[:, 7] = -9.0                                       # one that no token selects
+    dec = decoder(x, E, k, I, weights)
+    got = dec.forward(x, wgu, wd, logits=logits)
+    ids, w = topk64(logits, k)
+    assert torch.equal(dec.topk_ids.long(), ids)
+    check(got, x, wgu, wd, ids, w)
+
+
 def test_masked_logits():
     """-inf logits are empty slots: none left, fewer left than k, ties."""
     T, d, E, k, I = 6, 64, 8, 4, 32
