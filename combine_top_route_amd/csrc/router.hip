@@ -28,6 +28,15 @@ using tile::s16x4_t;
 using tile::s16x8_t;
 using tile::u32x4_t;
 
+// Place b of n work-groups: the eight XCDs, which take work-groups in turn, get
+// consecutive places, here the column blocks of a few runs of tokens, whose
+// dlogits they share in their L2 (dx 40 us at the size above in plain order,
+// 35 in this one).
+__device__ __forceinline__ int xcd_share(int b, int n) {
+  const int x = b & 7;
+  return x * (n >> 3) + min(x, n & 7) + (b >> 3);
+}
+
 // s + a b over the 16 (float) or 32 (bf16) values of K in two 16-byte operands.
 template <typename T>
 __device__ __forceinline__ f32x4_t mma16(u32x4_t a, u32x4_t b, f32x4_t s) {
@@ -185,9 +194,10 @@ hipError_t fwd_any(const LaunchCtx& c, const RouterArgs& a, void* logits) {
 // [token][column], two more steps' loads in flight in registers; a transposing
 // LDS read (16-bit) or plain 4-byte reads (the K = 4 float32 MFMA) hand the
 // MFMA its token-contiguous operands.  Two work-groups share a CU, so that one's
-// staging and barriers run beside the other's products: 31 us at the size
-// above; one work-group with 64-token steps took 35.  Parts are float32
-// [run][E][d].
+// staging and barriers run beside the other's products: 30 us at the size
+// above, of which loads and staging alone take 19; one work-group with 64-token
+// steps took 35, blocks of 64 experts with 64-token steps and half the parts 31.
+// Parts are float32 [run][E][d].
 // Each work-group then lays a piece of w out as the second launch's MFMA
 // operands (in work-groups of their own that took 2 us more: the others fill
 // the chip).
@@ -453,7 +463,7 @@ __device__ __forceinline__ void lay_out_w(const RouterArgs& a, int group, int gr
 template <typename T, typename LT>
 __global__ __launch_bounds__(512, 4) void router_dw_kernel(RouterArgs a) {
   extern __shared__ __align__(16) char smem[];
-  int b = blockIdx.x;
+  int b = xcd_share((int)blockIdx.x, a.dw_groups);
   const int db = b % a.d_blocks;
   b /= a.d_blocks;
   dw_part<T, LT>(a, smem, b % a.e_blocks, db, b / a.e_blocks);
@@ -615,8 +625,12 @@ template <typename T, typename LT, bool MULTI>
 __global__ __launch_bounds__(kDxWaves * 64, 2) void router_dx_kernel(RouterArgs a) {
   __shared__ __align__(16) char smem[4 * kDxTok * dx_stride<T>];
   const int b = blockIdx.x;
-  if (b < a.dx_groups) dx_part<T, LT, MULTI>(a, smem, b % a.dx_blocks, b / a.dx_blocks);
-  else join_dw<T>(a, b - a.dx_groups);
+  if (b < a.dx_groups) {
+    const int p = xcd_share(b, a.dx_groups);
+    dx_part<T, LT, MULTI>(a, smem, p % a.dx_blocks, p / a.dx_blocks);
+  } else {
+    join_dw<T>(a, b - a.dx_groups);
+  }
 }
 
 template <typename T, typename LT>
