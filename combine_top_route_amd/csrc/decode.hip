@@ -623,7 +623,7 @@ __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   if constexpr (NBMAX == 1) {
     gateup_rows<F, NT, NW, TB, UN, 1>(a, rows, 0, n, w, t, smem);
   } else {
-    for (int r0 = 0; r0 < n; r0 += 16 * NBMAX) {
+    for (int r0 = blockIdx.z * 16 * NBMAX; r0 < n; r0 += gridDim.z * 16 * NBMAX) {
       if (n - r0 <= 16) gateup_rows<F, NT, NW, TB, UN, 1>(a, rows, r0, n, w, t, smem);
       else gateup_rows<F, NT, NW, TB, UN, NBMAX>(a, rows, r0, n, w, t, smem);
     }
@@ -963,7 +963,7 @@ __global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(De
   if (F == WF_MX) sc += (int64_t)e * a.d * (a.I / 32);
   t.sc = sc;
   lds_t* lw = (lds_t*)work + wave * (2048 + 2048 * kActHalves<F>);
-  for (int r0 = 0; r0 < n; r0 += 32) {
+  for (int r0 = blockIdx.z * 32; r0 < n; r0 += gridDim.z * 32) {
     if (n - r0 <= 16) down_rows<F, NT, TB, UN, 1>(a, rows, r0, n, t, lw);
     else down_rows<F, NT, TB, UN, 2>(a, rows, r0, n, t, lw);
   }
@@ -1013,6 +1013,18 @@ bool wide_down(const DecodeArgs& a) {
   return cdiv(a.d, 32 * kDownRowWaves) * work_items(a) >= 1024 && a.T * a.k >= 8 * work_items(a);
 }
 
+// Work-groups that an expert's tokens are split over, 32 at a time, where the
+// experts and rows alone leave CUs free: each then reads the weights again,
+// from the caches, instead of passing over them for one block after another
+// (256 tokens of 2 of 8 experts, d = 2048, I = 768, bf16: gate/up 31 us without
+// and 23, down 19 and 13; 219 tokens, 2 experts, d = 192, I = 784: 15 and 7, 51
+// and 10.  Up to 512 or 2048 work-groups instead of 1024: the first case's
+// gate/up 35 and 25).
+unsigned token_split(const DecodeArgs& a, int64_t groups) {
+  const int64_t most = cdiv(a.T, 32), want = 1024 / groups;
+  return (unsigned)(want < 1 ? 1 : want < most ? want : most);
+}
+
 // Whether the weights that the tokens may select exceed the last-level cache.
 // Nothing of them is left there for the next call then, and non-temporal loads
 // keep them from displacing what this call reads again (64 tokens of 8 of 128
@@ -1037,7 +1049,14 @@ hipError_t run_gateup(const LaunchCtx& c, const DecodeArgs& a) {
     const dim3 wide((unsigned)cdiv(a.I, 32), grid.y);
     MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, NT, 2, 4, 2, UNW>), wide, dim3(4 * 64), 0, a);
   } else if (a.T > 16) {
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, NT, 2, 4, 1, 2>), grid, dim3(4 * 64), 0, a);
+    const dim3 split(grid.x, grid.y, token_split(a, gu_groups(a)));
+    // a work-group per CU or fewer: eight waves (57 tokens of both of 2 experts,
+    // d = 3792, I = 648, float32, 164 groups: 31 us with four and 26; 175 tokens,
+    // 5 experts, d = 960, I = 272, 510 groups: 8.1 and 9.4)
+    if (gu_groups(a) * split.z <= 256)
+      MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, NT, 2, 8, 1, 2>), split, dim3(8 * 64), 0, a);
+    else
+      MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, NT, 2, 4, 1, 2>), split, dim3(4 * 64), 0, a);
   }
   // As many work-groups as fit beside each other, two per CU: eight waves each,
   // so that all bytes are in flight at once (T = 1 above, 384 work-groups: 24.7
@@ -1074,7 +1093,8 @@ hipError_t run_down(const LaunchCtx& c, const DecodeArgs& a) {
     const dim3 grid((unsigned)cdiv(a.d, 32 * kDownRowWaves), items);
     MOE_LAUNCH(c, "decode_down", (decode_down_rows_kernel<F, NT, 2, UN / 2>), grid, dim3(kDownRowWaves * 64), 0, a);
   } else {
-    const dim3 grid((unsigned)cdiv(a.d, 16 * kDownRowWaves), items);
+    const unsigned tiles = (unsigned)cdiv(a.d, 16 * kDownRowWaves);
+    const dim3 grid(tiles, items, token_split(a, (int64_t)tiles * items));
     MOE_LAUNCH(c, "decode_down", (decode_down_rows_kernel<F, NT, 1, UN>), grid, dim3(kDownRowWaves * 64), 0, a);
   }
   const dim3 cg((unsigned)cdiv(a.d, 1024), (unsigned)a.T);

@@ -605,15 +605,29 @@ __device__ __forceinline__ void dx_part(const RouterArgs& a, char* smem, int cb,
   }
 }
 
-// dw = the sum of the parts, in run order; 4 values a thread.
+// dw = the sum of the parts: 4 values a lane, every fourth run a wave, then the
+// four waves' sums in order (6726 tokens, d = 136, E = 6: 17 us with all runs in
+// one wave, 6 so).
 template <typename T>
-__device__ __forceinline__ void join_dw(const RouterArgs& a, int b) {
-  const int64_t n = (int64_t)a.E * a.d, i = ((int64_t)b * kDxWaves * 64 + threadIdx.x) * 4;
-  if (i >= n) return;  // d is a multiple of 8: whole groups of 4
+__device__ __forceinline__ void join_dw(const RouterArgs& a, char* smem, int b) {
+  const int lane = threadIdx.x & 63, wave = tile::wave_id();
+  const int64_t n = (int64_t)a.E * a.d, i = ((int64_t)b * 64 + lane) * 4;
   f32x4_t s = {0, 0, 0, 0};
-#pragma unroll 4
-  for (int r = 0; r < a.runs; ++r) {
-    const f32x4_t v = *(const f32x4_t*)(a.parts + r * n + i);
+  if (i < n) {  // d is a multiple of 8: whole groups of 4
+#pragma unroll 8
+    for (int r = wave; r < a.runs; r += kDxWaves) {
+      const f32x4_t v = *(const f32x4_t*)(a.parts + r * n + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] += v[j];
+    }
+  }
+  f32x4_t* sums = (f32x4_t*)smem;
+  sums[threadIdx.x] = s;
+  __syncthreads();
+  if (wave != 0 || i >= n) return;
+#pragma unroll
+  for (int w = 1; w < kDxWaves; ++w) {
+    const f32x4_t v = sums[w * 64 + lane];
 #pragma unroll
     for (int j = 0; j < 4; ++j) s[j] += v[j];
   }
@@ -629,7 +643,7 @@ __global__ __launch_bounds__(kDxWaves * 64, 2) void router_dx_kernel(RouterArgs 
     const int p = xcd_share(b, a.dx_groups);
     dx_part<T, LT, MULTI>(a, smem, p % a.dx_blocks, p / a.dx_blocks);
   } else {
-    join_dw<T>(a, b - a.dx_groups);
+    join_dw<T>(a, smem, b - a.dx_groups);
   }
 }
 
@@ -638,7 +652,7 @@ hipError_t bwd(const LaunchCtx& c, const RouterArgs& a) {
   constexpr size_t smem = 2 * dw_stage<T, LT>();
   HIP_RET(tile::allow_smem_once<router_dw_kernel<T, LT>>(smem));
   MOE_LAUNCH(c, "router_dw", (router_dw_kernel<T, LT>), dim3((unsigned)a.dw_groups), dim3(512), smem, a);
-  const dim3 grid((unsigned)(a.dx_groups + cdiv((int64_t)a.E * a.d, kDxWaves * 256)));
+  const dim3 grid((unsigned)(a.dx_groups + cdiv((int64_t)a.E * a.d, 256)));
   if (a.dx_eblocks > 1)
     MOE_LAUNCH(c, "router_dx", (router_dx_kernel<T, LT, true>), grid, dim3(kDxWaves * 64), 0, a);
   else

@@ -11,9 +11,9 @@
 //             (zero where a clamp is active)
 //
 // Both are one pass over the rows, bound by memory: at I = 768 in bf16 the
-// forward moves 6.2 KB a row and the backward 7.7 KB.  One wave takes a row; a
-// lane takes 8 columns of both halves, so a block of 32 is four neighbouring
-// lanes, whose largest magnitude two DPP steps find.
+// forward moves 6.2 KB a row and the backward 7.7 KB.  A wave takes a row, or
+// several short ones; a lane takes 8 columns of both halves, so a block of 32 is
+// four neighbouring lanes, whose largest magnitude two DPP steps find.
 #include "common.h"
 #include "save8.h"
 #include "tile.h"
@@ -88,18 +88,18 @@ __device__ __forceinline__ void decode8(float (&f)[8], u32x2_t q, uint32_t byte)
 
 template <typename T, bool NT>
 __global__ __launch_bounds__(256) void save8_kernel(const T* __restrict__ H, const float* __restrict__ topk_w,
-                                                    const int32_t* __restrict__ src_of, int R, int I, float lim,
-                                                    T* __restrict__ aw, uint8_t* __restrict__ codes,
+                                                    const int32_t* __restrict__ src_of, int R, int I, int lsh,
+                                                    float lim, T* __restrict__ aw, uint8_t* __restrict__ codes,
                                                     uint8_t* __restrict__ scales) {
-  const int r = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int L = 1 << lsh, r = (blockIdx.x << (8 - lsh)) + (threadIdx.x >> lsh);
   if (r >= R) return;
-  const int lane = threadIdx.x & 63;
+  const int lane = (int)threadIdx.x & (L - 1);
   const int nb = (I + 31) / 32;
   const float wr = aw ? topk_w[src_of[r]] : 0.0f;
   const T* Hr = H + (int64_t)r * 2 * I;
   uint8_t* cr = codes + (int64_t)r * 2 * I;
   uint8_t* sr = scales + (int64_t)r * 2 * nb;
-  for (int c = lane; c < nb * 4; c += kWave) {
+  for (int c = lane; c < nb * 4; c += L) {
     const bool in = c * 8 < I;  // I is a multiple of 8: a lane's columns are in or out together
     float g[8] = {}, u[8] = {};
     if (in) {
@@ -132,12 +132,12 @@ template <typename T, bool NT>
 __global__ __launch_bounds__(256) void swiglu_bwd8_kernel(const T* __restrict__ G, const uint8_t* __restrict__ codes,
                                                           const uint8_t* __restrict__ scales,
                                                           const float* __restrict__ topk_w,
-                                                          const int32_t* __restrict__ src_of, int R, int I, float lim,
-                                                          T* __restrict__ dH, T* __restrict__ aw,
+                                                          const int32_t* __restrict__ src_of, int R, int I, int lsh,
+                                                          float lim, T* __restrict__ dH, T* __restrict__ aw,
                                                           float* __restrict__ dw) {
-  const int r = blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int L = 1 << lsh, r = (blockIdx.x << (8 - lsh)) + (threadIdx.x >> lsh);
   if (r >= R) return;
-  const int lane = threadIdx.x & 63;
+  const int lane = (int)threadIdx.x & (L - 1);
   const int nb = (I + 31) / 32;
   const float wr = topk_w[src_of[r]];
   const uint8_t* cr = codes + (int64_t)r * 2 * I;
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(256) void swiglu_bwd8_kernel(const T* __restrict__ 
   const T* Gr = G + (int64_t)r * I;
   T* dr = dH + (int64_t)r * 2 * I;
   float part = 0.0f;
-  for (int c = lane; c * 8 < I; c += kWave) {
+  for (int c = lane; c * 8 < I; c += L) {
     float gv[8], g[8], u[8], a[8], dg[8], du[8];
     load8(gv, Gr + c * 8);
     decode8(g, *(const u32x2_t*)(cr + c * 8), sr[c >> 2]);
@@ -165,27 +165,27 @@ __global__ __launch_bounds__(256) void swiglu_bwd8_kernel(const T* __restrict__ 
     store8<NT>(dr + I + c * 8, du);
     if (aw) store8<NT>(aw + (int64_t)r * I + c * 8, a);
   }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) part += __shfl_xor(part, off, kWave);
+  for (int off = L / 2; off >= 1; off >>= 1) part += __shfl_xor(part, off, kWave);
   if (lane == 0) dw[r] = part;
 }
 
-}  // namespace
+// log2 of the lanes that a row takes: 64, or fewer where its columns fill no more
+// (38304 rows of I = 112 in bf16, backward: 24 us with 64, 10 with 16).
+int row_lanes(int I) { return I > 256 ? 6 : I > 128 ? 5 : I > 64 ? 4 : 3; }
 
-namespace {
 template <typename T, bool NT>
 hipError_t save(const LaunchCtx& c, const void* H, const float* topk_w, const int32_t* src_of, int R, int I, float lim,
                 void* aw, uint8_t* codes, uint8_t* scales) {
-  MOE_LAUNCH(c, "swiglu_save8", (save8_kernel<T, NT>), dim3((unsigned)cdiv(R, 4)), dim3(256), 0, (const T*)H, topk_w,
-             src_of, R, I, lim, (T*)aw, codes, scales);
+  MOE_LAUNCH(c, "swiglu_save8", (save8_kernel<T, NT>), dim3((unsigned)cdiv(R, 256 >> row_lanes(I))), dim3(256), 0,
+             (const T*)H, topk_w, src_of, R, I, row_lanes(I), lim, (T*)aw, codes, scales);
   return hipSuccess;
 }
 template <typename T, bool NT>
 hipError_t backward(const LaunchCtx& c, const void* G, const uint8_t* codes, const uint8_t* scales,
                     const float* topk_w, const int32_t* src_of, int R, int I, float lim, void* dH, void* aw,
                     float* dw) {
-  MOE_LAUNCH(c, "swiglu_bwd8", (swiglu_bwd8_kernel<T, NT>), dim3((unsigned)cdiv(R, 4)), dim3(256), 0, (const T*)G,
-             codes, scales, topk_w, src_of, R, I, lim, (T*)dH, (T*)aw, dw);
+  MOE_LAUNCH(c, "swiglu_bwd8", (swiglu_bwd8_kernel<T, NT>), dim3((unsigned)cdiv(R, 256 >> row_lanes(I))), dim3(256), 0,
+             (const T*)G, codes, scales, topk_w, src_of, R, I, row_lanes(I), lim, (T*)dH, (T*)aw, dw);
   return hipSuccess;
 }
 }  // namespace

@@ -307,12 +307,15 @@ moe_status moe_swiglu_backward8(const moe_shape* shape, const void* G, const uin
 /* The layer for a few tokens (serving): the forward's arithmetic on at most
  * 256 tokens, reading each selected expert's weights once, from weights that
  * may have been encoded beforehand.  No tiles, sort or encoders run: the call
- * is one small routing kernel, the gate/up products, and the down products
- * with the combine (more than 16 tokens: the combine on its own).
+ * is the gate/up products and the down products, with the routing as a small
+ * kernel before them (or, for a few tokens, inside the first) and the combine
+ * inside the down products or, from 9 to 17 tokens on (the fewer the smaller d
+ * is), as a small kernel behind them.
  *
  * shape: T <= 256 and precision MOE_PREC_NATIVE (MOE_ERR_UNSUPPORTED
  * otherwise; moe_forward takes more tokens), T*k*I values of dtype below
- * 4 GiB - 512; dtype is that of x and out; flags are ignored.  weights names the expert weights' format:
+ * 4 GiB - 512; dtype is that of x and out; flags are ignored.  weights names
+ * the expert weights' format:
  *   MOE_WEIGHTS_NATIVE:    in dtype; s_gate_up and s_down are NULL;
  *   MOE_WEIGHTS_FP8_BLOCK: what moe_quantize_fp8 MOE_QUANT_WEIGHT writes:
  *                          codes, and fp32 scales [E, 2I/128, d/128] and

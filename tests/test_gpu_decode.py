@@ -203,6 +203,28 @@ def test_wide_row_tiles(T, d, E, k, I, dtype, weights):
     check(got, x, wgu, wd, ids, w)
 
 
+# few experts with many rows each: the tokens of one are split over work-groups
+# in blocks of 32, up to and over one work-group per CU, with a last block that
+# is short and an expert whose rows fill the first block alone
+@pytest.mark.parametrize("T,d,E,k,I,dtype,weights", [
+    (200, 136, 30, 4, 40, "f32", "native"), (33, 200, 2, 2, 24, "f32", "native"),
+    (256, 24, 3, 2, 136, "bf16", "native"), (255, 520, 9, 3, 88, "bf16", "native"),
+    (250, 256, 16, 3, 256, "bf16", "fp8_block"), (65, 384, 1, 1, 128, "bf16", "fp8_block"),
+    (250, 128, 20, 2, 256, "bf16", "mxfp8"), (97, 640, 2, 1, 128, "bf16", "mxfp8"),
+])
+def test_tokens_split(T, d, E, k, I, dtype, weights):
+    x, wgu, wd, logits = make(T, d, E, k, I, dtype, weights, seed=7)
+    if E > 2:
+        logits[:, 2] = -9.0
+        logits[:20, 2] = 9.0                                  # an expert with 20 rows
+    dec = decoder(x, E, k, I, weights)
+    got = dec.forward(x, wgu, wd, logits=logits)
+    ids, w = topk64(logits, k)
+    assert torch.equal(dec.topk_ids.long(), ids)
+    check(got, x, wgu, wd, ids, w)
+    assert torch.equal(dec.forward(x, wgu, wd, logits=logits), got)
+
+
 def test_masked_logits():
     """-inf logits are empty slots: none left, fewer left than k, ties."""
     T, d, E, k, I = 6, 64, 8, 4, 32

@@ -120,6 +120,15 @@ def test_save8_rows(T, k, E, I, dtype):
         assert only[0] is None and torch.equal(only[1], codes) and torch.equal(only[2], scales)
 
 
+# widths on both sides of those where a wave takes one, two, four or eight rows,
+# with a last group of rows that is not full
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("I", [16, 64, 72, 128, 136, 256, 264])
+def test_rows_of_a_wave(I, dtype):
+    test_save8_rows(37, 1, 3, I, dtype)
+    test_backward8_rows(37, 1, 3, I, dtype)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rows_past_the_cache(dtype):
     """More than 256 MiB written (non-temporal stores): the same results, bit
