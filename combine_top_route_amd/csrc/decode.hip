@@ -844,8 +844,9 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(Deco
 }
 
 // --------------------------------------------- down product, more tokens
-// One wave: 16 rows of d of one expert for its tokens, all of I; the products
-// go to y [T k, d] in float32, which decode_combine_kernel sums in slot order.
+// One wave: 16 TB rows of d of one expert for its tokens, all of I, or with KS
+// its fourth of I, joined in LDS; the products go to y [T k, d] in float32,
+// which decode_combine_kernel sums in slot order.
 constexpr int kDownRowWaves = 4;
 
 template <int TB>
@@ -856,9 +857,9 @@ struct DownTile {
   int row4, n0;
 };
 
-template <int F, bool NT, int TB, int UN, int NB>
+template <int F, bool NT, int TB, int UN, bool KS, int NB>
 __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, const DownTile<TB>& t,
-                                          lds_t* lw) {
+                                          lds_t* lw, float* red) {
   typedef typename Fmt<F>::act AT;
   const int lane = threadIdx.x & 63, q = lane >> 4, col = lane & 15;
   const int K = a.I;
@@ -882,7 +883,8 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
 #pragma unroll
     for (int m = 0; m < TB; ++m) acc[b][m] = f32x4_t{0, 0, 0, 0};
   constexpr int UB = NB == 1 ? UN : 1;
-  for (int base = 0; base < units; base += UN) {
+  const int wave = tile::wave_id();
+  for (int base = KS ? wave * UN : 0; base < units; base += (KS ? kDownRowWaves : 1) * UN) {
     u32x4_t wv[TB][UN][2];
     float sb[UN];
 #pragma unroll
@@ -924,6 +926,26 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
       }
     }
   }
+  if constexpr (KS) {  // parts [wave][b][16 tokens][16 rows], over the waves' work space
+    static_assert(TB == 1, "a part is 16 rows");
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < NB; ++b) *(f32x4_t*)(red + ((wave * NB + b) * 16 + col) * 16 + q * 4) = acc[b][0];
+    __syncthreads();
+    for (int o = threadIdx.x; o < NB * 64; o += kDownRowWaves * 64) {
+      const int r = r0 + (o >> 2), row = t.n0 + (o & 3) * 4;
+      f32x4_t s = *(const f32x4_t*)(red + o * 4);
+#pragma unroll
+      for (int w = 1; w < kDownRowWaves; ++w) {
+        const f32x4_t v = *(const f32x4_t*)(red + (w * NB * 64 + o) * 4);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) s[m] += v[m];
+      }
+      if (r < n && row < a.d) *(f32x4_t*)(a.y + (int64_t)rows.slot[r] * a.d + row) = s;
+    }
+    __syncthreads();
+    return;
+  }
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     const int r = r0 + b * 16 + col;
@@ -936,7 +958,7 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
   }
 }
 
-template <int F, bool NT, int TB, int UN>
+template <int F, bool NT, int TB, int UN, bool KS>
 __global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(DecodeArgs a) {
   static_assert(kDownRowWaves * 64 >= kDecodeMaxT, "Finder takes a thread per token");
   __shared__ Rows rows;
@@ -948,8 +970,8 @@ __global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(De
   find.list(rows);
   DownTile<TB> t;
   const int lane = threadIdx.x & 63, wave = tile::wave_id();
-  t.n0 = (blockIdx.x * kDownRowWaves + wave) * 16 * TB;
-  if (n == 0 || t.n0 >= a.d) return;  // no barrier follows
+  t.n0 = (KS ? (int)blockIdx.x : (int)blockIdx.x * kDownRowWaves + wave) * 16 * TB;
+  if (n == 0 || t.n0 >= a.d) return;  // the whole work-group with KS; else no barrier follows
   const int rowb = a.I * (F >= WF_FP8 ? 1 : (int)sizeof(typename Fmt<F>::act));
   const uint64_t wbytes = (uint64_t)a.d * rowb;
   t.w = buffer_of((const char*)a.w_down + e * wbytes, wbytes);
@@ -964,8 +986,8 @@ __global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(De
   t.sc = sc;
   lds_t* lw = (lds_t*)work + wave * (2048 + 2048 * kActHalves<F>);
   for (int r0 = blockIdx.z * 32; r0 < n; r0 += gridDim.z * 32) {
-    if (n - r0 <= 16) down_rows<F, NT, TB, UN, 1>(a, rows, r0, n, t, lw);
-    else down_rows<F, NT, TB, UN, 2>(a, rows, r0, n, t, lw);
+    if (n - r0 <= 16) down_rows<F, NT, TB, UN, KS, 1>(a, rows, r0, n, t, lw, (float*)work);
+    else down_rows<F, NT, TB, UN, KS, 2>(a, rows, r0, n, t, lw, (float*)work);
   }
 }
 
@@ -1091,11 +1113,20 @@ hipError_t run_down(const LaunchCtx& c, const DecodeArgs& a) {
   const unsigned items = (unsigned)work_items(a);
   if (wide_down(a)) {
     const dim3 grid((unsigned)cdiv(a.d, 32 * kDownRowWaves), items);
-    MOE_LAUNCH(c, "decode_down", (decode_down_rows_kernel<F, NT, 2, UN / 2>), grid, dim3(kDownRowWaves * 64), 0, a);
+    MOE_LAUNCH(c, "decode_down", (decode_down_rows_kernel<F, NT, 2, UN / 2, false>), grid, dim3(kDownRowWaves * 64), 0, a);
   } else {
     const unsigned tiles = (unsigned)cdiv(a.d, 16 * kDownRowWaves);
     const dim3 grid(tiles, items, token_split(a, (int64_t)tiles * items));
-    MOE_LAUNCH(c, "decode_down", (decode_down_rows_kernel<F, NT, 1, UN>), grid, dim3(kDownRowWaves * 64), 0, a);
+    // a work-group per CU or fewer: each of its waves takes a fourth of I instead
+    // of 16 rows (20 tokens, 4 experts, d = 224, I = 952, float32: 11.2 us
+    // without and 6.0; 219 tokens, 2 experts, d = 192, I = 784: 10.3 and 5.1; up
+    // to 1024, 256 tokens of 2 of 8 experts, d = 2048, I = 768: 12.5 and 15.1)
+    if ((int64_t)tiles * items * grid.z <= 256) {
+      const dim3 split((unsigned)cdiv(a.d, 16), items, grid.z);
+      MOE_LAUNCH(c, "decode_down", (decode_down_rows_kernel<F, NT, 1, UN, true>), split, dim3(kDownRowWaves * 64), 0, a);
+    } else {
+      MOE_LAUNCH(c, "decode_down", (decode_down_rows_kernel<F, NT, 1, UN, false>), grid, dim3(kDownRowWaves * 64), 0, a);
+    }
   }
   const dim3 cg((unsigned)cdiv(a.d, 1024), (unsigned)a.T);
   if constexpr (F == WF_F32) MOE_LAUNCH(c, "decode_combine", decode_combine_kernel<float>, cg, dim3(256), 0, a);
