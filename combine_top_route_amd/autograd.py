@@ -425,11 +425,14 @@ class _Router(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_router, logits_dtype):
         ctx.save_for_backward(x, w_router)
+        ctx.set_materialize_grads(False)  # no zeros to add where only the logits were used
         return router_fwd(x, w_router, logits_dtype), x.view_as(x)
 
     @staticmethod
     def backward(ctx, dlogits, dx_in):
         x, w_router = ctx.saved_tensors
+        if dlogits is None:  # the logits were not used
+            return dx_in, None, None
         dx, dw = router_bwd(dlogits, x, w_router, dx_in)
         return dx, dw, None
 

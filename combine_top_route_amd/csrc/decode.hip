@@ -1147,8 +1147,8 @@ hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
 }  // namespace
 
 hipError_t launch_decode(const LaunchCtx& c, DecodeArgs a, int weights) {
-  // 8 tokens above, 3072 work-groups: 103 us with each routing for itself, 98
-  // with a launch before; 4 tokens, 1536: 58.9 both ways
+  // 8 tokens above, 48 work-groups a slot: 103 us with each routing for itself, 98
+  // with a launch before; 4 tokens: 58.9 both ways
   a.route_inline = inline_route_fits(a.T, a.k, a.E) && gu_groups(a) <= 1024;
 #define TOPK(LT, KPL)                                                                                   \
   MOE_LAUNCH(c, "decode_route", (decode_topk_kernel<LT, KPL>), dim3((unsigned)a.T), dim3(64), 0,        \

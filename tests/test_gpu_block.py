@@ -169,3 +169,22 @@ def test_captured_step_beside_a_live_eager_graph():
         for a, b in zip(grads, want):
             assert torch.equal(a, b)
     assert live.shape == (T, d)
+
+
+def test_router_alone():
+    """Without a gradient through x's other use nothing is added; compiled and
+    eager calls agree; logits that nothing uses leave x's gradient as it is."""
+    from combine_top_route_amd.autograd import _Router, router
+    leaves, _ = tensors(torch.bfloat16, seed=9)
+    x, wr = (t.requires_grad_() for t in leaves[:2])
+    g = torch.randn((T, E), generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    want = B.router_backward(g, x.detach(), wr.detach())
+    for fn in (router, torch.compile(lambda *a: router(*a), fullgraph=True, backend="aot_eager")):
+        logits = fn(x, wr)
+        assert torch.equal(logits, B.router_logits(x.detach(), wr.detach()))
+        for a, b in zip(torch.autograd.grad(logits, (x, wr), g), want):
+            assert torch.equal(a, b)
+    dx_in = torch.randn((T, d), generator=torch.Generator(device=DEV).manual_seed(4), device=DEV).bfloat16()
+    through = _Router.apply(x, wr, torch.float32)[1]
+    got = torch.autograd.grad(through, (x, wr), dx_in, allow_unused=True)
+    assert torch.equal(got[0], dx_in) and got[1] is None
