@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -152,14 +153,14 @@ def saved_size(shape: MoeShape) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
     """torch's current stream on a device, as the library takes it (the raw
     handle: building a torch.cuda.Stream object costs 2 us a call)."""
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(
-        torch.cuda.current_device() if device.index is None else device.index))
+    return torch._C._cuda_getCurrentRawStream(
+        torch.cuda.current_device() if device.index is None else device.index)
 
 
 _HERE = contextlib.nullcontext()
@@ -178,7 +179,7 @@ def _need(t, name, shape, dtype, device):
         raise ValueError(f"{name} is required")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -306,7 +307,26 @@ def _router_shape(x, w_router, logits_dtype) -> MoeShape:
         raise ValueError(f"x has dtype {x.dtype}, the logits {logits_dtype}, expected two of {tuple(_DT)}")
     _need(x, "x", x.shape, x.dtype, x.device)
     _need(w_router, "w_router", w_router.shape, x.dtype, x.device)
-    return make_shape(x.shape[0], x.shape[1], w_router.shape[0], 1, 8, x.dtype, logits_dtype)
+    return _shape_of(x.shape[0], x.shape[1], w_router.shape[0], 1, 8, x.dtype, logits_dtype, 0.0)
+
+
+# The argument structs and sizes of recent calls: making one and asking for a
+# size costs as much as a small kernel.
+@functools.lru_cache(maxsize=256)
+def _shape_of(T, d, E, k, I, dtype, logits_dtype, swiglu_limit):
+    return make_shape(T, d, E, k, I, dtype, logits_dtype, swiglu_limit=swiglu_limit)
+
+
+@functools.lru_cache(maxsize=256)
+def _rows_shape(T, k, I, dtype, swiglu_limit):
+    shape = make_shape(T, 8, max(k, 1), k, I, dtype, swiglu_limit=swiglu_limit)
+    saved8_size(shape)  # refuses a bad T, k or I before anything is allocated
+    return shape
+
+
+@functools.lru_cache(maxsize=256)
+def _router_workspace(T, d, E, dtype):
+    return router_workspace_size(make_shape(T, d, E, 1, 8, dtype))
 
 
 def router_workspace_size(shape: MoeShape) -> int:
@@ -334,7 +354,7 @@ def router_backward(dlogits, x, w_router, dx_in=None):
     _need(dlogits, "dlogits", (x.shape[0], w_router.shape[0]), dlogits.dtype, dev)
     if dx_in is not None:
         _need(dx_in, "dx_in", x.shape, x.dtype, dev)
-    n = router_workspace_size(shape)
+    n = _router_workspace(x.shape[0], x.shape[1], w_router.shape[0], x.dtype)
     with _on(dev):
         dx, dw = torch.empty_like(x), torch.empty_like(w_router)
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
@@ -376,8 +396,7 @@ def swiglu_save8(H, routing: Routing | None, T, k, swiglu_limit=0.0):
         raise ValueError(f"H must be [T*k, 2I], got {tuple(H.shape)}")
     I = H.shape[1] // 2
     dev = _row_args(H, routing, T, k, "H", 2 * I)
-    shape = make_shape(T, 8, max(k, 1), k, I, H.dtype, swiglu_limit=swiglu_limit)
-    saved8_size(shape)  # refuses a bad T, k or I before anything is allocated
+    shape = _rows_shape(T, k, I, H.dtype, swiglu_limit)
     with _on(dev):
         aw = None if routing is None else torch.empty((T * k, I), dtype=H.dtype, device=dev)
         codes = torch.empty((T * k, 2 * I), dtype=torch.uint8, device=dev)
@@ -397,8 +416,7 @@ def swiglu_backward8(G, codes, scales, routing: Routing, T, k, swiglu_limit=0.0)
     dev = _row_args(G, routing, T, k, "G", I)
     _need(codes, "codes", (T * k, 2 * I), torch.uint8, dev)
     _need(scales, "scales", (T * k, 2 * -(-I // 32)), torch.uint8, dev)
-    shape = make_shape(T, 8, max(k, 1), k, I, G.dtype, swiglu_limit=swiglu_limit)
-    saved8_size(shape)
+    shape = _rows_shape(T, k, I, G.dtype, swiglu_limit)
     with _on(dev):
         dh = torch.empty((T * k, 2 * I), dtype=G.dtype, device=dev)
         aw = torch.empty((T * k, I), dtype=G.dtype, device=dev)
