@@ -15,6 +15,11 @@ kernel ...").  Here:
 * ``recompute=True`` keeps nothing from the forward: the backward reruns the
   gate/up GEMM from x (``moe_backward`` with ``saved == NULL``).
 
+Beside the layer: ``moe_fwd8`` / ``moe_bwd8`` (``save8=True``: the activations
+kept in 8 bits), ``router_fwd`` / ``router_bwd`` (the projection that makes the
+logits; ``router`` and, with the layer, ``moe_block``), and ``moe_decode`` (the
+layer for at most 256 tokens, without a gradient).
+
 Every call allocates its outputs and workspace from torch's caching
 allocator on the inputs' device and enqueues on torch's current stream.
 Routing comes from router logits; the gradient reaches them through the
