@@ -424,6 +424,10 @@ Layout8 layout8(const moe_shape* s, int op) {
 }
 
 // ------------------------------------------------------------------ router
+bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+  return (uintptr_t)p < (uintptr_t)q + nq && (uintptr_t)q < (uintptr_t)p + np;
+}
+
 RouterArgs router_args(const moe_shape* s, const void* x, const void* w) {
   RouterArgs a = {};
   a.T = (int)s->T;
@@ -439,15 +443,8 @@ RouterArgs router_args(const moe_shape* s, const void* x, const void* w) {
   return a;
 }
 
-struct RouterLayout {
-  size_t wf = 0, parts = 0, total = 0;
-};
-RouterLayout router_layout(const moe_shape* s) {
-  RouterLayout L;
-  const RouterPlan p = router_plan(s->T, s->d, s->E, s->dtype);
-  L.parts = align256(p.wf_bytes);
-  L.total = L.parts + sizeof(float) * p.runs * s->E * s->d;
-  return L;
+size_t router_workspace(const moe_shape* s) {  // the parts of dw
+  return sizeof(float) * router_plan(s->T, s->d, s->E, s->dtype).runs * s->E * s->d;
 }
 
 // ------------------------------------------------------------ few tokens
@@ -673,7 +670,7 @@ moe_status moe_router_forward(const moe_shape* shape, const void* x, const void*
 moe_status moe_router_workspace_size(const moe_shape* shape, size_t* bytes) {
   TRY(check_shape(shape));
   CHECK_PTR(bytes);
-  *bytes = router_layout(shape).total;
+  *bytes = router_workspace(shape);
   return MOE_OK;
 }
 
@@ -686,21 +683,28 @@ moe_status moe_router_backward(const moe_shape* shape, const void* dlogits, cons
   CHECK_PTR(w_router);
   CHECK_PTR(dx);
   CHECK_PTR(dw_router);
-  const RouterLayout L = router_layout(shape);
-  TRY(check_ws_bytes(L.total, workspace, workspace_bytes));
+  TRY(check_ws_bytes(router_workspace(shape), workspace, workspace_bytes));
   TRY(check_aligned16(dlogits, "dlogits"));
   TRY(check_aligned16(x, "x"));
   TRY(check_aligned16(w_router, "w_router"));
   if (dx_in) TRY(check_aligned16(dx_in, "dx_in"));
   TRY(check_aligned16(dx, "dx"));
   TRY(check_aligned16(dw_router, "dw_router"));
+  // dx is written while dw's work-groups still read
+  const size_t rows = elem_size(shape->dtype) * shape->T * shape->d;
+  const size_t wide = elem_size(shape->dtype) * shape->E * shape->d;
+  const size_t lg = elem_size(shape->logits_dtype) * shape->T * shape->E;
+  if (overlap(dx, rows, x, rows) || overlap(dx, rows, w_router, wide) || overlap(dx, rows, dlogits, lg) ||
+      overlap(dw_router, wide, x, rows) || overlap(dw_router, wide, w_router, wide) ||
+      overlap(dw_router, wide, dlogits, lg) || overlap(dx, rows, dw_router, wide) ||
+      (dx_in && (overlap(dw_router, wide, dx_in, rows) || (dx_in != dx && overlap(dx, rows, dx_in, rows)))))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dx and dw_router must not overlap an input or each other");
   RouterArgs a = router_args(shape, x, w_router);
   a.dlogits = dlogits;
   a.dx_in = dx_in;
   a.dx = dx;
   a.dw = dw_router;
-  a.wf = at(workspace, L.wf);
-  a.parts = (float*)at(workspace, L.parts);
+  a.parts = (float*)workspace;
   const LaunchCtx c = make_ctx(stream);
   (void)hipGetLastError();
   HIP_TRY(launch_router_bwd(c, a), "router_backward");

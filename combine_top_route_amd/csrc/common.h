@@ -224,7 +224,6 @@ hipError_t f32_bwd_gemms(const LaunchCtx& c, const LayerArgs& a, const void* dou
 // (router.hip) The router's projection and its gradients.
 struct RouterPlan {
   int64_t run_tokens, runs;  // dw is summed in `runs` parts of run_tokens tokens
-  int64_t wf_bytes;          // w in the order of the dx product's operands
 };
 RouterPlan router_plan(int64_t T, int64_t d, int64_t E, int dtype);
 struct RouterArgs {
@@ -236,12 +235,12 @@ struct RouterArgs {
   const void* dx_in;    // [T, d] or null
   void* dx;             // [T, d]
   void* dw;             // [E, d]
-  void* wf;             // workspace: w in operand order
   float* parts;         // [runs, E, d] workspace
   int64_t run_tokens;
   int runs;
   // set by the launcher
   int d_blocks, e_blocks, dw_groups, dx_eblocks, dx_blocks, dx_tokens, dx_groups;
+  bool dx_first;
 };
 hipError_t launch_router_fwd(const LaunchCtx& c, const RouterArgs& a, void* logits);
 hipError_t launch_router_bwd(const LaunchCtx& c, RouterArgs a);

@@ -188,19 +188,15 @@ hipError_t fwd_any(const LaunchCtx& c, const RouterArgs& a, void* logits) {
   return fwd_tokens<T, 8>(c, a, logits);
 }
 
-// ------------------------------------------------- backward, first launch
+// ---------------------------------------------------------------- backward
 // dw parts: work-group (E block of 128, d block of 128, run of tokens).  Steps
 // of TS tokens pass through two LDS buffers as they lie in memory,
 // [token][column], two more steps' loads in flight in registers; a transposing
 // LDS read (16-bit) or plain 4-byte reads (the K = 4 float32 MFMA) hand the
-// MFMA its token-contiguous operands.  Two work-groups share a CU, so that one's
-// staging and barriers run beside the other's products: 30 us at the size
-// above, of which loads and staging alone take 19; one work-group with 64-token
-// steps took 35, blocks of 64 experts with 64-token steps and half the parts 31.
-// Parts are float32 [run][E][d].
-// Each work-group then lays a piece of w out as the second launch's MFMA
-// operands (in work-groups of their own that took 2 us more: the others fill
-// the chip).
+// MFMA its token-contiguous operands.  Parts are float32 [run][E][d].  (In a
+// launch of its own with two work-groups per CU 30 us at the size above, of
+// which loads and staging alone took 19; one work-group with 64-token steps 35,
+// blocks of 64 experts with 64-token steps and half the parts 31.)
 constexpr int kDwE = 128, kDwD = 128;
 
 template <typename T> struct DwTile;
@@ -425,56 +421,44 @@ __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb,
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
         const int e = e0 + we + i * 16 + q * 4 + m, c = d0 + wd + j * 16 + col;
-        if (e < a.E && c < a.d) part[(int64_t)e * a.d + c] = acc[i][j][m];
+        if (e < a.E && c < a.d) {
+          if (a.runs > 1) part[(int64_t)e * a.d + c] = acc[i][j][m];
+          else ((T*)a.dw)[(int64_t)e * a.d + c] = from_f32<T>(acc[i][j][m]);
+        }
       }
 }
 
-// The second launch's operand layout of w.  A wave there takes 16 DT columns
-// of d, tile j of which holds columns base + DT col + j (so that its results
-// are DT neighbouring columns of a lane); step k of KS experts is 16 bytes a
-// lane: experts k KS + q 16/size .. of column col.  wf holds them [column
-// block][expert block of 128][j][k][lane], zeros past E and d.
+// dx: 8 waves, each with the operands of 16 DT columns of w and up to 128
+// experts in registers, over blocks of 32 tokens whose dlogits pass through LDS
+// once for all of them.  Tile j of a wave holds columns base + DT col + j, so a
+// lane's results are DT neighbouring columns.
+constexpr int kDxWaves = 8, kDxTok = 32, kDxE = 128;
 template <typename T> constexpr int dx_tiles = 8 / (int)sizeof(T);
-constexpr int kDxE = 128;
 template <typename T> constexpr int dx_steps = kDxE * (int)sizeof(T) / 64;
 
+// The DT operands of K step k: experts e0 .. of column c + j, 16 bytes a lane,
+// from 8 bytes (DT columns) of each expert's row; zeros past E and d.
 template <typename T>
-__device__ __forceinline__ void lay_out_w(const RouterArgs& a, int group, int groups) {
-  constexpr int DT = dx_tiles<T>, NK = dx_steps<T>, PER = 16 / (int)sizeof(T);
-  const int lane = threadIdx.x & 63, wave = tile::wave_id();
-  // 64 operands a wave, neighbouring lanes reading neighbouring columns of w
-  const int64_t chunks = (int64_t)((a.d + 16 * DT - 1) / (16 * DT)) * a.dx_eblocks * DT * NK;
-  for (int64_t ck = group + (int64_t)wave * groups; ck < chunks; ck += (int64_t)8 * groups) {
-    const int64_t blk = ck / (DT * NK);  // [column block][expert block]
-    const int i = (int)(ck % (DT * NK)) * 64 + lane;
-    const int j = i % DT, col = i / DT % 16, q = i / (16 * DT) % 4, k = i / (64 * DT);
-    const int cb = (int)(blk / a.dx_eblocks), eb = (int)(blk % a.dx_eblocks);
-    const int c = cb * 16 * DT + DT * col + j;
-    T v[PER];
+__device__ __forceinline__ void w_operands(u32x4_t (&o)[dx_tiles<T>], rsrc_t w, int e0, int E, int d, int c) {
+  constexpr int PER = 16 / (int)sizeof(T);
+  tile::u32x2_t v[PER];
 #pragma unroll
-    for (int m = 0; m < PER; ++m) {
-      const int e = eb * kDxE + k * 4 * PER + q * PER + m;
-      v[m] = e < a.E && c < a.d ? ((const T*)a.w)[(int64_t)e * a.d + c] : (T)0;
-    }
-    *(u32x4_t*)((T*)a.wf + ((blk * DT + j) * NK + k) * 64 * PER + (q * 16 + col) * PER) = *(const u32x4_t*)v;
+  for (int m = 0; m < PER; ++m) {
+    const uint32_t at = (uint32_t)((e0 + m) * d + c) * (uint32_t)sizeof(T);
+    v[m] = __builtin_bit_cast(tile::u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
+                                                 w, (int)(e0 + m < E && c < d ? at : kPast), 0, 0));
   }
+#pragma unroll
+  for (int j = 0; j < dx_tiles<T>; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4)
+        o[j][i] = v[i][j];
+      else
+        o[j][i] = __builtin_amdgcn_perm(v[2 * i + 1][j >> 1], v[2 * i][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
+    }
 }
 
-template <typename T, typename LT>
-__global__ __launch_bounds__(512, 4) void router_dw_kernel(RouterArgs a) {
-  extern __shared__ __align__(16) char smem[];
-  int b = xcd_share((int)blockIdx.x, a.dw_groups);
-  const int db = b % a.d_blocks;
-  b /= a.d_blocks;
-  dw_part<T, LT>(a, smem, b % a.e_blocks, db, b / a.e_blocks);
-  lay_out_w<T>(a, blockIdx.x, a.dw_groups);
-}
-
-// ------------------------------------------------ backward, second launch
-// dx: work-group of 4 waves, each with the operands of its 16 DT columns and
-// up to 128 experts in registers, over blocks of 32 tokens whose dlogits pass
-// through LDS once for all four.
-constexpr int kDxWaves = 4, kDxTok = 32;
 template <typename T> constexpr int dx_stride = 128 * (int)sizeof(T) + 16;  // bytes per token row in LDS
 template <typename T> struct DxPlace {
   static __device__ __forceinline__ int at(int r, int b) { return r * dx_stride<T> + b; }
@@ -494,20 +478,21 @@ __device__ __forceinline__ void dx_part(const RouterArgs& a, char* smem, int cb,
   const bool in = c < a.d;
   const bool vec = dl_vec<T, LT>(a);
   const int ebs = a.dx_eblocks;
-  const T* wp = (const T*)a.wf + (int64_t)wcb * ebs * DT * NK * 64 * PER + lane * PER;
-  u32x4_t wv[DT][MULTI ? 1 : NK];
+  const rsrc_t wb = buffer_of(a.w, (uint64_t)a.E * a.d * sizeof(T));
+  u32x4_t wv[MULTI ? 1 : NK][DT];
   if (!MULTI && busy) {
 #pragma unroll
-    for (int j = 0; j < DT; ++j)
-#pragma unroll
-      for (int k = 0; k < NK; ++k) wv[j][MULTI ? 0 : k] = *(const u32x4_t*)(wp + (j * NK + k) * 64 * PER);
+    for (int k = 0; k < NK; ++k) {
+      w_operands<T>(wv[MULTI ? 0 : k], wb, (k * 4 + q) * PER, a.E, a.d, c);
+      __builtin_amdgcn_sched_barrier(0);  // one step's loads at a time hold registers
+    }
   }
   const int64_t tb = (int64_t)run * a.dx_tokens, te = tb + a.dx_tokens < a.T ? tb + a.dx_tokens : a.T;
   DlTile<T, LT, kDxTok, kDxWaves * 64, DxPlace<T>> dl;
   auto fetch = [&](int64_t t, int eb) {
     dl.load((const LT*)a.dlogits + t * a.E, a.E, eb * kDxE, (int)(te - t < kDxTok ? te - t : kDxTok), vec);
   };
-  uint2 old[2][4];
+  tile::u32x2_t old[2][4];
   f32x4_t acc[HG][DT];
   auto clear = [&]() {
 #pragma unroll
@@ -520,53 +505,58 @@ __device__ __forceinline__ void dx_part(const RouterArgs& a, char* smem, int cb,
     const int at = (h * 16 + col) * ST + (k * 4 + q) * 16;
     const u32x4_t hv = *(const u32x4_t*)(hs + at);
 #pragma unroll
-    for (int j = 0; j < DT; ++j) acc[g][j] = mma16<T>(hv, wv[j][MULTI ? 0 : k], acc[g][j]);
+    for (int j = 0; j < DT; ++j) acc[g][j] = mma16<T>(hv, wv[MULTI ? 0 : k][j], acc[g][j]);
     if constexpr (LO) {
       const u32x4_t lv = *(const u32x4_t*)(ls + at);
 #pragma unroll
-      for (int j = 0; j < DT; ++j) acc[g][j] = mma16<T>(lv, wv[j][MULTI ? 0 : k], acc[g][j]);
+      for (int j = 0; j < DT; ++j) acc[g][j] = mma16<T>(lv, wv[MULTI ? 0 : k][j], acc[g][j]);
     }
   };
-  // result row 4 q + m is a token, and tile j column c + j of it
+  // result row 4 q + m is a token, and tile j column c + j of it; rows past the
+  // run's end lie past the buffers' and are neither read nor written
+  const uint32_t rowb = (uint32_t)a.d * sizeof(T);
+  auto rows_at = [&](const void* p, int64_t t0) {
+    return buffer_of((const T*)p + t0 * a.d, (uint64_t)(te - t0 < kDxTok ? te - t0 : kDxTok) * rowb);
+  };
+  auto place = [&](int h, int m) {
+    return (int)(in ? (uint32_t)(h * 16 + q * 4 + m) * rowb + (uint32_t)c * (uint32_t)sizeof(T) : kPast);
+  };
   auto write = [&](int64_t t0, int g, int h) {
+    const rsrc_t out = rows_at(a.dx, t0);
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      const int64_t t = t0 + h * 16 + q * 4 + m;
-      if (t < te && in) {
-        float v[DT];
+      float v[DT];
 #pragma unroll
-        for (int j = 0; j < DT; ++j) v[j] = acc[g][j][m];
-        uint2 o;
-        if constexpr (sizeof(T) == 2) {
-          if (a.dx_in) {
-            v[0] += __uint_as_float(old[h][m].x << 16);
-            v[1] += __uint_as_float(old[h][m].x & 0xffff0000u);
-            v[2] += __uint_as_float(old[h][m].y << 16);
-            v[3] += __uint_as_float(old[h][m].y & 0xffff0000u);
-          }
-          o = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        } else {
-          if (a.dx_in) {
-            v[0] += __uint_as_float(old[h][m].x);
-            v[1] += __uint_as_float(old[h][m].y);
-          }
-          o = uint2{__float_as_uint(v[0]), __float_as_uint(v[1])};
+      for (int j = 0; j < DT; ++j) v[j] = acc[g][j][m];
+      tile::u32x2_t o;
+      if constexpr (sizeof(T) == 2) {
+        if (a.dx_in) {
+          v[0] += __uint_as_float(old[h][m][0] << 16);
+          v[1] += __uint_as_float(old[h][m][0] & 0xffff0000u);
+          v[2] += __uint_as_float(old[h][m][1] << 16);
+          v[3] += __uint_as_float(old[h][m][1] & 0xffff0000u);
         }
-        *(uint2*)((T*)a.dx + t * a.d + c) = o;
+        o = tile::u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      } else {
+        if (a.dx_in) {
+          v[0] += __uint_as_float(old[h][m][0]);
+          v[1] += __uint_as_float(old[h][m][1]);
+        }
+        o = tile::u32x2_t{__float_as_uint(v[0]), __float_as_uint(v[1])};
       }
+      __builtin_amdgcn_raw_buffer_store_b64(o, out, place(h, m), 0, 0);
     }
   };
   fetch(tb, 0);
   int buf = 0;
   for (int64_t t0 = tb; t0 < te; t0 += kDxTok) {
-    if (a.dx_in && busy && in) {
+    if (a.dx_in && busy) {
+      const rsrc_t src = rows_at(a.dx_in, t0);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int64_t t = t0 + h * 16 + q * 4 + m;
-          if (t < te) old[h][m] = *(const uint2*)((const T*)a.dx_in + t * a.d + c);
-        }
+        for (int m = 0; m < 4; ++m)
+          old[h][m] = __builtin_bit_cast(tile::u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(src, place(h, m), 0, 0));
     }
     if (MULTI) clear();
     for (int eb = 0; eb < (MULTI ? ebs : 1); ++eb, buf ^= 1) {
@@ -581,9 +571,7 @@ __device__ __forceinline__ void dx_part(const RouterArgs& a, char* smem, int cb,
 #pragma unroll 1
         for (int k = 0; k < NK; ++k) {
           if (eb * kDxE + k * 4 * PER >= a.E) break;
-#pragma unroll
-          for (int j = 0; j < DT; ++j)
-            wv[j][0] = *(const u32x4_t*)(wp + (((int64_t)eb * DT + j) * NK + k) * 64 * PER);
+          w_operands<T>(wv[0], wb, eb * kDxE + (k * 4 + q) * PER, a.E, a.d, c);
           step(hs, ls, 0, 0, k);
           step(hs, ls, 1, 1, k);
         }
@@ -608,25 +596,26 @@ __device__ __forceinline__ void dx_part(const RouterArgs& a, char* smem, int cb,
 // dw = the sum of the parts: 4 values a lane, every fourth run a wave, then the
 // four waves' sums in order (6726 tokens, d = 136, E = 6: 17 us with all runs in
 // one wave, 6 so).
+constexpr int kJoinWaves = 4;
 template <typename T>
-__device__ __forceinline__ void join_dw(const RouterArgs& a, char* smem, int b) {
+__global__ __launch_bounds__(kJoinWaves * 64) void router_join_kernel(RouterArgs a) {
+  __shared__ f32x4_t sums[kJoinWaves * 64];
   const int lane = threadIdx.x & 63, wave = tile::wave_id();
-  const int64_t n = (int64_t)a.E * a.d, i = ((int64_t)b * 64 + lane) * 4;
+  const int64_t n = (int64_t)a.E * a.d, i = ((int64_t)blockIdx.x * 64 + lane) * 4;
   f32x4_t s = {0, 0, 0, 0};
   if (i < n) {  // d is a multiple of 8: whole groups of 4
 #pragma unroll 8
-    for (int r = wave; r < a.runs; r += kDxWaves) {
+    for (int r = wave; r < a.runs; r += kJoinWaves) {
       const f32x4_t v = *(const f32x4_t*)(a.parts + r * n + i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[j] += v[j];
     }
   }
-  f32x4_t* sums = (f32x4_t*)smem;
   sums[threadIdx.x] = s;
   __syncthreads();
   if (wave != 0 || i >= n) return;
 #pragma unroll
-  for (int w = 1; w < kDxWaves; ++w) {
+  for (int w = 1; w < kJoinWaves; ++w) {
     const f32x4_t v = sums[w * 64 + lane];
 #pragma unroll
     for (int j = 0; j < 4; ++j) s[j] += v[j];
@@ -635,29 +624,46 @@ __device__ __forceinline__ void join_dw(const RouterArgs& a, char* smem, int b) 
   else *(uint2*)((bf16_t*)a.dw + i) = uint2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
 }
 
+template <typename T, typename LT>
+constexpr size_t bwd_smem() {
+  const size_t w = 2 * dw_stage<T, LT>(), x = 4 * kDxTok * dx_stride<T>;
+  return w > x ? w : x;
+}
+
+// The dw work-groups and the dx ones, one of each on a CU at a time: dw waits for
+// its barriers and LDS while dx moves rows, and the other way round (in a launch
+// each, two work-groups of one kind on a CU: 30 and 35 us at the size above;
+// together 54).  The longer ones start first: dx where the rows are many (16384
+// tokens, d = 2048: 56 us with dw first, 53 with dx; 2048 tokens: 11.8 and 13.3).
 template <typename T, typename LT, bool MULTI>
-__global__ __launch_bounds__(kDxWaves * 64, 2) void router_dx_kernel(RouterArgs a) {
-  __shared__ __align__(16) char smem[4 * kDxTok * dx_stride<T>];
-  const int b = blockIdx.x;
-  if (b < a.dx_groups) {
-    const int p = xcd_share(b, a.dx_groups);
-    dx_part<T, LT, MULTI>(a, smem, p % a.dx_blocks, p / a.dx_blocks);
+__global__ __launch_bounds__(512, 4) void router_bwd_kernel(RouterArgs a) {
+  extern __shared__ __align__(16) char smem[];
+  int b = (int)blockIdx.x - (a.dx_first ? a.dx_groups : 0);
+  if (a.dx_first ? b >= 0 : b < a.dw_groups) {
+    b = xcd_share(b, a.dw_groups);
+    const int db = b % a.d_blocks;
+    b /= a.d_blocks;
+    dw_part<T, LT>(a, smem, b % a.e_blocks, db, b / a.e_blocks);
   } else {
-    join_dw<T>(a, smem, b - a.dx_groups);
+    b = xcd_share(a.dx_first ? b + a.dx_groups : b - a.dw_groups, a.dx_groups);
+    dx_part<T, LT, MULTI>(a, smem, b % a.dx_blocks, b / a.dx_blocks);
   }
 }
 
+template <typename T, typename LT, bool MULTI>
+hipError_t bwd(const LaunchCtx& c, const RouterArgs& a) {
+  constexpr size_t smem = bwd_smem<T, LT>();
+  HIP_RET(tile::allow_smem_once<router_bwd_kernel<T, LT, MULTI>>(smem));
+  MOE_LAUNCH(c, "router_bwd", (router_bwd_kernel<T, LT, MULTI>), dim3((unsigned)(a.dw_groups + a.dx_groups)), dim3(512),
+             smem, a);
+  if (a.runs > 1)
+    MOE_LAUNCH(c, "router_join", router_join_kernel<T>, dim3((unsigned)cdiv((int64_t)a.E * a.d, 256)),
+               dim3(kJoinWaves * 64), 0, a);
+  return hipSuccess;
+}
 template <typename T, typename LT>
 hipError_t bwd(const LaunchCtx& c, const RouterArgs& a) {
-  constexpr size_t smem = 2 * dw_stage<T, LT>();
-  HIP_RET(tile::allow_smem_once<router_dw_kernel<T, LT>>(smem));
-  MOE_LAUNCH(c, "router_dw", (router_dw_kernel<T, LT>), dim3((unsigned)a.dw_groups), dim3(512), smem, a);
-  const dim3 grid((unsigned)(a.dx_groups + cdiv((int64_t)a.E * a.d, 256)));
-  if (a.dx_eblocks > 1)
-    MOE_LAUNCH(c, "router_dx", (router_dx_kernel<T, LT, true>), grid, dim3(kDxWaves * 64), 0, a);
-  else
-    MOE_LAUNCH(c, "router_dx", (router_dx_kernel<T, LT, false>), grid, dim3(kDxWaves * 64), 0, a);
-  return hipSuccess;
+  return a.dx_eblocks > 1 ? bwd<T, LT, true>(c, a) : bwd<T, LT, false>(c, a);
 }
 
 }  // namespace
@@ -665,14 +671,14 @@ hipError_t bwd(const LaunchCtx& c, const RouterArgs& a) {
 RouterPlan router_plan(int64_t T, int64_t d, int64_t E, int dtype) {
   RouterPlan p;
   const int step = dtype == F32 ? DwTile<float>::TS : DwTile<bf16_t>::TS;
-  // two work-groups per CU, in whole steps; more runs cost more (E d floats of
-  // traffic each way) than they hide
+  // A work-group per CU, beside a dx one, in whole steps: more cost more parts
+  // (E d floats of traffic each way) than they hide (two: 66 us instead of 55 at
+  // the size above).  Up to four steps are one run, whose sums are dw itself
+  // without a second launch (51 tokens: 15.0 us with two runs, 12.0).
   const int64_t tiles = cdiv(d, kDwD) * cdiv(E, kDwE);
-  const int64_t want = 512 / tiles < 1 ? 1 : 512 / tiles;
-  p.run_tokens = cdiv(cdiv(T, step), want) * step;
+  const int64_t want = 256 / tiles < 1 ? 1 : 256 / tiles;
+  p.run_tokens = T <= 4 * step ? 4 * step : cdiv(cdiv(T, step), want) * step;
   p.runs = cdiv(T, p.run_tokens);
-  const int64_t cols = 16 * (dtype == F32 ? dx_tiles<float> : dx_tiles<bf16_t>);
-  p.wf_bytes = cdiv(d, cols) * cols * cdiv(E, kDxE) * kDxE * (dtype == F32 ? 4 : 2);
   return p;
 }
 
@@ -686,10 +692,11 @@ hipError_t launch_router_bwd(const LaunchCtx& c, RouterArgs a) {
   a.dw_groups = a.d_blocks * a.e_blocks * a.runs;
   a.dx_eblocks = (int)cdiv(a.E, kDxE);
   a.dx_blocks = (int)cdiv(a.d, 16 * (a.dtype == F32 ? dx_tiles<float> : dx_tiles<bf16_t>) * kDxWaves);
-  // two work-groups per CU (each first loads its part of w), in whole blocks
-  const int64_t tok = cdiv(cdiv((int64_t)a.T * a.dx_blocks, 512), kDxTok) * kDxTok;
+  // a work-group per CU (each first loads its part of w), in whole blocks
+  const int64_t tok = cdiv(cdiv((int64_t)a.T * a.dx_blocks, 256), kDxTok) * kDxTok;
   a.dx_tokens = (int)tok;
   a.dx_groups = a.dx_blocks * (int)cdiv(a.T, tok);
+  a.dx_first = (int64_t)a.T * a.d * (a.dtype == F32 ? 4 : 2) > int64_t(32) << 20;
   if (a.dtype == F32) return a.logits_dtype == F32 ? bwd<float, float>(c, a) : bwd<float, bf16_t>(c, a);
   return a.logits_dtype == F32 ? bwd<bf16_t, float>(c, a) : bwd<bf16_t, bf16_t>(c, a);
 }

@@ -254,8 +254,9 @@ moe_status moe_backward(const moe_shape* shape, const void* dout, const void* x,
  *   dw_router [E,d] = dlogits^T x;
  * all others in dtype; float32 sums in a fixed order, one rounding each.  With
  * dtype MOE_BF16 a float32 dlogits enters the products as the sum of two bf16
- * values (2^-18 of it is lost).  Every pointer 16-byte aligned; workspace:
- * moe_router_workspace_size bytes, for the backward only. */
+ * values (2^-18 of it is lost).  Every pointer 16-byte aligned; dx and
+ * dw_router overlap no input (but dx_in, as said) and not each other;
+ * workspace: moe_router_workspace_size bytes, for the backward only. */
 moe_status moe_router_forward(const moe_shape* shape, const void* x, const void* w_router,
                               void* logits, void* stream);
 moe_status moe_router_workspace_size(const moe_shape* shape, size_t* bytes);

@@ -45,6 +45,16 @@ def test_router_backward():
     each(call, ("dl", "x", "w", "dx_in", "dx", "dw"), make_bad=lambda: P(8))
     assert call(ws=P(64)) == 1
     assert call(n=16) == 3 and "workspace" in B.lib().moe_last_error().decode()
+    # outputs over inputs and over each other: a byte of overlap is enough
+    far = dict(dl=P(1 << 20), x=P(2 << 20), w=P(3 << 20), dx=P(4 << 20), dw=P(5 << 20), ws=P(6 << 20))
+    rows, wide, lg = 4 * 256 * 2, 8 * 256 * 2, 4 * 8 * 4
+    for out, n_out in (("dx", rows), ("dw", wide)):
+        for other, base, n in (("dl", 1, lg), ("x", 2, rows), ("w", 3, wide)):
+            for off in (0, n - 16, 16 - n_out):
+                assert call(**{**far, out: P((base << 20) + off)}) == 1
+                assert "overlap" in B.lib().moe_last_error().decode()
+        assert call(**{**far, out: P((7 << 20) + 16), "dx_in": P(7 << 20)}) == 1
+    assert call(**{**far, "dx": P(5 << 20)}) == 1
     for T in (1, 100, 1 << 24):       # the parts' size stays bounded as T grows
         n = B.router_workspace_size(shape(T=T, k=1))
         assert 0 < n < 1 << 29
