@@ -483,7 +483,7 @@ constexpr size_t gu_smem() {  // per wave: gate, up, activations; then the waves
 
 // The tokens r0 .. r0 + 16 NB of the expert.  w holds the first units.
 template <int F, bool NT, int NW, int TB, int UN, int NB>
-__device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& rows, int r0, int n,
+__device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, bool again,
                                             GuWeights<F, TB, UN>& w, const GuTile<TB>& t, char* smem) {
   typedef typename Fmt<F>::act AT;
   const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
@@ -510,7 +510,7 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
     for (int m = 0; m < TB; ++m) ag[b][m] = au[b][m] = f32x4_t{0, 0, 0, 0};
   constexpr int UB = NB == 1 ? UN : 1;  // units whose activations are in flight together
   for (int base = wave * UN; base < units; base += NW * UN) {
-    if (base != wave * UN || r0) load_gu<F, NT>(w, t, a.I, K, base);
+    if (base != wave * UN || again) load_gu<F, NT>(w, t, a.I, K, base);
 #pragma unroll
     for (int i0 = 0; i0 < UN; i0 += UB) {
       u32x4_t xv[UB][NB][kActHalves<F>][2];
@@ -621,11 +621,12 @@ __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   load_gu<F, NT>(w, t, a.I, a.d, tile::wave_id() * UN);
   find.list(rows);
   if constexpr (NBMAX == 1) {
-    gateup_rows<F, NT, NW, TB, UN, 1>(a, rows, 0, n, w, t, smem);
+    gateup_rows<F, NT, NW, TB, UN, 1>(a, rows, 0, n, false, w, t, smem);
   } else {
-    for (int r0 = blockIdx.z * 16 * NBMAX; r0 < n; r0 += gridDim.z * 16 * NBMAX) {
-      if (n - r0 <= 16) gateup_rows<F, NT, NW, TB, UN, 1>(a, rows, r0, n, w, t, smem);
-      else gateup_rows<F, NT, NW, TB, UN, NBMAX>(a, rows, r0, n, w, t, smem);
+    const int first = blockIdx.z * 16 * NBMAX;
+    for (int r0 = first; r0 < n; r0 += gridDim.z * 16 * NBMAX) {
+      if (n - r0 <= 16) gateup_rows<F, NT, NW, TB, UN, 1>(a, rows, r0, n, r0 != first, w, t, smem);
+      else gateup_rows<F, NT, NW, TB, UN, NBMAX>(a, rows, r0, n, r0 != first, w, t, smem);
     }
   }
 }
