@@ -556,7 +556,7 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int m = 0; m < TB; ++m) {
-      float* p = red + (((wave * NB + b) * TB + m) * 2 * 16 + col) * 16 + q * 4;
+      float* p = red + ((wave * NB + b) * TB + m) * 512 + part_at(col, q);
       *(f32x4_t*)p = ag[b][m];
       *(f32x4_t*)(p + 256) = au[b][m];
     }
@@ -569,7 +569,7 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
       float g = 0.0f, u = 0.0f;
 #pragma unroll
       for (int v = 0; v < NW; ++v) {
-        const float* p = red + (((v * NB + b) * TB + tb) * 2 * 16 + c) * 16 + m;
+        const float* p = red + ((v * NB + b) * TB + tb) * 512 + part_at(c, m >> 2) + (m & 3);
         g += p[0];
         u += p[256];
       }
@@ -730,14 +730,14 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_kernel(DecodeArgs
     }
   }
   __syncthreads();  // red lies over the waves' work space
-  *(f32x4_t*)(red + (wave * 16 + col) * 16 + q * 4) = acc;
+  *(f32x4_t*)(red + wave * 256 + part_at(col, q)) = acc;
   __syncthreads();
   for (int o = threadIdx.x; o < 256; o += kDownWaves * 64) {
     const int t = o >> 4, m = o & 15;
     if (t < a.T && n0 + m < a.d) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kDownWaves; ++w) v += red[(w * 16 + t) * 16 + m];
+      for (int w = 0; w < kDownWaves; ++w) v += red[w * 256 + part_at(t, m >> 2) + (m & 3)];
       ((AT*)a.out)[(int64_t)t * a.d + n0 + m] = from_f32<AT>(v);
     }
   }
@@ -931,14 +931,15 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
     static_assert(TB == 1, "a part is 16 rows");
     __syncthreads();
 #pragma unroll
-    for (int b = 0; b < NB; ++b) *(f32x4_t*)(red + ((wave * NB + b) * 16 + col) * 16 + q * 4) = acc[b][0];
+    for (int b = 0; b < NB; ++b) *(f32x4_t*)(red + (wave * NB + b) * 256 + part_at(col, q)) = acc[b][0];
     __syncthreads();
     for (int o = threadIdx.x; o < NB * 64; o += kDownRowWaves * 64) {
       const int r = r0 + (o >> 2), row = t.n0 + (o & 3) * 4;
-      f32x4_t s = *(const f32x4_t*)(red + o * 4);
+      const float* p = red + (o >> 6) * 256 + part_at((o >> 2) & 15, o & 3);
+      f32x4_t s = *(const f32x4_t*)p;
 #pragma unroll
       for (int w = 1; w < kDownRowWaves; ++w) {
-        const f32x4_t v = *(const f32x4_t*)(red + (w * NB * 64 + o) * 4);
+        const f32x4_t v = *(const f32x4_t*)(p + w * NB * 256);
 #pragma unroll
         for (int m = 0; m < 4; ++m) s[m] += v[m];
       }

@@ -129,13 +129,14 @@ __global__ __launch_bounds__(kFwdWaves * 64, 2) void router_fwd_kernel(const T* 
     for (int m = 0; m < MR; ++m)
 #pragma unroll
       for (int n = 0; n < NB; ++n)
-        *(f32x4_t*)(red + (((wave * MR + m) * NB + n) * 16 + col) * 16 + q * 4) = acc[m0 + m][n];
+        *(f32x4_t*)(red + ((wave * MR + m) * NB + n) * 256 + part_at(col, q)) = acc[m0 + m][n];
     __syncthreads();
     for (int o = threadIdx.x; o < MR * NB * 64; o += kFwdWaves * 64) {
       f32x4_t s = {0, 0, 0, 0};
 #pragma unroll
       for (int v = 0; v < kFwdWaves; ++v) {
-        const f32x4_t p = *(const f32x4_t*)(red + (v * MR * NB * 64 + o) * 4);
+        const f32x4_t p =
+            *(const f32x4_t*)(red + (v * MR * NB + (o >> 6)) * 256 + part_at((o >> 2) & 15, o & 3));
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[i] += p[i];
       }

@@ -66,5 +66,11 @@ __device__ __forceinline__ u32x4_t get_chunk(const lds_t* p, int row, int chunk)
   return *(const __attribute__((address_space(3))) u32x4_t*)(p + row_chunk(row, chunk));
 }
 
+// A 16 x 16 float result on its way to be added to other waves': where a lane
+// puts rows 4 q .. of its column (16 bytes, as the MFMA leaves them).  A column
+// takes 64 bytes, its four pieces permuted so that 16 lanes meet all banks once
+// (router forward at 16384 tokens, d = 2048, E = 128: 21.3 us without, 19.8).
+__device__ __forceinline__ int part_at(int col, int q) { return col * 16 + ((q ^ (col >> 2)) & 3) * 4; }
+
 }  // namespace rowload
 }  // namespace moe
