@@ -463,8 +463,8 @@ DecodeLayout decode_layout(const moe_shape* s) {
   const int64_t R = s->T * s->k;
   L.mid = take(sizeof(int32_t) * R);
   L.mw = take(sizeof(float) * R);
-  L.aw = take(elem_size(s->dtype) * R * s->I);
-  if (!decode_one_down(s->T, s->k, s->d)) L.y = take(sizeof(float) * R * s->d);
+  L.aw = take(sizeof(float) * R * s->I);  // float32, or two planes of bf16
+  if (!decode_one_down(s->T, s->k)) L.y = take(sizeof(float) * R * s->d);
   L.total = off;
   return L;
 }
@@ -927,7 +927,7 @@ moe_status moe_decode(const moe_shape* shape, int weights, const void* x, moe_ro
   a.mid = (int32_t*)at(workspace, L.mid);
   a.mw = (float*)at(workspace, L.mw);
   a.aw = at(workspace, L.aw);
-  a.y = decode_one_down(shape->T, shape->k, shape->d) ? nullptr : (float*)at(workspace, L.y);
+  a.y = decode_one_down(shape->T, shape->k) ? nullptr : (float*)at(workspace, L.y);
   const LaunchCtx c = make_ctx(stream);
   (void)hipGetLastError();
   HIP_TRY(launch_decode(c, a, weights), "decode");

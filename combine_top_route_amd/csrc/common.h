@@ -248,12 +248,12 @@ hipError_t launch_router_bwd(const LaunchCtx& c, RouterArgs a);
 // ------------------------------------------------------------ few tokens
 // The whole layer for up to kDecodeMaxT tokens (decode.hip).
 constexpr int kDecodeMaxT = 256;
-// Whether the down products of all experts are summed in one kernel (at most 16
-// tokens): its work-groups are one per 16 rows of d, so it takes a d that
-// fills the chip with them, or few slots.  Otherwise the products of each slot
-// go through memory.  (16 tokens of 8 of 128 experts, d = 2048, I = 768, bf16:
-// 59 us in one kernel, 50 in two; at d = 4096, 64 experts, e4m3: 44 in one.)
-inline bool decode_one_down(int64_t T, int64_t k, int64_t d) { return T <= 16 && (d >= 16 * 256 || T * k <= 64); }
+// Whether the down products of all experts are summed in one kernel (at most 32
+// slots of 8 tokens); otherwise the products of each slot go through memory and
+// a combine kernel (d = 2048, I = 768, 8 of 128 experts, bf16: 2 tokens 12.6 us
+// for the down product in one kernel; 4 tokens 19.2 and 17.7 + 4.0; 8 tokens,
+// 64 slots, 36.4 and 28.7 + 4.0).
+inline bool decode_one_down(int64_t T, int64_t k) { return T <= 8 && T * k <= 32; }
 struct DecodeArgs {
   int T, d, E, k, I;
   int dtype;              // of x, out and aw (and of uncoded weights)

@@ -243,17 +243,19 @@ __device__ __forceinline__ void to_frags(typename Fmt<F>::frag (&fr)[Fmt<F>::NF]
 }
 
 // The activations of 16 tokens that meet a unit's weights: the same values of
-// K, 128 bytes a token, or 256 beside codes.  Tokens 8.. are neither loaded
-// nor stored with `eight` (their columns hold anything and are dropped).
+// K, 128 bytes a token, or 256 beside codes.  Tokens 8.. come from r1, and are
+// neither loaded nor stored with `eight` (their columns hold anything and are
+// dropped).
 template <int F> constexpr int kActHalves = F >= WF_FP8 ? 2 : 1;
 template <int F>
-__device__ __forceinline__ void load_acts(u32x4_t (&v)[kActHalves<F>][2], rsrc_t r, const uint32_t (&row)[2],
-                                          const bool (&live)[2], int unit, int bytes, bool eight) {
+__device__ __forceinline__ void load_acts(u32x4_t (&v)[kActHalves<F>][2], rsrc_t r, rsrc_t r1,
+                                          const uint32_t (&row)[2], const bool (&live)[2], int unit, int bytes,
+                                          bool eight) {
 #pragma unroll
   for (int h = 0; h < kActHalves<F>; ++h) {
     const int off = (unit * kActHalves<F> + h) * 128 + (int)(threadIdx.x & 7) * 16;
     v[h][0] = load16(r, row[0] + off, live[0] && off < bytes);
-    if (!eight) v[h][1] = load16(r, row[1] + off, live[1] && off < bytes);
+    if (!eight) v[h][1] = load16(r1, row[1] + off, live[1] && off < bytes);
   }
 }
 template <int F>
@@ -321,6 +323,24 @@ __device__ __forceinline__ float block_scale_of(const void* s, int n, int K, int
 __device__ __forceinline__ float swiglu(float g, float u, float lim) {
   const float gc = clip_gate(g, lim);
   return gc * sigmoidf_(gc) * clip_up(u, lim);
+}
+
+// The weighted activation on its way to the down product.  The bf16 MFMA takes
+// bf16 operands, and one rounding to bf16 here would be as large an error as the
+// output's own; so bf16 calls keep two planes, the value rounded and what that
+// left, rounded (2^-17 of the value is lost), and both are multiplied.
+__device__ __forceinline__ int64_t aw_plane(const DecodeArgs& a) { return (int64_t)a.T * a.k * a.I; }
+template <typename AT>
+__device__ __forceinline__ void put_aw(const DecodeArgs& a, int64_t at, float v) {
+  if constexpr (sizeof(AT) == 4) {
+    ((float*)a.aw)[at] = v;
+  } else {
+    const bf16_t h = f2bf(v);
+    const float f = bf2f(h);
+    ((bf16_t*)a.aw)[at] = h;
+    // beside an infinity or NaN the rest would be NaN; h carries it alone
+    ((bf16_t*)a.aw)[aw_plane(a) + at] = fabsf(f) < __builtin_huge_valf() ? f2bf(v - f) : (bf16_t)0;
+  }
 }
 
 // The same routing inside the gate/up kernel, for a token or a few: every
@@ -517,7 +537,7 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
 #pragma unroll
       for (int i = 0; i < UB; ++i)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) load_acts<F>(xv[i][b], xb, xr[b], live[b], base + i0 + i, bytes, eight);
+        for (int b = 0; b < NB; ++b) load_acts<F>(xv[i][b], xb, xb, xr[b], live[b], base + i0 + i, bytes, eight);
       __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
 #pragma unroll
       for (int i = 0; i < UB; ++i) {
@@ -573,7 +593,7 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
         g += p[0];
         u += p[256];
       }
-      ((AT*)a.aw)[(int64_t)rows.slot[r] * a.I + row] = from_f32<AT>(rows.w[r] * swiglu(g, u, a.lim));
+      put_aw<AT>(a, (int64_t)rows.slot[r] * a.I + row, rows.w[r] * swiglu(g, u, a.lim));
     }
   }
   __syncthreads();
@@ -631,127 +651,16 @@ __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   }
 }
 
-// ---------------------------------------------- down product, up to 16 tokens
-// One work-group: 16 rows of d for all tokens and all experts.  An MFMA's
-// columns are the tokens, so one accumulator runs over every (expert, unit of
-// I) pair, and the combine is the sum itself (aw carries the weights).  aw is
-// rounded to the activations' type like the layer's, for the MFMA's operand.
+// ---------------------------------------------- down product, up to 32 slots
+// One work-group: 8 rows of d for all tokens; the waves take batches of the
+// (expert, unit of I) pairs, and the combine is the sum itself (aw carries the
+// weights).  The experts are found in the lanes of each wave, slot f in lane f,
+// without LDS or barriers.  An MFMA's rows and columns 0 .. 7 are the tile's
+// rows and the tokens at the first half of a unit, 8 .. 15 the same rows and
+// tokens at the second half; the two diagonal blocks of its result are the
+// sums, the others are dropped.  (T = 1, the case above: 23.1 us with tiles of
+// 16 rows, 22.4 with these.)
 constexpr int kDownWaves = 16;
-template <int F> constexpr int down_work() { return kDownWaves * (2048 + 2048 * kActHalves<F>); }
-
-template <int F, bool NT>
-__global__ __launch_bounds__(kDownWaves * 64) void decode_down_kernel(DecodeArgs a) {
-  typedef typename Fmt<F>::act AT;
-  extern __shared__ __align__(16) char smem[];
-  char* work = smem;                                      // per wave: a unit's weights and activations
-  float* red = (float*)smem;                              // then [waves][16 tokens][16 rows]
-  int* active = (int*)(work + down_work<F>());            // [E] experts with tokens
-  uint16_t* tab = (uint16_t*)(active + a.E);              // [E][T] slot of the token + 1, 0: none
-  __shared__ int counts[kDownWaves];
-  const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
-  const int R = a.T * a.k, cells = a.E * a.T;
-  for (int i = threadIdx.x; i < cells; i += kDownWaves * 64) tab[i] = 0;
-  __syncthreads();
-  for (int f = threadIdx.x; f < R; f += kDownWaves * 64) {
-    const int e = a.mid[f], t = f / a.k;
-    if (e >= 0) tab[e * a.T + t] = (uint16_t)(f - t * a.k + 1);
-  }
-  __syncthreads();
-  // E <= 1024 threads: expert e is thread e
-  bool on = false;
-  if ((int)threadIdx.x < a.E)
-    for (int t = 0; t < a.T; ++t) on |= tab[threadIdx.x * a.T + t] != 0;
-  const uint64_t has = __ballot(on);
-  if (lane == 0) counts[wave] = __popcll(has);
-  __syncthreads();
-  int before = 0, nact = 0;
-  for (int i = 0; i < kDownWaves; ++i) {
-    before += i < wave ? counts[i] : 0;
-    nact += counts[i];
-  }
-  if (on) active[before + __popcll(has & ((1ull << lane) - 1))] = threadIdx.x;
-  __syncthreads();
-
-  const int K = a.I, n0 = blockIdx.x * 16;
-  const int units = (K + Fmt<F>::UK - 1) / Fmt<F>::UK;
-  const int abytes = F >= WF_FP8 ? K : K * (int)sizeof(AT), bbytes = K * (int)sizeof(AT);
-  const uint64_t wbytes = (uint64_t)a.d * abytes;
-  uint32_t wrow[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) wrow[h] = (uint32_t)min(n0 + load_row(h), a.d - 1) * abytes;
-  const rsrc_t xb = buffer_of(a.aw, (uint64_t)a.T * a.k * bbytes);
-  const bool eight = a.T <= 8;
-  lds_t* lw = (lds_t*)work + wave * (2048 + 2048 * kActHalves<F>);
-  const int total = nact * units;
-  constexpr int UN = F >= WF_FP8 ? 2 : 4;
-  f32x4_t acc = {0, 0, 0, 0};
-  for (int base = wave * UN; base < total; base += kDownWaves * UN) {
-    u32x4_t wv[UN][2], xv[UN][kActHalves<F>][2];
-    uint32_t mx[UN];
-    float sb[UN];
-    bool on_expert[UN];
-#pragma unroll
-    for (int i = 0; i < UN; ++i) {
-      const int p = base + i;
-      const bool on = p < total;  // uniform in the wave
-      const int idx = on ? p / units : 0, unit = on ? p - idx * units : 0;
-      const int e = __builtin_amdgcn_readfirstlane(active[idx]);
-      load_rows<NT>(wv[i], buffer_of((const char*)a.w_down + e * wbytes, wbytes), wrow, unit * 128, on ? abytes : 0);
-      uint32_t xr[2];
-      bool live[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = load_row(h), j = t < a.T ? tab[e * a.T + t] : 0;
-        live[h] = on && j != 0;
-        xr[h] = (uint32_t)(t * a.k + j - 1) * bbytes;
-      }
-      load_acts<F>(xv[i], xb, xr, live, unit, bbytes, eight);
-      on_expert[i] = on && col < a.T && tab[e * a.T + min(col, a.T - 1)] != 0;
-      const char* sc = (const char*)a.s_down;
-      if (F == WF_FP8) sc += (int64_t)e * (a.d / 128) * (K / 128) * 4;
-      if (F == WF_MX) sc += (int64_t)e * a.d * (K / 32);
-      mx[i] = F == WF_MX ? ((const uint32_t*)sc)[(int64_t)(n0 + col) * (K >> 7) + unit] : 0;
-      sb[i] = block_scale_of<F>(sc, n0, K, unit);
-    }
-    __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
-#pragma unroll
-    for (int i = 0; i < UN; ++i) {
-      typename Fmt<F>::frag fr[Fmt<F>::NF];
-      u32x4_t xf[Fmt<F>::BV];
-      put_rows(lw, wv[i]);
-      put_acts<F>(lw + 2048, xv[i], eight);
-      to_frags<F>(fr, lw, mx[i], q, col);
-      get_acts<F>(xf, lw + 2048, q, col);
-      // a lane's results are its own column's: a token takes nothing from an
-      // expert that it did not choose, whatever that expert's weights hold
-      const f32x4_t s = unit_dot<F>(f32x4_t{0, 0, 0, 0}, fr, xf);
-#pragma unroll
-      for (int m = 0; m < 4; ++m) acc[m] = on_expert[i] ? fmaf(sb[i], s[m], acc[m]) : acc[m];
-    }
-  }
-  __syncthreads();  // red lies over the waves' work space
-  *(f32x4_t*)(red + wave * 256 + part_at(col, q)) = acc;
-  __syncthreads();
-  for (int o = threadIdx.x; o < 256; o += kDownWaves * 64) {
-    const int t = o >> 4, m = o & 15;
-    if (t < a.T && n0 + m < a.d) {
-      float v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kDownWaves; ++w) v += red[w * 256 + part_at(t, m >> 2) + (m & 3)];
-      ((AT*)a.out)[(int64_t)t * a.d + n0 + m] = from_f32<AT>(v);
-    }
-  }
-}
-
-// The same for at most 8 tokens with 64 slots in all: tiles of 8 rows, so twice
-// the work-groups, and the experts are found in the lanes of each wave, slot f
-// in lane f, without LDS or barriers.  An MFMA's rows and columns 0 .. 7 are
-// the tile's rows and the tokens at the first half of a unit, 8 .. 15 the same
-// rows and tokens at the second half; the two diagonal blocks of its result
-// are the sums, the others are dropped.  (T = 1, the case above: 23.1 us with the
-// kernel before, 22.4 with this one; 7 tokens in float32 22.8 and 21.6.)
-constexpr int kSmallT = 8;
-inline bool small_down(const DecodeArgs& a) { return a.T <= kSmallT && a.T * a.k <= kWave; }
 
 template <int F>
 __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(DecodeArgs a) {
@@ -771,13 +680,16 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(Deco
   const int abytes = F >= WF_FP8 ? K : K * (int)sizeof(AT), bbytes = K * (int)sizeof(AT);
   const uint64_t wbytes = (uint64_t)a.d * abytes;
   const uint32_t wrow = (uint32_t)min(n0 + load_row(0), a.d - 1) * abytes;
-  const rsrc_t xb = buffer_of(a.aw, (uint64_t)R * bbytes);
+  constexpr int P = F == WF_F32 ? 1 : 2;  // planes of aw
+  rsrc_t xb[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) xb[p] = buffer_of((const AT*)a.aw + p * aw_plane(a), (uint64_t)R * bbytes);
   lds_t* lw = (lds_t*)work + wave * WORK;
   const int total = nact * units;
   const uint64_t slots = a.k == 64 ? ~0ull : (1ull << a.k) - 1;  // a token's slots
   f32x4_t acc = {0, 0, 0, 0};
   for (int base = wave * UN; base < total; base += kDownWaves * UN) {
-    u32x4_t wv[UN], xv[UN][kActHalves<F>];
+    u32x4_t wv[UN], xv[UN][P][kActHalves<F>];
     uint32_t mx[UN];
     float sb[UN];
     bool on_expert[UN];
@@ -797,7 +709,8 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(Deco
 #pragma unroll
       for (int h = 0; h < kActHalves<F>; ++h) {
         const int o = (unit * kActHalves<F> + h) * 128 + (lane & 7) * 16;
-        xv[i][h] = load16(xb, xrow + o, on && ts && o < bbytes);
+#pragma unroll
+        for (int p = 0; p < P; ++p) xv[i][p][h] = load16(xb[p], xrow + o, on && ts && o < bbytes);
       }
       on_expert[i] = on && r8 < a.T && ((has >> (r8 * a.k)) & slots);
       const char* sc = (const char*)a.s_down;
@@ -816,15 +729,22 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(Deco
       const int chunk = lane & 7;
       turn_fence();
       *(__attribute__((address_space(3))) u32x4_t*)(lw + row_chunk(load_row(0), chunk)) = wv[i];
-#pragma unroll
-      for (int h = 0; h < kActHalves<F>; ++h)
-        *(__attribute__((address_space(3))) u32x4_t*)(lw + 2048 + h * 2048 + row_chunk(load_row(0), chunk)) = xv[i][h];
       turn_fence();
       typename Fmt<F>::frag fr[Fmt<F>::NF / 2];
-      u32x4_t xf[Fmt<F>::BV / 2];
       chunk_frags<F>(fr, get_chunk(lw, r8, 4 * half + q), mx[i], half, q);
-      chunk_acts<F>(xf, lw + 2048, half, q, r8);
-      const f32x4_t s = unit_dot<F, Fmt<F>::NF / 2>(f32x4_t{0, 0, 0, 0}, fr, xf);
+      f32x4_t s = {0, 0, 0, 0};
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        turn_fence();
+#pragma unroll
+        for (int h = 0; h < kActHalves<F>; ++h)
+          *(__attribute__((address_space(3))) u32x4_t*)(lw + 2048 + h * 2048 + row_chunk(load_row(0), chunk)) =
+              xv[i][p][h];
+        turn_fence();
+        u32x4_t xf[Fmt<F>::BV / 2];
+        chunk_acts<F>(xf, lw + 2048, half, q, r8);
+        s = unit_dot<F, Fmt<F>::NF / 2>(s, fr, xf);
+      }
 #pragma unroll
       for (int m = 0; m < 4; ++m) acc[m] = on_expert[i] ? fmaf(sb[i], s[m], acc[m]) : acc[m];
     }
@@ -858,7 +778,7 @@ struct DownTile {
   int row4, n0;
 };
 
-template <int F, bool NT, int TB, int UN, bool KS, int NB>
+template <int F, bool NT, int TB, int UN, bool KS, int NB, bool EIGHT = false>
 __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, const DownTile<TB>& t,
                                           lds_t* lw, float* red) {
   typedef typename Fmt<F>::act AT;
@@ -867,14 +787,18 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
   const int units = (K + Fmt<F>::UK - 1) / Fmt<F>::UK;
   const int abytes = F >= WF_FP8 ? K : K * (int)sizeof(AT), bbytes = K * (int)sizeof(AT);
   const rsrc_t xb = buffer_of(a.aw, (uint64_t)a.T * a.k * bbytes);
-  const bool eight = NB == 1 && n - r0 <= 8;
+  const rsrc_t xl = F == WF_F32 ? xb : buffer_of((const AT*)a.aw + aw_plane(a), (uint64_t)a.T * a.k * bbytes);
+  // P passes over a unit's weights, one for each plane of aw; with EIGHT (at most
+  // 8 rows) columns 8 .. are the same rows' second plane instead
+  static_assert(!EIGHT || (F != WF_F32 && NB == 1), "");
+  constexpr int P = F == WF_F32 || EIGHT ? 1 : 2;
   uint32_t xr[NB][2];
   bool live[NB][2];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = r0 + b * 16 + load_row(h);
+      const int r = r0 + b * 16 + load_row(EIGHT ? 0 : h);
       live[b][h] = r < n;
       xr[b][h] = (uint32_t)rows.slot[live[b][h] ? r : n - 1] * bbytes;
     }
@@ -899,15 +823,18 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
     for (int m = 0; m < TB; ++m) mx[m] = mx_words<F>(t.sc, t.row4 + 16 * m, K, base + (lane & 3));
 #pragma unroll
     for (int i0 = 0; i0 < UN; i0 += UB) {
-      u32x4_t xv[UB][NB][kActHalves<F>][2];
+      u32x4_t xv[UB][NB][P][kActHalves<F>][2];
 #pragma unroll
       for (int i = 0; i < UB; ++i)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) load_acts<F>(xv[i][b], xb, xr[b], live[b], base + i0 + i, bbytes, eight);
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+            load_acts<F>(xv[i][b][p], p ? xl : xb, p || EIGHT ? xl : xb, xr[b], live[b], base + i0 + i, bbytes, false);
       __builtin_amdgcn_sched_barrier(0);  // all loads leave before the first product waits
 #pragma unroll
       for (int i = 0; i < UB; ++i) {
-        u32x4_t xf[NB][Fmt<F>::BV];
+        u32x4_t xf[NB][P][Fmt<F>::BV];
 #pragma unroll
         for (int m = 0; m < TB; ++m) {
           typename Fmt<F>::frag fr[Fmt<F>::NF];
@@ -917,15 +844,24 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
           to_frags<F>(fr, lw, code, q, col);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            if (m == 0) {
-              put_acts<F>(lw + 2048, xv[i][b], eight);
-              get_acts<F>(xf[b], lw + 2048, q, col);
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+              if (m == 0) {
+                put_acts<F>(lw + 2048, xv[i][b][p], false);
+                get_acts<F>(xf[b][p], lw + 2048, q, col);
+              }
+              unit_mma<F>(acc[b][m], fr, xf[b][p], sb[i0 + i]);
             }
-            unit_mma<F>(acc[b][m], fr, xf[b], sb[i0 + i]);
           }
         }
       }
     }
+  }
+  if constexpr (EIGHT) {  // columns 8 .. belong to the columns eight before
+#pragma unroll
+    for (int m = 0; m < TB; ++m)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) acc[0][m][v] += __shfl_xor(acc[0][m][v], 8, kWave);
   }
   if constexpr (KS) {  // parts [wave][b][16 tokens][16 rows], over the waves' work space
     static_assert(TB == 1, "a part is 16 rows");
@@ -988,7 +924,9 @@ __global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(De
   t.sc = sc;
   lds_t* lw = (lds_t*)work + wave * (2048 + 2048 * kActHalves<F>);
   for (int r0 = blockIdx.z * 32; r0 < n; r0 += gridDim.z * 32) {
-    if (n - r0 <= 16) down_rows<F, NT, TB, UN, KS, 1>(a, rows, r0, n, t, lw, (float*)work);
+    if (F != WF_F32 && n - r0 <= 8)
+      down_rows<F, NT, TB, UN, KS, 1, F != WF_F32>(a, rows, r0, n, t, lw, (float*)work);
+    else if (n - r0 <= 16) down_rows<F, NT, TB, UN, KS, 1>(a, rows, r0, n, t, lw, (float*)work);
     else down_rows<F, NT, TB, UN, KS, 2>(a, rows, r0, n, t, lw, (float*)work);
   }
 }
@@ -1100,15 +1038,8 @@ hipError_t run_gateup(const LaunchCtx& c, const DecodeArgs& a) {
 
 template <int F, bool NT>
 hipError_t run_down(const LaunchCtx& c, const DecodeArgs& a) {
-  if (small_down(a)) {
+  if (decode_one_down(a.T, a.k)) {
     MOE_LAUNCH(c, "decode_down", decode_down_small_kernel<F>, dim3((unsigned)(a.d / 8)), dim3(kDownWaves * 64), 0, a);
-    return hipSuccess;
-  }
-  if (decode_one_down(a.T, a.k, a.d)) {
-    const size_t smem = down_work<F>() + (size_t)a.E * 4 + (size_t)a.E * a.T * 2;
-    HIP_RET(tile::allow_smem_once<decode_down_kernel<F, NT>>(down_work<F>() + kMaxExperts * (4 + 16 * 2)));
-    MOE_LAUNCH(c, "decode_down", (decode_down_kernel<F, NT>), dim3((unsigned)cdiv(a.d, 16)), dim3(kDownWaves * 64),
-               smem, a);
     return hipSuccess;
   }
   constexpr int UN = F >= WF_FP8 ? 2 : 4;

@@ -8,7 +8,7 @@
 //
 // A bf16 MFMA multiplies bf16 operands, and x and w are; a float32 dlogits is
 // split into the bf16 nearest to it and the bf16 nearest to the rest, which
-// leaves 2^-18 of it, and both parts are multiplied: the products stay bound by
+// leaves 2^-17 of it, and both parts are multiplied: the products stay bound by
 // memory, and rounding dlogits to bf16 alone would cost 2^-9.  Float32 tensors
 // go through the float32 MFMA.
 //

@@ -254,7 +254,7 @@ moe_status moe_backward(const moe_shape* shape, const void* dout, const void* x,
  *   dw_router [E,d] = dlogits^T x;
  * all others in dtype; float32 sums in a fixed order, one rounding each.  With
  * dtype MOE_BF16 a float32 dlogits enters the products as the sum of two bf16
- * values (2^-18 of it is lost).  Every pointer 16-byte aligned; dx and
+ * values (up to 2^-17 of it is lost).  Every pointer 16-byte aligned; dx and
  * dw_router overlap no input (but dx_in, as said) and not each other;
  * workspace: moe_router_workspace_size bytes, for the backward only. */
 moe_status moe_router_forward(const moe_shape* shape, const void* x, const void* w_router,
@@ -310,8 +310,8 @@ moe_status moe_swiglu_backward8(const moe_shape* shape, const void* G, const uin
  * may have been encoded beforehand.  No tiles, sort or encoders run: the call
  * is the gate/up products and the down products, with the routing as a small
  * kernel before them (or, for a few tokens, inside the first) and the combine
- * inside the down products or, from 9 to 17 tokens on (the fewer the smaller d
- * is), as a small kernel behind them.
+ * inside the down products (up to 8 tokens with 32 slots in all) or as a small
+ * kernel behind them.
  *
  * shape: T <= 256 and precision MOE_PREC_NATIVE (MOE_ERR_UNSUPPORTED
  * otherwise; moe_forward takes more tokens), T*k*I values of dtype below
@@ -327,8 +327,9 @@ moe_status moe_swiglu_backward8(const moe_shape* shape, const void* G, const uin
  *                          recognised.
  * Coded weights need dtype MOE_BF16 and d, I multiples of 128, and stand for
  * code * scale; x and the activations are not quantised, unlike in
- * moe_forward's fp8 precisions (the activations are rounded to dtype between
- * the two products, as in moe_forward).
+ * moe_forward's fp8 precisions.  Between the two products a bf16 call keeps the
+ * activations as two bf16 values (up to 2^-17 of one is lost), where moe_forward
+ * rounds them to one.
  *
  * routing: logits, topk_ids and topk_w as in moe_forward; the other members
  * are neither read nor written and may be NULL.  A slot can be empty: a given

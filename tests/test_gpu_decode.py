@@ -1,7 +1,8 @@
 """The layer for few tokens (moe_decode) against a plain float64 evaluation.
 
-Tolerances.  The output of a bf16 call is off by: the rounding of the weighted
-SwiGLU output (each factor of every product within 2^-8), of the result
+Tolerances.  The output of a bf16 call is off by: at most one rounding to bf16
+of the weighted SwiGLU output (each factor of every product within 2^-8; a
+test of its own holds it to 2^-17), that of the result
 (2^-8), float32 sums and the hardware exp and reciprocal (both far below).
 With s_t = sum over slots and columns of |w a W_down| an output's error is at
 most 2^-8 s_t + 2^-8 |out|; float32 calls: the products' sums run over K = d
@@ -162,7 +163,7 @@ def test_ids_form_with_empty_slots_and_repeats(T, d, E, k, I, dtype, weights):
 
 
 # weights beyond the last-level cache (256 MiB) take the kernels' non-temporal
-# loads: more than 16 tokens, 9 to 16, and 9 to 16 at a d that fills the chip
+# loads: more than 16 tokens, 9 to 16, and 9 to 16 at a larger d
 @pytest.mark.parametrize("T,d,E,k,I,dtype,weights", [
     (20, 1024, 48, 3, 1024, "bf16", "native"), (40, 1024, 24, 2, 1032, "f32", "native"),
     (24, 1024, 96, 5, 1024, "bf16", "fp8_block"), (130, 1024, 96, 2, 1024, "bf16", "mxfp8"),
@@ -223,6 +224,26 @@ def test_tokens_split(T, d, E, k, I, dtype, weights):
     assert torch.equal(dec.topk_ids.long(), ids)
     check(got, x, wgu, wd, ids, w)
     assert torch.equal(dec.forward(x, wgu, wd, logits=logits), got)
+
+
+# bf16 calls keep the activations between the products in two bf16 parts: hi =
+# rn(v) leaves |v - hi| <= 2^(e - 8) at |v| >= 2^e, and rounding that rest to 8
+# bits errs by half a step of its exponent, at most 2^(e - 17): 2^-17 of v.  So
+# an output is off by its own rounding and 2^-17 of the sum of magnitudes.
+@pytest.mark.parametrize("T,d,E,k,I,dtype,weights", [
+    (1, 256, 16, 4, 128, "bf16", "native"), (4, 264, 12, 8, 200, "bf16", "native"),
+    (8, 256, 16, 8, 256, "bf16", "fp8_block"), (12, 136, 40, 3, 72, "bf16", "native"),
+    (16, 256, 3, 2, 128, "bf16", "mxfp8"), (40, 128, 20, 4, 256, "bf16", "mxfp8"),
+    (200, 264, 5, 2, 136, "bf16", "native"), (130, 1024, 128, 9, 256, "bf16", "fp8_block"),
+])
+def test_activations_keep_sixteen_bits(T, d, E, k, I, dtype, weights):
+    x, wgu, wd, logits = make(T, d, E, k, I, dtype, weights, seed=8)
+    dec = decoder(x, E, k, I, weights)
+    got = dec.forward(x, wgu, wd, logits=logits)
+    ids, w = topk64(logits, k)
+    ref, tol = plain(x, wgu, wd, ids, w, eps_act=2.0 ** -17)
+    err = (got.double() - ref).abs()
+    assert bool((err <= tol).all()), f"worst error over bound {float((err / tol).max()):.3g}"
 
 
 def test_masked_logits():
