@@ -331,15 +331,16 @@ __device__ __forceinline__ float swiglu(float g, float u, float lim) {
 // left, rounded (2^-17 of the value is lost), and both are multiplied.
 __device__ __forceinline__ int64_t aw_plane(const DecodeArgs& a) { return (int64_t)a.T * a.k * a.I; }
 template <typename AT>
-__device__ __forceinline__ void put_aw(const DecodeArgs& a, int64_t at, float v) {
+__device__ __forceinline__ void put_aw(const DecodeArgs& a, int64_t at, float v0, float v1) {
   if constexpr (sizeof(AT) == 4) {
-    ((float*)a.aw)[at] = v;
+    *(f32x2_t*)((float*)a.aw + at) = f32x2_t{v0, v1};
   } else {
-    const bf16_t h = f2bf(v);
-    const float f = bf2f(h);
-    ((bf16_t*)a.aw)[at] = h;
+    const float h0 = bf2f(f2bf(v0)), h1 = bf2f(f2bf(v1));
     // beside an infinity or NaN the rest would be NaN; h carries it alone
-    ((bf16_t*)a.aw)[aw_plane(a) + at] = fabsf(f) < __builtin_huge_valf() ? f2bf(v - f) : (bf16_t)0;
+    const float l0 = fabsf(h0) < __builtin_huge_valf() ? v0 - h0 : 0.0f;
+    const float l1 = fabsf(h1) < __builtin_huge_valf() ? v1 - h1 : 0.0f;
+    *(uint32_t*)((bf16_t*)a.aw + at) = pack_bf16x2(h0, h1);
+    *(uint32_t*)((bf16_t*)a.aw + aw_plane(a) + at) = pack_bf16x2(l0, l1);
   }
 }
 
@@ -581,19 +582,24 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
       *(f32x4_t*)(p + 256) = au[b][m];
     }
   __syncthreads();
-  for (int o = threadIdx.x; o < NB * TB * 256; o += NW * 64) {
-    // neighbouring threads: neighbouring rows of all TB tiles, then tokens
-    const int m = o & 15, tb = (o >> 4) % TB, c = o / (16 * TB) & 15, b = o / (256 * TB);
+  for (int o = threadIdx.x; o < NB * TB * 128; o += NW * 64) {
+    // neighbouring threads: neighbouring pairs of rows of all TB tiles, then tokens
+    const int m = (o & 7) * 2, tb = (o >> 3) % TB, c = o / (8 * TB) & 15, b = o / (128 * TB);
     const int r = r0 + b * 16 + c, row = t.n0 + tb * 16 + m;
-    if (r < n && row < a.I) {
-      float g = 0.0f, u = 0.0f;
+    if (r < n && row < a.I) {  // I is a multiple of 8: both rows are in or out
+      f32x2_t g = {0, 0}, u = {0, 0};
 #pragma unroll
       for (int v = 0; v < NW; ++v) {
         const float* p = red + ((v * NB + b) * TB + tb) * 512 + part_at(c, m >> 2) + (m & 3);
-        g += p[0];
-        u += p[256];
+        const f32x2_t pg = *(const f32x2_t*)p, pu = *(const f32x2_t*)(p + 256);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          g[i] += pg[i];
+          u[i] += pu[i];
+        }
       }
-      put_aw<AT>(a, (int64_t)rows.slot[r] * a.I + row, rows.w[r] * swiglu(g, u, a.lim));
+      const float w = rows.w[r];
+      put_aw<AT>(a, (int64_t)rows.slot[r] * a.I + row, w * swiglu(g[0], u[0], a.lim), w * swiglu(g[1], u[1], a.lim));
     }
   }
   __syncthreads();
@@ -963,16 +969,18 @@ int64_t gu_groups(const DecodeArgs& a) { return cdiv(a.I, 16) * work_items(a); }
 
 // Whether work-groups of 32 rows (a wave's, in the down product) leave four for
 // each CU.  Twice the rows halve what is read of the activations; fewer groups
-// leave CUs idle at the end.  Above, us with 16 and 32 rows at 256 tokens, by
+// leave CUs idle at the end.  Above, us with 16 and 32 rows at 256 tokens (with
+// one plane of aw to write; two add 2 to 6), by
 // the experts: gate/up bf16 128 151 and 137, 64 (1536 groups) 94 and 86, 32
 // (768) 51 and 55; mxfp8, 200 tokens, 128 experts 97 and 82, 8 (192) 20 and 25.
 bool wide_gateup(const DecodeArgs& a) { return cdiv(a.I, 32) * work_items(a) >= 1024; }
 
-// For the down product also eight tokens an expert, below which its activations
-// are little beside its weights (64 tokens, four an expert: 64 and 65 us; 256:
-// 90 and 84; mxfp8, 200: 53 and 46; 32 experts, 512 groups: bf16 27 and 30).
+// For the down product also two tokens an expert, below which its activations
+// are little beside its weights (us with 16 and 32 rows, mxfp8, 200 tokens 69
+// and 55; e4m3, 16 of 8 of 64 experts, d = 4096, I = 1024 49 and 43; bf16, 256
+// tokens 107 and 95, 64 67 both ways; 32 experts, 512 groups: 27 and 30).
 bool wide_down(const DecodeArgs& a) {
-  return cdiv(a.d, 32 * kDownRowWaves) * work_items(a) >= 1024 && a.T * a.k >= 8 * work_items(a);
+  return cdiv(a.d, 32 * kDownRowWaves) * work_items(a) >= 1024 && a.T * a.k >= 2 * work_items(a);
 }
 
 // Work-groups that an expert's tokens are split over, 32 at a time, where the
