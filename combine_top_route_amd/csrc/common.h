@@ -271,7 +271,7 @@ struct DecodeArgs {
   bool route_inline;      // set by the launcher: the gate/up kernel routes
   int32_t* mid;           // [T, k] workspace: expert of the slot, -1 for an empty or merged slot
   float* mw;              // [T, k] workspace: its weight
-  void* aw;               // [T k, I] workspace: weighted SwiGLU output per live slot
+  void* aw;               // [T k, I] workspace: weighted SwiGLU output per live slot, float32 or two bf16 planes
   float* y;               // [T k, d] workspace unless decode_one_down: down products per live slot
 };
 // weights: moe_weight_format.

@@ -10,8 +10,9 @@
 // = 2048, I = 768: 75 MB).  The layer's 256-row tiles, its sort and its weight
 // encoders would cost more than that, so here:
 //   * an MFMA's 16 rows are 16 weight rows and its 16 columns are token rows:
-//     a weight is loaded once from memory straight into its fragment, 128
-//     bytes per row and step ("unit"), whatever the number of tokens;
+//     a weight is loaded once from memory, 128 bytes per row and step ("unit"),
+//     and turned into its fragment in the wave's own LDS, whatever the number
+//     of tokens;
 //   * the K axis of a tile is split over the waves of a work-group and joined
 //     in LDS in wave order, so all of a small problem's bytes are in flight
 //     at once;
@@ -969,10 +970,10 @@ int64_t gu_groups(const DecodeArgs& a) { return cdiv(a.I, 16) * work_items(a); }
 
 // Whether work-groups of 32 rows (a wave's, in the down product) leave four for
 // each CU.  Twice the rows halve what is read of the activations; fewer groups
-// leave CUs idle at the end.  Above, us with 16 and 32 rows at 256 tokens (with
-// one plane of aw to write; two add 2 to 6), by
-// the experts: gate/up bf16 128 151 and 137, 64 (1536 groups) 94 and 86, 32
-// (768) 51 and 55; mxfp8, 200 tokens, 128 experts 97 and 82, 8 (192) 20 and 25.
+// leave CUs idle at the end.  Above, us with 16 and 32 rows at 256 tokens by the
+// experts (with one plane of aw to write; two add 2 to 6): gate/up bf16 128 151
+// and 137, 64 (1536 groups) 94 and 86, 32 (768) 51 and 55; mxfp8, 200 tokens,
+// 128 experts 97 and 82, 8 (192) 20 and 25.
 bool wide_gateup(const DecodeArgs& a) { return cdiv(a.I, 32) * work_items(a) >= 1024; }
 
 // For the down product also two tokens an expert, below which its activations
