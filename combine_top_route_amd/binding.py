@@ -158,7 +158,10 @@ def _ptr(t):
 
 def _stream(device):
     """torch's current stream on a device, as the library takes it (the raw
-    handle: building a torch.cuda.Stream object costs 2 us a call)."""
+    handle: building a torch.cuda.Stream object costs 2 us a call).  Refuses
+    host memory: a CPU device has no index and would name the current GPU."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors are on {device}; the kernels need a GPU's memory")
     return torch._C._cuda_getCurrentRawStream(
         torch.cuda.current_device() if device.index is None else device.index)
 
