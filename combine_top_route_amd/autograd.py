@@ -123,15 +123,16 @@ def moe_fwd(x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: Tensor, k: int
     T, d = x.shape
     E = w_gate_up.shape[0]
     dev = x.device
-    out = torch.empty((T, d), dtype=x.dtype, device=dev)
-    saved = torch.empty(B.saved_size(shape) if save else 0, dtype=torch.uint8, device=dev)
-    rt = _routing_empty(T, E, k, dev)
-    r = B.Routing(*rt, logits=logits)
-    cr = r.c()
-    ws = _workspace(shape, B.OP_FORWARD, dev)
-    B._check("moe_forward", B.lib().moe_forward(
-        ctypes.byref(shape), B._ptr(x), ctypes.byref(cr), B._ptr(w_gate_up), B._ptr(w_down), B._ptr(out),
-        B._ptr(saved) if save else None, B._ptr(ws), ws.numel(), B._stream(dev)))
+    with B._on(dev):
+        out = torch.empty((T, d), dtype=x.dtype, device=dev)
+        saved = torch.empty(B.saved_size(shape) if save else 0, dtype=torch.uint8, device=dev)
+        rt = _routing_empty(T, E, k, dev)
+        r = B.Routing(*rt, logits=logits)
+        cr = r.c()
+        ws = _workspace(shape, B.OP_FORWARD, dev)
+        B._check("moe_forward", B.lib().moe_forward(
+            ctypes.byref(shape), B._ptr(x), ctypes.byref(cr), B._ptr(w_gate_up), B._ptr(w_down), B._ptr(out),
+            B._ptr(saved) if save else None, B._ptr(ws), ws.numel(), B._stream(dev)))
     return (out, saved) + rt
 
 
@@ -167,18 +168,19 @@ def moe_bwd(dout: Tensor, x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: 
     E, two_i, _ = w_gate_up.shape
     dev = x.device
     recompute = saved.numel() == 0
-    dx = torch.empty_like(x)
-    dlogits = torch.empty_like(logits)
-    dwgu = torch.empty_like(w_gate_up)
-    dwd = torch.empty_like(w_down)
-    d_topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    r = B.Routing(topk_ids, topk_w, counts, offsets, row_of, src_of, logits=logits)
-    cr = r.c()
-    ws = _workspace(shape, B.OP_BACKWARD_RECOMPUTE if recompute else B.OP_BACKWARD, dev)
-    B._check("moe_backward", B.lib().moe_backward(
-        ctypes.byref(shape), B._ptr(dout), B._ptr(x), ctypes.byref(cr), B._ptr(w_gate_up), B._ptr(w_down),
-        None if recompute else B._ptr(saved), B._ptr(dx), B._ptr(dwgu), B._ptr(dwd), B._ptr(d_topk_w),
-        B._ptr(dlogits), B._ptr(ws), ws.numel(), B._stream(dev)))
+    with B._on(dev):
+        dx = torch.empty_like(x)
+        dlogits = torch.empty_like(logits)
+        dwgu = torch.empty_like(w_gate_up)
+        dwd = torch.empty_like(w_down)
+        d_topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        r = B.Routing(topk_ids, topk_w, counts, offsets, row_of, src_of, logits=logits)
+        cr = r.c()
+        ws = _workspace(shape, B.OP_BACKWARD_RECOMPUTE if recompute else B.OP_BACKWARD, dev)
+        B._check("moe_backward", B.lib().moe_backward(
+            ctypes.byref(shape), B._ptr(dout), B._ptr(x), ctypes.byref(cr), B._ptr(w_gate_up), B._ptr(w_down),
+            None if recompute else B._ptr(saved), B._ptr(dx), B._ptr(dwgu), B._ptr(dwd), B._ptr(d_topk_w),
+            B._ptr(dlogits), B._ptr(ws), ws.numel(), B._stream(dev)))
     return dx, dlogits, dwgu, dwd
 
 

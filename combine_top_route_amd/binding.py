@@ -281,9 +281,10 @@ class MoeLayer:
             r.topk_ids, r.topk_w = topk_ids, topk_w
         cr = r.c()
         name = "moe_forward8" if self.save8 else "moe_forward"
-        _check(name, getattr(lib(), name)(
-            ctypes.byref(self.shape), _ptr(x), ctypes.byref(cr), _ptr(w_gate_up), _ptr(w_down),
-            _ptr(self.out), _ptr(self.saved), _ptr(self.ws_fwd), self.ws_fwd.numel(), _stream(dev)))
+        with _on(dev):
+            _check(name, getattr(lib(), name)(
+                ctypes.byref(self.shape), _ptr(x), ctypes.byref(cr), _ptr(w_gate_up), _ptr(w_down),
+                _ptr(self.out), _ptr(self.saved), _ptr(self.ws_fwd), self.ws_fwd.numel(), _stream(dev)))
         return self.out
 
     def backward(self, dout, x, w_gate_up, w_down, want_dlogits=True):
@@ -293,10 +294,11 @@ class MoeLayer:
         cr = r.c()
         dl = self.dlogits if (want_dlogits and r.logits is not None) else None
         name = "moe_backward8" if self.save8 else "moe_backward"
-        _check(name, getattr(lib(), name)(
-            ctypes.byref(self.shape), _ptr(dout), _ptr(x), ctypes.byref(cr), _ptr(w_gate_up),
-            _ptr(w_down), _ptr(self.saved), _ptr(self.dx), _ptr(self.dw_gate_up), _ptr(self.dw_down),
-            _ptr(self.d_topk_w), _ptr(dl), _ptr(self.ws_bwd), self.ws_bwd.numel(), _stream(dev)))
+        with _on(dev):
+            _check(name, getattr(lib(), name)(
+                ctypes.byref(self.shape), _ptr(dout), _ptr(x), ctypes.byref(cr), _ptr(w_gate_up),
+                _ptr(w_down), _ptr(self.saved), _ptr(self.dx), _ptr(self.dw_gate_up), _ptr(self.dw_down),
+                _ptr(self.d_topk_w), _ptr(dl), _ptr(self.ws_bwd), self.ws_bwd.numel(), _stream(dev)))
         res = dict(dx=self.dx, dW_gate_up=self.dw_gate_up, dW_down=self.dw_down, d_topk_w=self.d_topk_w)
         if dl is not None:
             res["dlogits"] = dl
@@ -532,8 +534,9 @@ def route(logits, k):
     r = Routing.empty(T, E, k, dev, logits=logits)
     ws = torch.empty(workspace_size(shape, OP_ROUTE), dtype=torch.uint8, device=dev)
     cr = r.c()
-    _check("moe_route", lib().moe_route(ctypes.byref(shape), ctypes.byref(cr), _ptr(ws), ws.numel(),
-                                         _stream(dev)))
+    with _on(dev):
+        _check("moe_route", lib().moe_route(ctypes.byref(shape), ctypes.byref(cr), _ptr(ws), ws.numel(),
+                                             _stream(dev)))
     return r
 
 
@@ -547,8 +550,9 @@ def route_ids(topk_ids, topk_w, E):
     r = Routing.empty(T, E, k, dev, topk_ids=topk_ids, topk_w=topk_w)
     ws = torch.empty(workspace_size(shape, OP_ROUTE), dtype=torch.uint8, device=dev)
     cr = r.c()
-    _check("moe_route", lib().moe_route(ctypes.byref(shape), ctypes.byref(cr), _ptr(ws), ws.numel(),
-                                         _stream(dev)))
+    with _on(dev):
+        _check("moe_route", lib().moe_route(ctypes.byref(shape), ctypes.byref(cr), _ptr(ws), ws.numel(),
+                                             _stream(dev)))
     return r
 
 
@@ -557,8 +561,9 @@ def route_noalloc(r: Routing, T, E, k, logits_dtype=torch.bfloat16):
     r.logits is set, else r.topk_ids / r.topk_w in); no workspace."""
     shape = make_shape(T, 8, E, k, 8, torch.bfloat16, logits_dtype)
     cr = r.c()
-    _check("moe_route_noalloc", lib().moe_route_noalloc(ctypes.byref(shape), ctypes.byref(cr),
-                                                         _stream(r.counts.device)))
+    with _on(r.counts.device):
+        _check("moe_route_noalloc", lib().moe_route_noalloc(ctypes.byref(shape), ctypes.byref(cr),
+                                                             _stream(r.counts.device)))
     return r
 
 
@@ -570,8 +575,9 @@ def permute(x, routing: Routing, k, out=None):
     xp = torch.empty((T * k, d), dtype=x.dtype, device=x.device) if out is None else out
     _need(xp, "out", (T * k, d), x.dtype, x.device)
     cr = routing.c()
-    _check("moe_permute", lib().moe_permute(ctypes.byref(shape), _ptr(x), ctypes.byref(cr), _ptr(xp),
-                                             _stream(x.device)))
+    with _on(x.device):
+        _check("moe_permute", lib().moe_permute(ctypes.byref(shape), _ptr(x), ctypes.byref(cr), _ptr(xp),
+                                                 _stream(x.device)))
     return xp
 
 
@@ -581,8 +587,9 @@ def combine(rows, routing: Routing, T, k):
     shape = make_shape(T, d, E, k, 8, rows.dtype)
     out = torch.empty((T, d), dtype=rows.dtype, device=rows.device)
     cr = routing.c()
-    _check("moe_combine", lib().moe_combine(ctypes.byref(shape), _ptr(rows), ctypes.byref(cr), _ptr(out),
-                                             _stream(rows.device)))
+    with _on(rows.device):
+        _check("moe_combine", lib().moe_combine(ctypes.byref(shape), _ptr(rows), ctypes.byref(cr), _ptr(out),
+                                                 _stream(rows.device)))
     return out
 
 
@@ -616,8 +623,9 @@ def quantize_fp8(src, kind=QUANT_ROWS):
         qs = (n0, n1, n2) if kind == QUANT_WEIGHT else (n0, n2, n1)
         q = torch.empty(qs, dtype=torch.uint8, device=dev)
         s = torch.empty((qs[0], qs[1] // 128, qs[2] // 128), dtype=torch.float32, device=dev)
-    _check("moe_quantize_fp8", lib().moe_quantize_fp8(kind, _ptr(src), n0, n1, n2, _ptr(q), _ptr(s),
-                                                      _stream(dev)))
+    with _on(dev):
+        _check("moe_quantize_fp8", lib().moe_quantize_fp8(kind, _ptr(src), n0, n1, n2, _ptr(q), _ptr(s),
+                                                          _stream(dev)))
     return q, s
 
 
@@ -634,9 +642,10 @@ def quantize_tokens_fp8(src, routing: Routing, T, k, gather):
     s = torch.zeros((C, nblk), dtype=torch.float32, device=dev)
     ws = torch.empty(workspace_size(shape, OP_ROUTE), dtype=torch.uint8, device=dev)
     cr = routing.c()
-    _check("moe_quantize_tokens_fp8", lib().moe_quantize_tokens_fp8(
-        ctypes.byref(shape), _ptr(src), C, 1 if gather else 0, ctypes.byref(cr), _ptr(q), _ptr(s), _ptr(ws),
-        ws.numel(), _stream(dev)))
+    with _on(dev):
+        _check("moe_quantize_tokens_fp8", lib().moe_quantize_tokens_fp8(
+            ctypes.byref(shape), _ptr(src), C, 1 if gather else 0, ctypes.byref(cr), _ptr(q), _ptr(s), _ptr(ws),
+            ws.numel(), _stream(dev)))
     return q, s
 
 
@@ -658,8 +667,9 @@ def quantize_mxfp8(src, kind=QUANT_ROWS):
         qs = (n0, n1, n2) if kind == QUANT_WEIGHT else (n0, n2, n1)
     q = torch.empty(qs, dtype=torch.uint8, device=dev)
     s = torch.empty(qs[:-1] + (qs[-1] // 32,), dtype=torch.uint8, device=dev)
-    _check("moe_quantize_mxfp8", lib().moe_quantize_mxfp8(kind, _ptr(src), n0, n1, n2, _ptr(q), _ptr(s),
-                                                          _stream(dev)))
+    with _on(dev):
+        _check("moe_quantize_mxfp8", lib().moe_quantize_mxfp8(kind, _ptr(src), n0, n1, n2, _ptr(q), _ptr(s),
+                                                              _stream(dev)))
     return q, s
 
 
@@ -675,7 +685,8 @@ def quantize_tokens_mxfp8(src, routing: Routing, T, k, gather):
     s = torch.zeros((C, 4 * nblk), dtype=torch.uint8, device=dev)
     ws = torch.empty(workspace_size(shape, OP_ROUTE), dtype=torch.uint8, device=dev)
     cr = routing.c()
-    _check("moe_quantize_tokens_mxfp8", lib().moe_quantize_tokens_mxfp8(
-        ctypes.byref(shape), _ptr(src), C, 1 if gather else 0, ctypes.byref(cr), _ptr(q), _ptr(s), _ptr(ws),
-        ws.numel(), _stream(dev)))
+    with _on(dev):
+        _check("moe_quantize_tokens_mxfp8", lib().moe_quantize_tokens_mxfp8(
+            ctypes.byref(shape), _ptr(src), C, 1 if gather else 0, ctypes.byref(cr), _ptr(q), _ptr(s), _ptr(ws),
+            ws.numel(), _stream(dev)))
     return q, s
