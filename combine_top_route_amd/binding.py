@@ -288,8 +288,11 @@ class MoeLayer:
         return self.out
 
     def backward(self, dout, x, w_gate_up, w_down, want_dlogits=True):
-        T, d, dt, dev = self.T, self.d, self.dtype, self.device
+        T, d, E, I, dt, dev = self.T, self.d, self.E, self.I, self.dtype, self.device
         _need(dout, "dout", (T, d), dt, dev)
+        _need(x, "x", (T, d), dt, dev)
+        _need(w_gate_up, "w_gate_up", (E, 2 * I, d), dt, dev)
+        _need(w_down, "w_down", (E, d, I), dt, dev)
         r = self.routing
         cr = r.c()
         dl = self.dlogits if (want_dlogits and r.logits is not None) else None
