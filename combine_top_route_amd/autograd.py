@@ -93,6 +93,13 @@ def _check_backward_args(dout: Tensor, x: Tensor, saved: Tensor, routing, k: int
         _require(t.is_contiguous(), f"{name} must be contiguous")
 
 
+def _dense(grad: Tensor) -> Tensor:
+    """A gradient as the library takes it: contiguous and 16-byte aligned.  What
+    autograd hands over may be a slice of a larger gradient at any element."""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
 def _shape(x: Tensor, logits: Tensor, w_gate_up: Tensor, k: int, precision: str, swiglu_limit: float = 0.0):
     T, d = x.shape
     E, two_i, _ = w_gate_up.shape
@@ -156,7 +163,7 @@ def moe_bwd(dout: Tensor, x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: 
     """Layer backward: (dx, dlogits, dw_gate_up, dw_down).  An empty `saved`
     selects recomputation."""
     _check_layer_args(x, logits, w_gate_up, w_down, k, precision)
-    dout = dout.contiguous()
+    dout = _dense(dout)
     _check_backward_args(dout, x, saved, (topk_ids, topk_w, counts, offsets, row_of, src_of), k, precision)
     shape = _shape(x, logits, w_gate_up, k, precision, swiglu_limit)
     _require(saved.numel() in (0, B.saved_size(shape)),
@@ -250,7 +257,7 @@ def moe_bwd8(dout: Tensor, x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down:
     """Layer backward from the 8-bit checkpoint: (dx, dlogits, dw_gate_up,
     dw_down)."""
     _check_layer_args(x, logits, w_gate_up, w_down, k, "native")
-    dout = dout.contiguous()
+    dout = _dense(dout)
     _check_backward_args(dout, x, saved, (topk_ids, topk_w, counts, offsets, row_of, src_of), k, "native")
     shape = _shape(x, logits, w_gate_up, k, "native", swiglu_limit)
     _require(saved.numel() == B.saved8_size(shape),
@@ -407,12 +414,12 @@ def _(x, w_router, logits_dtype):
 def router_bwd(dlogits: Tensor, x: Tensor, w_router: Tensor, dx_in: Tensor | None) -> tuple[Tensor, Tensor]:
     """(dx, dw_router): dx = dx_in + dlogits w_router, dw_router = dlogits^T x."""
     _check_router_args(x, w_router, dlogits.dtype)
-    dlogits = dlogits.contiguous()
+    dlogits = _dense(dlogits)
     _require(tuple(dlogits.shape) == (x.shape[0], w_router.shape[0]),
              f"dlogits must be [T={x.shape[0]}, E={w_router.shape[0]}], got {tuple(dlogits.shape)}")
     tensors = dict(x=x, w_router=w_router, dlogits=dlogits)
     if dx_in is not None:
-        dx_in = dx_in.contiguous()
+        dx_in = _dense(dx_in)
         _require(dx_in.shape == x.shape and dx_in.dtype == x.dtype,
                  f"dx_in must be {tuple(x.shape)} {x.dtype}, got {tuple(dx_in.shape)} {dx_in.dtype}")
         tensors["dx_in"] = dx_in
