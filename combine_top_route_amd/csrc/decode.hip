@@ -329,7 +329,10 @@ __device__ __forceinline__ float swiglu(float g, float u, float lim) {
 // The weighted activation on its way to the down product.  The bf16 MFMA takes
 // bf16 operands, and one rounding to bf16 here would be as large an error as the
 // output's own; so bf16 calls keep two planes, the value rounded and what that
-// left, rounded (2^-17 of the value is lost), and both are multiplied.
+// left, rounded (2^-17 of the value is lost), and both are multiplied.  Their
+// sums are kept apart until join_planes: where an infinite weight meets the
+// second plane, 0 inf or a rest of the other sign would make a NaN of the
+// formula's infinity.
 __device__ __forceinline__ int64_t aw_plane(const DecodeArgs& a) { return (int64_t)a.T * a.k * a.I; }
 template <typename AT>
 __device__ __forceinline__ void put_aw(const DecodeArgs& a, int64_t at, float v0, float v1) {
@@ -343,6 +346,11 @@ __device__ __forceinline__ void put_aw(const DecodeArgs& a, int64_t at, float v0
     *(uint32_t*)((bf16_t*)a.aw + at) = pack_bf16x2(h0, h1);
     *(uint32_t*)((bf16_t*)a.aw + aw_plane(a) + at) = pack_bf16x2(l0, l1);
   }
+}
+
+// The sum over both planes.
+__device__ __forceinline__ float join_planes(float main, float rest) {
+  return fabsf(main) < __builtin_huge_valf() ? main + rest : main;
 }
 
 // The same routing inside the gate/up kernel, for a token or a few: every
@@ -694,7 +702,9 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(Deco
   lds_t* lw = (lds_t*)work + wave * WORK;
   const int total = nact * units;
   const uint64_t slots = a.k == 64 ? ~0ull : (1ull << a.k) - 1;  // a token's slots
-  f32x4_t acc = {0, 0, 0, 0};
+  f32x4_t acc[P];  // a plane's sums each
+#pragma unroll
+  for (int p = 0; p < P; ++p) acc[p] = f32x4_t{0, 0, 0, 0};
   for (int base = wave * UN; base < total; base += kDownWaves * UN) {
     u32x4_t wv[UN], xv[UN][P][kActHalves<F>];
     uint32_t mx[UN];
@@ -739,7 +749,6 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(Deco
       turn_fence();
       typename Fmt<F>::frag fr[Fmt<F>::NF / 2];
       chunk_frags<F>(fr, get_chunk(lw, r8, 4 * half + q), mx[i], half, q);
-      f32x4_t s = {0, 0, 0, 0};
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         turn_fence();
@@ -750,15 +759,19 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(Deco
         turn_fence();
         u32x4_t xf[Fmt<F>::BV / 2];
         chunk_acts<F>(xf, lw + 2048, half, q, r8);
-        s = unit_dot<F, Fmt<F>::NF / 2>(s, fr, xf);
-      }
+        const f32x4_t s = unit_dot<F, Fmt<F>::NF / 2>(f32x4_t{0, 0, 0, 0}, fr, xf);
 #pragma unroll
-      for (int m = 0; m < 4; ++m) acc[m] = on_expert[i] ? fmaf(sb[i], s[m], acc[m]) : acc[m];
+        for (int m = 0; m < 4; ++m) acc[p][m] = on_expert[i] ? fmaf(sb[i], s[m], acc[p][m]) : acc[p][m];
+      }
     }
+  }
+  if constexpr (P == 2) {
+#pragma unroll
+    for (int m = 0; m < 4; ++m) acc[0][m] = join_planes(acc[0][m], acc[1][m]);
   }
   float* red = (float*)work;
   __syncthreads();
-  if ((q >> 1) == half) *(f32x4_t*)(red + ((wave * 2 + half) * 8 + r8) * 8 + (q & 1) * 4) = acc;
+  if ((q >> 1) == half) *(f32x4_t*)(red + ((wave * 2 + half) * 8 + r8) * 8 + (q & 1) * 4) = acc[0];
   __syncthreads();
   if (threadIdx.x < 64) {
     const int t = threadIdx.x >> 3, m = threadIdx.x & 7;
@@ -809,11 +822,13 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
       live[b][h] = r < n;
       xr[b][h] = (uint32_t)rows.slot[live[b][h] ? r : n - 1] * bbytes;
     }
-  f32x4_t acc[NB][TB];
+  f32x4_t acc[P][NB][TB];  // a plane's sums each
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int p = 0; p < P; ++p)
 #pragma unroll
-    for (int m = 0; m < TB; ++m) acc[b][m] = f32x4_t{0, 0, 0, 0};
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int m = 0; m < TB; ++m) acc[p][b][m] = f32x4_t{0, 0, 0, 0};
   constexpr int UB = NB == 1 ? UN : 1;
   const int wave = tile::wave_id();
   for (int base = KS ? wave * UN : 0; base < units; base += (KS ? kDownRowWaves : 1) * UN) {
@@ -857,7 +872,7 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
                 put_acts<F>(lw + 2048, xv[i][b][p], false);
                 get_acts<F>(xf[b][p], lw + 2048, q, col);
               }
-              unit_mma<F>(acc[b][m], fr, xf[b][p], sb[i0 + i]);
+              unit_mma<F>(acc[p][b][m], fr, xf[b][p], sb[i0 + i]);
             }
           }
         }
@@ -868,13 +883,21 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
 #pragma unroll
     for (int m = 0; m < TB; ++m)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) acc[0][m][v] += __shfl_xor(acc[0][m][v], 8, kWave);
+      for (int v = 0; v < 4; ++v)
+        acc[0][0][m][v] = join_planes(acc[0][0][m][v], __shfl_xor(acc[0][0][m][v], 8, kWave));
+  } else if constexpr (P == 2) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int m = 0; m < TB; ++m)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[0][b][m][v] = join_planes(acc[0][b][m][v], acc[1][b][m][v]);
   }
   if constexpr (KS) {  // parts [wave][b][16 tokens][16 rows], over the waves' work space
     static_assert(TB == 1, "a part is 16 rows");
     __syncthreads();
 #pragma unroll
-    for (int b = 0; b < NB; ++b) *(f32x4_t*)(red + (wave * NB + b) * 256 + part_at(col, q)) = acc[b][0];
+    for (int b = 0; b < NB; ++b) *(f32x4_t*)(red + (wave * NB + b) * 256 + part_at(col, q)) = acc[0][b][0];
     __syncthreads();
     for (int o = threadIdx.x; o < NB * 64; o += kDownRowWaves * 64) {
       const int r = r0 + (o >> 2), row = t.n0 + (o & 3) * 4;
@@ -898,13 +921,15 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
     for (int m = 0; m < TB; ++m) {
       const int row = t.n0 + 16 * m + q * 4;
       if (r < n && row < a.d)  // d is a multiple of 8: four rows are in or out together
-        *(f32x4_t*)(a.y + (int64_t)rows.slot[r] * a.d + row) = acc[b][m];
+        *(f32x4_t*)(a.y + (int64_t)rows.slot[r] * a.d + row) = acc[0][b][m];
     }
   }
 }
 
+// The wide blockwise form is held to three waves a SIMD: it would take 174
+// registers and leave two (16 tokens, e4m3 above: 46 us with two, 42 with three).
 template <int F, bool NT, int TB, int UN, bool KS>
-__global__ __launch_bounds__(kDownRowWaves * 64) void decode_down_rows_kernel(DecodeArgs a) {
+__global__ __launch_bounds__(kDownRowWaves * 64, F == WF_FP8 && TB == 2 ? 3 : 1) void decode_down_rows_kernel(DecodeArgs a) {
   static_assert(kDownRowWaves * 64 >= kDecodeMaxT, "Finder takes a thread per token");
   __shared__ Rows rows;
   __shared__ __align__(16) char work[kDownRowWaves * (2048 + 2048 * kActHalves<F>)];
