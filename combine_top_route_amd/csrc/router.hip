@@ -227,6 +227,29 @@ __device__ __forceinline__ void split_bf16(float v, bf16_t& hi, bf16_t& lo) {
   lo = fabsf(h) < __builtin_huge_valf() ? f2bf(v - h) : (bf16_t)0;
 }
 
+// The rest lo must not meet an infinity of x or w: 0 inf, or a rest of the other
+// sign, would make a NaN of the formula's infinity, which hi gives alone.
+__device__ __forceinline__ bool is_finite(float v) { return fabsf(v) < __builtin_huge_valf(); }
+// Of bf16 operands: whether one is not finite, and the same with those as zeros.
+struct NotFinite {
+  typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+  u16x2_t most = {0, 0};  // largest magnitudes of the low and the high halves
+  __device__ __forceinline__ void see(u32x4_t v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2_t, v[i] & 0x7fff7fffu));
+  }
+  __device__ __forceinline__ bool any() const { return __any(most[0] >= 0x7f80u || most[1] >= 0x7f80u); }
+};
+__device__ __forceinline__ u32x4_t finite_only(u32x4_t v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((v[i] & 0x7f80u) == 0x7f80u) v[i] &= 0xffff0000u;
+    if ((v[i] & 0x7f800000u) == 0x7f800000u) v[i] &= 0xffffu;
+  }
+  return v;
+}
+
 // Sixteen bytes of dlogits as floats.
 template <typename LT>
 __device__ __forceinline__ void unpack16(float* f, u32x4_t v) {
@@ -309,14 +332,15 @@ __device__ __forceinline__ bool dl_vec(const RouterArgs& a) { return (a.E * size
 template <typename T, typename LT>
 constexpr int dw_stage() { return (sizeof(T) == 2 && sizeof(LT) == 4 ? 3 : 2) * DwTile<T>::TS * DwTile<T>::STRIDE; }
 
-template <typename T, typename LT>
-__device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb, int db, int run) {
+// A wave's sums over one run, with the products of dlogits' second part if REST.
+// A sum that comes out not finite is taken from the first part's products alone,
+// in a second pass over the run that only such sums cause.
+template <typename T, typename LT, bool REST>
+__device__ __forceinline__ void dw_sums(f32x4_t (&acc)[4][2], const RouterArgs& a, char* smem, int e0, int d0, int run) {
   constexpr int TS = DwTile<T>::TS, ST = DwTile<T>::STRIDE;
-  constexpr bool LO = sizeof(T) == 2 && sizeof(LT) == 4;  // dlogits has a second part
   constexpr int XU = kDwD * (int)sizeof(T) / 16;          // 16-byte loads per row of x
   constexpr int XV = TS * XU / 512;
   const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
-  const int e0 = eb * kDwE, d0 = db * kDwD;
   const int64_t tb = (int64_t)run * a.run_tokens;
   const int tn = (int)(a.T - tb < a.run_tokens ? a.T - tb : a.run_tokens);
   const int xrow = a.d * (int)sizeof(T);
@@ -348,7 +372,6 @@ __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb,
   };
   const int we = (wave >> 2) * 64, wd = (wave & 3) * 32;
   const bool busy = e0 + we < a.E && d0 + wd < a.d;  // uniform: this quarter exists
-  f32x4_t acc[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -402,7 +425,7 @@ __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb,
           const bf16x8_t h = frag(hs, we + i * 16);
 #pragma unroll
           for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(h, bv[j], acc[i][j], 0, 0, 0);
-          if constexpr (LO) {
+          if constexpr (REST) {
             const bf16x8_t l = frag(ls, we + i * 16);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -416,20 +439,42 @@ __device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb,
     step(set0, set1, s);
     if (s + TS < tn) step(set1, set0, s + TS);
   }
-  if (!busy) return;
+}
+
+template <typename T, typename LT>
+__device__ __forceinline__ void dw_part(const RouterArgs& a, char* smem, int eb, int db, int run) {
+  constexpr bool LO = sizeof(T) == 2 && sizeof(LT) == 4;  // dlogits has a second part
+  const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
+  const int e0 = eb * kDwE, d0 = db * kDwD, we = (wave >> 2) * 64, wd = (wave & 3) * 32;
   float* part = a.parts + (int64_t)run * a.E * a.d;
+  f32x4_t acc[4][2];
+  // the sums (those of `which`, a bit each, if given); returns the ones that are not finite
+  auto write = [&](uint32_t which) {
+    uint32_t bad = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int e = e0 + we + i * 16 + q * 4 + m, c = d0 + wd + j * 16 + col;
-        if (e < a.E && c < a.d) {
-          if (a.runs > 1) part[(int64_t)e * a.d + c] = acc[i][j][m];
-          else ((T*)a.dw)[(int64_t)e * a.d + c] = from_f32<T>(acc[i][j][m]);
+        for (int m = 0; m < 4; ++m) {
+          const int e = e0 + we + i * 16 + q * 4 + m, c = d0 + wd + j * 16 + col;
+          const uint32_t bit = 1u << ((i * 2 + j) * 4 + m);
+          if (e < a.E && c < a.d && (which & bit)) {
+            if (LO && !is_finite(acc[i][j][m])) bad |= bit;
+            if (a.runs > 1) part[(int64_t)e * a.d + c] = acc[i][j][m];
+            else ((T*)a.dw)[(int64_t)e * a.d + c] = from_f32<T>(acc[i][j][m]);
+          }
         }
-      }
+    return bad;
+  };
+  dw_sums<T, LT, LO>(acc, a, smem, e0, d0, run);
+  const uint32_t bad = write(~0u);
+  if constexpr (LO) {
+    if (__syncthreads_or(bad != 0)) {
+      dw_sums<T, LT, false>(acc, a, smem, e0, d0, run);
+      write(bad);
+    }
+  }
 }
 
 // dx: 8 waves, each with the operands of 16 DT columns of w and up to 128
@@ -491,6 +536,25 @@ __device__ __forceinline__ void dx_part(const RouterArgs& a, char* smem, int cb,
       __builtin_amdgcn_sched_barrier(0);  // one step's loads at a time hold registers
     }
   }
+  // Weights that are not finite enter the MFMAs as zeros where dlogits has a second
+  // part, and `infinite` adds their products with the first part.
+  bool w_bad = false;  // uniform: the wave holds such a weight
+  auto clean = [&](u32x4_t (*o)[DT], int n) {
+    NotFinite bad;
+#pragma unroll
+    for (int k = 0; k < n; ++k)
+#pragma unroll
+      for (int j = 0; j < DT; ++j) bad.see(o[k][j]);
+    const bool any = bad.any();
+    if (any) {
+#pragma unroll
+      for (int k = 0; k < n; ++k)
+#pragma unroll
+        for (int j = 0; j < DT; ++j) o[k][j] = finite_only(o[k][j]);
+    }
+    return any;
+  };
+  if (LO && !MULTI && busy) w_bad = clean(wv, MULTI ? 1 : NK);
   const int64_t tb = (int64_t)run * a.dx_tokens, te = tb + a.dx_tokens < a.T ? tb + a.dx_tokens : a.T;
   DlTile<T, LT, kDxTok, kDxWaves * 64, DxPlace<T>> dl;
   auto fetch = [&](int64_t t, int eb) {
@@ -514,6 +578,24 @@ __device__ __forceinline__ void dx_part(const RouterArgs& a, char* smem, int cb,
       const u32x4_t lv = *(const u32x4_t*)(ls + at);
 #pragma unroll
       for (int j = 0; j < DT; ++j) acc[g][j] = mma16<T>(lv, wv[MULTI ? 0 : k][j], acc[g][j]);
+    }
+  };
+  // acc[g] += the products of tokens 16 h .. with this lane's weights of block eb
+  // that are not finite
+  auto infinite = [&](const char* hs, int g, int h, int eb) {
+    const int n = min(a.E - eb * kDxE, kDxE);
+#pragma unroll 1
+    for (int e = 0; e < n; ++e) {
+      const tile::u32x2_t w2 = __builtin_bit_cast(tile::u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
+          wb, (int)(in ? (uint32_t)((eb * kDxE + e) * a.d + c) * (uint32_t)sizeof(T) : kPast), 0, 0));
+#pragma unroll
+      for (int j = 0; j < DT; ++j) {
+        const float w = __uint_as_float(j & 1 ? w2[j >> 1] & 0xffff0000u : w2[j >> 1] << 16);
+        if (is_finite(w)) continue;
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          acc[g][j][m] += bf2f(*(const bf16_t*)(hs + (h * 16 + q * 4 + m) * ST + e * 2)) * w;
+      }
     }
   };
   // result row 4 q + m is a token, and tile j column c + j of it; rows past the
@@ -572,12 +654,20 @@ __device__ __forceinline__ void dx_part(const RouterArgs& a, char* smem, int cb,
       else if (t0 + kDxTok < te) fetch(t0 + kDxTok, 0);
       if (!busy) continue;
       if constexpr (MULTI) {
+        w_bad = false;
 #pragma unroll 1
         for (int k = 0; k < NK; ++k) {
           if (eb * kDxE + k * 4 * PER >= a.E) break;
           w_operands<T>(wv[0], wb, eb * kDxE + (k * 4 + q) * PER, a.E, a.d, c);
+          if (LO) w_bad |= clean(wv, 1);
           step(hs, ls, 0, 0, k);
           step(hs, ls, 1, 1, k);
+        }
+        if constexpr (LO) {
+          if (w_bad) {
+            infinite(hs, 0, 0, eb);
+            infinite(hs, HG - 1, 1, eb);
+          }
         }
       } else {
 #pragma unroll
@@ -586,6 +676,9 @@ __device__ __forceinline__ void dx_part(const RouterArgs& a, char* smem, int cb,
 #pragma unroll
           for (int k = 0; k < NK; ++k)
             if (k * 4 * PER < a.E) step(hs, ls, 0, h, k);
+          if constexpr (LO) {
+            if (w_bad) infinite(hs, 0, h, 0);
+          }
           write(t0, 0, h);
         }
       }
