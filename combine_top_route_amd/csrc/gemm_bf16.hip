@@ -610,12 +610,12 @@ __device__ __forceinline__ void lds_to_global(const lds_t* t, bf16_t* C, int64_t
 // neighbouring lanes' chunks.  Columns >= col_lim count as zeros.
 template <int ROWS, int S>
 __device__ __forceinline__ void lds_to_codes(const lds_t* t, uint8_t* C, int64_t ldc, uint8_t* scales, int64_t lds,
-                                             int row_lim, int col_lim) {
+                                             int row_lim, int col_lim, int tid = threadIdx.x) {
   constexpr int CPR = TBN / 2 / 8, NQ = ROWS * CPR / NTHR;
   static_assert(ROWS * CPR % NTHR == 0 && CPR % 4 == 0, "whole blocks per four lanes");
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
-    const int q = threadIdx.x + i * NTHR, row = q / CPR, c8 = q % CPR;
+    const int q = tid + i * NTHR, row = q / CPR, c8 = q % CPR;
     const bool in = c8 * 8 < col_lim;
     const u32x4_t v = *(const __attribute__((address_space(3))) u32x4_t*)(t + row * S + c8 * 16);
     float f[8];
@@ -898,7 +898,7 @@ struct NextIssue {
   __device__ void early() {
     if (!more) return;
     fetch_arow<TBM>(p, t.m0, t.seg1, arow);
-    if constexpr (EPI == EPI_GATEUP) wsrc = fetch_wsrc<TBM>(p, t.m0, t.seg1);
+    if constexpr (EPI != EPI_STORE) wsrc = fetch_wsrc<TBM>(p, t.m0, t.seg1);
   }
   __device__ void issue(lds_t* dst) {
     if (!more) return;
@@ -907,7 +907,7 @@ struct NextIssue {
     issue_stage<false>(oa, ob, 0, dst);
     oa.advance();
     ob.advance();
-    if constexpr (EPI == EPI_GATEUP) wrow = wsrc ? p.topk_w[wsrc - 1] : 0.0f;
+    if constexpr (EPI != EPI_STORE) wrow = wsrc ? p.topk_w[wsrc - 1] : 0.0f;
   }
 };
 
@@ -954,9 +954,9 @@ __device__ __forceinline__ void persist_epilogue(const RowsArgs& p, const RowTil
   if constexpr (EPI == EPI_STORE) {
     persist_store(base, last, acc, p.C + (int64_t)t.m0 * p.ldc + t.nt * TBN, p.ldc, rows_valid, p.N - t.nt * TBN);
   } else {
-    // three rounds of 256 x 128: Aw, then H's gate and up columns; the row
-    // weights sit in the 32 KB gap, clear of both the staged tile and the
-    // slots, so they are written before the first barrier
+    // three rounds of 256 x 128: Aw, then H's gate and up columns (or their
+    // codes); the row weights sit in the 32 KB gap, clear of both the staged
+    // tile and the slots, so they are written before the first barrier
     constexpr int S = ep_stride<TBN / 2>();
     constexpr int TB = TBM * S;
     static_assert(TB + 1024 <= kPSlot && 65 * 1024 + TB <= (int)kPSmem, "staging area beside either slot");
@@ -972,7 +972,18 @@ __device__ __forceinline__ void persist_epilogue(const RowsArgs& p, const RowTil
     }, tid);
     barrier_lds();
     lds_to_global<TBM, TBN / 2, S>(stg, p.Aout + (int64_t)t.m0 * p.I + gc0, p.I, rows_valid, p.I - gc0, RowId(), tid);
-    if (p.H) {
+    if constexpr (EPI == EPI_GATEUP8) {
+      const int64_t nb = cdiv(p.I, 32);
+      uint8_t* C0 = p.codes + (int64_t)t.m0 * 2 * p.I + gc0;
+      uint8_t* s0 = p.scales + t.m0 * 2 * nb + gc0 / 32;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        barrier_lds();
+        stage_quads<TM, 1, S>(stg, r0w, c0w, [&](int i, int, int r) { return acc[i][h][r]; }, tid);
+        barrier_lds();
+        lds_to_codes<TBM, S>(stg, C0 + h * p.I, 2 * p.I, s0 + h * nb, 2 * nb, rows_valid, p.I - gc0, tid);
+      }
+    } else if (p.H) {
       bf16_t* H0 = p.H + (int64_t)t.m0 * 2 * p.I + gc0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -1004,10 +1015,10 @@ __global__ __launch_bounds__(NTHR, 1) void rows_persist_kernel(RowsArgs p) {
   float wrow = 0.0f;
   {  // the first tile's first stage
     int wsrc = 0;
-    if constexpr (EPI == EPI_GATEUP) wsrc = fetch_wsrc<TBM>(p, t.m0, t.seg1);
+    if constexpr (EPI != EPI_STORE) wsrc = fetch_wsrc<TBM>(p, t.m0, t.seg1);
     int arow[OpMK<TBM>::NI];
     fetch_arow<TBM>(p, t.m0, t.seg1, arow);
-    if constexpr (EPI == EPI_GATEUP) {
+    if constexpr (EPI != EPI_STORE) {
       if (wsrc) wrow = p.topk_w[wsrc - 1];
     }
     init_a<TBM>(p, oa, arow);
@@ -1322,7 +1333,7 @@ hipError_t bf16_fwd_gemms(const LaunchCtx& c, const LayerArgs& a, void* H, void*
     p.H = (bf16_t*)H; p.Aout = (bf16_t*)Aw; p.I = a.I; p.lim = a.swiglu_lim;
     p.topk_w = a.topk_w; p.src_of = a.src_of;
     p.codes = codes; p.scales = scales;
-    hipError_t err = codes ? launch_rows_tiles<EPI_GATEUP8, B_MK_GATEUP>(c, "gemm_gateup_fwd8", p, a.R)
+    hipError_t err = codes ? launch_rows<EPI_GATEUP8, B_MK_GATEUP>(c, "gemm_gateup_fwd8", p, a.R, a.persistent)
                            : launch_rows<EPI_GATEUP, B_MK_GATEUP>(c, "gemm_gateup_fwd", p, a.R, a.persistent);
     if (err != hipSuccess) return err;
   }
