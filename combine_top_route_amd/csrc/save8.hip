@@ -91,7 +91,7 @@ __global__ __launch_bounds__(256) void save8_kernel(const T* __restrict__ H, con
                                                     const int32_t* __restrict__ src_of, int R, int I, int lsh,
                                                     float lim, T* __restrict__ aw, uint8_t* __restrict__ codes,
                                                     uint8_t* __restrict__ scales) {
-  const int L = 1 << lsh, r = (blockIdx.x << (8 - lsh)) + (threadIdx.x >> lsh);
+  const int L = 1 << lsh, r = ((int)(blockIdx.y * gridDim.x + blockIdx.x) << (8 - lsh)) + (int)(threadIdx.x >> lsh);
   if (r >= R) return;
   const int lane = (int)threadIdx.x & (L - 1);
   const int nb = (I + 31) / 32;
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(256) void swiglu_bwd8_kernel(const T* __restrict__ 
                                                           const int32_t* __restrict__ src_of, int R, int I, int lsh,
                                                           float lim, T* __restrict__ dH, T* __restrict__ aw,
                                                           float* __restrict__ dw) {
-  const int L = 1 << lsh, r = (blockIdx.x << (8 - lsh)) + (threadIdx.x >> lsh);
+  const int L = 1 << lsh, r = ((int)(blockIdx.y * gridDim.x + blockIdx.x) << (8 - lsh)) + (int)(threadIdx.x >> lsh);
   if (r >= R) return;
   const int lane = (int)threadIdx.x & (L - 1);
   const int nb = (I + 31) / 32;
@@ -173,10 +173,17 @@ __global__ __launch_bounds__(256) void swiglu_bwd8_kernel(const T* __restrict__ 
 // (38304 rows of I = 112 in bf16, backward: 24 us with 64, 10 with 16).
 int row_lanes(int I) { return I > 256 ? 6 : I > 128 ? 5 : I > 64 ? 4 : 3; }
 
+// The work-groups of R rows, in two dimensions: a launch takes less than 2^32
+// threads in one, and rows at a wave each reach 2^33.
+dim3 row_groups(int R, int I) {
+  const int64_t n = cdiv(R, 256 >> row_lanes(I)), x = n < (1 << 23) ? n : 1 << 23;
+  return dim3((unsigned)x, (unsigned)cdiv(n, x));
+}
+
 template <typename T, bool NT>
 hipError_t save(const LaunchCtx& c, const void* H, const float* topk_w, const int32_t* src_of, int R, int I, float lim,
                 void* aw, uint8_t* codes, uint8_t* scales) {
-  MOE_LAUNCH(c, "swiglu_save8", (save8_kernel<T, NT>), dim3((unsigned)cdiv(R, 256 >> row_lanes(I))), dim3(256), 0,
+  MOE_LAUNCH(c, "swiglu_save8", (save8_kernel<T, NT>), row_groups(R, I), dim3(256), 0,
              (const T*)H, topk_w, src_of, R, I, row_lanes(I), lim, (T*)aw, codes, scales);
   return hipSuccess;
 }
@@ -184,7 +191,7 @@ template <typename T, bool NT>
 hipError_t backward(const LaunchCtx& c, const void* G, const uint8_t* codes, const uint8_t* scales,
                     const float* topk_w, const int32_t* src_of, int R, int I, float lim, void* dH, void* aw,
                     float* dw) {
-  MOE_LAUNCH(c, "swiglu_bwd8", (swiglu_bwd8_kernel<T, NT>), dim3((unsigned)cdiv(R, 256 >> row_lanes(I))), dim3(256), 0,
+  MOE_LAUNCH(c, "swiglu_bwd8", (swiglu_bwd8_kernel<T, NT>), row_groups(R, I), dim3(256), 0,
              (const T*)G, codes, scales, topk_w, src_of, R, I, row_lanes(I), lim, (T*)dH, (T*)aw, dw);
   return hipSuccess;
 }
