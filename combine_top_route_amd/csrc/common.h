@@ -250,9 +250,10 @@ hipError_t launch_router_bwd(const LaunchCtx& c, RouterArgs a);
 constexpr int kDecodeMaxT = 256;
 // Whether the down products of all experts are summed in one kernel (at most 32
 // slots of 8 tokens); otherwise the products of each slot go through memory and
-// a combine kernel (d = 2048, I = 768, 8 of 128 experts, bf16: 2 tokens 12.6 us
-// for the down product in one kernel; 4 tokens 19.2 and 17.7 + 4.0; 8 tokens,
-// 64 slots, 36.4 and 28.7 + 4.0).
+// a combine kernel (d = 2048, where its d / 8 work-groups are one per CU, I = 768,
+// 8 of 128 experts, bf16: 2 tokens 12.6 us for the down product in one kernel; 4
+// tokens 19.2 and 17.7 + 4.0; 8 tokens, 64 slots, 36.4 and 28.7 + 4.0).  A smaller
+// d leaves CUs without a work-group (7 tokens, 21 slots, d = 1000, float32: 8 us).
 inline bool decode_one_down(int64_t T, int64_t k) { return T <= 8 && T * k <= 32; }
 struct DecodeArgs {
   int T, d, E, k, I;

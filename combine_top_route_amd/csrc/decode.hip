@@ -18,7 +18,7 @@
 //     at once;
 //   * nothing is sorted: each work-group finds its expert's tokens in the ids
 //     (at most 256 k of them).
-// All sums are float32 in a fixed order; there are no atomics.
+// All sums are float32 in a fixed order, without floating-point atomics.
 #include <type_traits>
 
 #include "common.h"
@@ -209,9 +209,10 @@ __device__ __forceinline__ uint32_t mx_words(const void* s, int row4, int K, int
 
 // The NF / 2 MFMA operands of 16 bytes of a weight row, chunk 4 c + q of its
 // unit.  Codes become bfloat16 exactly (e4m3 has four significant bits); an
-// E8M0 scale is a power of two and rides on the conversion, also exactly down
-// to bfloat16's smallest numbers (2^-133).  mx: the row's four scale bytes of
-// this unit.
+// E8M0 scale is a power of two and rides on the conversion, which takes it from
+// the exponent field alone: byte 0 arrives as the bits of +0 and stands for 2^-127.
+// Exact down to bfloat16's smallest numbers (2^-133).  mx: the row's four scale
+// bytes of this unit.
 template <int F>
 __device__ __forceinline__ void chunk_frags(typename Fmt<F>::frag* fr, u32x4_t a, uint32_t mx, int c, int q) {
   if constexpr (F == WF_F32) {
@@ -674,7 +675,9 @@ __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
 // rows and the tokens at the first half of a unit, 8 .. 15 the same rows and
 // tokens at the second half; the two diagonal blocks of its result are the
 // sums, the others are dropped.  (T = 1, the case above: 23.1 us with tiles of
-// 16 rows, 22.4 with these.)
+// 16 rows, 22.4 with these.)  Sixteen waves with six units each in flight hold
+// all of that case's pairs, 8 experts by 12 units, at once; codes have half the
+// units and, beside them, twice the registers of activations: four.
 constexpr int kDownWaves = 16;
 
 template <int F>
@@ -1024,8 +1027,11 @@ unsigned token_split(const DecodeArgs& a, int64_t groups) {
 // Whether the weights that the tokens may select exceed the last-level cache.
 // Nothing of them is left there for the next call then, and non-temporal loads
 // keep them from displacing what this call reads again (64 tokens of 8 of 128
-// experts above: 221 us without, 204 with; 8 experts of the same size for 256
-// tokens, 75 MB read twice: 55 and 64).
+// experts above: 221 us without, 204 with).  Below that size they cost the
+// reuse, also where other layers' weights were used since the last call (256
+// tokens of 2 of 8 experts of the same size, 75 MB read twice: 44 us without and
+// 56 with them on one layer's weights, 48 and 57 on those of 16 layers in turn;
+// one token of all 8 experts 22 and 23, and 26 both ways).
 template <int F>
 bool past_cache(const DecodeArgs& a) {
   constexpr int64_t kLastLevelCache = int64_t(256) << 20;

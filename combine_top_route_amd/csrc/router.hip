@@ -9,7 +9,7 @@
 // A bf16 MFMA multiplies bf16 operands, and x and w are; a float32 dlogits is
 // split into the bf16 nearest to it and the bf16 nearest to the rest, which
 // leaves 2^-17 of it, and both parts are multiplied: the products stay bound by
-// memory, and rounding dlogits to bf16 alone would cost 2^-9.  Float32 tensors
+// memory, and rounding dlogits to bf16 alone would cost 2^-8.  Float32 tensors
 // go through the float32 MFMA.
 //
 // No product uses atomics: K or T is split over waves or work-groups and the
@@ -336,7 +336,8 @@ constexpr int dw_stage() { return (sizeof(T) == 2 && sizeof(LT) == 4 ? 3 : 2) * 
 // A sum that comes out not finite is taken from the first part's products alone,
 // in a second pass over the run that only such sums cause.
 template <typename T, typename LT, bool REST>
-__device__ __forceinline__ void dw_sums(f32x4_t (&acc)[4][2], const RouterArgs& a, char* smem, int e0, int d0, int run) {
+__device__ __forceinline__ void dw_sums(f32x4_t (&acc)[4][2], const RouterArgs& a, char* smem, int e0, int d0,
+                                        int run) {
   constexpr int TS = DwTile<T>::TS, ST = DwTile<T>::STRIDE;
   constexpr int XU = kDwD * (int)sizeof(T) / 16;          // 16-byte loads per row of x
   constexpr int XV = TS * XU / 512;

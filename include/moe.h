@@ -254,7 +254,9 @@ moe_status moe_backward(const moe_shape* shape, const void* dout, const void* x,
  *   dw_router [E,d] = dlogits^T x;
  * all others in dtype; float32 sums in a fixed order, one rounding each.  With
  * dtype MOE_BF16 a float32 dlogits enters the products as the sum of two bf16
- * values (up to 2^-17 of it is lost).  Every pointer 16-byte aligned; dx and
+ * values (up to 2^-17 of it is lost; one beyond bfloat16's range counts as an
+ * infinity).  Infinities of x, w_router and dlogits give infinities where the
+ * formulas do.  Every pointer 16-byte aligned; dx and
  * dw_router overlap no input (but dx_in, as said) and not each other;
  * workspace: moe_router_workspace_size bytes, for the backward only. */
 moe_status moe_router_forward(const moe_shape* shape, const void* x, const void* w_router,
@@ -278,7 +280,7 @@ moe_status moe_router_backward(const moe_shape* shape, const void* dlogits, cons
  *              multiple of 256 bytes, scale bytes [T*k, 2 ceil(I/32)];
  *   workspace: moe_workspace8_size bytes (op MOE_OP_FORWARD or
  *              MOE_OP_BACKWARD).
- * Everything else is as for moe_forward and moe_backward. */
+ * Everything else, flags included, is as for moe_forward and moe_backward. */
 moe_status moe_saved8_size(const moe_shape* shape, size_t* bytes);
 moe_status moe_workspace8_size(const moe_shape* shape, int op, size_t* bytes);
 moe_status moe_forward8(const moe_shape* shape, const void* x, moe_routing* routing,
@@ -337,7 +339,8 @@ moe_status moe_swiglu_backward8(const moe_shape* shape, const void* G, const uin
  * expert; topk_ids then holds -1 and topk_w 0).  An empty slot adds nothing,
  * whatever its weight, and a token whose slots are all empty (the padding of
  * a batch) gets a row of zeros.  An id given twice in a row counts twice.
- * NaN and infinities stay in the tokens they reach.
+ * NaN and infinities stay in the tokens they reach, and an infinite weight gives
+ * infinities where the formula does.
  *
  * workspace: moe_decode_workspace_size bytes, 256-byte aligned (no initial
  * contents needed); calls that overlap in time, replayed graphs among them,
