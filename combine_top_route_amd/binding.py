@@ -210,6 +210,14 @@ class Routing:
             counts=torch.empty(E, **i32), offsets=torch.empty(E + 1, **i32),
             row_of=torch.empty(T * k, **i32), src_of=torch.empty(T * k, **i32), logits=logits)
 
+    def on(self, device, *names) -> "Routing":
+        """self, if the named tensors (those a call reads or writes) are on `device`."""
+        for name in names:
+            t = getattr(self, name)
+            if t is not None and t.device != device:
+                raise ValueError(f"routing.{name} is on {t.device}, expected {device}")
+        return self
+
     def c(self) -> MoeRouting:
         return MoeRouting(_ptr(self.logits), _ptr(self.topk_ids), _ptr(self.topk_w), _ptr(self.counts),
                           _ptr(self.offsets), _ptr(self.row_of), _ptr(self.src_of))
@@ -563,7 +571,7 @@ def route_noalloc(r: Routing, T, E, k, logits_dtype=torch.bfloat16):
     """moe_route_noalloc into the caller's routing tensors r (logits in when
     r.logits is set, else r.topk_ids / r.topk_w in); no workspace."""
     shape = make_shape(T, 8, E, k, 8, torch.bfloat16, logits_dtype)
-    cr = r.c()
+    cr = r.on(r.counts.device, "logits", "topk_ids", "topk_w", "offsets", "row_of", "src_of").c()
     with _on(r.counts.device):
         _check("moe_route_noalloc", lib().moe_route_noalloc(ctypes.byref(shape), ctypes.byref(cr),
                                                              _stream(r.counts.device)))
@@ -577,7 +585,7 @@ def permute(x, routing: Routing, k, out=None):
     shape = make_shape(T, d, E, k, 8, x.dtype)
     xp = torch.empty((T * k, d), dtype=x.dtype, device=x.device) if out is None else out
     _need(xp, "out", (T * k, d), x.dtype, x.device)
-    cr = routing.c()
+    cr = routing.on(x.device, "src_of", "row_of").c()
     with _on(x.device):
         _check("moe_permute", lib().moe_permute(ctypes.byref(shape), _ptr(x), ctypes.byref(cr), _ptr(xp),
                                                  _stream(x.device)))
@@ -589,7 +597,7 @@ def combine(rows, routing: Routing, T, k):
     E = routing.counts.numel()
     shape = make_shape(T, d, E, k, 8, rows.dtype)
     out = torch.empty((T, d), dtype=rows.dtype, device=rows.device)
-    cr = routing.c()
+    cr = routing.on(rows.device, "row_of", "topk_w").c()
     with _on(rows.device):
         _check("moe_combine", lib().moe_combine(ctypes.byref(shape), _ptr(rows), ctypes.byref(cr), _ptr(out),
                                                  _stream(rows.device)))
@@ -644,7 +652,7 @@ def quantize_tokens_fp8(src, routing: Routing, T, k, gather):
     q = torch.zeros((C, 128 * nblk), dtype=torch.uint8, device=dev)
     s = torch.zeros((C, nblk), dtype=torch.float32, device=dev)
     ws = torch.empty(workspace_size(shape, OP_ROUTE), dtype=torch.uint8, device=dev)
-    cr = routing.c()
+    cr = routing.on(dev, "offsets", *(["src_of"] if gather else [])).c()
     with _on(dev):
         _check("moe_quantize_tokens_fp8", lib().moe_quantize_tokens_fp8(
             ctypes.byref(shape), _ptr(src), C, 1 if gather else 0, ctypes.byref(cr), _ptr(q), _ptr(s), _ptr(ws),
@@ -687,7 +695,7 @@ def quantize_tokens_mxfp8(src, routing: Routing, T, k, gather):
     q = torch.zeros((C, 128 * nblk), dtype=torch.uint8, device=dev)
     s = torch.zeros((C, 4 * nblk), dtype=torch.uint8, device=dev)
     ws = torch.empty(workspace_size(shape, OP_ROUTE), dtype=torch.uint8, device=dev)
-    cr = routing.c()
+    cr = routing.on(dev, "offsets", *(["src_of"] if gather else [])).c()
     with _on(dev):
         _check("moe_quantize_tokens_mxfp8", lib().moe_quantize_tokens_mxfp8(
             ctypes.byref(shape), _ptr(src), C, 1 if gather else 0, ctypes.byref(cr), _ptr(q), _ptr(s), _ptr(ws),
