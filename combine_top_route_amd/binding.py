@@ -257,6 +257,7 @@ class MoeLayer:
         self.saved = torch.empty(ns, dtype=torch.uint8, device=dev) if save else None
         self.out = torch.empty((T, d), dtype=dtype, device=dev)
         self.routing = Routing.empty(T, E, k, dev)
+        self._topk = self.routing.topk_ids, self.routing.topk_w  # of the logits form
         self.dx = torch.empty((T, d), dtype=dtype, device=dev)
         self.dw_gate_up = torch.empty((E, 2 * I, d), dtype=dtype, device=dev)
         self.dw_down = torch.empty((E, d, I), dtype=dtype, device=dev)
@@ -282,6 +283,7 @@ class MoeLayer:
         if logits is not None:
             _need(logits, "logits", (T, E), self.logits_dtype, dev)
             r.logits = logits
+            r.topk_ids, r.topk_w = self._topk
         else:
             _need(topk_ids, "topk_ids", (T, k), torch.int32, dev)
             _need(topk_w, "topk_w", (T, k), torch.float32, dev)
