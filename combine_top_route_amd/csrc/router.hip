@@ -228,7 +228,8 @@ __device__ __forceinline__ void split_bf16(float v, bf16_t& hi, bf16_t& lo) {
 }
 
 // The rest lo must not meet an infinity of x or w: 0 inf, or a rest of the other
-// sign, would make a NaN of the formula's infinity, which hi gives alone.
+// sign, would make a NaN of the formula's infinity, which hi gives alone.  (At the
+// size above 60.3 us without what follows from this, 61.2 with.)
 __device__ __forceinline__ bool is_finite(float v) { return fabsf(v) < __builtin_huge_valf(); }
 // Of bf16 operands: whether one is not finite, and the same with those as zeros.
 struct NotFinite {

@@ -100,3 +100,17 @@ def test_routed_inside(T, d, E, k, I, dtype, weights):
     if k > 1:
         gid[0, 1] = gid[0, 0]
         check(dec.forward(x, wgu, wd, topk_ids=gid, topk_w=gw), x, cut(wgu), cut(wd), remap[gid.long()], gw)
+
+
+@pytest.mark.parametrize("T", [1, 7, 12, 40])
+def test_one_decoder_for_layers_in_a_row(T):
+    """The decoder's own output as the next layer's x."""
+    d, E, k, I = 136, 12, 3, 72
+    layers = [make(T, d, E, k, I, seed=90 + i) for i in range(4)]
+    one = decoder(layers[0][0], E, k, I)
+    h = g = layers[0][0]
+    for _, wgu, wd, lg in layers:
+        h = one.forward(h, wgu, wd, logits=lg)
+        g = decoder(g, E, k, I).forward(g.clone(), wgu, wd, logits=lg)
+        assert torch.equal(h, g)
+    assert bool(g.any())
