@@ -18,7 +18,9 @@ kernel ...").  Here:
 Beside the layer: ``moe_fwd8`` / ``moe_bwd8`` (``save8=True``: the activations
 kept in 8 bits), ``router_fwd`` / ``router_bwd`` (the projection that makes the
 logits; ``router`` and, with the layer, ``moe_block``), and ``moe_decode`` (the
-layer for at most 256 tokens, without a gradient).
+layer for at most 256 tokens, without a gradient), ``norm_fwd`` / ``norm_bwd``
+(the norms before and after the block with its gate and residual scale;
+``norm_residual`` and, around the block, ``moe_residual_block``).
 
 Every call allocates its outputs and workspace from torch's caching
 allocator on the inputs' device and enqueues on torch's current stream.
@@ -466,3 +468,110 @@ def moe_block(x: Tensor, w_router: Tensor, w_gate_up: Tensor, w_down: Tensor, k:
     _check_router_args(x, w_router, logits_dtype)
     logits, x = _Router.apply(x, w_router, logits_dtype)
     return moe_layer(x, logits, w_gate_up, w_down, k, precision, recompute, swiglu_limit, save8)
+
+
+# ------------------------------------------------------- norms and residual
+def _check_norm_args(rows: Tensor, name: str, same: dict, w_post, gate, w_next):
+    """rows [T,d] and whatever is given of `same` (like rows), the weights [d]
+    and the gate ([d] or [T,1]): one float type, contiguous."""
+    _require(rows.dim() == 2 and rows.dtype in _FLOATS,
+             f"{name} must be [T, d] of one of {_FLOATS}, got {tuple(rows.shape)} {rows.dtype}")
+    T, d = rows.shape
+    want = {name: (rows, [(T, d)]), "w_post": (w_post, [(d,)]), "w_next": (w_next, [(d,)]),
+            "gate": (gate, [(d,), (T, 1)])}
+    want.update({n: (t, [(T, d)]) for n, t in same.items()})
+    for n, (t, shapes) in want.items():
+        if t is not None:
+            _require(tuple(t.shape) in shapes and t.dtype == rows.dtype,
+                     f"{n} must be {shapes} {rows.dtype}, got {tuple(t.shape)} {t.dtype}")
+            _require(t.is_contiguous(), f"{n} must be contiguous")
+    return {n: t for n, (t, _) in want.items() if t is not None}
+
+
+@torch.library.custom_op(f"{_NS}::norm_fwd", mutates_args=())
+def norm_fwd(x: Tensor, y: Tensor | None, w_post: Tensor | None, gate: Tensor | None, w_next: Tensor | None,
+             res_scale: float, eps: float) -> tuple[Tensor, Tensor]:
+    """(z, h) of binding.norm_residual; empty where there is no y, or no w_next."""
+    _check_devices(**_check_norm_args(x, "x", {"y": y}, w_post, gate, w_next))
+    z, h = B.norm_residual(x, y, w_post, gate, res_scale, w_next, eps)
+    return x.new_empty(0) if y is None else z, x.new_empty(0) if h is None else h
+
+
+@norm_fwd.register_fake
+def _(x, y, w_post, gate, w_next, res_scale, eps):
+    return (x.new_empty(0) if y is None else torch.empty_like(x),
+            x.new_empty(0) if w_next is None else torch.empty_like(x))
+
+
+@torch.library.custom_op(f"{_NS}::norm_bwd", mutates_args=())
+def norm_bwd(dz: Tensor | None, dh: Tensor | None, z: Tensor, y: Tensor | None, w_post: Tensor | None,
+             gate: Tensor | None, w_next: Tensor | None, res_scale: float, eps: float
+             ) -> tuple[Tensor, Tensor, Tensor, Tensor, Tensor]:
+    """(dx, dy, dw_post, dgate, dw_next) of binding.norm_residual_backward;
+    empty where there is none."""
+    dz = None if dz is None else _dense(dz)
+    dh = None if dh is None else _dense(dh)
+    _check_devices(**_check_norm_args(z, "z", {"dz": dz, "dh": dh, "y": y}, w_post, gate, w_next))
+    g = B.norm_residual_backward(dz, dh, z, y, w_post, gate, res_scale, w_next, eps)
+    return tuple(z.new_empty(0) if g[n] is None else g[n] for n in ("dx", "dy", "dw_post", "dgate", "dw_next"))
+
+
+@norm_bwd.register_fake
+def _(dz, dh, z, y, w_post, gate, w_next, res_scale, eps):
+    return tuple(z.new_empty(0) if t is None else torch.empty_like(t) for t in (z, y, w_post, gate, w_next))
+
+
+class _NormResidual(torch.autograd.Function):
+    """z is saved as it leaves (x itself without a y, passed through so that
+    what comes back along the residual stream is added in the same pass)."""
+
+    @staticmethod
+    def forward(ctx, x, y, w_post, gate, w_next, res_scale, eps):
+        z, h = norm_fwd(x, y, w_post, gate, w_next, res_scale, eps)
+        if y is None:
+            z = x.view_as(x)
+        ctx.save_for_backward(z, y, w_post, gate, w_next)
+        ctx.scales = res_scale, eps
+        ctx.set_materialize_grads(False)  # no zeros to add where z or h was not used
+        return z, None if w_next is None else h
+
+    @staticmethod
+    def backward(ctx, dz, dh):
+        z, y, w_post, gate, w_next = ctx.saved_tensors
+        if dz is None and dh is None:
+            return (None,) * 7
+        if dh is None and y is None:
+            return (dz,) + (None,) * 6
+        used = None if dh is None else w_next
+        grads = norm_bwd(dz, dh, z, y, w_post, gate, used, *ctx.scales)
+        return tuple(g if t is not None else None for g, t in zip(grads, (z, y, w_post, gate, used))) + (None, None)
+
+
+def norm_residual(x: Tensor, y: Tensor | None = None, w_post: Tensor | None = None, gate: Tensor | None = None,
+                  res_scale: float = 1.0, w_next: Tensor | None = None, eps: float = 1e-6
+                  ) -> tuple[Tensor, Tensor | None]:
+    """(z, h) around a block, differentiable in every tensor: z = res_scale x +
+    gate N(y; w_post) and h = N(z; w_next), N(v; w) = v / sqrt(mean(v^2) + eps) w.
+    Without y z is x, without w_next h is None; gate: [d], or [T, 1] for one per
+    token.  In a HIP graph, capture on leaves of the graph's own (see
+    moe_layer)."""
+    _check_norm_args(x, "x", {"y": y}, w_post, gate, w_next)
+    if y is None:
+        _require(w_post is None and gate is None and res_scale == 1.0, "w_post, gate and res_scale need y")
+        _require(w_next is not None, "give y or w_next")
+    return _NormResidual.apply(x, y, w_post, gate, w_next, float(res_scale), float(eps))
+
+
+def moe_residual_block(x: Tensor, w_router: Tensor, w_gate_up: Tensor, w_down: Tensor, k: int,
+                       w_pre: Tensor | None = None, w_post: Tensor | None = None, gate: Tensor | None = None,
+                       res_scale: float = 1.0, w_next: Tensor | None = None, eps: float = 1e-6,
+                       h: Tensor | None = None, **layer) -> tuple[Tensor, Tensor | None]:
+    """moe_block with the norms and the residual around it: (z, h_next) of the
+    residual stream x [T,d], z = res_scale x + gate N(moe_block(h); w_post),
+    h_next = N(z; w_next), where h = N(x; w_pre), or is given (the last block's
+    h_next).  `layer`: moe_block's options."""
+    _require((w_pre is None) != (h is None), "give w_pre, or h from the block before")
+    if h is None:
+        x, h = norm_residual(x, w_next=w_pre, eps=eps)
+    y = moe_block(h, w_router, w_gate_up, w_down, k, **layer)
+    return norm_residual(x, y, w_post, gate, res_scale, w_next, eps)

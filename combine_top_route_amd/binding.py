@@ -23,6 +23,7 @@ PREC_NATIVE, PREC_FP8_BLOCK, PREC_MXFP8, PREC_FP8_BWD = 0, 1, 2, 3
 OP_ROUTE, OP_FORWARD, OP_BACKWARD, OP_BACKWARD_RECOMPUTE = 0, 1, 2, 3
 QUANT_ROWS, QUANT_WEIGHT, QUANT_WEIGHT_T = 0, 1, 2
 DECODE_MAX_T = 256
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 
 _DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _TORCH = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
@@ -35,6 +36,11 @@ class MoeShape(ctypes.Structure):
                 ("k", ctypes.c_int64), ("I", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("logits_dtype", ctypes.c_int32), ("precision", ctypes.c_int32),
                 ("swiglu_limit", ctypes.c_float), ("flags", ctypes.c_int32)]
+
+
+class MoeNormShape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("gate_kind", ctypes.c_int32), ("res_scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class MoeRouting(ctypes.Structure):
@@ -78,6 +84,9 @@ _SIGS = [
     ("moe_decode_workspace_size", ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.POINTER(ctypes.c_size_t)]),
     ("moe_decode", ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.c_int, _P, ctypes.POINTER(MoeRouting), _P, _P, _P,
                                   _P, _P, _P, ctypes.c_size_t, _P]),
+    ("moe_norm_forward", ctypes.c_int, [ctypes.POINTER(MoeNormShape)] + [_P] * 8),
+    ("moe_norm_workspace_size", ctypes.c_int, [ctypes.POINTER(MoeNormShape), ctypes.POINTER(ctypes.c_size_t)]),
+    ("moe_norm_backward", ctypes.c_int, [ctypes.POINTER(MoeNormShape)] + [_P] * 13 + [ctypes.c_size_t, _P]),
     ("moe_permute", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.POINTER(MoeRouting), _P, _P]),
     ("moe_combine", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.POINTER(MoeRouting), _P, _P]),
     ("moe_quantize_fp8", ctypes.c_int, [ctypes.c_int, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P,
@@ -444,6 +453,84 @@ def swiglu_backward8(G, codes, scales, routing: Routing, T, k, swiglu_limit=0.0)
             ctypes.byref(shape), _ptr(G), _ptr(codes), _ptr(scales), ctypes.byref(cr), _ptr(dh), _ptr(aw), _ptr(dw),
             _stream(dev)))
     return dh, aw, dw
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_shape(T, d, dtype, gate_kind, res_scale, eps):
+    return MoeNormShape(T, d, _DT[dtype], gate_kind, res_scale, eps)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(T, d, dtype):
+    return norm_workspace_size(MoeNormShape(T, d, _DT[dtype], GATE_NONE, 1.0, 1.0))
+
+
+def norm_workspace_size(shape: MoeNormShape) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_norm_workspace_size", lib().moe_norm_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def _norm_args(rows, name, w_post, gate, w_next, res_scale, eps):
+    """Checks a norm's weights against rows [T, d]; its shape argument."""
+    if rows.dim() != 2 or rows.dtype not in _DT:
+        raise ValueError(f"{name} must be [T, d] of one of {tuple(_DT)}, got {tuple(rows.shape)} {rows.dtype}")
+    T, d = rows.shape
+    dt, dev = rows.dtype, rows.device
+    _need(rows, name, (T, d), dt, dev)
+    if w_post is not None:
+        _need(w_post, "w_post", (d,), dt, dev)
+    if w_next is not None:
+        _need(w_next, "w_next", (d,), dt, dev)
+    kind = GATE_NONE
+    if gate is not None:
+        kind = GATE_CHANNEL if gate.dim() == 1 else GATE_TOKEN
+        _need(gate, "gate ([d] or [T, 1])", (d,) if kind == GATE_CHANNEL else (T, 1), dt, dev)
+    return _norm_shape(T, d, dt, kind, float(res_scale), float(eps))
+
+
+def norm_residual(x, y=None, w_post=None, gate=None, res_scale=1.0, w_next=None, eps=1e-6):
+    """(z, h) of the residual stream x [T, d] and a block's output y
+    (moe_norm_forward in include/moe.h): z = res_scale x + gate N(y; w_post), h
+    = N(z; w_next), N(v; w) = v / sqrt(mean(v^2) + eps) w.  Without y z is x
+    itself, without w_next h is None.  gate: [d], or [T, 1] for one per token.
+    All in x's dtype."""
+    shape = _norm_args(x, "x", w_post, gate, w_next, res_scale, eps)
+    dev = x.device
+    if y is not None:
+        _need(y, "y", x.shape, x.dtype, dev)
+    with _on(dev):
+        z = None if y is None else torch.empty_like(x)
+        h = None if w_next is None else torch.empty_like(x)
+        _check("moe_norm_forward", lib().moe_norm_forward(
+            ctypes.byref(shape), _ptr(x), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_next), _ptr(z), _ptr(h),
+            _stream(dev)))
+    return x if y is None else z, h
+
+
+def norm_residual_backward(dz, dh, z, y=None, w_post=None, gate=None, res_scale=1.0, w_next=None, eps=1e-6):
+    """Gradients of norm_residual from those of its z and h (dz or dh may be
+    None; dh and w_next come together), at its z (x where there was no y) and y
+    (moe_norm_backward): a dict of dx, dy (None without y), dw_post, dgate and
+    dw_next (None where that weight is)."""
+    if (dh is None) != (w_next is None):
+        raise ValueError("give dh and w_next, or neither")
+    shape = _norm_args(z, "z", w_post, gate, w_next, res_scale, eps)
+    dev = z.device
+    for name, t in (("dz", dz), ("dh", dh), ("y", y)):
+        if t is not None:
+            _need(t, name, z.shape, z.dtype, dev)
+    n = _norm_workspace(z.shape[0], z.shape[1], z.dtype)
+    with _on(dev):
+        out = {"dx": torch.empty_like(z)}
+        for name, t in (("dy", y), ("dw_post", w_post), ("dgate", gate), ("dw_next", w_next)):
+            out[name] = None if t is None else torch.empty_like(t)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        _check("moe_norm_backward", lib().moe_norm_backward(
+            ctypes.byref(shape), _ptr(dz), _ptr(dh), _ptr(z), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_next),
+            _ptr(out["dx"]), _ptr(out["dy"]), _ptr(out["dw_post"]), _ptr(out["dgate"]), _ptr(out["dw_next"]),
+            _ptr(ws), n, _stream(dev)))
+    return out
 
 
 def decode_workspace_size(shape: MoeShape) -> int:

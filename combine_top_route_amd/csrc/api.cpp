@@ -5,6 +5,7 @@
 // argument enqueues nothing.  The library owns no device memory: all buffers
 // come from the caller, and the workspace is carved into fixed regions.
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -445,6 +446,63 @@ RouterArgs router_args(const moe_shape* s, const void* x, const void* w) {
 
 size_t router_workspace(const moe_shape* s) {  // the parts of dw
   return sizeof(float) * router_plan(s->T, s->d, s->E, s->dtype).runs * s->E * s->d;
+}
+
+// ------------------------------------------------------------------- norms
+struct Span {  // p == NULL: nothing
+  const void* p;
+  size_t n;
+};
+bool overlap(const Span& a, const Span& b) { return a.p && b.p && overlap(a.p, a.n, b.p, b.n); }
+
+moe_status check_norm(const moe_norm_shape* s) {
+  if (!s) return fail(MOE_ERR_INVALID_ARGUMENT, "shape is NULL");
+  if (s->T < 1 || s->T > kMaxT) return fail(MOE_ERR_INVALID_ARGUMENT, "T=%lld outside [1, 2^24]", (long long)s->T);
+  if (s->d < 8 || s->d > 16384 || s->d % 8)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "d=%lld must be a multiple of 8 in [8, 16384]", (long long)s->d);
+  if (s->dtype != MOE_F32 && s->dtype != MOE_BF16) return fail(MOE_ERR_INVALID_ARGUMENT, "dtype=%d unknown", s->dtype);
+  if (s->gate_kind < MOE_GATE_NONE || s->gate_kind > MOE_GATE_TOKEN)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "gate_kind=%d unknown", s->gate_kind);
+  if (!(s->eps > 0.0f && s->eps <= std::numeric_limits<float>::max()))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "eps=%g must be positive and finite", (double)s->eps);
+  if (!(std::abs(s->res_scale) <= std::numeric_limits<float>::max()))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "res_scale=%g must be finite", (double)s->res_scale);
+  return MOE_OK;
+}
+
+moe_status check_norm_weights(const moe_norm_shape* s, const void* w_post, const void* gate, const void* w_next) {
+  if (!gate != (s->gate_kind == MOE_GATE_NONE))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "gate_kind=%d and a gate that is %s", s->gate_kind, gate ? "given" : "NULL");
+  TRY(check_aligned16(w_post, "w_post"));
+  TRY(check_aligned16(w_next, "w_next"));
+  if (s->gate_kind == MOE_GATE_CHANNEL) TRY(check_aligned16(gate, "gate"));
+  if ((uintptr_t)gate & (elem_size(s->dtype) - 1))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "gate must be aligned to its elements");
+  return MOE_OK;
+}
+
+size_t gate_bytes(const moe_norm_shape* s) {
+  return elem_size(s->dtype) * (s->gate_kind == MOE_GATE_CHANNEL ? s->d : s->gate_kind == MOE_GATE_TOKEN ? s->T : 0);
+}
+
+size_t norm_workspace(const moe_norm_shape* s) {  // the work-groups' two column sums
+  return sizeof(float) * 2 * s->d * norm_bwd_groups(s->T, s->d, s->dtype);
+}
+
+NormArgs norm_args(const moe_norm_shape* s, const void* y, const void* w_post, const void* gate, const void* w_next) {
+  NormArgs a = {};
+  a.T = s->T;
+  a.d = (int)s->d;
+  a.dtype = s->dtype;
+  a.gate_kind = s->gate_kind;
+  a.scale = s->res_scale;
+  a.eps = s->eps;
+  a.inv_d = 1.0f / (float)s->d;
+  a.y = y;
+  a.w_post = w_post;
+  a.gate = gate;
+  a.w_next = w_next;
+  return a;
 }
 
 // ------------------------------------------------------------ few tokens
@@ -931,6 +989,103 @@ moe_status moe_decode(const moe_shape* shape, int weights, const void* x, moe_ro
   const LaunchCtx c = make_ctx(stream);
   (void)hipGetLastError();
   HIP_TRY(launch_decode(c, a, weights), "decode");
+  return MOE_OK;
+}
+
+moe_status moe_norm_forward(const moe_norm_shape* shape, const void* x, const void* y, const void* w_post,
+                            const void* gate, const void* w_next, void* z, void* h, void* stream) {
+  TRY(check_norm(shape));
+  CHECK_PTR(x);
+  if (y) {
+    CHECK_PTR(z);
+  } else {
+    if (z || w_post || gate || shape->gate_kind != MOE_GATE_NONE)
+      return fail(MOE_ERR_INVALID_ARGUMENT, "z, w_post and gate need y");
+    if (shape->res_scale != 1.0f) return fail(MOE_ERR_INVALID_ARGUMENT, "res_scale must be 1 without y");
+    CHECK_PTR(w_next);
+  }
+  TRY(check_norm_weights(shape, w_post, gate, w_next));
+  if (!w_next != !h) return fail(MOE_ERR_INVALID_ARGUMENT, "give w_next and h, or neither");
+  TRY(check_aligned16(x, "x"));
+  TRY(check_aligned16(y, "y"));
+  TRY(check_aligned16(z, "z"));
+  TRY(check_aligned16(h, "h"));
+  const size_t es = elem_size(shape->dtype), rows = es * shape->T * shape->d, cols = es * shape->d;
+  const size_t gates = gate_bytes(shape);
+  const Span in[] = {{x, rows}, {y, rows}, {w_post, cols}, {gate, gates}, {w_next, cols}};
+  for (int i = 0; i < 5; ++i) {
+    const bool in_place = i < 2 && in[i].p == z;
+    if ((!in_place && overlap(Span{z, rows}, in[i])) || overlap(Span{h, rows}, in[i]))
+      return fail(MOE_ERR_INVALID_ARGUMENT, "z and h must not overlap an input");
+  }
+  if (overlap(Span{z, rows}, Span{h, rows})) return fail(MOE_ERR_INVALID_ARGUMENT, "z and h overlap");
+  NormArgs a = norm_args(shape, y, w_post, gate, w_next);
+  a.x = x;
+  a.z = z;
+  a.h = h;
+  const LaunchCtx c = make_ctx(stream);
+  (void)hipGetLastError();
+  HIP_TRY(launch_norm_fwd(c, a), "norm_forward");
+  return MOE_OK;
+}
+
+moe_status moe_norm_workspace_size(const moe_norm_shape* shape, size_t* bytes) {
+  TRY(check_norm(shape));
+  CHECK_PTR(bytes);
+  *bytes = norm_workspace(shape);
+  return MOE_OK;
+}
+
+moe_status moe_norm_backward(const moe_norm_shape* shape, const void* dz, const void* dh, const void* z,
+                             const void* y, const void* w_post, const void* gate, const void* w_next, void* dx,
+                             void* dy, void* dw_post, void* dgate, void* dw_next, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  TRY(check_norm(shape));
+  CHECK_PTR(dx);
+  if (!dz && !dh) return fail(MOE_ERR_INVALID_ARGUMENT, "dz and dh are both NULL");
+  if (!dh != !w_next || !dw_next != !w_next)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "give w_next, dh and dw_next, or none of them");
+  if (w_next) CHECK_PTR(z);
+  TRY(check_norm_weights(shape, w_post, gate, w_next));
+  if (!dy && (w_post || gate)) return fail(MOE_ERR_INVALID_ARGUMENT, "w_post and gate need dy");
+  if (!dy && shape->res_scale != 1.0f) return fail(MOE_ERR_INVALID_ARGUMENT, "res_scale must be 1 without dy");
+  if (w_post || gate) CHECK_PTR(y);
+  if (!dw_post != !w_post) return fail(MOE_ERR_INVALID_ARGUMENT, "give w_post and dw_post, or neither");
+  if (!dgate != !gate) return fail(MOE_ERR_INVALID_ARGUMENT, "give gate and dgate, or neither");
+  TRY(check_ws_bytes(norm_workspace(shape), workspace, workspace_bytes));
+  TRY(check_aligned16(dz, "dz"));
+  TRY(check_aligned16(dh, "dh"));
+  TRY(check_aligned16(z, "z"));
+  TRY(check_aligned16(y, "y"));
+  TRY(check_aligned16(dx, "dx"));
+  TRY(check_aligned16(dy, "dy"));
+  const size_t es = elem_size(shape->dtype);
+  if (((uintptr_t)dw_post | (uintptr_t)dgate | (uintptr_t)dw_next) & (es - 1))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "dw_post, dgate and dw_next must be aligned to their elements");
+  const size_t rows = es * shape->T * shape->d, cols = es * shape->d, gates = gate_bytes(shape);
+  const Span in[] = {{dz, rows},     {dh, rows},    {z, rows},      {y, rows},
+                     {w_post, cols}, {gate, gates}, {w_next, cols}, {workspace, norm_workspace(shape)}};
+  const Span out[] = {{dx, rows}, {dy, rows}, {dw_post, cols}, {dgate, gates}, {dw_next, cols}};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 8; ++j)
+      if (overlap(out[i], in[j]) && !(i == 0 && j == 0 && dx == dz))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "gradients must not overlap an input or the workspace");
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return fail(MOE_ERR_INVALID_ARGUMENT, "gradients overlap each other");
+  }
+  NormArgs a = norm_args(shape, w_post || gate ? y : nullptr, w_post, gate, w_next);
+  a.dz = dz;
+  a.dh = dh;
+  a.z_in = z;
+  a.dx = dx;
+  a.dy = dy;
+  a.dw_post = dw_post;
+  a.dgate = dgate;
+  a.dw_next = dw_next;
+  a.parts = (float*)workspace;
+  const LaunchCtx c = make_ctx(stream);
+  (void)hipGetLastError();
+  HIP_TRY(launch_norm_bwd(c, a), "norm_backward");
   return MOE_OK;
 }
 

@@ -245,6 +245,36 @@ struct RouterArgs {
 hipError_t launch_router_fwd(const LaunchCtx& c, const RouterArgs& a, void* logits);
 hipError_t launch_router_bwd(const LaunchCtx& c, RouterArgs a);
 
+// ------------------------------------------------------------------- norms
+// (norm.hip) The norms around a block with its gate and residual scale.
+struct NormArgs {
+  int64_t T;
+  int d;
+  int dtype;
+  int gate_kind;       // moe_gate_kind
+  float scale, eps, inv_d;
+  const void* x;       // forward: [T, d]
+  const void* y;       // [T, d] or null
+  const void* w_post;  // [d] or null
+  const void* gate;    // [d] or [T] by gate_kind
+  const void* w_next;  // [d] or null
+  void* z;             // forward's outputs (null: not made)
+  void* h;
+  const void* dz;      // backward: [T, d] or null
+  const void* dh;      // with w_next
+  const void* z_in;    // with w_next
+  void* dx;
+  void* dy;            // null: no block
+  void* dw_post;
+  void* dgate;
+  void* dw_next;
+  float* parts;        // [groups, 2, d] workspace
+};
+// Work-groups of the backward.
+int64_t norm_bwd_groups(int64_t T, int64_t d, int dtype);
+hipError_t launch_norm_fwd(const LaunchCtx& c, const NormArgs& a);
+hipError_t launch_norm_bwd(const LaunchCtx& c, const NormArgs& a);
+
 // ------------------------------------------------------------ few tokens
 // The whole layer for up to kDecodeMaxT tokens (decode.hip).
 constexpr int kDecodeMaxT = 256;

@@ -352,6 +352,46 @@ moe_status moe_decode(const moe_shape* shape, int weights, const void* x, moe_ro
                       const void* s_down, void* out, void* workspace, size_t workspace_bytes,
                       void* stream);
 
+/* The norms before and after a block with its gate and residual scale, in one
+ * pass over the rows.  With N(v; w) = v / sqrt(mean(v^2) + eps) * w over a
+ * row's d columns:
+ *   z = res_scale * x + gate * N(y; w_post)   (no w_post: N(y) = y; no gate: 1)
+ *   h = N(z; w_next)                          (of z before its rounding to dtype)
+ * x [T,d] is the residual stream, y [T,d] the block's output; z goes on as the
+ * residual stream and h into the next block.  y == NULL: the norm alone, h =
+ * N(x; w_next) (then w_post, gate and z are NULL and res_scale is 1).  w_next
+ * == NULL: no h (h is then NULL).  gate: [d] with MOE_GATE_CHANNEL, [T] with
+ * MOE_GATE_TOKEN.  All tensors in dtype; sums in float32, one rounding of each
+ * result.  An infinity or NaN of x or y stays in its row.  A row whose squares
+ * pass float32's range has rsqrt 0.
+ *
+ * moe_norm_backward: the gradient of sum(dz z) + sum(dh h) at z (moe_norm_forward's,
+ * or x without a block) and y.  dz or dh may be NULL; dh and w_next are given
+ * together (then z too).  Outputs: dx [T,d] and, with a block (dy != NULL; y is
+ * needed with w_post or a gate): dy [T,d], dw_post [d] with w_post, dgate (of
+ * gate's extents) with a gate; dw_next [d] with w_next.  The sums over tokens
+ * are float32, in a fixed order.  T <= 2^24, d as in moe_shape, eps > 0.
+ *
+ * Every matrix and weight 16-byte aligned (a gate per token and its gradient:
+ * by element); outputs overlap no input and not each other, but z may be x or
+ * y and dx may be dz.  workspace: moe_norm_workspace_size bytes, 256-byte
+ * aligned, for the backward only. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_gate_kind;
+typedef struct {
+  int64_t T, d;
+  int32_t dtype;     /* moe_dtype */
+  int32_t gate_kind; /* moe_gate_kind */
+  float res_scale, eps;
+} moe_norm_shape;
+moe_status moe_norm_forward(const moe_norm_shape* shape, const void* x, const void* y,
+                            const void* w_post, const void* gate, const void* w_next, void* z,
+                            void* h, void* stream);
+moe_status moe_norm_workspace_size(const moe_norm_shape* shape, size_t* bytes);
+moe_status moe_norm_backward(const moe_norm_shape* shape, const void* dz, const void* dh,
+                             const void* z, const void* y, const void* w_post, const void* gate,
+                             const void* w_next, void* dx, void* dy, void* dw_post, void* dgate,
+                             void* dw_next, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Dispatch alone ("token sorting": "Prime Mega MoE Trains Giant AI Models
  * 55% Faster", section "Where MoE training loses time"): xp[r] =
  * x[src_of[r] / k], xp [T*k, d] (dtype), rows in expert order; reads
