@@ -309,13 +309,16 @@ moe_fwd8.register_autograd(_backward8, setup_context=_setup_context8)
 # ---------------------------------------------------------------- few tokens
 def _check_decode_args(x, logits, w_gate_up, w_down, k, s_gate_up, s_down) -> str:
     """Shapes and dtypes of moe_decode; returns the weights' format."""
-    _require(x.dim() == 2 and w_gate_up.dim() == 3 and w_gate_up.shape[2] == x.shape[1]
+    # two e2m1 codes to a byte
+    per = 2 if s_gate_up is not None and x.dim() == 2 and w_gate_up.shape[-1] * 2 == x.shape[1] else 1
+    _require(x.dim() == 2 and w_gate_up.dim() == 3 and w_gate_up.shape[2] * per == x.shape[1]
              and w_gate_up.shape[1] % 2 == 0,
              f"x must be [T, d] and w_gate_up [E, 2I, d], got {tuple(x.shape)} and {tuple(w_gate_up.shape)}")
     T, d = x.shape
     E, two_i, _ = w_gate_up.shape
     I = two_i // 2
-    _require(tuple(w_down.shape) == (E, d, I), f"w_down must be [E={E}, d={d}, I={I}], got {tuple(w_down.shape)}")
+    _require(tuple(w_down.shape) == (E, d, I // per),
+             f"w_down must be [E={E}, d={d}, I={I}], got {tuple(w_down.shape)}" + " of two codes a byte" * (per - 1))
     _require(tuple(logits.shape) == (T, E) and logits.dtype in _FLOATS,
              f"logits must be [T={T}, E={E}] of one of {_FLOATS}, got {tuple(logits.shape)} {logits.dtype}")
     _require(1 <= k <= E, f"k={k} outside [1, E={E}]")
@@ -325,7 +328,7 @@ def _check_decode_args(x, logits, w_gate_up, w_down, k, s_gate_up, s_down) -> st
     if s_gate_up is None:
         fmt, dt = "native", x.dtype
     else:
-        fmt, dt = ("fp8_block" if s_gate_up.dtype == torch.float32 else "mxfp8"), torch.uint8
+        fmt, dt = ("mxfp4" if per == 2 else "fp8_block" if s_gate_up.dtype == torch.float32 else "mxfp8"), torch.uint8
         _require(d % 128 == 0 and I % 128 == 0, f"coded weights need d and I multiples of 128, got {d} and {I}")
         shapes = (((E, two_i // 128, d // 128), (E, d // 128, I // 128)) if fmt == "fp8_block"
                   else ((E, two_i, d // 32), (E, d, I // 32)))
@@ -346,15 +349,16 @@ def moe_decode(x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: Tensor, k: 
     """The layer for at most 256 tokens (binding.MoeDecoder as one operator that
     allocates its output and workspace): out [T,d].  With s_gate_up and s_down
     the weights are e4m3 codes, their scales float32 per 128x128 block or E8M0
-    bytes per 32 columns.  No gradient."""
+    bytes per 32 columns, or pairs of e2m1 codes ([E, 2I, d/2] and [E, d, I/2])
+    with E8M0 bytes.  No gradient."""
     fmt = _check_decode_args(x, logits, w_gate_up, w_down, k, s_gate_up, s_down)
     tensors = dict(x=x, logits=logits, w_gate_up=w_gate_up, w_down=w_down)
     if fmt != "native":
         tensors.update(s_gate_up=s_gate_up, s_down=s_down)
     _check_devices(**tensors)
-    E, two_i, d = w_gate_up.shape
+    E, two_i, _ = w_gate_up.shape
     with B._on(x.device):
-        dec = B.MoeDecoder(x.shape[0], d, E, k, two_i // 2, x.dtype, logits.dtype, fmt, x.device, swiglu_limit)
+        dec = B.MoeDecoder(x.shape[0], x.shape[1], E, k, two_i // 2, x.dtype, logits.dtype, fmt, x.device, swiglu_limit)
         pair = (lambda w, s: w) if fmt == "native" else (lambda w, s: (w, s))
         return dec.forward(x, pair(w_gate_up, s_gate_up), pair(w_down, s_down), logits=logits)
 

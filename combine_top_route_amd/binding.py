@@ -27,7 +27,7 @@ GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2
 
 _DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _TORCH = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
-_WEIGHTS = {"native": 0, "fp8_block": 1, "mxfp8": 2}
+_WEIGHTS = {"native": 0, "fp8_block": 1, "mxfp8": 2, "mxfp4": 3}
 _PREC = {"native": PREC_NATIVE, "fp8_block": PREC_FP8_BLOCK, "mxfp8": PREC_MXFP8, "fp8_bwd": PREC_FP8_BWD}
 
 
@@ -95,6 +95,7 @@ _SIGS = [
                                                ctypes.POINTER(MoeRouting), _P, _P, _P, ctypes.c_size_t, _P]),
     ("moe_quantize_mxfp8", ctypes.c_int, [ctypes.c_int, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P,
                                           _P, _P]),
+    ("moe_quantize_mxfp4", ctypes.c_int, [_P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P, _P]),
     ("moe_quantize_tokens_mxfp8", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.c_int64, ctypes.c_int,
                                                  ctypes.POINTER(MoeRouting), _P, _P, _P, ctypes.c_size_t, _P]),
     ("moe_status_string", ctypes.c_char_p, [ctypes.c_int]),
@@ -184,6 +185,23 @@ def _on(device):
     if device.type != "cuda":
         raise ValueError(f"tensors are on {device}; the kernels need a GPU's memory")
     return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+class _Entry:
+    """An entry point that enqueues work, called with its tensors' device current
+    and, as its last argument, torch's stream there.  Refuses host memory and
+    raises on a status."""
+
+    def __init__(self, name):
+        self.name = name
+
+    def __call__(self, device, *args):
+        with _on(device):
+            _check(self.name, getattr(lib(), self.name)(*args, _stream(device)))
+
+
+_norm_forward, _norm_backward = _Entry("moe_norm_forward"), _Entry("moe_norm_backward")
+_quantize_mxfp4 = _Entry("moe_quantize_mxfp4")
 
 
 def _need(t, name, shape, dtype, device):
@@ -499,12 +517,9 @@ def norm_residual(x, y=None, w_post=None, gate=None, res_scale=1.0, w_next=None,
     dev = x.device
     if y is not None:
         _need(y, "y", x.shape, x.dtype, dev)
-    with _on(dev):
-        z = None if y is None else torch.empty_like(x)
-        h = None if w_next is None else torch.empty_like(x)
-        _check("moe_norm_forward", lib().moe_norm_forward(
-            ctypes.byref(shape), _ptr(x), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_next), _ptr(z), _ptr(h),
-            _stream(dev)))
+    z = None if y is None else torch.empty_like(x)
+    h = None if w_next is None else torch.empty_like(x)
+    _norm_forward(dev, ctypes.byref(shape), _ptr(x), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_next), _ptr(z), _ptr(h))
     return x if y is None else z, h
 
 
@@ -521,15 +536,13 @@ def norm_residual_backward(dz, dh, z, y=None, w_post=None, gate=None, res_scale=
         if t is not None:
             _need(t, name, z.shape, z.dtype, dev)
     n = _norm_workspace(z.shape[0], z.shape[1], z.dtype)
-    with _on(dev):
-        out = {"dx": torch.empty_like(z)}
-        for name, t in (("dy", y), ("dw_post", w_post), ("dgate", gate), ("dw_next", w_next)):
-            out[name] = None if t is None else torch.empty_like(t)
-        ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        _check("moe_norm_backward", lib().moe_norm_backward(
-            ctypes.byref(shape), _ptr(dz), _ptr(dh), _ptr(z), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_next),
-            _ptr(out["dx"]), _ptr(out["dy"]), _ptr(out["dw_post"]), _ptr(out["dgate"]), _ptr(out["dw_next"]),
-            _ptr(ws), n, _stream(dev)))
+    out = {"dx": torch.empty_like(z)}
+    for name, t in (("dy", y), ("dw_post", w_post), ("dgate", gate), ("dw_next", w_next)):
+        out[name] = None if t is None else torch.empty_like(t)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _norm_backward(dev, ctypes.byref(shape), _ptr(dz), _ptr(dh), _ptr(z), _ptr(y), _ptr(w_post), _ptr(gate),
+                   _ptr(w_next), _ptr(out["dx"]), _ptr(out["dy"]), _ptr(out["dw_post"]), _ptr(out["dgate"]),
+                   _ptr(out["dw_next"]), _ptr(ws), n)
     return out
 
 
@@ -542,14 +555,14 @@ def decode_workspace_size(shape: MoeShape) -> int:
 def _weight_args(name, w, shape, dtype, weights, device):
     """Pointers of an expert weight [E, N, K] and of its scales: a tensor, or
     (coded formats) the (codes, scales) pair of quantize_fp8 / quantize_mxfp8
-    with QUANT_WEIGHT."""
+    with QUANT_WEIGHT, or of quantize_mxfp4."""
     if weights == "native":
         _need(w, name, shape, dtype, device)
         return _ptr(w), None
     if not isinstance(w, (tuple, list)) or len(w) != 2:
         raise ValueError(f"{name} must be a (codes, scales) pair for weights={weights!r}")
     E, N, K = shape
-    _need(w[0], f"{name} codes", shape, torch.uint8, device)
+    _need(w[0], f"{name} codes", (E, N, K // 2) if weights == "mxfp4" else shape, torch.uint8, device)
     if weights == "fp8_block":
         _need(w[1], f"{name} scales", (E, N // 128, K // 128), torch.float32, device)
     else:
@@ -567,7 +580,8 @@ class MoeDecoder:
     decoder each.
 
     weights: "native" (tensors in dtype), or "fp8_block" / "mxfp8": (codes,
-    scales) pairs from quantize_fp8 / quantize_mxfp8 with QUANT_WEIGHT.
+    scales) pairs from quantize_fp8 / quantize_mxfp8 with QUANT_WEIGHT, or
+    "mxfp4": those of quantize_mxfp4.
     Routing by logits [T, E], or by topk_ids and topk_w [T, k]; an id outside
     [0, E) or a logit of -inf is an empty slot.  No gradient."""
 
@@ -770,6 +784,20 @@ def quantize_mxfp8(src, kind=QUANT_ROWS):
     with _on(dev):
         _check("moe_quantize_mxfp8", lib().moe_quantize_mxfp8(kind, _ptr(src), n0, n1, n2, _ptr(q), _ptr(s),
                                                               _stream(dev)))
+    return q, s
+
+
+def quantize_mxfp4(src):
+    """MXFP4 codes [n0, n1, n2/2] (uint8, two e2m1 codes a byte, the even column
+    low) and E8M0 scale bytes [n0, n1, n2/32] of bf16 weights [n0, n1, n2], for
+    MoeDecoder(weights="mxfp4") and grouped_product (moe_quantize_mxfp4)."""
+    dev = src.device
+    if src.dtype != torch.bfloat16 or src.dim() != 3 or not src.is_contiguous():
+        raise ValueError("src must be a contiguous bf16 tensor [n0, n1, n2]")
+    n0, n1, n2 = src.shape
+    q = torch.empty((n0, n1, n2 // 2), dtype=torch.uint8, device=dev)
+    s = torch.empty((n0, n1, n2 // 32), dtype=torch.uint8, device=dev)
+    _quantize_mxfp4(dev, _ptr(src), n0, n1, n2, _ptr(q), _ptr(s))
     return q, s
 
 

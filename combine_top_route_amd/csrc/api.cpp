@@ -937,7 +937,7 @@ moe_status moe_decode(const moe_shape* shape, int weights, const void* x, moe_ro
                       const void* w_gate_up, const void* s_gate_up, const void* w_down, const void* s_down,
                       void* out, void* workspace, size_t workspace_bytes, void* stream) {
   TRY(check_decode(shape));
-  if (weights < MOE_WEIGHTS_NATIVE || weights > MOE_WEIGHTS_MXFP8)
+  if (weights < MOE_WEIGHTS_NATIVE || weights > MOE_WEIGHTS_MXFP4)
     return fail(MOE_ERR_INVALID_ARGUMENT, "weights=%d unknown", weights);
   CHECK_PTR(x);
   CHECK_PTR(routing);
@@ -1210,6 +1210,24 @@ moe_status moe_quantize_fp8(int kind, const void* src, int64_t n0, int64_t n1, i
 moe_status moe_quantize_mxfp8(int kind, const void* src, int64_t n0, int64_t n1, int64_t n2,
                               uint8_t* q, uint8_t* s, void* stream) {
   return quantize_common(true, kind, src, n0, n1, n2, q, s, stream);
+}
+
+moe_status moe_quantize_mxfp4(const void* src, int64_t n0, int64_t n1, int64_t n2, uint8_t* q, uint8_t* s,
+                              void* stream) {
+  CHECK_PTR(src);
+  CHECK_PTR(q);
+  CHECK_PTR(s);
+  if (n0 < 1 || n1 < 1 || n2 < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "extents must be positive");
+  if (n2 % 128) return fail(MOE_ERR_INVALID_ARGUMENT, "n2=%lld must be a multiple of 128", (long long)n2);
+  if (n0 > 65535 || n1 > 65535 * 128 || n2 > 65535 * 128 || n0 * n1 > (int64_t(1) << 41) / n2)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "weight extents too large");
+  TRY(check_aligned16(src, "src"));
+  TRY(check_aligned16(q, "q"));
+  if (((uintptr_t)s) & 3) return fail(MOE_ERR_INVALID_ARGUMENT, "s must be 4-byte aligned");
+  const LaunchCtx c = make_ctx(stream);
+  (void)hipGetLastError();
+  HIP_TRY(launch_quant_mxfp4(c, src, n0 * n1 * n2, q, s), "quant_mxfp4");
+  return MOE_OK;
 }
 
 moe_status moe_quantize_tokens_fp8(const moe_shape* shape, const void* src, int64_t C, int gather,

@@ -290,7 +290,7 @@ struct DecodeArgs {
   int dtype;              // of x, out and aw (and of uncoded weights)
   float lim;              // SwiGLU clamp limit, +inf for the plain SwiGLU
   const void* x;          // [T, d]
-  const void* w_gate_up;  // [E, 2I, d] in dtype, or e4m3 codes
+  const void* w_gate_up;  // [E, 2I, d] in dtype, or e4m3 codes, or e2m1 codes [E, 2I, d/2]
   const void* s_gate_up;  // coded: fp32 [E, 2I/128, d/128] or E8M0 [E, 2I, d/32]
   const void* w_down;     // [E, d, I]
   const void* s_down;     // fp32 [E, d/128, I/128] or E8M0 [E, d, I/32]
@@ -338,6 +338,10 @@ hipError_t launch_quant_tok(const LaunchCtx& c, const char* name, const void* sr
                             const int32_t* src_of, int kdiv, int C, const int32_t* offsets,
                             const int32_t* blk_off, int E, int nblk_max, uint8_t* q, void* s,
                             bool mx, bool run_major);
+
+// MXFP4 (quant_mxfp4.hip): src bf16, a multiple of 32 values -> e2m1 codes, two a
+// byte, and an E8M0 byte per 32.
+hipError_t launch_quant_mxfp4(const LaunchCtx& c, const void* src, int64_t values, uint8_t* q, uint8_t* s);
 
 // fp8 path's SwiGLU backward: from an fp32 G [R,I] and H, dH (bf16-rounded,
 // never stored) in two e4m3 encodings: row codes dhq [R,2I] with scale words

@@ -1,8 +1,9 @@
 // The whole layer for a few tokens (T <= kDecodeMaxT), as serving calls it:
 //   h = W_gate_up[e] x_t,  a = silu(min(g, L)) clamp(u, -L, L),
 //   out_t = sum_j w_tj W_down[e_tj] a,
-// with the expert weights in float32, bfloat16, or e4m3 codes with scales
-// (128 x 128 float32, or E8M0 per 32 columns) that were laid out once.
+// with the expert weights in float32, bfloat16, e4m3 codes with scales (128 x
+// 128 float32, or E8M0 per 32 columns) or pairs of e2m1 codes with E8M0 scales
+// per 32 columns, that were laid out once.
 //
 // What bounds it: every expert that some token selected is read once, 3 I d
 // values, and each value meets only that expert's few tokens, so the time is
@@ -180,9 +181,12 @@ __global__ __launch_bounds__(64) void decode_ids_kernel(const int32_t* __restric
 }
 
 // ------------------------------------------------------------ weight formats
-// A unit is 128 bytes of each of 16 weight rows.  UK: values of K per unit; BV:
-// 16-byte operands of a token's matching activations per lane; NF: MFMAs.
-enum WFormat { WF_F32 = 0, WF_BF16 = 1, WF_FP8 = 2, WF_MX = 3 };
+// A unit is 128 bytes of each of 16 weight rows, or 64 bytes of e2m1 codes, which
+// meet as many activations as 128 of e4m3.  UK: values of K per unit; BV: 16-byte
+// operands of a token's matching activations per lane; NF: MFMAs.
+enum WFormat { WF_F32 = 0, WF_BF16 = 1, WF_FP8 = 2, WF_MX = 3, WF_MX4 = 4 };
+template <int F> constexpr int kUnitLoads = F == WF_MX4 ? 1 : 2;
+template <int F> constexpr int kUnitBytes = 64 * kUnitLoads<F>;
 template <int F> struct Fmt {  // coded: 128 codes, 4 MFMAs of 32
   typedef bf16_t act;
   typedef bf16x8_t frag;
@@ -199,20 +203,58 @@ template <> struct Fmt<WF_BF16> {
   static constexpr int UK = 64, BV = 2, NF = 2;
 };
 
+// Bytes of a row of K weights.
+template <int F>
+__device__ __forceinline__ int row_bytes(int K) {
+  return F == WF_MX4 ? K >> 1 : F >= WF_FP8 ? K : K * (int)sizeof(typename Fmt<F>::act);
+}
+
+// The row of a 16-row group that this lane loads for its h-th load of a unit,
+// and one unit of the rows at offsets `row`, of which `bytes` exist.
+template <int F>
+__device__ __forceinline__ int unit_row(int h) {
+  return F == WF_MX4 ? (int)((threadIdx.x & 63) >> 2) : load_row(h);
+}
+template <int F, bool NT>
+__device__ __forceinline__ void load_unit(u32x4_t (&v)[kUnitLoads<F>], rsrc_t r, const uint32_t (&row)[kUnitLoads<F>],
+                                          int unit, int bytes) {
+  if constexpr (F == WF_MX4) {
+    const int off = unit * 64 + (int)(threadIdx.x & 3) * 16;
+    v[0] = load16<NT>(r, row[0] + off, off < bytes);
+  } else {
+    load_rows<NT>(v, r, row, unit * 128, bytes);
+  }
+}
+// The same on its way through LDS: [16 rows][128 bytes] as in rowload.h, or
+// [16 rows][64 bytes], whose chunks are swizzled by row / 4, so that the 16 rows
+// read at one chunk meet every bank once.
+template <int F>
+__device__ __forceinline__ void put_unit(lds_t* p, const u32x4_t (&v)[kUnitLoads<F>]) {
+  if constexpr (F == WF_MX4) {
+    const int row = unit_row<F>(0);
+    turn_fence();
+    *(__attribute__((address_space(3))) u32x4_t*)(p + row * 64 + (((threadIdx.x ^ (row >> 2)) & 3) << 4)) = v[0];
+    turn_fence();
+  } else {
+    put_rows(p, v);
+  }
+}
+
 // A unit's weights in flight, and its scale bytes: `mx` holds, in lane 4 r + i,
 // row r's four scale bytes of unit i of a batch of up to four units.
+template <int F> constexpr bool kMx = F == WF_MX || F == WF_MX4;
 template <int F>
 __device__ __forceinline__ uint32_t mx_words(const void* s, int row4, int K, int unit) {
-  if constexpr (F == WF_MX) return ((const uint32_t*)s)[(int64_t)row4 * (K >> 7) + min(unit, (K >> 7) - 1)];
+  if constexpr (kMx<F>) return ((const uint32_t*)s)[(int64_t)row4 * (K >> 7) + min(unit, (K >> 7) - 1)];
   return 0;
 }
 
-// The NF / 2 MFMA operands of 16 bytes of a weight row, chunk 4 c + q of its
-// unit.  Codes become bfloat16 exactly (e4m3 has four significant bits); an
-// E8M0 scale is a power of two and rides on the conversion, which takes it from
+// The MFMA operands of 16 bytes of a weight row (half of a unit's, chunk 4 c + q
+// of it, or of e2m1 codes all, chunk q).  Codes become bfloat16 exactly (e4m3 has
+// four significant bits, e2m1 two); an E8M0 scale is a power of two and rides on the conversion, which takes it from
 // the exponent field alone: byte 0 arrives as the bits of +0 and stands for 2^-127.
-// Exact down to bfloat16's smallest numbers (2^-133).  mx: the row's four scale
-// bytes of this unit.
+// Exact down to bfloat16's smallest numbers (2^-133).  For e2m1 codes it takes
+// byte 255 as E8M0's NaN.  mx: the row's four scale bytes of this unit.
 template <int F>
 __device__ __forceinline__ void chunk_frags(typename Fmt<F>::frag* fr, u32x4_t a, uint32_t mx, int c, int q) {
   if constexpr (F == WF_F32) {
@@ -220,6 +262,17 @@ __device__ __forceinline__ void chunk_frags(typename Fmt<F>::frag* fr, u32x4_t a
     for (int i = 0; i < 4; ++i) fr[i] = __uint_as_float(a[i]);
   } else if constexpr (F == WF_BF16) {
     fr[0] = __builtin_bit_cast(bf16x8_t, a);
+  } else if constexpr (F == WF_MX4) {  // its 32 codes are block q
+    const float s = __uint_as_float(((mx >> (8 * q)) & 0xffu) << 23);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      u32x4_t o;
+      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a[h], s, 0));
+      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a[h], s, 1));
+      o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a[h], s, 2));
+      o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a[h], s, 3));
+      fr[h] = __builtin_bit_cast(bf16x8_t, o);
+    }
   } else {
     // its 16 codes lie in block 2 c + q / 2
     const float s = F == WF_MX ? __uint_as_float(((mx >> (16 * c + 8 * (q >> 1))) & 0xffu) << 23) : 1.0f;
@@ -240,8 +293,14 @@ __device__ __forceinline__ void chunk_frags(typename Fmt<F>::frag* fr, u32x4_t a
 template <int F>
 __device__ __forceinline__ void to_frags(typename Fmt<F>::frag (&fr)[Fmt<F>::NF], const lds_t* p, uint32_t mx, int q,
                                          int col) {
+  if constexpr (F == WF_MX4) {
+    const u32x4_t a =
+        *(const __attribute__((address_space(3))) u32x4_t*)(p + col * 64 + (((q ^ (col >> 2)) & 3) << 4));
+    chunk_frags<F>(fr, a, mx, 0, q);
+  } else {
 #pragma unroll
-  for (int c = 0; c < 2; ++c) chunk_frags<F>(fr + c * (Fmt<F>::NF / 2), get_chunk(p, col, c * 4 + q), mx, c, q);
+    for (int c = 0; c < 2; ++c) chunk_frags<F>(fr + c * (Fmt<F>::NF / 2), get_chunk(p, col, c * 4 + q), mx, c, q);
+  }
 }
 
 // The activations of 16 tokens that meet a unit's weights: the same values of
@@ -271,20 +330,28 @@ __device__ __forceinline__ void put_acts(lds_t* p, const u32x4_t (&v)[kActHalves
   }
   turn_fence();
 }
-// The BV / 2 operands that meet weight chunk 4 c + q, and all of a unit's.
-template <int F>
+// The operands that meet weight chunk 4 c + q (of e2m1 codes: chunk q of 64
+// bytes, four), and all of a unit's.
+template <int F, int PIECE = 2048>
 __device__ __forceinline__ void chunk_acts(u32x4_t* b, const lds_t* p, int c, int q, int col) {
-  if constexpr (F >= WF_FP8) {
+  if constexpr (F == WF_MX4) {
 #pragma unroll
-    for (int v = 0; v < 2; ++v) b[v] = get_chunk(p + c * 2048, col, 2 * q + v);
+    for (int v = 0; v < 4; ++v) b[v] = get_chunk(p + (q >> 1) * PIECE, col, 4 * (q & 1) + v);
+  } else if constexpr (F >= WF_FP8) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) b[v] = get_chunk(p + c * PIECE, col, 2 * q + v);
   } else {
     b[0] = get_chunk(p, col, 4 * c + q);
   }
 }
 template <int F>
 __device__ __forceinline__ void get_acts(u32x4_t (&b)[Fmt<F>::BV], const lds_t* p, int q, int col) {
+  if constexpr (F == WF_MX4) {
+    chunk_acts<F>(b, p, 0, q, col);
+  } else {
 #pragma unroll
-  for (int c = 0; c < 2; ++c) chunk_acts<F>(b + c * (Fmt<F>::BV / 2), p, c, q, col);
+    for (int c = 0; c < 2; ++c) chunk_acts<F>(b + c * (Fmt<F>::BV / 2), p, c, q, col);
+  }
 }
 
 // s + the products of N operands (a unit's: NF of them), unscaled.
@@ -472,29 +539,29 @@ struct Finder {
 // all of its tokens, NBMAX blocks of 16 a pass; the NW waves take batches of UN units of K in turn.
 template <int F, int TB, int UN>
 struct GuWeights {  // UN units of the tile's gate and up rows, in flight
-  u32x4_t g[TB][UN][2], u[TB][UN][2];
+  u32x4_t g[TB][UN][kUnitLoads<F>], u[TB][UN][kUnitLoads<F>];
   uint32_t mg[TB], mu[TB];
   float sg[UN], su[UN];  // blockwise scales (a tile lies in one block of rows)
 };
 
-template <int TB>
+template <int F, int TB>
 struct GuTile {  // where a lane finds them
   rsrc_t w;
   const void* sc;
-  uint32_t g[TB][2], u[TB][2];  // offsets of this lane's gate and up rows
+  uint32_t g[TB][kUnitLoads<F>], u[TB][kUnitLoads<F>];  // offsets of this lane's gate and up rows
   int row4;                     // row whose scale bytes it loads, and 16 on
   int n0;
 };
 
 template <int F, bool NT, int TB, int UN>
-__device__ __forceinline__ void load_gu(GuWeights<F, TB, UN>& w, const GuTile<TB>& t, int I, int K, int base) {
-  const int bytes = F >= WF_FP8 ? K : K * (int)sizeof(typename Fmt<F>::act);
+__device__ __forceinline__ void load_gu(GuWeights<F, TB, UN>& w, const GuTile<F, TB>& t, int I, int K, int base) {
+  const int bytes = row_bytes<F>(K);
 #pragma unroll
   for (int i = 0; i < UN; ++i) {
 #pragma unroll
     for (int b = 0; b < TB; ++b) {
-      load_rows<NT>(w.g[b][i], t.w, t.g[b], (base + i) * 128, bytes);
-      load_rows<NT>(w.u[b][i], t.w, t.u[b], (base + i) * 128, bytes);
+      load_unit<F, NT>(w.g[b][i], t.w, t.g[b], base + i, bytes);
+      load_unit<F, NT>(w.u[b][i], t.w, t.u[b], base + i, bytes);
     }
     w.sg[i] = block_scale_of<F>(t.sc, t.n0, K, base + i);
     w.su[i] = block_scale_of<F>(t.sc, I + t.n0, K, base + i);
@@ -515,7 +582,7 @@ constexpr size_t gu_smem() {  // per wave: gate, up, activations; then the waves
 // The tokens r0 .. r0 + 16 NB of the expert.  w holds the first units.
 template <int F, bool NT, int NW, int TB, int UN, int NB>
 __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, bool again,
-                                            GuWeights<F, TB, UN>& w, const GuTile<TB>& t, char* smem) {
+                                            GuWeights<F, TB, UN>& w, const GuTile<F, TB>& t, char* smem) {
   typedef typename Fmt<F>::act AT;
   const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
   const int K = a.d;
@@ -555,10 +622,10 @@ __device__ __forceinline__ void gateup_rows(const DecodeArgs& a, const Rows& row
         u32x4_t xf[NB][Fmt<F>::BV];
 #pragma unroll
         for (int m = 0; m < TB; ++m) {
-          put_rows(lw, w.g[m][i0 + i]);
-          put_rows(lw + 2048, w.u[m][i0 + i]);
+          put_unit<F>(lw, w.g[m][i0 + i]);
+          put_unit<F>(lw + 2048, w.u[m][i0 + i]);
           uint32_t mg = 0, mu = 0;
-          if constexpr (F == WF_MX) {
+          if constexpr (kMx<F>) {
             mg = (uint32_t)__shfl((int)w.mg[m], col * 4 + i0 + i, kWave);
             mu = (uint32_t)__shfl((int)w.mu[m], col * 4 + i0 + i, kWave);
           }
@@ -635,23 +702,23 @@ __global__ __launch_bounds__(NW * 64) void decode_gateup_kernel(DecodeArgs a) {
   Finder find;
   const int n = find.count(rows, mid, mw, e, a.T, a.k);
   if (n == 0) return;
-  GuTile<TB> t;
+  GuTile<F, TB> t;
   t.n0 = blockIdx.x * 16 * TB;
-  const int rowb = a.d * (F >= WF_FP8 ? 1 : (int)sizeof(typename Fmt<F>::act));
+  const int rowb = row_bytes<F>(a.d);
   const uint64_t wbytes = (uint64_t)2 * a.I * rowb;
   t.w = buffer_of((const char*)a.w_gate_up + e * wbytes, wbytes);
 #pragma unroll
   for (int b = 0; b < TB; ++b)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = min(t.n0 + b * 16 + load_row(h), a.I - 1);  // rows past I repeat the last and are dropped
+    for (int h = 0; h < kUnitLoads<F>; ++h) {
+      const int row = min(t.n0 + b * 16 + unit_row<F>(h), a.I - 1);  // rows past I repeat the last and are dropped
       t.g[b][h] = (uint32_t)row * rowb;
       t.u[b][h] = (uint32_t)(a.I + row) * rowb;
     }
-  t.row4 = t.n0 + (lane >> 2);  // read for WF_MX, where I is a multiple of 128
+  t.row4 = t.n0 + (lane >> 2);  // read for the MX formats, where I is a multiple of 128
   const char* sc = (const char*)a.s_gate_up;
   if (F == WF_FP8) sc += (int64_t)e * (2 * a.I / 128) * (a.d / 128) * 4;
-  if (F == WF_MX) sc += (int64_t)e * 2 * a.I * (a.d / 32);
+  if (kMx<F>) sc += (int64_t)e * 2 * a.I * (a.d / 32);
   t.sc = sc;
   GuWeights<F, TB, UN> w;
   load_gu<F, NT>(w, t, a.I, a.d, tile::wave_id() * UN);
@@ -683,7 +750,10 @@ constexpr int kDownWaves = 16;
 template <int F>
 __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(DecodeArgs a) {
   typedef typename Fmt<F>::act AT;
-  constexpr int WORK = 2048 + 2048 * kActHalves<F>, UN = F >= WF_FP8 ? 4 : 6;
+  // of e2m1 codes 8 rows by 128 bytes are two units: a unit here is both
+  constexpr int SK = F == WF_MX4 ? 256 : Fmt<F>::UK, AH = F == WF_MX4 ? 4 : kActHalves<F>;
+  constexpr int PIECE = F == WF_MX4 ? 1024 : 2048;  // 128 bytes of 8 tokens
+  constexpr int WORK = 2048 + PIECE * AH, UN = F == WF_MX4 ? 2 : F == WF_FP8 || F == WF_MX ? 4 : 6;
   __shared__ __align__(16) char work[kDownWaves * WORK];  // then the parts [2 waves][8 tokens][8 rows]
   const int lane = threadIdx.x & 63, wave = tile::wave_id(), q = lane >> 4, col = lane & 15;
   const int r8 = col & 7, half = col >> 3;
@@ -694,8 +764,8 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(Deco
   const uint64_t firsts = __ballot(first);
   const int nact = __popcll(firsts);
   const int K = a.I, n0 = blockIdx.x * 8;
-  const int units = (K + Fmt<F>::UK - 1) / Fmt<F>::UK;
-  const int abytes = F >= WF_FP8 ? K : K * (int)sizeof(AT), bbytes = K * (int)sizeof(AT);
+  const int units = (K + SK - 1) / SK;
+  const int abytes = row_bytes<F>(K), bbytes = K * (int)sizeof(AT);
   const uint64_t wbytes = (uint64_t)a.d * abytes;
   const uint32_t wrow = (uint32_t)min(n0 + load_row(0), a.d - 1) * abytes;
   constexpr int P = F == WF_F32 ? 1 : 2;  // planes of aw
@@ -709,7 +779,7 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(Deco
 #pragma unroll
   for (int p = 0; p < P; ++p) acc[p] = f32x4_t{0, 0, 0, 0};
   for (int base = wave * UN; base < total; base += kDownWaves * UN) {
-    u32x4_t wv[UN], xv[UN][P][kActHalves<F>];
+    u32x4_t wv[UN], xv[UN][P][AH];
     uint32_t mx[UN];
     float sb[UN];
     bool on_expert[UN];
@@ -727,16 +797,20 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(Deco
       const uint64_t ts = t < a.T ? (has >> (t * a.k)) & slots : 0;
       const uint32_t xrow = (uint32_t)(t * a.k + (ts ? __builtin_ctzll(ts) : 0)) * bbytes;
 #pragma unroll
-      for (int h = 0; h < kActHalves<F>; ++h) {
-        const int o = (unit * kActHalves<F> + h) * 128 + (lane & 7) * 16;
+      for (int h = 0; h < AH; ++h) {
+        const int o = (unit * AH + h) * 128 + (lane & 7) * 16;
 #pragma unroll
         for (int p = 0; p < P; ++p) xv[i][p][h] = load16(xb[p], xrow + o, on && ts && o < bbytes);
       }
       on_expert[i] = on && r8 < a.T && ((has >> (r8 * a.k)) & slots);
       const char* sc = (const char*)a.s_down;
       if (F == WF_FP8) sc += (int64_t)e * (a.d / 128) * (K / 128) * 4;
-      if (F == WF_MX) sc += (int64_t)e * a.d * (K / 32);
-      mx[i] = F == WF_MX ? ((const uint32_t*)sc)[(int64_t)(n0 + r8) * (K >> 7) + unit] : 0;
+      if (kMx<F>) sc += (int64_t)e * a.d * (K / 32);
+      mx[i] = 0;
+      if constexpr (kMx<F>) {  // the word of 128 columns that holds this lane's scale
+        const int word = F == WF_MX4 ? min(2 * unit + half, (K >> 7) - 1) : unit;
+        mx[i] = ((const uint32_t*)sc)[(int64_t)(n0 + r8) * (K >> 7) + word];
+      }
       sb[i] = block_scale_of<F>(sc, n0, K, unit);
       if (on && ++unit == units) {
         unit = 0;
@@ -750,19 +824,20 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(Deco
       turn_fence();
       *(__attribute__((address_space(3))) u32x4_t*)(lw + row_chunk(load_row(0), chunk)) = wv[i];
       turn_fence();
-      typename Fmt<F>::frag fr[Fmt<F>::NF / 2];
+      constexpr int NO = F == WF_MX4 ? 4 : Fmt<F>::NF / 2;  // operands of a chunk
+      typename Fmt<F>::frag fr[NO];
       chunk_frags<F>(fr, get_chunk(lw, r8, 4 * half + q), mx[i], half, q);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         turn_fence();
 #pragma unroll
-        for (int h = 0; h < kActHalves<F>; ++h)
-          *(__attribute__((address_space(3))) u32x4_t*)(lw + 2048 + h * 2048 + row_chunk(load_row(0), chunk)) =
+        for (int h = 0; h < AH; ++h)
+          *(__attribute__((address_space(3))) u32x4_t*)(lw + 2048 + h * PIECE + row_chunk(load_row(0), chunk)) =
               xv[i][p][h];
         turn_fence();
-        u32x4_t xf[Fmt<F>::BV / 2];
-        chunk_acts<F>(xf, lw + 2048, half, q, r8);
-        const f32x4_t s = unit_dot<F, Fmt<F>::NF / 2>(f32x4_t{0, 0, 0, 0}, fr, xf);
+        u32x4_t xf[F == WF_MX4 ? 4 : Fmt<F>::BV / 2];
+        chunk_acts<F, PIECE>(xf, lw + 2048 + (F == WF_MX4 ? 2 * half * PIECE : 0), half, q, r8);
+        const f32x4_t s = unit_dot<F, NO>(f32x4_t{0, 0, 0, 0}, fr, xf);
 #pragma unroll
         for (int m = 0; m < 4; ++m) acc[p][m] = on_expert[i] ? fmaf(sb[i], s[m], acc[p][m]) : acc[p][m];
       }
@@ -793,22 +868,22 @@ __global__ __launch_bounds__(kDownWaves * 64) void decode_down_small_kernel(Deco
 // which decode_combine_kernel sums in slot order.
 constexpr int kDownRowWaves = 4;
 
-template <int TB>
+template <int F, int TB>
 struct DownTile {
   rsrc_t w;
   const void* sc;
-  uint32_t row[TB][2];  // offsets of this lane's rows
+  uint32_t row[TB][kUnitLoads<F>];  // offsets of this lane's rows
   int row4, n0;
 };
 
 template <int F, bool NT, int TB, int UN, bool KS, int NB, bool EIGHT = false>
-__device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, const DownTile<TB>& t,
+__device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows, int r0, int n, const DownTile<F, TB>& t,
                                           lds_t* lw, float* red) {
   typedef typename Fmt<F>::act AT;
   const int lane = threadIdx.x & 63, q = lane >> 4, col = lane & 15;
   const int K = a.I;
   const int units = (K + Fmt<F>::UK - 1) / Fmt<F>::UK;
-  const int abytes = F >= WF_FP8 ? K : K * (int)sizeof(AT), bbytes = K * (int)sizeof(AT);
+  const int abytes = row_bytes<F>(K), bbytes = K * (int)sizeof(AT);
   const rsrc_t xb = buffer_of(a.aw, (uint64_t)a.T * a.k * bbytes);
   const rsrc_t xl = F == WF_F32 ? xb : buffer_of((const AT*)a.aw + aw_plane(a), (uint64_t)a.T * a.k * bbytes);
   // P passes over a unit's weights, one for each plane of aw; with EIGHT (at most
@@ -835,12 +910,12 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
   constexpr int UB = NB == 1 ? UN : 1;
   const int wave = tile::wave_id();
   for (int base = KS ? wave * UN : 0; base < units; base += (KS ? kDownRowWaves : 1) * UN) {
-    u32x4_t wv[TB][UN][2];
+    u32x4_t wv[TB][UN][kUnitLoads<F>];
     float sb[UN];
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
 #pragma unroll
-      for (int m = 0; m < TB; ++m) load_rows<NT>(wv[m][i], t.w, t.row[m], (base + i) * 128, abytes);
+      for (int m = 0; m < TB; ++m) load_unit<F, NT>(wv[m][i], t.w, t.row[m], base + i, abytes);
       sb[i] = block_scale_of<F>(t.sc, t.n0, K, base + i);
     }
     uint32_t mx[TB];
@@ -863,9 +938,9 @@ __device__ __forceinline__ void down_rows(const DecodeArgs& a, const Rows& rows,
 #pragma unroll
         for (int m = 0; m < TB; ++m) {
           typename Fmt<F>::frag fr[Fmt<F>::NF];
-          put_rows(lw, wv[m][i0 + i]);
+          put_unit<F>(lw, wv[m][i0 + i]);
           uint32_t code = 0;
-          if constexpr (F == WF_MX) code = (uint32_t)__shfl((int)mx[m], col * 4 + i0 + i, kWave);
+          if constexpr (kMx<F>) code = (uint32_t)__shfl((int)mx[m], col * 4 + i0 + i, kWave);
           to_frags<F>(fr, lw, code, q, col);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
@@ -941,21 +1016,22 @@ __global__ __launch_bounds__(kDownRowWaves * 64, F == WF_FP8 && TB == 2 ? 3 : 1)
   Finder find;
   const int n = find.count(rows, a.mid, a.mw, e, a.T, a.k);
   find.list(rows);
-  DownTile<TB> t;
+  DownTile<F, TB> t;
   const int lane = threadIdx.x & 63, wave = tile::wave_id();
   t.n0 = (KS ? (int)blockIdx.x : (int)blockIdx.x * kDownRowWaves + wave) * 16 * TB;
   if (n == 0 || t.n0 >= a.d) return;  // the whole work-group with KS; else no barrier follows
-  const int rowb = a.I * (F >= WF_FP8 ? 1 : (int)sizeof(typename Fmt<F>::act));
+  const int rowb = row_bytes<F>(a.I);
   const uint64_t wbytes = (uint64_t)a.d * rowb;
   t.w = buffer_of((const char*)a.w_down + e * wbytes, wbytes);
 #pragma unroll
   for (int m = 0; m < TB; ++m)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) t.row[m][h] = (uint32_t)min(t.n0 + 16 * m + load_row(h), a.d - 1) * rowb;
-  t.row4 = t.n0 + (lane >> 2);  // read for WF_MX, where d is a multiple of 128
+    for (int h = 0; h < kUnitLoads<F>; ++h)
+      t.row[m][h] = (uint32_t)min(t.n0 + 16 * m + unit_row<F>(h), a.d - 1) * rowb;
+  t.row4 = t.n0 + (lane >> 2);  // read for the MX formats, where d is a multiple of 128
   const char* sc = (const char*)a.s_down;
   if (F == WF_FP8) sc += (int64_t)e * (a.d / 128) * (a.I / 128) * 4;
-  if (F == WF_MX) sc += (int64_t)e * a.d * (a.I / 32);
+  if (kMx<F>) sc += (int64_t)e * a.d * (a.I / 32);
   t.sc = sc;
   lds_t* lw = (lds_t*)work + wave * (2048 + 2048 * kActHalves<F>);
   for (int r0 = blockIdx.z * 32; r0 < n; r0 += gridDim.z * 32) {
@@ -1035,8 +1111,8 @@ unsigned token_split(const DecodeArgs& a, int64_t groups) {
 template <int F>
 bool past_cache(const DecodeArgs& a) {
   constexpr int64_t kLastLevelCache = int64_t(256) << 20;
-  const int64_t value = F >= WF_FP8 ? 1 : sizeof(typename Fmt<F>::act);
-  return work_items(a) * int64_t(3) * a.I * a.d * value > kLastLevelCache;
+  constexpr int64_t half_bytes = F == WF_MX4 ? 1 : F >= WF_FP8 ? 2 : 2 * sizeof(typename Fmt<F>::act);  // of a value
+  return work_items(a) * int64_t(3) * a.I * a.d * half_bytes > 2 * kLastLevelCache;
 }
 
 template <int F, bool NT>
@@ -1144,6 +1220,7 @@ hipError_t launch_decode(const LaunchCtx& c, DecodeArgs a, int weights) {
 #undef TOPK
   if (weights == 1) return run<WF_FP8>(c, a);
   if (weights == 2) return run<WF_MX>(c, a);
+  if (weights == 3) return run<WF_MX4>(c, a);
   return a.dtype == F32 ? run<WF_F32>(c, a) : run<WF_BF16>(c, a);
 }
 

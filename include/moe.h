@@ -326,7 +326,12 @@ moe_status moe_swiglu_backward8(const moe_shape* shape, const void* G, const uin
  *   MOE_WEIGHTS_MXFP8:     what moe_quantize_mxfp8 MOE_QUANT_WEIGHT writes:
  *                          codes, and scale bytes [E, 2I, d/32] and
  *                          [E, d, I/32]; byte 255 (E8M0's NaN) is not
- *                          recognised.
+ *                          recognised;
+ *   MOE_WEIGHTS_MXFP4:     what moe_quantize_mxfp4 writes: pairs of codes [E, 2I,
+ *                          d/2] and [E, d, I/2], and scale bytes as for
+ *                          MOE_WEIGHTS_MXFP8; byte 255 makes its block NaN, and a
+ *                          code times scale beyond bfloat16's range is an
+ *                          infinity.
  * Coded weights need dtype MOE_BF16 and d, I multiples of 128, and stand for
  * code * scale; x and the activations are not quantised, unlike in
  * moe_forward's fp8 precisions.  Between the two products a bf16 call keeps the
@@ -345,7 +350,8 @@ moe_status moe_swiglu_backward8(const moe_shape* shape, const void* G, const uin
  * workspace: moe_decode_workspace_size bytes, 256-byte aligned (no initial
  * contents needed); calls that overlap in time, replayed graphs among them,
  * need one each. */
-typedef enum { MOE_WEIGHTS_NATIVE = 0, MOE_WEIGHTS_FP8_BLOCK = 1, MOE_WEIGHTS_MXFP8 = 2 } moe_weight_format;
+typedef enum { MOE_WEIGHTS_NATIVE = 0, MOE_WEIGHTS_FP8_BLOCK = 1, MOE_WEIGHTS_MXFP8 = 2,
+               MOE_WEIGHTS_MXFP4 = 3 } moe_weight_format;
 moe_status moe_decode_workspace_size(const moe_shape* shape, size_t* bytes);
 moe_status moe_decode(const moe_shape* shape, int weights, const void* x, moe_routing* routing,
                       const void* w_gate_up, const void* s_gate_up, const void* w_down,
@@ -467,6 +473,20 @@ moe_status moe_quantize_tokens_fp8(const moe_shape* shape, const void* src, int6
  *                       n1, n2 multiples of 128 for both weight kinds. */
 moe_status moe_quantize_mxfp8(int kind, const void* src, int64_t n0, int64_t n1, int64_t n2,
                               uint8_t* q, uint8_t* s, void* stream);
+
+/* MXFP4 encoding of weights (OCP microscaling: blocks of 32 values, one E8M0
+ * scale byte per block, e2m1 elements) for MOE_WEIGHTS_MXFP4.  For a block with
+ * largest magnitude amax the scale is 2^X with X the smallest integer such that
+ * amax <= 6 * 2^X (so no value saturates), X >= -127, and X = 0 for an all-zero
+ * block; the scale byte is X + 127 and each value x becomes the code of the
+ * e2m1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) nearest to
+ * x / 2^X, ties to even.  A block with an infinity or a NaN gets the scale byte
+ * 255 (NaN).  src bf16 [n0, n1, n2], blocks of 32 along each row -> q [n0, n1,
+ * n2/2] (the even column in the low four bits), s [n0, n1, n2/32]; n2 a multiple
+ * of 128, n0 <= 65535, n1 and n2 <= 65535 * 128, 2^41 values in all; src and q
+ * 16-byte, s 4-byte aligned. */
+moe_status moe_quantize_mxfp4(const void* src, int64_t n0, int64_t n1, int64_t n2, uint8_t* q,
+                              uint8_t* s, void* stream);
 
 /* MXFP8 token-block quantisation of a weight-gradient operand: as
  * moe_quantize_tokens_fp8 (same runs of 128 rows, same q layout), but each
