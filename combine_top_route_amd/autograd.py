@@ -18,7 +18,8 @@ kernel ...").  Here:
 Beside the layer: ``moe_fwd8`` / ``moe_bwd8`` (``save8=True``: the activations
 kept in 8 bits), ``router_fwd`` / ``router_bwd`` (the projection that makes the
 logits; ``router`` and, with the layer, ``moe_block``), and ``moe_decode`` (the
-layer for at most 256 tokens, without a gradient), ``norm_fwd`` / ``norm_bwd``
+layer for at most 256 tokens, without a gradient), ``moe_prompt`` (the layer for
+more, from MXFP4 weights), ``norm_fwd`` / ``norm_bwd``
 (the norms before and after the block with its gate and residual scale;
 ``norm_residual`` and, around the block, ``moe_residual_block``).
 
@@ -365,6 +366,31 @@ def moe_decode(x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: Tensor, k: 
 
 @moe_decode.register_fake
 def _(x, logits, w_gate_up, w_down, k, s_gate_up=None, s_down=None, swiglu_limit=0.0):
+    return torch.empty_like(x)
+
+
+@torch.library.custom_op(f"{_NS}::moe_prompt", mutates_args=())
+def moe_prompt(x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: Tensor, k: int, s_gate_up: Tensor,
+               s_down: Tensor, swiglu_limit: float = 0.0) -> Tensor:
+    """The layer for any number of tokens from the MXFP4 weights that moe_decode
+    takes: routing, the two grouped products and the combine; out [T,d].  bf16
+    x; the activations and each slot's product are rounded to bf16 in between, as
+    in moe_forward.  A masked expert (a logit of -inf) has weight zero, so a token
+    of masked experts alone gets zeros.  No gradient."""
+    fmt = _check_decode_args(x, logits, w_gate_up, w_down, k, s_gate_up, s_down)
+    _require(fmt == "mxfp4" and x.dtype == torch.bfloat16, "moe_prompt takes bf16 x and MXFP4 weights")
+    _check_devices(x=x, logits=logits, w_gate_up=w_gate_up, w_down=w_down, s_gate_up=s_gate_up, s_down=s_down)
+    T = x.shape[0]
+    with B._on(x.device):
+        r = B.route(logits, k)
+        r.topk_w.masked_fill_(logits.gather(1, r.topk_ids.long()) == -float("inf"), 0.0)
+        a = B.grouped_product(x, (w_gate_up, s_gate_up), r, T, k, swiglu=True, swiglu_limit=swiglu_limit)
+        y = B.grouped_product(a, (w_down, s_down), r, T, k, gather=False)
+        return B.combine(y, r, T, k)
+
+
+@moe_prompt.register_fake
+def _(x, logits, w_gate_up, w_down, k, s_gate_up, s_down, swiglu_limit=0.0):
     return torch.empty_like(x)
 
 

@@ -87,6 +87,8 @@ _SIGS = [
     ("moe_norm_forward", ctypes.c_int, [ctypes.POINTER(MoeNormShape)] + [_P] * 8),
     ("moe_norm_workspace_size", ctypes.c_int, [ctypes.POINTER(MoeNormShape), ctypes.POINTER(ctypes.c_size_t)]),
     ("moe_norm_backward", ctypes.c_int, [ctypes.POINTER(MoeNormShape)] + [_P] * 13 + [ctypes.c_size_t, _P]),
+    ("moe_grouped_product", ctypes.c_int, [ctypes.POINTER(MoeShape), ctypes.c_int, _P, ctypes.c_int,
+                                           ctypes.POINTER(MoeRouting), _P, _P, ctypes.c_int64, ctypes.c_int, _P, _P]),
     ("moe_permute", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.POINTER(MoeRouting), _P, _P]),
     ("moe_combine", ctypes.c_int, [ctypes.POINTER(MoeShape), _P, ctypes.POINTER(MoeRouting), _P, _P]),
     ("moe_quantize_fp8", ctypes.c_int, [ctypes.c_int, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P, _P,
@@ -201,7 +203,7 @@ class _Entry:
 
 
 _norm_forward, _norm_backward = _Entry("moe_norm_forward"), _Entry("moe_norm_backward")
-_quantize_mxfp4 = _Entry("moe_quantize_mxfp4")
+_quantize_mxfp4, _grouped_product = _Entry("moe_quantize_mxfp4"), _Entry("moe_grouped_product")
 
 
 def _need(t, name, shape, dtype, device):
@@ -705,6 +707,35 @@ def combine(rows, routing: Routing, T, k):
         _check("moe_combine", lib().moe_combine(ctypes.byref(shape), _ptr(rows), ctypes.byref(cr), _ptr(out),
                                                  _stream(rows.device)))
     return out
+
+
+def grouped_product(x, weight, routing: Routing, T, k, gather=True, swiglu=False, swiglu_limit=0.0, out=None):
+    """y [T*k, N] of expert-sorted rows times their experts' MXFP4 matrices
+    (moe_grouped_product in include/moe.h): weight is the (codes [E, N, K/2],
+    scales [E, N, K/32]) pair of quantize_mxfp4, the rows are x[src_of // k] of x
+    [T, K], or without gather x [T*k, K] itself.  swiglu: weight holds N/2 gate
+    rows, then N/2 up rows, and y is silu(g) u [T*k, N/2].  Rows behind the last
+    expert's are left as they were (in `out` when given).  No gradient."""
+    if not isinstance(weight, (tuple, list)) or len(weight) != 2 or weight[0].dim() != 3:
+        raise ValueError("weight must be the (codes, scales) pair of quantize_mxfp4")
+    if x.dim() != 2:
+        raise ValueError(f"x must be [rows, K], got {tuple(x.shape)}")
+    codes, scales = weight
+    E, N, K = codes.shape[0], codes.shape[1], x.shape[1]
+    dev, bf = x.device, torch.bfloat16
+    _need(x, "x", (T if gather else T * k, K), bf, dev)
+    _need(codes, "codes", (E, N, K // 2), torch.uint8, dev)
+    _need(scales, "scales", (E, N, K // 32), torch.uint8, dev)
+    _need(routing.offsets, "routing.offsets", (E + 1,), torch.int32, dev)
+    if gather:
+        _need(routing.src_of, "routing.src_of", (T * k,), torch.int32, dev)
+    shape = _shape_of(T, K, E, k, 8, bf, bf, float(swiglu_limit))
+    y = torch.empty((T * k, N // 2 if swiglu else N), dtype=bf, device=dev) if out is None else out
+    _need(y, "out", (T * k, N // 2 if swiglu else N), bf, dev)
+    cr = MoeRouting(None, None, None, None, _ptr(routing.offsets), None, _ptr(routing.src_of))
+    _grouped_product(dev, ctypes.byref(shape), _WEIGHTS["mxfp4"], _ptr(x), int(gather), ctypes.byref(cr), _ptr(codes),
+                     _ptr(scales), N, int(swiglu), _ptr(y))
+    return y
 
 
 def profile_begin():

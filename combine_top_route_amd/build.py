@@ -21,7 +21,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_mi355x.so")
 SOURCES = ["api.cpp", "route.hip", "rows.hip", "gemm_bf16.hip", "gemm_f32.hip", "gemm_fp8.hip",
            "quant_fp8.hip", "decode.hip", "save8.hip",
-           "router.hip", "norm.hip", "quant_mxfp4.hip"]
+           "router.hip", "norm.hip", "quant_mxfp4.hip",
+           "grouped.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -1089,6 +1089,60 @@ moe_status moe_norm_backward(const moe_norm_shape* shape, const void* dz, const 
   return MOE_OK;
 }
 
+moe_status moe_grouped_product(const moe_shape* shape, int weights, const void* x, int gather,
+                               const moe_routing* routing, const uint8_t* codes, const uint8_t* scales, int64_t N,
+                               int swiglu, void* y, void* stream) {
+  TRY(check_shape(shape));
+  if (weights < MOE_WEIGHTS_NATIVE || weights > MOE_WEIGHTS_MXFP4)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "weights=%d unknown", weights);
+  if (weights != MOE_WEIGHTS_MXFP4) return fail(MOE_ERR_UNSUPPORTED, "moe_grouped_product takes MOE_WEIGHTS_MXFP4");
+  if (shape->dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "coded weights need dtype bf16");
+  if (shape->d % 128) return fail(MOE_ERR_UNSUPPORTED, "coded weights need d a multiple of 128");
+  const int64_t step = swiglu ? 16 : 8;
+  if (N < step || N > 32768 || N % step)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "N=%lld must be a multiple of %lld in [%lld, 32768]", (long long)N,
+                (long long)step, (long long)step);
+  CHECK_PTR(x);
+  CHECK_PTR(routing);
+  CHECK_PTR(routing->offsets);
+  if (gather) CHECK_PTR(routing->src_of);
+  CHECK_PTR(codes);
+  CHECK_PTR(scales);
+  CHECK_PTR(y);
+  TRY(check_aligned16(x, "x"));
+  TRY(check_aligned16(codes, "codes"));
+  TRY(check_aligned16(y, "y"));
+  if (((uintptr_t)scales) & 3) return fail(MOE_ERR_INVALID_ARGUMENT, "scales must be 4-byte aligned");
+  const int64_t R = shape->T * shape->k, rows = gather ? shape->T : R, width = swiglu ? N / 2 : N;
+  const Span out = {y, (size_t)(2 * R * width)};
+  const Span in[] = {{x, (size_t)(2 * rows * shape->d)},
+                     {codes, (size_t)(shape->E * N * (shape->d / 2))},
+                     {scales, (size_t)(shape->E * N * (shape->d / 32))},
+                     {routing->offsets, sizeof(int32_t) * (shape->E + 1)},
+                     {gather ? routing->src_of : nullptr, sizeof(int32_t) * R}};
+  for (const Span& s : in)
+    if (overlap(out, s)) return fail(MOE_ERR_INVALID_ARGUMENT, "y must not overlap an input");
+  GroupedArgs a;
+  a.R = (int)R;
+  a.k = (int)shape->k;
+  a.E = (int)shape->E;
+  a.N = (int)N;
+  a.K = (int)shape->d;
+  a.swiglu = swiglu != 0;
+  a.lim = swiglu_lim(shape);
+  a.x = x;
+  a.offsets = routing->offsets;
+  a.src_of = gather ? routing->src_of : nullptr;
+  a.codes = codes;
+  a.scales = scales;
+  a.y = y;
+  a.row_major = rows_tile_order(2 * rows * shape->d, shape->E * N * (shape->d / 2));
+  const LaunchCtx c = make_ctx(stream);
+  (void)hipGetLastError();
+  HIP_TRY(launch_grouped(c, a), "grouped_product");
+  return MOE_OK;
+}
+
 moe_status moe_permute(const moe_shape* shape, const void* x, const moe_routing* routing,
                        void* xp, void* stream) {
   TRY(check_shape(shape));

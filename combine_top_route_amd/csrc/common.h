@@ -308,6 +308,22 @@ struct DecodeArgs {
 // weights: moe_weight_format.
 hipError_t launch_decode(const LaunchCtx& c, DecodeArgs a, int weights);
 
+// ------------------------------------------------------- grouped products
+// (grouped.hip) Expert-sorted rows times their experts' MXFP4 matrices.
+struct GroupedArgs {
+  int R, k, E, N, K;       // R: rows there are, at most
+  bool swiglu;             // W = [gate; up]: y [R, N / 2]
+  float lim;               // SwiGLU clamp limit, +inf for the plain SwiGLU
+  const void* x;           // [R / k, K] with src_of, else [R, K]
+  const int32_t* offsets;  // [E + 1]
+  const int32_t* src_of;   // [R] or null
+  const uint8_t* codes;    // [E, N, K / 2]
+  const uint8_t* scales;   // [E, N, K / 32]
+  void* y;                 // [R, N or N / 2]
+  int row_major;           // tile order within an expert (rows_tile_order)
+};
+hipError_t launch_grouped(const LaunchCtx& c, const GroupedArgs& a);
+
 // ---------------------------------------------------------------- fp8 path
 // Block quantisation to e4m3 (quant_fp8.hip).  Two formats: blockwise (fp32
 // scales; rows 1 x 128, weights 128 x 128, tokens 128-row runs) and MX

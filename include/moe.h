@@ -406,6 +406,25 @@ moe_status moe_norm_backward(const moe_norm_shape* shape, const void* dz, const 
 moe_status moe_permute(const moe_shape* shape, const void* x,
                        const moe_routing* routing, void* xp, void* stream);
 
+/* Products of expert-sorted rows with their experts' coded matrices (a prompt
+ * through experts that moe_decode serves, or experts of another form):
+ *   y[r] = W_e a_r,  offsets[e] <= r < offsets[e+1],
+ *   a_r = x[src_of[r] / k] (gather != 0; x [T,d]) or x[r] (x [T*k,d]),
+ * or with swiglu != 0, where W_e holds N/2 gate rows and then N/2 up rows,
+ * y[r] = silu(g) u (clamped with shape->swiglu_limit > 0), not weighted.
+ * weights: MOE_WEIGHTS_MXFP4 (MOE_ERR_UNSUPPORTED otherwise): codes [E,N,d/2],
+ * scales [E,N,d/32] as moe_quantize_mxfp4 writes them; bf16 products, float32
+ * sums, one rounding.  y [T*k, N] or [T*k, N/2]; rows outside every expert's are
+ * left as they were, and so is whatever an offset or entry outside [0, T*k]
+ * would reach.  Of shape T, d, E, k and swiglu_limit are used (dtype MOE_BF16,
+ * d a multiple of 128); N a multiple of 8 (16 with swiglu) up to 32768.  Reads
+ * routing->offsets and, with gather, src_of.  NaN and infinities stay in the
+ * rows of x and the columns of W that hold them.  x, codes and y 16-byte, scales
+ * 4-byte aligned; y overlaps no input. */
+moe_status moe_grouped_product(const moe_shape* shape, int weights, const void* x, int gather,
+                               const moe_routing* routing, const uint8_t* codes,
+                               const uint8_t* scales, int64_t N, int swiglu, void* y, void* stream);
+
 /* Combine alone (outputs returned to their original positions: "Prime Mega
  * MoE Trains Giant AI Models 55% Faster", section "Where MoE training loses
  * time"; the weighted sum of a token's expert outputs: "Prime Intellect
