@@ -20,9 +20,11 @@
 //   * nothing is sorted: each work-group finds its expert's tokens in the ids
 //     (at most 256 k of them).
 // All sums are float32 in a fixed order, without floating-point atomics.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.h"
+#include "mx4tile.h"
 #include "rowload.h"
 #include "tile.h"
 
@@ -1042,6 +1044,116 @@ __global__ __launch_bounds__(kDownRowWaves * 64, F == WF_FP8 && TB == 2 ? 3 : 1)
   }
 }
 
+// ------------------------------------------------------- e2m1 codes, more tokens
+// With half the bytes of a weight the products above are bound by their own LDS
+// turns and by loads that wait for each other; these are the streaming tiles of
+// mx4tile.h (64 tokens of the layer above: gate/up TIME us and TIME, down TIME
+// and TIME; 200 tokens TIME).  A work-group takes an expert's tokens in blocks of
+// 64 (down: 32, whose two planes of activations are 64 rows).
+template <int RB> using GuTiles = mx4::Tiles<RB, 4, RB <= 2 ? 3 : 2>;  // 64 gate columns a tile of 256
+template <int RB> using DnTiles = mx4::Tiles<RB, 4, RB <= 2 ? 3 : 2>;
+constexpr int kGu4Lds = std::max({GuTiles<1>::LDS, GuTiles<2>::LDS, GuTiles<3>::LDS, GuTiles<4>::LDS});
+constexpr int kDn4Lds = std::max(DnTiles<2>::LDS, DnTiles<4>::LDS);
+
+template <class C>
+__device__ __forceinline__ void gateup4_rows(const DecodeArgs& a, const Rows& rows, int e, int r0, int n, int n0,
+                                             tile::lds_t* lds) {
+  mx4::Stream<C> st;
+  const int64_t mat = (int64_t)e * 2 * a.I;
+  st.init([&](int i) { return (const char*)a.x + (int64_t)(rows.slot[min(r0 + i, n - 1)] / a.k) * a.d * 2; },
+          [&](int c) -> int64_t {  // 16 gate columns, the same up columns, in turn; past I the last
+            return mat + min(n0 + (c >> 5) * 16 + (c & 15), a.I - 1) + ((c & 16) ? a.I : 0);
+          },
+          (const uint8_t*)a.w_gate_up, (const uint8_t*)a.s_gate_up, a.d);
+  f32x4_t acc[C::RB][C::CB];
+  mx4::products<C>(st, a.d / 128, lds, acc);
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int b = 0; b < C::RB; ++b) {
+    const int r = r0 + 16 * b + (lane & 15);
+    if (r >= n) continue;
+    const float w = rows.w[r];
+#pragma unroll
+    for (int c = 0; c < C::CB / 2; ++c) {
+      const int col = n0 + (tile::wave_id() * (C::CB / 2) + c) * 16 + 4 * (lane >> 4);
+      if (col >= a.I) continue;  // I is a multiple of 128: four columns are in or out
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = w * swiglu(acc[b][2 * c][i], acc[b][2 * c + 1][i], a.lim);
+      put_aw<bf16_t>(a, (int64_t)rows.slot[r] * a.I + col, v[0], v[1]);
+      put_aw<bf16_t>(a, (int64_t)rows.slot[r] * a.I + col + 2, v[2], v[3]);
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void decode_gateup4_kernel(DecodeArgs a) {
+  extern __shared__ __align__(16) char smem[];
+  __shared__ Rows rows;
+  const int e = __builtin_amdgcn_readfirstlane(item_expert(a.mid, blockIdx.y, a.T * a.k, a.E));
+  if (e < 0) return;
+  Finder find;
+  const int n = __builtin_amdgcn_readfirstlane(find.count(rows, a.mid, a.mw, e, a.T, a.k));
+  if (n == 0) return;
+  find.list(rows);
+  const int n0 = blockIdx.x * (GuTiles<1>::COLS / 2);
+  for (int r0 = blockIdx.z * 64; r0 < n; r0 += gridDim.z * 64) {
+    if (n - r0 <= 16) gateup4_rows<GuTiles<1>>(a, rows, e, r0, n, n0, (tile::lds_t*)smem);
+    else if (n - r0 <= 32) gateup4_rows<GuTiles<2>>(a, rows, e, r0, n, n0, (tile::lds_t*)smem);
+    else if (n - r0 <= 48) gateup4_rows<GuTiles<3>>(a, rows, e, r0, n, n0, (tile::lds_t*)smem);
+    else gateup4_rows<GuTiles<4>>(a, rows, e, r0, n, n0, (tile::lds_t*)smem);
+  }
+}
+
+// Rows 0 .. 8 RB - 1 of the tile are the first plane, the rest the second.
+template <class C>
+__device__ __forceinline__ void down4_rows(const DecodeArgs& a, const Rows& rows, int e, int r0, int n, int n0,
+                                           tile::lds_t* lds) {
+  constexpr int HB = C::RB / 2;
+  mx4::Stream<C> st;
+  const int64_t mat = (int64_t)e * a.d;
+  st.init(
+      [&](int i) {
+        const bool second = i >= 16 * HB;
+        const int64_t at = (int64_t)rows.slot[min(r0 + i - (second ? 16 * HB : 0), n - 1)] * a.I;
+        return (const char*)a.aw + (at + (second ? aw_plane(a) : 0)) * 2;
+      },
+      [&](int c) -> int64_t { return mat + min(n0 + c, a.d - 1); }, (const uint8_t*)a.w_down, (const uint8_t*)a.s_down,
+      a.I);
+  f32x4_t acc[C::RB][C::CB];
+  mx4::products<C>(st, a.I / 128, lds, acc);
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int b = 0; b < HB; ++b) {
+    const int r = r0 + 16 * b + (lane & 15);
+    if (r >= n) continue;
+#pragma unroll
+    for (int c = 0; c < C::CB; ++c) {
+      const int col = n0 + (tile::wave_id() * C::CB + c) * 16 + 4 * (lane >> 4);
+      if (col >= a.d) continue;  // d is a multiple of 128
+      f32x4_t v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = join_planes(acc[b][c][i], acc[HB + b][c][i]);
+      *(f32x4_t*)(a.y + (int64_t)rows.slot[r] * a.d + col) = v;
+    }
+  }
+}
+
+__global__ __launch_bounds__(256) void decode_down4_kernel(DecodeArgs a) {
+  extern __shared__ __align__(16) char smem[];
+  __shared__ Rows rows;
+  const int e = __builtin_amdgcn_readfirstlane(item_expert(a.mid, blockIdx.y, a.T * a.k, a.E));
+  if (e < 0) return;
+  Finder find;
+  const int n = __builtin_amdgcn_readfirstlane(find.count(rows, a.mid, a.mw, e, a.T, a.k));
+  if (n == 0) return;
+  find.list(rows);
+  const int n0 = blockIdx.x * DnTiles<2>::COLS;
+  for (int r0 = blockIdx.z * 32; r0 < n; r0 += gridDim.z * 32) {
+    if (n - r0 <= 16) down4_rows<DnTiles<2>>(a, rows, e, r0, n, n0, (tile::lds_t*)smem);
+    else down4_rows<DnTiles<4>>(a, rows, e, r0, n, n0, (tile::lds_t*)smem);
+  }
+}
+
 // out[t] = sum of the token's live slots of y, in slot order; one rounding.
 template <typename AT>
 __global__ __launch_bounds__(256) void decode_combine_kernel(DecodeArgs a) {
@@ -1183,6 +1295,21 @@ hipError_t run_down(const LaunchCtx& c, const DecodeArgs& a) {
   return hipSuccess;
 }
 
+hipError_t run4(const LaunchCtx& c, const DecodeArgs& a) {
+  const unsigned items = (unsigned)work_items(a);
+  HIP_RET((tile::allow_smem_once<decode_gateup4_kernel>(kGu4Lds)));
+  HIP_RET((tile::allow_smem_once<decode_down4_kernel>(kDn4Lds)));
+  const unsigned gu = (unsigned)cdiv(2 * a.I, GuTiles<1>::COLS), dn = (unsigned)cdiv(a.d, DnTiles<2>::COLS);
+  const auto split = [&](int rows, unsigned groups) {
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>(cdiv(a.T, rows), 512 / std::max(1u, groups)));
+  };
+  MOE_LAUNCH(c, "decode_gateup", decode_gateup4_kernel, dim3(gu, items, split(64, gu * items)), dim3(256), kGu4Lds, a);
+  MOE_LAUNCH(c, "decode_down", decode_down4_kernel, dim3(dn, items, split(32, dn * items)), dim3(256), kDn4Lds, a);
+  MOE_LAUNCH(c, "decode_combine", decode_combine_kernel<bf16_t>, dim3((unsigned)cdiv(a.d, 1024), (unsigned)a.T),
+             dim3(256), 0, a);
+  return hipSuccess;
+}
+
 template <int F>
 hipError_t run(const LaunchCtx& c, const DecodeArgs& a) {
   if (past_cache<F>(a)) {
@@ -1220,7 +1347,7 @@ hipError_t launch_decode(const LaunchCtx& c, DecodeArgs a, int weights) {
 #undef TOPK
   if (weights == 1) return run<WF_FP8>(c, a);
   if (weights == 2) return run<WF_MX>(c, a);
-  if (weights == 3) return run<WF_MX4>(c, a);
+  if (weights == 3) return a.T > 16 ? run4(c, a) : run<WF_MX4>(c, a);
   return a.dtype == F32 ? run<WF_F32>(c, a) : run<WF_BF16>(c, a);
 }
 

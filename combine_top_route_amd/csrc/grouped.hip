@@ -16,12 +16,18 @@
 #include <algorithm>
 
 #include "common.h"
+#include "mx4tile.h"
 #include "tile.h"
 
 namespace moe {
 namespace {
 
 using namespace tile;
+using mx4::decode8;
+using mx4::lds16;
+using mx4::scale_of;
+using mx4::Stream;
+using mx4::wait_lgkm0;
 
 constexpr int NW = 8, NT = NW * 64;
 constexpr int TN = 256;            // columns of W a tile
@@ -35,48 +41,59 @@ struct Tile {
   int e, m0, seg1, nt;
 };
 
-// Rows of expert e; whatever the offsets hold, inside the R rows there are.
-__device__ __forceinline__ int first_row(const GroupedArgs& a, int e) { return min(max(a.offsets[e], 0), a.R); }
+// Sums over the lanes up to each: DPP shifts inside rows of 16 lanes, then the
+// rows' last lanes to the rows behind.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
+  return v;
+}
 
 // The tile of this work-group, every wave for itself: lane l counts the row
-// tiles of experts l P .. l P + P - 1.  False: none.
+// tiles of experts l, l + 64, .., whose offsets it loads all at once.  EPL:
+// experts a lane.  False: none.  (A kernel that leaves a table of the tiles
+// behind costs a launch, 4 us; this about 1 us of each work-group, beside the
+// others' work.)
+template <int EPL>
 __device__ __forceinline__ bool find_tile(const GroupedArgs& a, int rows, int ntiles, Tile* t) {
   const int lane = threadIdx.x & 63;
-  const int P = (a.E + 63) >> 6;
-  int sum = 0;
-  for (int i = 0; i < P; ++i) {
-    const int e = lane * P + i;
-    const int n = e < a.E ? first_row(a, e + 1) - first_row(a, e) : 0;
-    sum += (max(n, 0) + rows - 1) / rows;
-  }
-  int incl = sum;
+  int o0[EPL], o1[EPL], incl[EPL], total = 0;
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += o;
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane + 64 * i;
+    o0[i] = a.offsets[min(e, a.E)];
+    o1[i] = a.offsets[min(e + 1, a.E)];
   }
-  const int total = __builtin_amdgcn_readlane(incl, 63);
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {  // whatever the offsets hold, rows that there are
+    o0[i] = min(max(o0[i], 0), a.R);
+    o1[i] = min(max(o1[i], 0), a.R);
+    const int n = (max(o1[i] - o0[i], 0) + rows - 1) / rows;
+    incl[i] = total + wave_scan(n);
+    total = __builtin_amdgcn_readlane(incl[i], 63);
+  }
   const int L = xcd_tile(blockIdx.y * gridDim.x + blockIdx.x, total * ntiles);
   if (L < 0) return false;
-  const int own = __builtin_ctzll(__ballot(incl * ntiles > L));
-  const int before = own ? __builtin_amdgcn_readlane(incl, own - 1) : 0;
-  // the lane's experts in turn, the same in every lane
-  int base = before;
-  for (int i = 0; i < P; ++i) {
-    const int e = own * P + i;
-    if (e >= a.E) break;
-    const int o0 = first_row(a, e), o1 = first_row(a, e + 1);
-    const int n = (max(o1 - o0, 0) + rows - 1) / rows;
-    if (L < (base + n) * ntiles) {
-      const int at = L - base * ntiles;
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const uint64_t past = __ballot(incl[i] * ntiles > L);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      if (l) before = __builtin_amdgcn_readlane(incl[i], l - 1);
+      const int n = __builtin_amdgcn_readlane(incl[i], l) - before, at = L - before * ntiles;
       const int rt = a.row_major ? at / ntiles : at % n;
-      t->nt = __builtin_amdgcn_readfirstlane(a.row_major ? at % ntiles : at / n);
-      t->e = __builtin_amdgcn_readfirstlane(e);
-      t->m0 = __builtin_amdgcn_readfirstlane(o0 + rt * rows);
-      t->seg1 = __builtin_amdgcn_readfirstlane(o1);
+      t->nt = a.row_major ? at % ntiles : at / n;
+      t->e = l + 64 * i;
+      t->m0 = __builtin_amdgcn_readlane(o0[i], l) + rt * rows;
+      t->seg1 = __builtin_amdgcn_readlane(o1[i], l);
       return true;
     }
-    base += n;
+    before = __builtin_amdgcn_readlane(incl[i], 63);
   }
   return false;
 }
@@ -145,22 +162,6 @@ struct Loads {
   }
 };
 
-__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F); }  // lgkmcnt(0) alone
-
-__device__ __forceinline__ u32x4_t lds16(const lds_t* p) {
-  return *(const __attribute__((address_space(3))) u32x4_t*)p;
-}
-
-// Eight codes under a scale.
-__device__ __forceinline__ bf16x8_t decode8(uint32_t c, float s) {
-  u32x4_t o;
-  o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0));
-  o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1));
-  o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2));
-  o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
-  return __builtin_bit_cast(bf16x8_t, o);
-}
-
 // One K step (P: the first or second half of the codes' 128 columns).
 template <int TMX, int P>
 __device__ __forceinline__ void step(const lds_t* __restrict__ As, const lds_t* __restrict__ Bs, int wm, int wn,
@@ -174,7 +175,7 @@ __device__ __forceinline__ void step(const lds_t* __restrict__ As, const lds_t* 
     code[j] = lds16(Bs + row * 64 + (((2 * P + h) ^ (row >> 2)) & 3) * 16);
     const uint32_t word =
         *(const __attribute__((address_space(3))) uint32_t*)(Bs + B_SCALES + (row >> 5) * 256 + (row & 31) * 4);
-    s[j] = __uint_as_float(((word >> (16 * P + 8 * h)) & 0xffu) << 23);
+    s[j] = scale_of(word, 16 * P + 8 * h);
   }
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
@@ -271,7 +272,6 @@ __device__ __forceinline__ void tile_rows(const GroupedArgs& a, const Tile& t, l
   barrier_lds();
   constexpr int CPR = COLS / 8;
   const int width = SWIGLU ? a.N / 2 : a.N, c0 = t.nt * COLS;
-#pragma unroll
   for (int q = threadIdx.x; q < ROWS * CPR; q += NT) {
     const int row = q / CPR, c = c0 + (q % CPR) * 8;
     if (t.m0 + row < t.seg1 && c < width)
@@ -279,34 +279,130 @@ __device__ __forceinline__ void tile_rows(const GroupedArgs& a, const Tile& t, l
   }
 }
 
-template <bool SWIGLU>
+template <bool SWIGLU, int EPL>
 __global__ __launch_bounds__(NT) void grouped_tile_kernel(GroupedArgs a, int ntiles) {
   extern __shared__ __align__(16) char smem[];
   lds_t* lds = (lds_t*)smem;
   Tile t;
-  if (!find_tile(a, 256, ntiles, &t)) return;
+  if (!find_tile<EPL>(a, 256, ntiles, &t)) return;
   const int rows = t.seg1 - t.m0;
   if (rows <= 64) tile_rows<64, SWIGLU>(a, t, lds);
   else if (rows <= 128) tile_rows<128, SWIGLU>(a, t, lds);
   else tile_rows<256, SWIGLU>(a, t, lds);
 }
 
-template <bool SWIGLU>
+// Few rows an expert: tiles of 64 rows (16, 32 or 48 where there are no more) by
+// 64 CB columns, or 32 CB gate and the same up columns.
+constexpr int SROWS = 64;
+
+template <class C, bool SWIGLU>
+__device__ __forceinline__ void stream_rows(const GroupedArgs& a, const Tile& t, lds_t* lds) {
+  constexpr int COLS = SWIGLU ? C::COLS / 2 : C::COLS, S = COLS * 2 + 16;
+  static_assert(C::ROWS * S <= C::LDS && (!SWIGLU || C::CB % 2 == 0), "");
+  Stream<C> st;
+  const int64_t mat = (int64_t)t.e * a.N;
+  st.init(
+      [&](int i) {  // rows past the segment repeat its last
+        const int r = min(t.m0 + i, t.seg1 - 1);
+        const int64_t s = a.src_of ? min(max(a.src_of[r], 0), a.R - 1) / a.k : r;
+        return (const char*)a.x + s * a.K * 2;
+      },
+      [&](int n) -> int64_t {  // columns past the last repeat it; SWIGLU: 16 gate, the same up, in turn
+        if constexpr (SWIGLU) {
+          const int c = min(t.nt * COLS + (n >> 5) * 16 + (n & 15), a.N / 2 - 1);
+          return mat + ((n & 16) ? a.N / 2 + c : c);
+        } else {
+          return mat + min(t.nt * COLS + n, a.N - 1);
+        }
+      },
+      a.codes, a.scales, a.K);
+  f32x4_t acc[C::RB][C::CB];
+  mx4::products<C>(st, a.K / 128, lds, acc);
+  const int lane = threadIdx.x & 63, w = wave_id();
+#pragma unroll
+  for (int b = 0; b < C::RB; ++b) {
+    lds_t* row = lds + (16 * b + (lane & 15)) * S + (w * (COLS / 4) + 4 * (lane >> 4)) * 2;
+#pragma unroll
+    for (int c = 0; c < (SWIGLU ? C::CB / 2 : C::CB); ++c) {
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (SWIGLU) {
+          const float gc = clip_gate(acc[b][2 * c][i], a.lim);
+          v[i] = gc * sigmoidf_(gc) * clip_up(acc[b][2 * c + 1][i], a.lim);
+        } else {
+          v[i] = acc[b][c][i];
+        }
+      }
+      *(__attribute__((address_space(3))) u32x2_t*)(row + c * 32) =
+          u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    }
+  }
+  wait_lgkm0();
+  barrier_lds();
+  constexpr int CPR = COLS / 8;
+  const int width = SWIGLU ? a.N / 2 : a.N, c0 = t.nt * COLS;
+  for (int i = threadIdx.x; i < C::ROWS * CPR; i += 256) {
+    const int row = i / CPR, c = c0 + (i % CPR) * 8;
+    if (t.m0 + row < t.seg1 && c < width)
+      *(u32x4_t*)((bf16_t*)a.y + (int64_t)(t.m0 + row) * width + c) = lds16(lds + row * S + (i % CPR) * 16);
+  }
+}
+
+template <int CB> using Rows16 = mx4::Tiles<1, CB, 3>;
+template <int CB> using Rows32 = mx4::Tiles<2, CB, 3>;
+template <int CB> using Rows48 = mx4::Tiles<3, CB, 2>;
+template <int CB> using Rows64 = mx4::Tiles<4, CB, 2>;
+template <int CB>
+constexpr int kStreamLds = std::max({Rows16<CB>::LDS, Rows32<CB>::LDS, Rows64<CB>::LDS});
+
+template <int CB, bool SWIGLU, int EPL>
+__global__ __launch_bounds__(256) void grouped_stream_kernel(GroupedArgs a, int ntiles) {
+  extern __shared__ __align__(16) char smem[];
+  lds_t* lds = (lds_t*)smem;
+  Tile t;
+  if (!find_tile<EPL>(a, SROWS, ntiles, &t)) return;
+  const int rows = t.seg1 - t.m0;
+  if (rows <= 16) stream_rows<Rows16<CB>, SWIGLU>(a, t, lds);
+  else if (rows <= 32) stream_rows<Rows32<CB>, SWIGLU>(a, t, lds);
+  else if (rows <= 48) stream_rows<Rows48<CB>, SWIGLU>(a, t, lds);
+  else stream_rows<Rows64<CB>, SWIGLU>(a, t, lds);
+}
+
+// Whether tiles of few rows are taken: on average at most 64 rows an expert.
+bool few_rows(const GroupedArgs& a) { return a.R <= 64 * (int64_t)a.E; }
+
+// A grid of at least `groups`, in two dimensions: one holds fewer than 2^32
+// threads along one.
+dim3 grid_of(int64_t groups) {
+  groups = cdiv(groups, 8) * 8;
+  const int64_t gx = std::min<int64_t>(groups, 1 << 22);
+  return dim3((unsigned)gx, (unsigned)cdiv(groups, gx));
+}
+
+template <bool SWIGLU, int EPL>
 hipError_t run(const LaunchCtx& c, const GroupedArgs& a) {
-  const int ntiles = (int)cdiv(a.N, TN);
-  const int64_t row_tiles = a.R / 256 + std::min<int64_t>(a.E, a.R);  // at most
-  // in two dimensions: a grid holds fewer than 2^32 threads along one
-  const int64_t groups = cdiv(row_tiles * ntiles, 8) * 8, gx = std::min<int64_t>(groups, 1 << 22);
-  const dim3 grid((unsigned)gx, (unsigned)cdiv(groups, gx));
-  HIP_RET((allow_smem_once<grouped_tile_kernel<SWIGLU>>(LDS_BYTES)));
-  MOE_LAUNCH(c, "grouped_product", grouped_tile_kernel<SWIGLU>, grid, dim3(NT), LDS_BYTES, a, ntiles);
+  const int64_t experts = std::min<int64_t>(a.E, a.R);
+  if (few_rows(a)) {
+    constexpr int CB = 4;
+    const int ntiles = (int)cdiv(a.N, 64 * CB);
+    HIP_RET((allow_smem_once<grouped_stream_kernel<CB, SWIGLU, EPL>>(kStreamLds<CB>)));
+    MOE_LAUNCH(c, "grouped_product", (grouped_stream_kernel<CB, SWIGLU, EPL>),
+               grid_of((a.R / SROWS + experts) * ntiles), dim3(256), kStreamLds<CB>, a, ntiles);
+  } else {
+    const int ntiles = (int)cdiv(a.N, TN);
+    HIP_RET((allow_smem_once<grouped_tile_kernel<SWIGLU, EPL>>(LDS_BYTES)));
+    MOE_LAUNCH(c, "grouped_product", (grouped_tile_kernel<SWIGLU, EPL>), grid_of((a.R / 256 + experts) * ntiles), dim3(NT),
+               LDS_BYTES, a, ntiles);
+  }
   return hipSuccess;
 }
 
 }  // namespace
 
 hipError_t launch_grouped(const LaunchCtx& c, const GroupedArgs& a) {
-  return a.swiglu ? run<true>(c, a) : run<false>(c, a);
+  if (a.E <= 128) return a.swiglu ? run<true, 2>(c, a) : run<false, 2>(c, a);
+  return a.swiglu ? run<true, 16>(c, a) : run<false, 16>(c, a);
 }
 
 }  // namespace moe
