@@ -29,12 +29,13 @@ using mx4::scale_of;
 using mx4::Stream;
 using mx4::wait_lgkm0;
 
-constexpr int NW = 8, NT = NW * 64;
-constexpr int TN = 256;            // columns of W a tile
-constexpr int SLOT_A = 32 * 1024;  // [256 rows][64 values]
-constexpr int SLOT_B = 18 * 1024;  // [256 rows][64 bytes: 128 codes], then scale words
-constexpr int B_SCALES = 16 * 1024;
-constexpr int LDS_BYTES = 3 * SLOT_A + 2 * SLOT_B;
+constexpr int NW = 4, NT = NW * 64;
+constexpr int TM = 128, TN = 256;          // rows and columns of W a tile
+constexpr int SLOT_A = TM * 128;           // [rows][64 values]
+constexpr int CODES_B = TN * 64;           // [columns][128 codes], then their scale words
+constexpr int SLOT_B = CODES_B + TN * 4;
+constexpr int LDS_BYTES = TM * (TN * 2 + 16);  // the ring, 2 SLOT_A + 2 SLOT_B, is smaller than the tile on its way out
+static_assert(2 * SLOT_A + 2 * SLOT_B <= LDS_BYTES && 2 * LDS_BYTES <= 160 * 1024, "");
 
 // An expert's row tile: rows m0 .. of [.., seg1), column tile nt.
 struct Tile {
@@ -112,143 +113,155 @@ __device__ __forceinline__ int w_row(const GroupedArgs& a, int nt, int n) {
 }
 
 // Direct loads of a K step's rows and of two steps' codes and scales.
-template <int ROWS>
+template <int TMX>
 struct Loads {
-  static constexpr int NA = ROWS / 64;
-  const char* pa[NA];
-  const char* pb[2];
+  static constexpr int NB = 5;  // loads of codes() a wave
+  const char* pa[TMX];
+  const char* pb[4];
   const char* ps;
   template <bool SWIGLU>
   __device__ __forceinline__ void init(const GroupedArgs& a, const Tile& t) {
     const int lane = threadIdx.x & 63, w = wave_id();
-    int src[NA];
+    int src[TMX];
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {  // rows past the segment repeat its last
+    for (int i = 0; i < TMX; ++i) {  // rows past the segment repeat its last
       const int r = min(t.m0 + 8 * (w + NW * i) + (lane >> 3), t.seg1 - 1);
       src[i] = a.src_of ? min(max(a.src_of[r], 0), a.R - 1) : r;
     }
+    const int64_t mat = (int64_t)t.e * a.N;
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * (w + NW * i) + (lane >> 2);
+      pb[i] = (const char*)a.codes + (mat + w_row<SWIGLU>(a, t.nt, row)) * (a.K / 2) + (((lane ^ (row >> 2)) & 3) << 4);
+    }
+    ps = (const char*)a.scales + (mat + w_row<SWIGLU>(a, t.nt, 64 * w + lane)) * (a.K / 32);
+#pragma unroll
+    for (int i = 0; i < TMX; ++i) {
       const int row = 8 * (w + NW * i) + (lane >> 3);
       const int64_t s = a.src_of ? src[i] / a.k : src[i];
       pa[i] = (const char*)a.x + s * a.K * 2 + (((lane & 7) ^ mk_swz(row)) << 4);
     }
-    const int64_t mat = (int64_t)t.e * a.N;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = 16 * (w + NW * i) + (lane >> 2);
-      pb[i] = (const char*)a.codes + (mat + w_row<SWIGLU>(a, t.nt, row)) * (a.K / 2) + (((lane ^ (row >> 2)) & 3) << 4);
-    }
-    ps = (const char*)a.scales + (mat + w_row<SWIGLU>(a, t.nt, 32 * w + (lane & 31))) * (a.K / 32);
   }
   __device__ __forceinline__ void rows(lds_t* slot) {
     const int w = wave_id();
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
+    for (int i = 0; i < TMX; ++i) {
       dma16(pa[i], slot + (w + NW * i) * 1024);
       pa[i] += 128;
     }
   }
-  // 16 KB of codes and a scale word a row: 32 rows' words (and again the same) a wave
   __device__ __forceinline__ void codes(lds_t* slot) {
     const int w = wave_id();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       dma16(pb[i], slot + (w + NW * i) * 1024);
       pb[i] += 64;
     }
-    dma4(ps, slot + B_SCALES + w * 256);
+    dma4(ps, slot + CODES_B + w * 256);
     ps += 4;
   }
 };
 
-// One K step (P: the first or second half of the codes' 128 columns).
+// One K step (P: the first or second half of the codes' 128 columns).  The
+// operands of the next quarter are read and decoded while a quarter's products
+// run.
 template <int TMX, int P>
-__device__ __forceinline__ void step(const lds_t* __restrict__ As, const lds_t* __restrict__ Bs, int wm, int wn,
+__device__ __forceinline__ void step(const lds_t* __restrict__ As, const lds_t* __restrict__ Bs,
                                      f32x16_t (&acc)[TMX][2]) {
-  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5, w = wave_id();
   u32x4_t code[2];
+  uint32_t word[2];
+  bf16x8_t av[2][TMX], bv[2][2];
+  const auto rows = [&](int kk, bf16x8_t (&v)[TMX]) {
+#pragma unroll
+    for (int i = 0; i < TMX; ++i) v[i] = __builtin_bit_cast(bf16x8_t, lds16(As + mk_off(i * 32 + r, 4 * h + kk)));
+  };
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int n = w * 64 + j * 32 + r;
+    word[j] = *(const __attribute__((address_space(3))) uint32_t*)(Bs + CODES_B + n * 4);
+    code[j] = lds16(Bs + n * 64 + (((2 * P + h) ^ (n >> 2)) & 3) * 16);
+  }
+  rows(0, av[0]);
+  __builtin_amdgcn_sched_barrier(0);
   float s[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int row = wn * 64 + j * 32 + r;
-    code[j] = lds16(Bs + row * 64 + (((2 * P + h) ^ (row >> 2)) & 3) * 16);
-    const uint32_t word =
-        *(const __attribute__((address_space(3))) uint32_t*)(Bs + B_SCALES + (row >> 5) * 256 + (row & 31) * 4);
-    s[j] = scale_of(word, 16 * P + 8 * h);
+    s[j] = scale_of(word[j], 16 * P + 8 * h);
+    bv[0][j] = decode8(code[j][0], s[j]);
   }
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk) {
-    bf16x8_t b[2];
+    const int c = kk & 1;
+    if (kk < 3) rows(kk + 1, av[c ^ 1]);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) b[j] = decode8(code[j][kk], s[j]);
-#pragma unroll
-    for (int i = 0; i < TMX; ++i) {
-      const bf16x8_t av =
-          __builtin_bit_cast(bf16x8_t, lds16(As + mk_off(wm * (TMX * 32) + i * 32 + r, 4 * h + kk)));
+    for (int i = 0; i < TMX; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], av, acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bv[c][j], av[c][i], acc[i][j], 0, 0, 0);
+    if (kk < 3) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) bv[c ^ 1][j] = decode8(code[j][kk + 1], s[j]);
+      // a read and some of the conversions after each product
+#pragma unroll
+      for (int q = 0; q < 2 * TMX; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                   // MFMA
+        if (q < TMX) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);      // DS read
+        __builtin_amdgcn_sched_group_barrier(0x002, TMX > 2 ? 2 : 4, 0);     // VALU
+      }
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// Rows of a step are in slot k mod 3, two steps ahead; codes of steps 2 s and
-// 2 s + 1 in slot s mod 2, filled one such pair ahead.  Loads land in the order
-// they left, so before the even step all but the next step's rows have, before
-// the odd one all but what the even step issued.
-template <int ROWS>
-__device__ __forceinline__ void mainloop(Loads<ROWS>& ld, int pairs, lds_t* lds, f32x16_t (&acc)[ROWS / 64][2]) {
-  constexpr int TMX = ROWS / 64, NA = Loads<ROWS>::NA;
-  const int w = wave_id(), wm = w >> 2, wn = w & 3;
+// Rows of step k are in slot k mod 2, filled during step k - 1; codes of steps
+// 2 p and 2 p + 1 in slot p mod 2, filled during the pair before.  Two
+// work-groups share a CU, so that one's barriers and waits pass under the
+// other's products.  Loads land in the order they left.
+template <int TMX>
+__device__ __forceinline__ void mainloop(Loads<TMX>& ld, int pairs, lds_t* lds, f32x16_t (&acc)[TMX][2]) {
 #pragma unroll
   for (int i = 0; i < TMX; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-  lds_t* const lb = lds + 3 * SLOT_A;
+  lds_t* const lb = lds + 2 * SLOT_A;
   ld.codes(lb);
   ld.rows(lds);
-  ld.rows(lds + SLOT_A);
-  int sa = 0;  // slot of the even step's rows
-  auto next = [](int s, int n) { return s + n >= 3 ? s + n - 3 : s + n; };
   for (int p = 0; p < pairs; ++p) {
     const bool more = p + 1 < pairs;
     const lds_t* Bs = lb + (p & 1) * SLOT_B;
-    wait_vmcnt<NA>();
-    barrier_lds();
-    if (more) {
-      ld.codes(lb + ((p & 1) ^ 1) * SLOT_B);
-      ld.rows(lds + next(sa, 2) * SLOT_A);
-    }
-    step<TMX, 0>(lds + sa * SLOT_A, Bs, wm, wn, acc);
+    wait_vmcnt<0>();
     wait_lgkm0();  // the slots are read before the barrier that lets them go
-    if (more) wait_vmcnt<NA + 3>();
-    else wait_vmcnt<0>();
     barrier_lds();
-    if (more) ld.rows(lds + sa * SLOT_A);
-    step<TMX, 1>(lds + next(sa, 1) * SLOT_A, Bs, wm, wn, acc);
+    ld.rows(lds + SLOT_A);
+    if (more) ld.codes(lb + ((p & 1) ^ 1) * SLOT_B);
+    step<TMX, 0>(lds, Bs, acc);
+    if (more) wait_vmcnt<Loads<TMX>::NB>();
+    else wait_vmcnt<0>();
     wait_lgkm0();
-    sa = next(sa, 2);
+    barrier_lds();
+    if (more) ld.rows(lds);
+    step<TMX, 1>(lds + SLOT_A, Bs, acc);
   }
+  wait_lgkm0();
+  barrier_lds();  // every wave is done with the slots
 }
 
-// Accumulators: lane l has row i * 32 + l % 32 of the wave's tile; register v its
+// Accumulators: lane l has row i * 32 + l % 32 of the tile; register v the wave's
 // column j * 32 + 8 (v / 4) + 4 (l / 32) + v % 4.  They leave through LDS.
-template <int ROWS, bool SWIGLU>
+template <int TMX, bool SWIGLU>
 __device__ __forceinline__ void tile_rows(const GroupedArgs& a, const Tile& t, lds_t* lds) {
-  constexpr int TMX = ROWS / 64;
   constexpr int COLS = SWIGLU ? TN / 2 : TN, S = COLS * 2 + 16;
   f32x16_t acc[TMX][2];
-  Loads<ROWS> ld;
+  Loads<TMX> ld;
   ld.template init<SWIGLU>(a, t);
-  mainloop<ROWS>(ld, a.K / 128, lds, acc);
-  barrier_lds();  // every wave is done with the slots
-  const int lane = threadIdx.x & 63, w = wave_id(), wm = w >> 2, wn = w & 3;
+  mainloop<TMX>(ld, a.K / 128, lds, acc);
+  const int lane = threadIdx.x & 63, w = wave_id();
 #pragma unroll
   for (int i = 0; i < TMX; ++i) {
-    lds_t* row = lds + (wm * (ROWS / 2) + i * 32 + (lane & 31)) * S;
+    lds_t* row = lds + (i * 32 + (lane & 31)) * S;
 #pragma unroll
     for (int j = 0; j < (SWIGLU ? 1 : 2); ++j)
 #pragma unroll
@@ -263,7 +276,7 @@ __device__ __forceinline__ void tile_rows(const GroupedArgs& a, const Tile& t, l
             v[q] = acc[i][j][4 * g + q];
           }
         }
-        const int col = wn * (COLS / 4) + j * 32 + 8 * g + 4 * (lane >> 5);
+        const int col = w * (COLS / 4) + j * 32 + 8 * g + 4 * (lane >> 5);
         *(__attribute__((address_space(3))) u32x2_t*)(row + col * 2) =
             u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
       }
@@ -272,7 +285,7 @@ __device__ __forceinline__ void tile_rows(const GroupedArgs& a, const Tile& t, l
   barrier_lds();
   constexpr int CPR = COLS / 8;
   const int width = SWIGLU ? a.N / 2 : a.N, c0 = t.nt * COLS;
-  for (int q = threadIdx.x; q < ROWS * CPR; q += NT) {
+  for (int q = threadIdx.x; q < TMX * 32 * CPR; q += NT) {
     const int row = q / CPR, c = c0 + (q % CPR) * 8;
     if (t.m0 + row < t.seg1 && c < width)
       *(u32x4_t*)((bf16_t*)a.y + (int64_t)(t.m0 + row) * width + c) = lds16(lds + row * S + (q % CPR) * 16);
@@ -280,15 +293,16 @@ __device__ __forceinline__ void tile_rows(const GroupedArgs& a, const Tile& t, l
 }
 
 template <bool SWIGLU, int EPL>
-__global__ __launch_bounds__(NT) void grouped_tile_kernel(GroupedArgs a, int ntiles) {
+__global__ __launch_bounds__(NT, 2) void grouped_tile_kernel(GroupedArgs a, int ntiles) {
   extern __shared__ __align__(16) char smem[];
   lds_t* lds = (lds_t*)smem;
   Tile t;
-  if (!find_tile<EPL>(a, 256, ntiles, &t)) return;
+  if (!find_tile<EPL>(a, TM, ntiles, &t)) return;
   const int rows = t.seg1 - t.m0;
-  if (rows <= 64) tile_rows<64, SWIGLU>(a, t, lds);
-  else if (rows <= 128) tile_rows<128, SWIGLU>(a, t, lds);
-  else tile_rows<256, SWIGLU>(a, t, lds);
+  if (rows <= 32) tile_rows<1, SWIGLU>(a, t, lds);
+  else if (rows <= 64) tile_rows<2, SWIGLU>(a, t, lds);
+  else if (rows <= 96) tile_rows<3, SWIGLU>(a, t, lds);
+  else tile_rows<4, SWIGLU>(a, t, lds);
 }
 
 // Few rows an expert: tiles of 64 rows (16, 32 or 48 where there are no more) by
@@ -392,7 +406,7 @@ hipError_t run(const LaunchCtx& c, const GroupedArgs& a) {
   } else {
     const int ntiles = (int)cdiv(a.N, TN);
     HIP_RET((allow_smem_once<grouped_tile_kernel<SWIGLU, EPL>>(LDS_BYTES)));
-    MOE_LAUNCH(c, "grouped_product", (grouped_tile_kernel<SWIGLU, EPL>), grid_of((a.R / 256 + experts) * ntiles), dim3(NT),
+    MOE_LAUNCH(c, "grouped_product", (grouped_tile_kernel<SWIGLU, EPL>), grid_of((a.R / TM + experts) * ntiles), dim3(NT),
                LDS_BYTES, a, ntiles);
   }
   return hipSuccess;
