@@ -1136,7 +1136,6 @@ moe_status moe_grouped_product(const moe_shape* shape, int weights, const void* 
   a.codes = codes;
   a.scales = scales;
   a.y = y;
-  a.row_major = rows_tile_order(2 * rows * shape->d, shape->E * N * (shape->d / 2));
   const LaunchCtx c = make_ctx(stream);
   (void)hipGetLastError();
   HIP_TRY(launch_grouped(c, a), "grouped_product");

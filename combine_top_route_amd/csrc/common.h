@@ -320,9 +320,9 @@ struct GroupedArgs {
   const uint8_t* codes;    // [E, N, K / 2]
   const uint8_t* scales;   // [E, N, K / 32]
   void* y;                 // [R, N or N / 2]
-  int row_major;           // tile order within an expert (rows_tile_order)
+  bool row_major;          // set by the launcher: tile order within an expert
 };
-hipError_t launch_grouped(const LaunchCtx& c, const GroupedArgs& a);
+hipError_t launch_grouped(const LaunchCtx& c, GroupedArgs a);
 
 // ---------------------------------------------------------------- fp8 path
 // Block quantisation to e4m3 (quant_fp8.hip).  Two formats: blockwise (fp32

@@ -1050,16 +1050,16 @@ __global__ __launch_bounds__(kDownRowWaves * 64, F == WF_FP8 && TB == 2 ? 3 : 1)
 // mx4tile.h (64 tokens of the layer above: gate/up TIME us and TIME, down TIME
 // and TIME; 200 tokens TIME).  A work-group takes an expert's tokens in blocks of
 // 64 (down: 32, whose two planes of activations are 64 rows).
-template <int RB> using GuTiles = mx4::Tiles<RB, 4, RB <= 2 ? 3 : 2>;  // 64 gate columns a tile of 256
-template <int RB> using DnTiles = mx4::Tiles<RB, 4, RB <= 2 ? 3 : 2>;
-constexpr int kGu4Lds = std::max({GuTiles<1>::LDS, GuTiles<2>::LDS, GuTiles<3>::LDS, GuTiles<4>::LDS});
-constexpr int kDn4Lds = std::max(DnTiles<2>::LDS, DnTiles<4>::LDS);
+template <int RB, int CB> using Tiles4 = mx4::Tiles<RB, CB, RB <= 2 ? 3 : 2>;
+template <int CB>
+constexpr int kLds4 = std::max({Tiles4<1, CB>::LDS, Tiles4<2, CB>::LDS, Tiles4<3, CB>::LDS, Tiles4<4, CB>::LDS});
 
 template <class C>
 __device__ __forceinline__ void gateup4_rows(const DecodeArgs& a, const Rows& rows, int e, int r0, int n, int n0,
                                              tile::lds_t* lds) {
-  mx4::Stream<C> st;
   const int64_t mat = (int64_t)e * 2 * a.I;
+  const int lane = threadIdx.x & 63;
+  mx4::Stream<C> st;
   st.init([&](int i) { return (const char*)a.x + (int64_t)(rows.slot[min(r0 + i, n - 1)] / a.k) * a.d * 2; },
           [&](int c) -> int64_t {  // 16 gate columns, the same up columns, in turn; past I the last
             return mat + min(n0 + (c >> 5) * 16 + (c & 15), a.I - 1) + ((c & 16) ? a.I : 0);
@@ -1067,7 +1067,6 @@ __device__ __forceinline__ void gateup4_rows(const DecodeArgs& a, const Rows& ro
           (const uint8_t*)a.w_gate_up, (const uint8_t*)a.s_gate_up, a.d);
   f32x4_t acc[C::RB][C::CB];
   mx4::products<C>(st, a.d / 128, lds, acc);
-  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int b = 0; b < C::RB; ++b) {
     const int r = r0 + 16 * b + (lane & 15);
@@ -1086,6 +1085,7 @@ __device__ __forceinline__ void gateup4_rows(const DecodeArgs& a, const Rows& ro
   }
 }
 
+template <int CB>
 __global__ __launch_bounds__(256) void decode_gateup4_kernel(DecodeArgs a) {
   extern __shared__ __align__(16) char smem[];
   __shared__ Rows rows;
@@ -1095,12 +1095,13 @@ __global__ __launch_bounds__(256) void decode_gateup4_kernel(DecodeArgs a) {
   const int n = __builtin_amdgcn_readfirstlane(find.count(rows, a.mid, a.mw, e, a.T, a.k));
   if (n == 0) return;
   find.list(rows);
-  const int n0 = blockIdx.x * (GuTiles<1>::COLS / 2);
-  for (int r0 = blockIdx.z * 64; r0 < n; r0 += gridDim.z * 64) {
-    if (n - r0 <= 16) gateup4_rows<GuTiles<1>>(a, rows, e, r0, n, n0, (tile::lds_t*)smem);
-    else if (n - r0 <= 32) gateup4_rows<GuTiles<2>>(a, rows, e, r0, n, n0, (tile::lds_t*)smem);
-    else if (n - r0 <= 48) gateup4_rows<GuTiles<3>>(a, rows, e, r0, n, n0, (tile::lds_t*)smem);
-    else gateup4_rows<GuTiles<4>>(a, rows, e, r0, n, n0, (tile::lds_t*)smem);
+  tile::lds_t* lds = (tile::lds_t*)smem;
+  const int n0 = blockIdx.x * 32 * CB;
+  for (int r0 = 0; r0 < n; r0 += 64) {
+    if (n - r0 <= 16) gateup4_rows<Tiles4<1, CB>>(a, rows, e, r0, n, n0, lds);
+    else if (n - r0 <= 32) gateup4_rows<Tiles4<2, CB>>(a, rows, e, r0, n, n0, lds);
+    else if (n - r0 <= 48) gateup4_rows<Tiles4<3, CB>>(a, rows, e, r0, n, n0, lds);
+    else gateup4_rows<Tiles4<4, CB>>(a, rows, e, r0, n, n0, lds);
   }
 }
 
@@ -1109,8 +1110,9 @@ template <class C>
 __device__ __forceinline__ void down4_rows(const DecodeArgs& a, const Rows& rows, int e, int r0, int n, int n0,
                                            tile::lds_t* lds) {
   constexpr int HB = C::RB / 2;
-  mx4::Stream<C> st;
   const int64_t mat = (int64_t)e * a.d;
+  const int lane = threadIdx.x & 63;
+  mx4::Stream<C> st;
   st.init(
       [&](int i) {
         const bool second = i >= 16 * HB;
@@ -1121,7 +1123,6 @@ __device__ __forceinline__ void down4_rows(const DecodeArgs& a, const Rows& rows
       a.I);
   f32x4_t acc[C::RB][C::CB];
   mx4::products<C>(st, a.I / 128, lds, acc);
-  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int b = 0; b < HB; ++b) {
     const int r = r0 + 16 * b + (lane & 15);
@@ -1138,6 +1139,7 @@ __device__ __forceinline__ void down4_rows(const DecodeArgs& a, const Rows& rows
   }
 }
 
+template <int CB>
 __global__ __launch_bounds__(256) void decode_down4_kernel(DecodeArgs a) {
   extern __shared__ __align__(16) char smem[];
   __shared__ Rows rows;
@@ -1147,10 +1149,11 @@ __global__ __launch_bounds__(256) void decode_down4_kernel(DecodeArgs a) {
   const int n = __builtin_amdgcn_readfirstlane(find.count(rows, a.mid, a.mw, e, a.T, a.k));
   if (n == 0) return;
   find.list(rows);
-  const int n0 = blockIdx.x * DnTiles<2>::COLS;
+  tile::lds_t* lds = (tile::lds_t*)smem;
+  const int n0 = blockIdx.x * 64 * CB;
   for (int r0 = blockIdx.z * 32; r0 < n; r0 += gridDim.z * 32) {
-    if (n - r0 <= 16) down4_rows<DnTiles<2>>(a, rows, e, r0, n, n0, (tile::lds_t*)smem);
-    else down4_rows<DnTiles<4>>(a, rows, e, r0, n, n0, (tile::lds_t*)smem);
+    if (n - r0 <= 16) down4_rows<Tiles4<2, CB>>(a, rows, e, r0, n, n0, lds);
+    else down4_rows<Tiles4<4, CB>>(a, rows, e, r0, n, n0, lds);
   }
 }
 
@@ -1295,19 +1298,38 @@ hipError_t run_down(const LaunchCtx& c, const DecodeArgs& a) {
   return hipSuccess;
 }
 
-hipError_t run4(const LaunchCtx& c, const DecodeArgs& a) {
-  const unsigned items = (unsigned)work_items(a);
-  HIP_RET((tile::allow_smem_once<decode_gateup4_kernel>(kGu4Lds)));
-  HIP_RET((tile::allow_smem_once<decode_down4_kernel>(kDn4Lds)));
-  const unsigned gu = (unsigned)cdiv(2 * a.I, GuTiles<1>::COLS), dn = (unsigned)cdiv(a.d, DnTiles<2>::COLS);
-  const auto split = [&](int rows, unsigned groups) {
-    return (unsigned)std::max<int64_t>(1, std::min<int64_t>(cdiv(a.T, rows), 512 / std::max(1u, groups)));
-  };
-  MOE_LAUNCH(c, "decode_gateup", decode_gateup4_kernel, dim3(gu, items, split(64, gu * items)), dim3(256), kGu4Lds, a);
-  MOE_LAUNCH(c, "decode_down", decode_down4_kernel, dim3(dn, items, split(32, dn * items)), dim3(256), kDn4Lds, a);
+template <int CB>
+hipError_t down4(const LaunchCtx& c, const DecodeArgs& a) {
+  const int64_t tiles = cdiv(a.d, 64 * CB), items = work_items(a);
+  const int64_t split = std::max<int64_t>(1, std::min<int64_t>(cdiv(a.T, 32), 512 / (tiles * items)));
+  HIP_RET((tile::allow_smem_once<decode_down4_kernel<CB>>(kLds4<CB>)));
+  MOE_LAUNCH(c, "decode_down", decode_down4_kernel<CB>, dim3((unsigned)tiles, (unsigned)items, (unsigned)split),
+             dim3(256), kLds4<CB>, a);
   MOE_LAUNCH(c, "decode_combine", decode_combine_kernel<bf16_t>, dim3((unsigned)cdiv(a.d, 1024), (unsigned)a.T),
              dim3(256), 0, a);
   return hipSuccess;
+}
+
+// Which products the streaming tiles make.  Gate/up: beyond 16 tokens, with a
+// work-group for each CU (us with the kernels above and with these, d = 2048, I =
+// 768, 8 of 128 experts: 16 tokens 39 and 43, 24 50 and 47, 256 67 and 57; 40
+// tokens of all of 6, d = 1792, I = 512, 24 work-groups: 8 and 14).  Down: where I
+// is long, or a tile's rows are used (8 tokens 20 and 16, 256 58 and 39; 194 of 6
+// of 10, d = 896, I = 128 8.2 and 6.2; 5 of 8 of 113, d = 2304, I = 256 7.9 and
+// 8.9).
+hipError_t run4(const LaunchCtx& c, const DecodeArgs& a) {
+  const int64_t items = work_items(a);
+  if (a.T > 16 && items * cdiv(2 * a.I, 256) >= 256) {
+    HIP_RET((tile::allow_smem_once<decode_gateup4_kernel<4>>(kLds4<4>)));
+    MOE_LAUNCH(c, "decode_gateup", decode_gateup4_kernel<4>, dim3((unsigned)cdiv(2 * a.I, 256), (unsigned)items),
+               dim3(256), kLds4<4>, a);
+  } else {
+    HIP_RET((past_cache<WF_MX4>(a) ? run_gateup<WF_MX4, true>(c, a) : run_gateup<WF_MX4, false>(c, a)));
+  }
+  if (decode_one_down(a.T, a.k) || (a.I < 512 && a.T * a.k < 16 * items))
+    return past_cache<WF_MX4>(a) ? run_down<WF_MX4, true>(c, a) : run_down<WF_MX4, false>(c, a);
+  // 128 columns a work-group instead of 256 where those leave CUs without two
+  return items * cdiv(a.d, 256) < 512 ? down4<2>(c, a) : down4<4>(c, a);
 }
 
 template <int F>
@@ -1347,7 +1369,7 @@ hipError_t launch_decode(const LaunchCtx& c, DecodeArgs a, int weights) {
 #undef TOPK
   if (weights == 1) return run<WF_FP8>(c, a);
   if (weights == 2) return run<WF_MX>(c, a);
-  if (weights == 3) return a.T > 16 ? run4(c, a) : run<WF_MX4>(c, a);
+  if (weights == 3) return run4(c, a);
   return a.dtype == F32 ? run<WF_F32>(c, a) : run<WF_BF16>(c, a);
 }
 

@@ -309,27 +309,31 @@ __global__ __launch_bounds__(NT, 2) void grouped_tile_kernel(GroupedArgs a, int 
 // 64 CB columns, or 32 CB gate and the same up columns.
 constexpr int SROWS = 64;
 
+// Row i of a tile (past the segment its last), and the row of W for its column n
+// (past the last that; SWIGLU: 16 gate, the same up, in turn).
+__device__ __forceinline__ const char* row_at(const GroupedArgs& a, const Tile& t, int i) {
+  const int r = min(t.m0 + i, t.seg1 - 1);
+  const int64_t s = a.src_of ? min(max(a.src_of[r], 0), a.R - 1) / a.k : r;
+  return (const char*)a.x + s * a.K * 2;
+}
+template <bool SWIGLU, int COLS>
+__device__ __forceinline__ int64_t col_at(const GroupedArgs& a, const Tile& t, int n) {
+  const int64_t mat = (int64_t)t.e * a.N;
+  if constexpr (SWIGLU) {
+    const int c = min(t.nt * COLS + (n >> 5) * 16 + (n & 15), a.N / 2 - 1);
+    return mat + ((n & 16) ? a.N / 2 + c : c);
+  } else {
+    return mat + min(t.nt * COLS + n, a.N - 1);
+  }
+}
+
 template <class C, bool SWIGLU>
 __device__ __forceinline__ void stream_rows(const GroupedArgs& a, const Tile& t, lds_t* lds) {
   constexpr int COLS = SWIGLU ? C::COLS / 2 : C::COLS, S = COLS * 2 + 16;
   static_assert(C::ROWS * S <= C::LDS && (!SWIGLU || C::CB % 2 == 0), "");
   Stream<C> st;
-  const int64_t mat = (int64_t)t.e * a.N;
-  st.init(
-      [&](int i) {  // rows past the segment repeat its last
-        const int r = min(t.m0 + i, t.seg1 - 1);
-        const int64_t s = a.src_of ? min(max(a.src_of[r], 0), a.R - 1) / a.k : r;
-        return (const char*)a.x + s * a.K * 2;
-      },
-      [&](int n) -> int64_t {  // columns past the last repeat it; SWIGLU: 16 gate, the same up, in turn
-        if constexpr (SWIGLU) {
-          const int c = min(t.nt * COLS + (n >> 5) * 16 + (n & 15), a.N / 2 - 1);
-          return mat + ((n & 16) ? a.N / 2 + c : c);
-        } else {
-          return mat + min(t.nt * COLS + n, a.N - 1);
-        }
-      },
-      a.codes, a.scales, a.K);
+  st.init([&](int i) { return row_at(a, t, i); }, [&](int n) { return col_at<SWIGLU, COLS>(a, t, n); }, a.codes,
+          a.scales, a.K);
   f32x4_t acc[C::RB][C::CB];
   mx4::products<C>(st, a.K / 128, lds, acc);
   const int lane = threadIdx.x & 63, w = wave_id();
@@ -367,6 +371,9 @@ template <int CB> using Rows16 = mx4::Tiles<1, CB, 3>;
 template <int CB> using Rows32 = mx4::Tiles<2, CB, 3>;
 template <int CB> using Rows48 = mx4::Tiles<3, CB, 2>;
 template <int CB> using Rows64 = mx4::Tiles<4, CB, 2>;
+using Split16 = mx4::SplitTiles<1, 3>;
+using Split32 = mx4::SplitTiles<2, 2>;
+constexpr int kSplitLds = std::max(Split16::LDS, Split32::LDS);
 template <int CB>
 constexpr int kStreamLds = std::max({Rows16<CB>::LDS, Rows32<CB>::LDS, Rows64<CB>::LDS});
 
@@ -383,8 +390,54 @@ __global__ __launch_bounds__(256) void grouped_stream_kernel(GroupedArgs a, int 
   else stream_rows<Rows64<CB>, SWIGLU>(a, t, lds);
 }
 
-// Whether tiles of few rows are taken: on average at most 64 rows an expert.
-bool few_rows(const GroupedArgs& a) { return a.R <= 64 * (int64_t)a.E; }
+// The same where they would leave the chip idle: 32 rows by 64 columns (32 gate,
+// the same up), K over the waves.
+constexpr int PROWS = 32;
+
+template <class C, bool SWIGLU>
+__device__ __forceinline__ void split_rows(const GroupedArgs& a, const Tile& t, lds_t* lds) {
+  constexpr int COLS = SWIGLU ? C::COLS / 2 : C::COLS;
+  mx4::SplitStream<C> st;
+  st.init([&](int i) { return row_at(a, t, i); }, [&](int n) { return col_at<SWIGLU, COLS>(a, t, n); }, a.codes,
+          a.scales, a.K);
+  f32x4_t acc[C::RB][4];
+  // a wave finishes one block of 16 columns, or of gate and up
+  const auto keep = [](int w, int c) { return SWIGLU ? (c >> 1) == w : c == w; };
+  mx4::split_products<C>(st, a.K / 128, lds, acc, keep);
+  const int lane = threadIdx.x & 63, w = wave_id(), width = SWIGLU ? a.N / 2 : a.N;
+#pragma unroll
+  for (int c = 0; c < (SWIGLU ? 2 : 4); ++c) {
+    if (c != w) continue;
+    const int col = t.nt * COLS + 16 * c + 4 * (lane >> 4);
+#pragma unroll
+    for (int b = 0; b < C::RB; ++b) {
+      const int r = t.m0 + 16 * b + (lane & 15);
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (SWIGLU) {
+          const float gc = clip_gate(acc[b][2 * c][i], a.lim);
+          v[i] = gc * sigmoidf_(gc) * clip_up(acc[b][2 * c + 1][i], a.lim);
+        } else {
+          v[i] = acc[b][c][i];
+        }
+      }
+      if (r < t.seg1 && col < width)  // the width is a multiple of 8
+        *(u32x2_t*)((bf16_t*)a.y + (int64_t)r * width + col) =
+            u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    }
+  }
+}
+
+template <bool SWIGLU, int EPL>
+__global__ __launch_bounds__(256) void grouped_split_kernel(GroupedArgs a, int ntiles) {
+  extern __shared__ __align__(16) char smem[];
+  lds_t* lds = (lds_t*)smem;
+  Tile t;
+  if (!find_tile<EPL>(a, PROWS, ntiles, &t)) return;
+  if (t.seg1 - t.m0 <= 16) split_rows<Split16, SWIGLU>(a, t, lds);
+  else split_rows<Split32, SWIGLU>(a, t, lds);
+}
 
 // A grid of at least `groups`, in two dimensions: one holds fewer than 2^32
 // threads along one.
@@ -394,27 +447,57 @@ dim3 grid_of(int64_t groups) {
   return dim3((unsigned)gx, (unsigned)cdiv(groups, gx));
 }
 
+template <int CB, bool SWIGLU, int EPL>
+hipError_t run_stream(const LaunchCtx& c, const GroupedArgs& a, int64_t experts) {
+  const int ntiles = (int)cdiv(a.N, 64 * CB);
+  HIP_RET((allow_smem_once<grouped_stream_kernel<CB, SWIGLU, EPL>>(kStreamLds<CB>)));
+  MOE_LAUNCH(c, "grouped_product", (grouped_stream_kernel<CB, SWIGLU, EPL>), grid_of((a.R / SROWS + experts) * ntiles),
+             dim3(256), kStreamLds<CB>, a, ntiles);
+  return hipSuccess;
+}
+
 template <bool SWIGLU, int EPL>
 hipError_t run(const LaunchCtx& c, const GroupedArgs& a) {
-  const int64_t experts = std::min<int64_t>(a.E, a.R);
-  if (few_rows(a)) {
-    constexpr int CB = 4;
-    const int ntiles = (int)cdiv(a.N, 64 * CB);
-    HIP_RET((allow_smem_once<grouped_stream_kernel<CB, SWIGLU, EPL>>(kStreamLds<CB>)));
-    MOE_LAUNCH(c, "grouped_product", (grouped_stream_kernel<CB, SWIGLU, EPL>),
-               grid_of((a.R / SROWS + experts) * ntiles), dim3(256), kStreamLds<CB>, a, ntiles);
-  } else {
-    const int ntiles = (int)cdiv(a.N, TN);
-    HIP_RET((allow_smem_once<grouped_tile_kernel<SWIGLU, EPL>>(LDS_BYTES)));
-    MOE_LAUNCH(c, "grouped_product", (grouped_tile_kernel<SWIGLU, EPL>), grid_of((a.R / TM + experts) * ntiles), dim3(NT),
-               LDS_BYTES, a, ntiles);
+  const int64_t experts = std::min<int64_t>(a.E, a.R);  // with rows, at most
+  const auto groups = [&](int rows, int cols) { return std::max<int64_t>(experts, a.R / rows) * cdiv(a.N, cols); };
+  // K over the waves: up to a work-group a CU, and enough of K to share out (us
+  // with tiles of 64 by 128 and with these: 8 rows of 8 experts, K = 2048, N =
+  // 1536, 192 work-groups, 9.9 and 7.4; 100 rows of one, K = N = 2048, 96, 15.3
+  // and 8.6; 16 of 16, 384, 10.1 and 12.3; 4 of one, K = 640, 4.3 and 5.2).
+  if (groups(PROWS, 64) <= 256 && a.K >= 1024) {
+    const int ntiles = (int)cdiv(a.N, 64);
+    HIP_RET((allow_smem_once<grouped_split_kernel<SWIGLU, EPL>>(kSplitLds)));
+    MOE_LAUNCH(c, "grouped_product", (grouped_split_kernel<SWIGLU, EPL>), grid_of((a.R / PROWS + experts) * ntiles),
+               dim3(256), kSplitLds, a, ntiles);
+    return hipSuccess;
   }
+  // tiles of 128 rows: more than 48 rows an expert, and one for each CU (us with
+  // them and with 64 by 256: 64 rows of 128 experts, K = 2048, N = 1536, 83 and
+  // 91, 32 rows 68 and 65; 2000 rows of one, K = N = 4096, 256 work-groups, 64 and
+  // 66; 250 rows of 8, 96, 31 and 25)
+  const bool tall = a.R > 48 * (int64_t)a.E && groups(TM, TN) >= 256;
+  if (!tall) {
+    // 128 columns instead of 256 where those leave CUs without their two
+    // work-groups (56 experts' 64 rows, 336: 22 us and 25; 128, 768: 45 and 44;
+    // 250 rows of 8, 186: 22 and 25)
+    if (groups(SROWS, 256) < 512) return run_stream<2, SWIGLU, EPL>(c, a, experts);
+    return run_stream<4, SWIGLU, EPL>(c, a, experts);
+  }
+  const int ntiles = (int)cdiv(a.N, TN);
+  HIP_RET((allow_smem_once<grouped_tile_kernel<SWIGLU, EPL>>(LDS_BYTES)));
+  MOE_LAUNCH(c, "grouped_product", (grouped_tile_kernel<SWIGLU, EPL>), grid_of((a.R / TM + experts) * ntiles), dim3(NT),
+             LDS_BYTES, a, ntiles);
   return hipSuccess;
 }
 
 }  // namespace
 
-hipError_t launch_grouped(const LaunchCtx& c, const GroupedArgs& a) {
+hipError_t launch_grouped(const LaunchCtx& c, GroupedArgs a) {
+  // Either order of an expert's tiles reads one operand again from the caches:
+  // along the rows' tiles the expert's codes (N K / 2 bytes), along the columns'
+  // its rows (2 K each).  The smaller one (1024 rows an expert, N = 1536: 695 us
+  // with the codes again, 717 with the rows).
+  a.row_major = 4 * (int64_t)a.R >= (int64_t)a.E * a.N;
   if (a.E <= 128) return a.swiglu ? run<true, 2>(c, a) : run<false, 2>(c, a);
   return a.swiglu ? run<true, 16>(c, a) : run<false, 16>(c, a);
 }

@@ -56,6 +56,40 @@ struct Tiles {
   static constexpr int LDS = STAGE * NS;
 };
 
+// One stage's operands of a wave into registers and its products; `col`: the
+// wave's first column in B.  Every read leaves before the first product waits
+// for one.
+template <int RB, int CB>
+__device__ __forceinline__ void stage_products(const lds_t* A, const lds_t* B, const lds_t* scales, int col,
+                                               f32x4_t (&acc)[RB][CB]) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  uint32_t word[CB];
+  u32x4_t code[CB], av[4][RB];
+#pragma unroll
+  for (int c = 0; c < CB; ++c) {
+    const int n = col + 16 * c + r;
+    word[c] = *(const __attribute__((address_space(3))) uint32_t*)(scales + (16 * c + r) * 4);
+    code[c] = lds16(B + n * 64 + ((q ^ (n >> 2)) & 3) * 16);
+  }
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+    for (int b = 0; b < RB; ++b) av[kk][b] = lds16(A + (16 * b + r) * 256 + (((4 * q + kk) ^ r) & 15) * 16);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int c = 0; c < CB; ++c) {
+    const float s = scale_of(word[c], 8 * q);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const bf16x8_t bv = decode8(code[c][kk], s);
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+        acc[b][c] =
+            __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv, __builtin_bit_cast(bf16x8_t, av[kk][b]), acc[b][c], 0, 0, 0);
+    }
+  }
+}
+
 // This lane's sources: row_at(i) is the address of tile row i of the activations,
 // col_at(n) the row of W (among all experts') that column n stands for.
 template <class C>
@@ -103,7 +137,7 @@ struct Stream {
 template <class C>
 __device__ __forceinline__ void products(Stream<C>& st, int stages, lds_t* lds, f32x4_t (&acc)[C::RB][C::CB]) {
   constexpr int NS = C::NS, L = Stream<C>::LOADS;
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4, w = wave_id();
+  const int w = wave_id();
 #pragma unroll
   for (int b = 0; b < C::RB; ++b)
 #pragma unroll
@@ -123,36 +157,122 @@ __device__ __forceinline__ void products(Stream<C>& st, int stages, lds_t* lds, 
     if (behind >= NS - 1) st.issue(lds + (slot == 0 ? NS - 1 : slot - 1) * C::STAGE);
     const lds_t* A = lds + slot * C::STAGE;
     const lds_t* B = A + C::A;
-    // every read leaves before the first product waits for one
-    uint32_t word[C::CB];
-    u32x4_t code[C::CB], av[4][C::RB];
-#pragma unroll
-    for (int c = 0; c < C::CB; ++c) {
-      const int n = 16 * (w * C::CB + c) + r;
-      word[c] = *(const __attribute__((address_space(3))) uint32_t*)(B + C::CODES + w * 256 + (16 * c + r) * 4);
-      code[c] = lds16(B + n * 64 + ((q ^ (n >> 2)) & 3) * 16);
-    }
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-      for (int b = 0; b < C::RB; ++b) av[kk][b] = lds16(A + (16 * b + r) * 256 + (((4 * q + kk) ^ r) & 15) * 16);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int c = 0; c < C::CB; ++c) {
-      const float s = scale_of(word[c], 8 * q);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const bf16x8_t bv = decode8(code[c][kk], s);
-#pragma unroll
-        for (int b = 0; b < C::RB; ++b)
-          acc[b][c] =
-              __builtin_amdgcn_mfma_f32_16x16x32_bf16(bv, __builtin_bit_cast(bf16x8_t, av[kk][b]), acc[b][c], 0, 0, 0);
-      }
-    }
+    stage_products<C::RB, C::CB>(A, B, B + C::CODES + w * 256, 16 * C::CB * w, acc);
     slot = slot + 1 == NS ? 0 : slot + 1;
   }
   wait_lgkm0();
   barrier_lds();  // the slots are free
+}
+
+// ------------------------------------------------------------- K over the waves
+// Where the tiles above are too few to fill the chip: a work-group makes 16 RB
+// rows by 64 columns, its waves taking every fourth stage each in a ring of its
+// own (no barriers), and their sums meet in LDS, in wave order.
+template <int RB_, int NS_>
+struct SplitTiles {
+  static constexpr int RB = RB_, CB = 4, NS = NS_;
+  static constexpr int ROWS = 16 * RB, COLS = 64;
+  static constexpr int A = ROWS * 256, CODES = COLS * 64;
+  static constexpr int STAGE = A + CODES + 256;
+  static constexpr int PARTS = kWaves * RB * CB * 1024;
+  static constexpr int LDS = STAGE * NS * kWaves > PARTS ? STAGE * NS * kWaves : PARTS;
+};
+
+template <class C>
+struct SplitStream {
+  static constexpr int NA = 4 * C::RB, LOADS = NA + 5;
+  const char* pa[NA];
+  const char* pb[4];
+  const char* ps;
+  // At the wave's first stage.
+  template <class RowAt, class ColAt>
+  __device__ __forceinline__ void init(RowAt row_at, ColAt col_at, const uint8_t* codes, const uint8_t* scales, int K) {
+    const int lane = threadIdx.x & 63, w = wave_id();
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const int r = 4 * i + (lane >> 4);
+      pa[i] = row_at(r) + (((lane ^ r) & 15) << 4) + w * 256;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = 16 * i + (lane >> 2);
+      pb[i] = (const char*)codes + col_at(n) * (K / 2) + (((lane ^ (n >> 2)) & 3) << 4) + w * 64;
+    }
+    ps = (const char*)scales + col_at(lane) * (K / 32) + w * 4;
+  }
+  __device__ __forceinline__ void issue(lds_t* slot) {
+    lds_t* const b = slot + C::A;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dma16(pb[i], b + i * 1024);
+      pb[i] += 64 * kWaves;
+    }
+    dma4(ps, b + C::CODES);
+    ps += 4 * kWaves;
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      dma16(pa[i], slot + i * 1024);
+      pa[i] += 256 * kWaves;
+    }
+  }
+};
+
+// The work-group's sums: each wave gets all rows of the 16-column blocks c with
+// keep(wave, c), as products() leaves them; the others' acc hold parts.
+template <class C, class Keep>
+__device__ __forceinline__ void split_products(SplitStream<C>& st, int stages, lds_t* lds, f32x4_t (&acc)[C::RB][4],
+                                               Keep keep) {
+  constexpr int NS = C::NS, L = SplitStream<C>::LOADS;
+  const int w = wave_id(), lane = threadIdx.x & 63;
+  const int mine = (stages - w + kWaves - 1) / kWaves;
+  lds_t* const ring = lds + w * NS * C::STAGE;
+#pragma unroll
+  for (int b = 0; b < C::RB; ++b)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[b][c] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i)
+    if (i < mine) st.issue(ring + i * C::STAGE);
+  int slot = 0;
+  for (int p = 0; p < mine; ++p) {
+    const int behind = mine - 1 - p;
+    wait_lgkm0();  // the slot to be filled has been read
+    if (behind >= NS - 1) st.issue(ring + (slot == 0 ? NS - 1 : slot - 1) * C::STAGE);
+    if (behind >= NS - 1) wait_vmcnt<(NS - 1) * L>();
+    else if (NS > 2 && behind == 1) wait_vmcnt<L>();
+    else wait_vmcnt<0>();
+    asm volatile("" ::: "memory");  // no read moves above the wait
+    const lds_t* A = ring + slot * C::STAGE;
+    const lds_t* B = A + C::A;
+    stage_products<C::RB, 4>(A, B, B + C::CODES, 0, acc);
+    asm volatile("" ::: "memory");
+    slot = slot + 1 == NS ? 0 : slot + 1;
+  }
+  wait_lgkm0();
+  barrier_lds();  // the rings are free
+#pragma unroll
+  for (int b = 0; b < C::RB; ++b)
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *(__attribute__((address_space(3))) f32x4_t*)(lds + ((w * C::RB + b) * 4 + c) * 1024 + lane * 16) = acc[b][c];
+  wait_lgkm0();
+  barrier_lds();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (!keep(w, c)) continue;
+#pragma unroll
+    for (int b = 0; b < C::RB; ++b) {
+      f32x4_t s = {0, 0, 0, 0};
+#pragma unroll
+      for (int v = 0; v < kWaves; ++v) {
+        const f32x4_t x =
+            *(const __attribute__((address_space(3))) f32x4_t*)(lds + ((v * C::RB + b) * 4 + c) * 1024 + lane * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] += x[i];
+      }
+      acc[b][c] = s;
+    }
+  }
 }
 
 }  // namespace mx4
