@@ -1047,12 +1047,13 @@ __global__ __launch_bounds__(kDownRowWaves * 64, F == WF_FP8 && TB == 2 ? 3 : 1)
 // ------------------------------------------------------- e2m1 codes, more tokens
 // With half the bytes of a weight the products above are bound by their own LDS
 // turns and by loads that wait for each other; these are the streaming tiles of
-// mx4tile.h (64 tokens of the layer above: gate/up TIME us and TIME, down TIME
-// and TIME; 200 tokens TIME).  A work-group takes an expert's tokens in blocks of
-// 64 (down: 32, whose two planes of activations are 64 rows).
-template <int RB, int CB> using Tiles4 = mx4::Tiles<RB, CB, RB <= 2 ? 3 : 2>;
+// mx4tile.h (gate/up of the layer above at 64 tokens: 214 MB in 44 us, 4.9 TB/s;
+// 200 tokens of 8 of 64 experts, d = 4096, I = 1024, in all 202 us before, 142).  A
+// work-group takes an expert's tokens in blocks of 64 (down: 32, whose two planes
+// of activations are 64 rows).  CB: 64 CB columns of W a work-group.
+template <int RB, int CB> using Tiles4 = mx4::Tiles<RB, CB, RB <= 2 && CB == 2 ? 2 : 1>;
 template <int CB>
-constexpr int kLds4 = std::max({Tiles4<1, CB>::LDS, Tiles4<2, CB>::LDS, Tiles4<3, CB>::LDS, Tiles4<4, CB>::LDS});
+constexpr int kLds4 = std::max(Tiles4<2, CB>::LDS, Tiles4<4, CB>::LDS);
 
 template <class C>
 __device__ __forceinline__ void gateup4_rows(const DecodeArgs& a, const Rows& rows, int e, int r0, int n, int n0,
@@ -1310,19 +1311,19 @@ hipError_t down4(const LaunchCtx& c, const DecodeArgs& a) {
   return hipSuccess;
 }
 
-// Which products the streaming tiles make.  Gate/up: beyond 16 tokens, with a
-// work-group for each CU (us with the kernels above and with these, d = 2048, I =
-// 768, 8 of 128 experts: 16 tokens 39 and 43, 24 50 and 47, 256 67 and 57; 40
-// tokens of all of 6, d = 1792, I = 512, 24 work-groups: 8 and 14).  Down: where I
-// is long, or a tile's rows are used (8 tokens 20 and 16, 256 58 and 39; 194 of 6
-// of 10, d = 896, I = 128 8.2 and 6.2; 5 of 8 of 113, d = 2304, I = 256 7.9 and
-// 8.9).
+// Which products the streaming tiles make.  Gate/up: with 256 work-groups of 128
+// columns or more, unless the kernel above routes too (us with the kernels above
+// and with these, d = 2048, I = 768, 8 of 128 experts: 4 tokens 16 and 14, 6 21 and
+// 23, 16 42 and 38, 64 60 and 44, 256 67 and 53; 40 tokens of all of 6, d = 1792,
+// I = 512, 48 work-groups, 7 and 14).  Down: where I is long, or a tile's rows are
+// used (8 tokens 20 and 14, 256 58 and 39; 194 of 6 of 10, d = 896, I = 128, 8.2
+// and 6.2; 5 of 8 of 113, d = 2304, I = 256, 7.9 and 8.9).
 hipError_t run4(const LaunchCtx& c, const DecodeArgs& a) {
   const int64_t items = work_items(a);
-  if (a.T > 16 && items * cdiv(2 * a.I, 256) >= 256) {
-    HIP_RET((tile::allow_smem_once<decode_gateup4_kernel<4>>(kLds4<4>)));
-    MOE_LAUNCH(c, "decode_gateup", decode_gateup4_kernel<4>, dim3((unsigned)cdiv(2 * a.I, 256), (unsigned)items),
-               dim3(256), kLds4<4>, a);
+  if (!a.route_inline && items * cdiv(2 * a.I, 256) >= 128) {
+    HIP_RET((tile::allow_smem_once<decode_gateup4_kernel<2>>(kLds4<2>)));
+    MOE_LAUNCH(c, "decode_gateup", decode_gateup4_kernel<2>, dim3((unsigned)cdiv(2 * a.I, 128), (unsigned)items),
+               dim3(256), kLds4<2>, a);
   } else {
     HIP_RET((past_cache<WF_MX4>(a) ? run_gateup<WF_MX4, true>(c, a) : run_gateup<WF_MX4, false>(c, a)));
   }

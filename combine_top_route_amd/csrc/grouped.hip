@@ -305,10 +305,8 @@ __global__ __launch_bounds__(NT, 2) void grouped_tile_kernel(GroupedArgs a, int 
   else tile_rows<4, SWIGLU>(a, t, lds);
 }
 
-// Few rows an expert: tiles of 64 rows (16, 32 or 48 where there are no more) by
+// Few rows an expert: tiles of SROWS rows (16, 32 or 48 where there are no more) by
 // 64 CB columns, or 32 CB gate and the same up columns.
-constexpr int SROWS = 64;
-
 // Row i of a tile (past the segment its last), and the row of W for its column n
 // (past the last that; SWIGLU: 16 gate, the same up, in turn).
 __device__ __forceinline__ const char* row_at(const GroupedArgs& a, const Tile& t, int i) {
@@ -367,17 +365,17 @@ __device__ __forceinline__ void stream_rows(const GroupedArgs& a, const Tile& t,
   }
 }
 
-template <int CB> using Rows16 = mx4::Tiles<1, CB, 3>;
-template <int CB> using Rows32 = mx4::Tiles<2, CB, 3>;
-template <int CB> using Rows48 = mx4::Tiles<3, CB, 2>;
-template <int CB> using Rows64 = mx4::Tiles<4, CB, 2>;
+template <int CB> using Rows16 = mx4::Tiles<1, CB, CB == 2 ? 2 : 1>;
+template <int CB> using Rows32 = mx4::Tiles<2, CB, CB == 2 ? 2 : 1>;
+template <int CB> using Rows48 = mx4::Tiles<3, CB, 1>;
+template <int CB> using Rows64 = mx4::Tiles<4, CB, 1>;
 using Split16 = mx4::SplitTiles<1, 3>;
 using Split32 = mx4::SplitTiles<2, 2>;
 constexpr int kSplitLds = std::max(Split16::LDS, Split32::LDS);
-template <int CB>
-constexpr int kStreamLds = std::max({Rows16<CB>::LDS, Rows32<CB>::LDS, Rows64<CB>::LDS});
+template <int CB, int SROWS>
+constexpr int kStreamLds = std::max({Rows16<CB>::LDS, Rows32<CB>::LDS, SROWS == 64 ? Rows64<CB>::LDS : 0});
 
-template <int CB, bool SWIGLU, int EPL>
+template <int CB, int SROWS, bool SWIGLU, int EPL>
 __global__ __launch_bounds__(256) void grouped_stream_kernel(GroupedArgs a, int ntiles) {
   extern __shared__ __align__(16) char smem[];
   lds_t* lds = (lds_t*)smem;
@@ -385,9 +383,11 @@ __global__ __launch_bounds__(256) void grouped_stream_kernel(GroupedArgs a, int 
   if (!find_tile<EPL>(a, SROWS, ntiles, &t)) return;
   const int rows = t.seg1 - t.m0;
   if (rows <= 16) stream_rows<Rows16<CB>, SWIGLU>(a, t, lds);
-  else if (rows <= 32) stream_rows<Rows32<CB>, SWIGLU>(a, t, lds);
-  else if (rows <= 48) stream_rows<Rows48<CB>, SWIGLU>(a, t, lds);
-  else stream_rows<Rows64<CB>, SWIGLU>(a, t, lds);
+  else if (SROWS == 32 || rows <= 32) stream_rows<Rows32<CB>, SWIGLU>(a, t, lds);
+  else if constexpr (SROWS == 64) {
+    if (rows <= 48) stream_rows<Rows48<CB>, SWIGLU>(a, t, lds);
+    else stream_rows<Rows64<CB>, SWIGLU>(a, t, lds);
+  }
 }
 
 // The same where they would leave the chip idle: 32 rows by 64 columns (32 gate,
@@ -447,12 +447,12 @@ dim3 grid_of(int64_t groups) {
   return dim3((unsigned)gx, (unsigned)cdiv(groups, gx));
 }
 
-template <int CB, bool SWIGLU, int EPL>
+template <int CB, int SROWS, bool SWIGLU, int EPL>
 hipError_t run_stream(const LaunchCtx& c, const GroupedArgs& a, int64_t experts) {
   const int ntiles = (int)cdiv(a.N, 64 * CB);
-  HIP_RET((allow_smem_once<grouped_stream_kernel<CB, SWIGLU, EPL>>(kStreamLds<CB>)));
-  MOE_LAUNCH(c, "grouped_product", (grouped_stream_kernel<CB, SWIGLU, EPL>), grid_of((a.R / SROWS + experts) * ntiles),
-             dim3(256), kStreamLds<CB>, a, ntiles);
+  HIP_RET((allow_smem_once<grouped_stream_kernel<CB, SROWS, SWIGLU, EPL>>(kStreamLds<CB, SROWS>)));
+  MOE_LAUNCH(c, "grouped_product", (grouped_stream_kernel<CB, SROWS, SWIGLU, EPL>),
+             grid_of((a.R / SROWS + experts) * ntiles), dim3(256), (kStreamLds<CB, SROWS>), a, ntiles);
   return hipSuccess;
 }
 
@@ -477,11 +477,15 @@ hipError_t run(const LaunchCtx& c, const GroupedArgs& a) {
   // 66; 250 rows of 8, 96, 31 and 25)
   const bool tall = a.R > 48 * (int64_t)a.E && groups(TM, TN) >= 256;
   if (!tall) {
-    // 128 columns instead of 256 where those leave CUs without their two
-    // work-groups (56 experts' 64 rows, 336: 22 us and 25; 128, 768: 45 and 44;
-    // 250 rows of 8, 186: 22 and 25)
-    if (groups(SROWS, 256) < 512) return run_stream<2, SWIGLU, EPL>(c, a, experts);
-    return run_stream<4, SWIGLU, EPL>(c, a, experts);
+    // 64 rows by 256 columns: more than 20 rows an expert, and one for each CU (us
+    // with them and with 64 by 128: 44 rows of 128, K = 1536, N = 4096, 122 and 133;
+    // 25 of 64, K = 4096, N = 2048, 71 and 75; 16 of 128, K = 2048, N = 1536, 56 and
+    // 50; 2 of 128 49 and 41; 250 of 8, 186 work-groups, 25 and 22)
+    if (a.R > 20 * (int64_t)a.E && groups(64, 256) >= 256) return run_stream<4, 64, SWIGLU, EPL>(c, a, experts);
+    // and 32 by 128 where those are fewer than CUs (75 rows of 8 experts, 108: 17.3
+    // and 15.1; 500 of one, K = N = 2048, 128: 18 and 13; 250 of 8, 372: 22 and 28)
+    if (groups(64, 128) >= 256) return run_stream<2, 64, SWIGLU, EPL>(c, a, experts);
+    return run_stream<2, 32, SWIGLU, EPL>(c, a, experts);
   }
   const int ntiles = (int)cdiv(a.N, TN);
   HIP_RET((allow_smem_once<grouped_tile_kernel<SWIGLU, EPL>>(LDS_BYTES)));

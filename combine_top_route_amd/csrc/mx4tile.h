@@ -3,15 +3,20 @@
 //
 // Four waves make 16 RB rows by 64 CB columns of W, a wave 16 CB of them, in
 // 16x16x32 MFMAs on bf16 (a code times its scale is exact in bfloat16).  What
-// bounds it is the stream of codes, so it is kept in flight: a stage is 128
-// values of K (64 bytes and four scales of each column, 256 bytes of each row),
-// moved by direct loads into a ring of NS slots, NS - 1 ahead, one barrier a
-// stage, two or three work-groups a CU.  The K order inside a stage suits the
-// codes: a quarter of a wave takes a 16-byte piece of its column (32 codes, one
-// scale), whose four words are four MFMA operands.  Next to the stream the LDS
-// reads are what costs: each wave reads all rows and its own columns, so it
-// takes as many columns as leave enough work-groups (RB CB products for RB + CB
-// operands).
+// bounds it is the stream of codes, moved by direct loads: a stage is H times 128
+// values of K (64 bytes of each column, 256 of each row), loaded one stage ahead,
+// one barrier a stage, two or three work-groups a CU.  The K order inside 128
+// values suits the codes: a quarter of a wave takes a 16-byte piece of its column
+// (32 codes, one scale), whose four words are four MFMA operands.
+//
+// What it measured at 33 tokens of 8 of 128 experts, K = 2048, N = 1536 (188 MB of
+// codes and scales): 57 us with 32x32x16 products of 32 columns a wave, whose rows
+// are read from LDS once for two products; 47 with these, 64 columns a wave; 44
+// with three slots of one 128-value stage; 41 with H = 2 and 128 columns a
+// work-group, 4.6 TB/s: both halves of a 128-byte line are asked for together (a
+// kernel that only loads reads 4.7 TB/s in 64-byte pieces of 256 rows 2 KB apart,
+// and 6.0 in 128-byte ones of 128).  Where more rows leave LDS for 128 values only
+// (RB > 2), wider tiles pay instead.
 #pragma once
 
 #include "common.h"
@@ -46,29 +51,32 @@ __device__ __forceinline__ bf16x8_t decode8(uint32_t c, float s) {
 
 constexpr int kWaves = 4;
 
-template <int RB_, int CB_, int NS_>
+// Two slots of a stage.  The scales are kept apart, four words of a column together
+// (512 values), in two buffers: a load of one word from each of 64 columns costs
+// the vector memory unit as much as 1 KB of codes.
+template <int RB_, int CB_, int H_>
 struct Tiles {
-  static constexpr int RB = RB_, CB = CB_, NS = NS_;
+  static constexpr int RB = RB_, CB = CB_, H = H_;
   static constexpr int ROWS = 16 * RB, COLS = 64 * CB;
   static constexpr int A = ROWS * 256, CODES = COLS * 64;
-  static constexpr int SCALES = 256 * kWaves;  // a word a column, 64 a wave (with 32 columns: twice)
-  static constexpr int STAGE = A + CODES + SCALES;
-  static constexpr int LDS = STAGE * NS;
+  static constexpr int HALF = A + CODES, STAGE = H * HALF;
+  static constexpr int SCALES = COLS * 16;
+  static constexpr int LDS = 2 * (STAGE + SCALES);
 };
 
 // One stage's operands of a wave into registers and its products; `col`: the
-// wave's first column in B.  Every read leaves before the first product waits
-// for one.
+// wave's first column in B, whose scale word is at `scales`.  Every read leaves
+// before the first product waits for one.
 template <int RB, int CB>
 __device__ __forceinline__ void stage_products(const lds_t* A, const lds_t* B, const lds_t* scales, int col,
-                                               f32x4_t (&acc)[RB][CB]) {
+                                               int scale_stride, f32x4_t (&acc)[RB][CB]) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   uint32_t word[CB];
   u32x4_t code[CB], av[4][RB];
 #pragma unroll
   for (int c = 0; c < CB; ++c) {
     const int n = col + 16 * c + r;
-    word[c] = *(const __attribute__((address_space(3))) uint32_t*)(scales + (16 * c + r) * 4);
+    word[c] = *(const __attribute__((address_space(3))) uint32_t*)(scales + (16 * c + r) * scale_stride);
     code[c] = lds16(B + n * 64 + ((q ^ (n >> 2)) & 3) * 16);
   }
 #pragma unroll
@@ -94,71 +102,83 @@ __device__ __forceinline__ void stage_products(const lds_t* A, const lds_t* B, c
 // col_at(n) the row of W (among all experts') that column n stands for.
 template <class C>
 struct Stream {
-  // 1 KB of rows a load, dealt to the waves; a single KB's other waves load it again
-  static constexpr int NA = C::RB, LOADS = C::RB + C::CB + 1;
-  const char* pa[NA];
+  const char* pa[C::RB];
   const char* pb[C::CB];
-  const char* ps;
+  const char* ps[C::CB];
   template <class RowAt, class ColAt>
   __device__ __forceinline__ void init(RowAt row_at, ColAt col_at, const uint8_t* codes, const uint8_t* scales, int K) {
     const int lane = threadIdx.x & 63, w = wave_id();
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
+    for (int i = 0; i < C::CB; ++i) {
+      const int n = 16 * (w * C::CB + i) + (lane >> 2);
+      const int64_t at = col_at(n);
+      pb[i] = (const char*)codes + at * (K / 2) + (((lane ^ (n >> 2)) & 3) << 4);
+      ps[i] = (const char*)scales + at * (K / 32);
+    }
+#pragma unroll
+    for (int i = 0; i < C::RB; ++i) {
       const int r = 4 * (w + kWaves * i) + (lane >> 4);
       pa[i] = row_at(r) + (((lane ^ r) & 15) << 4);
     }
-#pragma unroll
-    for (int i = 0; i < C::CB; ++i) {
-      const int n = 16 * (w * C::CB + i) + (lane >> 2);
-      pb[i] = (const char*)codes + col_at(n) * (K / 2) + (((lane ^ (n >> 2)) & 3) << 4);
-    }
-    ps = (const char*)scales + col_at(16 * C::CB * w + (lane & (16 * C::CB - 1))) * (K / 32);
   }
-  __device__ __forceinline__ void issue(lds_t* slot) {
+  // Words 4 g .. of 16 of the wave's columns (past the row's end its last word).
+  __device__ __forceinline__ void scales(int i, int g, int stages, lds_t* buffer) const {
+    const int word = min(4 * g + (int)(threadIdx.x & 3), stages - 1);
+    dma4(ps[i] + 4 * word, buffer + (wave_id() * C::CB + i) * 256);
+  }
+  // `halves` of H: the last stage may be short.
+  __device__ __forceinline__ void issue(lds_t* slot, int halves) {
     const int w = wave_id();
-    lds_t* const b = slot + C::A;
 #pragma unroll
     for (int i = 0; i < C::CB; ++i) {
-      dma16(pb[i], b + (w * C::CB + i) * 1024);
-      pb[i] += 64;
-    }
-    dma4(ps, b + C::CODES + w * 256);
-    ps += 4;
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      dma16(pa[i], slot + (w + kWaves * i) * 1024);
-      pa[i] += 256;
+      for (int h = 0; h < C::H; ++h)
+        if (h < halves) dma16(pb[i] + 64 * h, slot + h * C::HALF + C::A + (w * C::CB + i) * 1024);
+      pb[i] += 64 * C::H;
+    }
+#pragma unroll
+    for (int i = 0; i < C::RB; ++i) {
+#pragma unroll
+      for (int h = 0; h < C::H; ++h)
+        if (h < halves) dma16(pa[i] + 256 * h, slot + h * C::HALF + (w + kWaves * i) * 1024);
+      pa[i] += 256 * C::H;
     }
   }
 };
 
 // acc[b][c]: lane l has row 16 b + l % 16; register v the wave's column 16 c +
-// 4 (l / 16) + v.
+// 4 (l / 16) + v.  units: K / 128.
 template <class C>
-__device__ __forceinline__ void products(Stream<C>& st, int stages, lds_t* lds, f32x4_t (&acc)[C::RB][C::CB]) {
-  constexpr int NS = C::NS, L = Stream<C>::LOADS;
-  const int w = wave_id();
+__device__ __forceinline__ void products(Stream<C>& st, int units, lds_t* lds, f32x4_t (&acc)[C::RB][C::CB]) {
+  constexpr int H = C::H, PER = 4 / H;  // stages a group of scale words
+  static_assert(C::CB % PER == 0 || C::CB < PER, "");
+  const int w = wave_id(), stages = (units + H - 1) / H;
+  lds_t* const words = lds + 2 * C::STAGE;
 #pragma unroll
   for (int b = 0; b < C::RB; ++b)
 #pragma unroll
     for (int c = 0; c < C::CB; ++c) acc[b][c] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < NS - 1; ++i)
-    if (i < stages) st.issue(lds + i * C::STAGE);
-  int slot = 0;
+  for (int i = 0; i < C::CB; ++i) st.scales(i, 0, units, words);
+  st.issue(lds, units);
   for (int p = 0; p < stages; ++p) {
-    // loads land in the order they left: all but those of the stages behind
-    const int behind = stages - 1 - p;
-    if (behind >= NS - 2) wait_vmcnt<(NS - 2) * L>();
-    else if (NS > 3 && behind == 1) wait_vmcnt<L>();
-    else wait_vmcnt<0>();
-    wait_lgkm0();  // and the slot to be filled has been read
+    const int g = p / PER;
+    wait_vmcnt<0>();
+    wait_lgkm0();  // the slot and the buffer to be filled have been read
     barrier_lds();
-    if (behind >= NS - 1) st.issue(lds + (slot == 0 ? NS - 1 : slot - 1) * C::STAGE);
-    const lds_t* A = lds + slot * C::STAGE;
-    const lds_t* B = A + C::A;
-    stage_products<C::RB, C::CB>(A, B, B + C::CODES + w * 256, 16 * C::CB * w, acc);
-    slot = slot + 1 == NS ? 0 : slot + 1;
+    if (p + 1 < stages) {
+      // with each stage's loads some of the next group's words
+#pragma unroll
+      for (int i = 0; i < C::CB; ++i)
+        if (p % PER == i % PER) st.scales(i, g + 1, units, words + ((g & 1) ^ 1) * C::SCALES);
+      st.issue(lds + ((p & 1) ^ 1) * C::STAGE, units - (p + 1) * H);
+    }
+    const lds_t* A = lds + (p & 1) * C::STAGE;
+    const lds_t* word = words + (g & 1) * C::SCALES + w * C::CB * 256 + (p % PER) * H * 4;
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+      if (h == 0 || p * H + h < units)
+        stage_products<C::RB, C::CB>(A + h * C::HALF, A + h * C::HALF + C::A, word + h * 4, 16 * C::CB * w, 16, acc);
   }
   wait_lgkm0();
   barrier_lds();  // the slots are free
@@ -244,7 +264,7 @@ __device__ __forceinline__ void split_products(SplitStream<C>& st, int stages, l
     asm volatile("" ::: "memory");  // no read moves above the wait
     const lds_t* A = ring + slot * C::STAGE;
     const lds_t* B = A + C::A;
-    stage_products<C::RB, 4>(A, B, B + C::CODES, 0, acc);
+    stage_products<C::RB, 4>(A, B, B + C::CODES, 0, 4, acc);
     asm volatile("" ::: "memory");
     slot = slot + 1 == NS ? 0 : slot + 1;
   }
