@@ -190,37 +190,67 @@ __global__ __launch_bounds__(kThreads<L>) void norm_bwd_kernel(NormArgs a) {
   __shared__ float part[2][48];
   __shared__ __align__(16) float col[ROWS > 1 ? ROWS * L * N : 1];
   const int lane = threadIdx.x % L, sub = threadIdx.x / L, vecs = a.d / N;
-  u32x4_t wp[NV], wn[NV], gv[NV];
-  if (a.w_post) load_row<L>(wp, (const u32x4_t*)a.w_post, lane, vecs);
-  if (a.gate_kind == 1) load_row<L>(gv, (const u32x4_t*)a.gate, lane, vecs);
-  if (a.w_next) load_row<L>(wn, (const u32x4_t*)a.w_next, lane, vecs);
+  // 32 columns a lane leave no registers for the weights and the next row, which
+  // are then read where they are used (2048 rows of 16384 in bf16: 302 us with
+  // them spilled, TIME)
+  constexpr bool LEAN = NV * N >= 32;
+  constexpr int KEPT = LEAN ? 1 : NV;
+  u32x4_t wp_[KEPT], wn_[KEPT], gv_[KEPT];
+  if constexpr (!LEAN) {
+    if (a.w_post) load_row<L>(wp_, (const u32x4_t*)a.w_post, lane, vecs);
+    if (a.gate_kind == 1) load_row<L>(gv_, (const u32x4_t*)a.gate, lane, vecs);
+    if (a.w_next) load_row<L>(wn_, (const u32x4_t*)a.w_next, lane, vecs);
+  }
+  const auto weight = [&](const u32x4_t (&kept)[KEPT], const void* p, int i) {
+    if constexpr (LEAN) return lane + i * L < vecs ? ((const u32x4_t*)p)[lane + i * L] : u32x4_t{0, 0, 0, 0};
+    else return kept[i];
+  };
   float A[NV][N], B[NV][N];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < N; ++j) A[i][j] = B[i][j] = 0.0f;
-  for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < a.T; row0 += (int64_t)gridDim.x * ROWS) {
+  // the next row is on its way while one is worked on (16384 rows of 2048: 83 us, 92
+  // without)
+  struct In {
+    u32x4_t dz[NV], dh[NV], z[NV], y[NV];
+    float gt;
+  };
+  const auto load = [&](In& in, int64_t row) {
+    const int mine = row < a.T ? vecs : 0;
+    const int64_t at = row * vecs;
+    if (a.dz) load_row<L>(in.dz, (const u32x4_t*)a.dz + at, lane, mine);
+    if (a.w_next) {
+      load_row<L>(in.dh, (const u32x4_t*)a.dh + at, lane, mine);
+      load_row<L>(in.z, (const u32x4_t*)a.z_in + at, lane, mine);
+    }
+    if (a.y) load_row<L>(in.y, (const u32x4_t*)a.y + at, lane, mine);
+    in.gt = a.gate_kind == 2 && row < a.T ? to_f32<T>(((const T*)a.gate)[row]) : 1.0f;
+  };
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  In next;
+  if constexpr (!LEAN) load(next, (int64_t)blockIdx.x * ROWS + sub);
+  for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < a.T; row0 += step) {
     const int64_t row = row0 + sub, at = row * vecs;
     const bool in = row < a.T;
     const int mine = in ? vecs : 0;
-    u32x4_t dzv[NV], dhv[NV], zv[NV], yv[NV];
-    if (a.dz) load_row<L>(dzv, (const u32x4_t*)a.dz + at, lane, mine);
-    if (a.w_next) {
-      load_row<L>(dhv, (const u32x4_t*)a.dh + at, lane, mine);
-      load_row<L>(zv, (const u32x4_t*)a.z_in + at, lane, mine);
-    }
-    if (a.y) load_row<L>(yv, (const u32x4_t*)a.y + at, lane, mine);
-    const float gt = a.gate_kind == 2 && in ? to_f32<T>(((const T*)a.gate)[row]) : 1.0f;
+    if constexpr (LEAN) load(next, row);
+    const In now = next;
+    if constexpr (!LEAN) load(next, row + step);
+    const auto &dzv = now.dz, &dhv = now.dh, &zv = now.z, &yv = now.y;
+    const float gt = now.gt;
     float s[3] = {0.0f, 0.0f, 0.0f};  // z^2, t z, y^2
     if (a.w_next) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int i = 0; i < NV; ++i) {
+        const u32x4_t wn = weight(wn_, a.w_next, i);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           const float z = Row<T>::get(zv[i], j);
           s[0] = fmaf(z, z, s[0]);
-          s[1] = fmaf(Row<T>::get(dhv[i], j) * Row<T>::get(wn[i], j), z, s[1]);
+          s[1] = fmaf(Row<T>::get(dhv[i], j) * Row<T>::get(wn, j), z, s[1]);
         }
+      }
     }
     if (a.w_post) {
 #pragma unroll
@@ -239,13 +269,17 @@ __global__ __launch_bounds__(kThreads<L>) void norm_bwd_kernel(NormArgs a) {
     float q[1] = {0.0f};  // g w_post gate_c y
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      u32x4_t wn, wp, gv;
+      if (a.w_next) wn = weight(wn_, a.w_next, i);
+      if (a.w_post) wp = weight(wp_, a.w_post, i);
+      if (a.gate_kind == 1) gv = weight(gv_, a.gate, i);
       float o[N];
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         float v = a.dz ? Row<T>::get(dzv[i], j) : 0.0f;
         if (a.w_next) {
           const float dh = Row<T>::get(dhv[i], j), zh = Row<T>::get(zv[i], j) * rz;
-          v += rz * (dh * Row<T>::get(wn[i], j) - zh * mz);
+          v += rz * (dh * Row<T>::get(wn, j) - zh * mz);
           A[i][j] = fmaf(dh, zh, A[i][j]);
         }
         o[j] = a.scale * v;
@@ -253,8 +287,8 @@ __global__ __launch_bounds__(kThreads<L>) void norm_bwd_kernel(NormArgs a) {
           if (a.y) {
             const float y = Row<T>::get(yv[i], j);
             B[i][j] = fmaf(v * gt, y * ry, B[i][j]);
-            if (a.w_post) v *= Row<T>::get(wp[i], j);
-            if (a.gate_kind == 1) v *= Row<T>::get(gv[i], j);
+            if (a.w_post) v *= Row<T>::get(wp, j);
+            if (a.gate_kind == 1) v *= Row<T>::get(gv, j);
             q[0] = fmaf(v, y, q[0]);
           }
         }
@@ -332,6 +366,7 @@ __global__ __launch_bounds__(256) void norm_join_kernel(NormArgs a, int groups) 
     const int per = (groups + SL - 1) / SL;
     const int g1 = min(groups, (slice + 1) * per);
     const float* p = a.parts + (q >> 2) * a.d + c;
+#pragma unroll 8
     for (int g = slice * per; g < g1; ++g) {
       const f32x4_t v = *(const f32x4_t*)(p + (int64_t)g * 2 * a.d);
 #pragma unroll
@@ -355,7 +390,11 @@ __global__ __launch_bounds__(256) void norm_join_kernel(NormArgs a, int groups) 
 struct Spread {
   int L, NV;
 };
-Spread spread_of(int64_t T, int vecs) {
+
+// Forward: one piece a lane for few rows (one of 2048 values: 4.1 us, with four
+// 5.0); for many, a wave a row while four pieces hold it (16384 rows of 2048 in
+// bf16: 46 us with four waves a row, 43 with one).
+Spread fwd_spread(int64_t T, int vecs) {
   Spread p = {8, 1};
   const int most = T >= 2048 ? 4 : 1;
   while (p.L * p.NV < vecs) {
@@ -366,10 +405,25 @@ Spread spread_of(int64_t T, int vecs) {
   return p;
 }
 
-// Work-groups of the backward (of which each leaves a part of the column sums).
+// Backward: a row's four operands, the next row's and the two column sums take the
+// registers, so one piece a lane up to eight waves a row (8192 rows of 4096: 81 us,
+// with two pieces 89, with four 101; 2048 of 8192, eight waves and two pieces 47,
+// sixteen and one 63).
+Spread bwd_spread(int vecs) {
+  Spread p = {8, 1};
+  while (p.L * p.NV < vecs) {
+    if (p.L < 512) p.L *= 2;
+    else p.NV *= 2;
+  }
+  return p;
+}
+
+// Work-groups of the backward, of which each leaves a part of the column sums:
+// eight waves a CU (16384 rows of 2048: 83 us, with four 120, with sixteen 96 and
+// twice the parts to join).
 int64_t bwd_groups(int64_t T, Spread p) {
-  const int rows = (p.L > 256 ? p.L : 256) / p.L;
-  return std::min<int64_t>(cdiv(T, rows), 512);
+  const int threads = p.L > 256 ? p.L : 256;
+  return std::min<int64_t>(cdiv(T, threads / p.L), 256 * 512 / threads);
 }
 
 template <typename T, int L, int NV>
@@ -387,40 +441,52 @@ hipError_t run_bwd(const LaunchCtx& c, const NormArgs& a) {
   return hipSuccess;
 }
 
+#define CASE(RUN, l, nv) \
+  if (p.L == l && p.NV == nv) return RUN<T, l, nv>(c, a)
+#define UP_TO_512(RUN) \
+  CASE(RUN, 8, 1);     \
+  CASE(RUN, 16, 1);    \
+  CASE(RUN, 32, 1);    \
+  CASE(RUN, 64, 1);    \
+  CASE(RUN, 128, 1);   \
+  CASE(RUN, 256, 1);   \
+  CASE(RUN, 512, 1)
 template <typename T>
-hipError_t run(const LaunchCtx& c, const NormArgs& a, bool fwd) {
-  const Spread p = spread_of(a.T, a.d / Row<T>::N);
-#define CASE(l, nv) \
-  if (p.L == l && p.NV == nv) return fwd ? run_fwd<T, l, nv>(c, a) : run_bwd<T, l, nv>(c, a)
-  CASE(8, 1);
-  CASE(16, 1);
-  CASE(32, 1);
-  CASE(64, 1);
-  CASE(64, 2);
-  CASE(64, 4);
-  CASE(128, 1);
-  CASE(128, 4);
-  CASE(256, 1);
-  CASE(256, 4);
-  CASE(512, 1);
-  CASE(512, 4);
-  CASE(1024, 1);
-  CASE(1024, 2);
-  CASE(1024, 4);
-#undef CASE
+hipError_t fwd(const LaunchCtx& c, const NormArgs& a) {
+  const Spread p = fwd_spread(a.T, a.d / Row<T>::N);
+  UP_TO_512(run_fwd);
+  CASE(run_fwd, 1024, 1);
+  CASE(run_fwd, 64, 2);
+  CASE(run_fwd, 1024, 2);
+  CASE(run_fwd, 64, 4);
+  CASE(run_fwd, 128, 4);
+  CASE(run_fwd, 256, 4);
+  CASE(run_fwd, 512, 4);
+  CASE(run_fwd, 1024, 4);
   return hipErrorInvalidValue;
 }
+template <typename T>
+hipError_t bwd(const LaunchCtx& c, const NormArgs& a) {
+  const Spread p = bwd_spread(a.d / Row<T>::N);
+  UP_TO_512(run_bwd);
+  CASE(run_bwd, 512, 2);
+  CASE(run_bwd, 512, 4);
+  if constexpr (sizeof(T) == 4) CASE(run_bwd, 512, 8);
+  return hipErrorInvalidValue;
+}
+#undef UP_TO_512
+#undef CASE
 
 }  // namespace
 
 int64_t norm_bwd_groups(int64_t T, int64_t d, int dtype) {
-  return bwd_groups(T, spread_of(T, (int)(d / (dtype == F32 ? 4 : 8))));
+  return bwd_groups(T, bwd_spread((int)(d / (dtype == F32 ? 4 : 8))));
 }
 hipError_t launch_norm_fwd(const LaunchCtx& c, const NormArgs& a) {
-  return a.dtype == F32 ? run<float>(c, a, true) : run<bf16_t>(c, a, true);
+  return a.dtype == F32 ? fwd<float>(c, a) : fwd<bf16_t>(c, a);
 }
 hipError_t launch_norm_bwd(const LaunchCtx& c, const NormArgs& a) {
-  return a.dtype == F32 ? run<float>(c, a, false) : run<bf16_t>(c, a, false);
+  return a.dtype == F32 ? bwd<float>(c, a) : bwd<bf16_t>(c, a);
 }
 
 }  // namespace moe
