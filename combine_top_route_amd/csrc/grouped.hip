@@ -250,7 +250,8 @@ __device__ __forceinline__ void mainloop(Loads<TMX>& ld, int pairs, lds_t* lds, 
 }
 
 // Accumulators: lane l has row i * 32 + l % 32 of the tile; register v the wave's
-// column j * 32 + 8 (v / 4) + 4 (l / 32) + v % 4.  They leave through LDS.
+// column j * 32 + 8 (v / 4) + 4 (l / 32) + v % 4.  They leave through LDS, by
+// non-temporal stores (131072 rows of 256 by 1024: 111 us without, 92 with).
 template <int TMX, bool SWIGLU>
 __device__ __forceinline__ void tile_rows(const GroupedArgs& a, const Tile& t, lds_t* lds) {
   constexpr int COLS = SWIGLU ? TN / 2 : TN, S = COLS * 2 + 16;
@@ -288,7 +289,8 @@ __device__ __forceinline__ void tile_rows(const GroupedArgs& a, const Tile& t, l
   for (int q = threadIdx.x; q < TMX * 32 * CPR; q += NT) {
     const int row = q / CPR, c = c0 + (q % CPR) * 8;
     if (t.m0 + row < t.seg1 && c < width)
-      *(u32x4_t*)((bf16_t*)a.y + (int64_t)(t.m0 + row) * width + c) = lds16(lds + row * S + (q % CPR) * 16);
+      __builtin_nontemporal_store(lds16(lds + row * S + (q % CPR) * 16),
+                                  (u32x4_t*)((bf16_t*)a.y + (int64_t)(t.m0 + row) * width + c));
   }
 }
 
@@ -361,7 +363,8 @@ __device__ __forceinline__ void stream_rows(const GroupedArgs& a, const Tile& t,
   for (int i = threadIdx.x; i < C::ROWS * CPR; i += 256) {
     const int row = i / CPR, c = c0 + (i % CPR) * 8;
     if (t.m0 + row < t.seg1 && c < width)
-      *(u32x4_t*)((bf16_t*)a.y + (int64_t)(t.m0 + row) * width + c) = lds16(lds + row * S + (i % CPR) * 16);
+      __builtin_nontemporal_store(lds16(lds + row * S + (i % CPR) * 16),
+                                  (u32x4_t*)((bf16_t*)a.y + (int64_t)(t.m0 + row) * width + c));
   }
 }
 

@@ -97,10 +97,13 @@ __device__ __forceinline__ void row_sums(float (&v)[NS], float* part) {
 template <int L> constexpr int kThreads = L > 256 ? L : 256;
 
 // NV pieces of a row of `vecs`, this lane's; zeros past the end.
-template <int L, int NV>
+template <int L, int NV, bool NT = false>
 __device__ __forceinline__ void load_row(u32x4_t (&v)[NV], const u32x4_t* p, int lane, int vecs) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = lane + i * L < vecs ? p[lane + i * L] : u32x4_t{0, 0, 0, 0};
+  for (int i = 0; i < NV; ++i) {
+    v[i] = u32x4_t{0, 0, 0, 0};
+    if (lane + i * L < vecs) v[i] = NT ? __builtin_nontemporal_load(p + lane + i * L) : p[lane + i * L];
+  }
 }
 
 __device__ __forceinline__ float rstd_of(float squares, const NormArgs& a) {
@@ -184,7 +187,8 @@ __device__ __forceinline__ void column_finish(const NormArgs& a, int c, float A,
   if (a.gate_kind == 1) ((T*)a.dgate)[c] = from_f32<T>(a.w_post ? B * to_f32<T>(((const T*)a.w_post)[c]) : B);
 }
 
-template <typename T, int L, int NV>
+// NT: the rows are loaded past the caches.
+template <typename T, int L, int NV, bool NT>
 __global__ __launch_bounds__(kThreads<L>) void norm_bwd_kernel(NormArgs a) {
   constexpr int N = Row<T>::N, ROWS = kThreads<L> / L;
   __shared__ float part[2][48];
@@ -219,12 +223,12 @@ __global__ __launch_bounds__(kThreads<L>) void norm_bwd_kernel(NormArgs a) {
   const auto load = [&](In& in, int64_t row) {
     const int mine = row < a.T ? vecs : 0;
     const int64_t at = row * vecs;
-    if (a.dz) load_row<L>(in.dz, (const u32x4_t*)a.dz + at, lane, mine);
+    if (a.dz) load_row<L, NV, NT>(in.dz, (const u32x4_t*)a.dz + at, lane, mine);
     if (a.w_next) {
-      load_row<L>(in.dh, (const u32x4_t*)a.dh + at, lane, mine);
-      load_row<L>(in.z, (const u32x4_t*)a.z_in + at, lane, mine);
+      load_row<L, NV, NT>(in.dh, (const u32x4_t*)a.dh + at, lane, mine);
+      load_row<L, NV, NT>(in.z, (const u32x4_t*)a.z_in + at, lane, mine);
     }
-    if (a.y) load_row<L>(in.y, (const u32x4_t*)a.y + at, lane, mine);
+    if (a.y) load_row<L, NV, NT>(in.y, (const u32x4_t*)a.y + at, lane, mine);
     in.gt = a.gate_kind == 2 && row < a.T ? to_f32<T>(((const T*)a.gate)[row]) : 1.0f;
   };
   const int64_t step = (int64_t)gridDim.x * ROWS;
@@ -435,7 +439,14 @@ hipError_t run_fwd(const LaunchCtx& c, const NormArgs& a) {
 template <typename T, int L, int NV>
 hipError_t run_bwd(const LaunchCtx& c, const NormArgs& a) {
   const int groups = (int)bwd_groups(a.T, {L, NV});
-  MOE_LAUNCH(c, "norm_backward", (norm_bwd_kernel<T, L, NV>), dim3((unsigned)groups), dim3(kThreads<L>), 0, a);
+  // rows beyond the last-level cache leave it alone (16384 rows of 2048, 402 MB: 82
+  // us without, 77 with, 81 with the stores too; below its size they may be there from the step before:
+  // 4096 rows 27.7 and 29.1)
+  const int64_t rows = 2 + 2 * (a.w_next != nullptr) + 2 * (a.dy != nullptr);
+  if (rows * a.T * a.d * (int64_t)sizeof(T) > (int64_t(256) << 20))
+    MOE_LAUNCH(c, "norm_backward", (norm_bwd_kernel<T, L, NV, true>), dim3((unsigned)groups), dim3(kThreads<L>), 0, a);
+  else
+    MOE_LAUNCH(c, "norm_backward", (norm_bwd_kernel<T, L, NV, false>), dim3((unsigned)groups), dim3(kThreads<L>), 0, a);
   if (groups > 1 && (a.dw_next || a.dw_post || a.gate_kind == 1))
     MOE_LAUNCH(c, "norm_join", norm_join_kernel<T>, dim3((unsigned)cdiv(a.d, 16)), dim3(256), 0, a, groups);
   return hipSuccess;
