@@ -88,6 +88,38 @@ def test_products(name, N, K, gather, swiglu):
     near(got, *reference(x, w, r, k, gather, swiglu, limit))
 
 
+# enough work-groups for the larger tiles: 64 rows by 256 columns, then 128 by 256
+# (segments around each tile height, none, several tiles, K of one to five times
+# 128), and 64 by 128; more experts than 128
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("K", [128, 256, 384, 640])
+@pytest.mark.parametrize("E,mean,N", [(64, 30, 1040), (130, 33, 528), (66, 90, 1040), (140, 75, 528), (300, 7, 144)])
+def test_many(E, mean, N, K, swiglu):
+    g = torch.Generator().manual_seed(E + K)
+    counts = torch.poisson(torch.full((E,), float(mean)), generator=g).long().tolist()
+    edges = [0, 1, 15, 16, 17, 31, 32, 33, 48, 49, 63, 64, 65, 95, 96, 97, 127, 128, 129, 257]
+    counts[:len(edges)] = edges
+    k = 2
+    counts[-1] += sum(counts) % k
+    r = routing(counts, k, seed=E)
+    R = sum(counts)
+    w = weight(E, N, K, seed=N)
+    x = torch.randn((R // k, K), generator=torch.Generator(device=DEV).manual_seed(K), device=DEV).bfloat16()
+    near(B.grouped_product(x, w, r, R // k, k, swiglu=swiglu), *reference(x, w, r, k, True, swiglu, 0.0))
+
+
+# K over the waves: every number of stages a wave from none to four, one or two
+# blocks of 16 rows
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("K", [1024, 1152, 1280, 1408, 2048])
+def test_split(K, swiglu):
+    counts, k, N = [3, 0, 16, 17, 32, 33, 1, 2], 8, 208
+    r, w = routing(counts, k), weight(8, N, K, seed=K)
+    R = sum(counts)
+    x = torch.randn((R // k, K), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).bfloat16()
+    near(B.grouped_product(x, w, r, R // k, k, swiglu=swiglu), *reference(x, w, r, k, True, swiglu, 0.0))
+
+
 @pytest.mark.parametrize("N", [8, 24, 248, 264])
 def test_narrow(N):
     r = routing([5, 70, 0, 300, 1], 4)
@@ -96,7 +128,8 @@ def test_narrow(N):
 
 
 @pytest.mark.parametrize("swiglu", [False, True])
-@pytest.mark.parametrize("counts,k", [([20] * 30, 4), ([300, 0, 500], 2), ([1, 2, 3, 2], 2)])
+@pytest.mark.parametrize("counts,k", [([20] * 30, 4), ([300, 0, 500], 2), ([1, 2, 3, 2], 2), ([70] * 140, 4),
+                                      ([30] * 140, 4)])
 def test_rows_behind_and_odd_offsets(counts, k, swiglu):
     """Rows of no expert are left as they were; offsets outside or out of order
     reach no memory but y's rows."""
@@ -116,7 +149,8 @@ def test_rows_behind_and_odd_offsets(counts, k, swiglu):
     assert bool((pad[R:] == 5).all())
 
 
-@pytest.mark.parametrize("counts,k", [([3, 0, 5, 4], 2), ([200, 90, 0, 34], 4), ([12] * 40, 8)])
+@pytest.mark.parametrize("counts,k", [([3, 0, 5, 4], 2), ([200, 90, 0, 34], 4), ([12] * 40, 8), ([68] * 140, 8),
+                                      ([28] * 140, 8)])
 def test_nan_and_infinity_stay_where_they_are(counts, k):
     E, R, N, K = len(counts), sum(counts), 272, 384
     r = routing(counts, k)

@@ -130,6 +130,44 @@ def test_ids_with_empty_slots_and_repeats(T, d, E, k, I):
     assert not bool(got[T // 2].any())
 
 
+# gate/up in 128-column tiles from 256 of them on (more experts than slots, and
+# fewer), down in tiles of 128 and of 256; an expert with every token, one with
+# none, one with 20; d and I of one and of odd numbers of 128
+@pytest.mark.parametrize("T,d,E,k,I", [(256, 128, 64, 4, 256), (200, 384, 128, 5, 128), (70, 640, 40, 6, 512),
+                                       (9, 256, 200, 3, 384), (100, 1152, 128, 8, 640), (33, 1024, 130, 2, 128),
+                                       (256, 2176, 33, 3, 512), (17, 256, 128, 8, 1152)])
+def test_tiles(T, d, E, k, I):
+    x, wgu, wd, logits = make(T, d, E, k, I, seed=6)
+    logits[:, 5] = 9.0
+    logits[:, 7] = -9.0
+    logits[:20, 2] = 8.0
+    logits[20:, 2] = -9.0
+    dec = decoder(x, E, k, I, limit=1.25)
+    got = dec.forward(x, wgu, wd, logits=logits)
+    ids, w = topk64(logits, k)
+    assert torch.equal(dec.topk_ids.long(), ids)
+    a, b, used = cut(wgu, wd, ids)
+    check(got, x, a, b, used, w, limit=1.25)
+    again = decoder(x, E, k, I, limit=1.25)
+    assert torch.equal(again.forward(x, wgu, wd, logits=logits), got)
+
+
+@pytest.mark.parametrize("T", [40, 200])
+def test_nan_stays_in_its_tokens(T):
+    d, E, k, I = 256, 128, 2, 256
+    x, wgu, wd, _ = make(T, d, E, k, I, seed=9)
+    ids = (torch.arange(T, device=DEV)[:, None] % 3 + torch.tensor([0, 3], device=DEV)).to(torch.int32).contiguous()
+    w = torch.full((T, k), 0.5, device=DEV)
+    ids[4] = -1
+    clean = decoder(x, E, k, I).forward(x, wgu, wd, topk_ids=ids, topk_w=w).clone()
+    x[1, 7], x[4] = math.nan, math.inf
+    wgu[1][2, 3, 5] = 255                                  # experts 2 and 5: tokens 2, 5, 8, ...
+    got = decoder(x, E, k, I).forward(x, wgu, wd, topk_ids=ids, topk_w=w)
+    hit = torch.arange(T, device=DEV) % 3 == 2
+    hit[1] = True
+    assert bool(got[hit].isnan().all()) and torch.equal(got[~hit], clean[~hit]) and not bool(got[4].any())
+
+
 @pytest.mark.parametrize("T,d,E,k,I", [(1, 256, 16, 4, 128), (8, 256, 16, 8, 256), (16, 256, 3, 2, 128),
                                        (40, 128, 20, 4, 256), (130, 1024, 128, 9, 256)])
 def test_activations_keep_sixteen_bits(T, d, E, k, I):
