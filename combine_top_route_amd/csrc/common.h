@@ -67,6 +67,15 @@ __device__ __forceinline__ float clip_up(float u, float lim) { return u > lim ? 
 
 __host__ __device__ constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// A grid of at least `blocks` (each of up to 1024 threads), and a block's number in
+// it: one dimension of a grid holds fewer than 2^32 threads.
+constexpr int kFold = 21;
+inline dim3 folded_grid(int64_t blocks) {
+  const int64_t x = blocks < (1 << kFold) ? blocks : 1 << kFold;
+  return dim3((unsigned)x, (unsigned)cdiv(blocks, x));
+}
+__device__ __forceinline__ int64_t folded_block() { return ((int64_t)blockIdx.y << kFold) + blockIdx.x; }
+
 // Order of a row GEMM's tiles within an expert.  Either order re-reads one
 // operand once per group of tiles that runs together: taken N-tile-major,
 // the token rows (once per N tile); taken row-tile-major, the weight (once

@@ -116,7 +116,7 @@ __global__ __launch_bounds__(kThreads<L>) void norm_fwd_kernel(NormArgs a) {
   constexpr int N = Row<T>::N, ROWS = kThreads<L> / L;
   __shared__ float part[2][16];
   const int lane = threadIdx.x % L, vecs = a.d / N;
-  const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / L;
+  const int64_t row = folded_block() * ROWS + threadIdx.x / L;
   const bool in = row < a.T;
   const int mine = in ? vecs : 0;  // a row past the last loads and stores nothing
   const int64_t at = row * vecs;
@@ -432,8 +432,8 @@ int64_t bwd_groups(int64_t T, Spread p) {
 
 template <typename T, int L, int NV>
 hipError_t run_fwd(const LaunchCtx& c, const NormArgs& a) {
-  const dim3 grid((unsigned)cdiv(a.T, kThreads<L> / L));
-  MOE_LAUNCH(c, "norm_forward", (norm_fwd_kernel<T, L, NV>), grid, dim3(kThreads<L>), 0, a);
+  MOE_LAUNCH(c, "norm_forward", (norm_fwd_kernel<T, L, NV>), folded_grid(cdiv(a.T, kThreads<L> / L)),
+             dim3(kThreads<L>), 0, a);
   return hipSuccess;
 }
 template <typename T, int L, int NV>

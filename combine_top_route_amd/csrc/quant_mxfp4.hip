@@ -19,7 +19,7 @@ using tile::u32x4_t;
 
 __global__ __launch_bounds__(256) void quant_mxfp4_kernel(const u32x4_t* __restrict__ src, int64_t n,
                                                           uint32_t* __restrict__ q, uint8_t* __restrict__ s) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t i = folded_block() * 256 + threadIdx.x;
   if (i >= n) return;  // n is a multiple of 4: whole blocks leave together
   const u32x4_t v = __builtin_nontemporal_load(src + i);
   float f[8];
@@ -49,7 +49,7 @@ __global__ __launch_bounds__(256) void quant_mxfp4_kernel(const u32x4_t* __restr
 
 hipError_t launch_quant_mxfp4(const LaunchCtx& c, const void* src, int64_t values, uint8_t* q, uint8_t* s) {
   const int64_t n = values / 8;
-  MOE_LAUNCH(c, "quant_mxfp4", quant_mxfp4_kernel, dim3((unsigned)cdiv(n, 256)), dim3(256), 0, (const u32x4_t*)src, n,
+  MOE_LAUNCH(c, "quant_mxfp4", quant_mxfp4_kernel, folded_grid(cdiv(n, 256)), dim3(256), 0, (const u32x4_t*)src, n,
              (uint32_t*)q, s);
   return hipSuccess;
 }

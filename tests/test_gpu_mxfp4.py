@@ -246,3 +246,17 @@ def test_operator_graph_and_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, eager), i
+
+
+def test_encoding_beyond_one_launch_dimension():
+    """2^35 values: 2^32 threads of eight values, more than one dimension of a launch takes."""
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GiB of free GPU memory")
+    few = torch.randn((1, 128, 4096), device=DEV).bfloat16()
+    q0, s0 = B.quantize_mxfp4(few)
+    src = few.expand(64, 128, 4096).reshape(1, 8192, 4096).repeat(1024, 1, 1)
+    assert src.numel() == 1 << 35
+    q, s = B.quantize_mxfp4(src)
+    for got, want in ((q, q0), (s, s0)):
+        got = got.view(-1, *want.shape[1:])
+        assert all(bool((part == want).all()) for part in got.split(4096))

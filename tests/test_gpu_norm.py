@@ -379,3 +379,18 @@ def test_compiled():
     torch.compile(f, fullgraph=True, backend="aot_eager")(x, y, w).backward()
     for t, g in zip((x, y, w), want):
         assert (t.grad - g).abs().max().item() <= 2.0 ** -20 * g.abs().max().item()
+
+
+def test_blocks_beyond_one_launch_dimension():
+    """Two rows a work-group: more work-groups than one dimension of the grid takes."""
+    T, d = (1 << 22) + 3, 2056
+    if torch.cuda.mem_get_info()[0] < 48 << 30:
+        pytest.skip("needs 48 GiB of free GPU memory")
+    w = torch.randn(d, device="cuda").bfloat16()
+    few = torch.randn((64, d), device="cuda").bfloat16()
+    _, want = B.norm_residual(few, w_next=w)
+    x = torch.zeros((T, d), dtype=torch.bfloat16, device="cuda")
+    x[:32], x[-32:] = few[:32], few[32:]
+    _, h = B.norm_residual(x, w_next=w)
+    assert torch.equal(torch.cat((h[:32], h[-32:])), want)
+    assert not any(bool(part.any()) for part in h[32:-32].split(1 << 20))
