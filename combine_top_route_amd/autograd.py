@@ -375,17 +375,23 @@ def moe_prompt(x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: Tensor, k: 
     """The layer for any number of tokens from the MXFP4 weights that moe_decode
     takes: routing, the two grouped products and the combine; out [T,d].  bf16
     x; the activations and each slot's product are rounded to bf16 in between, as
-    in moe_forward.  A masked expert (a logit of -inf) has weight zero, so a token
-    of masked experts alone gets zeros.  No gradient."""
+    in moe_forward.  A masked expert (a logit of -inf) adds nothing, so a token of
+    masked experts alone gets zeros.  No gradient."""
     fmt = _check_decode_args(x, logits, w_gate_up, w_down, k, s_gate_up, s_down)
     _require(fmt == "mxfp4" and x.dtype == torch.bfloat16, "moe_prompt takes bf16 x and MXFP4 weights")
     _check_devices(x=x, logits=logits, w_gate_up=w_gate_up, w_down=w_down, s_gate_up=s_gate_up, s_down=s_down)
     T = x.shape[0]
     with B._on(x.device):
         r = B.route(logits, k)
-        r.topk_w.masked_fill_(logits.gather(1, r.topk_ids.long()) == -float("inf"), 0.0)
+        masked = logits.gather(1, r.topk_ids.long()) == -float("inf")
+        r.topk_w.masked_fill_(masked, 0.0)
         a = B.grouped_product(x, (w_gate_up, s_gate_up), r, T, k, swiglu=True, swiglu_limit=swiglu_limit)
-        y = B.grouped_product(a, (w_down, s_down), r, T, k, gather=False)
+        # a row of zeros behind the slots', which a masked slot adds for its own (0 times
+        # what its expert makes would be NaN where that is not finite)
+        y = x.new_empty((T * k + 1, x.shape[1]))
+        y[T * k].zero_()
+        r.row_of.masked_fill_(masked.view(-1), T * k)
+        B.grouped_product(a, (w_down, s_down), r, T, k, gather=False, out=y[:T * k])
         return B.combine(y, r, T, k)
 
 

@@ -228,3 +228,26 @@ def test_prompt(T, d, E, k, I):
         assert not bool(got[1].any())
     f = torch.compile(lambda *a: A.moe_prompt(*a[:4], k, *a[4:], 1.5), fullgraph=True, backend="aot_eager")
     assert torch.equal(f(x, lg, gu[0], dn[0], gu[1], dn[1]), got)
+
+
+def test_prompt_masks_what_is_not_finite():
+    """A masked slot adds nothing, whatever its token and its expert hold."""
+    T, d, E, k, I = 40, 256, 8, 3, 128
+    x = torch.randn((T, d), device=DEV).bfloat16()
+    lg = torch.randn((T, E), device=DEV)
+    gu, dn = weight(E, 2 * I, d, 7), weight(E, d, I, 8)
+    dn[1][5] = 255  # expert 5 makes NaN
+    lg[:, 5] = -math.inf
+    lg[4, :4] = lg[4, 6:] = -math.inf  # one expert left
+    lg[7] = -math.inf
+    lg[9] = -math.inf
+    x[7] = math.nan
+    x[9] = math.inf
+    got = A.moe_prompt(x, lg, gu[0], dn[0], k, gu[1], dn[1])
+    dec = B.MoeDecoder(T, d, E, k, I, weights="mxfp4", device=DEV, logits_dtype=torch.float32)
+    want = dec.forward(x, gu, dn, logits=lg)
+    assert bool(got.isfinite().all()) and bool(want.isfinite().all())
+    assert not bool(got[[7, 9]].any()) and not bool(want[[7, 9]].any())
+    one = A.moe_prompt(x[4:5], lg[4:5], gu[0], dn[0], k, gu[1], dn[1])  # the expert alone, weight 1
+    near = (got[4:5].double() - one.double()).abs()
+    assert bool((near <= 2.0 ** -7 * one.double().abs() + 2.0 ** -7 * one.double().abs().max()).all())
