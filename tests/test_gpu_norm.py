@@ -364,6 +364,45 @@ def test_block(save8):
     assert b.shape == a[0].shape
 
 
+def test_captured_step_beside_a_live_eager_graph():
+    """A whole block's forward and backward in a graph, on leaves of its own, while
+    an eager graph of the same weights lives; every replay against eager."""
+    T, d, E, k, I = 96, 256, 8, 2, 128
+    names = ("x", "w_router", "w_gate_up", "w_down", "w_pre", "w_post", "gate", "w_next")
+    shapes = ((T, d), (E, d), (E, 2 * I, d), (E, d, I), (d,), (d,), (T, 1), (d,))
+
+    def fresh(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda s: (torch.randn(s, generator=g, device="cuda") * (0.1 if len(s) == 3 else 1)).to(torch.bfloat16)
+        return [r(s) for s in shapes], [r((T, d)), r((T, d))]
+
+    def step(p):
+        z, h = A.moe_residual_block(**dict(zip(names, p)), k=k, res_scale=0.5)
+        return [z, h, *torch.autograd.grad((z, h), p, douts)]
+
+    data, douts = fresh(1)
+    own = lambda: [t.detach().requires_grad_() for t in data]
+    live = A.moe_residual_block(**dict(zip(names, own())), k=k)  # kept until the end
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(own())
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    leaf = own()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(leaf)
+    for i in range(3):
+        for t, f in zip([*data, *douts], sum(fresh(20 + i), [])):
+            t.copy_(f)
+        graph.replay()
+        want = step(own())
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+    assert live[0].shape == (T, d)
+
+
 def test_compiled():
     T, d = 64, 128
     x, y, w = (torch.randn(s, device="cuda", requires_grad=True) for s in ((T, d), (T, d), (d,)))
