@@ -12,10 +12,10 @@
 // What it measured at 33 tokens of 8 of 128 experts, K = 2048, N = 1536 (188 MB of
 // codes and scales): 57 us with 32x32x16 products of 32 columns a wave, whose rows
 // are read from LDS once for two products; 47 with these, 64 columns a wave; 44
-// with three slots of one 128-value stage; 41 with H = 2 and 128 columns a
-// work-group, 4.6 TB/s: both halves of a 128-byte line are asked for together (a
-// kernel that only loads reads 4.7 TB/s in 64-byte pieces of 256 rows 2 KB apart,
-// and 6.0 in 128-byte ones of 128).  Where more rows leave LDS for 128 values only
+// with three slots of one 128-value stage; 40 with H = 2 and 128 columns a
+// work-group, 4.7 TB/s: whole 128-byte lines are asked for (a kernel that only
+// loads reads 4.7 TB/s in 64-byte pieces of 256 rows 2 KB apart, and 6.0 in
+// 128-byte ones of 128; the two halves of a line in loads of their own: 41).  Where more rows leave LDS for 128 values only
 // (RB > 2), wider tiles pay instead.
 #pragma once
 
@@ -58,8 +58,9 @@ template <int RB_, int CB_, int H_>
 struct Tiles {
   static constexpr int RB = RB_, CB = CB_, H = H_;
   static constexpr int ROWS = 16 * RB, COLS = 64 * CB;
-  static constexpr int A = ROWS * 256, CODES = COLS * 64;
-  static constexpr int HALF = A + CODES, STAGE = H * HALF;
+  static constexpr int A = ROWS * 256;
+  static constexpr int B = 64 * H;  // bytes of a column's codes, beside each other
+  static constexpr int STAGE = H * A + COLS * B;
   static constexpr int SCALES = COLS * 16;
   static constexpr int LDS = 2 * (STAGE + SCALES);
 };
@@ -67,9 +68,9 @@ struct Tiles {
 // One stage's operands of a wave into registers and its products; `col`: the
 // wave's first column in B, whose scale word is at `scales`.  Every read leaves
 // before the first product waits for one.
-template <int RB, int CB>
+template <int RB, int CB, int BS = 64>
 __device__ __forceinline__ void stage_products(const lds_t* A, const lds_t* B, const lds_t* scales, int col,
-                                               int scale_stride, f32x4_t (&acc)[RB][CB]) {
+                                               int scale_stride, f32x4_t (&acc)[RB][CB], int h = 0) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   uint32_t word[CB];
   u32x4_t code[CB], av[4][RB];
@@ -77,7 +78,8 @@ __device__ __forceinline__ void stage_products(const lds_t* A, const lds_t* B, c
   for (int c = 0; c < CB; ++c) {
     const int n = col + 16 * c + r;
     word[c] = *(const __attribute__((address_space(3))) uint32_t*)(scales + (16 * c + r) * scale_stride);
-    code[c] = lds16(B + n * 64 + ((q ^ (n >> 2)) & 3) * 16);
+    if constexpr (BS == 128) code[c] = lds16(B + n * 128 + (((4 * h + q) ^ n) & 7) * 16);
+    else code[c] = lds16(B + n * 64 + ((q ^ (n >> 2)) & 3) * 16);
   }
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk)
@@ -102,19 +104,21 @@ __device__ __forceinline__ void stage_products(const lds_t* A, const lds_t* B, c
 // col_at(n) the row of W (among all experts') that column n stands for.
 template <class C>
 struct Stream {
+  static constexpr int NC = C::CB * C::H;  // 1 KB loads of codes: 16 / H columns
   const char* pa[C::RB];
-  const char* pb[C::CB];
+  const char* pb[NC];
   const char* ps[C::CB];
   template <class RowAt, class ColAt>
   __device__ __forceinline__ void init(RowAt row_at, ColAt col_at, const uint8_t* codes, const uint8_t* scales, int K) {
     const int lane = threadIdx.x & 63, w = wave_id();
 #pragma unroll
-    for (int i = 0; i < C::CB; ++i) {
-      const int n = 16 * (w * C::CB + i) + (lane >> 2);
-      const int64_t at = col_at(n);
-      pb[i] = (const char*)codes + at * (K / 2) + (((lane ^ (n >> 2)) & 3) << 4);
-      ps[i] = (const char*)scales + at * (K / 32);
+    for (int i = 0; i < NC; ++i) {
+      const int n = C::H == 2 ? 8 * (w * NC + i) + (lane >> 3) : 16 * (w * NC + i) + (lane >> 2);
+      pb[i] = (const char*)codes + col_at(n) * (K / 2) + (C::H == 2 ? (lane ^ n) & 7 : (lane ^ (n >> 2)) & 3) * 16;
     }
+#pragma unroll
+    for (int i = 0; i < C::CB; ++i)
+      ps[i] = (const char*)scales + col_at(16 * (w * C::CB + i) + (lane >> 2)) * (K / 32);
 #pragma unroll
     for (int i = 0; i < C::RB; ++i) {
       const int r = 4 * (w + kWaves * i) + (lane >> 4);
@@ -129,18 +133,19 @@ struct Stream {
   // `halves` of H: the last stage may be short.
   __device__ __forceinline__ void issue(lds_t* slot, int halves) {
     const int w = wave_id();
+    // a short stage repeats its codes: none are behind
+    const int lane = threadIdx.x & 63;
+    const int back = halves < C::H ? ((lane ^ (lane >> 3)) & 4) << 4 : 0;
 #pragma unroll
-    for (int i = 0; i < C::CB; ++i) {
-#pragma unroll
-      for (int h = 0; h < C::H; ++h)
-        if (h < halves) dma16(pb[i] + 64 * h, slot + h * C::HALF + C::A + (w * C::CB + i) * 1024);
-      pb[i] += 64 * C::H;
+    for (int i = 0; i < NC; ++i) {
+      dma16(pb[i] - back, slot + C::H * C::A + (w * NC + i) * 1024);
+      pb[i] += C::B;
     }
 #pragma unroll
     for (int i = 0; i < C::RB; ++i) {
 #pragma unroll
       for (int h = 0; h < C::H; ++h)
-        if (h < halves) dma16(pa[i] + 256 * h, slot + h * C::HALF + (w + kWaves * i) * 1024);
+        if (h < halves) dma16(pa[i] + 256 * h, slot + h * C::A + (w + kWaves * i) * 1024);
       pa[i] += 256 * C::H;
     }
   }
@@ -178,7 +183,7 @@ __device__ __forceinline__ void products(Stream<C>& st, int units, lds_t* lds, f
 #pragma unroll
     for (int h = 0; h < H; ++h)
       if (h == 0 || p * H + h < units)
-        stage_products<C::RB, C::CB>(A + h * C::HALF, A + h * C::HALF + C::A, word + h * 4, 16 * C::CB * w, 16, acc);
+        stage_products<C::RB, C::CB, C::B>(A + h * C::A, A + H * C::A, word + h * 4, 16 * C::CB * w, 16, acc, h);
   }
   wait_lgkm0();
   barrier_lds();  // the slots are free
