@@ -196,7 +196,7 @@ __global__ __launch_bounds__(kThreads<L>) void norm_bwd_kernel(NormArgs a) {
   const int lane = threadIdx.x % L, sub = threadIdx.x / L, vecs = a.d / N;
   // 32 columns a lane leave no registers for the weights and the next row, which
   // are then read where they are used (2048 rows of 16384 in bf16: 302 us with
-  // them spilled, TIME)
+  // them spilled, 116 so; in float32, with 32 more sums a lane, 270)
   constexpr bool LEAN = NV * N >= 32;
   constexpr int KEPT = LEAN ? 1 : NV;
   u32x4_t wp_[KEPT], wn_[KEPT], gv_[KEPT];
@@ -395,8 +395,8 @@ struct Spread {
   int L, NV;
 };
 
-// Forward: one piece a lane for few rows (one of 2048 values: 4.1 us, with four
-// 5.0); for many, a wave a row while four pieces hold it (16384 rows of 2048 in
+// Forward: one piece a lane for few rows (256 of 4096: 4.6 us, with four pieces
+// 5.9; 2047 of 2048 8.5 and 9.5); for many, a wave a row while four pieces hold it (16384 rows of 2048 in
 // bf16: 46 us with four waves a row, 43 with one).
 Spread fwd_spread(int64_t T, int vecs) {
   Spread p = {8, 1};
@@ -423,11 +423,14 @@ Spread bwd_spread(int vecs) {
 }
 
 // Work-groups of the backward, of which each leaves a part of the column sums:
-// eight waves a CU (16384 rows of 2048: 83 us, with four 120, with sixteen 96 and
-// twice the parts to join).
+// at most eight waves a CU (16384 rows of 2048: 83 us, with four 120, with sixteen
+// 96 and twice the parts to join), and no more than take the same number of steps
+// (333 rows of 4096: 16.3 us in 256, of which 77 take a second row, 15.1 in 167; 257
+// rows 15.9 and 13.8).
 int64_t bwd_groups(int64_t T, Spread p) {
   const int threads = p.L > 256 ? p.L : 256;
-  return std::min<int64_t>(cdiv(T, threads / p.L), 256 * 512 / threads);
+  const int64_t blocks = cdiv(T, threads / p.L), steps = cdiv(blocks, 256 * 512 / threads);
+  return cdiv(blocks, steps);
 }
 
 template <typename T, int L, int NV>
@@ -440,8 +443,8 @@ template <typename T, int L, int NV>
 hipError_t run_bwd(const LaunchCtx& c, const NormArgs& a) {
   const int groups = (int)bwd_groups(a.T, {L, NV});
   // rows beyond the last-level cache leave it alone (16384 rows of 2048, 402 MB: 82
-  // us without, 77 with, 81 with the stores too; below its size they may be there from the step before:
-  // 4096 rows 27.7 and 29.1)
+  // us without, 77 with, 81 with the stores too); below its size they may be there
+  // from the step before (4096 rows: 27.7 and 29.1)
   const int64_t rows = 2 + 2 * (a.w_next != nullptr) + 2 * (a.dy != nullptr);
   if (rows * a.T * a.d * (int64_t)sizeof(T) > (int64_t(256) << 20))
     MOE_LAUNCH(c, "norm_backward", (norm_bwd_kernel<T, L, NV, true>), dim3((unsigned)groups), dim3(kThreads<L>), 0, a);

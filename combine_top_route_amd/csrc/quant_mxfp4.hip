@@ -7,7 +7,8 @@
 //
 // Bound by memory: 2 bytes read and 17/32 written a value.  A lane takes 8
 // values (16 bytes), four lanes a block, whose largest magnitude they exchange
-// by DPP (601 M values, the weights of 128 experts at d = 2048, I = 768: TIME).
+// by DPP (403 M values, the gate/up weights of 128 experts at d = 2048, I = 768:
+// 162 us, 6.3 TB/s).
 #include "common.h"
 #include "save8.h"
 #include "tile.h"

@@ -427,9 +427,11 @@ def test_blocks_beyond_one_launch_dimension():
         pytest.skip("needs 48 GiB of free GPU memory")
     w = torch.randn(d, device="cuda").bfloat16()
     few = torch.randn((64, d), device="cuda").bfloat16()
-    _, want = B.norm_residual(few, w_next=w)
+    # 64 rows alone are spread over other lanes, whose sums differ in the last bits:
+    # the bound is the formula's
+    _, _, want, mag = forward_ref(dict(x=few, y=None, w_post=None, gate=None, w_next=w), 1.0)
     x = torch.zeros((T, d), dtype=torch.bfloat16, device="cuda")
     x[:32], x[-32:] = few[:32], few[32:]
     _, h = B.norm_residual(x, w_next=w)
-    assert torch.equal(torch.cat((h[:32], h[-32:])), want)
+    near(torch.cat((h[:32], h[-32:])), want, mag, 64)
     assert not any(bool(part.any()) for part in h[32:-32].split(1 << 20))
