@@ -1061,11 +1061,12 @@ __device__ __forceinline__ void gateup4_rows(const DecodeArgs& a, const Rows& ro
   const int64_t mat = (int64_t)e * 2 * a.I;
   const int lane = threadIdx.x & 63;
   mx4::Stream<C> st;
-  st.init([&](int i) { return (const char*)a.x + (int64_t)(rows.slot[min(r0 + i, n - 1)] / a.k) * a.d * 2; },
-          [&](int c) -> int64_t {  // 16 gate columns, the same up columns, in turn; past I the last
-            return mat + min(n0 + (c >> 5) * 16 + (c & 15), a.I - 1) + ((c & 16) ? a.I : 0);
-          },
-          (const uint8_t*)a.w_gate_up, (const uint8_t*)a.s_gate_up, a.d);
+  st.begin([&](int i) { return rows.slot[min(r0 + i, n - 1)]; },
+           [&](int slot) { return (const char*)a.x + (int64_t)(slot / a.k) * a.d * 2; },
+           [&](int c) -> int64_t {  // 16 gate columns, the same up columns, in turn; past I the last
+             return mat + min(n0 + (c >> 5) * 16 + (c & 15), a.I - 1) + ((c & 16) ? a.I : 0);
+           },
+           (const uint8_t*)a.w_gate_up, (const uint8_t*)a.s_gate_up, a.d, lds);
   f32x4_t acc[C::RB][C::CB];
   mx4::products<C>(st, a.d / 128, lds, acc);
 #pragma unroll
@@ -1114,14 +1115,14 @@ __device__ __forceinline__ void down4_rows(const DecodeArgs& a, const Rows& rows
   const int64_t mat = (int64_t)e * a.d;
   const int lane = threadIdx.x & 63;
   mx4::Stream<C> st;
-  st.init(
-      [&](int i) {
-        const bool second = i >= 16 * HB;
-        const int64_t at = (int64_t)rows.slot[min(r0 + i - (second ? 16 * HB : 0), n - 1)] * a.I;
-        return (const char*)a.aw + (at + (second ? aw_plane(a) : 0)) * 2;
-      },
-      [&](int c) -> int64_t { return mat + min(n0 + c, a.d - 1); }, (const uint8_t*)a.w_down, (const uint8_t*)a.s_down,
-      a.I);
+  st.begin([](int i) { return i; },
+           [&](int i) {
+             const bool second = i >= 16 * HB;
+             const int64_t at = (int64_t)rows.slot[min(r0 + i - (second ? 16 * HB : 0), n - 1)] * a.I;
+             return (const char*)a.aw + (at + (second ? aw_plane(a) : 0)) * 2;
+           },
+           [&](int c) -> int64_t { return mat + min(n0 + c, a.d - 1); }, (const uint8_t*)a.w_down,
+           (const uint8_t*)a.s_down, a.I, lds);
   f32x4_t acc[C::RB][C::CB];
   mx4::products<C>(st, a.I / 128, lds, acc);
 #pragma unroll

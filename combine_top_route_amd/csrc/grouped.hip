@@ -126,15 +126,18 @@ struct Loads {
   const char* pa[TMX];
   const char* pb[4];
   const char* ps;
+  // Sends the first codes while the rows' indices are on their way (131072 rows of
+  // 128 by 1536: 104 us with the codes behind the indices, 97 so).
   template <bool SWIGLU>
-  __device__ __forceinline__ void init(const GroupedArgs& a, const Tile& t) {
+  __device__ __forceinline__ void begin(const GroupedArgs& a, const Tile& t, lds_t* first_codes) {
     const int lane = threadIdx.x & 63, w = wave_id();
     int src[TMX];
 #pragma unroll
     for (int i = 0; i < TMX; ++i) {  // rows past the segment repeat its last
       const int r = min(t.m0 + 8 * (w + NW * i) + (lane >> 3), t.seg1 - 1);
-      src[i] = a.src_of ? min(max(a.src_of[r], 0), a.R - 1) : r;
+      src[i] = a.src_of ? a.src_of[r] : r;
     }
+    __builtin_amdgcn_sched_barrier(0);
     const int64_t mat = (int64_t)t.e * a.N;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -142,10 +145,12 @@ struct Loads {
       pb[i] = (const char*)a.codes + (mat + w_row<SWIGLU>(a, t.nt, row)) * (a.K / 2) + (((lane ^ (row >> 2)) & 3) << 4);
     }
     ps = (const char*)a.scales + (mat + w_row<SWIGLU>(a, t.nt, 64 * w + lane)) * (a.K / 32);
+    codes(first_codes);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < TMX; ++i) {
       const int row = 8 * (w + NW * i) + (lane >> 3);
-      const int64_t s = a.src_of ? src[i] / a.k : src[i];
+      const int64_t s = a.src_of ? min(max(src[i], 0), a.R - 1) / a.k : src[i];
       pa[i] = (const char*)a.x + s * a.K * 2 + (((lane & 7) ^ mk_swz(row)) << 4);
     }
   }
@@ -234,7 +239,6 @@ __device__ __forceinline__ void mainloop(Loads<TMX>& ld, int pairs, lds_t* lds, 
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
   lds_t* const lb = lds + 2 * SLOT_A;
-  ld.codes(lb);
   ld.rows(lds);
   for (int p = 0; p < pairs; ++p) {
     const bool more = p + 1 < pairs;
@@ -264,7 +268,7 @@ __device__ __forceinline__ void tile_rows(const GroupedArgs& a, const Tile& t, l
   constexpr int COLS = SWIGLU ? TN / 2 : TN, S = COLS * 2 + 16;
   f32x16_t acc[TMX][2];
   Loads<TMX> ld;
-  ld.template init<SWIGLU>(a, t);
+  ld.template begin<SWIGLU>(a, t, lds + 2 * SLOT_A);
   mainloop<TMX>(ld, a.K / 128, lds, acc);
   const int lane = threadIdx.x & 63, w = wave_id();
 #pragma unroll
@@ -316,11 +320,15 @@ __global__ __launch_bounds__(NT, 2) void grouped_tile_kernel(GroupedArgs a, int 
 
 // Few rows an expert: tiles of SROWS rows (16, 32 or 48 where there are no more) by
 // 64 CB columns, or 32 CB gate and the same up columns.
-// Row i of a tile (past the segment its last), and the row of W for its column n
-// (past the last that; SWIGLU: 16 gate, the same up, in turn).
-__device__ __forceinline__ const char* row_at(const GroupedArgs& a, const Tile& t, int i) {
+// Row i of a tile (past the segment its last; its entry with src_of) and where that
+// is, and the row of W for its column n (past the last that; SWIGLU: 16 gate, the
+// same up, in turn).
+__device__ __forceinline__ int index_of(const GroupedArgs& a, const Tile& t, int i) {
   const int r = min(t.m0 + i, t.seg1 - 1);
-  const int64_t s = a.src_of ? min(max(a.src_of[r], 0), a.R - 1) / a.k : r;
+  return a.src_of ? a.src_of[r] : r;
+}
+__device__ __forceinline__ const char* row_at(const GroupedArgs& a, int index) {
+  const int64_t s = a.src_of ? min(max(index, 0), a.R - 1) / a.k : index;
   return (const char*)a.x + s * a.K * 2;
 }
 template <bool SWIGLU, int COLS>
@@ -339,8 +347,8 @@ __device__ __forceinline__ void stream_rows(const GroupedArgs& a, const Tile& t,
   constexpr int COLS = SWIGLU ? C::COLS / 2 : C::COLS, S = COLS * 2 + 16;
   static_assert(C::ROWS * S <= C::LDS && (!SWIGLU || C::CB % 2 == 0), "");
   Stream<C> st;
-  st.init([&](int i) { return row_at(a, t, i); }, [&](int n) { return col_at<SWIGLU, COLS>(a, t, n); }, a.codes,
-          a.scales, a.K);
+  st.begin([&](int i) { return index_of(a, t, i); }, [&](int index) { return row_at(a, index); },
+           [&](int n) { return col_at<SWIGLU, COLS>(a, t, n); }, a.codes, a.scales, a.K, lds);
   f32x4_t acc[C::RB][C::CB];
   mx4::products<C>(st, a.K / 128, lds, acc);
   const int lane = threadIdx.x & 63, w = wave_id();
@@ -408,8 +416,8 @@ template <class C, bool SWIGLU>
 __device__ __forceinline__ void split_rows(const GroupedArgs& a, const Tile& t, lds_t* lds) {
   constexpr int COLS = SWIGLU ? C::COLS / 2 : C::COLS;
   mx4::SplitStream<C> st;
-  st.init([&](int i) { return row_at(a, t, i); }, [&](int n) { return col_at<SWIGLU, COLS>(a, t, n); }, a.codes,
-          a.scales, a.K);
+  st.begin([&](int i) { return index_of(a, t, i); }, [&](int index) { return row_at(a, index); },
+           [&](int n) { return col_at<SWIGLU, COLS>(a, t, n); }, a.codes, a.scales, a.K, lds);
   f32x4_t acc[C::RB][4];
   // a wave finishes one block of 16 columns, or of gate and up
   const auto keep = [](int w, int c) { return SWIGLU ? (c >> 1) == w : c == w; };

@@ -100,30 +100,42 @@ __device__ __forceinline__ void stage_products(const lds_t* A, const lds_t* B, c
   }
 }
 
-// This lane's sources: row_at(i) is the address of tile row i of the activations,
-// col_at(n) the row of W (among all experts') that column n stands for.
+// This lane's sources: row_at(index_of(i)) is the address of tile row i of the
+// activations, col_at(n) the row of W (among all experts') that column n stands for.
 template <class C>
 struct Stream {
   static constexpr int NC = C::CB * C::H;  // 1 KB loads of codes: 16 / H columns
   const char* pa[C::RB];
   const char* pb[NC];
   const char* ps[C::CB];
-  template <class RowAt, class ColAt>
-  __device__ __forceinline__ void init(RowAt row_at, ColAt col_at, const uint8_t* codes, const uint8_t* scales, int K) {
-    const int lane = threadIdx.x & 63, w = wave_id();
+  // Sends the first stage's loads: first those of the rows' indices, then the codes'
+  // and scales', and the rows' when the indices are there.
+  template <class IndexOf, class RowAt, class ColAt>
+  __device__ __forceinline__ void begin(IndexOf index_of, RowAt row_at, ColAt col_at, const uint8_t* codes,
+                                        const uint8_t* scales, int K, lds_t* lds) {
+    const int lane = threadIdx.x & 63, w = wave_id(), units = K / 128;
+    int index[C::RB];
+#pragma unroll
+    for (int i = 0; i < C::RB; ++i) index[i] = index_of(4 * (w + kWaves * i) + (lane >> 4));
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < C::CB; ++i)
+      ps[i] = (const char*)scales + col_at(16 * (w * C::CB + i) + (lane >> 2)) * (K / 32);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int n = C::H == 2 ? 8 * (w * NC + i) + (lane >> 3) : 16 * (w * NC + i) + (lane >> 2);
       pb[i] = (const char*)codes + col_at(n) * (K / 2) + (C::H == 2 ? (lane ^ n) & 7 : (lane ^ (n >> 2)) & 3) * 16;
     }
+    issue_codes(lds, units);
 #pragma unroll
-    for (int i = 0; i < C::CB; ++i)
-      ps[i] = (const char*)scales + col_at(16 * (w * C::CB + i) + (lane >> 2)) * (K / 32);
+    for (int i = 0; i < C::CB; ++i) this->scales(i, 0, units, lds + 2 * C::STAGE);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < C::RB; ++i) {
       const int r = 4 * (w + kWaves * i) + (lane >> 4);
-      pa[i] = row_at(r) + (((lane ^ r) & 15) << 4);
+      pa[i] = row_at(index[i]) + (((lane ^ r) & 15) << 4);
     }
+    issue_rows(lds, units);
   }
   // Words 4 g .. of 16 of the wave's columns (past the row's end its last word).
   __device__ __forceinline__ void scales(int i, int g, int stages, lds_t* buffer) const {
@@ -131,7 +143,7 @@ struct Stream {
     dma4(ps[i] + 4 * word, buffer + (wave_id() * C::CB + i) * 256);
   }
   // `halves` of H: the last stage may be short.
-  __device__ __forceinline__ void issue(lds_t* slot, int halves) {
+  __device__ __forceinline__ void issue_codes(lds_t* slot, int halves) {
     const int w = wave_id();
     // a short stage repeats its codes: none are behind
     const int lane = threadIdx.x & 63;
@@ -141,6 +153,9 @@ struct Stream {
       dma16(pb[i] - back, slot + C::H * C::A + (w * NC + i) * 1024);
       pb[i] += C::B;
     }
+  }
+  __device__ __forceinline__ void issue_rows(lds_t* slot, int halves) {
+    const int w = wave_id();
 #pragma unroll
     for (int i = 0; i < C::RB; ++i) {
 #pragma unroll
@@ -152,7 +167,7 @@ struct Stream {
 };
 
 // acc[b][c]: lane l has row 16 b + l % 16; register v the wave's column 16 c +
-// 4 (l / 16) + v.  units: K / 128.
+// 4 (l / 16) + v.  units: K / 128; the first stage is on its way.
 template <class C>
 __device__ __forceinline__ void products(Stream<C>& st, int units, lds_t* lds, f32x4_t (&acc)[C::RB][C::CB]) {
   constexpr int H = C::H, PER = 4 / H;  // stages a group of scale words
@@ -163,9 +178,6 @@ __device__ __forceinline__ void products(Stream<C>& st, int units, lds_t* lds, f
   for (int b = 0; b < C::RB; ++b)
 #pragma unroll
     for (int c = 0; c < C::CB; ++c) acc[b][c] = f32x4_t{0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < C::CB; ++i) st.scales(i, 0, units, words);
-  st.issue(lds, units);
   for (int p = 0; p < stages; ++p) {
     const int g = p / PER;
     wait_vmcnt<0>();
@@ -176,7 +188,8 @@ __device__ __forceinline__ void products(Stream<C>& st, int units, lds_t* lds, f
 #pragma unroll
       for (int i = 0; i < C::CB; ++i)
         if (p % PER == i % PER) st.scales(i, g + 1, units, words + ((g & 1) ^ 1) * C::SCALES);
-      st.issue(lds + ((p & 1) ^ 1) * C::STAGE, units - (p + 1) * H);
+      st.issue_codes(lds + ((p & 1) ^ 1) * C::STAGE, units - (p + 1) * H);
+      st.issue_rows(lds + ((p & 1) ^ 1) * C::STAGE, units - (p + 1) * H);
     }
     const lds_t* A = lds + (p & 1) * C::STAGE;
     const lds_t* word = words + (g & 1) * C::SCALES + w * C::CB * 256 + (p % PER) * H * 4;
@@ -209,23 +222,32 @@ struct SplitStream {
   const char* pa[NA];
   const char* pb[4];
   const char* ps;
-  // At the wave's first stage.
-  template <class RowAt, class ColAt>
-  __device__ __forceinline__ void init(RowAt row_at, ColAt col_at, const uint8_t* codes, const uint8_t* scales, int K) {
+  // Sends the wave's first stage, as Stream::begin does.
+  template <class IndexOf, class RowAt, class ColAt>
+  __device__ __forceinline__ void begin(IndexOf index_of, RowAt row_at, ColAt col_at, const uint8_t* codes,
+                                        const uint8_t* scales, int K, lds_t* lds) {
     const int lane = threadIdx.x & 63, w = wave_id();
+    lds_t* const slot = lds + w * C::NS * C::STAGE;
+    int index[NA];
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      const int r = 4 * i + (lane >> 4);
-      pa[i] = row_at(r) + (((lane ^ r) & 15) << 4) + w * 256;
-    }
+    for (int i = 0; i < NA; ++i) index[i] = index_of(4 * i + (lane >> 4));
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int n = 16 * i + (lane >> 2);
       pb[i] = (const char*)codes + col_at(n) * (K / 2) + (((lane ^ (n >> 2)) & 3) << 4) + w * 64;
     }
     ps = (const char*)scales + col_at(lane) * (K / 32) + w * 4;
+    if (w < K / 128) issue_codes(slot);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const int r = 4 * i + (lane >> 4);
+      pa[i] = row_at(index[i]) + (((lane ^ r) & 15) << 4) + w * 256;
+    }
+    if (w < K / 128) issue_rows(slot);
   }
-  __device__ __forceinline__ void issue(lds_t* slot) {
+  __device__ __forceinline__ void issue_codes(lds_t* slot) {
     lds_t* const b = slot + C::A;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -234,11 +256,17 @@ struct SplitStream {
     }
     dma4(ps, b + C::CODES);
     ps += 4 * kWaves;
+  }
+  __device__ __forceinline__ void issue_rows(lds_t* slot) {
 #pragma unroll
     for (int i = 0; i < NA; ++i) {
       dma16(pa[i], slot + i * 1024);
       pa[i] += 256 * kWaves;
     }
+  }
+  __device__ __forceinline__ void issue(lds_t* slot) {
+    issue_codes(slot);
+    issue_rows(slot);
   }
 };
 
@@ -256,7 +284,7 @@ __device__ __forceinline__ void split_products(SplitStream<C>& st, int stages, l
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[b][c] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < NS - 1; ++i)
+  for (int i = 1; i < NS - 1; ++i)
     if (i < mine) st.issue(ring + i * C::STAGE);
   int slot = 0;
   for (int p = 0; p < mine; ++p) {
