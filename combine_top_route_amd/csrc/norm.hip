@@ -426,10 +426,14 @@ Spread bwd_spread(int vecs) {
 // at most eight waves a CU (16384 rows of 2048: 83 us, with four 120, with sixteen
 // 96 and twice the parts to join), and no more than take the same number of steps
 // (333 rows of 4096: 16.3 us in 256, of which 77 take a second row, 15.1 in 167; 257
-// rows 15.9 and 13.8).
-int64_t bwd_groups(int64_t T, Spread p) {
+// rows 15.9 and 13.8).  Sixteen waves where a third or more of a row's lanes have
+// no column, up to four waves a row (16384 rows of 1032: 67 us with eight, 57 with
+// sixteen; of 520 39 and 34; in float32, 8192 of 600, 34 and 29; but 8192 of 4104,
+// eight waves a row, 105 and 113).
+int64_t bwd_groups(int64_t T, Spread p, int vecs) {
   const int threads = p.L > 256 ? p.L : 256;
-  const int64_t blocks = cdiv(T, threads / p.L), steps = cdiv(blocks, 256 * 512 / threads);
+  const int64_t most = (p.L <= 256 && 3 * vecs < 2 * p.L ? 2 : 1) * 256 * 512 / threads;
+  const int64_t blocks = cdiv(T, threads / p.L), steps = cdiv(blocks, most);
   return cdiv(blocks, steps);
 }
 
@@ -441,7 +445,7 @@ hipError_t run_fwd(const LaunchCtx& c, const NormArgs& a) {
 }
 template <typename T, int L, int NV>
 hipError_t run_bwd(const LaunchCtx& c, const NormArgs& a) {
-  const int groups = (int)bwd_groups(a.T, {L, NV});
+  const int groups = (int)bwd_groups(a.T, {L, NV}, a.d / Row<T>::N);
   // rows beyond the last-level cache leave it alone (16384 rows of 2048, 402 MB: 82
   // us without, 77 with, 81 with the stores too); below its size they may be there
   // from the step before (4096 rows: 27.7 and 29.1)
@@ -494,7 +498,8 @@ hipError_t bwd(const LaunchCtx& c, const NormArgs& a) {
 }  // namespace
 
 int64_t norm_bwd_groups(int64_t T, int64_t d, int dtype) {
-  return bwd_groups(T, bwd_spread((int)(d / (dtype == F32 ? 4 : 8))));
+  const int vecs = (int)(d / (dtype == F32 ? 4 : 8));
+  return bwd_groups(T, bwd_spread(vecs), vecs);
 }
 hipError_t launch_norm_fwd(const LaunchCtx& c, const NormArgs& a) {
   return a.dtype == F32 ? fwd<float>(c, a) : fwd<bf16_t>(c, a);
