@@ -93,8 +93,9 @@ __device__ __forceinline__ void row_sums(float (&v)[NS], float* part) {
   }
 }
 
-// A work-group: 256 threads, or a row's lanes where those are more.
-template <int L> constexpr int kThreads = L > 256 ? L : 256;
+// A work-group: 256 threads, or a row's lanes where those do not divide them.
+constexpr int threads_of(int L) { return 256 % L ? L : 256; }
+template <int L> constexpr int kThreads = threads_of(L);
 
 // NV pieces of a row of `vecs`, this lane's; zeros past the end.
 template <int L, int NV, bool NT = false>
@@ -412,28 +413,33 @@ Spread fwd_spread(int64_t T, int vecs) {
 // Backward: a row's four operands, the next row's and the two column sums take the
 // registers, so one piece a lane up to eight waves a row (8192 rows of 4096: 81 us,
 // with two pieces 89, with four 101; 2048 of 8192, eight waves and two pieces 47,
-// sixteen and one 63).
+// sixteen and one 63).  Five or six waves where they hold it, of which two
+// work-groups share a CU (8192 rows of 2560: 74 us with eight, 51 with five; of 2800
+// 74 and 58; seven instead of eight, one a CU, gain nothing).
 Spread bwd_spread(int vecs) {
   Spread p = {8, 1};
   while (p.L * p.NV < vecs) {
     if (p.L < 512) p.L *= 2;
     else p.NV *= 2;
   }
+  if (p.L == 512 && vecs <= 384) p.L = vecs <= 320 ? 320 : 384;
   return p;
 }
 
-// Work-groups of the backward, of which each leaves a part of the column sums:
-// at most eight waves a CU (16384 rows of 2048: 83 us, with four 120, with sixteen
-// 96 and twice the parts to join), and no more than take the same number of steps
-// (333 rows of 4096: 16.3 us in 256, of which 77 take a second row, 15.1 in 167; 257
-// rows 15.9 and 13.8).  Sixteen waves where a third or more of a row's lanes have
-// no column, up to four waves a row (16384 rows of 1032: 67 us with eight, 57 with
-// sixteen; of 520 39 and 34; in float32, 8192 of 600, 34 and 29; but 8192 of 4104,
-// eight waves a row, 105 and 113).
+// Work-groups of the backward, of which each leaves a part of the column sums: on a
+// CU two of up to six waves, one of eight (16384 rows of 2048: 83 us, with one 120,
+// with four 96 and twice the parts to join).  Four where a third or more of a row's
+// lanes have no column (16384 rows of 1032: 67 us with two, 57 with four; of 520 39
+// and 34; in float32, 8192 of 600, 34 and 29).  Half as many where each would take
+// one step (512 rows of 2048: 15.2 us in 512, 13.1 in 256; 2000 rows 19.9, in half
+// 23.5), and no more than take the same number of steps (333 rows of 4096: 16.3 us
+// in 256, of which 77 take a second row, 15.1 in 167; 257 rows 15.9 and 13.8).
 int64_t bwd_groups(int64_t T, Spread p, int vecs) {
-  const int threads = p.L > 256 ? p.L : 256;
-  const int64_t most = (p.L <= 256 && 3 * vecs < 2 * p.L ? 2 : 1) * 256 * 512 / threads;
-  const int64_t blocks = cdiv(T, threads / p.L), steps = cdiv(blocks, most);
+  const int threads = threads_of(p.L);
+  int64_t most = 256 * (p.L <= 256 && 3 * vecs < 2 * p.L ? 4 : p.L <= 384 ? 2 : 1);
+  const int64_t blocks = cdiv(T, threads / p.L);
+  if (blocks <= most) most = std::max<int64_t>(256, most / 2);
+  const int64_t steps = cdiv(blocks, most);
   return cdiv(blocks, steps);
 }
 
@@ -487,6 +493,8 @@ template <typename T>
 hipError_t bwd(const LaunchCtx& c, const NormArgs& a) {
   const Spread p = bwd_spread(a.d / Row<T>::N);
   UP_TO_512(run_bwd);
+  CASE(run_bwd, 320, 1);
+  CASE(run_bwd, 384, 1);
   CASE(run_bwd, 512, 2);
   CASE(run_bwd, 512, 4);
   if constexpr (sizeof(T) == 4) CASE(run_bwd, 512, 8);

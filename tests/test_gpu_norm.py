@@ -30,7 +30,8 @@ FORMS = {"pre": (False, False, None, True, 1.0), "all": (True, True, "channel", 
 # one row to several a work-group; a row in 8 lanes to 16 waves; one piece a lane
 # to four; several rows a work-group takes in turn
 SIZES = [(1, 8), (1, 2048), (3, 64), (5, 200), (37, 520), (130, 1000), (33, 2056), (9, 4096), (2, 8200), (3, 16384),
-         (700, 136), (2049, 72), (2100, 1024), (2051, 2048), (2100, 4104), (2048, 8200), (2050, 16384)]
+         (700, 136), (2049, 72), (2100, 1024), (2051, 2048), (2100, 4104), (2048, 8200), (2050, 16384),
+         (600, 2304), (1100, 2880), (700, 1032), (513, 528)]
 
 
 def inputs(T, d, dtype, form, seed=0):
