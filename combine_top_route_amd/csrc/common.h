@@ -312,7 +312,7 @@ struct DecodeArgs {
   int32_t* mid;           // [T, k] workspace: expert of the slot, -1 for an empty or merged slot
   float* mw;              // [T, k] workspace: its weight
   void* aw;               // [T k, I] workspace: weighted SwiGLU output per live slot, float32 or two bf16 planes
-  float* y;               // [T k, d] workspace unless decode_one_down: down products per live slot
+  float* y;               // [T k, d] workspace: down products per live slot, where they are not summed at once
 };
 // weights: moe_weight_format.
 hipError_t launch_decode(const LaunchCtx& c, DecodeArgs a, int weights);

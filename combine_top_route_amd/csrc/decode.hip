@@ -1318,7 +1318,10 @@ hipError_t down4(const LaunchCtx& c, const DecodeArgs& a) {
 // 23, 16 42 and 38, 64 60 and 44, 256 67 and 53; 40 tokens of all of 6, d = 1792,
 // I = 512, 48 work-groups, 7 and 14).  Down: where I is long, or a tile's rows are
 // used (8 tokens 20 and 14, 256 58 and 39; 194 of 6 of 10, d = 896, I = 128, 8.2
-// and 6.2; 5 of 8 of 113, d = 2304, I = 256, 7.9 and 8.9).
+// and 6.2; 5 of 8 of 113, d = 2304, I = 256, 7.9 and 8.9); instead of the kernel that
+// sums over all experts by itself, whose eight columns a work-group read slower but
+// need no combine (4 us), for the weights of 20 MB or more (4 tokens 15.8 and 8.9,
+// 3 12.0 and 9.0, 4 of 8 of 64, d = 4096, I = 1024, 35.6 and 16.8, 1 11.9 and 8.2).
 hipError_t run4(const LaunchCtx& c, const DecodeArgs& a) {
   const int64_t items = work_items(a);
   if (!a.route_inline && items * cdiv(2 * a.I, 256) >= 128) {
@@ -1328,7 +1331,8 @@ hipError_t run4(const LaunchCtx& c, const DecodeArgs& a) {
   } else {
     HIP_RET((past_cache<WF_MX4>(a) ? run_gateup<WF_MX4, true>(c, a) : run_gateup<WF_MX4, false>(c, a)));
   }
-  if (decode_one_down(a.T, a.k) || (a.I < 512 && a.T * a.k < 16 * items))
+  const bool one = decode_one_down(a.T, a.k) && items * a.d * a.I < int64_t(40) << 20;
+  if (one || (a.I < 512 && a.T * a.k < 16 * items))
     return past_cache<WF_MX4>(a) ? run_down<WF_MX4, true>(c, a) : run_down<WF_MX4, false>(c, a);
   // 128 columns a work-group instead of 256 where those leave CUs without two
   return items * cdiv(a.d, 256) < 512 ? down4<2>(c, a) : down4<4>(c, a);

@@ -135,7 +135,8 @@ def test_ids_with_empty_slots_and_repeats(T, d, E, k, I):
 # none, one with 20; d and I of one and of odd numbers of 128
 @pytest.mark.parametrize("T,d,E,k,I", [(256, 128, 64, 4, 256), (200, 384, 128, 5, 128), (70, 640, 40, 6, 512),
                                        (9, 256, 200, 3, 384), (100, 1152, 128, 8, 640), (33, 1024, 130, 2, 128),
-                                       (256, 2176, 33, 3, 512), (17, 256, 128, 8, 1152)])
+                                       (256, 2176, 33, 3, 512), (17, 256, 128, 8, 1152), (4, 2176, 40, 8, 640),
+                                       (8, 4096, 9, 4, 1280)])
 def test_tiles(T, d, E, k, I):
     x, wgu, wd, logits = make(T, d, E, k, I, seed=6)
     logits[:, 5] = 9.0
