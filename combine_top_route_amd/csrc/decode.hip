@@ -1048,7 +1048,7 @@ __global__ __launch_bounds__(kDownRowWaves * 64, F == WF_FP8 && TB == 2 ? 3 : 1)
 // With half the bytes of a weight the products above are bound by their own LDS
 // turns and by loads that wait for each other; these are the streaming tiles of
 // mx4tile.h (gate/up of the layer above at 64 tokens: 214 MB in 44 us, 4.9 TB/s;
-// 200 tokens of 8 of 64 experts, d = 4096, I = 1024, in all 202 us before, 142).  A
+// 200 tokens of 8 of 64 experts, d = 4096, I = 1024, in all 202 us before, 140).  A
 // work-group takes an expert's tokens in blocks of 64 (down: 32, whose two planes
 // of activations are 64 rows).  CB: 64 CB columns of W a work-group.
 template <int RB, int CB> using Tiles4 = mx4::Tiles<RB, CB, RB <= 2 && CB == 2 ? 2 : 1>;

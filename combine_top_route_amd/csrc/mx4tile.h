@@ -15,8 +15,8 @@
 // with three slots of one 128-value stage; 40 with H = 2 and 128 columns a
 // work-group, 4.7 TB/s: whole 128-byte lines are asked for (a kernel that only
 // loads reads 4.7 TB/s in 64-byte pieces of 256 rows 2 KB apart, and 6.0 in
-// 128-byte ones of 128; the two halves of a line in loads of their own: 41).  Where more rows leave LDS for 128 values only
-// (RB > 2), wider tiles pay instead.
+// 128-byte ones of 128; the two halves of a line in loads of their own: 41).  Where
+// more rows leave LDS for 128 values only (RB > 2), wider tiles pay instead.
 #pragma once
 
 #include "common.h"
