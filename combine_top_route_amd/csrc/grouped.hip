@@ -84,18 +84,25 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, int rows, int nt
     incl[i] = total + wave_scan(n);
     total = __builtin_amdgcn_readlane(incl[i], 63);
   }
-  const int L = xcd_tile(blockIdx.y * gridDim.x + blockIdx.x, total * ntiles);
+  // Counts of row tiles fit 32 bits whatever the offsets hold (E of them, each at
+  // most R / rows + 1: below 2^31 by the largest E and R, and by the launcher's
+  // rules, which give long inputs 128 rows a tile), their products with ntiles
+  // do not: offsets that go back and forth count rows E / 2 times.  Tiles beyond
+  // the grid's are not made (offsets in order never count so many).
+  const int64_t groups = (int64_t)gridDim.x * gridDim.y, tiles = (int64_t)total * ntiles;
+  const int L = xcd_tile(blockIdx.y * gridDim.x + blockIdx.x, (int)(tiles < groups ? tiles : groups));
   if (L < 0) return false;
+  const int row = L / ntiles;  // among all row tiles, were they taken one by one
   int before = 0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const uint64_t past = __ballot(incl[i] * ntiles > L);
+    const uint64_t past = __ballot(incl[i] > row);
     if (past) {
       const int l = __builtin_ctzll(past);
       if (l) before = __builtin_amdgcn_readlane(incl[i], l - 1);
       const int n = __builtin_amdgcn_readlane(incl[i], l) - before, at = L - before * ntiles;
-      const int rt = a.row_major ? at / ntiles : at % n;
-      t->nt = a.row_major ? at % ntiles : at / n;
+      const int rt = a.row_major ? row - before : at % n;
+      t->nt = a.row_major ? L - row * ntiles : at / n;
       t->e = l + 64 * i;
       t->m0 = __builtin_amdgcn_readlane(o0[i], l) + rt * rows;
       t->seg1 = __builtin_amdgcn_readlane(o1[i], l);
