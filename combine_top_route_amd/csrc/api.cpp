@@ -510,7 +510,9 @@ struct DecodeLayout {
   size_t mid = 0, mw = 0, aw = 0, y = 0, total = 0;
 };
 
-DecodeLayout decode_layout(const moe_shape* s) {
+// y: whether down products go through memory (launch_decode's paths; MXFP4's
+// streaming tiles always send theirs there).
+DecodeLayout decode_layout(const moe_shape* s, bool mxfp4) {
   DecodeLayout L;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -522,7 +524,7 @@ DecodeLayout decode_layout(const moe_shape* s) {
   L.mid = take(sizeof(int32_t) * R);
   L.mw = take(sizeof(float) * R);
   L.aw = take(sizeof(float) * R * s->I);  // float32, or two planes of bf16
-  L.y = take(sizeof(float) * R * s->d);
+  if (mxfp4 || !decode_one_down(s->T, s->k)) L.y = take(sizeof(float) * R * s->d);
   L.total = off;
   return L;
 }
@@ -929,7 +931,8 @@ moe_status moe_backward8(const moe_shape* shape, const void* dout, const void* x
 moe_status moe_decode_workspace_size(const moe_shape* shape, size_t* bytes) {
   TRY(check_decode(shape));
   CHECK_PTR(bytes);
-  *bytes = decode_layout(shape).total;
+  // for any format that the shape allows
+  *bytes = decode_layout(shape, shape->dtype == MOE_BF16 && shape->d % 128 == 0 && shape->I % 128 == 0).total;
   return MOE_OK;
 }
 
@@ -957,7 +960,7 @@ moe_status moe_decode(const moe_shape* shape, int weights, const void* x, moe_ro
   } else if (s_gate_up || s_down) {
     return fail(MOE_ERR_INVALID_ARGUMENT, "scales given for uncoded weights");
   }
-  const DecodeLayout L = decode_layout(shape);
+  const DecodeLayout L = decode_layout(shape, weights == MOE_WEIGHTS_MXFP4);
   TRY(check_ws_bytes(L.total, workspace, workspace_bytes));
   TRY(check_aligned16(x, "x"));
   TRY(check_aligned16(w_gate_up, "w_gate_up"));
@@ -985,7 +988,7 @@ moe_status moe_decode(const moe_shape* shape, int weights, const void* x, moe_ro
   a.mid = (int32_t*)at(workspace, L.mid);
   a.mw = (float*)at(workspace, L.mw);
   a.aw = at(workspace, L.aw);
-  a.y = (float*)at(workspace, L.y);
+  a.y = L.y ? (float*)at(workspace, L.y) : nullptr;
   const LaunchCtx c = make_ctx(stream);
   (void)hipGetLastError();
   HIP_TRY(launch_decode(c, a, weights), "decode");

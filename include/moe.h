@@ -349,7 +349,9 @@ moe_status moe_swiglu_backward8(const moe_shape* shape, const void* G, const uin
  *
  * workspace: moe_decode_workspace_size bytes, 256-byte aligned (no initial
  * contents needed); calls that overlap in time, replayed graphs among them,
- * need one each. */
+ * need one each.  The size is that of the format that needs most: for T <= 8 and
+ * T*k <= 32 the others take 4*T*k*d bytes (rounded up to 256) less than
+ * MOE_WEIGHTS_MXFP4, and are not refused without them. */
 typedef enum { MOE_WEIGHTS_NATIVE = 0, MOE_WEIGHTS_FP8_BLOCK = 1, MOE_WEIGHTS_MXFP8 = 2,
                MOE_WEIGHTS_MXFP4 = 3 } moe_weight_format;
 moe_status moe_decode_workspace_size(const moe_shape* shape, size_t* bytes);
