@@ -383,16 +383,9 @@ def moe_prompt(x: Tensor, logits: Tensor, w_gate_up: Tensor, w_down: Tensor, k: 
     T = x.shape[0]
     with B._on(x.device):
         r = B.route(logits, k)
-        masked = logits.gather(1, r.topk_ids.long()) == -float("inf")
-        r.topk_w.masked_fill_(masked, 0.0)
         a = B.grouped_product(x, (w_gate_up, s_gate_up), r, T, k, swiglu=True, swiglu_limit=swiglu_limit)
-        # a row of zeros behind the slots', which a masked slot adds for its own (0 times
-        # what its expert makes would be NaN where that is not finite)
-        y = x.new_empty((T * k + 1, x.shape[1]))
-        y[T * k].zero_()
-        r.row_of.masked_fill_(masked.view(-1), T * k)
-        B.grouped_product(a, (w_down, s_down), r, T, k, gather=False, out=y[:T * k])
-        return B.combine(y, r, T, k)
+        y = B.grouped_product(a, (w_down, s_down), r, T, k, gather=False)
+        return B.combine(y, r, T, k, skip_masked=True)
 
 
 @moe_prompt.register_fake

@@ -138,7 +138,7 @@ def _check(call: str, status: int):
         raise MoeError(call, status)
 
 
-FLAG_PERSISTENT = 1
+FLAG_PERSISTENT, FLAG_SKIP_MASKED = 1, 2
 
 
 def make_shape(T, d, E, k, I, dtype=torch.bfloat16, logits_dtype=None, precision="native",
@@ -697,15 +697,30 @@ def permute(x, routing: Routing, k, out=None):
     return xp
 
 
-def combine(rows, routing: Routing, T, k):
+def combine(rows, routing: Routing, T, k, skip_masked=False):
+    """out [T, d] of expert-sorted rows [T*k, d] (more are not read): each token's
+    rows by their weights (moe_combine in include/moe.h).  skip_masked: slots
+    whose logit (routing.logits) is -inf add nothing."""
+    dev = rows.device
+    if rows.dim() != 2 or rows.shape[0] < T * k or rows.dtype not in _DT or not rows.is_contiguous():
+        raise ValueError(f"rows must be contiguous [T*k={T * k}, d] of one of {tuple(_DT)}, got {tuple(rows.shape)} "
+                         f"{rows.dtype}")
     d = rows.shape[1]
     E = routing.counts.numel()
+    cr = routing.on(dev, "row_of", "topk_w").c()
     shape = make_shape(T, d, E, k, 8, rows.dtype)
-    out = torch.empty((T, d), dtype=rows.dtype, device=rows.device)
-    cr = routing.on(rows.device, "row_of", "topk_w").c()
-    with _on(rows.device):
+    if skip_masked:
+        lg = routing.logits
+        if lg is None or lg.dtype not in _DT:
+            raise ValueError(f"skip_masked needs routing.logits, of one of {tuple(_DT)}")
+        _need(lg, "routing.logits", (T, E), lg.dtype, dev)
+        _need(routing.topk_ids, "routing.topk_ids", (T, k), torch.int32, dev)
+        shape.logits_dtype = _DT[lg.dtype]
+        shape.flags |= FLAG_SKIP_MASKED
+    out = torch.empty((T, d), dtype=rows.dtype, device=dev)
+    with _on(dev):
         _check("moe_combine", lib().moe_combine(ctypes.byref(shape), _ptr(rows), ctypes.byref(cr), _ptr(out),
-                                                 _stream(rows.device)))
+                                                 _stream(dev)))
     return out
 
 

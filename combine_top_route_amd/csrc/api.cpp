@@ -1164,18 +1164,29 @@ moe_status moe_permute(const moe_shape* shape, const void* x, const moe_routing*
 
 moe_status moe_combine(const moe_shape* shape, const void* rows, const moe_routing* routing,
                        void* out, void* stream) {
+  CHECK_PTR(shape);
+  moe_shape plain = *shape;  // the flag is this call's alone
+  const bool skip = plain.flags & MOE_FLAG_SKIP_MASKED;
+  plain.flags &= ~MOE_FLAG_SKIP_MASKED;
+  shape = &plain;
   TRY(check_shape(shape));
   CHECK_PTR(rows);
   CHECK_PTR(out);
   CHECK_PTR(routing);
   CHECK_PTR(routing->row_of);
   CHECK_PTR(routing->topk_w);
+  CombineMask mask = {};
+  if (skip) {
+    CHECK_PTR(routing->logits);
+    CHECK_PTR(routing->topk_ids);
+    mask = {routing->logits, routing->topk_ids, (int)shape->E, shape->logits_dtype == MOE_F32};
+  }
   TRY(check_aligned16(rows, "rows"));
   TRY(check_aligned16(out, "out"));
   const LaunchCtx c = make_ctx(stream);
   (void)hipGetLastError();
   HIP_TRY(launch_combine(c, "combine_weighted", shape->dtype, rows, routing->row_of, routing->topk_w, (int)shape->T,
-                         (int)shape->k, (int)shape->d, out), "combine");
+                         (int)shape->k, (int)shape->d, out, skip ? &mask : nullptr), "combine");
   return MOE_OK;
 }
 

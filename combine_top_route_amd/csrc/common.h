@@ -152,9 +152,18 @@ inline int64_t max_row_tiles(int64_t R, int64_t E) { return R / kRowTile + E; }
 hipError_t launch_permute(const LaunchCtx& c, const char* name, int dtype, const void* x,
                           const int32_t* src_of, const int32_t* row_of,
                           int R, int k, int d, void* xp);
-// out[t] = sum_j (w ? w[t*k+j] : 1) * rows[row_of[t*k+j]]
+// Masked experts' slots: those whose logit (of expert ids[t*k+j]) is -inf.
+struct CombineMask {
+  const void* logits;  // [T, E], float32 or bf16
+  const int32_t* ids;  // [T, k]
+  int E;
+  bool f32;
+};
+// out[t] = sum_j (w ? w[t*k+j] : 1) * rows[row_of[t*k+j]], without the masked slots
+// where there is a mask.
 hipError_t launch_combine(const LaunchCtx& c, const char* name, int dtype, const void* rows,
-                          const int32_t* row_of, const float* w, int T, int k, int d, void* out);
+                          const int32_t* row_of, const float* w, int T, int k, int d, void* out,
+                          const CombineMask* mask = nullptr);
 // bf16 SwiGLU backward per row from G [R,I] and H [R,2I]: dH [R,2I] and the
 // row's top-k-weight gradient dw [R] = <G, silu(g) u>.
 // lim: the SwiGLU clamp (+inf: none).

@@ -65,13 +65,23 @@ __global__ __launch_bounds__(256) void permute_kernel(const uint4* __restrict__ 
   for (int c = lane; c < row_vecs; c += kWave) dst[c] = src[c];
 }
 
+// Whether a slot of token t counts: not when its expert's logit is -inf.  Its row
+// is there all the same and is loaded with the others, so that no load waits for
+// the masks.
+__device__ __forceinline__ bool counts(const CombineMask& m, int64_t t, int64_t slot) {
+  const int e = min(max(m.ids[slot], 0), m.E - 1);
+  const float l = m.f32 ? ((const float*)m.logits)[t * m.E + e] : bf2f(((const bf16_t*)m.logits)[t * m.E + e]);
+  return l != -__builtin_huge_valf();
+}
+
 // out[t] = sum_j w[t,j] * rows[row_of[t*k+j]] (w == null: weight 1), float32
-// sum in slot order, one rounding at the end.  One wave per token.
-template <typename T>
+// sum in slot order, one rounding at the end.  One wave per token.  MASKED: the
+// slots that do not count add nothing, whatever their row and weight hold.
+template <typename T, bool MASKED>
 __global__ __launch_bounds__(256) void combine_kernel(const uint4* __restrict__ rows,
                                                       const int32_t* __restrict__ row_of,
                                                       const float* __restrict__ w, int Tn, int k,
-                                                      int row_vecs, uint4* __restrict__ out) {
+                                                      int row_vecs, uint4* __restrict__ out, CombineMask mask) {
   constexpr int N = Vec<T>::N;
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= Tn) return;
@@ -85,13 +95,16 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint4* __restrict__ 
     for (; j + 4 <= k; j += 4) {  // four rows in flight, summed in slot order
       uint4 v[4];
       float s[4];
+      bool on[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         v[q] = rows[(int64_t)ro[j + q] * row_vecs + c];
         s[q] = w ? w[(int64_t)t * k + j + q] : 1.0f;
+        on[q] = !MASKED || counts(mask, t, (int64_t)t * k + j + q);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
+        if (MASKED && !on[q]) continue;
         float f[N];
         unpack<T>(v[q], f);
 #pragma unroll
@@ -99,6 +112,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint4* __restrict__ 
       }
     }
     for (; j < k; ++j) {
+      if (MASKED && !counts(mask, t, (int64_t)t * k + j)) continue;
       float f[N];
       unpack<T>(rows[(int64_t)ro[j] * row_vecs + c], f);
       const float s = w ? w[(int64_t)t * k + j] : 1.0f;
@@ -139,11 +153,11 @@ __global__ __launch_bounds__(256) void permute_scatter_kernel(const uint4* __res
 // before accumulating, so more of each token's rows are in flight.  Each
 // expert row is read exactly once, so the loads are non-temporal: they do
 // not evict lines that other kernels' operands reuse.
-template <typename T, int CPL, int RB>
+template <typename T, int CPL, int RB, bool MASKED>
 __global__ __launch_bounds__(256) void combine_wide_kernel(const uint4* __restrict__ rows,
                                                            const int32_t* __restrict__ row_of,
                                                            const float* __restrict__ w, int Tn, int k,
-                                                           uint4* __restrict__ out) {
+                                                           uint4* __restrict__ out, CombineMask mask) {
   constexpr int N = Vec<T>::N;
   constexpr int RV = 64 * CPL;  // 16-byte chunks per row
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -160,6 +174,7 @@ __global__ __launch_bounds__(256) void combine_wide_kernel(const uint4* __restri
   for (; j + RB <= k; j += RB) {
     uint4 v[RB][CPL];
     float s[RB];
+    bool on[RB];
 #pragma unroll
     for (int q = 0; q < RB; ++q) {
       const uint4* src = rows + (int64_t)ro[j + q] * RV + lane;
@@ -169,9 +184,11 @@ __global__ __launch_bounds__(256) void combine_wide_kernel(const uint4* __restri
         v[q][c] = uint4{x[0], x[1], x[2], x[3]};
       }
       s[q] = w ? w[(int64_t)t * k + j + q] : 1.0f;
+      on[q] = !MASKED || counts(mask, t, (int64_t)t * k + j + q);
     }
 #pragma unroll
-    for (int q = 0; q < RB; ++q)
+    for (int q = 0; q < RB; ++q) {
+      if (MASKED && !on[q]) continue;
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
         float f[N];
@@ -179,8 +196,10 @@ __global__ __launch_bounds__(256) void combine_wide_kernel(const uint4* __restri
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[c][i] += s[q] * f[i];
       }
+    }
   }
   for (; j < k; ++j) {
+    if (MASKED && !counts(mask, t, (int64_t)t * k + j)) continue;
     const uint4* src = rows + (int64_t)ro[j] * RV + lane;
     const float sj = w ? w[(int64_t)t * k + j] : 1.0f;
 #pragma unroll
@@ -341,27 +360,31 @@ hipError_t launch_permute(const LaunchCtx& c, const char* name, int dtype, const
 }
 
 hipError_t launch_combine(const LaunchCtx& c, const char* name, int dtype, const void* rows,
-                          const int32_t* row_of, const float* w, int T, int k, int d, void* out) {
+                          const int32_t* row_of, const float* w, int T, int k, int d, void* out,
+                          const CombineMask* mask) {
   const int row_vecs = d * (dtype == F32 ? 4 : 2) / 16;
   const dim3 grid((T + 3) / 4);
+  const uint4* r = (const uint4*)rows;
+  uint4* o = (uint4*)out;
+  const CombineMask m = mask ? *mask : CombineMask{};
+#define MOE_COMBINE(PLAIN, MASKED, ...)                                       \
+  do {                                                                        \
+    if (mask) MOE_LAUNCH(c, name, MASKED, grid, dim3(256), 0, __VA_ARGS__, m); \
+    else MOE_LAUNCH(c, name, PLAIN, grid, dim3(256), 0, __VA_ARGS__, m);       \
+  } while (0)
   // eight rows in flight per lane where a row takes four chunks a lane, four
   // at eight chunks (register budget)
-  if (dtype == BF16 && row_vecs == 256) {
-    MOE_LAUNCH(c, name, (combine_wide_kernel<bf16_t, 4, 8>), grid, dim3(256), 0, (const uint4*)rows,
-               row_of, w, T, k, (uint4*)out);
-    return hipSuccess;
-  }
-  if (dtype == BF16 && row_vecs == 512) {
-    MOE_LAUNCH(c, name, (combine_wide_kernel<bf16_t, 8, 4>), grid, dim3(256), 0, (const uint4*)rows,
-               row_of, w, T, k, (uint4*)out);
-    return hipSuccess;
-  }
-  if (dtype == F32)
-    MOE_LAUNCH(c, name, combine_kernel<float>, dim3((T + 3) / 4), dim3(256), 0,
-               (const uint4*)rows, row_of, w, T, k, row_vecs, (uint4*)out);
+  if (dtype == BF16 && row_vecs == 256)
+    MOE_COMBINE((combine_wide_kernel<bf16_t, 4, 8, false>), (combine_wide_kernel<bf16_t, 4, 8, true>), r, row_of, w, T,
+                k, o);
+  else if (dtype == BF16 && row_vecs == 512)
+    MOE_COMBINE((combine_wide_kernel<bf16_t, 8, 4, false>), (combine_wide_kernel<bf16_t, 8, 4, true>), r, row_of, w, T,
+                k, o);
+  else if (dtype == F32)
+    MOE_COMBINE((combine_kernel<float, false>), (combine_kernel<float, true>), r, row_of, w, T, k, row_vecs, o);
   else
-    MOE_LAUNCH(c, name, combine_kernel<bf16_t>, dim3((T + 3) / 4), dim3(256), 0,
-               (const uint4*)rows, row_of, w, T, k, row_vecs, (uint4*)out);
+    MOE_COMBINE((combine_kernel<bf16_t, false>), (combine_kernel<bf16_t, true>), r, row_of, w, T, k, row_vecs, o);
+#undef MOE_COMBINE
   return hipSuccess;
 }
 

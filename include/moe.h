@@ -117,8 +117,10 @@ typedef struct {
  * Intellect's Prime Mega MoE Trains Giant AI Models 55% Faster", section
  * "One kernel overlaps the pipeline".  Results are bit-identical to the
  * default engine's (every tile runs at full height, with the same MFMA
- * order).  Other precisions and MOE_F32 ignore the flag. */
-typedef enum { MOE_FLAG_PERSISTENT = 1 } moe_flags;
+ * order).  Other precisions and MOE_F32 ignore the flag.
+ *
+ * MOE_FLAG_SKIP_MASKED: for moe_combine alone (below); other calls refuse it. */
+typedef enum { MOE_FLAG_PERSISTENT = 1, MOE_FLAG_SKIP_MASKED = 2 } moe_flags;
 
 /* swiglu_limit > 0 selects the clamped SwiGLU that "Mario/overlap moe kernel
  * integration" names for DeepSeek V4 (commit on activations.ClampedSilu);
@@ -434,7 +436,10 @@ moe_status moe_grouped_product(const moe_shape* shape, int weights, const void* 
  * mixture-of-experts layer actually does"): out[t] = sum_j topk_w[t][j] *
  * rows[row_of[t*k+j]], summed in float32 in slot order; rows [T*k, d], out
  * [T,d] (dtype); reads routing->row_of and topk_w.  rows and out 16-byte
- * aligned. */
+ * aligned.  With MOE_FLAG_SKIP_MASKED in shape->flags a slot whose expert is
+ * masked (routing->logits, in logits_dtype, is -inf at topk_ids[t][j]) adds
+ * nothing, whatever its row and weight hold, and a token of masked experts
+ * alone gets a row of zeros; logits and topk_ids are then read too. */
 moe_status moe_combine(const moe_shape* shape, const void* rows,
                        const moe_routing* routing, void* out, void* stream);
 
