@@ -197,7 +197,7 @@ __global__ __launch_bounds__(kThreads<L>) void norm_bwd_kernel(NormArgs a) {
   const int lane = threadIdx.x % L, sub = threadIdx.x / L, vecs = a.d / N;
   // 32 columns a lane leave no registers for the weights and the next row, which
   // are then read where they are used (2048 rows of 16384 in bf16: 302 us with
-  // them spilled, 116 so; in float32, with 32 more sums a lane, 378)
+  // them spilled, 116 so; in float32, with 32 more sums a lane, 382)
   constexpr bool LEAN = NV * N >= 32;
   constexpr int KEPT = LEAN ? 1 : NV;
   u32x4_t wp_[KEPT], wn_[KEPT], gv_[KEPT];
@@ -434,13 +434,18 @@ Spread bwd_spread(int vecs) {
 // one step (512 rows of 2048: 15.2 us in 512, 13.1 in 256; 2000 rows 19.9, in half
 // 23.5), and no more than take the same number of steps (333 rows of 4096: 16.3 us
 // in 256, of which 77 take a second row, 15.1 in 167; 257 rows 15.9 and 13.8).  A
-// single one, which needs no parts and no join, for four steps (4 rows of 2048: a
-// call takes 20.2 us with the join and 17.4 without; eight steps 22.0 and 20.2).
+// single one, which needs no parts and no join, for two steps of rows of one piece a
+// lane: a call then launches once and takes 2.2 to 3.1 us less from Python, and in
+// a replayed graph 0.1 to 2.8 more (us with the join and without, eager and
+// captured: 2 rows of 2048 21.4 and 18.5, 6.5 and 8.5; of 4096 21.5 and 18.8, 7.1 and
+// 9.9; 64 of 64 21.7 and 18.6, 8.4 and 9.2; more steps lose more than they save, 4
+// rows of 2048 21.4 and 18.8, 6.6 and 11.8; so do longer rows, 2 of 16384 21.3 and
+// 31.2, 13.5 and 31.1, in float32 43 and 84 both ways).
 int64_t bwd_groups(int64_t T, Spread p, int vecs) {
   const int threads = threads_of(p.L);
   int64_t most = 256 * (p.L <= 256 && 3 * vecs < 2 * p.L ? 4 : p.L <= 384 ? 2 : 1);
   const int64_t blocks = cdiv(T, threads / p.L);
-  if (blocks <= 4) return 1;
+  if (blocks <= 2 && p.NV == 1) return 1;
   if (blocks <= most) most = std::max<int64_t>(256, most / 2);
   const int64_t steps = cdiv(blocks, most);
   return cdiv(blocks, steps);
