@@ -265,16 +265,9 @@ __device__ __forceinline__ void chunk_frags(typename Fmt<F>::frag* fr, u32x4_t a
   } else if constexpr (F == WF_BF16) {
     fr[0] = __builtin_bit_cast(bf16x8_t, a);
   } else if constexpr (F == WF_MX4) {  // its 32 codes are block q
-    const float s = __uint_as_float(((mx >> (8 * q)) & 0xffu) << 23);
+    const float s = mx4::scale_of(mx, 8 * q);
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      u32x4_t o;
-      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a[h], s, 0));
-      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a[h], s, 1));
-      o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a[h], s, 2));
-      o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a[h], s, 3));
-      fr[h] = __builtin_bit_cast(bf16x8_t, o);
-    }
+    for (int h = 0; h < 4; ++h) fr[h] = mx4::decode8(a[h], s);
   } else {
     // its 16 codes lie in block 2 c + q / 2
     const float s = F == WF_MX ? __uint_as_float(((mx >> (16 * c + 8 * (q >> 1))) & 0xffu) << 23) : 1.0f;
@@ -1228,21 +1221,23 @@ unsigned token_split(const DecodeArgs& a, int64_t groups) {
 template <int F>
 bool past_cache(const DecodeArgs& a) {
   constexpr int64_t kLastLevelCache = int64_t(256) << 20;
-  constexpr int64_t half_bytes = F == WF_MX4 ? 1 : F >= WF_FP8 ? 2 : 2 * sizeof(typename Fmt<F>::act);  // of a value
-  return work_items(a) * int64_t(3) * a.I * a.d * half_bytes > 2 * kLastLevelCache;
+  const int64_t value = F >= WF_FP8 ? 1 : sizeof(typename Fmt<F>::act);
+  return work_items(a) * int64_t(3) * a.I * a.d * value > kLastLevelCache;
 }
 
 template <int F, bool NT>
 hipError_t run_gateup(const LaunchCtx& c, const DecodeArgs& a) {
   const dim3 grid((unsigned)cdiv(a.I, 16), (unsigned)work_items(a));
   constexpr int UN = F >= WF_FP8 ? 2 : 4;
-  if (a.T > 16 && wide_gateup(a)) {
-    // units of K at a time: coded weights one (two leave room for fewer waves: 84
-    // us and 111 at 200 tokens), the others two (137 both ways at 256, at 64 125
-    // and with one 131)
-    constexpr int UNW = F >= WF_FP8 ? 1 : 2;
-    const dim3 wide((unsigned)cdiv(a.I, 32), grid.y);
-    MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, NT, 2, 4, 2, UNW>), wide, dim3(4 * 64), 0, a);
+  if (F != WF_MX4 && a.T > 16 && wide_gateup(a)) {  // e2m1 codes go to the streaming tiles there (run4)
+    if constexpr (F != WF_MX4) {
+      // units of K at a time: coded weights one (two leave room for fewer waves: 84
+      // us and 111 at 200 tokens), the others two (137 both ways at 256, at 64 125
+      // and with one 131)
+      constexpr int UNW = F >= WF_FP8 ? 1 : 2;
+      const dim3 wide((unsigned)cdiv(a.I, 32), grid.y);
+      MOE_LAUNCH(c, "decode_gateup", (decode_gateup_kernel<F, NT, 2, 4, 2, UNW>), wide, dim3(4 * 64), 0, a);
+    }
   } else if (a.T > 16) {
     const dim3 split(grid.x, grid.y, token_split(a, gu_groups(a)));
     // a work-group per CU or fewer: eight waves (57 tokens of both of 2 experts,
@@ -1322,6 +1317,10 @@ hipError_t down4(const LaunchCtx& c, const DecodeArgs& a) {
 // sums over all experts by itself, whose eight columns a work-group read slower but
 // need no combine (4 us), for the weights of 20 MB or more (4 tokens 15.8 and 8.9,
 // 3 12.0 and 9.0, 4 of 8 of 64, d = 4096, I = 1024, 35.6 and 16.8, 1 11.9 and 8.2).
+// Non-temporal loads in the kernels above, for weights beyond the last-level cache,
+// gain nothing with this format (us of both products with and without: 12 tokens of
+// 8 of 16, d = 16384, I = 896 103 and 98, 4 93.5 and 93.8, 40 of 4 of 8, I = 1920 141
+// and 139, 40 of 8 of 128, d = 8192, I = 256 118 and 115).
 hipError_t run4(const LaunchCtx& c, const DecodeArgs& a) {
   const int64_t items = work_items(a);
   if (!a.route_inline && items * cdiv(2 * a.I, 256) >= 128) {
@@ -1329,11 +1328,11 @@ hipError_t run4(const LaunchCtx& c, const DecodeArgs& a) {
     MOE_LAUNCH(c, "decode_gateup", decode_gateup4_kernel<2>, dim3((unsigned)cdiv(2 * a.I, 128), (unsigned)items),
                dim3(256), kLds4<2>, a);
   } else {
-    HIP_RET((past_cache<WF_MX4>(a) ? run_gateup<WF_MX4, true>(c, a) : run_gateup<WF_MX4, false>(c, a)));
+    HIP_RET((run_gateup<WF_MX4, false>(c, a)));
   }
   const bool one = decode_one_down(a.T, a.k) && items * a.d * a.I < int64_t(40) << 20;
   if (one || (a.I < 512 && a.T * a.k < 16 * items))
-    return past_cache<WF_MX4>(a) ? run_down<WF_MX4, true>(c, a) : run_down<WF_MX4, false>(c, a);
+    return run_down<WF_MX4, false>(c, a);
   // 128 columns a work-group instead of 256 where those leave CUs without two
   return items * cdiv(a.d, 256) < 512 ? down4<2>(c, a) : down4<4>(c, a);
 }
