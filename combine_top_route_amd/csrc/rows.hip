@@ -65,14 +65,17 @@ __global__ __launch_bounds__(256) void permute_kernel(const uint4* __restrict__ 
   for (int c = lane; c < row_vecs; c += kWave) dst[c] = src[c];
 }
 
-// Whether a slot of token t counts: not when its expert's logit is -inf.  Its row
-// is there all the same and is loaded with the others, so that no load waits for
-// the masks.
-__device__ __forceinline__ bool counts(const CombineMask& m, int64_t t, int64_t slot) {
-  const int e = min(max(m.ids[slot], 0), m.E - 1);
-  const float l = m.f32 ? ((const float*)m.logits)[t * m.E + e] : bf2f(((const bf16_t*)m.logits)[t * m.E + e]);
-  return l != -__builtin_huge_valf();
+// The logit of slot j's expert, and whether a slot with it counts.  A masked slot's
+// row is there all the same and is loaded with the others, so that no row waits for
+// the masks: a wave's lanes load the logits of 64 slots before the first rows and
+// vote behind them (16384 tokens of 8 slots, d = 2048: 97 us with masks
+// and without; 114 where each slot is asked on its own).
+__device__ __forceinline__ float slot_logit(const CombineMask& m, int64_t t, int k, int j) {
+  if (j >= k) return 0.0f;
+  const int e = min(max(m.ids[t * k + j], 0), m.E - 1);
+  return m.f32 ? ((const float*)m.logits)[t * m.E + e] : bf2f(((const bf16_t*)m.logits)[t * m.E + e]);
 }
+__device__ __forceinline__ bool counts(float logit) { return logit != -__builtin_huge_valf(); }
 
 // out[t] = sum_j w[t,j] * rows[row_of[t*k+j]] (w == null: weight 1), float32
 // sum in slot order, one rounding at the end.  One wave per token.  MASKED: the
@@ -87,6 +90,13 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint4* __restrict__ 
   if (t >= Tn) return;
   const int lane = threadIdx.x & 63;
   const int32_t* ro = row_of + (int64_t)t * k;
+  // the first 64 slots' masks; of more, each lane loads its own (the loop over c is
+  // not the whole wave's)
+  const uint64_t live = MASKED ? __ballot(counts(slot_logit(mask, t, k, lane))) : 0;
+  const auto on = [&](int j) {
+    if constexpr (!MASKED) return true;
+    else return j < 64 ? (bool)(live >> j & 1) : counts(slot_logit(mask, t, k, j));
+  };
   for (int c = lane; c < row_vecs; c += kWave) {
     float acc[N];
 #pragma unroll
@@ -95,16 +105,14 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint4* __restrict__ 
     for (; j + 4 <= k; j += 4) {  // four rows in flight, summed in slot order
       uint4 v[4];
       float s[4];
-      bool on[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         v[q] = rows[(int64_t)ro[j + q] * row_vecs + c];
         s[q] = w ? w[(int64_t)t * k + j + q] : 1.0f;
-        on[q] = !MASKED || counts(mask, t, (int64_t)t * k + j + q);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (MASKED && !on[q]) continue;
+        if (!on(j + q)) continue;
         float f[N];
         unpack<T>(v[q], f);
 #pragma unroll
@@ -112,7 +120,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const uint4* __restrict__ 
       }
     }
     for (; j < k; ++j) {
-      if (MASKED && !counts(mask, t, (int64_t)t * k + j)) continue;
+      if (!on(j)) continue;
       float f[N];
       unpack<T>(rows[(int64_t)ro[j] * row_vecs + c], f);
       const float s = w ? w[(int64_t)t * k + j] : 1.0f;
@@ -170,11 +178,18 @@ __global__ __launch_bounds__(256) void combine_wide_kernel(const uint4* __restri
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[c][i] = 0.0f;
   typedef unsigned int u32x4l __attribute__((ext_vector_type(4)));
+  float logit = MASKED ? slot_logit(mask, t, k, lane) : 0.0f;
+  uint64_t live = 0;
+  const auto vote = [&](int j) {  // at each multiple of 64
+    if (!MASKED || (j & 63)) return;
+    if (j) logit = slot_logit(mask, t, k, j + lane);
+    live = __ballot(counts(logit));
+  };
+  const auto on = [&](int j) { return !MASKED || (live >> (j & 63) & 1); };
   int j = 0;
   for (; j + RB <= k; j += RB) {
     uint4 v[RB][CPL];
     float s[RB];
-    bool on[RB];
 #pragma unroll
     for (int q = 0; q < RB; ++q) {
       const uint4* src = rows + (int64_t)ro[j + q] * RV + lane;
@@ -184,11 +199,11 @@ __global__ __launch_bounds__(256) void combine_wide_kernel(const uint4* __restri
         v[q][c] = uint4{x[0], x[1], x[2], x[3]};
       }
       s[q] = w ? w[(int64_t)t * k + j + q] : 1.0f;
-      on[q] = !MASKED || counts(mask, t, (int64_t)t * k + j + q);
     }
+    vote(j);
 #pragma unroll
     for (int q = 0; q < RB; ++q) {
-      if (MASKED && !on[q]) continue;
+      if (!on(j + q)) continue;
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
         float f[N];
@@ -199,7 +214,8 @@ __global__ __launch_bounds__(256) void combine_wide_kernel(const uint4* __restri
     }
   }
   for (; j < k; ++j) {
-    if (MASKED && !counts(mask, t, (int64_t)t * k + j)) continue;
+    vote(j);
+    if (!on(j)) continue;
     const uint4* src = rows + (int64_t)ro[j] * RV + lane;
     const float sj = w ? w[(int64_t)t * k + j] : 1.0f;
 #pragma unroll

@@ -140,3 +140,24 @@ def test_captured():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and bool(out.isfinite().all()), i
+
+
+@pytest.mark.parametrize("d", [8, 136, 2048, 4096])
+@pytest.mark.parametrize("k", [64, 65, 70, 130])
+def test_combine_more_slots_than_lanes(d, k):
+    T, E = 9, 140
+    g = torch.Generator(device=DEV).manual_seed(d + k)
+    lg = torch.randn((T, E), generator=g, device=DEV)
+    lg[:, ::3] = -math.inf
+    lg[4] = -math.inf
+    r = B.route(lg, k)
+    off = lg.gather(1, r.topk_ids.long()) == -math.inf
+    rows = torch.randn((T * k, d), generator=g, device=DEV).bfloat16()
+    at = r.row_of.view(T, k).long()
+    rows[at[off]] = math.nan
+    r.topk_w = torch.where(off, math.inf, torch.rand((T, k), generator=g, device=DEV)).contiguous()
+    got = B.combine(rows, r, T, k, skip_masked=True)
+    terms = torch.where(off[..., None], 0.0, r.topk_w[..., None].double() * rows[at].double())
+    want, mag = terms.sum(1), terms.abs().sum(1)
+    assert bool(off.any()) and bool(((got.double() - want).abs() <= (k + 2) * U * mag * 1.01 + HALF * want.abs()).all())
+    assert not bool(got[4].any())
